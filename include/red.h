@@ -7,7 +7,10 @@
  *                    optionally folding the old destination value in (accum);
  *   red_rows_ragged  the same for packed rows of varying length (CSR offsets);
  *   red_colprod      TCOLPROD column products dst[0,j] = prod_i src[i,j] for
- *                    fp32 and (wrapping) int32 matrices.
+ *                    fp32 and (wrapping) int32 matrices;
+ *   red_logprob, red_distill, red_policy, red_preference
+ *                    losses over rows of logits and their gradients (log
+ *                    softmax reductions of fp32, f16 or bf16 rows).
  *
  * Sources of the semantics (cited by page title and section):
  *   [TVM] Apache TVM docs, "reduction -> sm100_packed": "Algorithm" (sum of a
@@ -61,7 +64,8 @@
  *     rounding (tests bound it by 1e-5 * sum|x|).  Max / min are exact.
  *     Integer products are exact modulo 2^32.
  *   - NaN inputs are not supported (max / min then return an unspecified
- *     operand); infinities propagate as in IEEE arithmetic.
+ *     operand); infinities propagate as in IEEE arithmetic.  (The losses over
+ *     logits define both; see there.)
  */
 #ifndef RED_H
 #define RED_H
@@ -321,6 +325,129 @@ int red_colprod(int dtype, const void *x, int64_t R, int64_t C, void *out, red_s
  */
 #define RED_NOALLOC_MAX_PARTIALS 4096
 int red_full_noalloc(int op, const float *x, int64_t n, float *out, red_stream_t stream);
+
+/*
+ * Losses over rows of logits, with their gradients
+ * ------------------------------------------------
+ * x is a matrix of logits, one row per token and one column per entry of the
+ * vocabulary; each loss is a function of the log-softmax of the scaled rows,
+ *     z = scale * x,  lse = log sum_j e^z_j,  log p_j = z_j - lse,
+ * (scale is an inverse temperature), and its gradient goes to dx:
+ *     dx = grad_scale * d(sum of the losses of all rows or pairs) / dx.
+ * Conventions of these calls:
+ *   dtype    RED_F32, RED_F16 or RED_BF16, of x and of dx.  Arithmetic is in
+ *            fp32 (totals in 64 bits); dx is rounded once, to nearest.
+ *   rows, len, ld   x[r, j] is at x + r * ld + j; 1 <= len <= 2^30, ld >= len;
+ *            x needs the alignment of its elements only, and neither it nor
+ *            dx is touched between columns len and ld.
+ *   scale    > 0, finite.
+ *   dx, ldd  the gradient, rows of stride ldd >= len; may be x itself
+ *            (ldd == ld then) and must not overlap it otherwise; NULL where a
+ *            call allows it computes the loss alone.
+ *   target   one int64 column per row.  A row whose target is outside
+ *            [0, len) (such as -100) is ignored, as is a row or pair of
+ *            weight 0: its logits are never read, its loss and logp are 0
+ *            and its row of dx is 0, whatever they hold.
+ *   weight   a factor per row or pair, NULL for 1 everywhere (a mask over its
+ *            number of live tokens gives a mean).
+ *   logits   -inf removes an entry from the vocabulary.  A row that is -inf
+ *            throughout has lse = logp = -inf and a gradient of 0, and adds
+ *            nothing to a loss.  +inf or NaN in a row that takes part makes
+ *            its results NaN.
+ *   stats    totals over rows or pairs, summed in a fixed order: every result
+ *            of these calls is the same from call to call, bit for bit.
+ * They use the workspace (see above).
+ */
+
+/*
+ * red_logprob -- logp[r] = log p[r, target[r]] and lse[r], fp32, rows each.
+ * An ignored row gives logp = lse = 0.
+ */
+int red_logprob(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld, float scale, const int64_t *target,
+                float *logp, float *lse, red_stream_t stream);
+
+/*
+ * red_logprob_grad -- backward of red_logprob: for the gradient dlogp[r] of
+ * some loss by logp[r], dx[r, j] = scale * dlogp[r] * ([j == target[r]] - p_j)
+ * with p_j = e^(z_j - lse[r]), lse as red_logprob left it.  Rows whose dlogp
+ * is 0 are not read either.
+ */
+int red_logprob_grad(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld, float scale,
+                     const int64_t *target, const float *lse, const float *dlogp, void *dx, int64_t ldd,
+                     red_stream_t stream);
+
+/*
+ * red_distill -- distillation from the top k logits of a teacher:
+ *     loss[r] = weight[r] * sum_i q_i (log q_i - log p[ids_i]),
+ * with q = softmax(scale * vals) over the row's k entries (lse NULL), or
+ * q_i = e^(scale * vals_i - lse[r]) where the teacher's normaliser of the
+ * whole scaled row is given (the q then sum to less than 1 and the sum runs
+ * over them alone).
+ *   k        1 .. RED_DISTILL_MAX_K entries per row.
+ *   ids      (rows, k) int64 columns; an id outside [0, len) is no entry
+ *            (rows with fewer than k), an id that comes twice adds up.
+ *   vals     (rows, k) logits of type vdtype (RED_F32, RED_F16 or RED_BF16).
+ *   loss     rows floats;  stats: 2 floats, the sums of loss and of weight.
+ *   dx       [r, j]: grad_scale * weight[r] * scale * (Q p_j - sum of the q_i
+ *            with ids_i == j), Q = sum_i q_i; may be NULL.
+ */
+#define RED_DISTILL_MAX_K 1024
+int red_distill(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld, float scale, int64_t k,
+                const int64_t *ids, int vdtype, const void *vals, const float *lse, const float *weight,
+                float grad_scale, float *loss, float *stats, void *dx, int64_t ldd, red_stream_t stream);
+
+/*
+ * red_policy -- clipped policy loss with a KL term.  With logp as red_logprob,
+ * ratio = e^(logp - old_logp) and d = ref_logp - logp,
+ *     loss[r] = weight[r] * (-min(ratio * adv, clip(ratio, 1 - clip_low, 1 + clip_high) * adv)
+ *                            + kl_coef * (e^d - d - 1)).
+ *   old_logp, adv   rows floats;  ref_logp: rows floats, or NULL when kl_coef
+ *            is 0.  The KL term is left out where kl_coef is 0.
+ *   clip_low in 0..1, clip_high >= 0.
+ *   loss, logp   rows floats each.
+ *   stats    4 floats: the sums of loss, weight * (e^d - d - 1),
+ *            weight * [the clipped branch is taken] and weight over the rows
+ *            that take part (rows of logp -inf count in the first and last).
+ *   dx       may be NULL.  No gradient flows through a clipped ratio.
+ */
+int red_policy(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld, float scale, const int64_t *target,
+               const float *old_logp, const float *ref_logp, const float *adv, const float *weight, float clip_low,
+               float clip_high, float kl_coef, float grad_scale, float *loss, float *logp, float *stats, void *dx,
+               int64_t ldd, red_stream_t stream);
+
+/* The preference loss of u, the scaled difference of gains. */
+enum red_preference_kind {
+    RED_PREF_SIGMOID = 0, /* -(1 - smoothing) log sigma(u) - smoothing log sigma(-u) */
+    RED_PREF_HINGE = 1,   /* max(0, 1 - u) */
+    RED_PREF_SQUARED = 2  /* ((u - 1/2) / beta)^2 */
+};
+
+/*
+ * red_preference -- loss of pairs of packed sequences, one preferred to the
+ * other.  Sequence q holds the rows offsets[q] <= r < offsets[q + 1]; the
+ * chosen of pair i is sequence i, the rejected sequence pairs + i.  With
+ * s_q the sum of logp over the rows of q that take part (average != 0: their
+ * mean; 0 where there are none) and gain_q = s_q - ref_logp[q],
+ *     u = beta * (gain_i - gain_{pairs + i}) - margin,
+ *     loss[i] = weight[i] * the kind's loss of u.
+ *   offsets  2 * pairs + 1 ascending int64 (clamped to 0..rows); rows outside
+ *            every sequence are ignored.
+ *   ref_logp 2 * pairs floats: s_q of a reference model (summed or averaged
+ *            the same way), or NULL for 0 (no reference).
+ *   kind     enum red_preference_kind; beta > 0; smoothing in 0..1/2, for
+ *            RED_PREF_SIGMOID only.
+ *   loss     pairs floats;  seq_logp: 2 * pairs floats, s_q.
+ *   stats    4 floats: the sums over pairs of loss, weight * u,
+ *            weight * [u > 0] and weight.
+ *   work     3 * rows + pairs floats of scratch: the rows' logp, lse and dlogp
+ *            (as red_logprob_grad takes them) and the pairs' u afterwards.
+ *   dx       may be NULL.
+ */
+int red_preference(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld, float scale,
+                   const int64_t *target, const int64_t *offsets, int64_t pairs, const float *ref_logp,
+                   const float *weight, int kind, float beta, float margin, float smoothing, int average,
+                   float grad_scale, float *loss, float *seq_logp, float *stats, float *work, void *dx, int64_t ldd,
+                   red_stream_t stream);
 
 /* Select the grid stage of red_full (enum red_full_mode).  Process-wide.
  * Returns RED_OK, or RED_EINVAL for an unknown mode. */

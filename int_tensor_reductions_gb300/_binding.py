@@ -14,6 +14,8 @@ RED_KNOB_ROWS_GROUP, RED_KNOB_RAGGED_GROUP, RED_KNOB_COLPROD_SPLITS, RED_KNOB_FU
 RED_KNOB_RAGGED_STAGED = 5
 RED_KNOB_ROWS_ALIGNED = 6
 RED_KNOB_COLS_LANES = 7
+RED_PREF_SIGMOID, RED_PREF_HINGE, RED_PREF_SQUARED = 0, 1, 2
+RED_DISTILL_MAX_K = 1024
 
 _OPS = {"sum": RED_SUM, "max": RED_MAX, "min": RED_MIN, "prod": RED_PROD}
 # element type names of the column reductions and their sizes in bytes
@@ -28,7 +30,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libred.so")
 _lib = None
 
-_i64, _int, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
+_i64, _int, _vp, _f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_float
+# dtype, x, rows, len, ld, scale
+_LOGITS = [_int, _vp, _i64, _i64, _i64, _f32]
 _SIGNATURES = {
     "red_full": ([_int, _vp, _i64, _vp, _vp], _int),
     "red_full_noalloc": ([_int, _vp, _i64, _vp, _vp], _int),
@@ -42,6 +46,12 @@ _SIGNATURES = {
     "red_cols_ld": ([_int, _int, _vp, _i64, _i64, _i64, _vp, _vp], _int),
     "red_full_typed": ([_int, _int, _vp, _i64, _vp, _vp], _int),
     "red_rows_typed": ([_int, _int, _vp, _i64, _i64, _int, _vp, _vp], _int),
+    "red_logprob": (_LOGITS + [_vp, _vp, _vp, _vp], _int),
+    "red_logprob_grad": (_LOGITS + [_vp, _vp, _vp, _vp, _i64, _vp], _int),
+    "red_distill": (_LOGITS + [_i64, _vp, _int, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _i64, _vp], _int),
+    "red_policy": (_LOGITS + [_vp, _vp, _vp, _vp, _vp, _f32, _f32, _f32, _f32, _vp, _vp, _vp, _vp, _i64, _vp], _int),
+    "red_preference": (_LOGITS + [_vp, _vp, _i64, _vp, _vp, _int, _f32, _f32, _f32, _int, _f32, _vp, _vp, _vp, _vp,
+                                  _vp, _i64, _vp], _int),
     "red_set_full_mode": ([_int], _int),
     "red_get_full_mode": ([], _int),
     "red_set_knob": ([_int, _int], _int),
@@ -342,6 +352,186 @@ def red_colprod(x: torch.Tensor, out: torch.Tensor | None = None, stream=None, d
     with torch.cuda.device(x.device):
         _check(lib().red_cols_ld(RED_PROD, code, x.data_ptr(), R, C, ld, out.data_ptr(), _stream(stream, x.device)))
     return out
+
+
+# ------------------------------------------ losses over rows of logits
+
+_LOGIT_DTYPES = {torch.float32: RED_F32, torch.float16: RED_F16, torch.bfloat16: RED_BF16}
+_PREF_KINDS = {"sigmoid": RED_PREF_SIGMOID, "hinge": RED_PREF_HINGE, "squared": RED_PREF_SQUARED}
+
+
+def _logits(x, scale):
+    """The leading C arguments of a loss: (dtype, x, rows, len, ld, scale)."""
+    code = _LOGIT_DTYPES.get(x.dtype)
+    if code is None:
+        raise ValueError(f"x must be float32, float16 or bfloat16, got {x.dtype}")
+    ld = _row_strided(x)
+    return code, x.data_ptr(), x.shape[0], x.shape[1], ld, scale
+
+
+def _vector(t, name, dtype, x, n):
+    """Pointer of a contiguous vector of n elements beside x, or None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.device != x.device:
+        raise ValueError(f"{name} is on {t.device}, x on {x.device}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} element(s), has {t.numel()}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _grad_out(grad, x, ld, name="grad"):
+    """(tensor, pointer, row stride) of a gradient: False for none, None for a
+    new one with x's row stride, or a tensor to write (x itself for in place)."""
+    if grad is False:
+        return None, None, 0
+    if grad is None:
+        rows, length = x.shape
+        grad = torch.empty((rows, ld), dtype=x.dtype, device=x.device)
+        if ld != length:
+            grad = grad[:, :length]
+        return grad, grad.data_ptr(), ld
+    if grad.dtype != x.dtype or grad.device != x.device or grad.shape != x.shape:
+        raise ValueError(f"{name} must have x's dtype, device and shape")
+    return grad, grad.data_ptr(), _row_strided(grad, name)
+
+
+def _loss_call(name, x, stream, made, *args):
+    """C call `name` on ``stream``.  ``made`` are tensors this call allocated:
+    on a stream that is not the current one they are marked as used there, so
+    that the allocator does not hand them out again before the work is done."""
+    fn = getattr(lib(), name)
+    if stream is not None:
+        user = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=x.device)
+        for t in made:
+            if t is not None:
+                t.record_stream(user)
+    if torch.cuda.current_device() == x.device.index:
+        _check(fn(*args, _stream(stream, x.device)))
+    else:
+        with torch.cuda.device(x.device):
+            _check(fn(*args, _stream(stream, x.device)))
+
+
+def red_logprob(x: torch.Tensor, target: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
+                lse: torch.Tensor | None = None, stream=None):
+    """Log-probabilities logp[r] = log_softmax(scale * x[r])[target[r]] of a
+    (rows, vocab) matrix of float32, float16 or bfloat16 logits (rows may be
+    strided) and the rows' log-sum-exp; returns (logp, lse), fp32.  A row whose
+    target is outside the vocabulary (e.g. -100) is not read and gives 0."""
+    head = _logits(x, scale)
+    rows = x.shape[0]
+    if out is None:
+        out = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if lse is None:
+        lse = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _loss_call("red_logprob", x, stream, (out, lse), *head, _vector(target, "target", torch.int64, x, rows),
+               _vector(out, "out", torch.float32, x, rows), _vector(lse, "lse", torch.float32, x, rows))
+    return out, lse
+
+
+def red_logprob_grad(x: torch.Tensor, target: torch.Tensor, lse: torch.Tensor, dlogp: torch.Tensor,
+                     scale: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Backward of red_logprob: the gradient by x, given the gradient ``dlogp``
+    by logp and red_logprob's lse.  ``out`` may be x (in place); a new one has
+    x's row stride."""
+    head = _logits(x, scale)
+    rows = x.shape[0]
+    out, out_ptr, ldd = _grad_out(out, x, head[4], "out")
+    if out is None:
+        raise ValueError("out must be a tensor or None")
+    _loss_call("red_logprob_grad", x, stream, (out,), *head, _vector(target, "target", torch.int64, x, rows),
+               _vector(lse, "lse", torch.float32, x, rows), _vector(dlogp, "dlogp", torch.float32, x, rows),
+               out_ptr, ldd)
+    return out
+
+
+def red_distill(x: torch.Tensor, ids: torch.Tensor, vals: torch.Tensor, lse: torch.Tensor | None = None,
+                weight: torch.Tensor | None = None, scale: float = 1.0, grad_scale: float = 1.0, grad=None,
+                stream=None):
+    """Distillation from a teacher's top k logits ``vals`` (rows, k) at the
+    columns ``ids``: KL(q || softmax(scale * x)) per row over the teacher's
+    entries, q = softmax(scale * vals), or exp(scale * vals - lse) where the
+    teacher's normaliser ``lse`` is given.  Returns (loss, stats, grad): loss
+    per row times ``weight``, stats = (sum of loss, sum of weight), and
+    grad_scale times the gradient of the summed loss by x.  ``grad``: None for
+    a new tensor, a tensor to write (x: in place), False for the loss alone."""
+    head = _logits(x, scale)
+    rows = x.shape[0]
+    if ids.dim() != 2 or vals.shape != ids.shape or ids.shape[0] != rows:
+        raise ValueError("ids and vals must be (rows, k)")
+    vcode = _LOGIT_DTYPES.get(vals.dtype)
+    if vcode is None:
+        raise ValueError(f"vals must be float32, float16 or bfloat16, got {vals.dtype}")
+    k = ids.shape[1]
+    grad, grad_ptr, ldd = _grad_out(grad, x, head[4])
+    flat = torch.empty(rows + 2, dtype=torch.float32, device=x.device)
+    loss, stats = flat[2:], flat[:2]
+    _loss_call("red_distill", x, stream, (flat, grad), *head, k, _vector(ids, "ids", torch.int64, x, rows * k), vcode,
+               _vector(vals, "vals", vals.dtype, x, rows * k), _vector(lse, "lse", torch.float32, x, rows),
+               _vector(weight, "weight", torch.float32, x, rows), grad_scale, loss.data_ptr(), stats.data_ptr(),
+               grad_ptr, ldd)
+    return loss, stats, grad
+
+
+def red_policy(x: torch.Tensor, target: torch.Tensor, old_logp: torch.Tensor, adv: torch.Tensor,
+               ref_logp: torch.Tensor | None = None, weight: torch.Tensor | None = None, clip_low: float = 0.2,
+               clip_high: float = 0.2, kl_coef: float = 0.0, scale: float = 1.0, grad_scale: float = 1.0, grad=None,
+               stream=None):
+    """Clipped policy loss with a KL term, per token: -min(r * adv, clip(r,
+    1 - clip_low, 1 + clip_high) * adv) + kl_coef * (e^d - d - 1) with r =
+    e^(logp - old_logp), d = ref_logp - logp, times ``weight``.  Returns (loss,
+    logp, stats, grad); stats = sums of (loss, weight * (e^d - d - 1), weight
+    of clipped tokens, weight).  ``grad`` as for red_distill."""
+    head = _logits(x, scale)
+    rows = x.shape[0]
+    grad, grad_ptr, ldd = _grad_out(grad, x, head[4])
+    flat = torch.empty(2 * rows + 4, dtype=torch.float32, device=x.device)
+    stats, loss, logp = flat[:4], flat[4:4 + rows], flat[4 + rows:]
+    f32 = torch.float32
+    _loss_call("red_policy", x, stream, (flat, grad), *head, _vector(target, "target", torch.int64, x, rows),
+               _vector(old_logp, "old_logp", f32, x, rows), _vector(ref_logp, "ref_logp", f32, x, rows),
+               _vector(adv, "adv", f32, x, rows), _vector(weight, "weight", f32, x, rows), clip_low, clip_high,
+               kl_coef, grad_scale, loss.data_ptr(), logp.data_ptr(), stats.data_ptr(), grad_ptr, ldd)
+    return loss, logp, stats, grad
+
+
+def red_preference(x: torch.Tensor, target: torch.Tensor, offsets: torch.Tensor,
+                   ref_logp: torch.Tensor | None = None, weight: torch.Tensor | None = None, kind="sigmoid",
+                   beta: float = 0.1, margin: float = 0.0, smoothing: float = 0.0, average: bool = False,
+                   scale: float = 1.0, grad_scale: float = 1.0, grad=None, stream=None):
+    """Preference loss of pairs of packed sequences (rows offsets[q]:offsets[q+1];
+    first all chosen, then all rejected ones): with s the sum (``average``: the
+    mean) of a sequence's token log-probabilities less ``ref_logp``, u = beta *
+    (s_chosen - s_rejected) - margin and ``kind`` "sigmoid" (with label
+    ``smoothing``), "hinge" or "squared" the loss of u.  Returns (loss,
+    seq_logp, stats, grad): loss per pair times ``weight``, the sequences' sums
+    or means, stats = sums of (loss, weight * u, weight of u > 0, weight).
+    ``grad`` as for red_distill."""
+    head = _logits(x, scale)
+    rows = x.shape[0]
+    if offsets.numel() % 2 != 1:
+        raise ValueError("offsets needs 2 * pairs + 1 entries")
+    pairs = offsets.numel() // 2
+    if isinstance(kind, str):
+        if kind not in _PREF_KINDS:
+            raise ValueError(f"unknown kind {kind!r}")
+        kind = _PREF_KINDS[kind]
+    grad, grad_ptr, ldd = _grad_out(grad, x, head[4])
+    f32 = torch.float32
+    flat = torch.empty(3 * rows + 4 * pairs + 4, dtype=f32, device=x.device)
+    stats, seq_logp, loss, work = flat[:4], flat[4:4 + 2 * pairs], flat[4 + 2 * pairs:4 + 3 * pairs], \
+        flat[4 + 3 * pairs:]
+    _loss_call("red_preference", x, stream, (flat, grad), *head, _vector(target, "target", torch.int64, x, rows),
+               _vector(offsets, "offsets", torch.int64, x, 2 * pairs + 1), pairs,
+               _vector(ref_logp, "ref_logp", f32, x, 2 * pairs), _vector(weight, "weight", f32, x, pairs), int(kind),
+               beta, margin, smoothing, int(bool(average)), grad_scale, loss.data_ptr(), seq_logp.data_ptr(),
+               stats.data_ptr(), work.data_ptr(), grad_ptr, ldd)
+    return loss, seq_logp, stats, grad
 
 
 def red_set_full_mode(mode: int) -> None:
