@@ -97,7 +97,9 @@ enum red_dtype {
 
 /* Status codes.  There is no timeout status: no kernel of this library
  * waits on another CTA, stream or device (the last-block stages count
- * arrivals and the last arrival does the fold), so no wait can run out. */
+ * arrivals and the last arrival does the fold).  The losses over logits wait
+ * for their own bulk copies, with a limit: a copy that never arrived would
+ * make the results of its CTA's rows NaN. */
 enum red_status { RED_OK = 0, RED_EINVAL = -1, RED_ECUDA = -2, RED_ENOMEM = -3 };
 
 /* Grid stage of red_full (how the per-CTA partials become one scalar). */

@@ -121,17 +121,117 @@ __device__ __forceinline__ float exp_excess(float d)
     return expf(d) - d - 1.0f;
 }
 
-// Log-probabilities only.
-struct LogprobArgs {
-    const int64_t *target;
-    float *logp, *lse;
+enum : int { ROW_END = 0, ROW_OUT = 1, ROW_LIVE = 2 };
+
+// What a kernel knows of a row before its logits: its index, whether it takes
+// part, and the loss's inputs.
+struct RowEntry {
+    int64_t r;
+    int64_t target;
+    int state;    // ROW_*
+    uint32_t xy;  // the target's logit, as stored
+    float w;      // weight, or the gradient by logp
+    float f[3];
 };
 
-struct PolicyArgs {
+// Element i of a row as stored, for load latency to pass before it is widened.
+template <int DT>
+__device__ __forceinline__ uint32_t load_bits(const void *p, int64_t i)
+{
+    if constexpr (DT == RED_F32)
+        return static_cast<const uint32_t *>(p)[i];
+    else
+        return static_cast<const uint16_t *>(p)[i];
+}
+
+// The gradient of a row: g_j = mul * 2^(fma(x_j, fa, fb) * fc) + [j == y] cy,
+// or zeros throughout.
+struct RowGrad {
+    float fa, fb, fc, mul, cy;
+    int y;
+    bool zero;
+};
+
+__device__ __forceinline__ bool row_empty(SoftStat t) { return t.m == NEG_INF && t.l == 0.0f; }
+
+// c * ([j == y] - p_j) from the row's statistics.
+__device__ __forceinline__ RowGrad grad_of_target(const LogitRows &a, SoftStat t, int y, float c)
+{
+    return RowGrad{1.0f, -t.m, a.scale * LOG2E, -c / t.l, c, y, row_empty(t) || c == 0.0f};
+}
+
+// Each loss below gives the kernels
+//   STATS    whether a row's statistics come from its logits;
+//   TEACHER  whether it has a list of teacher entries per row;
+//   GRADIENT whether it can have a gradient;
+//   load()   the row's entry (its logits are still intact): issues loads and
+//            uses none of their values, so that a later settle() may be the
+//            first to wait for them;
+//   settle() whether the row takes part, and the load of the target's logit;
+//   grad()   the row's gradient from entry and statistics (any thread);
+//   write()  the row's scalar results (one thread), for rows out of the loss
+//            too.
+
+struct LogprobArgs {
+    static constexpr bool STATS = true, TEACHER = false, GRADIENT = false;
     const int64_t *target;
-    const float *old_logp, *ref_logp, *adv, *weight;  // ref_logp, weight may be NULL
-    float clip_low, clip_high, kl, gscale;
-    float *loss, *logp, *stats;
+    float *logp, *lse;
+
+    __device__ void load(int64_t r, RowEntry &e) const
+    {
+        e.r = r;
+        e.target = target[r];
+    }
+    template <int DT>
+    __device__ void settle(const LogitRows &a, RowEntry &e) const
+    {
+        e.state = valid_id(e.target, a.len) ? ROW_LIVE : ROW_OUT;
+        if (e.state == ROW_LIVE)
+            e.xy = load_bits<DT>(a.x, e.r * a.ld + e.target);
+    }
+    template <int DT>
+    __device__ RowGrad grad(const LogitRows &, const RowEntry &, SoftStat, float) const { return RowGrad{}; }
+    template <int DT>
+    __device__ void write(const LogitRows &a, const RowEntry &e, SoftStat t) const
+    {
+        float p = 0.0f, n = 0.0f;
+        if (e.state == ROW_LIVE) {
+            const float ln = logf(t.l);
+            n = row_empty(t) ? NEG_INF : fmaf(a.scale, t.m, ln);
+            p = row_empty(t) ? NEG_INF : (Elem<DT>::widen(e.xy) - t.m) * a.scale - ln;
+        }
+        logp[e.r] = p;
+        lse[e.r] = n;
+    }
+};
+
+struct LogprobGradArgs {
+    static constexpr bool STATS = false, TEACHER = false, GRADIENT = true;
+    const int64_t *target;
+    const float *lse, *dlogp;
+
+    __device__ void load(int64_t r, RowEntry &e) const
+    {
+        e.r = r;
+        e.target = target[r];
+        e.w = dlogp[r];
+        e.f[0] = lse[r];
+    }
+    template <int DT>
+    __device__ void settle(const LogitRows &a, RowEntry &e) const
+    {
+        e.state = valid_id(e.target, a.len) && e.w != 0.0f && e.f[0] != NEG_INF ? ROW_LIVE : ROW_OUT;
+    }
+    // p_j = 2^((scale x_j - lse) log2 e): the difference in one rounding, so
+    // that it is exact where p_j is near 1.
+    template <int DT>
+    __device__ RowGrad grad(const LogitRows &a, const RowEntry &e, SoftStat, float) const
+    {
+        const float c = e.w * a.scale;
+        return RowGrad{a.scale, -e.f[0], LOG2E, -c, c, (int)e.target, false};
+    }
+    template <int DT>
+    __device__ void write(const LogitRows &, const RowEntry &, SoftStat) const {}
 };
 
 struct PolicyTerms {
@@ -141,32 +241,88 @@ struct PolicyTerms {
     float dlogp;
 };
 
-// L = -min(r A, clip(r, 1 - low, 1 + high) A) + kl (e^d - d - 1) with
-// r = e^(logp - old) and d = ref - logp; its derivative by logp.
-__device__ __forceinline__ PolicyTerms policy_terms(float logp, float old, float ref, bool has_ref, float adv,
-                                                    float low, float high, float kl)
-{
-    PolicyTerms t;
-    const float ratio = expf(logp - old);
-    const float bounded = fminf(fmaxf(ratio, 1.0f - low), 1.0f + high);
-    // a ratio that overflowed times no advantage is no gain, not a NaN
-    const float a = adv == 0.0f ? 0.0f : ratio * adv;
-    const float b = bounded * adv;
-    const bool clipped = a > b;
-    t.clipped = clipped ? 1.0f : 0.0f;
-    t.loss = -(clipped ? b : a);
-    t.dlogp = clipped ? 0.0f : -a;
-    t.drift = 0.0f;
-    if (has_ref && kl != 0.0f) {
-        const float d = ref == logp ? 0.0f : ref - logp;  // equal infinities do not drift
-        t.drift = exp_excess(d);
-        t.loss += kl * t.drift;
-        t.dlogp -= kl * expm1f(d);
+struct PolicyArgs {
+    static constexpr bool STATS = true, TEACHER = false, GRADIENT = true;
+    const int64_t *target;
+    const float *old_logp, *ref_logp, *adv, *weight;  // ref_logp, weight may be NULL
+    float clip_low, clip_high, kl, gscale;
+    float *loss, *logp, *stats;
+
+    // L = -min(r A, clip(r, 1 - low, 1 + high) A) + kl (e^d - d - 1) with
+    // r = e^(logp - old) and d = ref - logp; its derivative by logp.
+    __device__ PolicyTerms terms(float lp, float old, float ref, float A) const
+    {
+        PolicyTerms t;
+        const float ratio = expf(lp - old);
+        const float bounded = fminf(fmaxf(ratio, 1.0f - clip_low), 1.0f + clip_high);
+        // a ratio that overflowed times no advantage is no gain, not a NaN
+        const float free = A == 0.0f ? 0.0f : ratio * A;
+        const float held = bounded * A;
+        const bool clipped = free > held;
+        t.clipped = clipped ? 1.0f : 0.0f;
+        t.loss = -(clipped ? held : free);
+        t.dlogp = clipped ? 0.0f : -free;
+        t.drift = 0.0f;
+        if (ref_logp && kl != 0.0f) {
+            const float d = ref == lp ? 0.0f : ref - lp;  // equal infinities do not drift
+            t.drift = exp_excess(d);
+            t.loss += kl * t.drift;
+            t.dlogp -= kl * expm1f(d);
+        }
+        return t;
     }
-    return t;
-}
+    __device__ void load(int64_t r, RowEntry &e) const
+    {
+        e.r = r;
+        e.target = target[r];
+        e.w = weight ? weight[r] : 1.0f;
+        e.f[0] = old_logp[r];
+        e.f[1] = ref_logp ? ref_logp[r] : 0.0f;
+        e.f[2] = adv[r];
+    }
+    template <int DT>
+    __device__ void settle(const LogitRows &a, RowEntry &e) const
+    {
+        e.state = valid_id(e.target, a.len) && e.w != 0.0f ? ROW_LIVE : ROW_OUT;
+        if (e.state == ROW_LIVE)
+            e.xy = load_bits<DT>(a.x, e.r * a.ld + e.target);
+    }
+    template <int DT>
+    __device__ float row_logp(const LogitRows &a, const RowEntry &e, SoftStat t) const
+    {
+        return (Elem<DT>::widen(e.xy) - t.m) * a.scale - logf(t.l);
+    }
+    template <int DT>
+    __device__ RowGrad grad(const LogitRows &a, const RowEntry &e, SoftStat t, float) const
+    {
+        const PolicyTerms q = terms(row_logp<DT>(a, e, t), e.f[0], e.f[1], e.f[2]);
+        return grad_of_target(a, t, (int)e.target, e.w * q.dlogp * gscale * a.scale);
+    }
+    template <int DT>
+    __device__ void write(const LogitRows &a, const RowEntry &e, SoftStat t) const
+    {
+        float p = 0.0f, v = 0.0f;
+        if (e.state == ROW_LIVE && row_empty(t)) {
+            p = NEG_INF;
+        } else if (e.state == ROW_LIVE) {
+            p = row_logp<DT>(a, e, t);
+            v = e.w * terms(p, e.f[0], e.f[1], e.f[2]).loss;
+        }
+        logp[e.r] = p;
+        loss[e.r] = v;
+    }
+};
+
+// Teacher entries of a row in shared memory, k of each.
+struct TeacherRow {
+    int *id;    // column, -1: no entry, or merged into an earlier one
+    float *q;   // probability
+    float *lq;  // its logarithm
+    float *x;   // the student's logit
+};
 
 struct DistillArgs {
+    static constexpr bool STATS = true, TEACHER = true, GRADIENT = true;
     int k, vdtype;
     const int64_t *ids;
     const void *vals;
@@ -174,6 +330,109 @@ struct DistillArgs {
     const float *weight;  // may be NULL
     float gscale;
     float *loss, *stats;
+
+    __device__ void load(int64_t r, RowEntry &e) const
+    {
+        e.r = r;
+        e.w = weight ? weight[r] : 1.0f;
+    }
+    template <int DT>
+    __device__ void settle(const LogitRows &, RowEntry &e) const
+    {
+        e.state = e.w != 0.0f ? ROW_LIVE : ROW_OUT;
+    }
+    template <int DT>
+    __device__ RowGrad grad(const LogitRows &a, const RowEntry &e, SoftStat t, float Q) const
+    {
+        const float s2 = a.scale * LOG2E, c = e.w * gscale * a.scale;
+        return RowGrad{1.0f, -t.m, s2, c * Q / t.l, 0.0f, -1, row_empty(t)};
+    }
+    template <int DT>
+    __device__ void write(const LogitRows &, const RowEntry &, SoftStat) const {}
+
+    // Teacher probabilities of a row, by a whole warp; returns Q = sum q.
+    template <int DT>
+    __device__ float prepare(const LogitRows &a, int64_t r, TeacherRow s) const
+    {
+        const int lane = threadIdx.x & 31;
+        float vmax = NEG_INF;
+        for (int i = lane; i < k; i += 32) {
+            const int64_t id = ids[r * k + i];
+            const bool ok = valid_id(id, a.len);
+            const float v = ok ? load_any(vdtype, vals, r * k + i) * a.scale : NEG_INF;
+            s.id[i] = ok ? (int)id : -1;
+            s.lq[i] = v;
+            s.x[i] = ok ? load_elem<DT>(a.x, r * a.ld + id) : 0.0f;
+            vmax = fmaxf(vmax, v);
+        }
+        float norm;
+        if (lse) {
+            norm = lse[r];
+        } else {
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+            float sum = 0.0f;
+            for (int i = lane; i < k; i += 32)
+                sum += expf(s.lq[i] - ref_of(vmax));
+            sum = warp_sum(sum);
+            norm = vmax == NEG_INF && sum == 0.0f ? 0.0f : vmax + logf(sum);
+        }
+        float Q = 0.0f;
+        for (int i = lane; i < k; i += 32) {
+            const float lq = s.lq[i] - norm;
+            const float q = s.id[i] < 0 ? 0.0f : expf(lq);
+            s.lq[i] = lq;
+            s.q[i] = q;
+            Q += q;
+        }
+        __syncwarp();
+        return warp_sum(Q);
+    }
+    // The row's loss, by a whole warp; `t` holds the student's statistics.
+    __device__ void finish(const LogitRows &a, const RowEntry &e, SoftStat t, TeacherRow s) const
+    {
+        const int lane = threadIdx.x & 31;
+        float v = 0.0f;
+        if (e.state == ROW_LIVE && !row_empty(t)) {
+            const float ln = logf(t.l);
+            for (int i = lane; i < k; i += 32)
+                if (s.q[i] != 0.0f)
+                    v += s.q[i] * (s.lq[i] - ((s.x[i] - t.m) * a.scale - ln));
+            v = warp_sum(v) * e.w;
+        }
+        if (lane == 0)
+            loss[e.r] = v;
+    }
+    // The teacher's columns of the gradient once more, by a whole warp after
+    // the rest of the row is written: g_id = mul 2^(...) - c q.  An id that
+    // comes more than once is written by its first entry.
+    template <int DT>
+    __device__ void patch(const LogitRows &a, const RowEntry &e, RowGrad g, TeacherRow s) const
+    {
+        const float c = e.w * gscale * a.scale;
+        for (int i = threadIdx.x & 31; i < k; i += 32) {
+            const int id = s.id[i];
+            if (id < 0)
+                continue;
+            float q = 0.0f;
+            bool first = true;
+            for (int j = 0; j < k; ++j)
+                if (s.id[j] == id) {
+                    first = first && j >= i;
+                    q += s.q[j];
+                }
+            if (first)
+                store_elem<DT>(a.dx, e.r * a.ldd + id, g.mul * ex2(fmaf(s.x[i], g.fa, g.fb) * g.fc) - c * q);
+        }
+    }
+    static __device__ __forceinline__ float warp_sum(float v)
+    {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            v += __shfl_xor_sync(0xffffffffu, v, off);
+        return v;
+    }
 };
 
 struct PreferenceArgs {
@@ -188,8 +447,7 @@ struct PreferenceArgs {
 
 // Launchers: arguments have been validated by the entry points.
 int launch_logprob(int dtype, const LogitRows &a, const LogprobArgs &p, cudaStream_t s);
-int launch_logprob_grad(int dtype, const LogitRows &a, const int64_t *target, const float *lse, const float *dlogp,
-                        cudaStream_t s);
+int launch_logprob_grad(int dtype, const LogitRows &a, const LogprobGradArgs &p, cudaStream_t s);
 int launch_policy(int dtype, const LogitRows &a, const PolicyArgs &p, cudaStream_t s);
 int launch_distill(int dtype, const LogitRows &a, const DistillArgs &p, cudaStream_t s);
 int launch_preference(int dtype, const LogitRows &a, const PreferenceArgs &p, cudaStream_t s);

@@ -552,6 +552,49 @@ def test_side_stream_and_graph():
             assert all(torch.equal(u, v) for u, v in zip(a, b))
 
 
+@pytest.mark.parametrize("dtype,length", [(torch.float32, 200001), (torch.float32, 65536), (torch.bfloat16, 131072),
+                                          (torch.float16, 50257), (torch.bfloat16, 20000), (torch.float32, 3001)])
+def test_many_rows_per_cta(dtype, length):
+    """Several rows per CTA at lengths that fit the kernel's shared memory
+    several times, about once and not at all; live and ignored rows mixed."""
+    rows = 1000 if length < 60000 else 480
+    g = torch.Generator(device=DEV)
+    g.manual_seed(length)
+    x = (torch.randn((rows, length), generator=g, device=DEV) * 3).to(dtype)
+    t = torch.randint(0, length, (rows,), generator=g, device=DEV)
+    t[torch.rand(rows, generator=g, device=DEV) < 0.4] = -1
+    old = torch.full((rows,), -10.0, device=DEV)
+    adv = torch.randn(rows, generator=g, device=DEV)
+    ids = torch.randint(0, length, (rows, 40), generator=g, device=DEV)
+    vals = torch.randn((rows, 40), generator=g, device=DEV)
+    w = torch.rand(rows, generator=g, device=DEV)
+    w[::3] = 0.0
+    logp, lse = itr.red_logprob(x, t)
+    _, _, _, pgrad = itr.red_policy(x, t, old, adv, clip_high=1e4)
+    _, _, dgrad = itr.red_distill(x, ids, vals, weight=w)
+    for lo in range(0, rows, 40):
+        part = slice(lo, lo + 40)
+        z = x[part].double()
+        norm = torch.logsumexp(z, 1)
+        p = (z - norm[:, None]).exp()
+        live = t[part] >= 0
+        at = t[part].clamp(min=0)
+        i = torch.arange(z.shape[0], device=DEV)
+        want = torch.where(live, z[i, at] - norm, torch.zeros_like(norm))
+        ref.assert_logp(logp[part], want, "logp")
+        ref.assert_logp(lse[part], torch.where(live, norm, torch.zeros_like(norm)), "lse")
+        free = (want + 10.0).exp() * adv[part].double()
+        held = (want + 10.0).exp().clamp(0.8, 1e4 + 1) * adv[part].double()
+        c = torch.where(live & (free <= held), -free, torch.zeros_like(free))
+        grad = -p * c[:, None]
+        grad[i, at] += c
+        ref.assert_grad(pgrad[part], grad, p.cpu(), c.cpu(), at.cpu(), extra=3e-5, what="policy")
+        q = torch.softmax(vals[part].double(), 1)
+        mass = torch.zeros_like(p).scatter_add_(1, ids[part], q)
+        wd = w[part].double()
+        ref.assert_grad(dgrad[part], (p - mass) * wd[:, None], (p + mass).cpu(), wd.cpu(), extra=3e-5, what="distill")
+
+
 def test_offsets_past_32_bits():
     """Rows whose elements start beyond 2^32 in the logits and in the gradient."""
     length = 65536
