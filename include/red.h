@@ -342,7 +342,7 @@ int red_full_noalloc(int op, const float *x, int64_t n, float *out, red_stream_t
  *   rows, len, ld   x[r, j] is at x + r * ld + j; 1 <= len <= 2^30, ld >= len;
  *            x needs the alignment of its elements only, and neither it nor
  *            dx is touched between columns len and ld.
- *   scale    > 0, finite.
+ *   scale    1e-30 .. 1e30.
  *   dx, ldd  the gradient, rows of stride ldd >= len; may be x itself
  *            (ldd == ld then) and must not overlap it otherwise; NULL where a
  *            call allows it computes the loss alone.

@@ -2,15 +2,20 @@
 // (red_logprob, red_distill, red_policy, red_preference).
 //
 // Every loss is a function of the scaled logits z = scale * x of a row
-// through its log-softmax.  A row is reduced to its maximum m (of the raw
-// logits) and l = sum_j 2^((x_j - m) * s2), s2 = scale * log2(e), so that
-//     logp_y = scale * (x_y - m) - ln l,   lse = scale * m + ln l,
-//     p_j    = 2^((x_j - m) * s2) / l.
-// The difference x_j - m is taken before the product: a product first could
-// overflow for logits near the type's lowest value (an additive mask) and
-// leave inf - inf, and the difference keeps the argument's error relative to
-// the distance from the maximum.  Partial (m, l) pairs combine by rescaling
-// to the larger maximum; where no logit is finite m = -inf and l = 0.
+// through its log-softmax.  With s2 = scale * log2(e) a row is reduced to its
+// maximum m and
+//     l = sum_j 2^(x_j * s2 - M),   M = m * s2 rounded to fp32,
+// one multiply-add and one exponential per element.  The rounding of M, m *
+// s2 - M = lo, is a common factor 2^lo of every term, taken back out where a
+// logarithm is formed:
+//     logp_y = scale * (x_y - m) - (ln l - lo ln 2),
+//     lse    = scale * m + (ln l - lo ln 2),
+//     p_j    = 2^(x_j * s2 - M) / l.
+// Beyond |M| = 2^24 (a row that is nothing but the type's lowest value, say,
+// as an additive mask leaves it) lo would no longer be small, and products of
+// x overflow; there the terms are 2^((x_j - m) * s2), difference first.
+// Partial (m, l) pairs combine by rescaling to the larger maximum; where no
+// logit is finite m = -inf and l = 0.
 #pragma once
 
 #include <cstdint>
@@ -34,6 +39,8 @@ struct LogitRows {
     int64_t ldd;
     int len;
     float scale;
+    float s2;          // scale * log2(e), rounded
+    float r_hi, r_lo;  // s2 / scale in two floats
 };
 
 __device__ __forceinline__ float ex2(float v)
@@ -74,31 +81,100 @@ struct SoftStat {
     float m, l;
 };
 
-// The reference point of exponentials under the maximum m: m itself, or 0
-// where nothing is finite yet (so that -inf - m stays -inf and a NaN logit
-// still reaches the sum).
-__device__ __forceinline__ float ref_of(float m) { return m == NEG_INF ? 0.0f : m; }
+constexpr float FAR = 16777216.0f;  // 2^24: the largest |M| of the multiply-add form
+
+// The multiply-add form does for the maximum m (m * s2 = m2; not for a NaN).
+__device__ __forceinline__ bool is_near(float m2) { return fabsf(m2) <= FAR; }
+
+// Factor of a sum under the maximum `from` when the maximum becomes `to`.
+__device__ __forceinline__ float soft_factor(float from, float to, float s2)
+{
+    if (from == to)
+        return 1.0f;
+    const float m2 = to * s2;
+    return ex2(is_near(m2) ? from * s2 - m2 : (from - to) * s2);
+}
 
 __device__ __forceinline__ SoftStat soft_join(SoftStat a, SoftStat b, float s2)
 {
-    SoftStat r;
-    r.m = fmaxf(a.m, b.m);
-    const float m = ref_of(r.m);
-    r.l = a.l * ex2((a.m - m) * s2) + b.l * ex2((b.m - m) * s2);
-    return r;
+    const float m = fmaxf(a.m, b.m);
+    return SoftStat{m, a.l * soft_factor(a.m, m, s2) + b.l * soft_factor(b.m, m, s2)};
 }
 
+// The largest of the lanes' values (no NaN), by the integer reduction: the
+// bits of floats compare like integers once those of negative ones are turned
+// around.
+__device__ __forceinline__ float warp_max(float v)
+{
+    int b = __float_as_int(v + 0.0f);  // -0 becomes +0
+    b ^= (b >> 31) & 0x7fffffff;
+    b = __reduce_max_sync(0xffffffffu, b);
+    return __int_as_float(b ^ ((b >> 31) & 0x7fffffff));
+}
+
+// The join over groups of W lanes that hold the same W values, in every lane:
+// the maximum first, then one rescaling and the sum.
+template <int W = 32>
 __device__ __forceinline__ SoftStat soft_warp(SoftStat a, float s2)
 {
+    const float m = warp_max(a.m);
+    float l = a.l * soft_factor(a.m, m, s2);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        SoftStat b;
-        b.m = __shfl_xor_sync(0xffffffffu, a.m, off);
-        b.l = __shfl_xor_sync(0xffffffffu, a.l, off);
-        a = soft_join(a, b, s2);
-    }
-    return a;
+    for (int off = W / 2; off > 0; off >>= 1)
+        l += __shfl_xor_sync(0xffffffffu, l, off);
+    return SoftStat{m, l};
 }
+
+// A row's statistics as the losses use them.
+struct RowStat {
+    float m, m2;  // maximum, and M
+    float l;      // the sum of terms
+    float ln;     // logarithm of the sum relative to m itself
+    bool far;     // terms are 2^((x - m) * s2)
+    bool empty;   // every logit is -inf
+};
+
+__device__ __forceinline__ RowStat row_stat(const LogitRows &a, SoftStat t)
+{
+    RowStat s;
+    s.m = t.m;
+    s.l = t.l;
+    s.m2 = t.m * a.s2;
+    s.far = !is_near(s.m2);
+    s.empty = t.m == NEG_INF && t.l == 0.0f;
+    s.ln = logf(t.l);
+    if (!s.far)
+        s.ln = fmaf(-0.69314718f, fmaf(t.m, a.s2, -s.m2), s.ln);
+    return s;
+}
+
+// ------------------------------------------------------------------- sums
+
+// A sum in two floats, s + c: each addition's rounding error is computed
+// (Knuth's two-sum) and carried along, so that the order of a long sum costs
+// nothing and 64-bit arithmetic, 1/64 of the fp32 rate here, is not needed.
+struct Sum {
+    float s = 0.0f, c = 0.0f;
+
+    __device__ __forceinline__ void add(float x)
+    {
+        const float t = s + x, z = t - s;
+        c += (s - (t - z)) + (x - z);
+        s = t;
+    }
+    __device__ __forceinline__ void add(const Sum &o)
+    {
+        add(o.s);
+        c += o.c;
+    }
+    __device__ __forceinline__ void join_warp()
+    {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            add(Sum{__shfl_xor_sync(0xffffffffu, s, off), __shfl_xor_sync(0xffffffffu, c, off)});
+    }
+    __device__ __forceinline__ float value() const { return isfinite(s) ? s + c : s; }
+};
 
 // ------------------------------------------------------------- the losses
 
@@ -145,25 +221,44 @@ __device__ __forceinline__ uint32_t load_bits(const void *p, int64_t i)
 }
 
 // The gradient of a row: g_j = mul * 2^(fma(x_j, fa, fb) * fc) + [j == y] cy,
-// or zeros throughout.
+// or zeros throughout.  fc is 1 unless `far`.
 struct RowGrad {
     float fa, fb, fc, mul, cy;
     int y;
-    bool zero;
+    bool zero, far;
 };
 
-__device__ __forceinline__ bool row_empty(SoftStat t) { return t.m == NEG_INF && t.l == 0.0f; }
-
-// c * ([j == y] - p_j) from the row's statistics.
-__device__ __forceinline__ RowGrad grad_of_target(const LogitRows &a, SoftStat t, int y, float c)
+// mul * 2^(...) = c * p_j.
+__device__ __forceinline__ RowGrad grad_of_stat(const LogitRows &a, const RowStat &t, float c)
 {
-    return RowGrad{1.0f, -t.m, a.scale * LOG2E, -c / t.l, c, y, row_empty(t) || c == 0.0f};
+    RowGrad g;
+    g.far = t.far;
+    g.fa = t.far ? 1.0f : a.s2;
+    g.fb = t.far ? -t.m : -t.m2;
+    g.fc = t.far ? a.s2 : 1.0f;
+    g.mul = c / t.l;
+    g.cy = 0.0f;
+    g.y = -1;
+    g.zero = t.empty;
+    return g;
+}
+
+// c * ([j == y] - p_j).
+__device__ __forceinline__ RowGrad grad_of_target(const LogitRows &a, const RowStat &t, int y, float c)
+{
+    RowGrad g = grad_of_stat(a, t, -c);
+    g.cy = c;
+    g.y = y;
+    g.zero = t.empty || c == 0.0f;
+    return g;
 }
 
 // Each loss below gives the kernels
 //   STATS    whether a row's statistics come from its logits;
 //   TEACHER  whether it has a list of teacher entries per row;
 //   GRADIENT whether it can have a gradient;
+//   TOTALS   how many sums over rows it has: total() adds a row's terms,
+//            stats is where they go;
 //   load()   the row's entry (its logits are still intact): issues loads and
 //            uses none of their values, so that a later settle() may be the
 //            first to wait for them;
@@ -174,6 +269,7 @@ __device__ __forceinline__ RowGrad grad_of_target(const LogitRows &a, SoftStat t
 
 struct LogprobArgs {
     static constexpr bool STATS = true, TEACHER = false, GRADIENT = false;
+    static constexpr int TOTALS = 0;
     const int64_t *target;
     float *logp, *lse;
 
@@ -190,15 +286,14 @@ struct LogprobArgs {
             e.xy = load_bits<DT>(a.x, e.r * a.ld + e.target);
     }
     template <int DT>
-    __device__ RowGrad grad(const LogitRows &, const RowEntry &, SoftStat, float) const { return RowGrad{}; }
+    __device__ RowGrad grad(const LogitRows &, const RowEntry &, const RowStat &, float) const { return RowGrad{}; }
     template <int DT>
-    __device__ void write(const LogitRows &a, const RowEntry &e, SoftStat t) const
+    __device__ void write(const LogitRows &a, const RowEntry &e, const RowStat &t) const
     {
         float p = 0.0f, n = 0.0f;
         if (e.state == ROW_LIVE) {
-            const float ln = logf(t.l);
-            n = row_empty(t) ? NEG_INF : fmaf(a.scale, t.m, ln);
-            p = row_empty(t) ? NEG_INF : (Elem<DT>::widen(e.xy) - t.m) * a.scale - ln;
+            n = t.empty ? NEG_INF : fmaf(a.scale, t.m, t.ln);
+            p = t.empty ? NEG_INF : (Elem<DT>::widen(e.xy) - t.m) * a.scale - t.ln;
         }
         logp[e.r] = p;
         lse[e.r] = n;
@@ -207,6 +302,7 @@ struct LogprobArgs {
 
 struct LogprobGradArgs {
     static constexpr bool STATS = false, TEACHER = false, GRADIENT = true;
+    static constexpr int TOTALS = 0;
     const int64_t *target;
     const float *lse, *dlogp;
 
@@ -222,16 +318,27 @@ struct LogprobGradArgs {
     {
         e.state = valid_id(e.target, a.len) && e.w != 0.0f && e.f[0] != NEG_INF ? ROW_LIVE : ROW_OUT;
     }
-    // p_j = 2^((scale x_j - lse) log2 e): the difference in one rounding, so
-    // that it is exact where p_j is near 1.
+    // p_j = 2^(x_j * s2 - lse * s2 / scale), the same rounding of s2 in both
+    // products; what the second one rounds away goes into the factor.  Far
+    // from zero: 2^((scale x_j - lse) log2 e), the difference in one rounding.
     template <int DT>
-    __device__ RowGrad grad(const LogitRows &a, const RowEntry &e, SoftStat, float) const
+    __device__ RowGrad grad(const LogitRows &a, const RowEntry &e, const RowStat &, float) const
     {
-        const float c = e.w * a.scale;
-        return RowGrad{a.scale, -e.f[0], LOG2E, -c, c, (int)e.target, false};
+        const float n = e.f[0], c = e.w * a.scale;
+        const float hi = n * a.r_hi, lo = fmaf(n, a.r_lo, fmaf(n, a.r_hi, -hi));
+        RowGrad g;
+        g.far = !is_near(hi);
+        g.fa = g.far ? a.scale : a.s2;
+        g.fb = g.far ? -n : -hi;
+        g.fc = g.far ? LOG2E : 1.0f;
+        g.mul = g.far ? -c : -c * ex2(-lo);
+        g.cy = c;
+        g.y = (int)e.target;
+        g.zero = false;
+        return g;
     }
     template <int DT>
-    __device__ void write(const LogitRows &, const RowEntry &, SoftStat) const {}
+    __device__ void write(const LogitRows &, const RowEntry &, const RowStat &) const {}
 };
 
 struct PolicyTerms {
@@ -243,6 +350,7 @@ struct PolicyTerms {
 
 struct PolicyArgs {
     static constexpr bool STATS = true, TEACHER = false, GRADIENT = true;
+    static constexpr int TOTALS = 4;
     const int64_t *target;
     const float *old_logp, *ref_logp, *adv, *weight;  // ref_logp, weight may be NULL
     float clip_low, clip_high, kl, gscale;
@@ -288,21 +396,21 @@ struct PolicyArgs {
             e.xy = load_bits<DT>(a.x, e.r * a.ld + e.target);
     }
     template <int DT>
-    __device__ float row_logp(const LogitRows &a, const RowEntry &e, SoftStat t) const
+    __device__ float row_logp(const LogitRows &a, const RowEntry &e, const RowStat &t) const
     {
-        return (Elem<DT>::widen(e.xy) - t.m) * a.scale - logf(t.l);
+        return (Elem<DT>::widen(e.xy) - t.m) * a.scale - t.ln;
     }
     template <int DT>
-    __device__ RowGrad grad(const LogitRows &a, const RowEntry &e, SoftStat t, float) const
+    __device__ RowGrad grad(const LogitRows &a, const RowEntry &e, const RowStat &t, float) const
     {
         const PolicyTerms q = terms(row_logp<DT>(a, e, t), e.f[0], e.f[1], e.f[2]);
         return grad_of_target(a, t, (int)e.target, e.w * q.dlogp * gscale * a.scale);
     }
     template <int DT>
-    __device__ void write(const LogitRows &a, const RowEntry &e, SoftStat t) const
+    __device__ void write(const LogitRows &a, const RowEntry &e, const RowStat &t) const
     {
         float p = 0.0f, v = 0.0f;
-        if (e.state == ROW_LIVE && row_empty(t)) {
+        if (e.state == ROW_LIVE && t.empty) {
             p = NEG_INF;
         } else if (e.state == ROW_LIVE) {
             p = row_logp<DT>(a, e, t);
@@ -310,6 +418,19 @@ struct PolicyArgs {
         }
         logp[e.r] = p;
         loss[e.r] = v;
+    }
+    __device__ void total(int64_t r, int len, Sum (&v)[TOTALS]) const
+    {
+        const float w = weight ? weight[r] : 1.0f, p = __ldcg(logp + r);
+        if (!valid_id(target[r], len) || w == 0.0f)
+            return;
+        v[0].add(__ldcg(loss + r));
+        v[3].add(w);
+        if (p == NEG_INF)  // no ratio or drift to speak of
+            return;
+        const PolicyTerms q = terms(p, old_logp[r], ref_logp ? ref_logp[r] : 0.0f, adv[r]);
+        v[1].add(w * q.drift);
+        v[2].add(w * q.clipped);
     }
 };
 
@@ -323,6 +444,7 @@ struct TeacherRow {
 
 struct DistillArgs {
     static constexpr bool STATS = true, TEACHER = true, GRADIENT = true;
+    static constexpr int TOTALS = 2;
     int k, vdtype;
     const int64_t *ids;
     const void *vals;
@@ -342,13 +464,12 @@ struct DistillArgs {
         e.state = e.w != 0.0f ? ROW_LIVE : ROW_OUT;
     }
     template <int DT>
-    __device__ RowGrad grad(const LogitRows &a, const RowEntry &e, SoftStat t, float Q) const
+    __device__ RowGrad grad(const LogitRows &a, const RowEntry &e, const RowStat &t, float Q) const
     {
-        const float s2 = a.scale * LOG2E, c = e.w * gscale * a.scale;
-        return RowGrad{1.0f, -t.m, s2, c * Q / t.l, 0.0f, -1, row_empty(t)};
+        return grad_of_stat(a, t, e.w * gscale * a.scale * Q);
     }
     template <int DT>
-    __device__ void write(const LogitRows &, const RowEntry &, SoftStat) const {}
+    __device__ void write(const LogitRows &, const RowEntry &, const RowStat &) const {}
 
     // Teacher probabilities of a row, by a whole warp; returns Q = sum q.
     template <int DT>
@@ -374,7 +495,7 @@ struct DistillArgs {
                 vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
             float sum = 0.0f;
             for (int i = lane; i < k; i += 32)
-                sum += expf(s.lq[i] - ref_of(vmax));
+                sum += expf(s.lq[i] - (vmax == NEG_INF ? 0.0f : vmax));
             sum = warp_sum(sum);
             norm = vmax == NEG_INF && sum == 0.0f ? 0.0f : vmax + logf(sum);
         }
@@ -390,30 +511,29 @@ struct DistillArgs {
         return warp_sum(Q);
     }
     // The row's loss, by a whole warp; `t` holds the student's statistics.
-    __device__ void finish(const LogitRows &a, const RowEntry &e, SoftStat t, TeacherRow s) const
+    __device__ void finish(const LogitRows &a, const RowEntry &e, const RowStat &t, TeacherRow s) const
     {
         const int lane = threadIdx.x & 31;
         float v = 0.0f;
-        if (e.state == ROW_LIVE && !row_empty(t)) {
-            const float ln = logf(t.l);
+        if (e.state == ROW_LIVE && !t.empty) {
             for (int i = lane; i < k; i += 32)
                 if (s.q[i] != 0.0f)
-                    v += s.q[i] * (s.lq[i] - ((s.x[i] - t.m) * a.scale - ln));
+                    v += s.q[i] * (s.lq[i] - ((s.x[i] - t.m) * a.scale - t.ln));
             v = warp_sum(v) * e.w;
         }
         if (lane == 0)
             loss[e.r] = v;
     }
     // The teacher's columns of the gradient once more, by a whole warp after
-    // the rest of the row is written: g_id = mul 2^(...) - c q.  An id that
-    // comes more than once is written by its first entry.
+    // the rest of the columns [begin, end) is written: g_id = mul 2^(...) - c q.
+    // An id that comes more than once is written by its first entry.
     template <int DT>
-    __device__ void patch(const LogitRows &a, const RowEntry &e, RowGrad g, TeacherRow s) const
+    __device__ void patch(const LogitRows &a, const RowEntry &e, RowGrad g, TeacherRow s, int begin, int end) const
     {
         const float c = e.w * gscale * a.scale;
         for (int i = threadIdx.x & 31; i < k; i += 32) {
             const int id = s.id[i];
-            if (id < 0)
+            if (id < begin || id >= end)
                 continue;
             float q = 0.0f;
             bool first = true;
@@ -425,6 +545,11 @@ struct DistillArgs {
             if (first)
                 store_elem<DT>(a.dx, e.r * a.ldd + id, g.mul * ex2(fmaf(s.x[i], g.fa, g.fb) * g.fc) - c * q);
         }
+    }
+    __device__ void total(int64_t r, int, Sum (&v)[TOTALS]) const
+    {
+        v[0].add(__ldcg(loss + r));
+        v[1].add(weight ? weight[r] : 1.0f);
     }
     static __device__ __forceinline__ float warp_sum(float v)
     {

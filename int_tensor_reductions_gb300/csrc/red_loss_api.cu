@@ -29,8 +29,8 @@ int logit_rows(const char *who, int dtype, const void *x, int64_t rows, int64_t 
     if (ld < len || ld > MAX_ELEMS || (rows > 0 && ld > MAX_ELEMS / rows))
         return fail(RED_EINVAL, "%s: row stride ld = %lld must be >= len = %lld and rows * ld in range", who,
                     (long long)ld, (long long)len);
-    if (!(scale > 0.0f) || std::isinf(scale))
-        return fail(RED_EINVAL, "%s: scale must be positive and finite", who);
+    if (!(scale >= 1e-30f && scale <= 1e30f))
+        return fail(RED_EINVAL, "%s: scale must be in 1e-30..1e30", who);
     if (dx || need_dx) {
         if (ldd < len || ldd > MAX_ELEMS || (rows > 0 && ldd > MAX_ELEMS / rows))
             return fail(RED_EINVAL, "%s: gradient row stride ldd = %lld must be >= len = %lld and rows * ldd in range",
@@ -44,7 +44,10 @@ int logit_rows(const char *who, int dtype, const void *x, int64_t rows, int64_t 
         if (need_dx ? bad_ptr(dx, elem_size(dtype)) : bad_opt(dx, elem_size(dtype)))
             return fail(RED_EINVAL, "%s: dx is NULL or not aligned to its element size", who);
     }
-    *a = LogitRows{x, rows, ld, dx, ldd, (int)len, scale};
+    const double log2e = 1.4426950408889634074;
+    const float s2 = (float)(scale * log2e);
+    const double ratio = (double)s2 / scale;
+    *a = LogitRows{x, rows, ld, dx, ldd, (int)len, scale, s2, (float)ratio, (float)(ratio - (double)(float)ratio)};
     return RED_OK;
 }
 

@@ -14,10 +14,11 @@
 // first batches after the statistics and has them fetched again for the
 // gradient (from L2: they are a few microseconds old).
 //
-// A service warp takes rows, reads their scalars (target, weight, the
-// target's logit) ahead into a queue, and writes the losses; teacher warps
-// do the same for the rows' lists of teacher entries.  One CTA barrier per
-// row joins the statistics and hands the queue over.
+// A scheduler warp takes rows and reads their scalars (target, weight, the
+// target's logit) ahead into a queue; a writer warp writes the losses, and
+// zeros over the gradient of rows out of the loss; for the distillation
+// teacher warps do that and read the rows' lists of teacher entries.  One CTA barrier per row joins the statistics and hands
+// the queue over.
 #pragma once
 
 #include <type_traits>
@@ -33,37 +34,60 @@ namespace red {
 template <int DT>
 constexpr int VEC_ELEMS = DT == RED_F32 ? 4 : 8;  // in 16 bytes
 
-__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b)
+// Two floats in one 64-bit register pair, the operand of Blackwell's packed
+// fp32 instructions.
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pack2(float a, float b)
 {
-    float2 d;
-    asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
     return d;
 }
-__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c)
+__device__ __forceinline__ float2 unpack2(f32x2 v)
 {
     float2 d;
-    asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; "
-        "fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w; }"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
     return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f32x2 exp2_2(f32x2 v)
+{
+    const float2 f = unpack2(v);
+    return pack2(ex2(f.x), ex2(f.y));
 }
 
 // Pair i of a vector, widened.
 template <int DT>
-__device__ __forceinline__ float2 vec_pair(const uint4 &v, int i)
+__device__ __forceinline__ f32x2 vec_pair(const uint4 &v, int i)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    if constexpr (DT == RED_F32)
-        return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-    else if constexpr (DT == RED_BF16)
-        return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-    else {
+    if constexpr (DT == RED_F32) {
+        return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    } else if constexpr (DT == RED_BF16) {
+        return pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
         __half2 h;
         memcpy(&h, &w[i], 4);
-        return __half22float2(h);
+        const float2 f = __half22float2(h);
+        return pack2(f.x, f.y);
     }
 }
 
@@ -87,23 +111,22 @@ __device__ __forceinline__ float vec_max(const uint4 &v)
 }
 
 template <int DT>
-__device__ __forceinline__ uint4 vec_pack(const float2 (&f)[VEC_ELEMS<DT> / 2])
+__device__ __forceinline__ uint4 vec_pack(const f32x2 (&f)[VEC_ELEMS<DT> / 2])
 {
     uint4 v;
     if constexpr (DT == RED_F32) {
-        v = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
-                       __float_as_uint(f[1].y));
+        memcpy(&v, f, 16);
     } else if constexpr (DT == RED_BF16) {
         __nv_bfloat162 h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            h[i] = __float22bfloat162_rn(f[i]);
+            h[i] = __float22bfloat162_rn(unpack2(f[i]));
         memcpy(&v, h, 16);
     } else {
         __half2 h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            h[i] = __float22half2_rn(f[i]);
+            h[i] = __float22half2_rn(unpack2(f[i]));
         memcpy(&v, h, 16);
     }
     return v;
@@ -112,53 +135,81 @@ __device__ __forceinline__ uint4 vec_pack(const float2 (&f)[VEC_ELEMS<DT> / 2])
 // Running statistics of one thread; the sum in two lanes.
 struct SoftRun {
     float m;
-    float2 l;
+    f32x2 l;
 
     __device__ __forceinline__ void init()
     {
         m = NEG_INF;
-        l = make_float2(0.0f, 0.0f);
+        l = pack2(0.0f, 0.0f);
     }
     __device__ __forceinline__ void raise(float to, float s2)
     {
         to = fmaxf(m, to);
-        const float f = ex2((m - ref_of(to)) * s2);
-        l = make_float2(l.x * f, l.y * f);
+        const float f = soft_factor(m, to, s2);
+        l = mul2(l, pack2(f, f));
         m = to;
     }
-    template <int DT>
-    __device__ __forceinline__ void add(const uint4 &v, float s2)
+    // n vectors, none of whose elements is above m
+    template <int DT, int N>
+    __device__ __forceinline__ void add(const uint4 (&v)[N], float s2)
     {
-        const float at = ref_of(m);
+        const float m2 = m * s2;
+        if (is_near(m2)) {
+            const f32x2 a = pack2(s2, s2), b = pack2(-m2, -m2);
 #pragma unroll
-        for (int i = 0; i < VEC_ELEMS<DT> / 2; ++i) {
-            const float2 d = mul_f32x2(add_f32x2(vec_pair<DT>(v, i), make_float2(-at, -at)), make_float2(s2, s2));
-            l = add_f32x2(l, make_float2(ex2(d.x), ex2(d.y)));
+            for (int u = 0; u < N; ++u)
+#pragma unroll
+                for (int i = 0; i < VEC_ELEMS<DT> / 2; ++i)
+                    l = add2(l, exp2_2(fma2(vec_pair<DT>(v[u], i), a, b)));
+        } else {
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+                l = far_sum<DT>(v[u], m, s2, l);
         }
     }
-    __device__ __forceinline__ void add(float v, float s2) { l.x += ex2((v - ref_of(m)) * s2); }
-    __device__ __forceinline__ SoftStat stat() const { return SoftStat{m, l.x + l.y}; }
+    __device__ __forceinline__ void add(float x, float s2) { l = add2(l, pack2(ex2(term(x, m, s2)), 0.0f)); }
+    // exponent of one logit under the maximum m, near or far
+    static __device__ __forceinline__ float term(float x, float m, float s2)
+    {
+        const float m2 = m * s2;
+        // (nothing finite yet: -inf is no term, and a NaN is one)
+        return is_near(m2) ? fmaf(x, s2, -m2) : (m == NEG_INF ? x : (x - m) * s2);
+    }
+    template <int DT>
+    static __device__ __noinline__ f32x2 far_sum(uint4 v, float m, float s2, f32x2 l)
+    {
+        for (int i = 0; i < VEC_ELEMS<DT> / 2; ++i) {
+            const float2 x = unpack2(vec_pair<DT>(v, i));
+            l = add2(l, pack2(ex2(term(x.x, m, s2)), ex2(term(x.y, m, s2))));
+        }
+        return l;
+    }
+    __device__ __forceinline__ SoftStat stat() const
+    {
+        const float2 f = unpack2(l);
+        return SoftStat{m, f.x + f.y};
+    }
 };
 
 // The gradient of one vector of logits whose first column is j0.
-template <int DT>
+template <int DT, bool FAR_ROW = false>
 __device__ __forceinline__ uint4 vec_grad(const uint4 &v, const RowGrad &g, int j0)
 {
     constexpr int E = VEC_ELEMS<DT>;
-    float2 o[E / 2];
+    const f32x2 a = pack2(g.fa, g.fa), b = pack2(g.fb, g.fb), m = pack2(g.mul, g.mul);
+    f32x2 o[E / 2];
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {
-        const float2 d = mul_f32x2(fma_f32x2(vec_pair<DT>(v, i), make_float2(g.fa, g.fa), make_float2(g.fb, g.fb)),
-                                   make_float2(g.fc, g.fc));
-        o[i] = mul_f32x2(make_float2(ex2(d.x), ex2(d.y)), make_float2(g.mul, g.mul));
+        f32x2 t = fma2(vec_pair<DT>(v, i), a, b);
+        if (FAR_ROW)
+            t = mul2(t, pack2(g.fc, g.fc));
+        o[i] = mul2(exp2_2(t), m);
     }
     const unsigned at = (unsigned)(g.y - j0);
     if (at < (unsigned)E) {
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            o[i].x += at == 2 * i ? g.cy : 0.0f;
-            o[i].y += at == 2 * i + 1 ? g.cy : 0.0f;
-        }
+        for (int i = 0; i < E / 2; ++i)
+            o[i] = add2(o[i], pack2(at == 2 * i ? g.cy : 0.0f, at == 2 * i + 1 ? g.cy : 0.0f));
     }
     return vec_pack<DT>(o);
 }
@@ -236,7 +287,7 @@ __device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity)
 
 // No wait is without end: one that runs out (which takes a hardware fault)
 // marks the CTA as failed, and its rows' results become NaN.
-constexpr int WAIT_TRIES = 1 << 20;
+constexpr int WAIT_TRIES = 1 << 26;
 
 __device__ __forceinline__ void mbar_wait(uint64_t *bar, uint32_t parity, volatile int *failed)
 {
@@ -247,6 +298,30 @@ __device__ __forceinline__ void mbar_wait(uint64_t *bar, uint32_t parity, volati
         }
 }
 
+// ---- clusters
+
+__device__ __forceinline__ int cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return (int)r;
+}
+__device__ __forceinline__ int cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return (int)r;
+}
+// The same shared variable in CTA `rank` of the cluster.
+template <class V>
+__device__ __forceinline__ V *in_cta(V *p, int rank)
+{
+    uint64_t d;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(d) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<V *>(d);
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // `bytes` (a multiple of 16) from src to shared memory; both 16-byte aligned.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
@@ -255,6 +330,38 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  "l"(src), "r"(bytes), "r"(smem_addr(bar))
                  : "memory");
 }
+
+// `bytes` (a multiple of 16) from shared memory to dst, in this thread's
+// current bulk group.
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+constexpr int ZERO_BYTES = 4096;
+
+// Zeros over one row of the gradient, by a warp: bulk stores from a block of
+// zeros in shared memory, on their way while the CTA goes on.
+template <int DT>
+__device__ __forceinline__ void zero_row_bulk(typename Elem<DT>::T *g, int len, const void *zeros)
+{
+    constexpr int E = VEC_ELEMS<DT>;
+    const int lane = threadIdx.x & 31;
+    const int h = head_elems<DT>(g, len), nvec = (len - h) / E;
+    if (lane == 0) {
+        constexpr int STEP = ZERO_BYTES / 16;
+        for (int v = 0; v < nvec; v += STEP)
+            bulk_store(g + h + (int64_t)v * E, zeros, (uint32_t)min(STEP, nvec - v) * 16u);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    if (lane < h)
+        g[lane] = 0;
+    if (h + nvec * E + lane < len)
+        g[h + nvec * E + lane] = 0;
+}
+__device__ __forceinline__ void bulk_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 constexpr int ROW_Q = 32;      // entries of the row queue
 constexpr int ROW_MAX_GROUP = 4;
@@ -268,6 +375,7 @@ struct RowShared {
     SoftStat part[PARTS][NW];  // statistics of row i's warps in part[i % PARTS]
     float mass[TEACHERS];  // sum of a row's teacher probabilities
     uint64_t full[ROW_MAX_SLOTS], empty[ROW_MAX_SLOTS];
+    alignas(16) unsigned char zeros[ZERO_BYTES];
     int published;  // entries written to the queue
     int loading;    // entry the loader is at
     int failed;     // a wait ran out
@@ -279,7 +387,7 @@ template <class OP>
 constexpr int PARTS = OP::TEACHER ? 2 * TEACHERS : 2;
 
 template <class OP>
-constexpr int SERVICE_WARPS = OP::TEACHER ? 2 + TEACHERS : 2;  // service, loader, teachers
+constexpr int SERVICE_WARPS = OP::TEACHER ? 2 + TEACHERS : 3;  // scheduler, loader, teachers or writer
 
 __device__ __forceinline__ void bar_sync(int id, int n)
 {
@@ -303,6 +411,7 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
 {
     using T = typename Elem<DT>::T;
     constexpr int E = VEC_ELEMS<DT>, NW = NT / 32;
+    static_assert((NW & (NW - 1)) == 0 && NW <= 32, "the join of the warps' statistics");
     extern __shared__ __align__(16) unsigned char smem[];
     uint4 *const ring = reinterpret_cast<uint4 *>(smem);
     using Shared = RowShared<NW, PARTS<OP>>;
@@ -315,7 +424,7 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int AHEAD = OP::TEACHER ? TEACHERS : 2;
     const int fixed = 3 * group + AHEAD;
-    const float s2 = a.scale * LOG2E;
+    const float s2 = a.s2;
     pdl_enter();
 
     if (warp == NW && lane < fixed) {
@@ -328,6 +437,9 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
         }
         sh.queue[lane] = e;
     }
+    for (int i = tid; i < ZERO_BYTES / 16; i += blockDim.x)
+        reinterpret_cast<uint4 *>(sh.zeros)[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (tid == 0) {
         for (int i = 0; i < slots; ++i) {
             mbar_init(&sh.full[i], 1);
@@ -342,45 +454,45 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
     volatile int *const failed = &sh.failed;
     volatile int *const published = &sh.published, *const loading = &sh.loading;
 
-    // The barrier of row i: consumers, service warp and, of the teacher
-    // warps, the row's own.  (The loader runs ahead by the slots alone.)
-    auto row_barrier = [&](int i) {
-        if constexpr (OP::TEACHER)
-            bar_sync(1 + i % TEACHERS, NT + 64);
-        else
-            bar_sync(0, NT + 32);
-    };
+    // The barrier of row i: consumers, scheduler, and the writer or, of the
+    // teacher warps, the row's own.  (The loader runs ahead by the slots
+    // alone.)
+    auto row_barrier = [&](int i) { bar_sync(OP::TEACHER ? 1 + i % TEACHERS : 0, NT + 64); };
     // Batches of a row of nvec vectors, and how many of them are fetched twice.
     auto batches = [](int nvec) { return (nvec + U * NT - 1) / (U * NT); };
     auto twice = [&](int nb) { return OP::STATS && a.dx && nb > slots ? nb - slots : 0; };
+    // Statistics of row i, after its barrier: copies of the NW parts throughout
+    // the warp, joined in log2(NW) levels.
     auto stat_of = [&](int i) {
-        SoftStat t = lane < NW ? sh.part[i % PARTS<OP>][lane] : SoftStat{NEG_INF, 0.0f};
+        SoftStat t = soft_warp<NW>(sh.part[i % PARTS<OP>][lane % NW], s2);
         if (*failed)
             t.l = __int_as_float(0x7fc00000);
-        return soft_warp(t, s2);
+        return t;
     };
 
     if (warp == NW) {
-        // ---- service warp
+        // ---- scheduler
         unsigned taken = 0;  // link 1: the counter's value, in lane 0
         RowEntry got, ready;  // links 2 and 3, an entry in each of the first `group` lanes
         got.state = ready.state = ROW_END;
         got.r = ready.r = a.rows;
         for (int i = 0;; ++i) {
-            const RowEntry e = sh.queue[i % ROW_Q];
-            if (e.state == ROW_END)
+            if (sh.queue[i % ROW_Q].state == ROW_END)
                 break;
             if (i % group == 0) {
                 const int step = i / group;
                 if (step >= 3) {
                     const int at = fixed + (step - 3) * group;
                     // (the loader may be behind on a run of ignored rows)
-                    for (int n = 0; *loading + ROW_Q <= at + group && n < WAIT_TRIES && !*failed; ++n)
-                        ;
+                    for (int n = 0; *loading + ROW_Q <= at + group && !*failed; ++n) {
+                        __nanosleep(32);
+                        if (n == WAIT_TRIES)
+                            *failed = 1;
+                    }
                     if (lane < group)
                         sh.queue[(at + lane) % ROW_Q] = ready;
-                    __threadfence_block();
                     __syncwarp();
+                    __threadfence_block();
                     if (lane == 0)
                         *published = at + group;
                 }
@@ -398,11 +510,8 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
                     taken = atomicAdd(next, (unsigned)group);
             }
             row_barrier(i);
-            const SoftStat t = OP::STATS ? stat_of(i) : SoftStat{};
-            if (lane == 0)
-                op.template write<DT>(a, e, t);
         }
-        // the last CTA to finish leaves the counters as they were
+        // the last to finish leaves the counters as they were
         if (lane == 0) {
             __threadfence();
             if (atomicAdd(next + 1, 1u) == gridDim.x - 1) {
@@ -410,20 +519,18 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
                 next[1] = 0;
             }
         }
-        return;
-    }
-    if (warp == NW + 1) {
+    } else if (warp == NW + 1 && lane == 0) {
         // ---- loader
-        if (lane != 0)
-            return;
         int slot = 0;
         uint32_t parity = 1;  // a fresh slot is empty
         for (int i = 0;; ++i) {
-            for (int n = 0; *published <= i; ++n)
-                if (n == WAIT_TRIES || *failed) {
+            for (int n = 0; *published <= i && !*failed; ++n) {
+                __nanosleep(32);
+                if (n == WAIT_TRIES)
                     *failed = 1;
-                    return;
-                }
+            }
+            if (*failed)
+                break;
             __threadfence_block();
             const int64_t r = sh.queue[i % ROW_Q].r;
             const int state = sh.queue[i % ROW_Q].state;
@@ -448,10 +555,25 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
                 }
             }
         }
-        return;
-    }
-    if constexpr (OP::TEACHER) {
-        if (warp > NW + 1) {
+    } else if (!OP::TEACHER && warp == NW + 2) {
+        // ---- writer
+        for (int i = 0;; ++i) {
+            const RowEntry e = sh.queue[i % ROW_Q];
+            if (e.state == ROW_END)
+                break;
+            row_barrier(i);
+            RowStat t{};
+            if (OP::STATS && e.state == ROW_LIVE)
+                t = row_stat(a, stat_of(i));
+            if (lane == 0)
+                op.template write<DT>(a, e, t);
+            if (a.dx && e.state == ROW_OUT)
+                zero_row_bulk<DT>(static_cast<T *>(a.dx) + e.r * a.ldd, a.len, sh.zeros);
+        }
+        if (lane == 0)
+            bulk_stores_done();
+    } else if (OP::TEACHER && warp > NW + 1) {
+        if constexpr (OP::TEACHER) {
             // ---- teacher warp w: rows w, w + TEACHERS, ...
             const int w = warp - NW - 2;
             const TeacherRow list = teacher(w);
@@ -468,160 +590,234 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
                         sh.mass[w] = Q;
                 }
                 row_barrier(i);
-                const SoftStat t = stat_of(i);
-                const float Q = sh.mass[w];
+                RowStat t{};
+                if (e.state == ROW_LIVE)
+                    t = row_stat(a, stat_of(i));
                 op.finish(a, e, t, list);
                 if (a.dx && e.state == ROW_LIVE) {
-                    const RowGrad g = op.template grad<DT>(a, e, t, Q);
+                    const RowGrad g = op.template grad<DT>(a, e, t, sh.mass[w]);
                     bar_sync(1 + TEACHERS + w, NT + 32);
                     if (!g.zero)
-                        op.template patch<DT>(a, e, g, list);
+                        op.template patch<DT>(a, e, g, list, 0, a.len);
+                } else if (a.dx) {
+                    zero_row_bulk<DT>(static_cast<T *>(a.dx) + e.r * a.ldd, a.len, sh.zeros);
                 }
                 __syncwarp();
             }
-            return;
-        }
-    }
-
-    // ---- consumers
-    const T *const x = static_cast<const T *>(a.x);
-    T *const dx = static_cast<T *>(a.dx);
-    int cslot = 0;  // slot of the next batch, and the phase it arrives in
-    uint32_t cphase = 0;
-    auto await_batch = [&]() { mbar_wait(&sh.full[cslot], cphase, failed); };
-    auto step_slot = [&]() {
-        if (++cslot == slots) {
-            cslot = 0;
-            cphase ^= 1;
-        }
-    };
-    auto release = [&](int slot) {
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&sh.empty[slot]);
-    };
-
-    for (int i = 0;; ++i) {
-        const RowEntry e = sh.queue[i % ROW_Q];
-        if (e.state == ROW_END)
-            break;
-        if (e.state == ROW_OUT) {
-            row_barrier(i);
-            if (dx)
-                zero_row<DT>(dx + e.r * a.ldd, a.len, tid, NT);
-            continue;
-        }
-        const T *const row = x + e.r * a.ld;
-        const int h = head_elems<DT>(row, a.len);
-        const int nvec = (a.len - h) / E, nb = batches(nvec), n1 = twice(nb);
-        // the row's ragged ends: threads 0..7 the head, 8..15 the tail
-        int edge = -1;
-        if (tid < h)
-            edge = tid;
-        else if (tid >= 8 && tid < 16 && h + nvec * E + tid - 8 < a.len)
-            edge = h + nvec * E + tid - 8;
-        float xe = 0.0f;
-        if (edge >= 0)
-            xe = load_elem<DT>(row, edge);
-
-        // whether all of the warp's vectors of batch b are within the row
-        auto whole = [&](int b) { return nvec - b * U * NT - (tid | 31) > (U - 1) * NT; };
-
-        SoftStat t{};
-        const int first = cslot;
-        if constexpr (OP::STATS) {
-            SoftRun run;
-            run.init();
-            for (int b = 0; b < nb; ++b) {
-                const uint4 *src = ring + cslot * U * NT + tid;
-                const int left = nvec - b * U * NT - tid;
-                await_batch();
-                uint4 v[U];
-                if (whole(b)) {
-                    float top = NEG_INF;
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        v[u] = src[u * NT];
-                        top = fmaxf(top, vec_max<DT>(v[u]));
-                    }
-                    run.raise(top, s2);
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        run.template add<DT>(v[u], s2);
-                } else {
-#pragma unroll 1
-                    for (int u = 0; u < U && u * NT < left; ++u) {
-                        v[0] = src[u * NT];
-                        run.raise(vec_max<DT>(v[0]), s2);
-                        run.template add<DT>(v[0], s2);
-                    }
-                }
-                if (!dx || b < n1)
-                    release(cslot);
-                step_slot();
-            }
-            if (edge >= 0) {
-                run.raise(xe, s2);
-                run.add(xe, s2);
-            }
-            t = soft_warp(run.stat(), s2);
             if (lane == 0)
-                sh.part[i % PARTS<OP>][warp] = t;
+                bulk_stores_done();
         }
-        row_barrier(i);
-        if (!dx)
-            continue;
-        if constexpr (OP::STATS)
-            t = stat_of(i);
-        const RowGrad g = op.template grad<DT>(a, e, t, OP::TEACHER ? sh.mass[i % TEACHERS] : 0.0f);
-        T *const grow = dx + e.r * a.ldd;
-        const bool aligned = ((uintptr_t)(grow + h) & 15u) == 0;
-        auto emit = [&](int b, int slot) {
-            const uint4 *src = ring + slot * U * NT + tid;
-            const int j = h + (b * U * NT + tid) * E;
-            const int left = nvec - b * U * NT - tid;
-            uint4 v[U];
-            if (g.zero) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (u * NT < left)
-                        store_vec<DT>(grow + j + u * NT * E, make_uint4(0, 0, 0, 0), aligned);
-                release(slot);
-            } else if (aligned && whole(b)) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    v[u] = src[u * NT];
-                release(slot);
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    *reinterpret_cast<uint4 *>(grow + j + u * NT * E) = vec_grad<DT>(v[u], g, j + u * NT * E);
-            } else {
-#pragma unroll 1
-                for (int u = 0; u < U && u * NT < left; ++u)
-                    store_vec<DT>(grow + j + u * NT * E, vec_grad<DT>(src[u * NT], g, j + u * NT * E), aligned);
-                release(slot);
+    } else if (warp < NW) {
+        // ---- consumers
+        const T *const x = static_cast<const T *>(a.x);
+        T *const dx = static_cast<T *>(a.dx);
+        int cslot = 0;  // slot of the next batch, and the phase it arrives in
+        uint32_t cphase = 0;
+        auto await_batch = [&]() { mbar_wait(&sh.full[cslot], cphase, failed); };
+        auto step_slot = [&]() {
+            if (++cslot == slots) {
+                cslot = 0;
+                cphase ^= 1;
             }
         };
-        if constexpr (OP::STATS) {
-            int slot = (first + n1) % slots;
-            for (int b = n1; b < nb; ++b) {
-                emit(b, slot);
-                slot = slot + 1 == slots ? 0 : slot + 1;
+        auto release = [&](int slot) {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.empty[slot]);
+        };
+
+        for (int i = 0;; ++i) {
+            const RowEntry e = sh.queue[i % ROW_Q];
+            if (e.state == ROW_END)
+                break;
+            if (e.state == ROW_OUT) {
+                row_barrier(i);
+                continue;
+            }
+            const T *const row = x + e.r * a.ld;
+            const int h = head_elems<DT>(row, a.len);
+            const int nvec = (a.len - h) / E, nb = batches(nvec), n1 = twice(nb);
+            // the row's ragged ends: threads 0..7 the head, 8..15 the tail
+            int edge = -1;
+            if (tid < h)
+                edge = tid;
+            else if (tid >= 8 && tid < 16 && h + nvec * E + tid - 8 < a.len)
+                edge = h + nvec * E + tid - 8;
+            float xe = 0.0f;
+            if (edge >= 0)
+                xe = load_elem<DT>(row, edge);
+
+            // whether all of the warp's vectors of batch b are within the row
+            auto whole = [&](int b) { return nvec - b * U * NT - (tid | 31) > (U - 1) * NT; };
+
+            RowStat t{};
+            const int first = cslot;
+            if constexpr (OP::STATS) {
+                SoftRun run;
+                run.init();
+                for (int b = 0; b < nb; ++b) {
+                    const uint4 *src = ring + cslot * U * NT + tid;
+                    const int left = nvec - b * U * NT - tid;
+                    await_batch();
+                    uint4 v[U];
+                    if (whole(b)) {
+                        float top = NEG_INF;
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            v[u] = src[u * NT];
+                            top = fmaxf(top, vec_max<DT>(v[u]));
+                        }
+                        run.raise(top, s2);
+                        run.template add<DT, U>(v, s2);
+                    } else {
+#pragma unroll 1
+                        for (int u = 0; u < U && u * NT < left; ++u) {
+                            const uint4 w[1] = {src[u * NT]};
+                            run.raise(vec_max<DT>(w[0]), s2);
+                            run.template add<DT, 1>(w, s2);
+                        }
+                    }
+                    if (!dx || b < n1)
+                        release(cslot);
+                    step_slot();
+                }
+                if (edge >= 0) {
+                    run.raise(xe, s2);
+                    run.add(xe, s2);
+                }
+                const SoftStat w = soft_warp(run.stat(), s2);
+                if (lane == 0)
+                    sh.part[i % PARTS<OP>][warp] = w;
+            }
+            row_barrier(i);
+            if (!dx)
+                continue;
+            if constexpr (OP::STATS)
+                t = row_stat(a, stat_of(i));
+            const RowGrad g = op.template grad<DT>(a, e, t, OP::TEACHER ? sh.mass[i % TEACHERS] : 0.0f);
+            T *const grow = dx + e.r * a.ldd;
+            const bool aligned = ((uintptr_t)(grow + h) & 15u) == 0;
+            auto emit = [&](int b, int slot) {
+                const uint4 *src = ring + slot * U * NT + tid;
+                const int c0 = h + (b * U * NT + tid) * E;
+                const int left = nvec - b * U * NT - tid;
+                uint4 v[U];
+                if (g.zero) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (u * NT < left)
+                            store_vec<DT>(grow + c0 + u * NT * E, make_uint4(0, 0, 0, 0), aligned);
+                    release(slot);
+                } else if (aligned && !g.far && whole(b)) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        v[u] = src[u * NT];
+                    release(slot);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        *reinterpret_cast<uint4 *>(grow + c0 + u * NT * E) = vec_grad<DT>(v[u], g, c0 + u * NT * E);
+                } else {
+#pragma unroll 1
+                    for (int u = 0; u < U && u * NT < left; ++u)
+                        store_vec<DT>(grow + c0 + u * NT * E, vec_grad<DT, true>(src[u * NT], g, c0 + u * NT * E), aligned);
+                    release(slot);
+                }
+            };
+            if constexpr (OP::STATS) {
+                int slot = (first + n1) % slots;
+                for (int b = n1; b < nb; ++b) {
+                    emit(b, slot);
+                    slot = slot + 1 == slots ? 0 : slot + 1;
+                }
+            }
+            // what is fetched for the gradient alone
+            for (int b = 0; b < (OP::STATS ? n1 : nb); ++b) {
+                await_batch();
+                emit(b, cslot);
+                step_slot();
+            }
+            if (edge >= 0)
+                store_elem<DT>(grow, edge, g.zero ? 0.0f : elem_grad<DT>(xe, g, edge));
+            if constexpr (OP::TEACHER) {
+                __threadfence_block();
+                asm volatile("bar.arrive %0, %1;" ::"r"(1 + TEACHERS + i % TEACHERS), "n"(NT + 32) : "memory");
             }
         }
-        // what is fetched for the gradient alone
-        for (int b = 0; b < (OP::STATS ? n1 : nb); ++b) {
-            await_batch();
-            emit(b, cslot);
-            step_slot();
-        }
-        if (edge >= 0)
-            store_elem<DT>(grow, edge, g.zero ? 0.0f : elem_grad<DT>(xe, g, edge));
-        if constexpr (OP::TEACHER) {
-            __threadfence_block();
-            asm volatile("bar.arrive %0, %1;" ::"r"(1 + TEACHERS + i % TEACHERS), "n"(NT + 32) : "memory");
-        }
     }
+}
+
+// ------------------------------------------------------------------ totals
+
+// The CTA's N sums, rounded to out[0, N).
+template <int N, int NT>
+__device__ void cta_totals(Sum (&v)[N], float *out)
+{
+    __shared__ Sum s[N][NT / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i].join_warp();
+        if (lane == 0)
+            s[i][warp] = v[i];
+    }
+    __syncthreads();
+    if (threadIdx.x < N) {
+        Sum t;
+        for (int w = 0; w < NT / 32; ++w)
+            t.add(s[threadIdx.x][w]);
+        out[threadIdx.x] = t.value();
+    }
+}
+
+constexpr int TOTAL_NT = 256, TOTAL_CTAS = 256, TOTAL_ROWS = 256;
+
+// Totals over rows from the results that a row kernel left: each CTA sums its
+// rows, the CTA that finishes last the CTAs' parts, in a fixed order.
+template <class OP>
+__global__ void __launch_bounds__(TOTAL_NT) total_kernel(int64_t rows, int len, OP op, Sum *part, unsigned *tick)
+{
+    constexpr int N = OP::TOTALS;
+    __shared__ Sum s[N][TOTAL_NT / 32];
+    __shared__ bool s_last;
+    const int tid = threadIdx.x;
+    pdl_enter();
+    Sum v[N];
+    for (int64_t r = (int64_t)blockIdx.x * TOTAL_NT + tid; r < rows; r += (int64_t)gridDim.x * TOTAL_NT)
+        op.total(r, len, v);
+    if (gridDim.x == 1) {
+        cta_totals<N, TOTAL_NT>(v, op.stats);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i].join_warp();
+        if ((tid & 31) == 0)
+            s[i][tid >> 5] = v[i];
+    }
+    __syncthreads();
+    if (tid < N) {
+        Sum t;
+        for (int w = 0; w < TOTAL_NT / 32; ++w)
+            t.add(s[tid][w]);
+        part[(int64_t)blockIdx.x * N + tid] = t;
+        __threadfence();
+    }
+    __syncthreads();
+    if (tid == 0)
+        s_last = atomicAdd(tick, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!s_last)
+        return;
+    __threadfence();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = Sum{};
+        if (tid < gridDim.x)
+            v[i] = part[(int64_t)tid * N + i];
+    }
+    cta_totals<N, TOTAL_NT>(v, op.stats);
+    if (tid == 0)
+        *tick = 0;
 }
 
 // ------------------------------------------------------------- short rows
@@ -640,7 +836,7 @@ __global__ void __launch_bounds__(WARP_NT) warp_row_kernel(LogitRows a, OP op, i
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *const f = reinterpret_cast<float *>(smem) + warp * 4 * teacher_k;
     const TeacherRow list{reinterpret_cast<int *>(f), f + teacher_k, f + 2 * teacher_k, f + 3 * teacher_k};
-    const float s2 = a.scale * LOG2E;
+    const float s2 = a.s2;
     const T *const x = static_cast<const T *>(a.x);
     T *const dx = static_cast<T *>(a.dx);
     pdl_enter();
@@ -661,9 +857,9 @@ __global__ void __launch_bounds__(WARP_NT) warp_row_kernel(LogitRows a, OP op, i
                 op.template settle<DT>(a, n);
             }
             if constexpr (OP::TEACHER)
-                op.finish(a, e, SoftStat{}, list);
+                op.finish(a, e, RowStat{}, list);
             else if (lane == 0)
-                op.template write<DT>(a, e, SoftStat{});
+                op.template write<DT>(a, e, RowStat{});
             if (dx)
                 zero_row<DT>(grow, a.len, lane, 32);
             continue;
@@ -689,30 +885,30 @@ __global__ void __launch_bounds__(WARP_NT) warp_row_kernel(LogitRows a, OP op, i
         if constexpr (OP::TEACHER)
             Q = op.template prepare<DT>(a, r, list);
 
-        SoftStat t{};
+        RowStat t{};
         if constexpr (OP::STATS) {
-            float top = edge >= 0 ? xe : NEG_INF;
+            float top = edge >= 0 ? fmaxf(xe, NEG_INF) : NEG_INF;  // (not a NaN)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (i * 32 + lane < nvec)
                     top = fmaxf(top, vec_max<DT>(v[i]));
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            top = warp_max(top);
             SoftRun run;
             run.init();
             run.m = top;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (i * 32 + lane < nvec)
-                    run.template add<DT>(v[i], s2);
+                if (i * 32 + lane < nvec) {
+                    const uint4 w[1] = {v[i]};
+                    run.template add<DT, 1>(w, s2);
+                }
             if (edge >= 0)
                 run.add(xe, s2);
-            float l = run.l.x + run.l.y;
+            float l = run.stat().l;
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1)
                 l += __shfl_xor_sync(0xffffffffu, l, off);
-            t = SoftStat{top, l};
+            t = row_stat(a, SoftStat{top, l});
             if constexpr (OP::TEACHER)
                 op.finish(a, e, t, list);
             else if (lane == 0)
@@ -728,42 +924,194 @@ __global__ void __launch_bounds__(WARP_NT) warp_row_kernel(LogitRows a, OP op, i
         for (int i = 0; i < NV; ++i)
             if (i * 32 + lane < nvec) {
                 const int j = h + (i * 32 + lane) * E;
-                store_vec<DT>(grow + j, g.zero ? make_uint4(0, 0, 0, 0) : vec_grad<DT>(v[i], g, j), aligned);
+                const uint4 o = g.zero ? make_uint4(0, 0, 0, 0)
+                                       : (g.far ? vec_grad<DT, true>(v[i], g, j) : vec_grad<DT>(v[i], g, j));
+                store_vec<DT>(grow + j, o, aligned);
             }
         if (edge >= 0)
             store_elem<DT>(grow, edge, g.zero ? 0.0f : elem_grad<DT>(xe, g, edge));
         if constexpr (OP::TEACHER) {
             __syncwarp();
             if (!g.zero)
-                op.template patch<DT>(a, e, g, list);
+                op.template patch<DT>(a, e, g, list, 0, a.len);
             __syncwarp();
         }
     }
 }
 
+// --------------------------------------------------------------- few rows
+
+constexpr int FEW_NT = 256, FEW_NW = FEW_NT / 32, MAX_CLUSTER = 8;
+
+// A cluster of CTAs per row, a slice of the columns each, held in registers
+// (NV vectors per thread): few rows, for which latency counts.  All loads are
+// out at once, the statistics of the slices meet through distributed shared
+// memory, and the CTA that finishes last sums the totals.
+template <int DT, class OP, int NV>
+__global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int teacher_k, unsigned *tick)
+{
+    using T = typename Elem<DT>::T;
+    constexpr int E = VEC_ELEMS<DT>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ SoftStat s_part[FEW_NW], s_slice[MAX_CLUSTER];
+    __shared__ float s_mass;
+    __shared__ bool s_last;
+    float *const f = reinterpret_cast<float *>(smem);
+    const TeacherRow list{reinterpret_cast<int *>(f), f + teacher_k, f + 2 * teacher_k, f + 3 * teacher_k};
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cs = cluster_size(), rank = cluster_rank();
+    const int64_t r = blockIdx.x / cs;
+    const float s2 = a.s2;
+    cluster_arrive();
+    pdl_enter();
+
+    RowEntry e;
+    op.load(r, e);
+    const T *const row = static_cast<const T *>(a.x) + r * a.ld;
+    T *const grow = static_cast<T *>(a.dx) + r * a.ldd;
+    const int h = head_elems<DT>(row, a.len), all = (a.len - h) / E;
+    const int q = (all + cs - 1) / cs, begin = min(rank * q, all), n = min(q, all - begin);
+    const int j0 = h + begin * E;  // first column of the slice
+    uint4 v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (i * FEW_NT + tid < n)
+            v[i] = reinterpret_cast<const uint4 *>(row + j0)[i * FEW_NT + tid];
+    // the row's ragged ends: the first CTA's threads 0..7, the last one's 8..15
+    int edge = -1;
+    if (rank == 0 && tid < h)
+        edge = tid;
+    else if (rank == cs - 1 && tid >= 8 && tid < 16 && h + all * E + tid - 8 < a.len)
+        edge = h + all * E + tid - 8;
+    float xe = 0.0f;
+    if (edge >= 0)
+        xe = load_elem<DT>(row, edge);
+    op.template settle<DT>(a, e);
+
+    RowStat t{};
+    if (e.state == ROW_LIVE) {
+        if constexpr (OP::TEACHER) {
+            if (warp == 0) {
+                const float Q = op.template prepare<DT>(a, r, list);
+                if (lane == 0)
+                    s_mass = Q;
+            }
+        }
+        if constexpr (OP::STATS) {
+            SoftRun run;
+            run.init();
+            float top = edge >= 0 ? fmaxf(xe, NEG_INF) : NEG_INF;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (i * FEW_NT + tid < n)
+                    top = fmaxf(top, vec_max<DT>(v[i]));
+            run.m = top;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (i * FEW_NT + tid < n) {
+                    const uint4 w[1] = {v[i]};
+                    run.template add<DT, 1>(w, s2);
+                }
+            if (edge >= 0)
+                run.add(xe, s2);
+            SoftStat w = soft_warp(run.stat(), s2);
+            if (lane == 0)
+                s_part[warp] = w;
+            __syncthreads();
+            w = soft_warp<FEW_NW>(s_part[lane % FEW_NW], s2);
+            cluster_wait();  // for the others to have started
+            if (tid < cs)
+                *in_cta(&s_slice[rank], tid) = w;
+            cluster_arrive();
+            cluster_wait();
+            w = soft_warp<MAX_CLUSTER>(s_slice[lane % cs], s2);
+            w.l *= (float)cs / MAX_CLUSTER;  // (every slice was there MAX_CLUSTER / cs times)
+            t = row_stat(a, w);
+        }
+    }
+    if (rank == 0) {
+        if constexpr (OP::TEACHER) {
+            if (warp == 0)
+                op.finish(a, e, t, list);
+        } else if (tid == 0) {
+            op.template write<DT>(a, e, t);
+        }
+    }
+    if (a.dx && e.state == ROW_LIVE) {
+        const RowGrad g = op.template grad<DT>(a, e, t, OP::TEACHER ? s_mass : 0.0f);
+        const bool aligned = ((uintptr_t)(grow + h) & 15u) == 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (i * FEW_NT + tid < n) {
+                const int j = j0 + (i * FEW_NT + tid) * E;
+                const uint4 o = g.zero ? make_uint4(0, 0, 0, 0)
+                                       : (g.far ? vec_grad<DT, true>(v[i], g, j) : vec_grad<DT>(v[i], g, j));
+                store_vec<DT>(grow + j, o, aligned);
+            }
+        if (edge >= 0)
+            store_elem<DT>(grow, edge, g.zero ? 0.0f : elem_grad<DT>(xe, g, edge));
+        if constexpr (OP::TEACHER) {
+            __syncthreads();
+            if (warp == 0 && !g.zero)
+                op.template patch<DT>(a, e, g, list, rank == 0 ? 0 : j0, rank == cs - 1 ? a.len : j0 + n * E);
+        }
+    } else if (a.dx) {
+        zero_row<DT>(grow, a.len, rank * FEW_NT + tid, cs * FEW_NT);
+    }
+    if constexpr (OP::TOTALS > 0) {
+        if (rank != 0)
+            return;
+        if (tid == 0) {
+            __threadfence();
+            s_last = atomicAdd(tick, 1u) == (unsigned)a.rows - 1;
+        }
+        __syncthreads();
+        if (!s_last)
+            return;
+        __threadfence();
+        Sum v2[OP::TOTALS];
+        for (int64_t k = tid; k < a.rows; k += FEW_NT)
+            op.total(k, a.len, v2);
+        cta_totals<OP::TOTALS, FEW_NT>(v2, op.stats);
+        if (tid == 0)
+            *tick = 0;
+    }
+}
+
 // --------------------------------------------------------------- launchers
 
-// Launch with dynamic shared memory and programmatic serialization (as
-// launch_pdl).
+// Launch with dynamic shared memory, programmatic serialization (as
+// launch_pdl) and clusters of `cluster` CTAs.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
-                            Args... args)
+cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                            cudaStream_t s, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
 // Longest row of the warp kernel.
 constexpr size_t WARP_ROW_BYTES = 8192;
+// The few-row kernel is taken while its CTAs, with the largest cluster that
+// allows it, are at most this many per two SMs (and a thread's slice 8
+// vectors).  us, few-row kernel against the row kernel: logprob 1 x 65536 bf16
+// 2.4 / 5.9, 64 rows 4.6 / 6.3; policy 1 row 5.5 / 9.4, 30 rows 7.2 / 9.5, 64
+// rows 8.5 / 9.4, 100 rows 9.4 / 9.8, 300 x 16384 f32 9.4 / 10.5.  With 4
+// CTAs per SM they no longer all run at once: 152 x 65536 bf16 12.5 / 10.1.
+constexpr int FEW_CTAS_PER_2_SMS = 7;
 
 constexpr size_t SM_SMEM = 228 * 1024, CTA_SMEM = 227 * 1024, CTA_RESERVED = 1024;
 
@@ -798,7 +1146,7 @@ int launch_row_kernel(const LogitRows &a, const OP &op, int per_sm, int teacher_
     // Rows taken at a time: one where a CTA gets few rows (the last row taken
     // is what CTAs wait for at the end), more where rows are many.
     const int group = a.rows >= 32 * cap ? 4 : (a.rows >= 16 * cap ? 2 : 1);
-    const cudaError_t e = launch_pdl_smem(kernel, grid, NT + SERVICE, smem, s, a, op, ws.tick, slots,
+    const cudaError_t e = launch_pdl_smem(kernel, grid, NT + SERVICE, smem, 1, s, a, op, ws.tick, slots,
                                           group, teacher_k);
     count_launches(1);
     return cuda_fail(e != cudaSuccess ? e : cudaGetLastError(), "row kernel launch");
@@ -822,13 +1170,45 @@ int launch_warp_kernel(const LogitRows &a, const OP &op, int teacher_k, cudaStre
     if (e != cudaSuccess || occ < 1)
         return cuda_fail(e, "warp row kernel: occupancy");
     const int64_t want = (a.rows + WARP_NT / 32 - 1) / (WARP_NT / 32), cap = (int64_t)di.sms * occ;
-    e = launch_pdl_smem(kernel, (unsigned)(want < cap ? want : cap), WARP_NT, smem, s, a, op, teacher_k);
+    e = launch_pdl_smem(kernel, (unsigned)(want < cap ? want : cap), WARP_NT, smem, 1, s, a, op, teacher_k);
     count_launches(1);
     return cuda_fail(e != cudaSuccess ? e : cudaGetLastError(), "warp row kernel launch");
 }
 
+template <int DT, class OP, int NV>
+int launch_few_kernel(const LogitRows &a, const OP &op, int cluster, int teacher_k, cudaStream_t s)
+{
+    Workspace ws;
+    const int st = get_workspace(&ws);
+    if (st != RED_OK)
+        return st;
+    const size_t smem = (size_t)4 * 4 * teacher_k;
+    const cudaError_t e = launch_pdl_smem(few_row_kernel<DT, OP, NV>, (unsigned)(a.rows * cluster), FEW_NT, smem,
+                                          (unsigned)cluster, s, a, op, teacher_k, ws.tick);
+    count_launches(1);
+    return cuda_fail(e != cudaSuccess ? e : cudaGetLastError(), "few-row kernel launch");
+}
+
+template <class OP>
+int launch_totals(const LogitRows &a, const OP &op, cudaStream_t s)
+{
+    if constexpr (OP::TOTALS > 0) {
+        Workspace ws;
+        const int st = get_workspace(&ws);
+        if (st != RED_OK)
+            return st;
+        const int64_t want = (a.rows + TOTAL_ROWS - 1) / TOTAL_ROWS;
+        const cudaError_t e = launch_pdl(total_kernel<OP>, dim3((unsigned)(want < TOTAL_CTAS ? want : TOTAL_CTAS)),
+                                         dim3(TOTAL_NT), s, a.rows, a.len, op, static_cast<Sum *>(ws.part), ws.tick);
+        count_launches(1);
+        return cuda_fail(e != cudaSuccess ? e : cudaGetLastError(), "totals launch");
+    }
+    return RED_OK;
+}
+
+// Rows and columns by a row kernel; *summed: the totals are done, too.
 template <int DT, class OP>
-int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s)
+int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s, bool *summed)
 {
     DeviceInfo di;
     const int st = device_info(&di);
@@ -843,6 +1223,15 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
         if (nv <= 8)
             return launch_warp_kernel<DT, OP, 8>(a, op, teacher_k, s, di);
         return launch_warp_kernel<DT, OP, 16>(a, op, teacher_k, s, di);
+    }
+    const int64_t nvec = (int64_t)(bytes / 16);
+    for (int cluster = MAX_CLUSTER; cluster >= 2; cluster /= 2) {
+        const int64_t slice = (nvec + cluster - 1) / cluster;
+        if (2 * a.rows * cluster > FEW_CTAS_PER_2_SMS * di.sms || slice > 8 * FEW_NT)
+            continue;
+        *summed = true;
+        return slice <= 4 * FEW_NT ? launch_few_kernel<DT, OP, 4>(a, op, cluster, teacher_k, s)
+                                   : launch_few_kernel<DT, OP, 8>(a, op, cluster, teacher_k, s);
     }
     // Threads, vectors per thread and batch, and CTAs per SM, by row bytes.  A
     // CTA is busy with one row at a time, so short rows need several CTAs to
@@ -870,74 +1259,14 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
 template <class OP>
 int launch_loss_rows(int dtype, const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s)
 {
+    bool summed = false;
+    int st;
     switch (dtype) {
-    case RED_F32: return launch_rows_of<RED_F32>(a, op, teacher_k, s);
-    case RED_F16: return launch_rows_of<RED_F16>(a, op, teacher_k, s);
-    default: return launch_rows_of<RED_BF16>(a, op, teacher_k, s);
+    case RED_F32: st = launch_rows_of<RED_F32>(a, op, teacher_k, s, &summed); break;
+    case RED_F16: st = launch_rows_of<RED_F16>(a, op, teacher_k, s, &summed); break;
+    default: st = launch_rows_of<RED_BF16>(a, op, teacher_k, s, &summed); break;
     }
-}
-
-// ------------------------------------------------------ totals over rows
-
-constexpr int TOTAL_NT = 256, TOTAL_CTAS = 128, TOTAL_ROWS = 1024;
-
-// N sums over the rows in 64 bits and a fixed order: each CTA sums its rows,
-// the CTA that finishes last the CTAs' parts.  row(r, v) adds row r's terms.
-template <int N, class ROW>
-__device__ void total_rows(int64_t rows, ROW row, float *out, double *part, unsigned *tick)
-{
-    __shared__ double s[N][TOTAL_NT / 32];
-    __shared__ bool s_last;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    auto cta_total = [&](double (&v)[N]) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            for (int off = 16; off > 0; off >>= 1)
-                v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
-            if (lane == 0)
-                s[i][warp] = v[i];
-        }
-        __syncthreads();
-        double t = 0.0;
-        if (tid < N)
-            for (int w = 0; w < TOTAL_NT / 32; ++w)
-                t += s[tid][w];
-        return t;  // total i in thread i
-    };
-    double v[N] = {};
-    for (int64_t r = (int64_t)blockIdx.x * TOTAL_NT + tid; r < rows; r += (int64_t)gridDim.x * TOTAL_NT)
-        row(r, v);
-    double t = cta_total(v);
-    if (gridDim.x == 1) {
-        if (tid < N)
-            out[tid] = (float)t;
-        return;
-    }
-    if (tid < N)
-        part[(int64_t)blockIdx.x * N + tid] = t;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0)
-        s_last = atomicAdd(tick, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!s_last)
-        return;
-    __threadfence();
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        v[i] = tid < gridDim.x ? __ldcg(part + (int64_t)tid * N + i) : 0.0;
-    __syncthreads();
-    t = cta_total(v);
-    if (tid < N)
-        out[tid] = (float)t;
-    if (tid == 0)
-        *tick = 0;
-}
-
-inline unsigned total_ctas(int64_t rows)
-{
-    const int64_t want = (rows + TOTAL_ROWS - 1) / TOTAL_ROWS;
-    return (unsigned)(want < TOTAL_CTAS ? want : TOTAL_CTAS);
+    return st != RED_OK || summed ? st : launch_totals(a, op, s);
 }
 
 }  // namespace red

@@ -2,8 +2,8 @@
 // row kernels of the log-probabilities and of their gradient around one
 // kernel that reduces the packed tokens to sequences and pairs.
 //
-// One CTA per pair sums the log-probabilities of its two sequences (64-bit
-// sums in a fixed order: a sequence of thousands of tokens adds values of a
+// One CTA per pair sums the log-probabilities of its two sequences (in two
+// floats and a fixed order: a sequence of thousands of tokens adds values of a
 // few nats, and the loss depends on the difference of two such sums), forms
 // u = beta * (gain of the chosen - gain of the rejected) - margin, the loss
 // of u and its derivative, and writes each token's share of it.  The CTA that
@@ -19,43 +19,42 @@ constexpr int NT = 256;
 constexpr int NW = NT / 32;
 
 // Sum over the CTA, in every thread.
-__device__ double cta_sum(double v, double *s)
+__device__ Sum cta_sum(Sum v, Sum *s)
 {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, off);
+    v.join_warp();
     __syncthreads();
     if ((threadIdx.x & 31) == 0)
         s[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0;
+    v = Sum{};
 #pragma unroll
     for (int w = 0; w < NW; ++w)
-        v += s[w];
+        v.add(s[w]);
     return v;
 }
 
 struct PairTerms {
-    double loss, du;
+    float loss, du;
 };
 
-__device__ PairTerms pair_terms(const PreferenceArgs &p, double u)
+__device__ PairTerms pair_terms(const PreferenceArgs &p, float u)
 {
     PairTerms t;
     if (p.kind == RED_PREF_SIGMOID) {
         // -(1 - e) log sigma(u) - e log sigma(-u); log sigma through
         // log1p(e^-|u|), which neither overflows nor loses small values
-        const float f = (float)u, e = p.smoothing;
-        const float soft = log1pf(expf(-fabsf(f)));
-        t.loss = (1.0f - e) * (soft + fmaxf(-f, 0.0f)) + e * (soft + fmaxf(f, 0.0f));
-        t.du = e - 1.0f / (1.0f + expf(f));
+        const float e = p.smoothing, soft = log1pf(expf(-fabsf(u)));
+        t.loss = (1.0f - e) * (soft + fmaxf(-u, 0.0f)) + e * (soft + fmaxf(u, 0.0f));
+        t.du = e - 1.0f / (1.0f + expf(u));
+        if (u != u)
+            t.loss = u;
     } else if (p.kind == RED_PREF_HINGE) {
-        t.loss = u < 1.0 ? 1.0 - u : (u != u ? u : 0.0);
-        t.du = u < 1.0 ? -1.0 : 0.0;
+        t.loss = u < 1.0f ? 1.0f - u : (u != u ? u : 0.0f);
+        t.du = u < 1.0f ? -1.0f : 0.0f;
     } else {
-        const double off = (u - 0.5) / p.beta;
+        const float off = (u - 0.5f) / p.beta;
         t.loss = off * off;
-        t.du = 2.0 * off / p.beta;
+        t.du = 2.0f * off / p.beta;
     }
     return t;
 }
@@ -63,33 +62,47 @@ __device__ PairTerms pair_terms(const PreferenceArgs &p, double u)
 __global__ void __launch_bounds__(NT) pair_kernel(int64_t rows, int len, PreferenceArgs p, unsigned *tick)
 {
     pdl_enter();
-    __shared__ double s[NW];
+    __shared__ Sum s[NW];
     __shared__ bool s_last;
     const int64_t pair = blockIdx.x;
     int64_t lo[2], hi[2];
-    double sum[2], count[2];
+    Sum sum[2];
+    float count[2];
     for (int side = 0; side < 2; ++side) {
         const int64_t q = pair + side * p.pairs;
         // offsets outside [0, rows] are clamped, so no row outside is touched
         lo[side] = min(max(p.offsets[q], (int64_t)0), rows);
         hi[side] = min(max(p.offsets[q + 1], lo[side]), rows);
-        double v = 0.0, n = 0.0;
+    }
+    for (int side = 0; side < 2; ++side) {
+        Sum v;
+        int n = 0;
         for (int64_t t = lo[side] + threadIdx.x; t < hi[side]; t += NT) {
             if (valid_id(p.target[t], len) && p.lse[t] != NEG_INF) {
-                v += p.logp[t];
-                n += 1.0;
+                v.add(p.logp[t]);
+                ++n;
             }
         }
         sum[side] = cta_sum(v, s);
-        count[side] = p.average ? fmax(cta_sum(n, s), 1.0) : 1.0;
-        sum[side] /= count[side];
+        count[side] = 1.0f;
+        if (p.average) {
+            // (exact up to 2^24 tokens of one sequence)
+            Sum m;
+            m.add((float)n);
+            count[side] = fmaxf(cta_sum(m, s).value(), 1.0f);
+            const float mean = sum[side].s / count[side];
+            sum[side] = Sum{mean, (fmaf(-mean, count[side], sum[side].s) + sum[side].c) / count[side]};
+        }
     }
-    double gain[2];
-    for (int side = 0; side < 2; ++side)
-        gain[side] = sum[side] - (p.ref_logp ? p.ref_logp[pair + side * p.pairs] : 0.0f);
-    const double u = p.beta * (gain[0] - gain[1]) - p.margin;
+    Sum gain = sum[0];
+    gain.add(Sum{-sum[1].s, -sum[1].c});
+    if (p.ref_logp) {
+        gain.add(-p.ref_logp[pair]);
+        gain.add(p.ref_logp[pair + p.pairs]);
+    }
+    const float u = fmaf(p.beta, gain.value(), -p.margin);
     const float w = p.weight ? p.weight[pair] : 1.0f;
-    PairTerms t{0.0, 0.0};
+    PairTerms t{0.0f, 0.0f};
     if (w != 0.0f)
         t = pair_terms(p, u);
     // rows before the first sequence and after the last belong to no loss
@@ -100,15 +113,15 @@ __global__ void __launch_bounds__(NT) pair_kernel(int64_t rows, int len, Prefere
         for (int64_t r = hi[1] + threadIdx.x; r < rows; r += NT)
             p.dlogp[r] = 0.0f;
     for (int side = 0; side < 2; ++side) {
-        const double c = w == 0.0f ? 0.0 : (side ? -1.0 : 1.0) * w * t.du * p.beta * p.gscale / count[side];
+        const float c = w == 0.0f ? 0.0f : (side ? -w : w) * t.du * p.beta * p.gscale / count[side];
         for (int64_t r = lo[side] + threadIdx.x; r < hi[side]; r += NT)
-            p.dlogp[r] = (float)c;
+            p.dlogp[r] = c;
     }
     if (threadIdx.x == 0) {
-        p.loss[pair] = (float)(w * t.loss);
-        p.seq_logp[pair] = (float)sum[0];
-        p.seq_logp[pair + p.pairs] = (float)sum[1];
-        p.u[pair] = (float)u;
+        p.loss[pair] = w == 0.0f ? 0.0f : w * t.loss;
+        p.seq_logp[pair] = sum[0].value();
+        p.seq_logp[pair + p.pairs] = sum[1].value();
+        p.u[pair] = u;
         __threadfence();
         s_last = atomicAdd(tick, 1u) == gridDim.x - 1;
     }
@@ -116,21 +129,21 @@ __global__ void __launch_bounds__(NT) pair_kernel(int64_t rows, int len, Prefere
     if (!s_last)
         return;
     __threadfence();
-    double v[4] = {0.0, 0.0, 0.0, 0.0};
+    Sum v[4];
     for (int64_t q = threadIdx.x; q < p.pairs; q += NT) {
         const float wq = p.weight ? p.weight[q] : 1.0f;
         if (wq == 0.0f)
             continue;
         const float uq = __ldcg(p.u + q);
-        v[0] += __ldcg(p.loss + q);
-        v[1] += (double)wq * uq;
-        v[2] += uq > 0.0f ? wq : 0.0f;
-        v[3] += wq;
+        v[0].add(__ldcg(p.loss + q));
+        v[1].add(wq * uq);
+        v[2].add(uq > 0.0f ? wq : 0.0f);
+        v[3].add(wq);
     }
     for (int i = 0; i < 4; ++i) {
-        const double total = cta_sum(v[i], s);
+        const float total = cta_sum(v[i], s).value();
         if (threadIdx.x == 0)
-            p.stats[i] = (float)total;
+            p.stats[i] = total;
     }
     if (threadIdx.x == 0)
         *tick = 0;
