@@ -434,12 +434,44 @@ struct PolicyArgs {
     }
 };
 
-// Teacher entries of a row in shared memory, k of each.
+// Sum over groups of G lanes, in every lane; all lanes of the warp call it.
+template <int G>
+__device__ __forceinline__ float group_sum(float v)
+{
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+template <int G>
+__device__ __forceinline__ float group_max(float v)
+{
+    if constexpr (G == 32)
+        return warp_max(v);
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+// Teacher entries of a row in shared memory: k ids, then 3 * k floats.
 struct TeacherRow {
-    int *id;    // column, -1: no entry, or merged into an earlier one
+    int *id;    // column, -1: no entry
     float *q;   // probability
     float *lq;  // its logarithm
     float *x;   // the student's logit
+    float mass;   // sum of q (in the warp that prepared the row)
+    bool repeat;  // an id comes more than once
+
+    __device__ TeacherRow(void *base, int k)
+    {
+        id = static_cast<int *>(base);
+        q = reinterpret_cast<float *>(id + k);
+        lq = q + k;
+        x = lq + k;
+        mass = 0.0f;
+        repeat = false;
+    }
 };
 
 struct DistillArgs {
@@ -471,92 +503,116 @@ struct DistillArgs {
     template <int DT>
     __device__ void write(const LogitRows &, const RowEntry &, const RowStat &) const {}
 
-    // Teacher probabilities of a row, by a whole warp; returns Q = sum q.
-    template <int DT>
-    __device__ float prepare(const LogitRows &a, int64_t r, TeacherRow s) const
+    // The three steps below are for groups of G lanes, a row each; all lanes
+    // of the warp take part, those of rows out of the loss (`live` false) too.
+
+    // Teacher probabilities of a row.
+    template <int DT, int G>
+    __device__ void prepare(const LogitRows &a, int64_t r, bool live, TeacherRow &s) const
     {
-        const int lane = threadIdx.x & 31;
+        const int gl = threadIdx.x & (G - 1);
+        // Ids that come twice are looked for with a hash table in the space of
+        // the floats, filled to two thirds at most; they are rare, and what
+        // they cost is left to patch().
+        const int size = 1 << (31 - __clz(3 * k));
+        int *const table = reinterpret_cast<int *>(s.q);
+        for (int i = gl; i < size; i += G)
+            table[i] = -1;
+        for (int i = gl; i < k; i += G) {
+            const int64_t id = live ? ids[r * k + i] : -1;
+            s.id[i] = valid_id(id, a.len) ? (int)id : -1;
+        }
+        __syncwarp();
+        bool twice = false;
+        for (int i = gl; i < k; i += G) {
+            const int id = s.id[i];
+            if (id < 0)
+                continue;
+            for (unsigned h = (unsigned)id * 2654435761u >> 7;; ++h) {
+                const int was = atomicCAS(&table[h & (size - 1)], -1, id);
+                twice = twice || was == id;
+                if (was == -1 || was == id)
+                    break;
+            }
+        }
+        const unsigned any = __ballot_sync(0xffffffffu, twice);
+        s.repeat = (any >> (threadIdx.x & 31 & ~(G - 1)) & (G == 32 ? 0xffffffffu : (1u << (G & 31)) - 1u)) != 0;
         float vmax = NEG_INF;
-        for (int i = lane; i < k; i += 32) {
-            const int64_t id = ids[r * k + i];
-            const bool ok = valid_id(id, a.len);
-            const float v = ok ? load_any(vdtype, vals, r * k + i) * a.scale : NEG_INF;
-            s.id[i] = ok ? (int)id : -1;
+        for (int i = gl; i < k; i += G) {
+            const int id = s.id[i];
+            const float v = id >= 0 ? load_any(vdtype, vals, r * k + i) * a.scale : NEG_INF;
             s.lq[i] = v;
-            s.x[i] = ok ? load_elem<DT>(a.x, r * a.ld + id) : 0.0f;
+            s.x[i] = id >= 0 ? load_elem<DT>(a.x, r * a.ld + id) : 0.0f;
             vmax = fmaxf(vmax, v);
         }
         float norm;
         if (lse) {
-            norm = lse[r];
+            norm = live ? lse[r] : 0.0f;
         } else {
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-                vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+            vmax = group_max<G>(fmaxf(vmax, NEG_INF));
             float sum = 0.0f;
-            for (int i = lane; i < k; i += 32)
+            for (int i = gl; i < k; i += G)
                 sum += expf(s.lq[i] - (vmax == NEG_INF ? 0.0f : vmax));
-            sum = warp_sum(sum);
+            sum = group_sum<G>(sum);
             norm = vmax == NEG_INF && sum == 0.0f ? 0.0f : vmax + logf(sum);
         }
         float Q = 0.0f;
-        for (int i = lane; i < k; i += 32) {
+        for (int i = gl; i < k; i += G) {
             const float lq = s.lq[i] - norm;
             const float q = s.id[i] < 0 ? 0.0f : expf(lq);
             s.lq[i] = lq;
             s.q[i] = q;
             Q += q;
         }
+        s.mass = group_sum<G>(Q);
         __syncwarp();
-        return warp_sum(Q);
     }
-    // The row's loss, by a whole warp; `t` holds the student's statistics.
-    __device__ void finish(const LogitRows &a, const RowEntry &e, const RowStat &t, TeacherRow s) const
+    // The row's loss, from the student's statistics.
+    template <int G>
+    __device__ void finish(const LogitRows &a, const RowEntry &e, const RowStat &t, const TeacherRow &s) const
     {
-        const int lane = threadIdx.x & 31;
+        const int gl = threadIdx.x & (G - 1);
+        const bool on = e.state == ROW_LIVE && !t.empty;
         float v = 0.0f;
-        if (e.state == ROW_LIVE && !t.empty) {
-            for (int i = lane; i < k; i += 32)
+        if (on)
+            for (int i = gl; i < k; i += G)
                 if (s.q[i] != 0.0f)
                     v += s.q[i] * (s.lq[i] - ((s.x[i] - t.m) * a.scale - t.ln));
-            v = warp_sum(v) * e.w;
-        }
-        if (lane == 0)
-            loss[e.r] = v;
+        v = group_sum<G>(v);
+        if (gl == 0 && e.state != ROW_END)
+            loss[e.r] = on ? v * e.w : 0.0f;
     }
-    // The teacher's columns of the gradient once more, by a whole warp after
-    // the rest of the columns [begin, end) is written: g_id = mul 2^(...) - c q.
-    // An id that comes more than once is written by its first entry.
-    template <int DT>
-    __device__ void patch(const LogitRows &a, const RowEntry &e, RowGrad g, TeacherRow s, int begin, int end) const
+    // The teacher's columns of the gradient once more, after the rest of the
+    // columns [begin, end) is written: g_id = mul 2^(...) - c q.  An id that
+    // comes more than once is written by its first entry.
+    template <int DT, int G>
+    __device__ void patch(const LogitRows &a, const RowEntry &e, const RowGrad &g, const TeacherRow &s, int begin,
+                          int end) const
     {
         const float c = e.w * gscale * a.scale;
-        for (int i = threadIdx.x & 31; i < k; i += 32) {
+        for (int i = threadIdx.x & (G - 1); i < k; i += G) {
             const int id = s.id[i];
             if (id < begin || id >= end)
                 continue;
-            float q = 0.0f;
-            bool first = true;
-            for (int j = 0; j < k; ++j)
-                if (s.id[j] == id) {
-                    first = first && j >= i;
-                    q += s.q[j];
-                }
-            if (first)
-                store_elem<DT>(a.dx, e.r * a.ldd + id, g.mul * ex2(fmaf(s.x[i], g.fa, g.fb) * g.fc) - c * q);
+            float q = s.q[i];
+            if (s.repeat) {
+                q = 0.0f;
+                bool first = true;
+                for (int j = 0; j < k; ++j)
+                    if (s.id[j] == id) {
+                        first = first && j >= i;
+                        q += s.q[j];
+                    }
+                if (!first)
+                    continue;
+            }
+            store_elem<DT>(a.dx, e.r * a.ldd + id, g.mul * ex2(fmaf(s.x[i], g.fa, g.fb) * g.fc) - c * q);
         }
     }
     __device__ void total(int64_t r, int, Sum (&v)[TOTALS]) const
     {
         v[0].add(__ldcg(loss + r));
         v[1].add(weight ? weight[r] : 1.0f);
-    }
-    static __device__ __forceinline__ float warp_sum(float v)
-    {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            v += __shfl_xor_sync(0xffffffffu, v, off);
-        return v;
     }
 };
 

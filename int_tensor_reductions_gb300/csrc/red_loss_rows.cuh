@@ -158,14 +158,19 @@ struct SoftRun {
             const f32x2 a = pack2(s2, s2), b = pack2(-m2, -m2);
 #pragma unroll
             for (int u = 0; u < N; ++u)
-#pragma unroll
-                for (int i = 0; i < VEC_ELEMS<DT> / 2; ++i)
-                    l = add2(l, exp2_2(fma2(vec_pair<DT>(v[u], i), a, b)));
+                add_near<DT>(v[u], a, b);
         } else {
 #pragma unroll
             for (int u = 0; u < N; ++u)
                 l = far_sum<DT>(v[u], m, s2, l);
         }
+    }
+    template <int DT>
+    __device__ __forceinline__ void add_near(const uint4 &v, f32x2 a, f32x2 b)
+    {
+#pragma unroll
+        for (int i = 0; i < VEC_ELEMS<DT> / 2; ++i)
+            l = add2(l, exp2_2(fma2(vec_pair<DT>(v, i), a, b)));
     }
     __device__ __forceinline__ void add(float x, float s2) { l = add2(l, pack2(ex2(term(x, m, s2)), 0.0f)); }
     // exponent of one logit under the maximum m, near or far
@@ -417,10 +422,6 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
     using Shared = RowShared<NW, PARTS<OP>>;
     Shared &sh = *reinterpret_cast<Shared *>(ring + slots * U * NT);
     unsigned char *const lists = reinterpret_cast<unsigned char *>(&sh + 1);
-    auto teacher = [&](int buf) {
-        float *const f = reinterpret_cast<float *>(lists) + buf * 4 * teacher_k;
-        return TeacherRow{reinterpret_cast<int *>(f), f + teacher_k, f + 2 * teacher_k, f + 3 * teacher_k};
-    };
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int AHEAD = OP::TEACHER ? TEACHERS : 2;
     const int fixed = 3 * group + AHEAD;
@@ -576,7 +577,7 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
         if constexpr (OP::TEACHER) {
             // ---- teacher warp w: rows w, w + TEACHERS, ...
             const int w = warp - NW - 2;
-            const TeacherRow list = teacher(w);
+            TeacherRow list(lists + (size_t)w * 16 * teacher_k, teacher_k);
             for (int i = 0;; ++i) {
                 // entries are visible a few rows ahead; walk to this warp's next
                 const RowEntry e = sh.queue[i % ROW_Q];
@@ -585,20 +586,20 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
                 if (i % TEACHERS != w)
                     continue;
                 if (e.state == ROW_LIVE) {
-                    const float Q = op.template prepare<DT>(a, e.r, list);
+                    op.template prepare<DT, 32>(a, e.r, true, list);
                     if (lane == 0)
-                        sh.mass[w] = Q;
+                        sh.mass[w] = list.mass;
                 }
                 row_barrier(i);
                 RowStat t{};
                 if (e.state == ROW_LIVE)
                     t = row_stat(a, stat_of(i));
-                op.finish(a, e, t, list);
+                op.template finish<32>(a, e, t, list);
                 if (a.dx && e.state == ROW_LIVE) {
-                    const RowGrad g = op.template grad<DT>(a, e, t, sh.mass[w]);
+                    const RowGrad g = op.template grad<DT>(a, e, t, list.mass);
                     bar_sync(1 + TEACHERS + w, NT + 32);
                     if (!g.zero)
-                        op.template patch<DT>(a, e, g, list, 0, a.len);
+                        op.template patch<DT, 32>(a, e, g, list, 0, a.len);
                 } else if (a.dx) {
                     zero_row_bulk<DT>(static_cast<T *>(a.dx) + e.r * a.ldd, a.len, sh.zeros);
                 }
@@ -822,118 +823,138 @@ __global__ void __launch_bounds__(TOTAL_NT) total_kernel(int64_t rows, int len, 
 
 // ------------------------------------------------------------- short rows
 
-constexpr int WARP_NT = 256;
+constexpr int GROUP_NT = 256;
 
-// A warp per row, the row in registers (NV vectors per lane): rows too short
-// for a CTA barrier each.  The next row's entry is fetched while this row is
-// on its way.
-template <int DT, class OP, int NV>
-__global__ void __launch_bounds__(WARP_NT) warp_row_kernel(LogitRows a, OP op, int teacher_k)
+// G lanes per row, the row in registers (NV vectors per lane): rows too short
+// for a CTA barrier each.  The shorter the row, the fewer the lanes, so that
+// what is done once per row (the loss itself, its logarithms and exponentials,
+// the reductions) is done for 32 / G rows at a time.  The next row's entry is
+// fetched while this row is on its way.
+template <int DT, class OP, int G, int NV>
+__global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(LogitRows a, OP op, int teacher_k)
 {
     using T = typename Elem<DT>::T;
     constexpr int E = VEC_ELEMS<DT>;
+    constexpr int ROWS = GROUP_NT / G;  // rows of a CTA at a time
     extern __shared__ __align__(16) unsigned char smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float *const f = reinterpret_cast<float *>(smem) + warp * 4 * teacher_k;
-    const TeacherRow list{reinterpret_cast<int *>(f), f + teacher_k, f + 2 * teacher_k, f + 3 * teacher_k};
+    const int gl = threadIdx.x & (G - 1), group = threadIdx.x / G;
+    TeacherRow list(smem + (size_t)group * 16 * teacher_k, teacher_k);
     const float s2 = a.s2;
     const T *const x = static_cast<const T *>(a.x);
     T *const dx = static_cast<T *>(a.dx);
     pdl_enter();
 
-    const int64_t step = (int64_t)gridDim.x * (WARP_NT / 32);
-    int64_t r = (int64_t)blockIdx.x * (WARP_NT / 32) + warp;
-    RowEntry e{}, n{};
-    if (r < a.rows) {
-        op.load(r, n);
-        op.template settle<DT>(a, n);
-    }
-    for (; r < a.rows; r += step) {
-        e = n;
-        T *const grow = dx + r * a.ldd;
-        if (e.state == ROW_OUT) {
-            if (r + step < a.rows) {
-                op.load(r + step, n);
-                op.template settle<DT>(a, n);
-            }
-            if constexpr (OP::TEACHER)
-                op.finish(a, e, RowStat{}, list);
-            else if (lane == 0)
-                op.template write<DT>(a, e, RowStat{});
-            if (dx)
-                zero_row<DT>(grow, a.len, lane, 32);
-            continue;
+    const int64_t step = (int64_t)gridDim.x * ROWS;
+    RowEntry n{};
+    auto fetch = [&](int64_t r) {
+        n.state = ROW_END;
+        if (r < a.rows) {
+            op.load(r, n);
+            op.template settle<DT>(a, n);
         }
+    };
+    fetch((int64_t)blockIdx.x * ROWS + group);
+    // (the loop is the same for all of a warp: its first group has the first row)
+    for (int64_t r0 = (int64_t)blockIdx.x * ROWS + (group & ~(32 / G - 1)); r0 < a.rows; r0 += step) {
+        const int64_t r = r0 + (group & (32 / G - 1));
+        const RowEntry e = n;
+        const bool live = e.state == ROW_LIVE;
         const T *const row = x + r * a.ld;
         const int h = head_elems<DT>(row, a.len), nvec = (a.len - h) / E;
         uint4 v[NV];
+        // the row's ragged ends, fewer than E elements each
+        constexpr int ENDS = (2 * (E - 1) + G - 1) / G;
+        float end_x[ENDS];
+        auto end_at = [&](int k) {
+            const int i = gl + k * G, tail = a.len - h - nvec * E;
+            return i < h ? i : (i - h < tail ? a.len - tail + i - h : -1);
+        };
+        if (live) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (i * 32 + lane < nvec)
-                v[i] = reinterpret_cast<const uint4 *>(row + h)[i * 32 + lane];
-        int edge = -1;
-        if (lane < h)
-            edge = lane;
-        else if (lane >= 8 && lane < 16 && h + nvec * E + lane - 8 < a.len)
-            edge = h + nvec * E + lane - 8;
-        float xe = 0.0f;
-        if (edge >= 0)
-            xe = load_elem<DT>(row, edge);
-        if (r + step < a.rows)
-            op.load(r + step, n);
-        float Q = 0.0f;
+            for (int i = 0; i < NV; ++i)
+                if (i * G + gl < nvec)
+                    v[i] = reinterpret_cast<const uint4 *>(row + h)[i * G + gl];
+#pragma unroll
+            for (int k = 0; k < ENDS; ++k) {
+                const int j = end_at(k);
+                end_x[k] = j >= 0 ? load_elem<DT>(row, j) : NEG_INF;
+            }
+        }
+        fetch(r + step);
         if constexpr (OP::TEACHER)
-            Q = op.template prepare<DT>(a, r, list);
+            op.template prepare<DT, G>(a, r, live, list);
 
         RowStat t{};
         if constexpr (OP::STATS) {
-            float top = edge >= 0 ? fmaxf(xe, NEG_INF) : NEG_INF;  // (not a NaN)
+            float top = NEG_INF;
+            if (live) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i * 32 + lane < nvec)
-                    top = fmaxf(top, vec_max<DT>(v[i]));
-            top = warp_max(top);
+                for (int i = 0; i < NV; ++i)
+                    if (i * G + gl < nvec)
+                        top = fmaxf(top, vec_max<DT>(v[i]));
+#pragma unroll
+                for (int k = 0; k < ENDS; ++k)
+                    top = fmaxf(top, end_x[k]);
+            }
+            top = group_max<G>(top);
             SoftRun run;
             run.init();
             run.m = top;
+            if (live && is_near(top * s2)) {
+                const f32x2 sa = pack2(s2, s2), sb = pack2(-top * s2, -top * s2);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (i * 32 + lane < nvec) {
-                    const uint4 w[1] = {v[i]};
-                    run.template add<DT, 1>(w, s2);
-                }
-            if (edge >= 0)
-                run.add(xe, s2);
-            float l = run.stat().l;
+                for (int i = 0; i < NV; ++i)
+                    if (i * G + gl < nvec)
+                        run.template add_near<DT>(v[i], sa, sb);
+            } else if (live) {
+                for (int i = gl; i < nvec; i += G)
+                    run.l = SoftRun::template far_sum<DT>(reinterpret_cast<const uint4 *>(row + h)[i], top, s2, run.l);
+            }
+            if (live) {
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-                l += __shfl_xor_sync(0xffffffffu, l, off);
-            t = row_stat(a, SoftStat{top, l});
-            if constexpr (OP::TEACHER)
-                op.finish(a, e, t, list);
-            else if (lane == 0)
-                op.template write<DT>(a, e, t);
+                for (int k = 0; k < ENDS; ++k)
+                    run.add(end_x[k], s2);
+            }
+            t = row_stat(a, SoftStat{top, group_sum<G>(run.stat().l)});
         }
-        if (r + step < a.rows)
-            op.template settle<DT>(a, n);
+        if constexpr (OP::TEACHER)
+            op.template finish<G>(a, e, t, list);
+        else if (gl == 0 && e.state != ROW_END)
+            op.template write<DT>(a, e, t);
         if (!dx)
             continue;
-        const RowGrad g = op.template grad<DT>(a, e, t, Q);
+        T *const grow = dx + r * a.ldd;
+        RowGrad g = op.template grad<DT>(a, e, t, list.mass);
+        g.zero = g.zero || !live;
         const bool aligned = ((uintptr_t)(grow + h) & 15u) == 0;
+        if (!g.zero && !g.far && aligned) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (i * 32 + lane < nvec) {
-                const int j = h + (i * 32 + lane) * E;
-                const uint4 o = g.zero ? make_uint4(0, 0, 0, 0)
-                                       : (g.far ? vec_grad<DT, true>(v[i], g, j) : vec_grad<DT>(v[i], g, j));
-                store_vec<DT>(grow + j, o, aligned);
+            for (int i = 0; i < NV; ++i)
+                if (i * G + gl < nvec) {
+                    const int j = h + (i * G + gl) * E;
+                    *reinterpret_cast<uint4 *>(grow + j) = vec_grad<DT>(v[i], g, j);
+                }
+        } else if (e.state != ROW_END) {
+            // rarer rows, one vector at a time from memory again
+            for (int i = gl; i < nvec; i += G) {
+                const int j = h + i * E;
+                store_vec<DT>(grow + j, g.zero ? make_uint4(0, 0, 0, 0)
+                                               : vec_grad<DT, true>(*reinterpret_cast<const uint4 *>(row + j), g, j),
+                              aligned);
             }
-        if (edge >= 0)
-            store_elem<DT>(grow, edge, g.zero ? 0.0f : elem_grad<DT>(xe, g, edge));
+        }
+        if (e.state != ROW_END) {
+#pragma unroll
+            for (int k = 0; k < ENDS; ++k) {
+                const int j = end_at(k);
+                if (j >= 0)
+                    store_elem<DT>(grow, j, g.zero ? 0.0f : elem_grad<DT>(end_x[k], g, j));
+            }
+        }
         if constexpr (OP::TEACHER) {
             __syncwarp();
             if (!g.zero)
-                op.template patch<DT>(a, e, g, list, 0, a.len);
+                op.template patch<DT, G>(a, e, g, list, 0, a.len);
             __syncwarp();
         }
     }
@@ -956,8 +977,7 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
     __shared__ SoftStat s_part[FEW_NW], s_slice[MAX_CLUSTER];
     __shared__ float s_mass;
     __shared__ bool s_last;
-    float *const f = reinterpret_cast<float *>(smem);
-    const TeacherRow list{reinterpret_cast<int *>(f), f + teacher_k, f + 2 * teacher_k, f + 3 * teacher_k};
+    TeacherRow list(smem, teacher_k);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cs = cluster_size(), rank = cluster_rank();
     const int64_t r = blockIdx.x / cs;
@@ -992,9 +1012,9 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
     if (e.state == ROW_LIVE) {
         if constexpr (OP::TEACHER) {
             if (warp == 0) {
-                const float Q = op.template prepare<DT>(a, r, list);
+                op.template prepare<DT, 32>(a, r, true, list);
                 if (lane == 0)
-                    s_mass = Q;
+                    s_mass = list.mass;
             }
         }
         if constexpr (OP::STATS) {
@@ -1032,7 +1052,7 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
     if (rank == 0) {
         if constexpr (OP::TEACHER) {
             if (warp == 0)
-                op.finish(a, e, t, list);
+                op.template finish<32>(a, e, t, list);
         } else if (tid == 0) {
             op.template write<DT>(a, e, t);
         }
@@ -1053,7 +1073,7 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
         if constexpr (OP::TEACHER) {
             __syncthreads();
             if (warp == 0 && !g.zero)
-                op.template patch<DT>(a, e, g, list, rank == 0 ? 0 : j0, rank == cs - 1 ? a.len : j0 + n * E);
+                op.template patch<DT, 32>(a, e, g, list, rank == 0 ? 0 : j0, rank == cs - 1 ? a.len : j0 + n * E);
         }
     } else if (a.dx) {
         zero_row<DT>(grow, a.len, rank * FEW_NT + tid, cs * FEW_NT);
@@ -1103,8 +1123,9 @@ cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), unsigned grid, unsigned bl
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// Longest row of the warp kernel.
-constexpr size_t WARP_ROW_BYTES = 8192;
+// Longest row of the group kernel.
+constexpr size_t GROUP_ROW_BYTES = 8192;
+
 // The few-row kernel is taken while its CTAs, with the largest cluster that
 // allows it, are at most this many per two SMs (and a thread's slice 8
 // vectors).  us, few-row kernel against the row kernel: logprob 1 x 65536 bf16
@@ -1152,27 +1173,33 @@ int launch_row_kernel(const LogitRows &a, const OP &op, int per_sm, int teacher_
     return cuda_fail(e != cudaSuccess ? e : cudaGetLastError(), "row kernel launch");
 }
 
-template <int DT, class OP, int NV>
-int launch_warp_kernel(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s, const DeviceInfo &di)
+template <int DT, class OP, int G, int NV>
+int launch_group_kernel(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s, const DeviceInfo &di)
 {
-    const auto kernel = warp_row_kernel<DT, OP, NV>;
-    const size_t smem = (size_t)(WARP_NT / 32) * 4 * 4 * teacher_k;
-    static std::atomic<int> ready{0};
-    if (smem > 48 * 1024 && !ready.load(std::memory_order_relaxed)) {
-        const cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)CTA_SMEM);
-        if (e != cudaSuccess)
-            return cuda_fail(e, "warp row kernel: shared memory");
-        ready.store(1, std::memory_order_relaxed);
+    const auto kernel = group_row_kernel<DT, OP, G, NV>;
+    constexpr int ROWS = GROUP_NT / G;
+    const size_t smem = (size_t)ROWS * 16 * teacher_k;
+    // residency, kept per instance for the last list length asked for
+    static std::atomic<int64_t> known{-1};
+    int64_t k = known.load(std::memory_order_relaxed);
+    if (k < 0 || (k >> 8) != teacher_k) {
+        cudaError_t e = cudaSuccess;
+        if (smem > 48 * 1024)
+            e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CTA_SMEM);
+        int occ = 0;
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, (const void *)kernel, GROUP_NT, smem);
+        if (e != cudaSuccess || occ < 1)
+            return e != cudaSuccess ? cuda_fail(e, "row group kernel: occupancy")
+                                    : fail(RED_ECUDA, "row group kernel cannot be resident on this device");
+        k = (int64_t)teacher_k << 8 | occ;
+        known.store(k, std::memory_order_relaxed);
     }
-    int occ = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, (const void *)kernel, WARP_NT, smem);
-    if (e != cudaSuccess || occ < 1)
-        return cuda_fail(e, "warp row kernel: occupancy");
-    const int64_t want = (a.rows + WARP_NT / 32 - 1) / (WARP_NT / 32), cap = (int64_t)di.sms * occ;
-    e = launch_pdl_smem(kernel, (unsigned)(want < cap ? want : cap), WARP_NT, smem, 1, s, a, op, teacher_k);
+    const int64_t want = (a.rows + ROWS - 1) / ROWS, cap = di.sms * (k & 255);
+    const cudaError_t e =
+        launch_pdl_smem(kernel, (unsigned)(want < cap ? want : cap), GROUP_NT, smem, 1, s, a, op, teacher_k);
     count_launches(1);
-    return cuda_fail(e != cudaSuccess ? e : cudaGetLastError(), "warp row kernel launch");
+    return cuda_fail(e != cudaSuccess ? e : cudaGetLastError(), "row group kernel launch");
 }
 
 template <int DT, class OP, int NV>
@@ -1215,14 +1242,19 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
     if (st != RED_OK)
         return st;
     const size_t bytes = (size_t)a.len * sizeof(typename Elem<DT>::T);
-    if (bytes <= WARP_ROW_BYTES) {
-        // vectors per lane of the longest interior
-        const size_t nv = (bytes / 16 + 31) / 32;
-        if (nv <= 2)
-            return launch_warp_kernel<DT, OP, 2>(a, op, teacher_k, s, di);
-        if (nv <= 8)
-            return launch_warp_kernel<DT, OP, 8>(a, op, teacher_k, s, di);
-        return launch_warp_kernel<DT, OP, 16>(a, op, teacher_k, s, di);
+    if (bytes <= GROUP_ROW_BYTES) {
+        // lanes per row: 128 bytes each; a warp where the lists of that many
+        // rows would not leave room for a second CTA
+        const bool wide = (size_t)(GROUP_NT / 4) * 16 * teacher_k > 96 * 1024;
+        if (bytes <= 512 && !wide)
+            return launch_group_kernel<DT, OP, 4, 8>(a, op, teacher_k, s, di);
+        if (bytes <= 1024 && !wide)
+            return launch_group_kernel<DT, OP, 8, 8>(a, op, teacher_k, s, di);
+        if (bytes <= 2048 && !wide)
+            return launch_group_kernel<DT, OP, 16, 8>(a, op, teacher_k, s, di);
+        if (bytes <= 4096)
+            return launch_group_kernel<DT, OP, 32, 8>(a, op, teacher_k, s, di);
+        return launch_group_kernel<DT, OP, 32, 16>(a, op, teacher_k, s, di);
     }
     const int64_t nvec = (int64_t)(bytes / 16);
     for (int cluster = MAX_CLUSTER; cluster >= 2; cluster /= 2) {
