@@ -356,95 +356,38 @@ def red_colprod(x: torch.Tensor, out: torch.Tensor | None = None, stream=None, d
 
 # ------------------------------------------ losses over rows of logits
 
-_LOGIT_DTYPES = {torch.float32: RED_F32, torch.float16: RED_F16, torch.bfloat16: RED_BF16}
 _PREF_KINDS = {"sigmoid": RED_PREF_SIGMOID, "hinge": RED_PREF_HINGE, "squared": RED_PREF_SQUARED}
+_entry = None
 
 
-# The calls of one training step on a few rows are shorter than a dozen Python
-# attribute look-ups are long: the checks below use integers (device indices,
-# raw streams) rather than torch.device and Stream objects.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+def _losses():
+    """The compiled entry of the losses (csrc/red_torch.cpp), beside libred.so."""
+    global _entry
+    if _entry is None:
+        lib()
+        from . import _red_torch
+        _entry = _red_torch
+    return _entry
 
 
-def _logits(x, scale):
-    """(C arguments (dtype, x, rows, len, ld, scale), rows, device index) of the logits."""
-    code = _LOGIT_DTYPES.get(x.dtype)
-    if code is None:
-        raise ValueError(f"x must be float32, float16 or bfloat16, got {x.dtype}")
-    device = x.get_device()
-    if device < 0:
-        raise ValueError("x must be a CUDA tensor")
-    if x.dim() != 2:
-        raise ValueError("x must be 2-D (rows, vocab)")
-    rows, length = x.shape
-    ld, step = x.stride()
-    if rows <= 1:
-        ld = length
-    if step != 1 and length > 1 and rows > 0:
-        raise ValueError("x's rows must be contiguous (stride 1 along the vocabulary)")
-    if ld < length:
-        raise ValueError(f"x's row stride {ld} is smaller than its {length} columns")
-    return (code, x.data_ptr(), rows, length, ld, scale), rows, device
+def _on(stream, device):
+    """(address, stream object) of a stream argument that is not None."""
+    user = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+    return user.cuda_stream, user
 
 
-def _vector(t, name, dtype, device, n):
-    """Pointer of a contiguous vector of n elements on the given device, or None for None."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, x on cuda:{device}")
-    if t.numel() != n:
-        raise ValueError(f"{name} must hold {n} element(s), has {t.numel()}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _grad_out(grad, x, ld, name="grad"):
-    """(tensor, pointer, row stride) of a gradient: False for none, None for a
-    new one with x's row stride, or a tensor to write (x itself for in place)."""
-    if grad is None:
-        rows, length = x.shape
-        grad = torch.empty((rows, ld), dtype=x.dtype, device=x.device)
-        if ld != length:
-            grad = grad[:, :length]
-        return grad, grad.data_ptr(), ld
-    if grad is False:
-        return None, None, 0
-    if grad.dtype != x.dtype or grad.get_device() != x.get_device() or grad.shape != x.shape:
-        raise ValueError(f"{name} must have x's dtype, device and shape")
-    return grad, grad.data_ptr(), _row_strided(grad, name)
-
-
-def _floats(x, n):
-    """(tensor, pointer) of n new floats beside x."""
-    t = torch.empty(n, dtype=torch.float32, device=x.device)
-    return t, t.data_ptr()
-
-
-def _loss_call(fn, device, stream, made, *args):
-    """C function ``fn`` on ``stream``.  ``made`` are tensors this call
-    allocated: on a stream that is not the current one they are marked as used
-    there, so that the allocator does not hand them out again before the work
-    is done."""
-    if stream is None:
-        raw = _raw_stream(device)
-    else:
-        user = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
-        raw = user.cuda_stream
-        for t in made:
-            if t is not None:
+def _done(result, user, given=None):
+    """The results of a compiled call, or RedError for its status.  What the
+    call allocated is marked as used on the ``user`` stream when that is not
+    the current one, so that the allocator does not hand it out again before
+    the work is done."""
+    if result.__class__ is int:
+        raise RedError(result, red_last_error())
+    if user is not None:
+        for t in result if isinstance(result, tuple) else (result,):
+            if t is not None and t is not given:
                 t.record_stream(user)
-    if _current_device() == device:
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, raw)
-    if status != RED_OK:
-        raise RedError(status, red_last_error())
+    return result
 
 
 def red_logprob(x: torch.Tensor, target: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
@@ -452,20 +395,9 @@ def red_logprob(x: torch.Tensor, target: torch.Tensor, scale: float = 1.0, out: 
     """Log-probabilities logp[r] = log_softmax(scale * x[r])[target[r]] of a
     (rows, vocab) matrix of float32, float16 or bfloat16 logits (rows may be
     strided) and the rows' log-sum-exp; returns (logp, lse), fp32.  A row whose
-    target is outside the vocabulary (e.g. -100) is not read and gives 0."""
-    head, rows, device = _logits(x, scale)
-    f32 = torch.float32
-    if out is None:
-        out, out_ptr = _floats(x, rows)
-    else:
-        out_ptr = _vector(out, "out", f32, device, rows)
-    if lse is None:
-        lse, lse_ptr = _floats(x, rows)
-    else:
-        lse_ptr = _vector(lse, "lse", f32, device, rows)
-    _loss_call(lib().red_logprob, device, stream, (out, lse), *head,
-               _vector(target, "target", torch.int64, device, rows), out_ptr, lse_ptr)
-    return out, lse
+    target is outside the vocabulary (e.g. -100) gives 0."""
+    at, user = (None, None) if stream is None else _on(stream, x.device)
+    return _done((_entry or _losses()).logprob(x, target, scale, out, lse, at), user)
 
 
 def red_logprob_grad(x: torch.Tensor, target: torch.Tensor, lse: torch.Tensor, dlogp: torch.Tensor,
@@ -473,14 +405,8 @@ def red_logprob_grad(x: torch.Tensor, target: torch.Tensor, lse: torch.Tensor, d
     """Backward of red_logprob: the gradient by x, given the gradient ``dlogp``
     by logp and red_logprob's lse.  ``out`` may be x (in place); a new one has
     x's row stride."""
-    head, rows, device = _logits(x, scale)
-    if out is False:
-        raise ValueError("out must be a tensor or None")
-    out, out_ptr, ldd = _grad_out(out, x, head[4], "out")
-    _loss_call(lib().red_logprob_grad, device, stream, (out,), *head,
-               _vector(target, "target", torch.int64, device, rows), _vector(lse, "lse", torch.float32, device, rows),
-               _vector(dlogp, "dlogp", torch.float32, device, rows), out_ptr, ldd)
-    return out
+    at, user = (None, None) if stream is None else _on(stream, x.device)
+    return _done((_entry or _losses()).logprob_grad(x, target, lse, dlogp, scale, out, at), user, out)
 
 
 def red_distill(x: torch.Tensor, ids: torch.Tensor, vals: torch.Tensor, lse: torch.Tensor | None = None,
@@ -493,22 +419,8 @@ def red_distill(x: torch.Tensor, ids: torch.Tensor, vals: torch.Tensor, lse: tor
     per row times ``weight``, stats = (sum of loss, sum of weight), and
     grad_scale times the gradient of the summed loss by x.  ``grad``: None for
     a new tensor, a tensor to write (x: in place), False for the loss alone."""
-    head, rows, device = _logits(x, scale)
-    if ids.dim() != 2 or vals.shape != ids.shape or ids.shape[0] != rows:
-        raise ValueError("ids and vals must be (rows, k)")
-    vcode = _LOGIT_DTYPES.get(vals.dtype)
-    if vcode is None:
-        raise ValueError(f"vals must be float32, float16 or bfloat16, got {vals.dtype}")
-    k = ids.shape[1]
-    f32 = torch.float32
-    grad, grad_ptr, ldd = _grad_out(grad, x, head[4])
-    flat, at = _floats(x, rows + 2)
-    stats, loss = flat.split((2, rows))
-    _loss_call(lib().red_distill, device, stream, (flat, grad), *head, k,
-               _vector(ids, "ids", torch.int64, device, rows * k), vcode,
-               _vector(vals, "vals", vals.dtype, device, rows * k), _vector(lse, "lse", f32, device, rows),
-               _vector(weight, "weight", f32, device, rows), grad_scale, at + 8, at, grad_ptr, ldd)
-    return loss, stats, grad
+    at, user = (None, None) if stream is None else _on(stream, x.device)
+    return _done((_entry or _losses()).distill(x, ids, vals, lse, weight, scale, grad_scale, grad, at), user, grad)
 
 
 def red_policy(x: torch.Tensor, target: torch.Tensor, old_logp: torch.Tensor, adv: torch.Tensor,
@@ -520,17 +432,9 @@ def red_policy(x: torch.Tensor, target: torch.Tensor, old_logp: torch.Tensor, ad
     e^(logp - old_logp), d = ref_logp - logp, times ``weight``.  Returns (loss,
     logp, stats, grad); stats = sums of (loss, weight * (e^d - d - 1), weight
     of clipped tokens, weight).  ``grad`` as for red_distill."""
-    head, rows, device = _logits(x, scale)
-    f32 = torch.float32
-    grad, grad_ptr, ldd = _grad_out(grad, x, head[4])
-    flat, at = _floats(x, 2 * rows + 4)
-    stats, loss, logp = flat.split((4, rows, rows))
-    _loss_call(lib().red_policy, device, stream, (flat, grad), *head,
-               _vector(target, "target", torch.int64, device, rows),
-               _vector(old_logp, "old_logp", f32, device, rows), _vector(ref_logp, "ref_logp", f32, device, rows),
-               _vector(adv, "adv", f32, device, rows), _vector(weight, "weight", f32, device, rows), clip_low,
-               clip_high, kl_coef, grad_scale, at + 16, at + 16 + 4 * rows, at, grad_ptr, ldd)
-    return loss, logp, stats, grad
+    at, user = (None, None) if stream is None else _on(stream, x.device)
+    return _done((_entry or _losses()).policy(x, target, old_logp, adv, ref_logp, weight, clip_low, clip_high, kl_coef,
+                                              scale, grad_scale, grad, at), user, grad)
 
 
 def red_preference(x: torch.Tensor, target: torch.Tensor, offsets: torch.Tensor,
@@ -545,26 +449,13 @@ def red_preference(x: torch.Tensor, target: torch.Tensor, offsets: torch.Tensor,
     seq_logp, stats, grad): loss per pair times ``weight``, the sequences' sums
     or means, stats = sums of (loss, weight * u, weight of u > 0, weight).
     ``grad`` as for red_distill."""
-    head, rows, device = _logits(x, scale)
-    entries = offsets.numel()
-    if entries % 2 != 1:
-        raise ValueError("offsets needs 2 * pairs + 1 entries")
-    pairs = entries // 2
     if isinstance(kind, str):
         if kind not in _PREF_KINDS:
             raise ValueError(f"unknown kind {kind!r}")
         kind = _PREF_KINDS[kind]
-    grad, grad_ptr, ldd = _grad_out(grad, x, head[4])
-    f32 = torch.float32
-    flat, at = _floats(x, 3 * rows + 4 * pairs + 4)
-    stats, seq_logp, loss, _ = flat.split((4, 2 * pairs, pairs, 3 * rows + pairs))
-    _loss_call(lib().red_preference, device, stream, (flat, grad), *head,
-               _vector(target, "target", torch.int64, device, rows),
-               _vector(offsets, "offsets", torch.int64, device, entries), pairs,
-               _vector(ref_logp, "ref_logp", f32, device, 2 * pairs), _vector(weight, "weight", f32, device, pairs),
-               int(kind), beta, margin, smoothing, int(bool(average)), grad_scale, at + 16 + 8 * pairs, at + 16, at,
-               at + 16 + 12 * pairs, grad_ptr, ldd)
-    return loss, seq_logp, stats, grad
+    at, user = (None, None) if stream is None else _on(stream, x.device)
+    return _done((_entry or _losses()).preference(x, target, offsets, ref_logp, weight, kind, beta, margin, smoothing,
+                                                  average, scale, grad_scale, grad, at), user, grad)[:4]
 
 
 def red_set_full_mode(mode: int) -> None:

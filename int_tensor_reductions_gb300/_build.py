@@ -1,5 +1,6 @@
 """Build step of libred.so: nvcc for sm_103a, one object per .cu (compiled in
-parallel), linked into ``int_tensor_reductions_gb300/libred.so`` in-tree."""
+parallel), linked into ``int_tensor_reductions_gb300/libred.so`` in-tree, and
+of the losses' Python entry, ``_red_torch`` (g++ against torch and libred.so)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -13,6 +14,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build", "red")
 LIB = os.path.join(PKG, "libred.so")
+EXT = os.path.join(PKG, "_red_torch.so")
+EXT_SRC = os.path.join(CSRC, "red_torch.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -33,14 +36,45 @@ def _sources():
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.cuh")) + \
-        [os.path.abspath(__file__)]
+        [EXT_SRC, os.path.abspath(__file__)]
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return any(os.path.getmtime(d) > t for d in _deps())
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (what, " ".join(cmd), r.stdout + r.stderr))
+    return r
+
+
+def _compile_ext() -> str:
+    """The object of the Python entry."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    obj = os.path.join(OBJDIR, "red_torch.o")
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    dirs = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)] + ["-I" + d for d in dirs] +
+         ["-c", EXT_SRC, "-o", obj], "g++ on red_torch.cpp")
+    return obj
+
+
+def _link_ext(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = EXT + ".tmp%d" % os.getpid()
+    _run(["g++", "-shared", obj, "-o", tmp, "-L" + PKG, "-l:libred.so", "-Wl,-rpath,$ORIGIN", "-L" + libs,
+          "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], "link of _red_torch")
+    os.replace(tmp, EXT)
 
 
 def build_lib(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -62,14 +96,17 @@ def build_lib(force: bool = False, verbose: bool = False, extra_flags=()) -> str
         return obj
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        ext = ex.submit(_compile_ext)
         objs = list(ex.map(compile_one, srcs))
+        ext = ext.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stdout + r.stderr))
     os.replace(tmp, LIB)
+    _link_ext(ext)
     return LIB
 
 
