@@ -197,7 +197,7 @@ __device__ __forceinline__ float exp_excess(float d)
     return expf(d) - d - 1.0f;
 }
 
-enum : int { ROW_END = 0, ROW_OUT = 1, ROW_LIVE = 2 };
+enum : int { ROW_END = 0, ROW_OUT = 1, ROW_LIVE = 2 };  // past the last row, out of the loss, in it
 
 // What a kernel knows of a row before its logits: its index, whether it takes
 // part, and the loss's inputs.
@@ -262,10 +262,11 @@ __device__ __forceinline__ RowGrad grad_of_target(const LogitRows &a, const RowS
 //   load()   the row's entry (its logits are still intact): issues loads and
 //            uses none of their values, so that a later settle() may be the
 //            first to wait for them;
-//   settle() whether the row takes part, and the load of the target's logit;
+//   settle() whether the row takes part;
+//   touch()  the load of the target's logit, its value not used either;
+//   skip()   the row's scalar results when it takes no part;
 //   grad()   the row's gradient from entry and statistics (any thread);
-//   write()  the row's scalar results (one thread), for rows out of the loss
-//            too.
+//   write()  the row's scalar results (one thread).
 
 struct LogprobArgs {
     static constexpr bool STATS = true, TEACHER = false, GRADIENT = false;
@@ -278,25 +279,23 @@ struct LogprobArgs {
         e.r = r;
         e.target = target[r];
     }
-    template <int DT>
     __device__ void settle(const LogitRows &a, RowEntry &e) const
     {
         e.state = valid_id(e.target, a.len) ? ROW_LIVE : ROW_OUT;
-        if (e.state == ROW_LIVE)
-            e.xy = load_bits<DT>(a.x, e.r * a.ld + e.target);
     }
+    template <int DT>
+    __device__ void touch(const LogitRows &a, RowEntry &e) const
+    {
+        e.xy = load_bits<DT>(a.x, e.r * a.ld + e.target);
+    }
+    __device__ void skip(int64_t r) const { logp[r] = lse[r] = 0.0f; }
     template <int DT>
     __device__ RowGrad grad(const LogitRows &, const RowEntry &, const RowStat &, float) const { return RowGrad{}; }
     template <int DT>
     __device__ void write(const LogitRows &a, const RowEntry &e, const RowStat &t) const
     {
-        float p = 0.0f, n = 0.0f;
-        if (e.state == ROW_LIVE) {
-            n = t.empty ? NEG_INF : fmaf(a.scale, t.m, t.ln);
-            p = t.empty ? NEG_INF : (Elem<DT>::widen(e.xy) - t.m) * a.scale - t.ln;
-        }
-        logp[e.r] = p;
-        lse[e.r] = n;
+        logp[e.r] = t.empty ? NEG_INF : (Elem<DT>::widen(e.xy) - t.m) * a.scale - t.ln;
+        lse[e.r] = t.empty ? NEG_INF : fmaf(a.scale, t.m, t.ln);
     }
 };
 
@@ -305,19 +304,25 @@ struct LogprobGradArgs {
     static constexpr int TOTALS = 0;
     const int64_t *target;
     const float *lse, *dlogp;
+    int64_t rows;
 
+    // From the last row to the first: the logits that the forward pass read
+    // last are the ones still in L2.
     __device__ void load(int64_t r, RowEntry &e) const
     {
+        r = rows - 1 - r;
         e.r = r;
         e.target = target[r];
         e.w = dlogp[r];
         e.f[0] = lse[r];
     }
-    template <int DT>
     __device__ void settle(const LogitRows &a, RowEntry &e) const
     {
         e.state = valid_id(e.target, a.len) && e.w != 0.0f && e.f[0] != NEG_INF ? ROW_LIVE : ROW_OUT;
     }
+    template <int DT>
+    __device__ void touch(const LogitRows &, RowEntry &) const {}
+    __device__ void skip(int64_t) const {}
     // p_j = 2^(x_j * s2 - lse * s2 / scale), the same rounding of s2 in both
     // products; what the second one rounds away goes into the factor.  Far
     // from zero: 2^((scale x_j - lse) log2 e), the difference in one rounding.
@@ -388,13 +393,16 @@ struct PolicyArgs {
         e.f[1] = ref_logp ? ref_logp[r] : 0.0f;
         e.f[2] = adv[r];
     }
-    template <int DT>
     __device__ void settle(const LogitRows &a, RowEntry &e) const
     {
         e.state = valid_id(e.target, a.len) && e.w != 0.0f ? ROW_LIVE : ROW_OUT;
-        if (e.state == ROW_LIVE)
-            e.xy = load_bits<DT>(a.x, e.r * a.ld + e.target);
     }
+    template <int DT>
+    __device__ void touch(const LogitRows &a, RowEntry &e) const
+    {
+        e.xy = load_bits<DT>(a.x, e.r * a.ld + e.target);
+    }
+    __device__ void skip(int64_t r) const { logp[r] = loss[r] = 0.0f; }
     template <int DT>
     __device__ float row_logp(const LogitRows &a, const RowEntry &e, const RowStat &t) const
     {
@@ -409,10 +417,8 @@ struct PolicyArgs {
     template <int DT>
     __device__ void write(const LogitRows &a, const RowEntry &e, const RowStat &t) const
     {
-        float p = 0.0f, v = 0.0f;
-        if (e.state == ROW_LIVE && t.empty) {
-            p = NEG_INF;
-        } else if (e.state == ROW_LIVE) {
+        float p = NEG_INF, v = 0.0f;
+        if (!t.empty) {
             p = row_logp<DT>(a, e, t);
             v = e.w * terms(p, e.f[0], e.f[1], e.f[2]).loss;
         }
@@ -490,11 +496,10 @@ struct DistillArgs {
         e.r = r;
         e.w = weight ? weight[r] : 1.0f;
     }
+    __device__ void settle(const LogitRows &, RowEntry &e) const { e.state = e.w != 0.0f ? ROW_LIVE : ROW_OUT; }
     template <int DT>
-    __device__ void settle(const LogitRows &, RowEntry &e) const
-    {
-        e.state = e.w != 0.0f ? ROW_LIVE : ROW_OUT;
-    }
+    __device__ void touch(const LogitRows &, RowEntry &) const {}
+    __device__ void skip(int64_t r) const { loss[r] = 0.0f; }
     template <int DT>
     __device__ RowGrad grad(const LogitRows &a, const RowEntry &e, const RowStat &t, float Q) const
     {
@@ -579,7 +584,7 @@ struct DistillArgs {
                 if (s.q[i] != 0.0f)
                     v += s.q[i] * (s.lq[i] - ((s.x[i] - t.m) * a.scale - t.ln));
         v = group_sum<G>(v);
-        if (gl == 0 && e.state != ROW_END)
+        if (gl == 0 && e.state == ROW_LIVE)
             loss[e.r] = on ? v * e.w : 0.0f;
     }
     // The teacher's columns of the gradient once more, after the rest of the

@@ -14,11 +14,11 @@
 // first batches after the statistics and has them fetched again for the
 // gradient (from L2: they are a few microseconds old).
 //
-// A scheduler warp takes rows and reads their scalars (target, weight, the
-// target's logit) ahead into a queue; a writer warp writes the losses, and
-// zeros over the gradient of rows out of the loss; for the distillation
-// teacher warps do that and read the rows' lists of teacher entries.  One CTA barrier per row joins the statistics and hands
-// the queue over.
+// A scheduler warp takes rows, reads their scalars (target, weight), writes
+// zeros over the gradient of rows out of the loss and hands the others on
+// through a queue; a writer warp writes the losses; for the distillation
+// teacher warps do that and read the rows' lists of teacher entries.  One CTA
+// barrier per row joins the statistics and hands the queue over.
 #pragma once
 
 #include <type_traits>
@@ -382,7 +382,6 @@ struct RowShared {
     uint64_t full[ROW_MAX_SLOTS], empty[ROW_MAX_SLOTS];
     alignas(16) unsigned char zeros[ZERO_BYTES];
     int published;  // entries written to the queue
-    int loading;    // entry the loader is at
     int failed;     // a wait ran out
 };
 
@@ -403,16 +402,15 @@ __device__ __forceinline__ void bar_sync(int id, int n)
 // vectors in shared memory.  next: the row counter and the count of finished
 // CTAs, both zero before and after.
 //
-// The queue: entry i is in slot i % ROW_Q.  Its first 3 * group + AHEAD
-// entries are fixed rows; after that the service warp takes `group` rows at a
-// time from the counter, in steps of `group` rows that each advance a chain
-// of three loads (counter, scalars, target's logit) by one link, so that no
-// step waits for more than one latency: step s, before the barrier of row s *
-// group, publishes the group that step s - 3 took.  After the barrier of row
-// i at least the entries up to i + AHEAD can be read.
+// The queue: entry i, a row of the loss, is in slot i % ROW_Q, and entries up to
+// i + 1 + ahead can be read after the barrier of row i.  The scheduler takes
+// `group` rows at a time, when they are needed and not before: a row that
+// waits in one CTA's queue at the end is one that another, idle by then, could
+// have had (with the next rows always on their way: policy 8192 x 65536 bf16
+// 300 us instead of 290).
 template <int DT, class OP, int NT, int U>
 __global__ void __launch_bounds__(NT + 32 * SERVICE_WARPS<OP>)
-row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher_k)
+row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, int teacher_k)
 {
     using T = typename Elem<DT>::T;
     constexpr int E = VEC_ELEMS<DT>, NW = NT / 32;
@@ -423,21 +421,9 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
     Shared &sh = *reinterpret_cast<Shared *>(ring + slots * U * NT);
     unsigned char *const lists = reinterpret_cast<unsigned char *>(&sh + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int AHEAD = OP::TEACHER ? TEACHERS : 2;
-    const int fixed = 3 * group + AHEAD;
     const float s2 = a.s2;
     pdl_enter();
 
-    if (warp == NW && lane < fixed) {
-        RowEntry e;
-        e.state = ROW_END;
-        const int64_t r = blockIdx.x + (int64_t)lane * gridDim.x;
-        if (r < a.rows) {
-            op.load(r, e);
-            op.template settle<DT>(a, e);
-        }
-        sh.queue[lane] = e;
-    }
     for (int i = tid; i < ZERO_BYTES / 16; i += blockDim.x)
         reinterpret_cast<uint4 *>(sh.zeros)[i] = make_uint4(0, 0, 0, 0);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -446,19 +432,19 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], NW);
         }
-        sh.published = fixed;
-        sh.loading = 0;
+        sh.published = 0;
         sh.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
     volatile int *const failed = &sh.failed;
-    volatile int *const published = &sh.published, *const loading = &sh.loading;
+    volatile int *const published = &sh.published;
 
     // The barrier of row i: consumers, scheduler, and the writer or, of the
     // teacher warps, the row's own.  (The loader runs ahead by the slots
-    // alone.)
+    // alone.)  Barrier 15: the first entries are there.
     auto row_barrier = [&](int i) { bar_sync(OP::TEACHER ? 1 + i % TEACHERS : 0, NT + 64); };
+    auto first_barrier = [&]() { bar_sync(15, NT + 32 * (SERVICE_WARPS<OP> - 1)); };
     // Batches of a row of nvec vectors, and how many of them are fetched twice.
     auto batches = [](int nvec) { return (nvec + U * NT - 1) / (U * NT); };
     auto twice = [&](int nb) { return OP::STATS && a.dx && nb > slots ? nb - slots : 0; };
@@ -473,45 +459,59 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
 
     if (warp == NW) {
         // ---- scheduler
-        unsigned taken = 0;  // link 1: the counter's value, in lane 0
-        RowEntry got, ready;  // links 2 and 3, an entry in each of the first `group` lanes
-        got.state = ready.state = ROW_END;
-        got.r = ready.r = a.rows;
-        for (int i = 0;; ++i) {
-            if (sh.queue[i % ROW_Q].state == ROW_END)
-                break;
-            if (i % group == 0) {
-                const int step = i / group;
-                if (step >= 3) {
-                    const int at = fixed + (step - 3) * group;
-                    // (the loader may be behind on a run of ignored rows)
-                    for (int n = 0; *loading + ROW_Q <= at + group && !*failed; ++n) {
-                        __nanosleep(32);
-                        if (n == WAIT_TRIES)
-                            *failed = 1;
-                    }
-                    if (lane < group)
-                        sh.queue[(at + lane) % ROW_Q] = ready;
-                    __syncwarp();
-                    __threadfence_block();
-                    if (lane == 0)
-                        *published = at + group;
-                }
-                ready = got;
-                if (ready.r < a.rows)
-                    op.template settle<DT>(a, ready);
-                got.state = ROW_END;
-                got.r = a.rows;
-                if (step >= 1) {
-                    const int64_t r = (int64_t)fixed * gridDim.x + __shfl_sync(0xffffffffu, taken, 0) + lane;
-                    if (lane < group && r < a.rows)
-                        op.load(r, got);
-                }
-                if (lane == 0)
-                    taken = atomicAdd(next, (unsigned)group);
+        int count = 0;       // entries published
+        bool ended = false;  // and the last of them is the end
+        bool first = true;   // the first rows are fixed, the rest come from the counter
+        RowEntry got;        // an entry in each of the first `group` lanes,
+        int64_t base = 0;    // rows base, base + 1, ... (as the loss counts them)
+        auto load = [&]() {
+            unsigned t = 0;
+            if (!first && lane == 0)
+                t = atomicAdd(next, (unsigned)group);
+            t = __shfl_sync(0xffffffffu, t, 0);
+            base = first ? (int64_t)blockIdx.x * group : (int64_t)gridDim.x * group + t;
+            first = false;
+            if (lane < group && base + lane < a.rows)
+                op.load(base + lane, got);
+        };
+        auto publish = [&]() {
+            const bool in = lane < group && base + lane < a.rows;
+            if (in)
+                op.settle(a, got);
+            const bool live = in && got.state == ROW_LIVE;
+            const unsigned lives = __ballot_sync(0xffffffffu, live);
+            unsigned outs = __ballot_sync(0xffffffffu, in && !live);
+            ended = base >= a.rows;
+            if (live)
+                sh.queue[(count + __popc(lives & ((1u << lane) - 1u))) % ROW_Q] = got;
+            if (ended && lane == 0)
+                sh.queue[count % ROW_Q].state = ROW_END;
+            count += __popc(lives) + ended;
+            __syncwarp();
+            __threadfence_block();
+            if (lane == 0)
+                *published = count;
+            if (in && !live)
+                op.skip(got.r);
+            for (; a.dx && outs; outs &= outs - 1) {
+                const int64_t r = __shfl_sync(0xffffffffu, got.r, __ffs(outs) - 1);
+                zero_row_bulk<DT>(static_cast<T *>(a.dx) + r * a.ldd, a.len, sh.zeros);
             }
+        };
+        auto want = [&](int upto) {
+            while (!ended && count < upto) {
+                load();
+                publish();
+            }
+        };
+        want(1 + ahead);
+        first_barrier();
+        for (int i = 0; sh.queue[i % ROW_Q].state != ROW_END; ++i) {
+            want(i + 2 + ahead);
             row_barrier(i);
         }
+        if (lane == 0)
+            bulk_stores_done();
         // the last to finish leaves the counters as they were
         if (lane == 0) {
             __threadfence();
@@ -534,12 +534,8 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
                 break;
             __threadfence_block();
             const int64_t r = sh.queue[i % ROW_Q].r;
-            const int state = sh.queue[i % ROW_Q].state;
-            *loading = i;
-            if (state == ROW_END)
+            if (sh.queue[i % ROW_Q].state == ROW_END)
                 break;
-            if (state == ROW_OUT)
-                continue;
             const T *row = static_cast<const T *>(a.x) + r * a.ld;
             const int h = head_elems<DT>(row, a.len), nvec = (a.len - h) / E;
             const int nb = batches(nvec), total = nb + twice(nb);
@@ -558,55 +554,47 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
         }
     } else if (!OP::TEACHER && warp == NW + 2) {
         // ---- writer
+        first_barrier();
         for (int i = 0;; ++i) {
-            const RowEntry e = sh.queue[i % ROW_Q];
+            RowEntry e = sh.queue[i % ROW_Q];
             if (e.state == ROW_END)
                 break;
+            if (lane == 0)
+                op.template touch<DT>(a, e);
             row_barrier(i);
             RowStat t{};
-            if (OP::STATS && e.state == ROW_LIVE)
+            if (OP::STATS)
                 t = row_stat(a, stat_of(i));
             if (lane == 0)
                 op.template write<DT>(a, e, t);
-            if (a.dx && e.state == ROW_OUT)
-                zero_row_bulk<DT>(static_cast<T *>(a.dx) + e.r * a.ldd, a.len, sh.zeros);
         }
-        if (lane == 0)
-            bulk_stores_done();
     } else if (OP::TEACHER && warp > NW + 1) {
         if constexpr (OP::TEACHER) {
             // ---- teacher warp w: rows w, w + TEACHERS, ...
             const int w = warp - NW - 2;
             TeacherRow list(lists + (size_t)w * 16 * teacher_k, teacher_k);
+            first_barrier();
             for (int i = 0;; ++i) {
-                // entries are visible a few rows ahead; walk to this warp's next
+                // entries are there a few rows ahead; walk to this warp's next
                 const RowEntry e = sh.queue[i % ROW_Q];
                 if (e.state == ROW_END)
                     break;
                 if (i % TEACHERS != w)
                     continue;
-                if (e.state == ROW_LIVE) {
-                    op.template prepare<DT, 32>(a, e.r, true, list);
-                    if (lane == 0)
-                        sh.mass[w] = list.mass;
-                }
+                op.template prepare<DT, 32>(a, e.r, true, list);
+                if (lane == 0)
+                    sh.mass[w] = list.mass;
                 row_barrier(i);
-                RowStat t{};
-                if (e.state == ROW_LIVE)
-                    t = row_stat(a, stat_of(i));
+                const RowStat t = row_stat(a, stat_of(i));
                 op.template finish<32>(a, e, t, list);
-                if (a.dx && e.state == ROW_LIVE) {
+                if (a.dx) {
                     const RowGrad g = op.template grad<DT>(a, e, t, list.mass);
                     bar_sync(1 + TEACHERS + w, NT + 32);
                     if (!g.zero)
                         op.template patch<DT, 32>(a, e, g, list, 0, a.len);
-                } else if (a.dx) {
-                    zero_row_bulk<DT>(static_cast<T *>(a.dx) + e.r * a.ldd, a.len, sh.zeros);
                 }
                 __syncwarp();
             }
-            if (lane == 0)
-                bulk_stores_done();
         }
     } else if (warp < NW) {
         // ---- consumers
@@ -627,14 +615,12 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int teacher
                 mbar_arrive(&sh.empty[slot]);
         };
 
+        first_barrier();
         for (int i = 0;; ++i) {
-            const RowEntry e = sh.queue[i % ROW_Q];
+            RowEntry e = sh.queue[i % ROW_Q];
             if (e.state == ROW_END)
                 break;
-            if (e.state == ROW_OUT) {
-                row_barrier(i);
-                continue;
-            }
+            op.template touch<DT>(a, e);
             const T *const row = x + e.r * a.ld;
             const int h = head_elems<DT>(row, a.len);
             const int nvec = (a.len - h) / E, nb = batches(nvec), n1 = twice(nb);
@@ -850,7 +836,9 @@ __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(Log
         n.state = ROW_END;
         if (r < a.rows) {
             op.load(r, n);
-            op.template settle<DT>(a, n);
+            op.settle(a, n);
+            if (n.state == ROW_LIVE)
+                op.template touch<DT>(a, n);
         }
     };
     fetch((int64_t)blockIdx.x * ROWS + group);
@@ -859,7 +847,7 @@ __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(Log
         const int64_t r = r0 + (group & (32 / G - 1));
         const RowEntry e = n;
         const bool live = e.state == ROW_LIVE;
-        const T *const row = x + r * a.ld;
+        const T *const row = x + e.r * a.ld;
         const int h = head_elems<DT>(row, a.len), nvec = (a.len - h) / E;
         uint4 v[NV];
         // the row's ragged ends, fewer than E elements each
@@ -882,7 +870,7 @@ __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(Log
         }
         fetch(r + step);
         if constexpr (OP::TEACHER)
-            op.template prepare<DT, G>(a, r, live, list);
+            op.template prepare<DT, G>(a, e.r, live, list);
 
         RowStat t{};
         if constexpr (OP::STATS) {
@@ -919,11 +907,13 @@ __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(Log
         }
         if constexpr (OP::TEACHER)
             op.template finish<G>(a, e, t, list);
-        else if (gl == 0 && e.state != ROW_END)
+        else if (gl == 0 && live)
             op.template write<DT>(a, e, t);
+        if (gl == 0 && e.state == ROW_OUT)
+            op.skip(e.r);
         if (!dx)
             continue;
-        T *const grow = dx + r * a.ldd;
+        T *const grow = dx + e.r * a.ldd;
         RowGrad g = op.template grad<DT>(a, e, t, list.mass);
         g.zero = g.zero || !live;
         const bool aligned = ((uintptr_t)(grow + h) & 15u) == 0;
@@ -980,13 +970,13 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
     TeacherRow list(smem, teacher_k);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cs = cluster_size(), rank = cluster_rank();
-    const int64_t r = blockIdx.x / cs;
     const float s2 = a.s2;
     cluster_arrive();
     pdl_enter();
 
     RowEntry e;
-    op.load(r, e);
+    op.load(blockIdx.x / cs, e);
+    const int64_t r = e.r;
     const T *const row = static_cast<const T *>(a.x) + r * a.ld;
     T *const grow = static_cast<T *>(a.dx) + r * a.ldd;
     const int h = head_elems<DT>(row, a.len), all = (a.len - h) / E;
@@ -1006,7 +996,9 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
     float xe = 0.0f;
     if (edge >= 0)
         xe = load_elem<DT>(row, edge);
-    op.template settle<DT>(a, e);
+    op.settle(a, e);
+    if (e.state == ROW_LIVE)
+        op.template touch<DT>(a, e);
 
     RowStat t{};
     if (e.state == ROW_LIVE) {
@@ -1049,7 +1041,10 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
             t = row_stat(a, w);
         }
     }
-    if (rank == 0) {
+    if (rank == 0 && e.state == ROW_OUT) {
+        if (tid == 0)
+            op.skip(r);
+    } else if (rank == 0) {
         if constexpr (OP::TEACHER) {
             if (warp == 0)
                 op.template finish<32>(a, e, t, list);
@@ -1164,11 +1159,13 @@ int launch_row_kernel(const LogitRows &a, const OP &op, int per_sm, int teacher_
     }
     const int64_t cap = (int64_t)di.sms * per_sm;
     const unsigned grid = (unsigned)(a.rows < cap ? a.rows : cap);
-    // Rows taken at a time: one where a CTA gets few rows (the last row taken
-    // is what CTAs wait for at the end), more where rows are many.
-    const int group = a.rows >= 32 * cap ? 4 : (a.rows >= 16 * cap ? 2 : 1);
+    // Rows taken at a time: one, except short ones, which the counter's latency
+    // would hold up where many are out of the loss (policy 20000 x 8192 bf16, 40%
+    // of them: 91 us with two, 96 with one; 8192 x 65536: 283 and 278).
+    const int group = a.len * (int64_t)sizeof(typename Elem<DT>::T) <= 24576 ? 2 : 1;
+    const int ahead = OP::TEACHER ? TEACHERS : 0;
     const cudaError_t e = launch_pdl_smem(kernel, grid, NT + SERVICE, smem, 1, s, a, op, ws.tick, slots,
-                                          group, teacher_k);
+                                          group, ahead, teacher_k);
     count_launches(1);
     return cuda_fail(e != cudaSuccess ? e : cudaGetLastError(), "row kernel launch");
 }
@@ -1268,24 +1265,35 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
     // Threads, vectors per thread and batch, and CTAs per SM, by row bytes.  A
     // CTA is busy with one row at a time, so short rows need several CTAs to
     // cover each other's barriers, and long ones a ring that holds a row and
-    // the start of the next.  us, policy loss and gradient unless said:
-    //                          512x4,1   256x4,2   256x4,3   128x4,4   128x4,6
-    //   8192 x 65536 bf16          328       326       366       376       404
-    //   4096 x 131072 bf16         358       434       460       478       491
-    //   1000 x 32001 f32            52        58        60        61        64
-    //   4096 x 16384 f32           106        99       105       109       114
-    //   8192 x 16384 bf16          170       109       107       100       107
-    //   16384 x 8192 bf16          262       139       133       110       106
-    //   logprob 4096 x 50257 f16    65        56        54        56        56
-    // (A loss with a gradient keeps its mapping when the gradient is not asked
-    // for: the mapping sets the order of the sums.)
-    if constexpr (!OP::GRADIENT)
-        return launch_row_kernel<DT, OP, 256, 4>(a, op, 3, teacher_k, s, di);
-    if (bytes > 98304)
-        return launch_row_kernel<DT, OP, 512, 4>(a, op, 1, teacher_k, s, di);
-    if (bytes > 49152)
-        return launch_row_kernel<DT, OP, 256, 4>(a, op, 2, teacher_k, s, di);
-    return launch_row_kernel<DT, OP, 128, 4>(a, op, bytes > 24576 ? 4 : 6, teacher_k, s, di);
+    // the start of the next.  us, policy loss and gradient:
+    //                          512x4,1   256x4,2   256x4,3   128x8,4   128x4,4   128x4,6
+    //   8192 x 65536 bf16          289       309       343       357       359       370
+    //   4096 x 60000 bf16          171       166       188         -       200         -
+    //   4096 x 30000 bf16          112        92        84         -        90         -
+    //   8192 x 16384 bf16          139       105        92        87        88        94
+    //   16384 x 8192 bf16          235       136       116        94       101       101
+    //   20000 x 6000 bf16            -         -         -       131       120       118
+    // (the first line with two rows taken at a time; 279 with one).  Without a
+    // gradient a row need not stay: logprob 4096 x 50257 f16 59, 54, 49, 48, 51,
+    // 53; 16384 x 8192 bf16 113, 60, 51, 43, 47, 48; 32768 x 4100 bf16 -, -,
+    // 103, 86, 76, 78.  Without statistics nothing does: logprob_grad 3001 x
+    // 32001 bf16 59, 55, 56, 57, 57, 55; 32768 x 4100 bf16 250, 133, 104, 92,
+    // 86, 87.  (A loss with a gradient keeps its mapping when the gradient is
+    // not asked for: the mapping sets the order of the sums.)
+    if constexpr (!OP::GRADIENT) {
+        return bytes > 16384 ? launch_row_kernel<DT, OP, 128, 8>(a, op, 4, teacher_k, s, di)
+                             : launch_row_kernel<DT, OP, 128, 4>(a, op, 4, teacher_k, s, di);
+    } else if constexpr (!OP::STATS) {
+        return bytes > 24576 ? launch_row_kernel<DT, OP, 256, 4>(a, op, 2, teacher_k, s, di)
+                             : launch_row_kernel<DT, OP, 128, 4>(a, op, 4, teacher_k, s, di);
+    } else {
+        if (bytes > 122880)
+            return launch_row_kernel<DT, OP, 512, 4>(a, op, 1, teacher_k, s, di);
+        if (bytes > 40960)
+            return launch_row_kernel<DT, OP, 256, 4>(a, op, bytes > 65536 ? 2 : 3, teacher_k, s, di);
+        return bytes > 12288 ? launch_row_kernel<DT, OP, 128, 8>(a, op, 4, teacher_k, s, di)
+                             : launch_row_kernel<DT, OP, 128, 4>(a, op, 6, teacher_k, s, di);
+    }
 }
 
 template <class OP>

@@ -174,7 +174,7 @@ int launch_preference(int dtype, const LogitRows &a, const PreferenceArgs &p, cu
     }
     if (st != RED_OK || !a.dx || a.rows == 0)
         return st;
-    return launch_logprob_grad(dtype, a, LogprobGradArgs{p.target, p.lse, p.dlogp}, s);
+    return launch_logprob_grad(dtype, a, LogprobGradArgs{p.target, p.lse, p.dlogp, a.rows}, s);
 }
 
 }  // namespace red
