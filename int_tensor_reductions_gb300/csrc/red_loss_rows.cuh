@@ -735,23 +735,23 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
 
 // ------------------------------------------------------------------ totals
 
-// The CTA's N sums, rounded to out[0, N).
+// The CTA's N sums by way of s[N * NT / 32], rounded to out[0, N).
 template <int N, int NT>
-__device__ void cta_totals(Sum (&v)[N], float *out)
+__device__ void cta_totals(Sum (&v)[N], Sum *s, float *out)
 {
-    __shared__ Sum s[N][NT / 32];
+    constexpr int NW = NT / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         v[i].join_warp();
         if (lane == 0)
-            s[i][warp] = v[i];
+            s[i * NW + warp] = v[i];
     }
     __syncthreads();
     if (threadIdx.x < N) {
         Sum t;
-        for (int w = 0; w < NT / 32; ++w)
-            t.add(s[threadIdx.x][w]);
+        for (int w = 0; w < NW; ++w)
+            t.add(s[threadIdx.x * NW + w]);
         out[threadIdx.x] = t.value();
     }
 }
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(TOTAL_NT) total_kernel(int64_t rows, int len, 
     for (int64_t r = (int64_t)blockIdx.x * TOTAL_NT + tid; r < rows; r += (int64_t)gridDim.x * TOTAL_NT)
         op.total(r, len, v);
     if (gridDim.x == 1) {
-        cta_totals<N, TOTAL_NT>(v, op.stats);
+        cta_totals<N, TOTAL_NT>(v, s[0], op.stats);
         return;
     }
 #pragma unroll
@@ -802,7 +802,8 @@ __global__ void __launch_bounds__(TOTAL_NT) total_kernel(int64_t rows, int len, 
         if (tid < gridDim.x)
             v[i] = part[(int64_t)tid * N + i];
     }
-    cta_totals<N, TOTAL_NT>(v, op.stats);
+    __syncthreads();  // (s is free again)
+    cta_totals<N, TOTAL_NT>(v, s[0], op.stats);
     if (tid == 0)
         *tick = 0;
 }
@@ -1087,7 +1088,8 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
         Sum v2[OP::TOTALS];
         for (int64_t k = tid; k < a.rows; k += FEW_NT)
             op.total(k, a.len, v2);
-        cta_totals<OP::TOTALS, FEW_NT>(v2, op.stats);
+        __shared__ Sum s_sum[OP::TOTALS * FEW_NW];
+        cta_totals<OP::TOTALS, FEW_NT>(v2, s_sum, op.stats);
         if (tid == 0)
             *tick = 0;
     }

@@ -2,36 +2,22 @@
 // row kernels of the log-probabilities and of their gradient around one
 // kernel that reduces the packed tokens to sequences and pairs.
 //
-// One CTA per pair sums the log-probabilities of its two sequences (in two
-// floats and a fixed order: a sequence of thousands of tokens adds values of a
-// few nats, and the loss depends on the difference of two such sums), forms
-// u = beta * (gain of the chosen - gain of the rejected) - margin, the loss
-// of u and its derivative, and writes each token's share of it.  The CTA that
-// finishes last folds the totals over pairs.
+// One CTA per pair sums the log-probabilities of its two sequences, half of
+// the threads each (in two floats and a fixed order: a sequence of thousands
+// of tokens adds values of a few nats, and the loss depends on the difference
+// of two such sums), forms u = beta * (gain of the chosen - gain of the
+// rejected) - margin, the loss of u and its derivative, and writes each
+// token's share of it.  The CTA that finishes last folds the totals over
+// pairs.  It is bound by latency: three loads that wait for one another and
+// two barriers, 4 us.
 #include "red_internal.h"
-#include "red_loss.cuh"
-#include "red_prims.cuh"
+#include "red_loss_rows.cuh"
 
 namespace red {
 namespace {
 
-constexpr int NT = 256;
-constexpr int NW = NT / 32;
-
-// Sum over the CTA, in every thread.
-__device__ Sum cta_sum(Sum v, Sum *s)
-{
-    v.join_warp();
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = Sum{};
-#pragma unroll
-    for (int w = 0; w < NW; ++w)
-        v.add(s[w]);
-    return v;
-}
+constexpr int NT = 512;
+constexpr int NW = NT / 32, HALF = NT / 2;
 
 struct PairTerms {
     float loss, du;
@@ -62,62 +48,73 @@ __device__ PairTerms pair_terms(const PreferenceArgs &p, float u)
 __global__ void __launch_bounds__(NT) pair_kernel(int64_t rows, int len, PreferenceArgs p, unsigned *tick)
 {
     pdl_enter();
-    __shared__ Sum s[NW];
+    __shared__ Sum s[4 * NW];
+    __shared__ int s_n[NW];
     __shared__ bool s_last;
+    const int tid = threadIdx.x, side = tid / HALF;
     const int64_t pair = blockIdx.x;
     int64_t lo[2], hi[2];
-    Sum sum[2];
-    float count[2];
-    for (int side = 0; side < 2; ++side) {
-        const int64_t q = pair + side * p.pairs;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t q = pair + i * p.pairs;
         // offsets outside [0, rows] are clamped, so no row outside is touched
-        lo[side] = min(max(p.offsets[q], (int64_t)0), rows);
-        hi[side] = min(max(p.offsets[q + 1], lo[side]), rows);
+        lo[i] = min(max(p.offsets[q], (int64_t)0), rows);
+        hi[i] = min(max(p.offsets[q + 1], lo[i]), rows);
     }
-    for (int side = 0; side < 2; ++side) {
-        Sum v;
-        int n = 0;
-        for (int64_t t = lo[side] + threadIdx.x; t < hi[side]; t += NT) {
-            if (valid_id(p.target[t], len) && p.lse[t] != NEG_INF) {
-                v.add(p.logp[t]);
-                ++n;
-            }
+    const float w = p.weight ? p.weight[pair] : 1.0f;
+    const float ref0 = p.ref_logp ? p.ref_logp[pair] : 0.0f, ref1 = p.ref_logp ? p.ref_logp[pair + p.pairs] : 0.0f;
+    Sum v;
+    int n = 0;
+    for (int64_t t = (side ? lo[1] : lo[0]) + tid % HALF; t < (side ? hi[1] : hi[0]); t += HALF) {
+        const int64_t y = p.target[t];
+        const float logp = p.logp[t], lse = p.lse[t];
+        if (valid_id(y, len) && lse != NEG_INF) {
+            v.add(logp);
+            ++n;
         }
-        sum[side] = cta_sum(v, s);
-        count[side] = 1.0f;
+    }
+    v.join_warp();
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (tid % 32 == 0) {
+        s[tid / 32] = v;
+        s_n[tid / 32] = n;
+    }
+    __syncthreads();
+    Sum sum[2];
+    float count[2] = {1.0f, 1.0f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int total = 0;
+#pragma unroll
+        for (int k = 0; k < NW / 2; ++k) {
+            sum[i].add(s[i * NW / 2 + k]);
+            total += s_n[i * NW / 2 + k];
+        }
         if (p.average) {
-            // (exact up to 2^24 tokens of one sequence)
-            Sum m;
-            m.add((float)n);
-            count[side] = fmaxf(cta_sum(m, s).value(), 1.0f);
-            const float mean = sum[side].s / count[side];
-            sum[side] = Sum{mean, (fmaf(-mean, count[side], sum[side].s) + sum[side].c) / count[side]};
+            count[i] = fmaxf((float)total, 1.0f);
+            const float mean = sum[i].s / count[i];
+            sum[i] = Sum{mean, (fmaf(-mean, count[i], sum[i].s) + sum[i].c) / count[i]};
         }
     }
     Sum gain = sum[0];
     gain.add(Sum{-sum[1].s, -sum[1].c});
-    if (p.ref_logp) {
-        gain.add(-p.ref_logp[pair]);
-        gain.add(p.ref_logp[pair + p.pairs]);
-    }
+    gain.add(-ref0);
+    gain.add(ref1);
     const float u = fmaf(p.beta, gain.value(), -p.margin);
-    const float w = p.weight ? p.weight[pair] : 1.0f;
     PairTerms t{0.0f, 0.0f};
     if (w != 0.0f)
         t = pair_terms(p, u);
     // rows before the first sequence and after the last belong to no loss
     if (pair == 0)
-        for (int64_t r = threadIdx.x; r < lo[0]; r += NT)
+        for (int64_t r = tid; r < lo[0]; r += NT)
             p.dlogp[r] = 0.0f;
     if (pair == p.pairs - 1)
-        for (int64_t r = hi[1] + threadIdx.x; r < rows; r += NT)
+        for (int64_t r = hi[1] + tid; r < rows; r += NT)
             p.dlogp[r] = 0.0f;
-    for (int side = 0; side < 2; ++side) {
-        const float c = w == 0.0f ? 0.0f : (side ? -w : w) * t.du * p.beta * p.gscale / count[side];
-        for (int64_t r = lo[side] + threadIdx.x; r < hi[side]; r += NT)
-            p.dlogp[r] = c;
-    }
-    if (threadIdx.x == 0) {
+    const float c = w == 0.0f ? 0.0f : (side ? -w : w) * t.du * p.beta * p.gscale / (side ? count[1] : count[0]);
+    for (int64_t r = (side ? lo[1] : lo[0]) + tid % HALF; r < (side ? hi[1] : hi[0]); r += HALF)
+        p.dlogp[r] = c;
+    if (tid == 0) {
         p.loss[pair] = w == 0.0f ? 0.0f : w * t.loss;
         p.seq_logp[pair] = sum[0].value();
         p.seq_logp[pair + p.pairs] = sum[1].value();
@@ -129,23 +126,19 @@ __global__ void __launch_bounds__(NT) pair_kernel(int64_t rows, int len, Prefere
     if (!s_last)
         return;
     __threadfence();
-    Sum v[4];
-    for (int64_t q = threadIdx.x; q < p.pairs; q += NT) {
+    Sum all[4];
+    for (int64_t q = tid; q < p.pairs; q += NT) {
         const float wq = p.weight ? p.weight[q] : 1.0f;
         if (wq == 0.0f)
             continue;
         const float uq = __ldcg(p.u + q);
-        v[0].add(__ldcg(p.loss + q));
-        v[1].add(wq * uq);
-        v[2].add(uq > 0.0f ? wq : 0.0f);
-        v[3].add(wq);
+        all[0].add(__ldcg(p.loss + q));
+        all[1].add(wq * uq);
+        all[2].add(uq > 0.0f ? wq : 0.0f);
+        all[3].add(wq);
     }
-    for (int i = 0; i < 4; ++i) {
-        const float total = cta_sum(v[i], s).value();
-        if (threadIdx.x == 0)
-            p.stats[i] = total;
-    }
-    if (threadIdx.x == 0)
+    cta_totals<4, NT>(all, s, p.stats);
+    if (tid == 0)
         *tick = 0;
 }
 
