@@ -16,9 +16,10 @@
 //
 // A scheduler warp takes rows, reads their scalars (target, weight), writes
 // zeros over the gradient of rows out of the loss and hands the others on
-// through a queue; a writer warp writes the losses; for the distillation
-// teacher warps do that and read the rows' lists of teacher entries.  One CTA
-// barrier per row joins the statistics and hands the queue over.
+// through a queue; a writer warp joins a row's statistics, gives the other
+// warps the coefficients of its gradient and writes its loss; for the
+// distillation teacher warps do that, and read the rows' lists of teacher
+// entries.
 #pragma once
 
 #include <type_traits>
@@ -374,28 +375,28 @@ constexpr int ROW_MAX_SLOTS = 32;
 constexpr int TEACHERS = 4;    // teacher warps: each has the time of this many rows for one list
 
 // Shared memory of the row kernel behind the slots.
-template <int NW, int PARTS>
+template <int NW>
 struct RowShared {
     RowEntry queue[ROW_Q];
-    SoftStat part[PARTS][NW];  // statistics of row i's warps in part[i % PARTS]
-    float mass[TEACHERS];  // sum of a row's teacher probabilities
+    SoftStat part[2][NW];  // statistics of row i's warps in part[i % 2]
+    RowGrad grad;          // of the row at hand
     uint64_t full[ROW_MAX_SLOTS], empty[ROW_MAX_SLOTS];
     alignas(16) unsigned char zeros[ZERO_BYTES];
     int published;  // entries written to the queue
     int failed;     // a wait ran out
 };
 
-// A buffer of statistics is written again PARTS rows later: after the next
-// barrier of its readers, which for a teacher warp is TEACHERS rows later.
 template <class OP>
-constexpr int PARTS = OP::TEACHER ? 2 * TEACHERS : 2;
-
-template <class OP>
-constexpr int SERVICE_WARPS = OP::TEACHER ? 2 + TEACHERS : 3;  // scheduler, loader, teachers or writer
+constexpr int SERVICE_WARPS = 2 + (OP::TEACHER ? TEACHERS : OP::STATS);  // scheduler, loader, teachers or writer
 
 __device__ __forceinline__ void bar_sync(int id, int n)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int n)
+{
+    __threadfence_block();
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
 // NT consumer threads and the service warps; `slots` batches of U * NT
@@ -403,7 +404,7 @@ __device__ __forceinline__ void bar_sync(int id, int n)
 // CTAs, both zero before and after.
 //
 // The queue: entry i, a row of the loss, is in slot i % ROW_Q, and entries up to
-// i + 1 + ahead can be read after the barrier of row i.  The scheduler takes
+// i + 1 + ahead can be read after row i is `given`.  The scheduler takes
 // `group` rows at a time, when they are needed and not before: a row that
 // waits in one CTA's queue at the end is one that another, idle by then, could
 // have had (with the next rows always on their way: policy 8192 x 65536 bf16
@@ -417,7 +418,7 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
     static_assert((NW & (NW - 1)) == 0 && NW <= 32, "the join of the warps' statistics");
     extern __shared__ __align__(16) unsigned char smem[];
     uint4 *const ring = reinterpret_cast<uint4 *>(smem);
-    using Shared = RowShared<NW, PARTS<OP>>;
+    using Shared = RowShared<NW>;
     Shared &sh = *reinterpret_cast<Shared *>(ring + slots * U * NT);
     unsigned char *const lists = reinterpret_cast<unsigned char *>(&sh + 1);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -440,20 +441,39 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
     volatile int *const failed = &sh.failed;
     volatile int *const published = &sh.published;
 
-    // The barrier of row i: consumers, scheduler, and the writer or, of the
-    // teacher warps, the row's own.  (The loader runs ahead by the slots
-    // alone.)  Barrier 15: the first entries are there.
-    auto row_barrier = [&](int i) { bar_sync(OP::TEACHER ? 1 + i % TEACHERS : 0, NT + 64); };
+    // Named barriers.  Per row i, and for the distillation per teacher warp w =
+    // i % TEACHERS: `summed`, the consumers' statistics are there (the writer, or
+    // the teacher, waits); `given`, the gradient's coefficients and the next
+    // entries are there (all wait, so that none reads an entry too early);
+    // `done`, the row's gradient is written (its teacher waits).
+    // The loader runs ahead by the slots alone.
+    auto summed = [](int i) { return OP::TEACHER ? 1 + i % TEACHERS : 1; };
+    auto given = [](int i) { return OP::TEACHER ? 1 + TEACHERS + i % TEACHERS : 2; };
+    auto done = [](int i) { return 1 + 2 * TEACHERS + i % TEACHERS; };
+    constexpr int GIVEN = NT + 32 + 32 * OP::STATS;  // threads of `given`
+    // The first entries are there.
     auto first_barrier = [&]() { bar_sync(15, NT + 32 * (SERVICE_WARPS<OP> - 1)); };
     // Batches of a row of nvec vectors, and how many of them are fetched twice.
     auto batches = [](int nvec) { return (nvec + U * NT - 1) / (U * NT); };
     auto twice = [&](int nb) { return OP::STATS && a.dx && nb > slots ? nb - slots : 0; };
-    // Statistics of row i, after its barrier: copies of the NW parts throughout
-    // the warp, joined in log2(NW) levels.
-    auto stat_of = [&](int i) {
-        SoftStat t = soft_warp<NW>(sh.part[i % PARTS<OP>][lane % NW], s2);
+    // By the writer, or row i's teacher, between the consumers' statistics and
+    // their gradient pass; the statistics.
+    auto give_row = [&](int i, const RowEntry &e, float mass) {
+        bar_sync(summed(i), NT + 32);
+        if (!a.dx)  // (the statistics of the next row go to the other buffer)
+            bar_sync(given(i), GIVEN);
+        // copies of the NW parts throughout the warp, joined in log2(NW) levels
+        SoftStat w = soft_warp<NW>(sh.part[i % 2][lane % NW], s2);
         if (*failed)
-            t.l = __int_as_float(0x7fc00000);
+            w.l = __int_as_float(0x7fc00000);
+        const RowStat t = row_stat(a, w);
+        if (a.dx) {
+            const RowGrad g = op.template grad<DT>(a, e, t, mass);
+            if (lane == 0)
+                sh.grad = g;
+            __syncwarp();
+            bar_sync(given(i), GIVEN);
+        }
         return t;
     };
 
@@ -508,7 +528,7 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
         first_barrier();
         for (int i = 0; sh.queue[i % ROW_Q].state != ROW_END; ++i) {
             want(i + 2 + ahead);
-            row_barrier(i);
+            bar_sync(given(i), GIVEN);
         }
         if (lane == 0)
             bulk_stores_done();
@@ -552,19 +572,15 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
                 }
             }
         }
-    } else if (!OP::TEACHER && warp == NW + 2) {
+    } else if (OP::STATS && !OP::TEACHER && warp == NW + 2) {
         // ---- writer
         first_barrier();
         for (int i = 0;; ++i) {
             RowEntry e = sh.queue[i % ROW_Q];
             if (e.state == ROW_END)
                 break;
-            if (lane == 0)
-                op.template touch<DT>(a, e);
-            row_barrier(i);
-            RowStat t{};
-            if (OP::STATS)
-                t = row_stat(a, stat_of(i));
+            op.template touch<DT>(a, e);
+            const RowStat t = give_row(i, e, 0.0f);
             if (lane == 0)
                 op.template write<DT>(a, e, t);
         }
@@ -582,14 +598,11 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
                 if (i % TEACHERS != w)
                     continue;
                 op.template prepare<DT, 32>(a, e.r, true, list);
-                if (lane == 0)
-                    sh.mass[w] = list.mass;
-                row_barrier(i);
-                const RowStat t = row_stat(a, stat_of(i));
+                const RowStat t = give_row(i, e, list.mass);
                 op.template finish<32>(a, e, t, list);
                 if (a.dx) {
                     const RowGrad g = op.template grad<DT>(a, e, t, list.mass);
-                    bar_sync(1 + TEACHERS + w, NT + 32);
+                    bar_sync(done(i), NT + 32);
                     if (!g.zero)
                         op.template patch<DT, 32>(a, e, g, list, 0, a.len);
                 }
@@ -617,11 +630,10 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
 
         first_barrier();
         for (int i = 0;; ++i) {
-            RowEntry e = sh.queue[i % ROW_Q];
-            if (e.state == ROW_END)
+            if (sh.queue[i % ROW_Q].state == ROW_END)
                 break;
-            op.template touch<DT>(a, e);
-            const T *const row = x + e.r * a.ld;
+            const int64_t r = sh.queue[i % ROW_Q].r;
+            const T *const row = x + r * a.ld;
             const int h = head_elems<DT>(row, a.len);
             const int nvec = (a.len - h) / E, nb = batches(nvec), n1 = twice(nb);
             // the row's ragged ends: threads 0..7 the head, 8..15 the tail
@@ -637,7 +649,6 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
             // whether all of the warp's vectors of batch b are within the row
             auto whole = [&](int b) { return nvec - b * U * NT - (tid | 31) > (U - 1) * NT; };
 
-            RowStat t{};
             const int first = cslot;
             if constexpr (OP::STATS) {
                 SoftRun run;
@@ -674,15 +685,19 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
                 }
                 const SoftStat w = soft_warp(run.stat(), s2);
                 if (lane == 0)
-                    sh.part[i % PARTS<OP>][warp] = w;
+                    sh.part[i % 2][warp] = w;
             }
-            row_barrier(i);
+            RowGrad g;
+            if constexpr (OP::STATS)
+                bar_arrive(summed(i), NT + 32);
+            else
+                g = op.template grad<DT>(a, sh.queue[i % ROW_Q], RowStat{}, 0.0f);
+            bar_sync(given(i), GIVEN);
             if (!dx)
                 continue;
             if constexpr (OP::STATS)
-                t = row_stat(a, stat_of(i));
-            const RowGrad g = op.template grad<DT>(a, e, t, OP::TEACHER ? sh.mass[i % TEACHERS] : 0.0f);
-            T *const grow = dx + e.r * a.ldd;
+                g = sh.grad;
+            T *const grow = dx + r * a.ldd;
             const bool aligned = ((uintptr_t)(grow + h) & 15u) == 0;
             auto emit = [&](int b, int slot) {
                 const uint4 *src = ring + slot * U * NT + tid;
@@ -726,8 +741,7 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
             if (edge >= 0)
                 store_elem<DT>(grow, edge, g.zero ? 0.0f : elem_grad<DT>(xe, g, edge));
             if constexpr (OP::TEACHER) {
-                __threadfence_block();
-                asm volatile("bar.arrive %0, %1;" ::"r"(1 + TEACHERS + i % TEACHERS), "n"(NT + 32) : "memory");
+                bar_arrive(done(i), NT + 32);
             }
         }
     }
@@ -1042,15 +1056,18 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
             t = row_stat(a, w);
         }
     }
-    if (rank == 0 && e.state == ROW_OUT) {
-        if (tid == 0)
-            op.skip(r);
-    } else if (rank == 0) {
-        if constexpr (OP::TEACHER) {
-            if (warp == 0)
-                op.template finish<32>(a, e, t, list);
+    if (rank == 0 && warp == 0) {
+        if (e.state == ROW_OUT) {
+            if (tid == 0)
+                op.skip(r);
+        } else if constexpr (OP::TEACHER) {
+            op.template finish<32>(a, e, t, list);
         } else if (tid == 0) {
             op.template write<DT>(a, e, t);
+        }
+        if (OP::TOTALS > 0 && tid == 0) {
+            __threadfence();
+            s_last = atomicAdd(tick, 1u) == (unsigned)a.rows - 1;
         }
     }
     if (a.dx && e.state == ROW_LIVE) {
@@ -1077,10 +1094,6 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
     if constexpr (OP::TOTALS > 0) {
         if (rank != 0)
             return;
-        if (tid == 0) {
-            __threadfence();
-            s_last = atomicAdd(tick, 1u) == (unsigned)a.rows - 1;
-        }
         __syncthreads();
         if (!s_last)
             return;
@@ -1142,7 +1155,7 @@ int launch_row_kernel(const LogitRows &a, const OP &op, int per_sm, int teacher_
         return st;
     constexpr int SERVICE = 32 * SERVICE_WARPS<OP>;
     constexpr size_t batch = (size_t)U * NT * 16;
-    const size_t fixed = sizeof(RowShared<NT / 32, PARTS<OP>>) + (size_t)TEACHERS * 4 * 4 * teacher_k;
+    const size_t fixed = sizeof(RowShared<NT / 32>) + (size_t)TEACHERS * 4 * 4 * teacher_k;
     size_t most = SM_SMEM / per_sm - CTA_RESERVED;
     most = most < CTA_SMEM ? most : CTA_SMEM;
     int slots = most > fixed ? (int)((most - fixed) / batch) : 0;
@@ -1269,19 +1282,20 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
     // cover each other's barriers, and long ones a ring that holds a row and
     // the start of the next.  us, policy loss and gradient:
     //                          512x4,1   256x4,2   256x4,3   128x8,4   128x4,4   128x4,6
-    //   8192 x 65536 bf16          289       309       343       357       359       370
-    //   4096 x 60000 bf16          171       166       188         -       200         -
-    //   4096 x 30000 bf16          112        92        84         -        90         -
-    //   8192 x 16384 bf16          139       105        92        87        88        94
-    //   16384 x 8192 bf16          235       136       116        94       101       101
-    //   20000 x 6000 bf16            -         -         -       131       120       118
-    // (the first line with two rows taken at a time; 279 with one).  Without a
-    // gradient a row need not stay: logprob 4096 x 50257 f16 59, 54, 49, 48, 51,
-    // 53; 16384 x 8192 bf16 113, 60, 51, 43, 47, 48; 32768 x 4100 bf16 -, -,
-    // 103, 86, 76, 78.  Without statistics nothing does: logprob_grad 3001 x
-    // 32001 bf16 59, 55, 56, 57, 57, 55; 32768 x 4100 bf16 250, 133, 104, 92,
-    // 86, 87.  (A loss with a gradient keeps its mapping when the gradient is
-    // not asked for: the mapping sets the order of the sums.)
+    //   8192 x 65536 bf16          278       301       332       351       354       368
+    //   4096 x 50257 bf16          149       135       150       162       161       161
+    //   4096 x 30000 bf16          108        85        83        89        89        91
+    //   8192 x 16384 bf16          126        96        86        87        87        93
+    //   16384 x 8192 bf16          222       121       103        91        96        97
+    //   20000 x 6000 bf16          256       153       127       124       112       111
+    // A teacher's list takes time that more rows at once cover: distill 4096 x
+    // 16384 bf16 75, 63, 65, 68, 59, 64.  Without a gradient a row need not
+    // stay: logprob 4096 x 50257 f16 62, 53, 48, 48, 50, 53; 16384 x 8192 bf16
+    // 145, 76, 58, 48, 50, 52; 32768 x 4100 bf16 267, 143, 104, 86, 76, 78.
+    // Without statistics nothing does: logprob_grad 3001 x 32001 bf16 54, 54,
+    // 55, 56, 56, 54; 32768 x 4100 bf16 250, 133, 104, 92, 86, 87.  (A loss
+    // with a gradient keeps its mapping when the gradient is not asked for:
+    // the mapping sets the order of the sums.)
     if constexpr (!OP::GRADIENT) {
         return bytes > 16384 ? launch_row_kernel<DT, OP, 128, 8>(a, op, 4, teacher_k, s, di)
                              : launch_row_kernel<DT, OP, 128, 4>(a, op, 4, teacher_k, s, di);
@@ -1293,8 +1307,10 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
             return launch_row_kernel<DT, OP, 512, 4>(a, op, 1, teacher_k, s, di);
         if (bytes > 40960)
             return launch_row_kernel<DT, OP, 256, 4>(a, op, bytes > 65536 ? 2 : 3, teacher_k, s, di);
-        return bytes > 12288 ? launch_row_kernel<DT, OP, 128, 8>(a, op, 4, teacher_k, s, di)
-                             : launch_row_kernel<DT, OP, 128, 4>(a, op, 6, teacher_k, s, di);
+        if constexpr (!OP::TEACHER)
+            if (bytes > 12288)
+                return launch_row_kernel<DT, OP, 128, 8>(a, op, 4, teacher_k, s, di);
+        return launch_row_kernel<DT, OP, 128, 4>(a, op, bytes > 12288 ? 4 : 6, teacher_k, s, di);
     }
 }
 
