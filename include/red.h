@@ -348,8 +348,8 @@ int red_full_noalloc(int op, const float *x, int64_t n, float *out, red_stream_t
  *            call allows it computes the loss alone.
  *   target   one int64 column per row.  A row whose target is outside
  *            [0, len) (such as -100) is ignored, as is a row or pair of
- *            weight 0: its logits are never read, its loss and logp are 0
- *            and its row of dx is 0, whatever they hold.
+ *            weight 0: its loss and logp are 0 and its row of dx is 0,
+ *            whatever its logits and its other inputs hold.
  *   weight   a factor per row or pair, NULL for 1 everywhere (a mask over its
  *            number of live tokens gives a mean).
  *   logits   -inf removes an entry from the vocabulary.  A row that is -inf
@@ -371,8 +371,8 @@ int red_logprob(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld,
 /*
  * red_logprob_grad -- backward of red_logprob: for the gradient dlogp[r] of
  * some loss by logp[r], dx[r, j] = scale * dlogp[r] * ([j == target[r]] - p_j)
- * with p_j = e^(z_j - lse[r]), lse as red_logprob left it.  Rows whose dlogp
- * is 0 are not read either.
+ * with p_j = e^(z_j - lse[r]), lse as red_logprob left it.  A row whose dlogp
+ * is 0 has a gradient of 0, whatever its logits hold.
  */
 int red_logprob_grad(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld, float scale,
                      const int64_t *target, const float *lse, const float *dlogp, void *dx, int64_t ldd,

@@ -1164,13 +1164,13 @@ int launch_row_kernel(const LogitRows &a, const OP &op, int per_sm, int teacher_
         slots = 2;
     const size_t smem = slots * batch + fixed;
     const auto kernel = row_kernel<DT, OP, NT, U>;
-    static std::atomic<int> ready{0};
-    if (!ready.load(std::memory_order_relaxed)) {
+    static std::atomic<uint64_t> ready{0};  // a bit per device
+    if (!(ready.load(std::memory_order_relaxed) >> di.dev & 1)) {
         const cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)CTA_SMEM);
         if (e != cudaSuccess)
             return cuda_fail(e, "row kernel: shared memory");
-        ready.store(1, std::memory_order_relaxed);
+        ready.fetch_or(uint64_t(1) << di.dev, std::memory_order_relaxed);
     }
     const int64_t cap = (int64_t)di.sms * per_sm;
     const unsigned grid = (unsigned)(a.rows < cap ? a.rows : cap);
@@ -1191,10 +1191,11 @@ int launch_group_kernel(const LogitRows &a, const OP &op, int teacher_k, cudaStr
     const auto kernel = group_row_kernel<DT, OP, G, NV>;
     constexpr int ROWS = GROUP_NT / G;
     const size_t smem = (size_t)ROWS * 16 * teacher_k;
-    // residency, kept per instance for the last list length asked for
+    // residency, kept per instance for the last device and list length asked for
     static std::atomic<int64_t> known{-1};
+    const int64_t want_key = (int64_t)di.dev << 24 | teacher_k;
     int64_t k = known.load(std::memory_order_relaxed);
-    if (k < 0 || (k >> 8) != teacher_k) {
+    if (k < 0 || (k >> 8) != want_key) {
         cudaError_t e = cudaSuccess;
         if (smem > 48 * 1024)
             e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CTA_SMEM);
@@ -1204,7 +1205,7 @@ int launch_group_kernel(const LogitRows &a, const OP &op, int teacher_k, cudaStr
         if (e != cudaSuccess || occ < 1)
             return e != cudaSuccess ? cuda_fail(e, "row group kernel: occupancy")
                                     : fail(RED_ECUDA, "row group kernel cannot be resident on this device");
-        k = (int64_t)teacher_k << 8 | occ;
+        k = want_key << 8 | occ;
         known.store(k, std::memory_order_relaxed);
     }
     const int64_t want = (a.rows + ROWS - 1) / ROWS, cap = di.sms * (k & 255);

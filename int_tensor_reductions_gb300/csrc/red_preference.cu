@@ -30,7 +30,9 @@ __device__ PairTerms pair_terms(const PreferenceArgs &p, float u)
         // -(1 - e) log sigma(u) - e log sigma(-u); log sigma through
         // log1p(e^-|u|), which neither overflows nor loses small values
         const float e = p.smoothing, soft = log1pf(expf(-fabsf(u)));
-        t.loss = (1.0f - e) * (soft + fmaxf(-u, 0.0f)) + e * (soft + fmaxf(u, 0.0f));
+        t.loss = (1.0f - e) * (soft + fmaxf(-u, 0.0f));
+        if (e != 0.0f)  // (u may be infinite: a token that the policy rules out)
+            t.loss += e * (soft + fmaxf(u, 0.0f));
         t.du = e - 1.0f / (1.0f + expf(u));
         if (u != u)
             t.loss = u;

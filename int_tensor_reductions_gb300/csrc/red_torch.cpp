@@ -16,6 +16,7 @@
 #include <ATen/ops/empty_strided.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "red.h"
@@ -185,14 +186,13 @@ PyObject *guarded(const char *name, Py_ssize_t given, Py_ssize_t wanted, F f)
         PyErr_Format(PyExc_TypeError, "%s takes %zd arguments", name, wanted);
         return nullptr;
     }
+    HANDLE_TH_ERRORS  // torch's exceptions as Python's
     try {
         return f();
     } catch (const Refused &) {
         return nullptr;
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
     }
+    END_HANDLE_TH_ERRORS
 }
 
 #define RETURN_IF_REFUSED(status) \

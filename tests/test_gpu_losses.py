@@ -148,6 +148,84 @@ def test_logprob_extremes(dtype):
         assert bool(got[7].isnan().all())
 
 
+@pytest.mark.parametrize("dtype", ref.DTYPES)
+@pytest.mark.parametrize("length", [40, 700, 3000, 5001, 9000, 40000])
+@pytest.mark.parametrize("copies", [1, 60, 200])
+def test_extremes_by_every_mapping(dtype, length, copies):
+    """The extreme rows once more, among few rows and among many (other
+    kernels), through every loss: masked entries, the type's lowest value in
+    part of a row and throughout, a lone entry, NaN and infinity."""
+    if length * copies > 2_100_000:
+        pytest.skip("as large as needed")
+    low = torch.finfo(dtype).min
+    kinds = 9
+    rows = kinds * copies
+    x, _ = logits(rows, length, dtype, length + copies, pad=3)
+    t = torch.full((rows,), 1)
+    one = torch.zeros(rows, dtype=torch.bool)
+    one[::copies] = True
+    k = torch.arange(rows) // copies
+    x[k == 0, length // 2:] = -math.inf
+    x[k == 1, :length - 2] = -math.inf
+    t[k == 1] = length - 1
+    x[k == 2] = -math.inf               # nothing left
+    x[k == 3] = low                     # uniform
+    x[k == 4, 2:] = low
+    x[k == 5, :length - 2] = low        # a prefix far below the rest
+    t[k == 5] = length - 2
+    x[k == 6, length - 1] = math.nan
+    x[k == 7, length // 2] = math.inf
+    x[k == 8] = -low                    # uniform at the other end
+    lp, norm = ref.log_softmax(x, 1.0)
+    want, live = ref.taken(lp, t)
+    sane = (k != 6) & (k != 7)
+    logp, lse = itr.red_logprob(x, t.to(DEV))
+    ref.assert_logp(logp[sane.to(DEV)], want[sane], "logp")
+    assert bool(logp.cpu()[~sane].isnan().all())
+    old = torch.where(want.isfinite(), want, torch.zeros_like(want)).float()
+    ones = torch.ones(rows)
+    loss, got, stats, grad = itr.red_policy(x, t.to(DEV), old.to(DEV), -ones.to(DEV))
+    ref.assert_logp(got[sane.to(DEV)], want[sane], "policy logp")
+    assert bool((loss.cpu()[k == 2] == 0).all()) and bool((grad[(k == 2).to(DEV)] == 0).all())
+    assert bool(grad[(~sane).to(DEV)].isnan().all()) and bool(loss.cpu()[~sane].isnan().all())
+    on = sane & (k != 2)
+    # the ratio is 1 up to the rounding of old and the error of logp; -min(r A, ...) falls with logp for A = -1
+    c = torch.ones(rows, dtype=torch.float64)
+    g = ref.target_grad(lp, norm, t, live, c)
+    p = lp.exp()
+    ref.assert_grad(grad.cpu()[on], g[on], p[on], c[on], t[on], extra=3e-5, what="policy")
+    ids = torch.tensor([[1, 2 % length, length - 1]]).repeat(rows, 1)
+    vals = torch.zeros((rows, 3))
+    loss, stats, grad = itr.red_distill(x, ids.to(DEV), vals.to(DEV))
+    assert bool((grad[(k == 2).to(DEV)] == 0).all()) and bool((loss.cpu()[k == 2] == 0).all())
+    assert bool(grad[(~sane).to(DEV)].isnan().all())
+    q = torch.full((rows, 3), 1 / 3, dtype=torch.float64)
+    mass = torch.zeros_like(p).scatter_add_(1, ids, q)
+    ref.assert_grad(grad.cpu()[on], (p - mass)[on], (p + mass)[on], c[on], extra=3e-5, what="distill")
+    # the gradient from lse, where fp32 has room for it beside the row's logits
+    near = on & (k != 3) & (k != 8)
+    got = itr.red_logprob_grad(x, t.to(DEV), lse, ones.to(DEV))
+    ref.assert_grad(got.cpu()[near], g[near], p[near], c[near], t[near],
+                    extra=2.0 ** -23 * float(norm[near].abs().max()), what="grad")
+    assert bool((got[(k == 2).to(DEV)] == 0).all())
+
+
+def test_preference_with_a_token_ruled_out():
+    """A rejected answer that the policy cannot give costs nothing; a chosen one
+    costs everything."""
+    for length in (50, 9000):
+        x, _ = logits(4, length, torch.float32, 3)
+        t = torch.tensor([1, 2, 3, 4], device=DEV)
+        x[3, 4] = -math.inf
+        off = torch.tensor([0, 1, 2, 3, 4], device=DEV)
+        loss, seq, stats, grad = itr.red_preference(x, t, off)
+        assert loss[1].item() == 0.0 and math.isfinite(loss[0].item()) and seq[3].item() == -math.inf
+        assert bool((grad[1] == 0).all()) and bool((grad[3] == 0).all()) and bool((grad[0] != 0).any())
+        swapped = torch.tensor([4, 3, 2, 1], device=DEV)
+        loss = itr.red_preference(x.flip(0), swapped, off, grad=False)[0]
+        assert loss[0].item() == math.inf
+
+
 def policy_inputs(rows, logp, seed):
     g = gen(seed)
     old = logp.float() + torch.randn(rows, generator=g) * 0.3
