@@ -291,17 +291,40 @@ __device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
-// No wait is without end: one that runs out (which takes a hardware fault)
-// marks the CTA as failed, and its rows' results become NaN.
-constexpr int WAIT_TRIES = 1 << 26;
+// No wait is without end: one that runs out (20 s, which takes a hardware
+// fault) marks the CTA as failed, and its rows' results become NaN.
+struct Patience {
+    unsigned tries = 0;
+    uint64_t since = 0;
+
+    static __device__ __forceinline__ uint64_t now()
+    {
+        uint64_t t;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        return t;
+    }
+    // After a try in vain: whether to give up.
+    __device__ __forceinline__ bool spent(volatile int *failed)
+    {
+        if (++tries % 256 != 0)
+            return false;
+        if (tries == 256)
+            since = now();
+        if (!*failed && now() - since < 20000000000ull)
+            return false;
+        *failed = 1;
+        return true;
+    }
+};
 
 __device__ __forceinline__ void mbar_wait(uint64_t *bar, uint32_t parity, volatile int *failed)
 {
-    for (int n = 0; !mbar_try(bar, parity); ++n)
-        if (n == WAIT_TRIES || ((n & 255) == 255 && *failed)) {
-            *failed = 1;
+    if (mbar_try(bar, parity))
+        return;
+    Patience patience;
+    while (!mbar_try(bar, parity))
+        if (patience.spent(failed))
             return;
-        }
 }
 
 // ---- clusters
@@ -545,11 +568,9 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
         int slot = 0;
         uint32_t parity = 1;  // a fresh slot is empty
         for (int i = 0;; ++i) {
-            for (int n = 0; *published <= i && !*failed; ++n) {
+            Patience patience;
+            while (*published <= i && !patience.spent(failed))
                 __nanosleep(32);
-                if (n == WAIT_TRIES)
-                    *failed = 1;
-            }
             if (*failed)
                 break;
             __threadfence_block();
@@ -572,6 +593,11 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
                 }
             }
         }
+        // after a failure the consumers no longer wait for the copies in flight
+        if (*failed)
+            for (int k = 0; k < slots; ++k)
+                for (int n = 0; n < 65536 && !mbar_try(&sh.full[k], k < slot ? parity ^ 1 : parity); ++n)
+                    __nanosleep(64);
     } else if (OP::STATS && !OP::TEACHER && warp == NW + 2) {
         // ---- writer
         first_barrier();
