@@ -259,6 +259,8 @@ __device__ __forceinline__ RowGrad grad_of_target(const LogitRows &a, const RowS
 //   GRADIENT whether it can have a gradient;
 //   TOTALS   how many sums over rows it has: total() adds a row's terms,
 //            stats is where they go;
+//   TAIL     whether something remains when all rows are done: the totals, or
+//            tail();
 //   load()   the row's entry (its logits are still intact): issues loads and
 //            uses none of their values, so that a later settle() may be the
 //            first to wait for them;
@@ -270,6 +272,7 @@ __device__ __forceinline__ RowGrad grad_of_target(const LogitRows &a, const RowS
 
 struct LogprobArgs {
     static constexpr bool STATS = true, TEACHER = false, GRADIENT = false;
+    static constexpr bool TAIL = false;
     static constexpr int TOTALS = 0;
     const int64_t *target;
     float *logp, *lse;
@@ -301,6 +304,7 @@ struct LogprobArgs {
 
 struct LogprobGradArgs {
     static constexpr bool STATS = false, TEACHER = false, GRADIENT = true;
+    static constexpr bool TAIL = false;
     static constexpr int TOTALS = 0;
     const int64_t *target;
     const float *lse, *dlogp;
@@ -355,6 +359,7 @@ struct PolicyTerms {
 
 struct PolicyArgs {
     static constexpr bool STATS = true, TEACHER = false, GRADIENT = true;
+    static constexpr bool TAIL = true;
     static constexpr int TOTALS = 4;
     const int64_t *target;
     const float *old_logp, *ref_logp, *adv, *weight;  // ref_logp, weight may be NULL
@@ -482,6 +487,7 @@ struct TeacherRow {
 
 struct DistillArgs {
     static constexpr bool STATS = true, TEACHER = true, GRADIENT = true;
+    static constexpr bool TAIL = true;
     static constexpr int TOTALS = 2;
     int k, vdtype;
     const int64_t *ids;

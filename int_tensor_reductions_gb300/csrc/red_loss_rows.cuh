@@ -796,6 +796,21 @@ __device__ void cta_totals(Sum (&v)[N], Sum *s, float *out)
     }
 }
 
+// What remains of a loss when all rows are done, by one CTA of NT threads; s
+// has room for 4 sums per warp.
+template <class OP, int NT>
+__device__ void run_tail(int64_t rows, int len, const OP &op, Sum *s)
+{
+    if constexpr (OP::TOTALS > 0) {
+        Sum v[OP::TOTALS];
+        for (int64_t r = threadIdx.x; r < rows; r += NT)
+            op.total(r, len, v);
+        cta_totals<OP::TOTALS, NT>(v, s, op.stats);
+    } else {
+        op.template tail<NT>(rows, len, s);
+    }
+}
+
 constexpr int TOTAL_NT = 256, TOTAL_CTAS = 256, TOTAL_ROWS = 256;
 
 // Totals over rows from the results that a row kernel left: each CTA sums its
@@ -1091,7 +1106,7 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
         } else if (tid == 0) {
             op.template write<DT>(a, e, t);
         }
-        if (OP::TOTALS > 0 && tid == 0) {
+        if (OP::TAIL && tid == 0) {
             __threadfence();
             s_last = atomicAdd(tick, 1u) == (unsigned)a.rows - 1;
         }
@@ -1117,18 +1132,15 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
     } else if (a.dx) {
         zero_row<DT>(grow, a.len, rank * FEW_NT + tid, cs * FEW_NT);
     }
-    if constexpr (OP::TOTALS > 0) {
+    if constexpr (OP::TAIL) {
+        __shared__ Sum s_sum[4 * FEW_NW];
         if (rank != 0)
             return;
         __syncthreads();
         if (!s_last)
             return;
         __threadfence();
-        Sum v2[OP::TOTALS];
-        for (int64_t k = tid; k < a.rows; k += FEW_NT)
-            op.total(k, a.len, v2);
-        __shared__ Sum s_sum[OP::TOTALS * FEW_NW];
-        cta_totals<OP::TOTALS, FEW_NT>(v2, s_sum, op.stats);
+        run_tail<OP, FEW_NT>(a.rows, a.len, op, s_sum);
         if (tid == 0)
             *tick = 0;
     }
@@ -1224,7 +1236,8 @@ int launch_group_kernel(const LogitRows &a, const OP &op, int teacher_k, cudaStr
     if (k < 0 || (k >> 8) != want_key) {
         cudaError_t e = cudaSuccess;
         if (smem > 48 * 1024)
-            e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CTA_SMEM);
+            e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     GROUP_NT / 32 * 16 * RED_DISTILL_MAX_K);
         int occ = 0;
         if (e == cudaSuccess)
             e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, (const void *)kernel, GROUP_NT, smem);
@@ -1272,13 +1285,34 @@ int launch_totals(const LogitRows &a, const OP &op, cudaStream_t s)
     return RED_OK;
 }
 
-// Rows and columns by a row kernel; *summed: the totals are done, too.
+// Rows longer than the group kernel's, where they are few: *taken, and what
+// remains after the rows is done, too.
 template <int DT, class OP>
-int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s, bool *summed)
+int launch_few(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s, const DeviceInfo &di, bool *taken)
+{
+    const size_t bytes = (size_t)a.len * sizeof(typename Elem<DT>::T);
+    const int64_t nvec = (int64_t)(bytes / 16);
+    for (int cluster = MAX_CLUSTER; bytes > GROUP_ROW_BYTES && cluster >= 2; cluster /= 2) {
+        const int64_t slice = (nvec + cluster - 1) / cluster;
+        if (2 * a.rows * cluster > FEW_CTAS_PER_2_SMS * di.sms || slice > 8 * FEW_NT)
+            continue;
+        *taken = true;
+        return slice <= 4 * FEW_NT ? launch_few_kernel<DT, OP, 4>(a, op, cluster, teacher_k, s)
+                                   : launch_few_kernel<DT, OP, 8>(a, op, cluster, teacher_k, s);
+    }
+    return RED_OK;
+}
+
+// All rows, by the kernel for their number and length; *finished: what remains
+// after them is done, too.
+template <int DT, class OP>
+int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s, bool *finished)
 {
     DeviceInfo di;
-    const int st = device_info(&di);
-    if (st != RED_OK)
+    int st = device_info(&di);
+    if (st == RED_OK)
+        st = launch_few<DT>(a, op, teacher_k, s, di, finished);
+    if (st != RED_OK || *finished)
         return st;
     const size_t bytes = (size_t)a.len * sizeof(typename Elem<DT>::T);
     if (bytes <= GROUP_ROW_BYTES) {
@@ -1294,15 +1328,6 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
         if (bytes <= 4096)
             return launch_group_kernel<DT, OP, 32, 8>(a, op, teacher_k, s, di);
         return launch_group_kernel<DT, OP, 32, 16>(a, op, teacher_k, s, di);
-    }
-    const int64_t nvec = (int64_t)(bytes / 16);
-    for (int cluster = MAX_CLUSTER; cluster >= 2; cluster /= 2) {
-        const int64_t slice = (nvec + cluster - 1) / cluster;
-        if (2 * a.rows * cluster > FEW_CTAS_PER_2_SMS * di.sms || slice > 8 * FEW_NT)
-            continue;
-        *summed = true;
-        return slice <= 4 * FEW_NT ? launch_few_kernel<DT, OP, 4>(a, op, cluster, teacher_k, s)
-                                   : launch_few_kernel<DT, OP, 8>(a, op, cluster, teacher_k, s);
     }
     // Threads, vectors per thread and batch, and CTAs per SM, by row bytes.  A
     // CTA is busy with one row at a time, so short rows need several CTAs to
@@ -1344,14 +1369,14 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
 template <class OP>
 int launch_loss_rows(int dtype, const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s)
 {
-    bool summed = false;
+    bool finished = false;
     int st;
     switch (dtype) {
-    case RED_F32: st = launch_rows_of<RED_F32>(a, op, teacher_k, s, &summed); break;
-    case RED_F16: st = launch_rows_of<RED_F16>(a, op, teacher_k, s, &summed); break;
-    default: st = launch_rows_of<RED_BF16>(a, op, teacher_k, s, &summed); break;
+    case RED_F32: st = launch_rows_of<RED_F32>(a, op, teacher_k, s, &finished); break;
+    case RED_F16: st = launch_rows_of<RED_F16>(a, op, teacher_k, s, &finished); break;
+    default: st = launch_rows_of<RED_BF16>(a, op, teacher_k, s, &finished); break;
     }
-    return st != RED_OK || summed ? st : launch_totals(a, op, s);
+    return st != RED_OK || finished ? st : launch_totals(a, op, s);
 }
 
 }  // namespace red

@@ -507,6 +507,44 @@ def test_preference_edges():
     assert abs(loss.item() - math.log(2.0)) < 1e-6 and grad.shape == (0, 50)
 
 
+# Pairs of one call and of the same call with more, empty pairs: other kernels
+# sum them, each result within 1.5e-7 of its sums' sizes.
+@pytest.mark.parametrize("average", [False, True])
+@pytest.mark.parametrize("rows,length", [(60, 5003), (25, 33000), (200, 300)])
+def test_preference_pairs_by_either_kernel(rows, length, average):
+    pairs, more = 6, 40
+    x, _ = logits(rows, length, torch.bfloat16, 3, pad=5)
+    t = targets(rows, length, 4, 0.2).to(DEV)
+    t[rows // 3] = length                 # out of range
+    x[rows // 2] = -math.inf
+    off = torch.linspace(2, rows - 3, 2 * pairs + 1).long()
+    off[3] = off[4]                       # an empty rejected sequence
+    w = torch.tensor([1.0, 0.0, 0.5, 2.0, 1.0, 1.0])
+    rf = torch.randn(2 * pairs, generator=gen(1)) * 3
+    kw = dict(beta=0.3, margin=0.2, smoothing=0.1, average=average)
+    a = itr.red_preference(x, t, off.to(DEV), ref_logp=rf.to(DEV), weight=w.to(DEV), **kw)
+    # chosen sequences come first, then the rejected ones: the empty pairs go between and behind
+    mid, end = off[pairs].repeat(more), off[-1].repeat(more)
+    off2 = torch.cat([off[:pairs], mid, off[pairs:], end])
+    pad = torch.zeros(more)
+    b = itr.red_preference(x, t, off2.to(DEV), ref_logp=torch.cat([rf[:pairs], pad, rf[pairs:], pad]).to(DEV),
+                           weight=torch.cat([w, pad]).to(DEV), **kw)
+    size = float(a[1].abs().max()) + 10.0
+    n = pairs + more
+    assert (a[0] - b[0][:pairs]).abs().max() <= 1e-6 * size
+    seq = torch.cat([b[1][:pairs], b[1][n:n + pairs]])
+    assert (a[1] - seq).abs().max() <= 4e-7 * size
+    assert (a[2] - b[2]).abs().max() <= 1e-5 * size
+    assert bool((b[0][pairs:] == 0).all()) and bool(a[0][1] == 0)
+    # c differs by du's 0.3 * 1e-6 * size, and bf16 by a rounding
+    assert bool(((a[3].float() - b[3].float()).abs() <= 2.0 ** -7 * a[3].float().abs() + 1e-6 * size).all())
+    dead = torch.zeros(rows, dtype=torch.bool)
+    dead[:2], dead[-3:], dead[rows // 3], dead[rows // 2] = True, True, True, True
+    dead |= (t.cpu() < 0)
+    dead[int(off[1]):int(off[2])] = True  # chosen of the pair without weight
+    assert bool((a[3].cpu()[dead] == 0).all()) and bool((b[3].cpu()[dead] == 0).all())
+
+
 def test_no_rows():
     x = torch.empty((0, 40), device=DEV)
     none = torch.empty(0, device=DEV)
