@@ -197,6 +197,14 @@ struct SoftRun {
     }
 };
 
+// 16 bytes into shared memory, and the wait for all that the thread asked for.
+__device__ __forceinline__ void async_load16(void *dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // The gradient of one vector of logits whose first column is j0.
 template <int DT, bool FAR_ROW = false>
 __device__ __forceinline__ uint4 vec_grad(const uint4 &v, const RowGrad &g, int j0)
@@ -867,64 +875,109 @@ __global__ void __launch_bounds__(TOTAL_NT) total_kernel(int64_t rows, int len, 
 
 constexpr int GROUP_NT = 256;
 
+// Whether the next row is fetched into shared memory while a row is at work
+// (before and after, us: policy 20000 x 4000 bf16 69.1, 59.6; 30000 x 1000
+// 32.8, 30.5; logprob 60000 x 1024 bf16 25.5, 23.2; 60000 x 4000 81.9, 75.9;
+// 60000 x 400 f32 21.7, 18.7; one row per group costs 0.2).  Not where the
+// lists of a teacher want the space and the row in L1 (distill 30000 x 400
+// bf16, 64 entries: 50.5, 64.5), nor for the shortest rows (policy 65536 x 120
+// bf16 16.1, 17.7: the registers are short).
+template <class OP, int G>
+constexpr bool group_staged = !OP::TEACHER && G > 4;
+
 // G lanes per row, the row in registers (NV vectors per lane): rows too short
 // for a CTA barrier each.  The shorter the row, the fewer the lanes, so that
 // what is done once per row (the loss itself, its logarithms and exponentials,
 // the reductions) is done for 32 / G rows at a time.  The next row's entry is
-// fetched while this row is on its way.
+// fetched while this row is at work, and so is (`staged`) the next row.
 template <int DT, class OP, int G, int NV>
 __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(LogitRows a, OP op, int teacher_k)
 {
     using T = typename Elem<DT>::T;
     constexpr int E = VEC_ELEMS<DT>;
     constexpr int ROWS = GROUP_NT / G;  // rows of a CTA at a time
+    constexpr bool STAGED = group_staged<OP, G>;
     extern __shared__ __align__(16) unsigned char smem[];
     const int gl = threadIdx.x & (G - 1), group = threadIdx.x / G;
-    TeacherRow list(smem + (size_t)group * 16 * teacher_k, teacher_k);
+    uint4 *const stage = reinterpret_cast<uint4 *>(smem) + threadIdx.x;  // of this lane, GROUP_NT apart
+    TeacherRow list(smem + (STAGED ? NV * GROUP_NT * 16 : 0) + (size_t)group * 16 * teacher_k, teacher_k);
     const float s2 = a.s2;
     const T *const x = static_cast<const T *>(a.x);
     T *const dx = static_cast<T *>(a.dx);
     pdl_enter();
 
     const int64_t step = (int64_t)gridDim.x * ROWS;
+    // The entry of the next row, and (if staged) that row on its way into shared
+    // memory: each lane fetches and reads its own vectors, so no other waits.
     RowEntry n{};
-    auto fetch = [&](int64_t r) {
-        n.state = ROW_END;
+    constexpr int ENDS = (2 * (E - 1) + G - 1) / G;  // the row's ragged ends, fewer than E elements each
+    float n_x[ENDS];
+    auto end_at = [&](int k, int h, int nvec) {
+        const int i = gl + k * G, tail = a.len - h - nvec * E;
+        return i < h ? i : (i - h < tail ? a.len - tail + i - h : -1);
+    };
+    auto load = [&](int64_t r, RowEntry &to) {
+        to.state = ROW_END;
         if (r < a.rows) {
-            op.load(r, n);
+            op.load(r, to);
+            to.state = ROW_LIVE;
+        }
+    };
+    auto settle = [&]() {
+        if (n.state != ROW_END) {
             op.settle(a, n);
             if (n.state == ROW_LIVE)
                 op.template touch<DT>(a, n);
         }
     };
-    fetch((int64_t)blockIdx.x * ROWS + group);
+    auto load_ends = [&](const T *row, int h, int nvec) {
+#pragma unroll
+        for (int k = 0; k < ENDS; ++k) {
+            const int j = end_at(k, h, nvec);
+            n_x[k] = j >= 0 ? load_elem<DT>(row, j) : NEG_INF;
+        }
+    };
+    auto request = [&]() {
+        if (STAGED && n.state == ROW_LIVE) {
+            const T *const row = x + n.r * a.ld;
+            const int h = head_elems<DT>(row, a.len), nvec = (a.len - h) / E;
+            const uint4 *const vec = reinterpret_cast<const uint4 *>(row + h) + gl;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (i * G + gl < nvec)
+                    async_load16(stage + i * GROUP_NT, vec + i * G);
+            load_ends(row, h, nvec);
+        }
+    };
     // (the loop is the same for all of a warp: its first group has the first row)
-    for (int64_t r0 = (int64_t)blockIdx.x * ROWS + (group & ~(32 / G - 1)); r0 < a.rows; r0 += step) {
-        const int64_t r = r0 + (group & (32 / G - 1));
+    int64_t r0 = (int64_t)blockIdx.x * ROWS + (group & ~(32 / G - 1));
+    const int sub = group & (32 / G - 1);
+    load(r0 + sub, n);
+    settle();
+    request();
+    for (; r0 < a.rows; r0 += step) {
         const RowEntry e = n;
         const bool live = e.state == ROW_LIVE;
         const T *const row = x + e.r * a.ld;
         const int h = head_elems<DT>(row, a.len), nvec = (a.len - h) / E;
         uint4 v[NV];
-        // the row's ragged ends, fewer than E elements each
-        constexpr int ENDS = (2 * (E - 1) + G - 1) / G;
         float end_x[ENDS];
-        auto end_at = [&](int k) {
-            const int i = gl + k * G, tail = a.len - h - nvec * E;
-            return i < h ? i : (i - h < tail ? a.len - tail + i - h : -1);
-        };
+        if (!STAGED && live)
+            load_ends(row, h, nvec);
+#pragma unroll
+        for (int k = 0; k < ENDS; ++k)
+            end_x[k] = n_x[k];
+        load(r0 + sub + step, n);
+        if (STAGED)
+            async_wait();
         if (live) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (i * G + gl < nvec)
-                    v[i] = reinterpret_cast<const uint4 *>(row + h)[i * G + gl];
-#pragma unroll
-            for (int k = 0; k < ENDS; ++k) {
-                const int j = end_at(k);
-                end_x[k] = j >= 0 ? load_elem<DT>(row, j) : NEG_INF;
-            }
+                    v[i] = STAGED ? stage[i * GROUP_NT] : reinterpret_cast<const uint4 *>(row + h)[i * G + gl];
         }
-        fetch(r + step);
+        settle();
+        request();
         if constexpr (OP::TEACHER)
             op.template prepare<DT, G>(a, e.r, live, list);
 
@@ -992,7 +1045,7 @@ __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(Log
         if (e.state != ROW_END) {
 #pragma unroll
             for (int k = 0; k < ENDS; ++k) {
-                const int j = end_at(k);
+                const int j = end_at(k, h, nvec);
                 if (j >= 0)
                     store_elem<DT>(grow, j, g.zero ? 0.0f : elem_grad<DT>(end_x[k], g, j));
             }
@@ -1228,7 +1281,8 @@ int launch_group_kernel(const LogitRows &a, const OP &op, int teacher_k, cudaStr
 {
     const auto kernel = group_row_kernel<DT, OP, G, NV>;
     constexpr int ROWS = GROUP_NT / G;
-    const size_t smem = (size_t)ROWS * 16 * teacher_k;
+    constexpr int STAGE = group_staged<OP, G> ? NV * GROUP_NT * 16 : 0;
+    const size_t smem = STAGE + (size_t)ROWS * 16 * teacher_k;
     // residency, kept per instance for the last device and list length asked for
     static std::atomic<int64_t> known{-1};
     const int64_t want_key = (int64_t)di.dev << 24 | teacher_k;
@@ -1237,7 +1291,7 @@ int launch_group_kernel(const LogitRows &a, const OP &op, int teacher_k, cudaStr
         cudaError_t e = cudaSuccess;
         if (smem > 48 * 1024)
             e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     GROUP_NT / 32 * 16 * RED_DISTILL_MAX_K);
+                                     STAGE + GROUP_NT / 32 * 16 * RED_DISTILL_MAX_K);
         int occ = 0;
         if (e == cudaSuccess)
             e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, (const void *)kernel, GROUP_NT, smem);
