@@ -888,7 +888,8 @@ constexpr bool group_staged = !OP::TEACHER && G > 4;
 // G lanes per row, the row in registers (NV vectors per lane): rows too short
 // for a CTA barrier each.  The shorter the row, the fewer the lanes, so that
 // what is done once per row (the loss itself, its logarithms and exponentials,
-// the reductions) is done for 32 / G rows at a time.  The next row's entry is
+// the reductions) is done for 32 / G rows at a time; two warps (G = 64) join
+// their statistics by way of shared memory and a barrier of their own.  The next row's entry is
 // fetched while this row is at work, and so is (`staged`) the next row.
 template <int DT, class OP, int G, int NV>
 __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(LogitRows a, OP op, int teacher_k)
@@ -949,9 +950,31 @@ __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(Log
             load_ends(row, h, nvec);
         }
     };
+    // The maximum and the sum of two warps' values: each is read between its own
+    // barrier and the other's next, and written after that.
+    __shared__ float s_max[GROUP_NT / 32], s_sum[GROUP_NT / 32];
+    const int warp = threadIdx.x / 32;
+    auto join_max = [&](float v) {
+        s_max[warp] = v;
+        bar_sync(1 + group, G);
+#pragma unroll
+        for (int k = 0; k < G / 32; ++k)
+            v = fmaxf(v, s_max[group * (G / 32) + k]);
+        return v;
+    };
+    auto join_sum = [&](float v) {
+        s_sum[warp] = v;
+        bar_sync(1 + group, G);
+        v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < G / 32; ++k)
+            v += s_sum[group * (G / 32) + k];
+        return v;
+    };
     // (the loop is the same for all of a warp: its first group has the first row)
-    int64_t r0 = (int64_t)blockIdx.x * ROWS + (group & ~(32 / G - 1));
-    const int sub = group & (32 / G - 1);
+    constexpr int PER_WARP = G < 32 ? 32 / G : 1;
+    int64_t r0 = (int64_t)blockIdx.x * ROWS + (group & ~(PER_WARP - 1));
+    const int sub = group & (PER_WARP - 1);
     load(r0 + sub, n);
     settle();
     request();
@@ -993,7 +1016,7 @@ __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(Log
                 for (int k = 0; k < ENDS; ++k)
                     top = fmaxf(top, end_x[k]);
             }
-            top = group_max<G>(top);
+            top = G > 32 ? join_max(group_max<32>(top)) : group_max<G>(top);
             SoftRun run;
             run.init();
             run.m = top;
@@ -1012,7 +1035,8 @@ __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(Log
                 for (int k = 0; k < ENDS; ++k)
                     run.add(end_x[k], s2);
             }
-            t = row_stat(a, SoftStat{top, group_sum<G>(run.stat().l)});
+            const float l = run.stat().l;
+            t = row_stat(a, SoftStat{top, G > 32 ? join_sum(group_sum<32>(l)) : group_sum<G>(l)});
         }
         if constexpr (OP::TEACHER)
             op.template finish<G>(a, e, t, list);
@@ -1226,6 +1250,8 @@ cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), unsigned grid, unsigned bl
 
 // Longest row of the group kernel.
 constexpr size_t GROUP_ROW_BYTES = 8192;
+// Longest row of two warps of it.
+constexpr size_t PAIR_ROW_BYTES = 16384;
 
 // The few-row kernel is taken while its CTAs, with the largest cluster that
 // allows it, are at most this many per two SMs (and a thread's slice 8
@@ -1233,6 +1259,8 @@ constexpr size_t GROUP_ROW_BYTES = 8192;
 // 2.4 / 5.9, 64 rows 4.6 / 6.3; policy 1 row 5.5 / 9.4, 30 rows 7.2 / 9.5, 64
 // rows 8.5 / 9.4, 100 rows 9.4 / 9.8, 300 x 16384 f32 9.4 / 10.5.  With 4
 // CTAs per SM they no longer all run at once: 152 x 65536 bf16 12.5 / 10.1.
+// Against two warps of the group kernel: logprob 20 x 8100 bf16 2.8 / 3.8, 250 x
+// 8100 4.4 / 4.5, 250 x 4200 4.1 / 3.1; preference 250 x 4200 11.8 / 12.4.
 constexpr int FEW_CTAS_PER_2_SMS = 7;
 
 constexpr size_t SM_SMEM = 228 * 1024, CTA_SMEM = 227 * 1024, CTA_RESERVED = 1024;
@@ -1289,7 +1317,7 @@ int launch_group_kernel(const LogitRows &a, const OP &op, int teacher_k, cudaStr
     int64_t k = known.load(std::memory_order_relaxed);
     if (k < 0 || (k >> 8) != want_key) {
         cudaError_t e = cudaSuccess;
-        if (smem > 48 * 1024)
+        if (smem > 47 * 1024)  // 48 KB with the static part
             e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      STAGE + GROUP_NT / 32 * 16 * RED_DISTILL_MAX_K);
         int occ = 0;
@@ -1369,20 +1397,39 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
     if (st != RED_OK || *finished)
         return st;
     const size_t bytes = (size_t)a.len * sizeof(typename Elem<DT>::T);
+    auto fits = [&](int lanes, int vectors) { return bytes <= (size_t)lanes * vectors * 16; };
     if (bytes <= GROUP_ROW_BYTES) {
-        // lanes per row: 128 bytes each; a warp where the lists of that many
-        // rows would not leave room for a second CTA
+        // Lanes per row: up to 192 bytes each, and no more registers than they
+        // need; a warp where the lists of that many rows would not leave room for
+        // a second CTA.  us with 12 vectors per lane and with the next row's form:
+        // policy 22882 x 576 f32 25.7, 30.5; 60000 x 1300 bf16 77.8, 82.2; 60000 x
+        // 2400 116, 123; logprob 60000 x 2400 55.2, 62.0; but distill 60000 x 1300,
+        // whose lists are read by as many lanes, 142, 138 and logprob_grad 54.0, 53.8.
         const bool wide = (size_t)(GROUP_NT / 4) * 16 * teacher_k > 96 * 1024;
-        if (bytes <= 512 && !wide)
+        if (fits(4, 8) && !wide)
             return launch_group_kernel<DT, OP, 4, 8>(a, op, teacher_k, s, di);
-        if (bytes <= 1024 && !wide)
+        if (fits(8, 8) && !wide)
             return launch_group_kernel<DT, OP, 8, 8>(a, op, teacher_k, s, di);
-        if (bytes <= 2048 && !wide)
+        if (fits(16, 8) && !wide)
             return launch_group_kernel<DT, OP, 16, 8>(a, op, teacher_k, s, di);
-        if (bytes <= 4096)
+        if constexpr (OP::STATS && !OP::TEACHER)
+            if (fits(16, 12))
+                return launch_group_kernel<DT, OP, 16, 12>(a, op, teacher_k, s, di);
+        if (fits(32, 8))
             return launch_group_kernel<DT, OP, 32, 8>(a, op, teacher_k, s, di);
-        return launch_group_kernel<DT, OP, 32, 16>(a, op, teacher_k, s, di);
+        return fits(32, 12) ? launch_group_kernel<DT, OP, 32, 12>(a, op, teacher_k, s, di)
+                            : launch_group_kernel<DT, OP, 32, 16>(a, op, teacher_k, s, di);
     }
+    // Two warps per row, us against the row kernel: policy 20000 x 8000 bf16 109,
+    // 142; 30000 x 6000 bf16 128, 162; 30000 x 4104 bf16 110, 140; 800 x 5000 bf16
+    // 9.6, 11.9; logprob 30000 x 6000 bf16 63, 84.  Four warps for up to 32 KB lose
+    // (policy 16000 x 10000 bf16 130, 115), and so do four for up to 16 KB where
+    // rows are many (20000 x 4000 f32 112, 106 with two; 800 x 8000 bf16 9.8, 10.7).
+    // With 12 vectors per lane and 16: 30000 x 6000 bf16 128, 135.
+    if constexpr (OP::STATS && !OP::TEACHER)
+        if (bytes <= PAIR_ROW_BYTES)
+            return fits(64, 12) ? launch_group_kernel<DT, OP, 64, 12>(a, op, teacher_k, s, di)
+                                : launch_group_kernel<DT, OP, 64, 16>(a, op, teacher_k, s, di);
     // Threads, vectors per thread and batch, and CTAs per SM, by row bytes.  A
     // CTA is busy with one row at a time, so short rows need several CTAs to
     // cover each other's barriers, and long ones a ring that holds a row and
@@ -1393,18 +1440,16 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
     //   4096 x 30000 bf16          108        85        83        89        89        91
     //   8192 x 16384 bf16          126        96        86        87        87        93
     //   16384 x 8192 bf16          222       121       103        91        96        97
-    //   20000 x 6000 bf16          256       153       127       124       112       111
     // A teacher's list takes time that more rows at once cover: distill 4096 x
     // 16384 bf16 75, 63, 65, 68, 59, 64.  Without a gradient a row need not
     // stay: logprob 4096 x 50257 f16 62, 53, 48, 48, 50, 53; 16384 x 8192 bf16
-    // 145, 76, 58, 48, 50, 52; 32768 x 4100 bf16 267, 143, 104, 86, 76, 78.
+    // 145, 76, 58, 48, 50, 52.
     // Without statistics nothing does: logprob_grad 3001 x 32001 bf16 54, 54,
     // 55, 56, 56, 54; 32768 x 4100 bf16 250, 133, 104, 92, 86, 87.  (A loss
     // with a gradient keeps its mapping when the gradient is not asked for:
     // the mapping sets the order of the sums.)
     if constexpr (!OP::GRADIENT) {
-        return bytes > 16384 ? launch_row_kernel<DT, OP, 128, 8>(a, op, 4, teacher_k, s, di)
-                             : launch_row_kernel<DT, OP, 128, 4>(a, op, 4, teacher_k, s, di);
+        return launch_row_kernel<DT, OP, 128, 8>(a, op, 4, teacher_k, s, di);
     } else if constexpr (!OP::STATS) {
         return bytes > 24576 ? launch_row_kernel<DT, OP, 256, 4>(a, op, 2, teacher_k, s, di)
                              : launch_row_kernel<DT, OP, 128, 4>(a, op, 4, teacher_k, s, di);
@@ -1414,9 +1459,9 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
         if (bytes > 40960)
             return launch_row_kernel<DT, OP, 256, 4>(a, op, bytes > 65536 ? 2 : 3, teacher_k, s, di);
         if constexpr (!OP::TEACHER)
-            if (bytes > 12288)
-                return launch_row_kernel<DT, OP, 128, 8>(a, op, 4, teacher_k, s, di);
-        return launch_row_kernel<DT, OP, 128, 4>(a, op, bytes > 12288 ? 4 : 6, teacher_k, s, di);
+            return launch_row_kernel<DT, OP, 128, 8>(a, op, 4, teacher_k, s, di);
+        else
+            return launch_row_kernel<DT, OP, 128, 4>(a, op, bytes > 12288 ? 4 : 6, teacher_k, s, di);
     }
 }
 
