@@ -1399,21 +1399,43 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
     const size_t bytes = (size_t)a.len * sizeof(typename Elem<DT>::T);
     auto fits = [&](int lanes, int vectors) { return bytes <= (size_t)lanes * vectors * 16; };
     if (bytes <= GROUP_ROW_BYTES) {
-        // Lanes per row: up to 192 bytes each, and no more registers than they
-        // need; a warp where the lists of that many rows would not leave room for
-        // a second CTA.  us with 12 vectors per lane and with the next row's form:
-        // policy 22882 x 576 f32 25.7, 30.5; 60000 x 1300 bf16 77.8, 82.2; 60000 x
-        // 2400 116, 123; logprob 60000 x 2400 55.2, 62.0; but distill 60000 x 1300,
-        // whose lists are read by as many lanes, 142, 138 and logprob_grad 54.0, 53.8.
-        const bool wide = (size_t)(GROUP_NT / 4) * 16 * teacher_k > 96 * 1024;
-        if (fits(4, 8) && !wide)
+        // Lanes per row.  Many rows: as few as hold the row, up to 8 vectors each
+        // (what is done once per row is then done for more of them at a time), but
+        // enough for the teacher's list.  Few rows: as many as let all rows run at
+        // once.  us with 4, 8, 16 and 32 lanes (- where 4 do not hold the row):
+        //   policy       500 x 250 bf16      8.4    7.4    6.9    7.0
+        //               3600 x 250           9.2    9.0    8.1    9.2
+        //               7000 x 250          10.7    9.4    8.8   11.3
+        //              15000 x 250          11.7   11.4   13.2   17.8
+        //              30000 x 120          11.5   12.7   17.1   28.7
+        //               7000 x 500             -   10.9    9.4   11.8
+        //              30000 x 500             -   18.9   22.4   33.0
+        //   distill 30000 x 120, k = 4      13.1   15.9   22.8   37.1
+        //                        k = 16     22.6   19.9   24.3   40.6
+        //                        k = 64     68.2   38.5   34.9   49.3
+        //   logprob_grad 3600 x 500            -    3.7    2.9    2.8
+        int lanes = fits(4, 8) ? 4 : fits(8, 8) ? 8 : fits(16, 8) ? 16 : 32;
+        while (lanes < 16 && teacher_k > lanes * lanes / 2)
+            lanes *= 2;
+        while (lanes < 32 && a.rows <= (int64_t)di.sms * 3 * (GROUP_NT / (2 * lanes)))
+            lanes *= 2;
+        // room for the lists of a second CTA's rows
+        while (lanes < 32 && (size_t)(GROUP_NT / lanes) * 16 * teacher_k > 96 * 1024)
+            lanes *= 2;
+        if (lanes == 4)
             return launch_group_kernel<DT, OP, 4, 8>(a, op, teacher_k, s, di);
-        if (fits(8, 8) && !wide)
+        if (lanes == 8)
             return launch_group_kernel<DT, OP, 8, 8>(a, op, teacher_k, s, di);
-        if (fits(16, 8) && !wide)
+        if (lanes == 16)
             return launch_group_kernel<DT, OP, 16, 8>(a, op, teacher_k, s, di);
+        // Registers for 12 vectors where the row needs no more, us against the next
+        // form: policy 22882 x 576 f32 25.7, 30.5; 60000 x 1300 bf16 77.8, 82.2;
+        // 60000 x 2400 116, 123; logprob 60000 x 2400 55.2, 62.0.  Half a warp only
+        // for many rows (policy 2500 x 1056 bf16 8.9, 8.6), and not for a teacher's
+        // lists and the gradient alone (distill 60000 x 1300 142, 138; logprob_grad
+        // 54.0, 53.8).
         if constexpr (OP::STATS && !OP::TEACHER)
-            if (fits(16, 12))
+            if (fits(16, 12) && a.rows > (int64_t)di.sms * 3 * (GROUP_NT / 32))
                 return launch_group_kernel<DT, OP, 16, 12>(a, op, teacher_k, s, di);
         if (fits(32, 8))
             return launch_group_kernel<DT, OP, 32, 8>(a, op, teacher_k, s, di);
