@@ -875,29 +875,18 @@ __global__ void __launch_bounds__(TOTAL_NT) total_kernel(int64_t rows, int len, 
 
 constexpr int GROUP_NT = 256;
 
-// Whether the next row is fetched into shared memory while a row is at work
-// (before and after, us: policy 20000 x 4000 bf16 69.1, 59.6; 30000 x 1000
-// 32.8, 30.5; logprob 60000 x 1024 bf16 25.5, 23.2; 60000 x 4000 81.9, 75.9;
-// 60000 x 400 f32 21.7, 18.7; one row per group costs 0.2).  Not where the
-// lists of a teacher want the space and the row in L1 (distill 30000 x 400
-// bf16, 64 entries: 50.5, 64.5), nor for the shortest rows (policy 65536 x 120
-// bf16 16.1, 17.7: the registers are short).
-template <class OP, int G>
-constexpr bool group_staged = !OP::TEACHER && G > 4;
-
 // G lanes per row, the row in registers (NV vectors per lane): rows too short
 // for a CTA barrier each.  The shorter the row, the fewer the lanes, so that
 // what is done once per row (the loss itself, its logarithms and exponentials,
 // the reductions) is done for 32 / G rows at a time; two warps (G = 64) join
 // their statistics by way of shared memory and a barrier of their own.  The next row's entry is
-// fetched while this row is at work, and so is (`staged`) the next row.
-template <int DT, class OP, int G, int NV>
+// fetched while this row is at work, and so is (STAGED) the next row.
+template <int DT, class OP, int G, int NV, bool STAGED>
 __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(LogitRows a, OP op, int teacher_k)
 {
     using T = typename Elem<DT>::T;
     constexpr int E = VEC_ELEMS<DT>;
     constexpr int ROWS = GROUP_NT / G;  // rows of a CTA at a time
-    constexpr bool STAGED = group_staged<OP, G>;
     extern __shared__ __align__(16) unsigned char smem[];
     const int gl = threadIdx.x & (G - 1), group = threadIdx.x / G;
     uint4 *const stage = reinterpret_cast<uint4 *>(smem) + threadIdx.x;  // of this lane, GROUP_NT apart
@@ -908,7 +897,7 @@ __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(Log
     pdl_enter();
 
     const int64_t step = (int64_t)gridDim.x * ROWS;
-    // The entry of the next row, and (if staged) that row on its way into shared
+    // The entry of the next row, and (if STAGED) that row on its way into shared
     // memory: each lane fetches and reads its own vectors, so no other waits.
     RowEntry n{};
     constexpr int ENDS = (2 * (E - 1) + G - 1) / G;  // the row's ragged ends, fewer than E elements each
@@ -1304,12 +1293,12 @@ int launch_row_kernel(const LogitRows &a, const OP &op, int per_sm, int teacher_
     return cuda_fail(e != cudaSuccess ? e : cudaGetLastError(), "row kernel launch");
 }
 
-template <int DT, class OP, int G, int NV>
+template <int DT, class OP, int G, int NV, bool STAGED>
 int launch_group_kernel(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s, const DeviceInfo &di)
 {
-    const auto kernel = group_row_kernel<DT, OP, G, NV>;
+    const auto kernel = group_row_kernel<DT, OP, G, NV, STAGED>;
     constexpr int ROWS = GROUP_NT / G;
-    constexpr int STAGE = group_staged<OP, G> ? NV * GROUP_NT * 16 : 0;
+    constexpr int STAGE = STAGED ? NV * GROUP_NT * 16 : 0;
     const size_t smem = STAGE + (size_t)ROWS * 16 * teacher_k;
     // residency, kept per instance for the last device and list length asked for
     static std::atomic<int64_t> known{-1};
@@ -1385,6 +1374,26 @@ int launch_few(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s, 
     return RED_OK;
 }
 
+// Many rows per group of lanes have the next one fetched into shared memory
+// while one is at work.  us without and with, at 1.3, 2.6, 3.8 and 6 rows per
+// group: policy of 1000 bf16 logits 13.6 13.3, 23.1 22.2, 32.4 29.5, 43.5 39.7;
+// of 8000 16.5 16.4, 29.4 25.5, 38.5 33.6, 53.1 45.9; logprob of 350 5.3 5.8,
+// 8.1 8.8, 11.9 11.3, 20.2 17.9.  Not for the gradient alone, which has little
+// else to do (14592 x 4000 39.8 38.0, 43776 x 1000 29.4 29.5), not where the
+// lists of a teacher want the space and the row in L1 (distill 30000 x 400, 64
+// entries: 50.5 64.5), nor for the shortest rows, for want of registers (policy
+// 65536 x 120 16.1 17.7).
+template <int DT, class OP, int G, int NV>
+int launch_group(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s, const DeviceInfo &di)
+{
+    if constexpr (OP::STATS && !OP::TEACHER && G > 4) {
+        const int64_t resident = (int64_t)di.sms * (NV > 8 ? 2 : 3) * (GROUP_NT / G);
+        if (a.rows > 3 * resident)
+            return launch_group_kernel<DT, OP, G, NV, true>(a, op, teacher_k, s, di);
+    }
+    return launch_group_kernel<DT, OP, G, NV, false>(a, op, teacher_k, s, di);
+}
+
 // All rows, by the kernel for their number and length; *finished: what remains
 // after them is done, too.
 template <int DT, class OP>
@@ -1423,11 +1432,11 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
         while (lanes < 32 && (size_t)(GROUP_NT / lanes) * 16 * teacher_k > 96 * 1024)
             lanes *= 2;
         if (lanes == 4)
-            return launch_group_kernel<DT, OP, 4, 8>(a, op, teacher_k, s, di);
+            return launch_group<DT, OP, 4, 8>(a, op, teacher_k, s, di);
         if (lanes == 8)
-            return launch_group_kernel<DT, OP, 8, 8>(a, op, teacher_k, s, di);
+            return launch_group<DT, OP, 8, 8>(a, op, teacher_k, s, di);
         if (lanes == 16)
-            return launch_group_kernel<DT, OP, 16, 8>(a, op, teacher_k, s, di);
+            return launch_group<DT, OP, 16, 8>(a, op, teacher_k, s, di);
         // Registers for 12 vectors where the row needs no more, us against the next
         // form: policy 22882 x 576 f32 25.7, 30.5; 60000 x 1300 bf16 77.8, 82.2;
         // 60000 x 2400 116, 123; logprob 60000 x 2400 55.2, 62.0.  Half a warp only
@@ -1436,11 +1445,11 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
         // 54.0, 53.8).
         if constexpr (OP::STATS && !OP::TEACHER)
             if (fits(16, 12) && a.rows > (int64_t)di.sms * 3 * (GROUP_NT / 32))
-                return launch_group_kernel<DT, OP, 16, 12>(a, op, teacher_k, s, di);
+                return launch_group<DT, OP, 16, 12>(a, op, teacher_k, s, di);
         if (fits(32, 8))
-            return launch_group_kernel<DT, OP, 32, 8>(a, op, teacher_k, s, di);
-        return fits(32, 12) ? launch_group_kernel<DT, OP, 32, 12>(a, op, teacher_k, s, di)
-                            : launch_group_kernel<DT, OP, 32, 16>(a, op, teacher_k, s, di);
+            return launch_group<DT, OP, 32, 8>(a, op, teacher_k, s, di);
+        return fits(32, 12) ? launch_group<DT, OP, 32, 12>(a, op, teacher_k, s, di)
+                            : launch_group<DT, OP, 32, 16>(a, op, teacher_k, s, di);
     }
     // Two warps per row, us against the row kernel: policy 20000 x 8000 bf16 109,
     // 142; 30000 x 6000 bf16 128, 162; 30000 x 4104 bf16 110, 140; 800 x 5000 bf16
@@ -1450,8 +1459,8 @@ int launch_rows_of(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t
     // With 12 vectors per lane and 16: 30000 x 6000 bf16 128, 135.
     if constexpr (OP::STATS && !OP::TEACHER)
         if (bytes <= PAIR_ROW_BYTES)
-            return fits(64, 12) ? launch_group_kernel<DT, OP, 64, 12>(a, op, teacher_k, s, di)
-                                : launch_group_kernel<DT, OP, 64, 16>(a, op, teacher_k, s, di);
+            return fits(64, 12) ? launch_group<DT, OP, 64, 12>(a, op, teacher_k, s, di)
+                                : launch_group<DT, OP, 64, 16>(a, op, teacher_k, s, di);
     // Threads, vectors per thread and batch, and CTAs per SM, by row bytes.  A
     // CTA is busy with one row at a time, so short rows need several CTAs to
     // cover each other's barriers, and long ones a ring that holds a row and
