@@ -711,6 +711,45 @@ def test_many_rows_per_cta(dtype, length):
         ref.assert_grad(dgrad[part], (p - mass) * wd[:, None], (p + mass).cpu(), wd.cpu(), extra=3e-5, what="distill")
 
 
+@pytest.mark.parametrize("dtype,length,rows", [
+    (torch.bfloat16, 300, 46000), (torch.float32, 201, 46000), (torch.float16, 901, 23500), (torch.float32, 700, 15600),
+    (torch.bfloat16, 1300, 15600), (torch.bfloat16, 2001, 11700), (torch.float16, 2900, 7800),
+    (torch.float32, 1999, 7800), (torch.bfloat16, 5500, 3900), (torch.bfloat16, 8001, 3900), (torch.float32, 4003, 3900),
+    (torch.bfloat16, 150, 46000)])
+def test_many_short_rows(dtype, length, rows):
+    """More rows than run at once several times over, each length by another
+    number of lanes and registers; rows of odd starts, masked, empty or ignored."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(length)
+    x = (torch.randn((rows, length + 3), generator=g, device=DEV) * 3).to(dtype)[:, :length]
+    r = torch.arange(rows, device=DEV)
+    x[r % 50 == 3, length // 2:] = -math.inf
+    x[r % 50 == 4] = -math.inf
+    x[r % 50 == 5, :length - 1] = torch.finfo(dtype).min
+    t = torch.randint(0, length // 2, (rows,), generator=g, device=DEV)
+    t[r % 50 == 5] = length - 1
+    t[torch.rand(rows, generator=g, device=DEV) < 0.3] = -1
+    t[r == rows - 1] = 0
+    old = torch.full((rows,), -8.0, device=DEV)
+    adv = torch.randn(rows, generator=g, device=DEV)
+    logp, lse = itr.red_logprob(x, t)
+    loss, plogp, _, grad = itr.red_policy(x, t, old, adv, clip_high=1e6)
+    some = torch.cat([r[:200], r[-200:], r[::61]])
+    for part in some.split(100):
+        y = t[part].cpu()
+        p, norm = ref.log_softmax(x[part], 1.0)
+        want, live = ref.taken(p, y)
+        ref.assert_logp(logp[part], want, "logp")
+        ref.assert_logp(plogp[part], want, "policy logp")
+        ref.assert_logp(lse[part], torch.where(live, norm, torch.zeros_like(norm)), "lse")
+        a = adv[part].cpu().double()
+        ratio = (want + 8.0).exp()
+        c = torch.where(live & (ratio * a <= ratio.clamp(min=0.8) * a), -ratio * a, torch.zeros_like(a))
+        c[want == -math.inf] = 0.0
+        ref.assert_grad(grad[part], ref.target_grad(p, norm, y, live, c), p.exp(), (ratio * a).abs(), y,
+                        extra=3e-5, what="policy")
+
+
 def test_offsets_past_32_bits():
     """Rows whose elements start beyond 2^32 in the logits and in the gradient."""
     length = 65536
