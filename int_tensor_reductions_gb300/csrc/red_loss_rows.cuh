@@ -1245,14 +1245,15 @@ constexpr size_t PAIR_ROW_BYTES = 16384;
 // The few-row kernel is taken while its CTAs, with the largest cluster that
 // allows it, are at most this many per two SMs (and a thread's slice 8
 // vectors).  us, few-row kernel against the row kernel: logprob 1 x 65536 bf16
-// 2.4 / 5.9, 64 rows 4.6 / 6.3; policy 1 row 5.5 / 9.4, 30 rows 7.2 / 9.5, 64
-// rows 8.5 / 9.4, 100 rows 9.4 / 9.8, 300 x 16384 f32 9.4 / 10.5.  With 4
+// 2.4 / 5.9, 64 rows 4.6 / 6.3; policy 1 row 5.5 / 9.4, 30 rows 6.3 / 9.5, 64
+// rows 8.0 / 9.4, 100 rows 9.4 / 9.8, 300 x 16384 f32 9.4 / 10.5.  With 4
 // CTAs per SM they no longer all run at once: 152 x 65536 bf16 12.5 / 10.1.
 // Against two warps of the group kernel: logprob 20 x 8100 bf16 2.8 / 3.8, 250 x
 // 8100 4.4 / 4.5, 250 x 4200 4.1 / 3.1; preference 250 x 4200 11.8 / 12.4.
 constexpr int FEW_CTAS_PER_2_SMS = 7;
 
 constexpr size_t SM_SMEM = 228 * 1024, CTA_SMEM = 227 * 1024, CTA_RESERVED = 1024;
+constexpr size_t FEW_SMEM = CTA_SMEM - 1024;  // beside the few-row kernel's static part
 
 template <int DT, class OP, int NT, int U>
 int launch_row_kernel(const LogitRows &a, const OP &op, int per_sm, int teacher_k, cudaStream_t s, const DeviceInfo &di)
@@ -1326,15 +1327,31 @@ int launch_group_kernel(const LogitRows &a, const OP &op, int teacher_k, cudaStr
 }
 
 template <int DT, class OP, int NV>
-int launch_few_kernel(const LogitRows &a, const OP &op, int cluster, int teacher_k, cudaStream_t s)
+int launch_few_kernel(const LogitRows &a, const OP &op, int cluster, int teacher_k, cudaStream_t s,
+                      const DeviceInfo &di)
 {
     Workspace ws;
     const int st = get_workspace(&ws);
     if (st != RED_OK)
         return st;
-    const size_t smem = (size_t)4 * 4 * teacher_k;
-    const cudaError_t e = launch_pdl_smem(few_row_kernel<DT, OP, NV>, (unsigned)(a.rows * cluster), FEW_NT, smem,
-                                          (unsigned)cluster, s, a, op, teacher_k, ws.tick);
+    const auto kernel = few_row_kernel<DT, OP, NV>;
+    static std::atomic<uint64_t> ready{0};  // a bit per device
+    if (!(ready.load(std::memory_order_relaxed) >> di.dev & 1)) {
+        const cudaError_t e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)FEW_SMEM);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "few-row kernel: shared memory");
+        ready.fetch_or(uint64_t(1) << di.dev, std::memory_order_relaxed);
+    }
+    // Shared memory that leaves room on an SM for its share of the CTAs and no
+    // more: left to themselves clusters crowd some SMs and leave others idle.  us
+    // without and with: policy 64 x 65536 bf16 8.8, 7.9; 30 x 65536 7.4, 6.3; 200 x
+    // 32001 9.8, 8.8; logprob_grad 200 x 32000 4.3, 3.8; 120 x 50257 unchanged.
+    const int64_t ctas = a.rows * cluster, share = (ctas + di.sms - 1) / di.sms;
+    const size_t list = (size_t)4 * 4 * teacher_k, part = SM_SMEM / share - 2 * CTA_RESERVED;
+    const size_t smem = list > part ? list : (part < FEW_SMEM ? part : FEW_SMEM);
+    const cudaError_t e = launch_pdl_smem(kernel, (unsigned)ctas, FEW_NT, smem, (unsigned)cluster, s, a, op,
+                                          teacher_k, ws.tick);
     count_launches(1);
     return cuda_fail(e != cudaSuccess ? e : cudaGetLastError(), "few-row kernel launch");
 }
@@ -1368,8 +1385,8 @@ int launch_few(const LogitRows &a, const OP &op, int teacher_k, cudaStream_t s, 
         if (2 * a.rows * cluster > FEW_CTAS_PER_2_SMS * di.sms || slice > 8 * FEW_NT)
             continue;
         *taken = true;
-        return slice <= 4 * FEW_NT ? launch_few_kernel<DT, OP, 4>(a, op, cluster, teacher_k, s)
-                                   : launch_few_kernel<DT, OP, 8>(a, op, cluster, teacher_k, s);
+        return slice <= 4 * FEW_NT ? launch_few_kernel<DT, OP, 4>(a, op, cluster, teacher_k, s, di)
+                                   : launch_few_kernel<DT, OP, 8>(a, op, cluster, teacher_k, s, di);
     }
     return RED_OK;
 }
