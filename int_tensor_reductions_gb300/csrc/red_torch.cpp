@@ -11,6 +11,8 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <array>
+
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_strided.h>
@@ -117,6 +119,28 @@ struct Logits {
     at::Tensor floats(int64_t n) const { return at::empty({n}, x.options().dtype(at::kFloat)); }
 };
 
+// Vectors of floats in one allocation, each from a 16-byte boundary on: an
+// allocation is a microsecond of the host's time.
+template <size_t N>
+std::array<at::Tensor, N> float_vectors(const Logits &l, const int64_t (&sizes)[N])
+{
+    int64_t total = 0;
+    for (const int64_t n : sizes)
+        total += (n + 3) / 4 * 4;
+    const at::Tensor whole = l.floats(total);
+    std::array<at::Tensor, N> parts;
+    int64_t begin = 0;
+    for (size_t i = 0; i < N; ++i) {
+        auto part = c10::make_intrusive<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(whole.storage()),
+                                                         whole.key_set(), whole.dtype());
+        part->set_storage_offset(begin);
+        part->set_sizes_contiguous(sizes[i]);
+        parts[i] = at::Tensor(std::move(part));
+        begin += (sizes[i] + 3) / 4 * 4;
+    }
+    return parts;
+}
+
 float *data(const at::Tensor &t) { return static_cast<float *>(t.data_ptr()); }
 
 // The gradient: None for a new tensor of x's row stride, False for none, or a
@@ -206,8 +230,15 @@ PyObject *logprob(PyObject *, PyObject *const *a, Py_ssize_t n)
         const Logits l(a[0]);
         const int64_t *target = l.vector<int64_t>(a[1], "target", l.rows);
         const float *given = l.vector<float>(a[3], "out", l.rows), *given_lse = l.vector<float>(a[4], "lse", l.rows);
-        const at::Tensor out = given ? tensor(a[3], "out") : l.floats(l.rows);
-        const at::Tensor lse = given_lse ? tensor(a[4], "lse") : l.floats(l.rows);
+        at::Tensor out, lse;
+        if (!given && !given_lse) {
+            auto made = float_vectors(l, {l.rows, l.rows});
+            out = std::move(made[0]);
+            lse = std::move(made[1]);
+        } else {
+            out = given ? tensor(a[3], "out") : l.floats(l.rows);
+            lse = given_lse ? tensor(a[4], "lse") : l.floats(l.rows);
+        }
         const c10::cuda::OptionalCUDAGuard guard(l.x.device());
         RETURN_IF_REFUSED(red_logprob(l.dtype, l.x.data_ptr(), l.rows, l.len, l.ld, (float)number(a[2]), target,
                                       data(out), data(lse), stream_of(a[5], l)));
@@ -247,7 +278,7 @@ PyObject *distill(PyObject *, PyObject *const *a, Py_ssize_t n)
         const int64_t *id = l.vector<int64_t>(a[1], "ids", l.rows * k);
         const float *lse = l.vector<float>(a[3], "lse", l.rows), *weight = l.vector<float>(a[4], "weight", l.rows);
         const Gradient g(a[7], l, "grad");
-        const at::Tensor loss = l.floats(l.rows), stats = l.floats(2);
+        const auto [loss, stats] = float_vectors(l, {l.rows, 2});
         const c10::cuda::OptionalCUDAGuard guard(l.x.device());
         RETURN_IF_REFUSED(red_distill(l.dtype, l.x.data_ptr(), l.rows, l.len, l.ld, (float)number(a[5]), k, id, vcode,
                                       vals.data_ptr(), lse, weight, (float)number(a[6]), data(loss), data(stats),
@@ -265,7 +296,7 @@ PyObject *policy(PyObject *, PyObject *const *a, Py_ssize_t n)
         const float *old_logp = l.vector<float>(a[2], "old_logp", l.rows), *adv = l.vector<float>(a[3], "adv", l.rows);
         const float *ref = l.vector<float>(a[4], "ref_logp", l.rows), *weight = l.vector<float>(a[5], "weight", l.rows);
         const Gradient g(a[11], l, "grad");
-        const at::Tensor loss = l.floats(l.rows), logp = l.floats(l.rows), stats = l.floats(4);
+        const auto [loss, logp, stats] = float_vectors(l, {l.rows, l.rows, 4});
         const c10::cuda::OptionalCUDAGuard guard(l.x.device());
         RETURN_IF_REFUSED(red_policy(l.dtype, l.x.data_ptr(), l.rows, l.len, l.ld, (float)number(a[9]), target,
                                      old_logp, ref, adv, weight, (float)number(a[6]), (float)number(a[7]),
@@ -288,7 +319,7 @@ PyObject *preference(PyObject *, PyObject *const *a, Py_ssize_t n)
         const int64_t *offsets = l.vector<int64_t>(a[2], "offsets", entries);
         const float *ref = l.vector<float>(a[3], "ref_logp", 2 * pairs), *weight = l.vector<float>(a[4], "weight", pairs);
         const Gradient g(a[12], l, "grad");
-        const at::Tensor loss = l.floats(pairs), seq = l.floats(2 * pairs), stats = l.floats(4);
+        const auto [loss, seq, stats] = float_vectors(l, {pairs, 2 * pairs, 4});
         // (freed on return: the allocator keeps it for this stream's later work,
         // and the wrapper holds it for any other stream)
         const at::Tensor work = l.floats(3 * l.rows + pairs);
