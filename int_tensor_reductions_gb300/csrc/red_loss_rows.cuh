@@ -491,10 +491,14 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
     // their gradient pass; the statistics.
     auto give_row = [&](int i, const RowEntry &e, float mass) {
         bar_sync(summed(i), NT + 32);
-        if (!a.dx)  // (the statistics of the next row go to the other buffer)
+        // Copies of the NW parts throughout the warp, joined in log2(NW) levels.
+        // They are read before `given`: the consumers write the same buffer for
+        // row i + 2, and that only waits for row i + 1 to be given, which for the
+        // distillation another warp does.
+        const SoftStat part = sh.part[i % 2][lane % NW];
+        if (!a.dx)
             bar_sync(given(i), GIVEN);
-        // copies of the NW parts throughout the warp, joined in log2(NW) levels
-        SoftStat w = soft_warp<NW>(sh.part[i % 2][lane % NW], s2);
+        SoftStat w = soft_warp<NW>(part, s2);
         if (*failed)
             w.l = __int_as_float(0x7fc00000);
         const RowStat t = row_stat(a, w);
