@@ -86,19 +86,31 @@ constexpr float FAR = 16777216.0f;  // 2^24: the largest |M| of the multiply-add
 // The multiply-add form does for the maximum m (m * s2 = m2; not for a NaN).
 __device__ __forceinline__ bool is_near(float m2) { return fabsf(m2) <= FAR; }
 
-// Factor of a sum under the maximum `from` when the maximum becomes `to`.
-__device__ __forceinline__ float soft_factor(float from, float to, float s2)
+// Factor of a sum under the maximum `from` when the maximum becomes `to`; f2, t2:
+// their products with s2, each rounded by itself (__fmul_rn).  The terms under a
+// maximum are relative to its rounded product, so the exponent is the
+// difference of those: with from * s2 - t2 in one multiply-add each partial sum
+// would be off by 2^lo of its own maximum (log-probabilities near logits of
+// 10^4 by 1.9e-4; 1e-6 as it is).  A far maximum is its product itself, unrounded.
+__device__ __forceinline__ float soft_factor(float from, float f2, float to, float t2, float s2)
 {
-    if (from == to)
-        return 1.0f;
-    const float m2 = to * s2;
-    return ex2(is_near(m2) ? from * s2 - m2 : (from - to) * s2);
+    float e = f2 - t2;
+    if (!(fmaxf(fabsf(f2), fabsf(t2)) <= FAR)) {  // far, or -inf
+        if (is_near(t2))
+            e = fmaf(from, s2, -t2);
+        else if (is_near(f2))
+            e = fmaf(-to, s2, f2);
+        else
+            e = from == to ? 0.0f : (from - to) * s2;
+    }
+    return ex2(e);
 }
 
 __device__ __forceinline__ SoftStat soft_join(SoftStat a, SoftStat b, float s2)
 {
-    const float m = fmaxf(a.m, b.m);
-    return SoftStat{m, a.l * soft_factor(a.m, m, s2) + b.l * soft_factor(b.m, m, s2)};
+    const float m = fmaxf(a.m, b.m), m2 = __fmul_rn(m, s2);
+    return SoftStat{m, a.l * soft_factor(a.m, __fmul_rn(a.m, s2), m, m2, s2) +
+                           b.l * soft_factor(b.m, __fmul_rn(b.m, s2), m, m2, s2)};
 }
 
 // The largest of the lanes' values (no NaN), by the integer reduction: the
@@ -118,7 +130,7 @@ template <int W = 32>
 __device__ __forceinline__ SoftStat soft_warp(SoftStat a, float s2)
 {
     const float m = warp_max(a.m);
-    float l = a.l * soft_factor(a.m, m, s2);
+    float l = a.l * soft_factor(a.m, __fmul_rn(a.m, s2), m, __fmul_rn(m, s2), s2);
 #pragma unroll
     for (int off = W / 2; off > 0; off >>= 1)
         l += __shfl_xor_sync(0xffffffffu, l, off);

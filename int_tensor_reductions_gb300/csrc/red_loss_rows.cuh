@@ -135,26 +135,28 @@ __device__ __forceinline__ uint4 vec_pack(const f32x2 (&f)[VEC_ELEMS<DT> / 2])
 
 // Running statistics of one thread; the sum in two lanes.
 struct SoftRun {
-    float m;
+    float m, m2;  // m2 = m * s2, rounded
     f32x2 l;
 
-    __device__ __forceinline__ void init()
+    __device__ __forceinline__ void init(float top, float s2)
     {
-        m = NEG_INF;
+        m = top;
+        m2 = __fmul_rn(top, s2);
         l = pack2(0.0f, 0.0f);
     }
     __device__ __forceinline__ void raise(float to, float s2)
     {
         to = fmaxf(m, to);
-        const float f = soft_factor(m, to, s2);
+        const float t2 = __fmul_rn(to, s2);
+        const float f = soft_factor(m, m2, to, t2, s2);
         l = mul2(l, pack2(f, f));
         m = to;
+        m2 = t2;
     }
     // n vectors, none of whose elements is above m
     template <int DT, int N>
     __device__ __forceinline__ void add(const uint4 (&v)[N], float s2)
     {
-        const float m2 = m * s2;
         if (is_near(m2)) {
             const f32x2 a = pack2(s2, s2), b = pack2(-m2, -m2);
 #pragma unroll
@@ -173,20 +175,20 @@ struct SoftRun {
         for (int i = 0; i < VEC_ELEMS<DT> / 2; ++i)
             l = add2(l, exp2_2(fma2(vec_pair<DT>(v, i), a, b)));
     }
-    __device__ __forceinline__ void add(float x, float s2) { l = add2(l, pack2(ex2(term(x, m, s2)), 0.0f)); }
+    __device__ __forceinline__ void add(float x, float s2) { l = add2(l, pack2(ex2(term(x, m, m2, s2)), 0.0f)); }
     // exponent of one logit under the maximum m, near or far
-    static __device__ __forceinline__ float term(float x, float m, float s2)
+    static __device__ __forceinline__ float term(float x, float m, float m2, float s2)
     {
-        const float m2 = m * s2;
         // (nothing finite yet: -inf is no term, and a NaN is one)
         return is_near(m2) ? fmaf(x, s2, -m2) : (m == NEG_INF ? x : (x - m) * s2);
     }
     template <int DT>
     static __device__ __noinline__ f32x2 far_sum(uint4 v, float m, float s2, f32x2 l)
     {
+        const float m2 = __fmul_rn(m, s2);
         for (int i = 0; i < VEC_ELEMS<DT> / 2; ++i) {
             const float2 x = unpack2(vec_pair<DT>(v, i));
-            l = add2(l, pack2(ex2(term(x.x, m, s2)), ex2(term(x.y, m, s2))));
+            l = add2(l, pack2(ex2(term(x.x, m, m2, s2)), ex2(term(x.y, m, m2, s2))));
         }
         return l;
     }
@@ -690,7 +692,7 @@ row_kernel(LogitRows a, OP op, unsigned *next, int slots, int group, int ahead, 
             const int first = cslot;
             if constexpr (OP::STATS) {
                 SoftRun run;
-                run.init();
+                run.init(NEG_INF, s2);
                 for (int b = 0; b < nb; ++b) {
                     const uint4 *src = ring + cslot * U * NT + tid;
                     const int left = nvec - b * U * NT - tid;
@@ -1011,10 +1013,9 @@ __global__ void __launch_bounds__(GROUP_NT, NV > 8 ? 2 : 3) group_row_kernel(Log
             }
             top = G > 32 ? join_max(group_max<32>(top)) : group_max<G>(top);
             SoftRun run;
-            run.init();
-            run.m = top;
-            if (live && is_near(top * s2)) {
-                const f32x2 sa = pack2(s2, s2), sb = pack2(-top * s2, -top * s2);
+            run.init(top, s2);
+            if (live && is_near(run.m2)) {
+                const f32x2 sa = pack2(s2, s2), sb = pack2(-run.m2, -run.m2);
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
                     if (i * G + gl < nvec)
@@ -1137,13 +1138,12 @@ __global__ void __launch_bounds__(FEW_NT) few_row_kernel(LogitRows a, OP op, int
         }
         if constexpr (OP::STATS) {
             SoftRun run;
-            run.init();
             float top = edge >= 0 ? fmaxf(xe, NEG_INF) : NEG_INF;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (i * FEW_NT + tid < n)
                     top = fmaxf(top, vec_max<DT>(v[i]));
-            run.m = top;
+            run.init(top, s2);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (i * FEW_NT + tid < n) {
