@@ -372,7 +372,8 @@ int red_logprob(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld,
  * red_logprob_grad -- backward of red_logprob: for the gradient dlogp[r] of
  * some loss by logp[r], dx[r, j] = scale * dlogp[r] * ([j == target[r]] - p_j)
  * with p_j = e^(z_j - lse[r]), lse as red_logprob left it.  A row whose dlogp
- * is 0 has a gradient of 0, whatever its logits hold.
+ * is 0 has a gradient of 0, whatever its logits hold.  lse is one float, and
+ * its rounding is in every p_j of the row: up to 6e-8 * |lse[r]|, relative.
  */
 int red_logprob_grad(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld, float scale,
                      const int64_t *target, const float *lse, const float *dlogp, void *dx, int64_t ldd,
@@ -443,7 +444,8 @@ enum red_preference_kind {
  *            weight * [u > 0] and weight.
  *   work     3 * rows + pairs floats of scratch: the rows' logp, lse and dlogp
  *            (as red_logprob_grad takes them) and the pairs' u afterwards.
- *   dx       may be NULL.
+ *   dx       may be NULL.  It is formed from the rows' maxima and sums, not
+ *            from their lse, whose rounding is therefore not in it.
  */
 int red_preference(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld, float scale,
                    const int64_t *target, const int64_t *offsets, int64_t pairs, const float *ref_logp,

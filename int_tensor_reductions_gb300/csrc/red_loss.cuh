@@ -288,6 +288,8 @@ struct LogprobArgs {
     static constexpr int TOTALS = 0;
     const int64_t *target;
     float *logp, *lse;
+    SoftStat *stat;  // statistics of rows [0, stat_rows) that take part, for their gradient
+    int64_t stat_rows;
 
     __device__ void load(int64_t r, RowEntry &e) const
     {
@@ -311,6 +313,8 @@ struct LogprobArgs {
     {
         logp[e.r] = t.empty ? NEG_INF : (Elem<DT>::widen(e.xy) - t.m) * a.scale - t.ln;
         lse[e.r] = t.empty ? NEG_INF : fmaf(a.scale, t.m, t.ln);
+        if (e.r < stat_rows)
+            stat[e.r] = SoftStat{t.m, t.l};
     }
 };
 
@@ -320,6 +324,7 @@ struct LogprobGradArgs {
     static constexpr int TOTALS = 0;
     const int64_t *target;
     const float *lse, *dlogp;
+    const SoftStat *stat;  // the rows' statistics; NULL: lse alone is known
     int64_t rows;
 
     // From the last row to the first: the logits that the forward pass read
@@ -331,6 +336,11 @@ struct LogprobGradArgs {
         e.target = target[r];
         e.w = dlogp[r];
         e.f[0] = lse[r];
+        if (stat) {
+            const SoftStat s = stat[r];
+            e.f[1] = s.m;
+            e.f[2] = s.l;
+        }
     }
     __device__ void settle(const LogitRows &a, RowEntry &e) const
     {
@@ -339,6 +349,8 @@ struct LogprobGradArgs {
     template <int DT>
     __device__ void touch(const LogitRows &, RowEntry &) const {}
     __device__ void skip(int64_t) const {}
+    // From the statistics as every loss forms it.  From lse, which its own
+    // rounding leaves off by up to 2^-24 |lse|, and each probability by as much:
     // p_j = 2^(x_j * s2 - lse * s2 / scale), the same rounding of s2 in both
     // products; what the second one rounds away goes into the factor.  Far
     // from zero: 2^((scale x_j - lse) log2 e), the difference in one rounding.
@@ -346,6 +358,14 @@ struct LogprobGradArgs {
     __device__ RowGrad grad(const LogitRows &a, const RowEntry &e, const RowStat &, float) const
     {
         const float n = e.f[0], c = e.w * a.scale;
+        if (stat) {
+            RowStat t{};
+            t.m = e.f[1];
+            t.l = e.f[2];
+            t.m2 = t.m * a.s2;
+            t.far = !is_near(t.m2);
+            return grad_of_target(a, t, (int)e.target, c);
+        }
         const float hi = n * a.r_hi, lo = fmaf(n, a.r_lo, fmaf(n, a.r_hi, -hi));
         RowGrad g;
         g.far = !is_near(hi);

@@ -73,7 +73,7 @@ int red_logprob(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld,
         return fail(RED_EINVAL, "red_logprob: target is NULL or not 8-byte aligned");
     if (bad_ptr(logp, 4) || bad_ptr(lse, 4))
         return fail(RED_EINVAL, "red_logprob: logp or lse is NULL or not 4-byte aligned");
-    return launch_logprob(dtype, a, LogprobArgs{target, logp, lse}, reinterpret_cast<cudaStream_t>(stream));
+    return launch_logprob(dtype, a, LogprobArgs{target, logp, lse, nullptr, 0}, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int red_logprob_grad(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld, float scale,
@@ -90,7 +90,7 @@ int red_logprob_grad(int dtype, const void *x, int64_t rows, int64_t len, int64_
         return fail(RED_EINVAL, "red_logprob_grad: target is NULL or not 8-byte aligned");
     if (bad_ptr(lse, 4) || bad_ptr(dlogp, 4))
         return fail(RED_EINVAL, "red_logprob_grad: lse or dlogp is NULL or not 4-byte aligned");
-    return launch_logprob_grad(dtype, a, LogprobGradArgs{target, lse, dlogp, rows}, reinterpret_cast<cudaStream_t>(stream));
+    return launch_logprob_grad(dtype, a, LogprobGradArgs{target, lse, dlogp, nullptr, rows}, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int red_distill(int dtype, const void *x, int64_t rows, int64_t len, int64_t ld, float scale, int64_t k,

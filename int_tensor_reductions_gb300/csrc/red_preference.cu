@@ -247,6 +247,19 @@ int launch_forward(const LogitRows &a, const PreferenceForward &f, cudaStream_t 
 int launch_preference(int dtype, const LogitRows &a, const PreferenceArgs &p, cudaStream_t s)
 {
     int st = RED_OK;
+    const bool grad = a.dx && a.rows > 0;
+    Workspace ws;
+    if (grad || p.pairs > 0)
+        st = get_workspace(&ws);
+    if (st != RED_OK)
+        return st;
+    // The gradient takes the rows' statistics as the forward pass left them in
+    // the workspace: lse in 32 bits would put the probabilities off, by 3e-5 at
+    // |lse| = 1000, and make each of them 1 in a row of nothing but the type's
+    // lowest value.
+    SoftStat *const stat = static_cast<SoftStat *>(ws.part);
+    const int64_t room = WS_PART_BYTES / sizeof(SoftStat);
+    const int64_t kept = !grad ? 0 : (a.rows < room ? a.rows : room);
     if (p.pairs == 0) {  // nothing to compare: no loss, a zero gradient
         cudaError_t e = cudaMemsetAsync(p.stats, 0, 4 * sizeof(float), s);
         if (e == cudaSuccess && a.rows > 0)
@@ -254,7 +267,7 @@ int launch_preference(int dtype, const LogitRows &a, const PreferenceArgs &p, cu
         if (e != cudaSuccess)
             return cuda_fail(e, "red_preference: cudaMemsetAsync");
     } else {
-        const LogprobArgs forward{p.target, p.logp, p.lse};
+        const LogprobArgs forward{p.target, p.logp, p.lse, stat, kept};
         bool taken = false;
         if (a.rows > 0 && p.pairs <= TAIL_PAIRS) {
             LogitRows rows = a;
@@ -271,9 +284,7 @@ int launch_preference(int dtype, const LogitRows &a, const PreferenceArgs &p, cu
         if (st != RED_OK)
             return st;
         if (!taken) {
-            Workspace ws;
-            st = get_workspace(&ws);
-            if (st == RED_OK && a.rows > 0)
+            if (a.rows > 0)
                 st = launch_logprob(dtype, a, forward, s);
             if (st != RED_OK)
                 return st;
@@ -283,9 +294,22 @@ int launch_preference(int dtype, const LogitRows &a, const PreferenceArgs &p, cu
             st = cuda_fail(e != cudaSuccess ? e : cudaGetLastError(), "red_preference launch");
         }
     }
-    if (st != RED_OK || !a.dx || a.rows == 0)
-        return st;
-    return launch_logprob_grad(dtype, a, LogprobGradArgs{p.target, p.lse, p.dlogp, a.rows}, s);
+    // Rows beyond the workspace's room (2^21) have their statistics formed again,
+    // as many at a time.
+    for (int64_t lo = 0; grad && st == RED_OK && lo < a.rows; lo += room) {
+        const int64_t size = dtype == RED_F32 ? 4 : 2;
+        LogitRows part = a;
+        part.rows = a.rows - lo < room ? a.rows - lo : room;
+        part.x = static_cast<const char *>(a.x) + lo * a.ld * size;
+        part.dx = static_cast<char *>(a.dx) + lo * a.ldd * size;
+        const int64_t *const target = p.target + lo;
+        if (lo > 0)
+            st = launch_logprob(dtype, part, LogprobArgs{target, p.logp + lo, p.lse + lo, stat, part.rows}, s);
+        if (st == RED_OK)
+            st = launch_logprob_grad(dtype, part,
+                                     LogprobGradArgs{target, p.lse + lo, p.dlogp + lo, stat, part.rows}, s);
+    }
+    return st;
 }
 
 }  // namespace red

@@ -100,3 +100,124 @@ def test_logits_far_from_zero(rows, length, dtype, offset, scale):
     assert bool(((loss.cpu().double() - (-math.log(3.0) - at.mean(1))).abs() <= 1.2e-5 + 1e-6 * size).all())
     mass = torch.zeros_like(p).scatter_add_(1, ids.cpu(), torch.full((rows, 3), 1 / 3, dtype=torch.float64))
     ref.assert_grad(grad, (p - mass) * scale, p + mass, c, extra=3e-5, what="distill")
+
+
+def check_preference(x, t, offsets, w=None, kind="sigmoid", beta=0.5, margin=0.0, eps=0.0, average=False, scale=1.0,
+                     gs=1.0, rf=None, only=None):
+    """red_preference against 64 bits, each row's gradient by the tolerance of
+    its own pair; ``only``: the rows whose gradient is compared."""
+    rows, pairs = x.shape[0], offsets.numel() // 2
+    w = torch.ones(pairs) if w is None else w
+    rf = torch.zeros(2 * pairs) if rf is None else rf
+    loss, seq, stats, grad = itr.red_preference(
+        x, t, offsets.to(DEV), ref_logp=rf.to(DEV), weight=w.to(DEV), kind=kind, beta=beta, margin=margin, smoothing=eps,
+        average=average, scale=scale, grad_scale=gs)
+    lp, lse = log_softmax(x, scale)
+    tc = t.cpu()
+    logp, live = ref.taken(lp, tc)
+    live = live & (lse != -math.inf)
+    of = torch.bucketize(torch.arange(rows), offsets[1:], right=True)
+    inside = (torch.arange(rows) >= offsets[0]) & (of < 2 * pairs)
+    live, of = live & inside, of.clamp(max=2 * pairs - 1)
+    zero = torch.zeros(2 * pairs, dtype=torch.float64)
+    count = zero.index_add(0, of, live.double()).clamp(min=1.0) if average else zero + 1.0
+    sums = zero.index_add(0, of[live], logp[live]) / count
+    # the sums' errors: 1.2e-5 and 4e-7 |logp| per token
+    slack = zero.index_add(0, of[live], 1.2e-5 + 4e-7 * logp[live].abs()) / count
+    assert bool(((seq.cpu().double() - sums).abs() <= slack + 2e-7 * sums.abs()).all())
+    gain = sums - rf.double()
+    u = beta * (gain[:pairs] - gain[pairs:]) - margin
+    want, du = ref.pair_loss(u, kind, beta, eps)
+    du_u = beta * (slack[:pairs] + slack[pairs:]) + 2e-7 * (u.abs() + beta * gain.abs().max()) + 1e-7
+    curve = {"sigmoid": 0.25, "hinge": 0.0, "squared": 2.0 / beta ** 2}[kind] * du_u
+    if kind == "hinge":
+        curve = ((u - 1).abs() <= du_u).double()     # either side of the kink
+    wd = w.double()
+    assert bool(((loss.cpu().double() - want * wd).abs() <= wd * (du_u * (du.abs() + curve) + 2e-6 * want.abs() + 1e-7)).all())
+    f = wd * beta * gs * scale
+    c, dc = torch.cat([du * f, -du * f]) / count, torch.cat([curve * f, curve * f]) / count + 0.0
+    c, dc = c[of], dc[of] + 2e-6 * c[of].abs()
+    c, dc = torch.where(live, c, torch.zeros_like(c)), torch.where(live, dc, torch.zeros_like(dc))
+    only = torch.arange(rows) if only is None else only
+    p = lp[only].exp()
+    g = ref.target_grad(lp[only], lse[only], tc[only], live[only], c[only])
+    got = grad[only.to(DEV)].cpu().double()
+    tol = p.nan_to_num(nan=0.0) * (c[only].abs() * ref.PROB_REL + dc[only])[:, None]
+    tol += ref.ROUND[x.dtype] * g.abs() + ref.TINY[x.dtype]
+    at = tc[only].clamp(0, x.shape[1] - 1)
+    tol[torch.arange(only.numel()), at] += 1e-6 * c[only].abs() + dc[only]
+    bad = ~((got - g).abs() <= tol)
+    assert not bad.any(), (f"{int(bad.sum())} off, first at {bad.nonzero()[0].tolist()}: {got[bad][0]} for {g[bad][0]} "
+                           f"+- {tol[bad][0]}")
+    return loss, seq, stats, grad
+
+
+@pytest.mark.parametrize("rows,length", ROWS)
+@pytest.mark.parametrize("dtype,offset,scale", FARAWAY)
+def test_preference_far_from_zero(rows, length, dtype, offset, scale):
+    """The gradient's probabilities do not suffer from the size of the row's
+    log-sum-exp."""
+    g = device_gen(length + rows)
+    width = 3.0 / scale if scale > 1 else 3.0
+    x = (torch.randn((rows, length), generator=g, device=DEV) * width + offset).to(dtype)
+    t = torch.randint(0, length, (rows,), generator=g, device=DEV)
+    pairs = min(rows // 2, 40)      # the few-row kernel's last CTA does few pairs, a kernel of their own more
+    off = torch.linspace(0, rows, 2 * pairs + 1).round().long()
+    # the squared loss pulls even where the policy has decided
+    check_preference(x, t, off, kind="squared", average=True, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", ref.DTYPES)
+@pytest.mark.parametrize("copies,length", [(1, 700), (60, 700), (1, 9000), (60, 9000), (1, 40000), (32, 40000)])
+def test_preference_of_extreme_rows(copies, length, dtype):
+    """Rows whose masks leave little or nothing, and rows of nothing but the
+    type's lowest or highest value, which are uniform."""
+    low = torch.finfo(dtype).min
+    rows = 10 * copies
+    g = device_gen(length)
+    x = (torch.randn((rows, length), generator=g, device=DEV) * 3).to(dtype)
+    t = torch.full((rows,), 1)
+    k = torch.arange(rows) % 10
+    x[k == 0, length // 2:] = -math.inf
+    x[k == 1, :length - 2] = -math.inf
+    t[k == 1] = length - 1
+    x[k == 2] = -math.inf               # nothing left
+    x[k == 3] = low                     # uniform
+    x[k == 4, 2:] = low
+    x[k == 5, :length - 2] = low        # a prefix far below the rest
+    t[k == 5] = length - 2
+    x[k == 6] = -low                    # uniform at the other end
+    t[k == 7] = -100
+    x[k == 7] = math.nan
+    pairs = rows // 5
+    off = torch.linspace(0, rows, 2 * pairs + 1).round().long()
+    check_preference(x, t.to(DEV), off, kind="squared", average=True, scale=1.0, gs=2.0)
+
+
+@pytest.mark.parametrize("kind,average", [("sigmoid", False), ("sigmoid", True), ("hinge", False), ("squared", True)])
+@pytest.mark.parametrize("rows,length,pairs", [(64, 4099, 8), (900, 257, 200), (600, 9001, 50)])
+def test_preference_by_its_own_pair(rows, length, pairs, kind, average):
+    """Each pair's rows within the tolerance of that pair, saturated ones among
+    them."""
+    g = device_gen(rows)
+    x = (torch.randn((rows, length), generator=g, device=DEV) * 3).to(torch.float32)
+    t = torch.randint(0, length, (rows,), generator=g, device=DEV)
+    t[torch.rand(rows, generator=g, device=DEV) < 0.3] = -100
+    off = torch.randint(0, rows + 1, (2 * pairs + 1,), generator=g, device=DEV).cpu().sort().values
+    w = torch.rand(pairs) + 0.05
+    w[::7] = 0.0
+    rf = torch.randn(2 * pairs) * 4
+    rf[0] += 60.0       # a pair of no doubt
+    check_preference(x, t, off, w=w, kind=kind, beta=0.6, margin=0.1, eps=0.1 if kind == "sigmoid" else 0.0,
+                     average=average, scale=0.9, gs=3.0, rf=rf)
+
+
+def test_preference_of_many_rows():
+    """More rows than the workspace has room for their statistics, at an offset."""
+    rows, length = (1 << 21) + 1003, 6
+    g = device_gen(3)
+    x = torch.randn((rows, length), generator=g, device=DEV) * 2 + 3e4
+    t = torch.randint(0, length, (rows,), generator=g, device=DEV)
+    off = torch.tensor([5, 1000000, rows - 3])
+    only = torch.cat([torch.arange(2000), torch.arange((1 << 21) - 700, rows)])
+    check_preference(x, t, off, kind="hinge", average=True, only=only)
