@@ -120,8 +120,10 @@ enum red_knob {
     RED_KNOB_RAGGED_STAGED = 5, /* red_rows_ragged mapping: 1 CTA-staged tiles, 2 direct (lanes per row) */
     RED_KNOB_ROWS_ALIGNED = 6, /* red_rows on rows of whole 32-byte blocks: 2 = the general row kernel
                                   instead of the aligned one (1 and 0: automatic) */
-    RED_KNOB_COLS_LANES = 7    /* red_cols / red_colprod: at most this many lanes per row of a column tile
+    RED_KNOB_COLS_LANES = 7,   /* red_cols / red_colprod: at most this many lanes per row of a column tile
                                   (1, 2, 4, 8, 16 or 32) */
+    RED_KNOB_LOSS_TRIES = 8    /* losses over logits: tries in vain after which a wait gives up (0: 20 s),
+                                  to test what it gives then: NaN in what its CTA has not written yet */
 };
 
 /*

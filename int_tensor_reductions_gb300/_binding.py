@@ -14,6 +14,7 @@ RED_KNOB_ROWS_GROUP, RED_KNOB_RAGGED_GROUP, RED_KNOB_COLPROD_SPLITS, RED_KNOB_FU
 RED_KNOB_RAGGED_STAGED = 5
 RED_KNOB_ROWS_ALIGNED = 6
 RED_KNOB_COLS_LANES = 7
+RED_KNOB_LOSS_TRIES = 8
 RED_PREF_SIGMOID, RED_PREF_HINGE, RED_PREF_SQUARED = 0, 1, 2
 RED_DISTILL_MAX_K = 1024
 

@@ -363,6 +363,10 @@ int red_set_knob(int k, int value)
         if (!(value == 0 || value == 1 || value == 2 || value == 4 || value == 8 || value == 16 || value == 32))
             return fail(RED_EINVAL, "red_set_knob: lanes per row must be 0 or a power of two <= 32");
         break;
+    case RED_KNOB_LOSS_TRIES:
+        if (value < 0)
+            return fail(RED_EINVAL, "red_set_knob: tries of a wait must be >= 0");
+        break;
     default:
         return fail(RED_EINVAL, "red_set_knob: unknown knob %d", k);
     }
@@ -372,7 +376,7 @@ int red_set_knob(int k, int value)
 
 int red_get_knob(int k)
 {
-    if (k < RED_KNOB_ROWS_GROUP || k > RED_KNOB_COLS_LANES)
+    if (k < RED_KNOB_ROWS_GROUP || k > RED_KNOB_LOSS_TRIES)
         return fail(RED_EINVAL, "red_get_knob: unknown knob %d", k);
     return knob(k);
 }

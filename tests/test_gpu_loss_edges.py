@@ -221,3 +221,44 @@ def test_preference_of_many_rows():
     off = torch.tensor([5, 1000000, rows - 3])
     only = torch.cat([torch.arange(2000), torch.arange((1 << 21) - 700, rows)])
     check_preference(x, t, off, kind="hinge", average=True, only=only)
+
+
+@pytest.mark.parametrize("dtype,length,rows", [(torch.float32, 9001, 400), (torch.bfloat16, 30001, 300),
+                                               (torch.float32, 70001, 300)])
+def test_wait_that_runs_out(dtype, length, rows):
+    """A wait that gives up at its first try in vain: rows whose copies it did
+    not wait for are NaN, in every output, and none holds anything else that is
+    wrong.  The calls after it are as before."""
+    g = device_gen(rows)
+    x = (torch.randn((rows, length), generator=g, device=DEV) * 3).to(dtype)
+    t = torch.randint(0, length, (rows,), generator=g, device=DEV)
+    t[::5] = -100
+    live = t >= 0
+    f = torch.randn(rows, generator=g, device=DEV)
+    ids = torch.randint(0, length, (rows, 5), generator=g, device=DEV)
+    vals = torch.randn((rows, 5), generator=g, device=DEV)
+    w = live.float()
+    off = torch.linspace(0, rows, 2 * 20 + 1).round().long().to(DEV)
+    lse = itr.red_logprob(x, t)[1]
+    calls = [lambda: itr.red_logprob(x, t),
+             lambda: (itr.red_logprob_grad(x, t, lse, f),),
+             lambda: itr.red_policy(x, t, f - 9, f),
+             lambda: itr.red_distill(x, ids, vals, weight=w),
+             lambda: itr.red_distill(x, ids, vals, weight=w, grad=False)[:1],
+             lambda: itr.red_preference(x, t, off)]
+    good = [call() for call in calls]
+    itr.red_set_knob(itr.RED_KNOB_LOSS_TRIES, 1)
+    try:
+        bad = [call() for call in calls]
+        torch.cuda.synchronize()
+    finally:
+        itr.red_set_knob(itr.RED_KNOB_LOSS_TRIES, 0)
+    for a, b in zip(good, bad):
+        for u, v in zip(a, b):
+            nan = v.isnan()
+            assert bool(nan.any())
+            if u.shape[0] == rows:      # results of rows: NaN or what they are; those out of the loss 0
+                assert bool((nan | (u == v)).all()) and bool((v[~live] == 0).all())
+    for call, a in zip(calls, good):
+        for u, v in zip(a, call()):
+            assert torch.equal(u, v)
