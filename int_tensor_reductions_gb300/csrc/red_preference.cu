@@ -40,7 +40,7 @@ __device__ PairTerms pair_terms(const PreferenceArgs &p, float u)
             t.loss = u;
     } else if (p.kind == RED_PREF_HINGE) {
         t.loss = u < 1.0f ? 1.0f - u : (u != u ? u : 0.0f);
-        t.du = u < 1.0f ? -1.0f : 0.0f;
+        t.du = u < 1.0f ? -1.0f : (u != u ? u : 0.0f);
     } else {
         const float off = (u - 0.5f) / p.beta;
         t.loss = off * off;

@@ -262,3 +262,15 @@ def test_wait_that_runs_out(dtype, length, rows):
     for call, a in zip(calls, good):
         for u, v in zip(a, call()):
             assert torch.equal(u, v)
+
+
+def test_hinge_of_nan():
+    """NaN in a token makes its pair's loss and gradient NaN, and no other's."""
+    for length in (60, 9000):
+        x = torch.randn((8, length), generator=device_gen(1), device=DEV)
+        t = torch.full((8,), 3, device=DEV)
+        x[1, 5] = math.nan
+        for kind in ("hinge", "sigmoid", "squared"):
+            loss, _, _, grad = itr.red_preference(x, t, torch.tensor([0, 2, 4, 6, 8], device=DEV), kind=kind)
+            assert math.isnan(loss[0].item()) and math.isfinite(loss[1].item())
+            assert bool(grad[[0, 1, 4, 5]].isnan().all()) and bool(grad[[2, 3, 6, 7]].isfinite().all())
