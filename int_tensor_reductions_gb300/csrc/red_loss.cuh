@@ -405,8 +405,9 @@ struct PolicyArgs {
         PolicyTerms t;
         const float ratio = expf(lp - old);
         const float bounded = fminf(fmaxf(ratio, 1.0f - clip_low), 1.0f + clip_high);
-        // a ratio that overflowed times no advantage is no gain, not a NaN
-        const float free = A == 0.0f ? 0.0f : ratio * A;
+        // a ratio that overflowed, or of two tokens ruled out, times no advantage
+        // is no gain, not a NaN; one of a NaN is
+        const float free = A == 0.0f && (ratio == ratio || lp == old) ? 0.0f : ratio * A;
         const float held = bounded * A;
         const bool clipped = free > held;
         t.clipped = clipped ? 1.0f : 0.0f;

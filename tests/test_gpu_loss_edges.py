@@ -274,3 +274,23 @@ def test_hinge_of_nan():
             loss, _, _, grad = itr.red_preference(x, t, torch.tensor([0, 2, 4, 6, 8], device=DEV), kind=kind)
             assert math.isnan(loss[0].item()) and math.isfinite(loss[1].item())
             assert bool(grad[[0, 1, 4, 5]].isnan().all()) and bool(grad[[2, 3, 6, 7]].isfinite().all())
+
+
+def test_policy_nan_without_advantage():
+    """No advantage does not hide a NaN, and makes nothing of an infinite ratio
+    or of a token that neither policy gives."""
+    for length in (60, 9000):
+        x = torch.randn((5, length), generator=device_gen(1), device=DEV)
+        t = torch.full((5,), 3, device=DEV)
+        old, adv = torch.full((5,), -5.0, device=DEV), torch.zeros(5, device=DEV)
+        x[0, 7] = math.nan
+        old[1] = -1000.0
+        x[2, 3] = -math.inf
+        old[2] = -math.inf
+        old[3] = math.nan
+        loss, logp, _, grad = itr.red_policy(x, t, old, adv)
+        for r in (0, 3):
+            assert math.isnan(loss[r].item()) and bool(grad[r].isnan().all())
+        for r in (1, 2, 4):
+            assert loss[r].item() == 0.0 and bool((grad[r] == 0).all())
+        assert math.isnan(logp[0].item()) and logp[2].item() == -math.inf
