@@ -206,7 +206,8 @@ __device__ __forceinline__ float exp_excess(float d)
         s = 1.0f + d * (1.0f / 3.0f) * s;
         return 0.5f * d * d * s;
     }
-    return expf(d) - d - 1.0f;
+    const float e = expf(d);
+    return e - (isinf(e) ? 0.0f : d + 1.0f);  // e^inf - inf is infinite
 }
 
 enum : int { ROW_END = 0, ROW_OUT = 1, ROW_LIVE = 2 };  // past the last row, out of the loss, in it

@@ -294,3 +294,17 @@ def test_policy_nan_without_advantage():
         for r in (1, 2, 4):
             assert loss[r].item() == 0.0 and bool((grad[r] == 0).all())
         assert math.isnan(logp[0].item()) and logp[2].item() == -math.inf
+
+
+def test_policy_drift_of_a_token_ruled_out():
+    """A token that the reference gives and the policy does not: e^d - d - 1 is
+    infinite, not NaN; likewise one that the reference alone rules out."""
+    for length in (60, 9000):
+        x = torch.randn((3, length), generator=device_gen(1), device=DEV)
+        t = torch.full((3,), 3, device=DEV)
+        x[0, 3] = -math.inf
+        old, adv = torch.full((3,), -5.0, device=DEV), torch.ones(3, device=DEV)
+        rf = torch.tensor([-4.0, -math.inf, -5.0], device=DEV)
+        loss, _, stats, _ = itr.red_policy(x, t, old, adv, ref_logp=rf, kl_coef=0.1)
+        assert loss[0].item() == loss[1].item() == math.inf and math.isfinite(loss[2].item())
+        assert stats[0].item() == math.inf
