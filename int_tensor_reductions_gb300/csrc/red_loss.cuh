@@ -585,25 +585,28 @@ struct DistillArgs {
         float vmax = NEG_INF;
         for (int i = gl; i < k; i += G) {
             const int id = s.id[i];
-            const float v = id >= 0 ? load_any(vdtype, vals, r * k + i) * a.scale : NEG_INF;
+            const float v = id >= 0 ? load_any(vdtype, vals, r * k + i) : NEG_INF;
             s.lq[i] = v;
             s.x[i] = id >= 0 ? load_elem<DT>(a.x, r * a.ld + id) : 0.0f;
             vmax = fmaxf(vmax, v);
         }
-        float norm;
+        // log q = scale * (v - base) - norm: from the largest value, or with the
+        // normaliser that is given, in one rounding each, whatever the values' size
+        float base = 0.0f, norm;
         if (lse) {
             norm = live ? lse[r] : 0.0f;
         } else {
             vmax = group_max<G>(fmaxf(vmax, NEG_INF));
+            base = vmax == NEG_INF ? 0.0f : vmax;
             float sum = 0.0f;
             for (int i = gl; i < k; i += G)
-                sum += expf(s.lq[i] - (vmax == NEG_INF ? 0.0f : vmax));
+                sum += expf((s.lq[i] - base) * a.scale);
             sum = group_sum<G>(sum);
-            norm = vmax == NEG_INF && sum == 0.0f ? 0.0f : vmax + logf(sum);
+            norm = vmax == NEG_INF && sum == 0.0f ? 0.0f : logf(sum);
         }
         float Q = 0.0f;
         for (int i = gl; i < k; i += G) {
-            const float lq = s.lq[i] - norm;
+            const float lq = fmaf(s.lq[i] - base, a.scale, -norm);
             const float q = s.id[i] < 0 ? 0.0f : expf(lq);
             s.lq[i] = lq;
             s.q[i] = q;

@@ -308,3 +308,41 @@ def test_policy_drift_of_a_token_ruled_out():
         loss, _, stats, _ = itr.red_policy(x, t, old, adv, ref_logp=rf, kl_coef=0.1)
         assert loss[0].item() == loss[1].item() == math.inf and math.isfinite(loss[2].item())
         assert stats[0].item() == math.inf
+
+
+@pytest.mark.parametrize("normalised", [False, True])
+@pytest.mark.parametrize("offset,scale", [(0.0, 1.0), (1e4, 0.7), (-1e5, 1.25), (300.0, 30.0)])
+@pytest.mark.parametrize("rows,length", [(40, 500), (5, 9001), (300, 9001)])
+def test_teacher_logits_far_from_zero(rows, length, offset, scale, normalised):
+    """A constant in all of a teacher's logits changes no q."""
+    k = 12
+    g = device_gen(rows)
+    x = torch.randn((rows, length), generator=g, device=DEV) / scale
+    ids = torch.stack([torch.randperm(length, generator=g, device=DEV)[:k] for _ in range(rows)])
+    vals = torch.randn((rows, k), generator=g, device=DEV) * 2 / scale + offset
+    scale = float(torch.tensor(scale, dtype=torch.float32))     # as the call has it: 1.7e-8 of 7000 is not nothing
+    lse = torch.logsumexp(vals.double() * scale, 1).float() + 0.5 if normalised else None
+    loss, _, grad = itr.red_distill(x, ids, vals, lse=lse, scale=scale)
+    v = vals.double() * scale
+    logq = v - (lse.double()[:, None] if normalised else torch.logsumexp(v, 1, keepdim=True))
+    q = logq.exp()
+    lp = log_softmax(x, scale)[0]
+    at = lp.gather(1, ids.cpu())
+    logq, q = logq.cpu(), q.cpu()
+    want = (q * (logq - at)).sum(1)
+    # log q is off by a few roundings of its size (at most 20), q by as much relative
+    assert bool(((loss.cpu().double() - want).abs() <= 4e-5 * (q * (logq.abs() + at.abs() + 1)).sum(1)).all())
+    p = lp.exp() * q.sum(1, keepdim=True)
+    mass = torch.zeros_like(p).scatter_add_(1, ids.cpu(), q)
+    c = torch.full((rows,), scale, dtype=torch.float64)
+    ref.assert_grad(grad, (p - mass) * scale, p + mass, c, extra=3e-5)
+
+
+def test_teacher_of_lowest_values():
+    """A teacher's list of nothing but the lowest value is uniform, at any scale."""
+    x = torch.randn((3, 500), generator=device_gen(2), device=DEV)
+    ids = torch.tensor([[1, 5, 9, 200]] * 3, device=DEV)
+    vals = torch.full((3, 4), torch.finfo(torch.float32).min, device=DEV)
+    flat = itr.red_distill(x, ids, torch.zeros_like(vals), scale=1.25)
+    for a, b in zip(itr.red_distill(x, ids, vals, scale=1.25), flat):
+        assert torch.equal(a, b)
