@@ -378,16 +378,16 @@ def _on(stream, device):
 
 
 def _done(result, user, given=None):
-    """The results of a compiled call, or RedError for its status.  What the
-    call allocated is marked as used on the ``user`` stream when that is not
-    the current one, so that the allocator does not hand it out again before
-    the work is done."""
+    """The results of a compiled call, or RedError for its status.  What a call
+    on the ``user`` stream allocated belongs to that stream; it is marked as
+    used on the current one, whose program has it now, so that the allocator
+    does not hand it out again before that work is done, too."""
     if result.__class__ is int:
         raise RedError(result, red_last_error())
     if user is not None:
         for t in result if isinstance(result, tuple) else (result,):
             if t is not None and t is not given:
-                t.record_stream(user)
+                t.record_stream(torch.cuda.current_stream(t.device))
     return result
 
 
@@ -456,7 +456,7 @@ def red_preference(x: torch.Tensor, target: torch.Tensor, offsets: torch.Tensor,
         kind = _PREF_KINDS[kind]
     at, user = (None, None) if stream is None else _on(stream, x.device)
     return _done((_entry or _losses()).preference(x, target, offsets, ref_logp, weight, kind, beta, margin, smoothing,
-                                                  average, scale, grad_scale, grad, at), user, grad)[:4]
+                                                  average, scale, grad_scale, grad, at), user, grad)
 
 
 def red_set_full_mode(mode: int) -> None:

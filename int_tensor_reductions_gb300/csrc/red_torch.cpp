@@ -195,13 +195,29 @@ PyObject *results(const T &...t)
     return r;
 }
 
-// The stream of a call: an address, or the device's current one for None.
-red_stream_t stream_of(PyObject *o, const Logits &l)
-{
-    if (o != Py_None)
-        return reinterpret_cast<red_stream_t>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(o)));
-    return reinterpret_cast<red_stream_t>(c10::cuda::getCurrentCUDAStream(l.device).stream());
-}
+// The stream of a call: an address, or the device's current one for None.  It is
+// the current one while this lives, so that what the call allocates is memory of
+// that stream: a block of the caller's own stream may still be in use there.
+struct OnStream {
+    c10::cuda::OptionalCUDAGuard device;
+    c10::cuda::OptionalCUDAStreamGuard given;
+    red_stream_t stream;
+
+    OnStream(PyObject *o, const Logits &l)
+    {
+        if (o == Py_None) {
+            device.set_index(l.device);
+            stream = reinterpret_cast<red_stream_t>(c10::cuda::getCurrentCUDAStream(l.device).stream());
+            return;
+        }
+        const unsigned long long address = PyLong_AsUnsignedLongLong(o);
+        if (PyErr_Occurred())
+            throw Refused();
+        stream = reinterpret_cast<red_stream_t>(static_cast<uintptr_t>(address));
+        given.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream),
+                                                            static_cast<c10::DeviceIndex>(l.device)));
+    }
+};
 
 template <class F>
 PyObject *guarded(const char *name, Py_ssize_t given, Py_ssize_t wanted, F f)
@@ -228,6 +244,7 @@ PyObject *logprob(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return guarded("logprob", n, 6, [&] {
         const Logits l(a[0]);
+        const OnStream on(a[5], l);
         const int64_t *target = l.vector<int64_t>(a[1], "target", l.rows);
         const float *given = l.vector<float>(a[3], "out", l.rows), *given_lse = l.vector<float>(a[4], "lse", l.rows);
         at::Tensor out, lse;
@@ -239,9 +256,8 @@ PyObject *logprob(PyObject *, PyObject *const *a, Py_ssize_t n)
             out = given ? tensor(a[3], "out") : l.floats(l.rows);
             lse = given_lse ? tensor(a[4], "lse") : l.floats(l.rows);
         }
-        const c10::cuda::OptionalCUDAGuard guard(l.x.device());
         RETURN_IF_REFUSED(red_logprob(l.dtype, l.x.data_ptr(), l.rows, l.len, l.ld, (float)number(a[2]), target,
-                                      data(out), data(lse), stream_of(a[5], l)));
+                                      data(out), data(lse), on.stream));
         return results(out, lse);
     });
 }
@@ -251,14 +267,14 @@ PyObject *logprob_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return guarded("logprob_grad", n, 7, [&] {
         const Logits l(a[0]);
+        const OnStream on(a[6], l);
         if (a[5] == Py_False)
             refuse("out must be a tensor or None");
         const int64_t *target = l.vector<int64_t>(a[1], "target", l.rows);
         const float *lse = l.vector<float>(a[2], "lse", l.rows), *dlogp = l.vector<float>(a[3], "dlogp", l.rows);
         const Gradient g(a[5], l, "out");
-        const c10::cuda::OptionalCUDAGuard guard(l.x.device());
         RETURN_IF_REFUSED(red_logprob_grad(l.dtype, l.x.data_ptr(), l.rows, l.len, l.ld, (float)number(a[4]), target,
-                                           lse, dlogp, g.ptr, g.ld, stream_of(a[6], l)));
+                                           lse, dlogp, g.ptr, g.ld, on.stream));
         return wrap(g.t);
     });
 }
@@ -268,6 +284,7 @@ PyObject *distill(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return guarded("distill", n, 9, [&] {
         const Logits l(a[0]);
+        const OnStream on(a[8], l);
         const at::Tensor &ids = tensor(a[1], "ids"), &vals = tensor(a[2], "vals");
         if (ids.dim() != 2 || vals.sizes() != ids.sizes() || ids.size(0) != l.rows)
             refuse("ids and vals must be (rows, k)");
@@ -279,10 +296,9 @@ PyObject *distill(PyObject *, PyObject *const *a, Py_ssize_t n)
         const float *lse = l.vector<float>(a[3], "lse", l.rows), *weight = l.vector<float>(a[4], "weight", l.rows);
         const Gradient g(a[7], l, "grad");
         const auto [loss, stats] = float_vectors(l, {l.rows, 2});
-        const c10::cuda::OptionalCUDAGuard guard(l.x.device());
         RETURN_IF_REFUSED(red_distill(l.dtype, l.x.data_ptr(), l.rows, l.len, l.ld, (float)number(a[5]), k, id, vcode,
                                       vals.data_ptr(), lse, weight, (float)number(a[6]), data(loss), data(stats),
-                                      g.ptr, g.ld, stream_of(a[8], l)));
+                                      g.ptr, g.ld, on.stream));
         return results(loss, stats, g.t);
     });
 }
@@ -292,16 +308,16 @@ PyObject *policy(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return guarded("policy", n, 13, [&] {
         const Logits l(a[0]);
+        const OnStream on(a[12], l);
         const int64_t *target = l.vector<int64_t>(a[1], "target", l.rows);
         const float *old_logp = l.vector<float>(a[2], "old_logp", l.rows), *adv = l.vector<float>(a[3], "adv", l.rows);
         const float *ref = l.vector<float>(a[4], "ref_logp", l.rows), *weight = l.vector<float>(a[5], "weight", l.rows);
         const Gradient g(a[11], l, "grad");
         const auto [loss, logp, stats] = float_vectors(l, {l.rows, l.rows, 4});
-        const c10::cuda::OptionalCUDAGuard guard(l.x.device());
         RETURN_IF_REFUSED(red_policy(l.dtype, l.x.data_ptr(), l.rows, l.len, l.ld, (float)number(a[9]), target,
                                      old_logp, ref, adv, weight, (float)number(a[6]), (float)number(a[7]),
                                      (float)number(a[8]), (float)number(a[10]), data(loss), data(logp), data(stats),
-                                     g.ptr, g.ld, stream_of(a[12], l)));
+                                     g.ptr, g.ld, on.stream));
         return results(loss, logp, stats, g.t);
     });
 }
@@ -311,6 +327,7 @@ PyObject *preference(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     return guarded("preference", n, 14, [&] {
         const Logits l(a[0]);
+        const OnStream on(a[13], l);
         const int64_t entries = tensor(a[2], "offsets").numel();
         if (entries % 2 != 1)
             refuse("offsets needs 2 * pairs + 1 entries");
@@ -320,10 +337,8 @@ PyObject *preference(PyObject *, PyObject *const *a, Py_ssize_t n)
         const float *ref = l.vector<float>(a[3], "ref_logp", 2 * pairs), *weight = l.vector<float>(a[4], "weight", pairs);
         const Gradient g(a[12], l, "grad");
         const auto [loss, seq, stats] = float_vectors(l, {pairs, 2 * pairs, 4});
-        // (freed on return: the allocator keeps it for this stream's later work,
-        // and the wrapper holds it for any other stream)
+        // (freed on return: the allocator keeps it for this stream's later work)
         const at::Tensor work = l.floats(3 * l.rows + pairs);
-        const c10::cuda::OptionalCUDAGuard guard(l.x.device());
         const int average = PyObject_IsTrue(a[9]);
         if (average < 0)
             throw Refused();
@@ -331,8 +346,8 @@ PyObject *preference(PyObject *, PyObject *const *a, Py_ssize_t n)
                                          offsets, pairs, ref, weight, (int)integer(a[5]), (float)number(a[6]),
                                          (float)number(a[7]), (float)number(a[8]), average, (float)number(a[11]),
                                          data(loss), data(seq), data(stats), data(work), g.ptr, g.ld,
-                                         stream_of(a[13], l)));
-        return results(loss, seq, stats, g.t, work);
+                                         on.stream));
+        return results(loss, seq, stats, g.t);
     });
 }
 

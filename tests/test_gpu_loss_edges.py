@@ -346,3 +346,37 @@ def test_teacher_of_lowest_values():
     flat = itr.red_distill(x, ids, torch.zeros_like(vals), scale=1.25)
     for a, b in zip(itr.red_distill(x, ids, vals, scale=1.25), flat):
         assert torch.equal(a, b)
+
+
+def test_results_are_memory_of_the_calls_stream():
+    """A block that the current stream's program gave back may be in use there
+    still: a call on another stream does not get it."""
+    rows, length = 400_000, 8
+    x = torch.randn((rows, length), generator=device_gen(1), device=DEV)
+    t = torch.randint(0, length, (rows,), generator=device_gen(2), device=DEV)
+    f = torch.randn(rows, generator=device_gen(3), device=DEV)
+    ids, vals = t[:, None].expand(rows, 2).contiguous(), torch.zeros((rows, 2), device=DEV)
+    off = torch.linspace(0, rows, 2 * 30000 + 1).round().long().to(DEV)
+    lse = itr.red_logprob(x, t)[1]
+    calls = [lambda s: itr.red_logprob(x, t, stream=s),
+             lambda s: (itr.red_logprob_grad(x, t, lse, f, stream=s),),
+             lambda s: itr.red_policy(x, t, f - 2, f, stream=s),
+             lambda s: itr.red_distill(x, ids, vals, stream=s),
+             lambda s: itr.red_preference(x, t, off, stream=s)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        for call in calls:
+            want = call(None)
+            torch.cuda.synchronize()
+            sizes = [v.untyped_storage().nbytes() for v in want]
+            blocks = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes]
+            spans = [(b.data_ptr(), b.data_ptr() + b.numel()) for b in blocks]
+            del blocks
+            got = call(stream)
+            for u, v in zip(want, got):
+                assert not any(lo <= v.data_ptr() < hi for lo, hi in spans)
+            side.synchronize()
+            assert all(torch.equal(u, v) for u, v in zip(want, got))
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+            del want, got
