@@ -51,12 +51,14 @@ double number(PyObject *o)
     return v;
 }
 
-int64_t integer(PyObject *o)
+int integer(PyObject *o, const char *name)
 {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred())
         throw Refused();
-    return v;
+    if (v != static_cast<int>(v))
+        refuse("%s = %lld is out of range", name, v);
+    return static_cast<int>(v);
 }
 
 int dtype_code(at::ScalarType t, const char *name)
@@ -343,7 +345,7 @@ PyObject *preference(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (average < 0)
             throw Refused();
         RETURN_IF_REFUSED(red_preference(l.dtype, l.x.data_ptr(), l.rows, l.len, l.ld, (float)number(a[10]), target,
-                                         offsets, pairs, ref, weight, (int)integer(a[5]), (float)number(a[6]),
+                                         offsets, pairs, ref, weight, integer(a[5], "kind"), (float)number(a[6]),
                                          (float)number(a[7]), (float)number(a[8]), average, (float)number(a[11]),
                                          data(loss), data(seq), data(stats), data(work), g.ptr, g.ld,
                                          on.stream));

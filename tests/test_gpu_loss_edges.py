@@ -380,3 +380,15 @@ def test_results_are_memory_of_the_calls_stream():
             assert all(torch.equal(u, v) for u, v in zip(want, got))
             assert torch.cuda.current_stream() == torch.cuda.default_stream()
             del want, got
+
+
+def test_kind_is_not_cut_to_32_bits():
+    x = torch.zeros((2, 5), device=DEV)
+    t = torch.zeros(2, dtype=torch.int64, device=DEV)
+    off = torch.arange(3, device=DEV)
+    for kind in (1 << 32, -(1 << 32), (1 << 32) + 1):
+        with pytest.raises(ValueError):
+            itr.red_preference(x, t, off, kind=kind)
+    for kind in (3, -1):
+        with pytest.raises(itr.RedError):
+            itr.red_preference(x, t, off, kind=kind)
