@@ -106,13 +106,6 @@ __device__ __forceinline__ float soft_factor(float from, float f2, float to, flo
     return ex2(e);
 }
 
-__device__ __forceinline__ SoftStat soft_join(SoftStat a, SoftStat b, float s2)
-{
-    const float m = fmaxf(a.m, b.m), m2 = __fmul_rn(m, s2);
-    return SoftStat{m, a.l * soft_factor(a.m, __fmul_rn(a.m, s2), m, m2, s2) +
-                           b.l * soft_factor(b.m, __fmul_rn(b.m, s2), m, m2, s2)};
-}
-
 // The largest of the lanes' values (no NaN), by the integer reduction: the
 // bits of floats compare like integers once those of negative ones are turned
 // around.

@@ -420,7 +420,6 @@ __device__ __forceinline__ void zero_row_bulk(typename Elem<DT>::T *g, int len, 
 __device__ __forceinline__ void bulk_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 constexpr int ROW_Q = 32;      // entries of the row queue
-constexpr int ROW_MAX_GROUP = 4;
 constexpr int ROW_MAX_SLOTS = 32;
 constexpr int TEACHERS = 4;    // teacher warps: each has the time of this many rows for one list
 
