@@ -96,10 +96,11 @@ enum red_dtype {
 };
 
 /* Status codes.  There is no timeout status: no kernel of this library
- * waits on another CTA, stream or device (the last-block stages count
- * arrivals and the last arrival does the fold).  The losses over logits wait
- * for their own bulk copies, with a limit: a copy that never arrived would
- * make the results of its CTA's rows NaN. */
+ * waits on another stream or device, and none of the reductions on another
+ * CTA (the last-block stages count arrivals and the last arrival does the
+ * fold).  The losses over logits wait for the CTAs of their own cluster, at
+ * the hardware's barrier, and inside a CTA for its own bulk copies, with a
+ * limit: what its CTA has not written when such a wait runs out becomes NaN. */
 enum red_status { RED_OK = 0, RED_EINVAL = -1, RED_ECUDA = -2, RED_ENOMEM = -3 };
 
 /* Grid stage of red_full (how the per-CTA partials become one scalar). */
@@ -340,7 +341,10 @@ int red_full_noalloc(int op, const float *x, int64_t n, float *out, red_stream_t
  *     dx = grad_scale * d(sum of the losses of all rows or pairs) / dx.
  * Conventions of these calls:
  *   dtype    RED_F32, RED_F16 or RED_BF16, of x and of dx.  Arithmetic is in
- *            fp32 (totals in 64 bits); dx is rounded once, to nearest.
+ *            fp32, sums over rows and pairs in two floats (the rounding error
+ *            of each addition is carried along); dx is rounded once, to
+ *            nearest.  A constant added to a row's logits, or to a teacher's,
+ *            costs no accuracy but in lse itself.
  *   rows, len, ld   x[r, j] is at x + r * ld + j; 1 <= len <= 2^30, ld >= len;
  *            x needs the alignment of its elements only, and neither it nor
  *            dx is touched between columns len and ld.

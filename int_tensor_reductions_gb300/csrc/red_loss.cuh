@@ -14,8 +14,8 @@
 // Beyond |M| = 2^24 (a row that is nothing but the type's lowest value, say,
 // as an additive mask leaves it) lo would no longer be small, and products of
 // x overflow; there the terms are 2^((x_j - m) * s2), difference first.
-// Partial (m, l) pairs combine by rescaling to the larger maximum; where no
-// logit is finite m = -inf and l = 0.
+// Partial (m, l) pairs combine by rescaling to the larger maximum, from one
+// rounded M to the other; where no logit is finite m = -inf and l = 0.
 #pragma once
 
 #include <cstdint>
