@@ -10,7 +10,13 @@
  *                    fp32 and (wrapping) int32 matrices;
  *   red_logprob, red_distill, red_policy, red_preference
  *                    losses over rows of logits and their gradients (log
- *                    softmax reductions of fp32, f16 or bf16 rows).
+ *                    softmax reductions of fp32, f16 or bf16 rows);
+ *   red_linear_logprob
+ *                    log-probabilities from hidden states and the vocabulary's
+ *                    weights, without the logits, and their gradients;
+ *   red_rmsnorm      root-mean-square norm of rows with the residual's addition,
+ *                    an output in 8 bits, and the backward;
+ *   red_balance      balance loss of a router of experts, with its gradient.
  *
  * Sources of the semantics (cited by page title and section):
  *   [TVM] Apache TVM docs, "reduction -> sm100_packed": "Algorithm" (sum of a
@@ -458,6 +464,151 @@ int red_preference(int dtype, const void *x, int64_t rows, int64_t len, int64_t 
                    const float *weight, int kind, float beta, float margin, float smoothing, int average,
                    float grad_scale, float *loss, float *seq_logp, float *stats, float *work, void *dx, int64_t ldd,
                    red_stream_t stream);
+
+/*
+ * Log-probabilities from hidden states and weights, without the logits
+ * --------------------------------------------------------------------
+ * red_linear_logprob is red_logprob of the logits hidden * weight^T, which are
+ * never stored:
+ *     z[r, j] = scale * sum_d hidden[r, d] * weight[j, d],
+ *     lse[r] = log sum_j e^z[r, j],  logp[r] = z[r, target[r]] - lse[r].
+ * Conventions:
+ *   dtype    RED_F16 or RED_BF16, of all matrices.  Products are summed in fp32;
+ *            logits, maxima and sums of exponentials are fp32 throughout.
+ *   hidden   rows x dim, row stride ldh;  weight: vocab x dim, row stride ldw.
+ *            Every matrix starts on a 16-byte boundary and its row stride is a
+ *            multiple of 8 elements (where it has more than one row), dim
+ *            itself is any number up to 2^20; rows and vocab up to 2^24.
+ *   target   one int64 column of the vocabulary per row; a row whose target is
+ *            outside [0, vocab) is ignored: its results are 0, and what it holds
+ *            (NaN, say) reaches no other row and no gradient.
+ *   scale    1e-30 .. 1e30.
+ *   work     scratch of at least red_linear_work_bytes() bytes, from a 256-byte
+ *            boundary on, the call's own until its work is done; what it holds
+ *            before does not matter.  These calls do not use the library's
+ *            workspace: two of them may run at the same time, with scratch
+ *            and results of their own.
+ * +inf or NaN in a row that takes part, or in the weights, makes NaN of what
+ * depends on it.  Results are the same from call to call, bit for bit.
+ */
+int64_t red_linear_work_bytes(int64_t rows, int64_t dim, int64_t vocab, int grad);
+int red_linear_logprob(int dtype, const void *hidden, int64_t rows, int64_t dim, int64_t ldh, const void *weight,
+                       int64_t vocab, int64_t ldw, float scale, const int64_t *target, float *logp, float *lse,
+                       void *work, int64_t work_bytes, red_stream_t stream);
+
+/*
+ * red_linear_logprob_grad -- backward of red_linear_logprob: for the gradients
+ * dlogp[r] and dlse[r] (NULL: 0) of some loss by logp[r] and lse[r],
+ *     g[r, j] = scale * (dlogp[r] * ([j == target[r]] - p_j) + dlse[r] * p_j),
+ *     dhidden = g * weight,  dweight = g^T * hidden,
+ * with p_j = e^(z[r, j] - lse[r]), lse as red_linear_logprob left it.  A row
+ * whose dlogp and dlse are both 0 is ignored, too.  The vocabulary is taken in
+ * pieces; g is rounded to dtype once, against a power of two that the largest
+ * coefficient sets, and each result once more; their sums are fp32.
+ *   dhidden  rows x dim, row stride ldd, or NULL for none.  May be `hidden`.
+ *   dweight  vocab x dim, row stride lddw, or NULL for none (not both).
+ *   work     red_linear_work_bytes(..., 1) bytes.
+ */
+int red_linear_logprob_grad(int dtype, const void *hidden, int64_t rows, int64_t dim, int64_t ldh,
+                            const void *weight, int64_t vocab, int64_t ldw, float scale, const int64_t *target,
+                            const float *lse, const float *dlogp, const float *dlse, void *dhidden, int64_t ldd,
+                            void *dweight, int64_t lddw, void *work, int64_t work_bytes, red_stream_t stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition
+ * -----------------------------------------------------------
+ *     t = x + residual  (x where residual is NULL),
+ *     rstd[r] = 1 / sqrt(mean_j t[r, j]^2 + eps),  y[r, j] = t[r, j] * rstd[r] * weight[j].
+ * Conventions:
+ *   dtype    RED_F32, RED_F16 or RED_BF16, of x, residual, total, y and their
+ *            gradients; wtype: dtype or RED_F32, of weight and dweight.
+ *            Arithmetic is in fp32; each result is rounded once, to nearest (y
+ *            from the sum t before it is rounded to total).
+ *   rows, len   1 <= len <= RED_RMSNORM_MAX_LEN; each matrix has a row stride of
+ *            its own (>= len), needs the alignment of its elements only, and is
+ *            not touched between columns len and its stride.  Rows on 16-byte
+ *            boundaries are read fastest.
+ *   weight   len elements, or NULL for 1.
+ *   total    t, with residual; NULL without.  Results may lie exactly over inputs
+ *            (total over x or residual, y over the other), of the same stride, and
+ *            must not overlap them otherwise, nor each other.
+ *   rstd     rows floats (the backward wants them), or NULL.
+ *   eps      0 .. 1e30.
+ * Squares are summed in fp32: rows of values beyond 1e19 overflow.  NaN and
+ * infinities spread over their row and no further (in dweight, over their
+ * column).  Results are the same from call to call, bit for bit.
+ */
+#define RED_RMSNORM_MAX_LEN 16384
+int red_rmsnorm(int dtype, const void *x, int64_t rows, int64_t len, int64_t ldx, const void *residual, int64_t ldr,
+                int wtype, const void *weight, float eps, void *y, int64_t ldy, void *total, int64_t ldt, float *rstd,
+                red_stream_t stream);
+
+/* 8-bit types of red_rmsnorm_quant. */
+enum red_quant {
+    RED_QUANT_E4M3 = 1, /* 4 bits of exponent, 3 of mantissa, no infinities; the largest is 448 */
+    RED_QUANT_I8 = 2    /* -127 .. 127 */
+};
+
+/*
+ * red_rmsnorm_quant -- the same with y in 8 bits and a scale for each `block`
+ * neighbouring values of a row (32, 64, 128 or 256; the last block of a row may
+ * be shorter), or for each row (block = 0):
+ *     scale = max |y| / (448 or 127), 1 where that is 0;  q = y / scale, to nearest (ties to even).
+ *   q        rows x len bytes, row stride ldq;
+ *   scales   rows x ceil(len / block) floats (rows floats for block = 0).
+ * A NaN makes NaN of its block's scale; its e4m3 values are NaN, its integers
+ * are unspecified.
+ */
+int red_rmsnorm_quant(int dtype, const void *x, int64_t rows, int64_t len, int64_t ldx, const void *residual,
+                      int64_t ldr, int wtype, const void *weight, float eps, int kind, int64_t block, void *q,
+                      int64_t ldq, float *scales, void *total, int64_t ldt, float *rstd, red_stream_t stream);
+
+/*
+ * red_rmsnorm_grad -- backward of red_rmsnorm.  With x the norm's input (total,
+ * where there was a residual), h = x * rstd and g = dy * weight:
+ *     dx = rstd * (g - h * mean_j(g * h)) + dtotal,   dweight[j] = sum_r dy[r, j] * h[r, j].
+ *   dtotal   the gradient that reaches x (or total) on other ways, or NULL.
+ *   dx       the gradient by x, and by the residual; may lie exactly over dy, x
+ *            or dtotal.
+ *   dweight  len elements of wtype, or NULL for none.  Uses the workspace.
+ */
+int red_rmsnorm_grad(int dtype, const void *dy, int64_t lddy, const void *x, int64_t rows, int64_t len, int64_t ldx,
+                     const float *rstd, int wtype, const void *weight, const void *dtotal, int64_t ldt, void *dx,
+                     int64_t ldd, void *dweight, red_stream_t stream);
+
+/* How a router's logits become probabilities. */
+enum red_balance_kind {
+    RED_BALANCE_SOFTMAX = 0, /* p = softmax(x) */
+    RED_BALANCE_SIGMOID = 1  /* p = s / sum of the row's s, s = 1 / (1 + e^-x) */
+};
+
+/*
+ * red_balance -- balance loss of a router of experts, the experts' counts and
+ * the gradient.  Row t of x holds token t's logits of the experts, ids its k
+ * experts.  Over the n tokens that take part (live: one byte per token, 0: out;
+ * NULL: all),
+ *     count_e = entries of ids that are e,  prob_e = mean of p_te,
+ *     loss = coef * experts * sum_e count_e / (k n) * prob_e + z_coef * mean lse_t^2,
+ * lse_t = log sum_e e^x_te (RED_BALANCE_SOFTMAX; z_coef is 0 otherwise).
+ *   dtype    RED_F32, RED_F16 or RED_BF16, of x and dx; fp32 arithmetic.
+ *   experts  1 .. RED_BALANCE_MAX_EXPERTS;  k: 1 .. experts, rows * k < 2^31.
+ *   ids      (rows, k) int64; an id outside [0, experts) counts nowhere, one that
+ *            comes twice counts twice.
+ *   counts   experts int64;  prob: experts floats.
+ *   stats    4 floats: loss, experts * sum_e count_e / (k n) * prob_e, mean
+ *            lse^2, n.
+ *   dx       grad_scale * d loss / dx (counts are constants), rows of stride ldd;
+ *            0 for a token that is out, whatever its logits hold.  May be x
+ *            (ldd == ld then), or NULL for none.
+ * -inf takes an expert out of a token's choice; a token with nothing else has
+ * no probabilities and a gradient of 0.  NaN (and +inf, of a softmax) in a token
+ * that takes part makes its gradient, prob and the loss NaN.  Results are the same from call to
+ * call, bit for bit.  Uses the workspace.
+ */
+#define RED_BALANCE_MAX_EXPERTS 4096
+int red_balance(int dtype, const void *x, int64_t rows, int64_t experts, int64_t ld, const int64_t *ids, int64_t k,
+                const uint8_t *live, int kind, float coef, float z_coef, float grad_scale, int64_t *counts, float *prob,
+                float *stats, void *dx, int64_t ldd, red_stream_t stream);
 
 /* Select the grid stage of red_full (enum red_full_mode).  Process-wide.
  * Returns RED_OK, or RED_EINVAL for an unknown mode. */

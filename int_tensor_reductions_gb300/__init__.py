@@ -26,6 +26,18 @@ Losses over rows of logits (float32, float16 or bfloat16), with their gradients:
     red_policy(x, target, old_logp, adv)           clipped policy loss with a KL term
     red_preference(x, target, offsets)             pairs of packed sequences
 
+The same from hidden states and the vocabulary's weights (float16 or bfloat16), without the logits:
+
+    red_linear_logprob(hidden, weight, target)     (log-probabilities, log-sum-exp) per row
+    red_linear_logprob_grad(hidden, weight, target, lse, dlogp)   its backward
+
+Root-mean-square norm of rows, with the residual's addition, and the balance loss of a router:
+
+    red_rmsnorm(x, weight, residual=r)             (y, x + r, 1 / root mean square)
+    red_rmsnorm_quant(x, weight, residual=r)       with y in 8 bits and scales
+    red_rmsnorm_grad(dy, x, rstd, weight)          the backward
+    red_balance(x, ids)                            counts, mean probabilities, loss, gradient
+
 Every call takes an optional ``stream`` (default: the current stream of x's
 device) and returns ``out``.  Calls on one device must be ordered (one
 stream, or streams ordered by events): they share the library's workspace.
@@ -34,8 +46,10 @@ from ._binding import (  # noqa: F401
     RED_BF16, RED_DISTILL_MAX_K, RED_EINVAL, RED_ECUDA, RED_ENOMEM, RED_F16, RED_F32, RED_I16, RED_I32, RED_KNOB_COLPROD_SPLITS,
     RED_KNOB_FULL_CTAS_PER_SM, RED_KNOB_RAGGED_GROUP, RED_KNOB_RAGGED_STAGED, RED_KNOB_ROWS_ALIGNED, RED_KNOB_ROWS_GROUP,
     RED_KNOB_COLS_LANES, RED_KNOB_LOSS_TRIES, RED_MAX, RED_MIN,
+    RED_BALANCE_MAX_EXPERTS, RED_BALANCE_SIGMOID, RED_BALANCE_SOFTMAX, RED_QUANT_E4M3, RED_QUANT_I8, RED_RMSNORM_MAX_LEN,
     RED_PREF_HINGE, RED_PREF_SIGMOID, RED_PREF_SQUARED,
     RED_MODE_ATOMIC, RED_MODE_AUTO, RED_MODE_LAST_BLOCK, RED_MODE_TWO_PASS, RED_OK, RED_PROD, RED_SUM, RED_U16, RED_U32,
-    RedError, lib, lib_path, red_colprod, red_cols, red_distill, red_full, red_full_noalloc, red_full_stats, red_full_typed, red_get_full_mode, red_get_knob, red_last_error, red_launch_count, red_logprob, red_logprob_grad, red_policy, red_preference,
-    red_release_workspace, red_rows, red_rows_ragged, red_rows_stats, red_rows_thread, red_rows_typed, red_set_full_mode, red_set_knob, red_version,
+    RedError, lib, lib_path, red_colprod, red_cols, red_distill, red_full, red_full_noalloc, red_full_stats, red_full_typed, red_get_full_mode, red_get_knob, red_last_error, red_balance, red_launch_count, red_linear_logprob,
+    red_linear_logprob_grad, red_logprob, red_logprob_grad, red_policy, red_preference,
+    red_release_workspace, red_rmsnorm, red_rmsnorm_grad, red_rmsnorm_quant, red_rows, red_rows_ragged, red_rows_stats, red_rows_thread, red_rows_typed, red_set_full_mode, red_set_knob, red_version,
 )

@@ -17,6 +17,10 @@ RED_KNOB_COLS_LANES = 7
 RED_KNOB_LOSS_TRIES = 8
 RED_PREF_SIGMOID, RED_PREF_HINGE, RED_PREF_SQUARED = 0, 1, 2
 RED_DISTILL_MAX_K = 1024
+RED_RMSNORM_MAX_LEN = 16384
+RED_QUANT_E4M3, RED_QUANT_I8 = 1, 2
+RED_BALANCE_SOFTMAX, RED_BALANCE_SIGMOID = 0, 1
+RED_BALANCE_MAX_EXPERTS = 4096
 
 _OPS = {"sum": RED_SUM, "max": RED_MAX, "min": RED_MIN, "prod": RED_PROD}
 # element type names of the column reductions and their sizes in bytes
@@ -34,6 +38,8 @@ _lib = None
 _i64, _int, _vp, _f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_float
 # dtype, x, rows, len, ld, scale
 _LOGITS = [_int, _vp, _i64, _i64, _i64, _f32]
+# dtype, hidden, rows, dim, ldh, weight, vocab, ldw, scale, target
+_LINEAR = [_int, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _f32, _vp]
 _SIGNATURES = {
     "red_full": ([_int, _vp, _i64, _vp, _vp], _int),
     "red_full_noalloc": ([_int, _vp, _i64, _vp, _vp], _int),
@@ -53,6 +59,16 @@ _SIGNATURES = {
     "red_policy": (_LOGITS + [_vp, _vp, _vp, _vp, _vp, _f32, _f32, _f32, _f32, _vp, _vp, _vp, _vp, _i64, _vp], _int),
     "red_preference": (_LOGITS + [_vp, _vp, _i64, _vp, _vp, _int, _f32, _f32, _f32, _int, _f32, _vp, _vp, _vp, _vp,
                                   _vp, _i64, _vp], _int),
+    "red_linear_work_bytes": ([_i64, _i64, _i64, _int], _i64),
+    "red_linear_logprob": (_LINEAR + [_vp, _vp, _vp, _i64, _vp], _int),
+    "red_linear_logprob_grad": (_LINEAR + [_vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp], _int),
+    "red_rmsnorm": ([_int, _vp, _i64, _i64, _i64, _vp, _i64, _int, _vp, _f32, _vp, _i64, _vp, _i64, _vp, _vp], _int),
+    "red_rmsnorm_quant": ([_int, _vp, _i64, _i64, _i64, _vp, _i64, _int, _vp, _f32, _int, _i64, _vp, _i64, _vp, _vp,
+                           _i64, _vp, _vp], _int),
+    "red_rmsnorm_grad": ([_int, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _int, _vp, _vp, _i64, _vp, _i64, _vp, _vp],
+                         _int),
+    "red_balance": ([_int, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _int, _f32, _f32, _f32, _vp, _vp, _vp, _vp, _i64,
+                     _vp], _int),
     "red_set_full_mode": ([_int], _int),
     "red_get_full_mode": ([], _int),
     "red_set_knob": ([_int, _int], _int),
@@ -377,7 +393,7 @@ def _on(stream, device):
     return user.cuda_stream, user
 
 
-def _done(result, user, given=None):
+def _done(result, user, given=()):
     """The results of a compiled call, or RedError for its status.  What a call
     on the ``user`` stream allocated belongs to that stream; it is marked as
     used on the current one, whose program has it now, so that the allocator
@@ -386,7 +402,7 @@ def _done(result, user, given=None):
         raise RedError(result, red_last_error())
     if user is not None:
         for t in result if isinstance(result, tuple) else (result,):
-            if t is not None and t is not given:
+            if t is not None and not any(t is g for g in given):
                 t.record_stream(torch.cuda.current_stream(t.device))
     return result
 
@@ -407,7 +423,7 @@ def red_logprob_grad(x: torch.Tensor, target: torch.Tensor, lse: torch.Tensor, d
     by logp and red_logprob's lse.  ``out`` may be x (in place); a new one has
     x's row stride."""
     at, user = (None, None) if stream is None else _on(stream, x.device)
-    return _done((_entry or _losses()).logprob_grad(x, target, lse, dlogp, scale, out, at), user, out)
+    return _done((_entry or _losses()).logprob_grad(x, target, lse, dlogp, scale, out, at), user, (out,))
 
 
 def red_distill(x: torch.Tensor, ids: torch.Tensor, vals: torch.Tensor, lse: torch.Tensor | None = None,
@@ -421,7 +437,7 @@ def red_distill(x: torch.Tensor, ids: torch.Tensor, vals: torch.Tensor, lse: tor
     grad_scale times the gradient of the summed loss by x.  ``grad``: None for
     a new tensor, a tensor to write (x: in place), False for the loss alone."""
     at, user = (None, None) if stream is None else _on(stream, x.device)
-    return _done((_entry or _losses()).distill(x, ids, vals, lse, weight, scale, grad_scale, grad, at), user, grad)
+    return _done((_entry or _losses()).distill(x, ids, vals, lse, weight, scale, grad_scale, grad, at), user, (grad,))
 
 
 def red_policy(x: torch.Tensor, target: torch.Tensor, old_logp: torch.Tensor, adv: torch.Tensor,
@@ -435,7 +451,7 @@ def red_policy(x: torch.Tensor, target: torch.Tensor, old_logp: torch.Tensor, ad
     of clipped tokens, weight).  ``grad`` as for red_distill."""
     at, user = (None, None) if stream is None else _on(stream, x.device)
     return _done((_entry or _losses()).policy(x, target, old_logp, adv, ref_logp, weight, clip_low, clip_high, kl_coef,
-                                              scale, grad_scale, grad, at), user, grad)
+                                              scale, grad_scale, grad, at), user, (grad,))
 
 
 def red_preference(x: torch.Tensor, target: torch.Tensor, offsets: torch.Tensor,
@@ -456,7 +472,102 @@ def red_preference(x: torch.Tensor, target: torch.Tensor, offsets: torch.Tensor,
         kind = _PREF_KINDS[kind]
     at, user = (None, None) if stream is None else _on(stream, x.device)
     return _done((_entry or _losses()).preference(x, target, offsets, ref_logp, weight, kind, beta, margin, smoothing,
-                                                  average, scale, grad_scale, grad, at), user, grad)
+                                                  average, scale, grad_scale, grad, at), user, (grad,))
+
+
+# ----------------------- log-probabilities from hidden states and weights
+
+def red_linear_logprob(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, scale: float = 1.0,
+                       stream=None):
+    """red_logprob of the logits ``hidden @ weight.T`` without storing them:
+    hidden (rows, dim) and weight (vocab, dim) are float16 or bfloat16, their
+    rows on 16-byte boundaries; returns (logp, lse), fp32.  A row whose target
+    is outside the vocabulary (e.g. -100) gives 0."""
+    at, user = (None, None) if stream is None else _on(stream, hidden.device)
+    return _done((_entry or _losses()).linear_logprob(hidden, weight, target, scale, at), user)
+
+
+def red_linear_logprob_grad(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, lse: torch.Tensor,
+                            dlogp: torch.Tensor, dlse: torch.Tensor | None = None, scale: float = 1.0,
+                            grad_hidden=None, grad_weight=None, stream=None):
+    """Backward of red_linear_logprob: (grad_hidden, grad_weight) for the
+    gradients ``dlogp`` by logp and ``dlse`` by lse (None: 0), with
+    red_linear_logprob's lse.  Cross entropy is dlogp = -weight; a penalty c *
+    lse**2 on the normaliser is dlse = 2 * c * lse.  ``grad_hidden`` and
+    ``grad_weight``: None for a new tensor, a tensor to write (hidden itself for
+    grad_hidden), False for none."""
+    at, user = (None, None) if stream is None else _on(stream, hidden.device)
+    return _done((_entry or _losses()).linear_logprob_grad(hidden, weight, target, lse, dlogp, dlse, scale, grad_hidden,
+                                                           grad_weight, at), user, (grad_hidden, grad_weight))
+
+
+# -------------------------------------------------- root-mean-square norm
+
+_QUANT_KINDS = {"e4m3": RED_QUANT_E4M3, "int8": RED_QUANT_I8}
+_BALANCE_KINDS = {"softmax": RED_BALANCE_SOFTMAX, "sigmoid": RED_BALANCE_SIGMOID}
+
+
+def _kind(kind, kinds):
+    if isinstance(kind, str):
+        if kind not in kinds:
+            raise ValueError(f"unknown kind {kind!r}")
+        return kinds[kind]
+    return kind
+
+
+def red_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                eps: float = 1e-6, out: torch.Tensor | None = None, total: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norm of the rows of x + residual (rows, len), float32,
+    float16 or bfloat16, len <= RED_RMSNORM_MAX_LEN: t = x + residual, y = t /
+    sqrt(mean(t**2) + eps) * weight.  ``weight``: len values of x's dtype or
+    float32, None for 1.  Returns (y, total, rstd): total is t (None without a
+    residual), rstd the rows' 1 / sqrt(...), fp32.  ``out`` and ``total``:
+    tensors to write; they may be x or residual."""
+    at, user = (None, None) if stream is None else _on(stream, x.device)
+    return _done((_entry or _losses()).rmsnorm(x, weight, residual, eps, out, total, at), user, (out, total))
+
+
+def red_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                      eps: float = 1e-6, kind="e4m3", block: int = 0, out: torch.Tensor | None = None,
+                      total: torch.Tensor | None = None, stream=None):
+    """red_rmsnorm with y in 8 bits: ``kind`` "e4m3" (float8_e4m3fn) or "int8",
+    with a scale for each row (``block`` 0) or for each ``block`` (32, 64, 128
+    or 256) neighbouring values of it: y is about q * scale.  Returns (q,
+    scales, total, rstd), scales (rows, blocks) fp32."""
+    at, user = (None, None) if stream is None else _on(stream, x.device)
+    return _done((_entry or _losses()).rmsnorm_quant(x, weight, residual, eps, _kind(kind, _QUANT_KINDS), block, out,
+                                                     total, at), user, (out, total))
+
+
+def red_rmsnorm_grad(dy: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor | None = None,
+                     dtotal: torch.Tensor | None = None, grad: torch.Tensor | None = None, grad_weight=None,
+                     stream=None):
+    """Backward of red_rmsnorm: (grad, grad_weight) for the gradient ``dy`` by y,
+    with x the norm's input (total, where there was a residual), its rstd and
+    its weight.  ``dtotal``, the gradient that reaches x or total on other ways,
+    is added to grad, which is the residual's gradient, too.  ``grad``: a tensor
+    to write (dy, x or dtotal: in place).  ``grad_weight``: None for a new
+    tensor where there is a weight, a tensor to write, False for none."""
+    at, user = (None, None) if stream is None else _on(stream, x.device)
+    return _done((_entry or _losses()).rmsnorm_grad(dy, x, rstd, weight, dtotal, grad, grad_weight, at), user,
+                 (grad, grad_weight))
+
+
+# ------------------------------------------------------------ balance loss
+
+def red_balance(x: torch.Tensor, ids: torch.Tensor, live: torch.Tensor | None = None, coef: float = 1.0,
+                z_coef: float = 0.0, kind="softmax", grad_scale: float = 1.0, grad=None, stream=None):
+    """Balance loss of a router: x (rows, experts) logits of float32, float16 or
+    bfloat16, ids (rows, k) int64 the tokens' experts, live (rows) bool or uint8
+    the tokens that take part (None: all n).  With prob the mean of softmax(x)
+    (``kind`` "sigmoid": of sigmoid(x) over its sum), loss = coef * experts *
+    sum(counts / (k n) * prob) + z_coef * mean(logsumexp(x)**2).  Returns
+    (counts, prob, stats, grad): entries of ids per expert (int64), the means,
+    stats = (loss, its two parts without their coefficients, n), and grad_scale
+    times the gradient by x.  ``grad`` as for red_distill."""
+    at, user = (None, None) if stream is None else _on(stream, x.device)
+    return _done((_entry or _losses()).balance(x, ids, live, coef, z_coef, _kind(kind, _BALANCE_KINDS), grad_scale, grad,
+                                               at), user, (grad,))
 
 
 def red_set_full_mode(mode: int) -> None:

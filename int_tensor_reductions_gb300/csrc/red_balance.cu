@@ -1,0 +1,432 @@
+// red_balance.cu -- balance loss of a router of experts, with the experts'
+// counts and the gradient by the router's logits (red_balance).
+//
+// With n the tokens that take part and count_e the entries of their ids that
+// name expert e,
+//     share_e = count_e / (k n),  prob_e = mean over them of p_te,
+//     loss = coef * E * sum_e share_e prob_e + z_coef * mean lse_t^2.
+// The counts do not depend on the logits, and the gradient depends on the other
+// tokens through the counts alone:
+//     d loss / dp_te = c_e = coef E share_e / n,
+// so that after the counts one pass reads the logits, writes the gradient and
+// sums p.  Three kernels: counts (integer atomics: any order gives the same),
+// rows, and a join of the CTAs' sums; one CTA does all three where tokens are
+// few.  Bound by the logits' and the gradient's way through memory, or for
+// few tokens by latency.
+#include "red_balance.cuh"
+#include "red_groups.cuh"
+#include "red_prims.cuh"
+
+namespace red {
+namespace {
+
+// Workspace: counters of the experts and of the tokens (zero between calls) and a
+// ticket; sums per CTA.
+__device__ __forceinline__ unsigned *ticket_of(unsigned *tick) { return tick + RED_BALANCE_MAX_EXPERTS + 1; }
+
+constexpr int COUNT_NT = 256;
+
+// Adds the ids' entries to the counters in shared memory.
+__device__ __forceinline__ void count_ids(const BalanceArgs &a, unsigned *counts, unsigned *tokens, int64_t first,
+                                          int64_t step)
+{
+    const int64_t entries = a.rows * a.k;
+    unsigned mine = 0;
+    for (int64_t i = first; i < entries; i += step) {
+        // (below 2^31 entries: 32-bit division)
+        const unsigned row = (unsigned)i / (unsigned)a.k;
+        if (a.live && !a.live[row])
+            continue;
+        if (row * (unsigned)a.k == (unsigned)i)
+            ++mine;
+        const int64_t e = a.ids[i];
+        if (e >= 0 && e < a.experts)
+            atomicAdd(counts + e, 1u);
+    }
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (threadIdx.x % 32 == 0 && mine)
+        atomicAdd(tokens, mine);
+}
+
+__global__ void __launch_bounds__(COUNT_NT) balance_count_kernel(const BalanceArgs a)
+{
+    pdl_enter();
+    extern __shared__ unsigned counts[];  // experts, tokens
+    for (int e = threadIdx.x; e <= a.experts; e += COUNT_NT)
+        counts[e] = 0;
+    __syncthreads();
+    count_ids(a, counts, counts + a.experts, (int64_t)blockIdx.x * COUNT_NT + threadIdx.x, (int64_t)gridDim.x * COUNT_NT);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= a.experts; e += COUNT_NT)
+        if (counts[e])
+            atomicAdd(a.tick + (e < a.experts ? e : RED_BALANCE_MAX_EXPERTS), counts[e]);
+}
+
+// A lane's share of what the rows need: c_e (in units of grad_scale), and its sums.
+template <int VECS>
+struct RowSums {
+    float c[VECS][8], p[VECS][8];
+    float z;
+};
+
+__device__ __forceinline__ float tokens_of(unsigned n) { return (float)(n ? n : 1u); }
+
+template <int LANES, int VECS>
+__device__ __forceinline__ void begin_sums(const BalanceArgs &a, RowSums<VECS> &s, const unsigned *counts, float n, int lane)
+{
+    const float unit = a.coef * a.grad_scale * (float)a.experts / ((float)a.k * n * n);
+#pragma unroll
+    for (int v = 0; v < VECS; ++v)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int e = (v * LANES + lane) * 8 + k;
+            s.c[v][k] = e < a.experts ? (float)counts[e] * unit : 0.0f;
+            s.p[v][k] = 0.0f;
+        }
+    s.z = 0.0f;
+}
+
+// One token: its probabilities into the sums, its gradient to memory.  `here`:
+// there is such a token; a group without one goes along.
+template <int DT, bool SIGMOID, int LANES, int VECS, bool VEC>
+__device__ __forceinline__ void balance_row(const BalanceArgs &a, RowSums<VECS> &s, GroupShared<LANES> &sh, int &turn,
+                                            float z_unit, int64_t r, bool here, int lane)
+{
+    const bool takes = here && (!a.live || a.live[r]);
+    float x[VECS][8];
+    float top = NEG_INF;
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) {
+        const int i = (v * LANES + lane) * 8;
+        if (takes)
+            load8<DT, VEC>(a.x, r * a.ldx, i, a.experts, x[v]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (!takes || i + k >= a.experts)
+                x[v][k] = NEG_INF;
+            if (!SIGMOID)
+                top = Max()(top, x[v][k]);
+        }
+    }
+    float sum = 0.0f, off = 0.0f;  // (differences first: a row of the type's lowest value has no room for a product)
+    float e[VECS][8];  // exponentials, or sigmoids
+    if constexpr (!SIGMOID) {
+        top = group_fold<LANES>(top, sh, turn, Max());
+        off = top == NEG_INF ? 0.0f : top;
+    }
+#pragma unroll
+    for (int v = 0; v < VECS; ++v)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            e[v][k] = SIGMOID ? __fdividef(1.0f, 1.0f + ex2(-x[v][k] * LOG2E)) : ex2((x[v][k] - off) * LOG2E);
+            if (SIGMOID && x[v][k] == NEG_INF)
+                e[v][k] = 0.0f;
+            sum += e[v][k];
+        }
+    sum = group_fold<LANES>(sum, sh, turn, Add());
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // nothing but -inf: no probabilities
+    float d = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VECS; ++v)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float p = e[v][k] * inv;
+            s.p[v][k] += p;
+            d = fmaf(p, s.c[v][k], d);
+            x[v][k] = p;
+        }
+    float by_lse = 0.0f;
+    if constexpr (!SIGMOID) {
+        const float lse = sum == 0.0f ? 0.0f : fmaf(log2f(sum), 0.6931471805599453f, off);
+        s.z = fmaf(lse, lse, s.z);
+        by_lse = z_unit * lse;
+    }
+    if (!a.dx)
+        return;
+    d = group_fold<LANES>(d, sh, turn, Add());
+    if (!here)
+        return;
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) {
+        float g[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float p = x[v][k];
+            g[k] = SIGMOID ? p * (1.0f - e[v][k]) * (s.c[v][k] - d) : p * (s.c[v][k] - d + by_lse);
+            if (!takes)
+                g[k] = 0.0f;
+        }
+        store8<DT, VEC>(a.dx, r * a.ldd, (v * LANES + lane) * 8, a.experts, g);
+    }
+}
+
+// The groups' sums of a CTA in `meet` (a row of LANES * VECS * 8 per warp, or per
+// CTA), ready for sum_of().
+template <int LANES, int VECS>
+__device__ __forceinline__ void meet_sums(RowSums<VECS> &s, float *meet, float *meet_z, int lane)
+{
+    constexpr int WIDTH = LANES * VECS * 8;
+    float *const row = LANES > 32 ? meet : meet + threadIdx.x / 32 * WIDTH;
+    if constexpr (LANES < 32) {
+#pragma unroll
+        for (int o = LANES; o < 32; o <<= 1) {
+#pragma unroll
+            for (int v = 0; v < VECS; ++v)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    s.p[v][k] += __shfl_xor_sync(0xffffffffu, s.p[v][k], o);
+            s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
+        }
+    }
+    if (LANES > 32 || threadIdx.x % 32 < LANES) {
+#pragma unroll
+        for (int v = 0; v < VECS; ++v)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                row[(v * LANES + lane) * 8 + k] = s.p[v][k];
+    }
+    if (LANES > 32 ? threadIdx.x == 0 : threadIdx.x % 32 == 0)
+        meet_z[LANES > 32 ? 0 : threadIdx.x / 32] = s.z;
+    __syncthreads();
+}
+template <int LANES, int VECS, int NT>
+__device__ __forceinline__ float sum_of(const float *meet, int e)
+{
+    float p = meet[e];
+    if constexpr (LANES <= 32) {
+#pragma unroll
+        for (int w = 1; w < NT / 32; ++w)
+            p += meet[w * LANES * VECS * 8 + e];
+    }
+    return p;
+}
+template <int LANES, int NT>
+__device__ __forceinline__ float sum_of_z(const float *meet_z)
+{
+    float z = meet_z[0];
+    if constexpr (LANES <= 32) {
+#pragma unroll
+        for (int w = 1; w < NT / 32; ++w)
+            z += meet_z[w];
+    }
+    return z;
+}
+
+template <int DT, bool SIGMOID, int LANES, int VECS, bool VEC>
+__global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const BalanceArgs a)
+{
+    pdl_enter();
+    constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
+    __shared__ GroupShared<LANES> sh;
+    __shared__ float meet[(LANES > 32 ? 1 : NT / 32) * LANES * VECS * 8], meet_z[NT / 32];
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    const float n = tokens_of(a.tick[RED_BALANCE_MAX_EXPERTS]);
+    RowSums<VECS> s;
+    begin_sums<LANES, VECS>(a, s, a.tick, n, lane);
+    const float z_unit = 2.0f * a.z_coef * a.grad_scale / n;
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += (int64_t)gridDim.x * GROUPS)
+        balance_row<DT, SIGMOID, LANES, VECS, VEC>(a, s, sh, turn, z_unit, r0 + group, r0 + group < a.rows, lane);
+    meet_sums<LANES, VECS>(s, meet, meet_z, lane);
+    float *const part = a.part + (int64_t)blockIdx.x * (a.experts + 1);
+    for (int e = threadIdx.x; e < a.experts; e += NT)
+        part[e] = sum_of<LANES, VECS, NT>(meet, e);
+    if (threadIdx.x == 0)
+        part[a.experts] = sum_of_z<LANES, NT>(meet_z);
+}
+
+// loss, its two parts and the tokens, from sum_e count_e * (sum of p_e) and the sum of lse^2.
+__device__ __forceinline__ void write_stats(const BalanceArgs &a, unsigned tokens, float dot, float z)
+{
+    const float n = tokens_of(tokens);
+    const float balance = dot * (float)a.experts / ((float)a.k * n * n);
+    z /= n;
+    a.stats[0] = a.z_coef == 0.0f ? a.coef * balance : fmaf(a.coef, balance, a.z_coef * z);  // (z may be infinite)
+    a.stats[1] = balance;
+    a.stats[2] = z;
+    a.stats[3] = (float)tokens;
+}
+
+// 32 experts per CTA by 8 lanes of parts; the last CTA does the totals and clears the counters.
+__global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a, int parts)
+{
+    pdl_enter();
+    __shared__ float sums[8][33];
+    __shared__ bool last;
+    const int e = blockIdx.x * 32 + threadIdx.x % 32, turn = threadIdx.x / 32;
+    const unsigned tokens = a.tick[RED_BALANCE_MAX_EXPERTS];
+    float p = 0.0f;
+    if (e <= a.experts) {
+#pragma unroll 4
+        for (int i = turn; i < parts; i += 8)
+            p += a.part[(int64_t)i * (a.experts + 1) + e];
+    }
+    sums[turn][threadIdx.x % 32] = p;
+    __syncthreads();
+    float *const terms = a.part + (int64_t)parts * (a.experts + 1);  // one per expert, and the sum of lse^2
+    if (turn == 0 && e <= a.experts) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k)
+            p += sums[k][threadIdx.x % 32];
+        if (e < a.experts) {
+            const unsigned count = a.tick[e];
+            a.counts[e] = count;
+            a.prob[e] = p / tokens_of(tokens);
+            terms[e] = (float)count * p;
+        } else {
+            terms[e] = p;
+        }
+        __threadfence();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = atomicAdd(ticket_of(a.tick), 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last)
+        return;
+    __threadfence();
+    float dot = 0.0f;
+    for (int i = threadIdx.x; i < a.experts; i += 256)
+        dot += __ldcg(terms + i);
+    for (int o = 16; o; o >>= 1)
+        dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (threadIdx.x % 32 == 0)
+        sums[0][threadIdx.x / 32] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        dot = 0.0f;
+        for (int k = 0; k < 8; ++k)
+            dot += sums[0][k];
+        write_stats(a, tokens, dot, __ldcg(terms + a.experts));
+        *ticket_of(a.tick) = 0;
+    }
+    for (int i = threadIdx.x; i <= a.experts; i += 256)
+        a.tick[i < a.experts ? i : RED_BALANCE_MAX_EXPERTS] = 0;
+}
+
+// Few tokens: one CTA counts, passes over the rows and joins, in shared memory.
+constexpr int FEW_THREADS = 1024;
+constexpr int FEW_EXPERTS = 256;
+
+template <int DT, bool SIGMOID, int LANES, bool VEC>
+__global__ void __launch_bounds__(FEW_THREADS) balance_few_kernel(const BalanceArgs a)
+{
+    pdl_enter();
+    constexpr int GROUPS = FEW_THREADS / LANES;
+    __shared__ GroupShared<LANES> sh;
+    __shared__ float meet[FEW_THREADS / 32 * LANES * 8], meet_z[FEW_THREADS / 32], dots[FEW_THREADS / 32];
+    __shared__ unsigned counts[FEW_EXPERTS], tokens;
+    const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    if (threadIdx.x < FEW_EXPERTS)
+        counts[threadIdx.x] = 0;
+    if (threadIdx.x == 0)
+        tokens = 0;
+    __syncthreads();
+    count_ids(a, counts, &tokens, threadIdx.x, FEW_THREADS);
+    __syncthreads();
+    const float n = tokens_of(tokens);
+    RowSums<1> s;
+    begin_sums<LANES, 1>(a, s, counts, n, lane);
+    const float z_unit = 2.0f * a.z_coef * a.grad_scale / n;
+    int turn = 0;
+    for (int64_t r0 = 0; r0 < a.rows; r0 += GROUPS)
+        balance_row<DT, SIGMOID, LANES, 1, VEC>(a, s, sh, turn, z_unit, r0 + group, r0 + group < a.rows, lane);
+    meet_sums<LANES, 1>(s, meet, meet_z, lane);
+    float dot = 0.0f;
+    if (threadIdx.x < a.experts) {
+        const float p = sum_of<LANES, 1, FEW_THREADS>(meet, threadIdx.x);
+        a.counts[threadIdx.x] = counts[threadIdx.x];
+        a.prob[threadIdx.x] = p / n;
+        dot = (float)counts[threadIdx.x] * p;
+    }
+    for (int o = 16; o; o >>= 1)
+        dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (threadIdx.x % 32 == 0)
+        dots[threadIdx.x / 32] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        dot = 0.0f;
+        for (int k = 0; k < FEW_EXPERTS / 32; ++k)
+            dot += dots[k];
+        write_stats(a, tokens, dot, sum_of_z<LANES, FEW_THREADS>(meet_z));
+    }
+}
+
+// One CTA does all of it up to this many logits.
+constexpr int64_t FEW_LOGITS = 1 << 16;
+
+template <int DT, bool SIGMOID, int LANES, int VECS, bool VEC>
+int launch_rows(BalanceArgs &a, cudaStream_t s)
+{
+    if constexpr (VECS == 1) {
+        if (a.rows * a.experts <= FEW_LOGITS) {
+            count_launches(1);
+            return cuda_fail(launch_pdl(balance_few_kernel<DT, SIGMOID, LANES, VEC>, dim3(1), dim3(FEW_THREADS), s, a),
+                             "balance_few");
+        }
+    }
+    static std::atomic<int> cache{0};
+    constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
+    DeviceInfo di;
+    int st = device_info(&di);
+    Workspace ws;
+    if (st == RED_OK)
+        st = get_workspace(&ws);
+    unsigned grid = 1;
+    if (st == RED_OK)
+        st = resident_grid(balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>, cache, NT, (a.rows + GROUPS - 1) / GROUPS,
+                           2 * (int64_t)di.sms, &grid);
+    if (st != RED_OK)
+        return st;
+    a.tick = ws.tick;
+    a.part = static_cast<float *>(ws.part);
+    const int64_t per = 8 * COUNT_NT, want = (a.rows * a.k + per - 1) / per;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(want < di.sms ? want : di.sms));
+    cfg.blockDim = dim3(COUNT_NT);
+    cfg.dynamicSmemBytes = (size_t)(a.experts + 1) * sizeof(unsigned);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    st = cuda_fail(cudaLaunchKernelEx(&cfg, balance_count_kernel, (const BalanceArgs)a), "balance_count");
+    if (st == RED_OK)
+        st = cuda_fail(launch_pdl(balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>, dim3(grid), dim3(NT), s, a),
+                       "balance_rows");
+    if (st == RED_OK)
+        st = cuda_fail(launch_pdl(balance_join_kernel, dim3((unsigned)(a.experts / 32 + 1)), dim3(256), s, a, (int)grid),
+                       "balance_join");
+    if (st == RED_OK)
+        count_launches(3);
+    return st;
+}
+
+template <int DT, bool SIGMOID>
+int launch_typed_balance(BalanceArgs &a, cudaStream_t s)
+{
+    const int elem = DT == RED_F32 ? 4 : 2;
+    const bool vec = aligned_rows(a.x, a.ldx, a.rows, elem) && aligned_rows(a.dx, a.ldd, a.rows, elem);
+    return with_group((a.experts + 7) / 8, [&](auto lanes, auto vecs) {
+        constexpr int L = decltype(lanes)::value, V = decltype(vecs)::value;
+        if constexpr (L * V * 8 <= RED_BALANCE_MAX_EXPERTS)
+            return vec ? launch_rows<DT, SIGMOID, L, V, true>(a, s) : launch_rows<DT, SIGMOID, L, V, false>(a, s);
+        else
+            return fail(RED_EINVAL, "red_balance: too many experts");
+    });
+}
+
+}  // namespace
+
+int launch_balance(int dtype, BalanceArgs a, int kind, cudaStream_t s)
+{
+    const bool sigmoid = kind == RED_BALANCE_SIGMOID;
+    switch (dtype) {
+    case RED_F32: return sigmoid ? launch_typed_balance<RED_F32, true>(a, s) : launch_typed_balance<RED_F32, false>(a, s);
+    case RED_F16: return sigmoid ? launch_typed_balance<RED_F16, true>(a, s) : launch_typed_balance<RED_F16, false>(a, s);
+    default: return sigmoid ? launch_typed_balance<RED_BF16, true>(a, s) : launch_typed_balance<RED_BF16, false>(a, s);
+    }
+}
+
+}  // namespace red

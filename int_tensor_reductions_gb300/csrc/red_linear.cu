@@ -1,0 +1,863 @@
+// red_linear.cu -- log-probabilities of given tokens from hidden states h
+// (rows x dim) and the vocabulary's weights w (vocab x dim), and their
+// gradients, without the logits z = scale * h w^T ever being in memory.
+//
+//   forward    z tile by tile on the tensor cores; each tile leaves, per row,
+//              its maximum and its sum of exponentials (and the target's z);
+//              a join makes lse and logp of them.
+//   backward   piece by piece of the vocabulary: z again, from it the gradient
+//              by the logits,
+//                  g_j = dlogp ([j = target] - p_j) + dlse p_j,  p_j = e^(z_j - lse),
+//              in the inputs' 16-bit type, then the two products
+//                  dh += g w_piece,   dw_piece = g^T h,
+//              as tiles of one launch (both need nothing but g).
+//
+// Rows that do not take part are left out first: the others' hidden states are
+// packed, which saves their share of the products and keeps what padded
+// rows hold (NaN, say) out of dw.
+#include <cuda.h>
+
+#include "red_linear.cuh"
+#include "red_mma.cuh"
+
+namespace red {
+namespace {
+
+// Blocks of 64 of K whose products are summed by the tensor cores before the
+// sum moves to fp32 registers.  The tensor cores' additions round toward
+// zero, so a long sum drifts with its number of steps.
+constexpr int CHUNK = 8;
+// Rows of tiles that are taken in turn along the vocabulary.
+constexpr int BAND = 16;
+
+struct TileAt {
+    int m, n;
+};
+// Tile t of m_tiles x n_tiles: bands of BAND rows of tiles, in a band column by
+// column, so that the tiles at work share both operands in L2.
+__device__ __forceinline__ TileAt tile_at(int t, int m_tiles, int n_tiles)
+{
+    const int band = t / (BAND * n_tiles);
+    const int in = t - band * BAND * n_tiles;
+    const int high = min(BAND, m_tiles - band * BAND);
+    return {band * BAND + in % high, in / high};
+}
+
+// ------------------------------------------------------ rows that take part
+
+constexpr int SCAN_NT = 1024, SCAN_ROWS = 8;
+
+struct ScanArgs {
+    const int64_t *target;
+    int64_t rows, vocab;
+    const float *lse, *dlogp, *dlse;  // gradients only
+    float scale;
+    LinearWork w;
+};
+
+template <class V, class F>
+__device__ __forceinline__ V block_fold(V v, V *sh, F f)
+{
+    for (int o = 16; o; o >>= 1)
+        v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    __syncthreads();
+    if (threadIdx.x % 32 == 0)
+        sh[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = sh[threadIdx.x % 32];
+    for (int o = 16; o; o >>= 1)
+        v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// One CTA: which rows take part and, for the gradients, their coefficients,
+// divided by a power of two so that the largest is between 1 and 2 (f16 holds
+// nothing below 6e-8, and a mean over a batch has weights of 1e-4).
+template <bool GRAD>
+__global__ void __launch_bounds__(SCAN_NT) linear_scan_kernel(const ScanArgs a)
+{
+    pdl_enter();
+    __shared__ int sums[32];
+    __shared__ float tops[32];
+    const int tid = threadIdx.x;
+    auto coefs = [&](int64_t r, float &by_target, float &by_p) {
+        const float d = a.dlogp[r], n = a.dlse ? a.dlse[r] : 0.0f;
+        by_target = d * a.scale;
+        by_p = (n - d) * a.scale;
+        return !(d == 0.0f && n == 0.0f);
+    };
+    auto live = [&](int64_t r, float &by_target, float &by_p) {
+        if (r >= a.rows)
+            return false;
+        const int64_t t = a.target[r];
+        if (t < 0 || t >= a.vocab)
+            return false;
+        return GRAD ? coefs(r, by_target, by_p) : true;
+    };
+    float unit = 1.0f;
+    if constexpr (GRAD) {
+        float top = 0.0f;
+        for (int64_t r = tid; r < a.rows; r += SCAN_NT) {
+            float x = 0.0f, y = 0.0f;
+            if (live(r, x, y))
+                top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+        }
+        top = block_fold(top, tops, [](float x, float y) { return fmaxf(x, y); });
+        if (top > 0.0f && top < __builtin_huge_valf())
+            unit = exp2f(fminf(fmaxf((float)ilogbf(top), -120.0f), 120.0f));
+    }
+    const float inv = 1.0f / unit;
+    int before = 0;
+    for (int64_t r0 = 0; r0 < a.rows; r0 += SCAN_NT * SCAN_ROWS) {
+        const int64_t first = r0 + (int64_t)tid * SCAN_ROWS;
+        float ct[SCAN_ROWS], cp[SCAN_ROWS];
+        unsigned mask = 0;
+#pragma unroll
+        for (int i = 0; i < SCAN_ROWS; ++i) {
+            ct[i] = cp[i] = 0.0f;
+            if (live(first + i, ct[i], cp[i]))
+                mask |= 1u << i;
+        }
+        const int mine = __popc(mask);
+        int upto = mine;  // inclusive sum over the block
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (tid % 32 >= o)
+                upto += v;
+        }
+        __syncthreads();
+        if (tid % 32 == 31)
+            sums[tid / 32] = upto;
+        __syncthreads();
+        const int sum = sums[tid % 32];
+        int scan = sum;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, o);
+            if (tid % 32 >= o)
+                scan += v;
+        }
+        const int warps_before = __shfl_sync(0xffffffffu, scan - sum, tid / 32);
+        const int all = __shfl_sync(0xffffffffu, scan, 31);
+        int at = before + warps_before + upto - mine;
+#pragma unroll
+        for (int i = 0; i < SCAN_ROWS; ++i) {
+            const int64_t r = first + i;
+            if (r >= a.rows)
+                break;
+            if (!(mask >> i & 1)) {
+                a.w.pos[r] = -1;
+                continue;
+            }
+            a.w.pos[r] = at;
+            a.w.idx[at] = (int)r;
+            a.w.target[at] = (int)a.target[r];
+            if constexpr (GRAD) {
+                a.w.by_target[at] = ct[i] * inv;
+                a.w.by_p[at] = cp[i] * inv;
+                a.w.lse2[at] = a.lse[r] * LOG2E;
+            }
+            ++at;
+        }
+        before += all;
+    }
+    if (tid == 0) {
+        a.w.head->live = before;
+        a.w.head->unit = unit;
+    }
+}
+
+// The hidden states of the rows that take part, packed; a warp per row.  Zeros
+// up to a whole tile behind them.
+__global__ void __launch_bounds__(256) linear_pack_kernel(const void *hidden, int64_t dim, int64_t ldh, const LinearWork w)
+{
+    pdl_enter();
+    const int live = w.head->live;
+    const int64_t end = ((int64_t)live + TILE - 1) / TILE * TILE;
+    const int lane = threadIdx.x % 32;
+    const int64_t vecs = dim / 8;
+    const int tail = (int)(dim % 8);
+    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < end; r += (int64_t)gridDim.x * 8) {
+        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(w.hidden) + r * w.ld);
+        const uint16_t *from = r < live ? static_cast<const uint16_t *>(hidden) + (int64_t)w.idx[r] * ldh : nullptr;
+        const uint4 *v = reinterpret_cast<const uint4 *>(from);
+        int64_t i = lane;
+        for (; i + 96 < vecs && from; i += 128) {
+            const uint4 v0 = v[i], v1 = v[i + 32], v2 = v[i + 64], v3 = v[i + 96];
+            to[i] = v0;
+            to[i + 32] = v1;
+            to[i + 64] = v2;
+            to[i + 96] = v3;
+        }
+        for (; i < vecs; i += 32)
+            to[i] = from ? v[i] : make_uint4(0, 0, 0, 0);
+        if (lane < tail)
+            reinterpret_cast<uint16_t *>(to)[vecs * 8 + lane] = from ? from[vecs * 8 + lane] : (uint16_t)0;
+    }
+}
+
+// --------------------------------------------------------------- logit tiles
+
+struct LogitArgs {
+    CUtensorMap h, w, g;
+    LinearWork work;
+    int v0, n_tiles;   // columns of the vocabulary: the first, and tiles from it on
+    int vocab, k_blocks;
+    float s2;          // scale * log2(e)
+};
+
+// One warp's 32 rows x 128 columns of z / scale in fp32 registers: the sums of
+// the chunks.
+__device__ __forceinline__ void take_sums(float (&z)[HALF], MmaBarriers &b, AccPos &acc, int blocks, uint32_t lanes,
+                                          int half, uint32_t (&empty)[2])
+{
+    for (int k = 0; k < blocks; k += CHUNK) {
+        const bool ok = mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
+        tmem_after();
+        const uint32_t from = b.tmem + lanes + acc.slot * TILE + half * HALF;
+        if (!ok) {
+#pragma unroll
+            for (int i = 0; i < HALF; ++i)
+                z[i] = __int_as_float(0x7fffffff);
+        } else if (k == 0) {
+#pragma unroll
+            for (int i = 0; i < HALF; i += 16)
+                tmem_load16(from + i, reinterpret_cast<uint32_t *>(z + i));
+            tmem_wait();
+        } else {
+#pragma unroll
+            for (int i = 0; i < HALF; i += 16) {
+                uint32_t v[16];
+                tmem_load16(from + i, v);
+                tmem_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    z[i + j] += __uint_as_float(v[j]);
+            }
+        }
+        tmem_before();
+        __syncwarp();
+        if (threadIdx.x % 32 == 0)
+            arrive_at(empty[acc.slot]);
+        acc.next();
+    }
+}
+
+// Two floats as 16-bit values, the first in the low half.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (DT == RED_BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// GRAD: g of the tile to `piece`; else the tile's statistics to `part`.
+template <int DT, bool GRAD>
+__global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __grid_constant__ LogitArgs a)
+{
+    extern __shared__ unsigned char raw[];
+    __shared__ MmaBarriers b;
+    unsigned char *const ring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = cluster_rank();
+    mma_begin(b, warp, lane);
+    pdl_enter();
+    const int live = a.work.head->live;
+    const int m_tiles = (live + TILE - 1) / TILE;
+    const int tiles = m_tiles * a.n_tiles;
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+
+    auto job = [&](TileAt at) {
+        return TileJob{&a.h, &a.w, at.m * TILE, a.v0 + at.n * TILE, 0, 0, a.k_blocks, true, true};
+    };
+    if (warp < 4)
+        fewer_registers();
+    if (warp == 0 && lane == 0) {
+        RingPos pos;
+        for (int t = pair; t < tiles; t += pairs)
+            if (!copy_tile(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, rank)) {
+                drain_copies(b, pos, rank);
+                break;
+            }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        RingPos pos;
+        AccPos acc;
+        const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true);
+        for (int t = pair; t < tiles; t += pairs)
+            if (!multiply_tile(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, acc, idesc, CHUNK)) {
+                drain_products(b);
+                break;
+            }
+    } else if (warp >= 4) {
+        more_registers();  // the sums of a tile take 128 per thread
+        AccPos acc;
+        const int group = warp % 4, half = (warp - 4) / 4;
+        uint32_t empty[2] = {leader_addr(&b.acc_empty[0]), leader_addr(&b.acc_empty[1])};
+        unsigned char *const staging = ring + STAGES * STAGE_BYTES + (warp - 4) * STAGING_BYTES;
+        for (int t = pair; t < tiles; t += pairs) {
+            const TileAt at = tile_at(t, m_tiles, a.n_tiles);
+            const int row = at.m * TILE + rank * HALF + group * 32 + lane;
+            const int col = a.v0 + at.n * TILE + half * HALF;
+            const bool takes = row < live;
+            const int target = takes ? a.work.target[row] - col : -1;
+            const bool tail = col + HALF > a.vocab;
+            float z[HALF];
+            take_sums(z, b, acc, a.k_blocks, (uint32_t)(group * 32) << 16, half, empty);
+            if constexpr (!GRAD) {
+                if (tail) {
+#pragma unroll
+                    for (int i = 0; i < HALF; ++i)
+                        if (col + i >= a.vocab)
+                            z[i] = NEG_INF;
+                }
+                if (__any_sync(0xffffffffu, (unsigned)target < (unsigned)HALF)) {
+                    float zt = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < HALF; ++i)
+                        zt = i == target ? z[i] : zt;
+                    if ((unsigned)target < (unsigned)HALF)
+                        a.work.taken[row] = zt;
+                }
+                float m = NEG_INF;
+#pragma unroll
+                for (int i = 0; i < HALF; i += 2)
+                    m = fmaxf(m, fmaxf(z[i], z[i + 1]));
+                const float m2 = m * a.s2;
+                const float off = m == NEG_INF ? 0.0f : m2;
+                float l[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < HALF; ++i)
+                    l[i % 4] += ex2(fmaf(z[i], a.s2, -off));
+                if (takes)
+                    a.work.part[(int64_t)row * a.work.slots + (at.n * 2 + half)] =
+                        make_float2(m2, (l[0] + l[1]) + (l[2] + l[3]));
+            } else {
+                const float ct = takes ? a.work.by_target[row] : 0.0f;
+                const float cp = takes ? a.work.by_p[row] : 0.0f;
+                const float lse2 = takes ? a.work.lse2[row] : 0.0f;
+                const bool here = __any_sync(0xffffffffu, (unsigned)target < (unsigned)HALF);
+#pragma unroll
+                for (int i = 0; i < HALF; ++i)
+                    z[i] = cp * ex2(fmaf(z[i], a.s2, -lse2));
+                if (here) {
+#pragma unroll
+                    for (int i = 0; i < HALF; ++i)
+                        z[i] = i == target ? z[i] + ct : z[i];
+                }
+                if (tail) {
+#pragma unroll
+                    for (int i = 0; i < HALF; ++i)
+                        if (col + i >= a.vocab)
+                            z[i] = 0.0f;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    // 32 rows of 64 columns through shared memory, 16-byte units swizzled as the map says
+                    if (lane == 0)
+                        store_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const float *v = z + c * 64 + u * 8;
+                        *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) * 16)) =
+                            make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
+                                       pack2<DT>(v[6], v[7]));
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store(&a.g, at.n * TILE + half * HALF + c * 64, at.m * TILE + rank * HALF + group * 32,
+                                  staging);
+                        store_commit();
+                    }
+                }
+            }
+        }
+        if (GRAD && lane == 0)
+            store_done();
+    }
+    __syncwarp();
+    mma_end(b, warp);
+}
+
+// ----------------------------------------------------------- join of the parts
+
+// A warp per row: (maximum, sum) pairs of the tiles to lse and logp.
+__global__ void __launch_bounds__(256) linear_join_kernel(const LinearWork w, int64_t rows, float s2, float *logp, float *lse)
+{
+    pdl_enter();
+    const int lane = threadIdx.x % 32;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < rows; r += (int64_t)gridDim.x * 8) {
+        const int at = w.pos[r];
+        if (at < 0) {
+            if (lane == 0)
+                logp[r] = lse[r] = 0.0f;
+            continue;
+        }
+        const float2 *part = w.part + (int64_t)at * w.slots;
+        float m = NEG_INF, l = 0.0f;
+        for (int64_t i = lane; i < w.slots; i += 32) {
+            const float2 p = part[i];
+            const float top = fmaxf(m, p.x);
+            const float ref = top == NEG_INF ? 0.0f : top;
+            l = l * ex2(m - ref) + p.y * ex2(p.x - ref);
+            m = top;
+        }
+        for (int o = 16; o; o >>= 1) {
+            const float om = __shfl_xor_sync(0xffffffffu, m, o), ol = __shfl_xor_sync(0xffffffffu, l, o);
+            const float top = fmaxf(m, om);
+            const float ref = top == NEG_INF ? 0.0f : top;
+            l = l * ex2(m - ref) + ol * ex2(om - ref);
+            m = top;
+        }
+        if (lane == 0) {
+            constexpr float LN2 = 0.6931471805599453f;
+            const float log_l = log2f(l);
+            lse[r] = (m + log_l) * LN2;
+            logp[r] = (fmaf(w.taken[at], s2, -m) - log_l) * LN2;
+        }
+    }
+}
+
+// ------------------------------------------------------- products with weights
+
+struct ProductArgs {
+    CUtensorMap g_k;    // piece, along the vocabulary: boxes of 64 x 128        (dh: A)
+    CUtensorMap w_n;    // weights, along dim: boxes of 64 x 64                  (dh: B)
+    CUtensorMap g_m;    // piece: boxes of 64 (vocabulary) x 64 (rows)           (dw: A)
+    CUtensorMap h_n;    // packed hidden states, along dim: boxes of 64 x 64     (dw: B)
+    CUtensorMap dh, dw; // results: boxes of 32 x 32 fp32, 64 x 32 16-bit
+    LinearWork work;
+    int v0, v_count;    // the piece: first column of the vocabulary, columns
+    int n_tiles;        // along dim
+    int first;          // dh: store (1) or add (0)
+    uint16_t *dweight;  // dw's memory, for the end of rows that do not end on 16 bytes
+    int64_t lddw;
+    int dim, vocab;
+    int with_dh, with_dw;
+};
+
+// A warp's 32 rows x 128 columns of a product from tensor memory (`free`: the
+// barrier that gives the accumulators back; 0: there were no products, the sums
+// are 0) to memory, 128 bytes of each row at a time.
+template <int DT, bool DH>
+__device__ __forceinline__ void store_product(const ProductArgs &a, bool ok, uint32_t from, uint32_t free, int row,
+                                              int col, float unit, unsigned char *staging, int lane)
+{
+    constexpr int WIDTH = DH ? 32 : 64;
+#pragma unroll
+    for (int c = 0; c < HALF; c += WIDTH) {
+        float v[WIDTH];
+        if (free) {
+#pragma unroll
+            for (int i = 0; i < WIDTH; i += 16)
+                tmem_load16(from + c + i, reinterpret_cast<uint32_t *>(v + i));
+            tmem_wait();
+        } else {
+#pragma unroll
+            for (int i = 0; i < WIDTH; ++i)
+                v[i] = 0.0f;
+        }
+        if (!ok) {
+#pragma unroll
+            for (int i = 0; i < WIDTH; ++i)
+                v[i] = __int_as_float(0x7fffffff);
+        }
+        if (c + WIDTH == HALF && free) {
+            tmem_before();
+            __syncwarp();
+            if (lane == 0)
+                arrive_at(free);
+        }
+        if (!DH && a.dim % 8 != 0 && col + c < a.dim && col + c + WIDTH > a.dim) {
+            // (a map's box ends on 16 bytes, here beyond the row)
+            const int64_t r = (int64_t)a.v0 + row + lane;
+            if (r < a.vocab) {
+#pragma unroll
+                for (int i = 0; i < WIDTH; ++i)
+                    if (col + c + i < a.dim)
+                        a.dweight[r * a.lddw + col + c + i] = (uint16_t)pack2<DT>(v[i] * unit, 0.0f);
+            }
+            continue;
+        }
+        if (lane == 0)
+            store_read();
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            uint4 o;
+            if constexpr (DH) {
+                const float *x = v + u * 4;
+                o = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+            } else {
+                const float *x = v + u * 8;
+                o = make_uint4(pack2<DT>(x[0] * unit, x[1] * unit), pack2<DT>(x[2] * unit, x[3] * unit),
+                               pack2<DT>(x[4] * unit, x[5] * unit), pack2<DT>(x[6] * unit, x[7] * unit));
+            }
+            *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) * 16)) = o;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (DH && a.first)
+                tma_store(&a.dh, col + c, row, staging);
+            else if (DH)
+                tma_add(&a.dh, col + c, row, staging);
+            else
+                tma_store(&a.dw, col + c, a.v0 + row, staging);
+            store_commit();
+        }
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const __grid_constant__ ProductArgs a)
+{
+    extern __shared__ unsigned char raw[];
+    __shared__ MmaBarriers b;
+    unsigned char *const ring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = cluster_rank();
+    mma_begin(b, warp, lane);
+    pdl_enter();
+    const int live = a.work.head->live;
+    const int h_rows = a.with_dh ? (live + TILE - 1) / TILE : 0;
+    const int w_rows = a.with_dw ? (a.v_count + TILE - 1) / TILE : 0;
+    const int h_tiles = h_rows * a.n_tiles, tiles = h_tiles + w_rows * a.n_tiles;
+    const int v_blocks = (a.v_count + BLOCK_K - 1) / BLOCK_K, r_blocks = (live + BLOCK_K - 1) / BLOCK_K;
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+
+    auto job = [&](int t) {
+        if (t < h_tiles) {
+            const TileAt at = tile_at(t, h_rows, a.n_tiles);
+            return TileJob{&a.g_k, &a.w_n, at.m * TILE, at.n * TILE, 0, a.v0, v_blocks, true, false};
+        }
+        const TileAt at = tile_at(t - h_tiles, w_rows, a.n_tiles);
+        return TileJob{&a.g_m, &a.h_n, at.m * TILE, at.n * TILE, 0, 0, r_blocks, false, false};
+    };
+    if (warp == 0 && lane == 0) {
+        RingPos pos;
+        for (int t = pair; t < tiles; t += pairs)
+            if (!copy_tile(job(t), b, ring, pos, rank)) {
+                drain_copies(b, pos, rank);
+                break;
+            }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        RingPos pos;
+        AccPos acc;
+        for (int t = pair; t < tiles; t += pairs) {
+            const TileJob j = job(t);
+            if (!multiply_tile(j, b, ring, pos, acc, instruction_desc(DT == RED_BF16, j.a_along_k, j.b_along_k),
+                               1 << 30)) {
+                drain_products(b);
+                break;
+            }
+        }
+    } else if (warp >= 4) {
+        AccPos acc;
+        const int group = warp % 4, half = (warp - 4) / 4;
+        uint32_t empty[2] = {leader_addr(&b.acc_empty[0]), leader_addr(&b.acc_empty[1])};
+        unsigned char *const staging = ring + STAGES * STAGE_BYTES + (warp - 4) * STAGING_BYTES;
+        const float unit = a.work.head->unit;
+        for (int t = pair; t < tiles; t += pairs) {
+            const TileJob j = job(t);
+            const bool ok = j.blocks == 0 || mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
+            tmem_after();
+            const uint32_t from = b.tmem + ((uint32_t)(group * 32) << 16) + acc.slot * TILE + half * HALF;
+            const int row = j.a_row + rank * HALF + group * 32, col = j.b_row + half * HALF;
+            const uint32_t free = j.blocks == 0 ? 0 : empty[acc.slot];
+            if (t < h_tiles)
+                store_product<DT, true>(a, ok, from, free, row, col, unit, staging, lane);
+            else
+                store_product<DT, false>(a, ok, from, free, row, col, unit, staging, lane);
+            if (j.blocks != 0)
+                acc.next();
+        }
+        if (lane == 0)
+            store_done();
+    }
+    __syncwarp();
+    mma_end(b, warp);
+}
+
+// The sums of the pieces to the rows' gradients, rounded once; a warp per row.
+// Zeros where a row takes no part.
+template <int DT>
+__global__ void __launch_bounds__(256)
+    linear_scatter_kernel(const LinearWork w, int64_t rows, int64_t dim, uint16_t *dhidden, int64_t ldd)
+{
+    pdl_enter();
+    const int lane = threadIdx.x % 32;
+    const float unit = w.head->unit;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < rows; r += (int64_t)gridDim.x * 8) {
+        const int at = w.pos[r];
+        uint16_t *to = dhidden + r * ldd;
+        const float *from = w.dhidden + (int64_t)at * w.dim4;
+        const int64_t vecs = dim / 8;
+        for (int64_t i = lane; i < vecs; i += 32) {
+            uint4 o = make_uint4(0, 0, 0, 0);
+            if (at >= 0) {
+                const float4 x = reinterpret_cast<const float4 *>(from)[2 * i];
+                const float4 y = reinterpret_cast<const float4 *>(from)[2 * i + 1];
+                o = make_uint4(pack2<DT>(x.x * unit, x.y * unit), pack2<DT>(x.z * unit, x.w * unit),
+                               pack2<DT>(y.x * unit, y.y * unit), pack2<DT>(y.z * unit, y.w * unit));
+            }
+            reinterpret_cast<uint4 *>(to)[i] = o;
+        }
+        for (int64_t i = vecs * 8 + lane; i < dim; i += 32)
+            to[i] = at >= 0 ? (uint16_t)pack2<DT>(from[i] * unit, 0.0f) : (uint16_t)0;
+    }
+}
+
+// ------------------------------------------------------------------ launches
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
+{
+    static std::atomic<void *> cached{nullptr};
+    void *f = cached.load(std::memory_order_relaxed);
+    if (!f) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        cached.store(f, std::memory_order_relaxed);
+    }
+    return reinterpret_cast<EncodeFn>(f);
+}
+
+// A matrix of `outer` rows of `inner` elements, row stride ld elements, in boxes
+// with the 128-byte swizzle; what lies outside reads as zero and is not written.
+int matrix_map(CUtensorMap *map, int dtype, const void *base, int64_t inner, int64_t outer, int64_t ld, int box_inner,
+               int box_outer)
+{
+    const EncodeFn encode = encode_fn();
+    if (!encode)
+        return fail(RED_ECUDA, "the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t sizes[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * (dtype == RED_F32 ? 4 : 2)};
+    const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer}, step[2] = {1, 1};
+    const CUtensorMapDataType type = dtype == RED_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == RED_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult e = encode(map, type, 2, const_cast<void *>(base), sizes, strides, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return e == CUDA_SUCCESS ? RED_OK : fail(RED_ECUDA, "cuTensorMapEncodeTiled: error %d", (int)e);
+}
+
+#define RETURN_IF(call)            \
+    do {                           \
+        const int st_ = (call);    \
+        if (st_ != RED_OK)         \
+            return st_;            \
+    } while (0)
+
+constexpr int MAX_DEVICES = 64;
+
+// Pairs of CTAs of a kernel that run at once on the current device.
+template <class Args>
+int resident_pairs(void (*kernel)(const Args), std::atomic<int> (&cache)[MAX_DEVICES], int *pairs)
+{
+    DeviceInfo di;
+    RETURN_IF(device_info(&di));
+    int v = cache[di.dev].load(std::memory_order_relaxed);
+    if (v == 0) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MMA_SMEM);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "cudaFuncSetAttribute");
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)di.sms / 2 * 2);
+        cfg.blockDim = dim3(MMA_THREADS);
+        cfg.dynamicSmemBytes = MMA_SMEM;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&v, kernel, &cfg);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+        if (v < 1)
+            return fail(RED_ECUDA, "no pair of CTAs fits this device");
+        cache[di.dev].store(v, std::memory_order_relaxed);
+    }
+    *pairs = v;
+    return RED_OK;
+}
+
+template <class Args>
+int launch_pairs(void (*kernel)(const Args), std::atomic<int> (&cache)[MAX_DEVICES], int64_t tiles, cudaStream_t s,
+                 const Args &a, const char *what)
+{
+    int pairs;
+    RETURN_IF(resident_pairs(kernel, cache, &pairs));
+    if (tiles < pairs)
+        pairs = (int)tiles;
+    RETURN_IF(cuda_fail(launch_pdl_smem(kernel, 2u * (unsigned)pairs, MMA_THREADS, MMA_SMEM, 2, s, a), what));
+    count_launches(1);
+    return RED_OK;
+}
+
+template <int DT, bool GRAD>
+int launch_logits(int64_t tiles, cudaStream_t s, const LogitArgs &a)
+{
+    static std::atomic<int> cache[MAX_DEVICES];
+    return launch_pairs(linear_logits_kernel<DT, GRAD>, cache, tiles, s, a, "linear_logits");
+}
+template <int DT>
+int launch_products(int64_t tiles, cudaStream_t s, const ProductArgs &a)
+{
+    static std::atomic<int> cache[MAX_DEVICES];
+    return launch_pairs(linear_products_kernel<DT>, cache, tiles, s, a, "linear_products");
+}
+
+unsigned warp_rows_grid(int64_t rows) { return (unsigned)((rows + 7) / 8 < 65536 ? (rows + 7) / 8 : 65536); }
+
+template <bool GRAD>
+int pack_rows(const LinearArgs &a, const LinearWork &w, const float *lse, const float *dlogp, const float *dlse,
+              cudaStream_t s)
+{
+    const ScanArgs scan = {a.target, a.rows, a.vocab, lse, dlogp, dlse, a.scale, w};
+    RETURN_IF(cuda_fail(launch_pdl(linear_scan_kernel<GRAD>, dim3(1), dim3(SCAN_NT), s, scan), "linear_scan"));
+    RETURN_IF(cuda_fail(launch_pdl(linear_pack_kernel, dim3(warp_rows_grid(w.padded)), dim3(256), s, a.hidden, a.dim,
+                                   a.ldh, w),
+                        "linear_pack"));
+    count_launches(2);
+    return RED_OK;
+}
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+}  // namespace
+
+LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, bool grad)
+{
+    LinearWork w = {};
+    unsigned char *const p = static_cast<unsigned char *>(base);
+    int64_t at = 0;
+    auto take = [&](auto *&field, int64_t bytes) {
+        field = reinterpret_cast<std::remove_reference_t<decltype(field)>>(p + at);
+        at += up(bytes, 256);
+    };
+    w.padded = up(rows, TILE);
+    w.ld = up(dim, 8);
+    w.dim4 = up(dim, 4);
+    w.slots = up(vocab, TILE) / HALF;
+    take(w.head, sizeof(LinearHead));
+    take(w.pos, rows * 4);
+    take(w.idx, rows * 4);
+    take(w.target, rows * 4);
+    uint16_t *h, *g;
+    take(h, w.padded * w.ld * 2);
+    w.hidden = h;
+    if (!grad) {
+        take(w.taken, rows * 4);
+        take(w.part, rows * w.slots * 8);
+    } else {
+        // a piece's gradient by the logits takes 256 MB; pieces narrower than 4096 columns would
+        // pass over the sums of dh too often
+        int64_t cols = ((int64_t)1 << 27) / w.padded / TILE * TILE;
+        cols = cols < 4096 ? 4096 : cols;
+        w.piece_cols = cols < up(vocab, TILE) ? cols : up(vocab, TILE);
+        take(w.by_target, rows * 4);
+        take(w.by_p, rows * 4);
+        take(w.lse2, rows * 4);
+        take(g, w.padded * w.piece_cols * 2);
+        w.piece = g;
+        take(w.dhidden, w.padded * w.dim4 * 4);
+    }
+    w.bytes = at;
+    return w;
+}
+
+int launch_linear_logprob(const LinearArgs &a, float *logp, float *lse, void *work, cudaStream_t s)
+{
+    const LinearWork w = linear_work(work, a.rows, a.dim, a.vocab, false);
+    RETURN_IF(pack_rows<false>(a, w, nullptr, nullptr, nullptr, s));
+    LogitArgs l;
+    RETURN_IF(matrix_map(&l.h, a.dtype, w.hidden, a.dim, w.padded, w.ld, BLOCK_K, HALF));
+    RETURN_IF(matrix_map(&l.w, a.dtype, a.weight, a.dim, a.vocab, a.ldw, BLOCK_K, HALF));
+    l.g = l.w;
+    l.work = w;
+    l.v0 = 0;
+    l.n_tiles = (int)(up(a.vocab, TILE) / TILE);
+    l.vocab = (int)a.vocab;
+    l.k_blocks = (int)(up(a.dim, BLOCK_K) / BLOCK_K);
+    l.s2 = (float)(a.scale * 1.4426950408889634);
+    const int64_t tiles = w.padded / TILE * l.n_tiles;
+    RETURN_IF((a.dtype == RED_BF16 ? launch_logits<RED_BF16, false>(tiles, s, l) : launch_logits<RED_F16, false>(tiles, s, l)));
+    RETURN_IF(cuda_fail(launch_pdl(linear_join_kernel, dim3(warp_rows_grid(a.rows)), dim3(256), s, w, a.rows, l.s2, logp,
+                                   lse),
+                        "linear_join"));
+    count_launches(1);
+    return RED_OK;
+}
+
+int launch_linear_logprob_grad(const LinearArgs &a, const float *lse, const float *dlogp, const float *dlse,
+                               void *dhidden, int64_t ldd, void *dweight, int64_t lddw, void *work, cudaStream_t s)
+{
+    const LinearWork w = linear_work(work, a.rows, a.dim, a.vocab, true);
+    RETURN_IF(pack_rows<true>(a, w, lse, dlogp, dlse, s));
+    LogitArgs l;
+    ProductArgs p;
+    RETURN_IF(matrix_map(&l.h, a.dtype, w.hidden, a.dim, w.padded, w.ld, BLOCK_K, HALF));
+    RETURN_IF(matrix_map(&l.w, a.dtype, a.weight, a.dim, a.vocab, a.ldw, BLOCK_K, HALF));
+    RETURN_IF(matrix_map(&l.g, a.dtype, w.piece, w.piece_cols, w.padded, w.piece_cols, 64, 32));
+    RETURN_IF(matrix_map(&p.g_k, a.dtype, w.piece, w.piece_cols, w.padded, w.piece_cols, BLOCK_K, HALF));
+    RETURN_IF(matrix_map(&p.g_m, a.dtype, w.piece, w.piece_cols, w.padded, w.piece_cols, 64, BLOCK_K));
+    RETURN_IF(matrix_map(&p.w_n, a.dtype, a.weight, a.dim, a.vocab, a.ldw, 64, BLOCK_K));
+    RETURN_IF(matrix_map(&p.h_n, a.dtype, w.hidden, a.dim, w.padded, w.ld, 64, BLOCK_K));
+    RETURN_IF(matrix_map(&p.dh, RED_F32, w.dhidden, a.dim, w.padded, w.dim4, 32, 32));
+    if (dweight)
+        RETURN_IF(matrix_map(&p.dw, a.dtype, dweight, a.dim, a.vocab, lddw, 64, 32));
+    else
+        p.dw = p.w_n;
+    l.work = p.work = w;
+    l.vocab = (int)a.vocab;
+    l.k_blocks = (int)(up(a.dim, BLOCK_K) / BLOCK_K);
+    l.s2 = (float)(a.scale * 1.4426950408889634);
+    p.n_tiles = (int)(up(a.dim, TILE) / TILE);
+    p.with_dh = dhidden != nullptr;
+    p.with_dw = dweight != nullptr;
+    p.dweight = static_cast<uint16_t *>(dweight);
+    p.lddw = lddw;
+    p.dim = (int)a.dim;
+    p.vocab = (int)a.vocab;
+    for (int64_t v0 = 0; v0 < a.vocab; v0 += w.piece_cols) {
+        const int64_t count = a.vocab - v0 < w.piece_cols ? a.vocab - v0 : w.piece_cols;
+        l.v0 = p.v0 = (int)v0;
+        l.n_tiles = (int)(up(count, TILE) / TILE);
+        p.v_count = (int)count;
+        p.first = v0 == 0;
+        const int64_t m_tiles = w.padded / TILE;
+        const int64_t tiles = (p.with_dh ? m_tiles : 0) * p.n_tiles + (int64_t)(p.with_dw ? l.n_tiles : 0) * p.n_tiles;
+        if (a.dtype == RED_BF16) {
+            RETURN_IF((launch_logits<RED_BF16, true>(m_tiles * l.n_tiles, s, l)));
+            RETURN_IF(launch_products<RED_BF16>(tiles, s, p));
+        } else {
+            RETURN_IF((launch_logits<RED_F16, true>(m_tiles * l.n_tiles, s, l)));
+            RETURN_IF(launch_products<RED_F16>(tiles, s, p));
+        }
+    }
+    if (dhidden) {
+        auto *const kernel = a.dtype == RED_BF16 ? linear_scatter_kernel<RED_BF16> : linear_scatter_kernel<RED_F16>;
+        RETURN_IF(cuda_fail(launch_pdl(kernel, dim3(warp_rows_grid(a.rows)), dim3(256), s, w, a.rows, a.dim,
+                                       static_cast<uint16_t *>(dhidden), ldd),
+                            "linear_scatter"));
+        count_launches(1);
+    }
+    return RED_OK;
+}
+
+}  // namespace red

@@ -1,5 +1,5 @@
-// red_torch.cpp -- Python entry of the losses over rows of logits: torch
-// tensors to the C calls of red.h.
+// red_torch.cpp -- Python entry of the losses, of the root-mean-square norm and of
+// the balance loss: torch tensors to the C calls of red.h.
 //
 // One training step on a few rows, or the scoring of one token, takes the GPU
 // 2 to 10 us; checking and unpacking a dozen tensors and allocating the
@@ -78,23 +78,23 @@ struct Logits {
     int64_t rows, len, ld;
     int device;
 
-    explicit Logits(PyObject *o) : x(tensor(o, "x"))
+    explicit Logits(PyObject *o, const char *name = "x") : x(tensor(o, name))
     {
-        dtype = dtype_code(x.scalar_type(), "x");
+        dtype = dtype_code(x.scalar_type(), name);
         if (!x.is_cuda())
-            refuse("x must be a CUDA tensor");
+            refuse("%s must be a CUDA tensor", name);
         if (x.dim() != 2)
-            refuse("x must be 2-D (rows, vocab)");
+            refuse("%s must be 2-D (rows, columns)", name);
         rows = x.size(0);
         len = x.size(1);
-        ld = stride(x, "x");
+        ld = stride(x, name);
         device = x.get_device();
     }
     static int64_t stride(const at::Tensor &t, const char *name)
     {
         const int64_t rows = t.size(0), len = t.size(1);
         if (rows > 0 && len > 1 && t.stride(1) != 1)
-            refuse("%s's rows must be contiguous (stride 1 along the vocabulary)", name);
+            refuse("%s's rows must be contiguous (stride 1 along the columns)", name);
         const int64_t ld = rows > 1 ? t.stride(0) : len;
         if (ld < len)
             refuse("%s's row stride is smaller than its number of columns", name);
@@ -353,10 +353,266 @@ PyObject *preference(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
+// ------------------------------------- log-probabilities without the logits
+
+// Hidden states (rows, dim) and the vocabulary's weights (vocab, dim) beside
+// them.  Both need what the C call's tensor maps need: rows from 16-byte
+// boundaries on.
+struct Linear {
+    Logits h;
+    const at::Tensor &w;
+    int64_t vocab, ldw;
+
+    Linear(PyObject *hidden, PyObject *weight) : h(hidden, "hidden"), w(tensor(weight, "weight"))
+    {
+        if (h.dtype == RED_F32)
+            refuse("hidden must be float16 or bfloat16");
+        if (w.scalar_type() != h.x.scalar_type() || !w.is_cuda() || w.get_device() != h.device || w.dim() != 2 ||
+            w.size(1) != h.len)
+            refuse("weight must be (vocab, dim) of hidden's dtype, dim and device");
+        vocab = w.size(0);
+        ldw = Logits::stride(w, "weight");
+    }
+    // Scratch of a call (freed on return: the allocator keeps it for this stream's later work).
+    at::Tensor work(bool grad, int64_t *bytes) const
+    {
+        *bytes = red_linear_work_bytes(h.rows, h.len, vocab, grad);
+        return at::empty({*bytes < 0 ? 0 : *bytes}, h.x.options().dtype(at::kByte));
+    }
+    // A gradient: None for a new matrix (rows on 16-byte boundaries), False for none, or one to write.
+    struct Out {
+        at::Tensor t;
+        void *ptr = nullptr;
+        int64_t ld = 0;
+    };
+    Out out(PyObject *o, const at::Tensor &like, const char *name) const
+    {
+        Out g;
+        if (o == Py_False)
+            return g;
+        if (o == Py_None) {
+            const int64_t ld = (h.len + 7) / 8 * 8;
+            g.t = ld == h.len ? at::empty(like.sizes(), like.options())
+                              : at::empty_strided(like.sizes(), {ld, 1}, like.options());
+        } else {
+            g.t = tensor(o, name);
+            if (g.t.scalar_type() != like.scalar_type() || !g.t.is_cuda() || g.t.get_device() != h.device ||
+                g.t.sizes() != like.sizes())
+                refuse("%s must have the dtype, device and shape of what it is the gradient of", name);
+        }
+        g.ld = Logits::stride(g.t, name);
+        g.ptr = g.t.data_ptr();
+        return g;
+    }
+};
+
+// (hidden, weight, target, scale, stream)
+PyObject *linear_logprob(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded("linear_logprob", n, 5, [&] {
+        const Linear l(a[0], a[1]);
+        const OnStream on(a[4], l.h);
+        const int64_t *target = l.h.vector<int64_t>(a[2], "target", l.h.rows);
+        const auto [logp, lse] = float_vectors(l.h, {l.h.rows, l.h.rows});
+        int64_t bytes;
+        const at::Tensor work = l.work(false, &bytes);
+        RETURN_IF_REFUSED(red_linear_logprob(l.h.dtype, l.h.x.data_ptr(), l.h.rows, l.h.len, l.h.ld, l.w.data_ptr(),
+                                             l.vocab, l.ldw, (float)number(a[3]), target, data(logp), data(lse),
+                                             work.data_ptr(), bytes, on.stream));
+        return results(logp, lse);
+    });
+}
+
+// (hidden, weight, target, lse, dlogp, dlse, scale, grad_hidden, grad_weight, stream)
+PyObject *linear_logprob_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded("linear_logprob_grad", n, 10, [&] {
+        const Linear l(a[0], a[1]);
+        const OnStream on(a[9], l.h);
+        const int64_t rows = l.h.rows;
+        const int64_t *target = l.h.vector<int64_t>(a[2], "target", rows);
+        const float *lse = l.h.vector<float>(a[3], "lse", rows), *dlogp = l.h.vector<float>(a[4], "dlogp", rows);
+        const float *dlse = l.h.vector<float>(a[5], "dlse", rows);
+        const auto gh = l.out(a[7], l.h.x, "grad_hidden"), gw = l.out(a[8], l.w, "grad_weight");
+        int64_t bytes;
+        const at::Tensor work = l.work(true, &bytes);
+        RETURN_IF_REFUSED(red_linear_logprob_grad(l.h.dtype, l.h.x.data_ptr(), rows, l.h.len, l.h.ld, l.w.data_ptr(),
+                                                  l.vocab, l.ldw, (float)number(a[6]), target, lse, dlogp, dlse, gh.ptr,
+                                                  gh.ld, gw.ptr, gw.ld, work.data_ptr(), bytes, on.stream));
+        return results(gh.t, gw.t);
+    });
+}
+
+// ------------------------------------------------- root-mean-square norm
+
+// A matrix like x: dtype, device and shape; its row stride through *ld.
+const at::Tensor &beside(const Logits &l, PyObject *o, const char *name, int64_t *ld)
+{
+    const at::Tensor &t = tensor(o, name);
+    if (t.scalar_type() != l.x.scalar_type() || !t.is_cuda() || t.get_device() != l.device || t.sizes() != l.x.sizes())
+        refuse("%s must have x's dtype, device and shape", name);
+    *ld = Logits::stride(t, name);
+    return t;
+}
+// A new matrix in x's layout.
+at::Tensor new_rows(const Logits &l)
+{
+    return l.ld == l.len ? at::empty({l.rows, l.len}, l.x.options())
+                         : at::empty_strided({l.rows, l.len}, {l.ld, 1}, l.x.options());
+}
+// The weight (len values of x's type or fp32; None: 1) and its type.
+const void *norm_weight(const Logits &l, PyObject *o, int *wtype)
+{
+    *wtype = l.dtype;
+    if (o == Py_None)
+        return nullptr;
+    const at::Tensor &t = tensor(o, "weight");
+    *wtype = dtype_code(t.scalar_type(), "weight");
+    if (!t.is_cuda() || t.get_device() != l.device || t.numel() != l.len || !t.is_contiguous())
+        refuse("weight must be a contiguous vector of x's columns on x's device");
+    return t.data_ptr();
+}
+
+struct NormInputs {
+    Logits l;
+    const void *residual = nullptr, *weight;
+    int64_t ldr = 0, ldt = 0;
+    int wtype;
+    bool with_residual;  // (a matrix without rows has no address)
+    at::Tensor total, rstd;
+
+    NormInputs(PyObject *x, PyObject *w, PyObject *res) : l(x)
+    {
+        weight = norm_weight(l, w, &wtype);
+        with_residual = res != Py_None;
+        if (with_residual)
+            residual = beside(l, res, "residual", &ldr).data_ptr();
+    }
+    // After the stream is set: what the call allocates is that stream's.
+    void results(PyObject *given_total)
+    {
+        if (with_residual) {
+            total = given_total == Py_None ? new_rows(l) : beside(l, given_total, "total", &ldt);
+            ldt = Logits::stride(total, "total");
+        } else if (given_total != Py_None) {
+            refuse("total comes with a residual");
+        }
+        rstd = l.floats(l.rows);
+    }
+    void *total_ptr() const { return total.defined() ? total.data_ptr() : nullptr; }
+};
+
+// (x, weight, residual, eps, out, total, stream)
+PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded("rmsnorm", n, 7, [&] {
+        NormInputs in(a[0], a[1], a[2]);
+        const OnStream on(a[6], in.l);
+        int64_t ldy = in.l.ld;
+        const at::Tensor y = a[4] == Py_None ? new_rows(in.l) : beside(in.l, a[4], "out", &ldy);
+        in.results(a[5]);
+        RETURN_IF_REFUSED(red_rmsnorm(in.l.dtype, in.l.x.data_ptr(), in.l.rows, in.l.len, in.l.ld, in.residual, in.ldr,
+                                      in.wtype, in.weight, (float)number(a[3]), y.data_ptr(), ldy, in.total_ptr(),
+                                      in.ldt, data(in.rstd), on.stream));
+        return results(y, in.total, in.rstd);
+    });
+}
+
+// (x, weight, residual, eps, kind, block, out, total, stream)
+PyObject *rmsnorm_quant(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded("rmsnorm_quant", n, 9, [&] {
+        NormInputs in(a[0], a[1], a[2]);
+        const OnStream on(a[8], in.l);
+        const int kind = integer(a[4], "kind"), block = integer(a[5], "block");
+        const at::ScalarType type = kind == RED_QUANT_I8 ? at::kChar : at::kFloat8_e4m3fn;
+        at::Tensor q;
+        if (a[6] == Py_None) {
+            q = at::empty({in.l.rows, in.l.len}, in.l.x.options().dtype(type));
+        } else {
+            q = tensor(a[6], "out");
+            if (q.scalar_type() != type || !q.is_cuda() || q.get_device() != in.l.device || q.sizes() != in.l.x.sizes())
+                refuse("out must be of the 8-bit type, on x's device and of x's shape");
+        }
+        const int64_t blocks = block > 0 ? (in.l.len + block - 1) / block : 1;
+        const at::Tensor scales = at::empty({in.l.rows, blocks}, in.l.x.options().dtype(at::kFloat));
+        in.results(a[7]);
+        RETURN_IF_REFUSED(red_rmsnorm_quant(in.l.dtype, in.l.x.data_ptr(), in.l.rows, in.l.len, in.l.ld, in.residual,
+                                            in.ldr, in.wtype, in.weight, (float)number(a[3]), kind, block, q.data_ptr(),
+                                            Logits::stride(q, "out"), data(scales), in.total_ptr(), in.ldt,
+                                            data(in.rstd), on.stream));
+        return results(q, scales, in.total, in.rstd);
+    });
+}
+
+// (dy, x, rstd, weight, dtotal, grad, grad_weight, stream)
+PyObject *rmsnorm_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded("rmsnorm_grad", n, 8, [&] {
+        const Logits l(a[1]);
+        const OnStream on(a[7], l);
+        int64_t lddy, ldt = 0, ldd = l.ld;
+        const at::Tensor &dy = beside(l, a[0], "dy", &lddy);
+        const float *rstd = l.vector<float>(a[2], "rstd", l.rows);
+        int wtype;
+        const void *weight = norm_weight(l, a[3], &wtype);
+        const void *dtotal = a[4] == Py_None ? nullptr : beside(l, a[4], "dtotal", &ldt).data_ptr();
+        const at::Tensor dx = a[5] == Py_None ? new_rows(l) : beside(l, a[5], "grad", &ldd);
+        at::Tensor dw;
+        if (a[6] == Py_None) {
+            if (weight)
+                dw = at::empty({l.len}, tensor(a[3], "weight").options());
+        } else if (a[6] != Py_False) {
+            dw = tensor(a[6], "grad_weight");
+            if (dw.scalar_type() != (weight ? tensor(a[3], "weight") : l.x).scalar_type() || !dw.is_cuda() ||
+                dw.get_device() != l.device || dw.numel() != l.len || !dw.is_contiguous())
+                refuse("grad_weight must be a contiguous vector of weight's dtype, size and device");
+        }
+        RETURN_IF_REFUSED(red_rmsnorm_grad(l.dtype, dy.data_ptr(), lddy, l.x.data_ptr(), l.rows, l.len, l.ld, rstd, wtype,
+                                           weight, dtotal, ldt, dx.data_ptr(), ldd,
+                                           dw.defined() ? dw.data_ptr() : nullptr, on.stream));
+        return results(dx, dw);
+    });
+}
+
+// ------------------------------------------------------------ balance loss
+
+// (x, ids, live, coef, z_coef, kind, grad_scale, grad, stream)
+PyObject *balance(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    return guarded("balance", n, 9, [&] {
+        const Logits l(a[0]);
+        const OnStream on(a[8], l);
+        const at::Tensor &ids = tensor(a[1], "ids");
+        if (ids.dim() != 2 || ids.size(0) != l.rows)
+            refuse("ids must be (rows, k)");
+        const int64_t k = ids.size(1);
+        const int64_t *id = l.vector<int64_t>(a[1], "ids", l.rows * k);
+        const uint8_t *live = nullptr;
+        if (a[2] != Py_None) {
+            const at::Tensor &t = tensor(a[2], "live");
+            if ((t.scalar_type() != at::kBool && t.scalar_type() != at::kByte) || !t.is_cuda() ||
+                t.get_device() != l.device || t.numel() != l.rows || !t.is_contiguous())
+                refuse("live must be a contiguous vector of one bool or uint8 per row on x's device");
+            live = static_cast<const uint8_t *>(t.data_ptr());
+        }
+        const Gradient g(a[7], l, "grad");
+        const at::Tensor counts = at::empty({l.len}, l.x.options().dtype(at::kLong));
+        const auto [prob, stats] = float_vectors(l, {l.len, 4});
+        RETURN_IF_REFUSED(red_balance(l.dtype, l.x.data_ptr(), l.rows, l.len, l.ld, id, k, live,
+                                      integer(a[5], "kind"), (float)number(a[3]), (float)number(a[4]),
+                                      (float)number(a[6]), static_cast<int64_t *>(counts.data_ptr()), data(prob),
+                                      data(stats), g.ptr, g.ld, on.stream));
+        return results(counts, prob, stats, g.t);
+    });
+}
+
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(logprob), FAST(logprob_grad), FAST(distill), FAST(policy), FAST(preference),
+                         FAST(linear_logprob), FAST(linear_logprob_grad), FAST(rmsnorm),
+                         FAST(rmsnorm_quant), FAST(rmsnorm_grad), FAST(balance),
                          {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_red_torch", "Losses of libred.so on torch tensors.", -1, methods,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_red_torch", "Losses and norms of libred.so on torch tensors.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
