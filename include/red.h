@@ -503,7 +503,7 @@ int red_linear_logprob(int dtype, const void *hidden, int64_t rows, int64_t dim,
  *     dhidden = g * weight,  dweight = g^T * hidden,
  * with p_j = e^(z[r, j] - lse[r]), lse as red_linear_logprob left it.  A row
  * whose dlogp and dlse are both 0 is ignored, too.  The vocabulary is taken in
- * pieces; g is rounded to dtype once, against a power of two that the largest
+ * pieces; g is rounded to dtype once, in units that the largest
  * coefficient sets, and each result once more; their sums are fp32.
  *   dhidden  rows x dim, row stride ldd, or NULL for none.  May be `hidden`.
  *   dweight  vocab x dim, row stride lddw, or NULL for none (not both).

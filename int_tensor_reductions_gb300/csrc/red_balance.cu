@@ -26,22 +26,33 @@ __device__ __forceinline__ unsigned *ticket_of(unsigned *tick) { return tick + R
 
 constexpr int COUNT_NT = 256;
 
-// Adds the ids' entries to the counters in shared memory.
+// Adds the ids' entries to the counters in shared memory: eight loads at a time, and
+// what depends on them afterwards (one after the other they took 8 us of 500,000).
 __device__ __forceinline__ void count_ids(const BalanceArgs &a, unsigned *counts, unsigned *tokens, int64_t first,
                                           int64_t step)
 {
+    constexpr int BATCH = 8;
     const int64_t entries = a.rows * a.k;
     unsigned mine = 0;
-    for (int64_t i = first; i < entries; i += step) {
-        // (below 2^31 entries: 32-bit division)
-        const unsigned row = (unsigned)i / (unsigned)a.k;
-        if (a.live && !a.live[row])
-            continue;
-        if (row * (unsigned)a.k == (unsigned)i)
-            ++mine;
-        const int64_t e = a.ids[i];
-        if (e >= 0 && e < a.experts)
-            atomicAdd(counts + e, 1u);
+    for (int64_t i0 = first; i0 < entries; i0 += BATCH * step) {
+        int64_t id[BATCH];
+        unsigned takes = 0;
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int64_t i = i0 + b * step;
+            const bool in = i < entries;
+            id[b] = in ? a.ids[i] : -1;
+            // (below 2^31 entries: 32-bit division)
+            const unsigned row = (unsigned)i / (unsigned)a.k;
+            if (in && (!a.live || a.live[row])) {
+                takes |= 1u << b;
+                mine += row * (unsigned)a.k == (unsigned)i;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+            if ((takes >> b & 1) && id[b] >= 0 && id[b] < a.experts)
+                atomicAdd(counts + id[b], 1u);
     }
     mine = __reduce_add_sync(0xffffffffu, mine);
     if (threadIdx.x % 32 == 0 && mine)
@@ -69,6 +80,10 @@ struct RowSums {
     float z;
 };
 
+__device__ __forceinline__ bool takes_part(const BalanceArgs &a, int64_t r)
+{
+    return r < a.rows && (!a.live || a.live[r]);
+}
 __device__ __forceinline__ float tokens_of(unsigned n) { return (float)(n ? n : 1u); }
 
 template <int LANES, int VECS>
@@ -86,20 +101,19 @@ __device__ __forceinline__ void begin_sums(const BalanceArgs &a, RowSums<VECS> &
     s.z = 0.0f;
 }
 
-// One token: its probabilities into the sums, its gradient to memory.  `here`:
-// there is such a token; a group without one goes along.
+// One token's logits: its probabilities into the sums, its gradient to memory.
+// `here`: there is such a token; a group without one goes along.
 template <int DT, bool SIGMOID, int LANES, int VECS, bool VEC>
-__device__ __forceinline__ void balance_row(const BalanceArgs &a, RowSums<VECS> &s, GroupShared<LANES> &sh, int &turn,
-                                            float z_unit, int64_t r, bool here, int lane)
+__device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw<DT> (&raw)[VECS], RowSums<VECS> &s,
+                                            GroupShared<LANES> &sh, int &turn, float z_unit, int64_t r, bool here,
+                                            bool takes, int lane)
 {
-    const bool takes = here && (!a.live || a.live[r]);
     float x[VECS][8];
     float top = NEG_INF;
 #pragma unroll
     for (int v = 0; v < VECS; ++v) {
         const int i = (v * LANES + lane) * 8;
-        if (takes)
-            load8<DT, VEC>(a.x, r * a.ldx, i, a.experts, x[v]);
+        widen<DT>(raw[v], x[v]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             if (!takes || i + k >= a.experts)
@@ -219,14 +233,41 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const Ba
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
     __shared__ GroupShared<LANES> sh;
     __shared__ float meet[(LANES > 32 ? 1 : NT / 32) * LANES * VECS * 8], meet_z[NT / 32];
+    using Rows = Ring<DT, LANES, VECS, 1>;
+    extern __shared__ __align__(16) unsigned char ring[];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+    const int64_t step = (int64_t)gridDim.x * GROUPS, first = (int64_t)blockIdx.x * GROUPS + group;
+    auto fetch = [&](int64_t r, int to) {
+        if (r < a.rows)  // (one that is out is fetched, too: what says so is not known yet)
+            Rows::fetch(ring, to, 0, a.x, r * a.ldx, lane, a.experts);
+        fetch_commit();
+    };
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < Rows::STAGES - 1; ++k)
+            fetch(first + k * step, k);
+    }
     const float n = tokens_of(a.tick[RED_BALANCE_MAX_EXPERTS]);
     RowSums<VECS> s;
     begin_sums<LANES, VECS>(a, s, a.tick, n, lane);
     const float z_unit = 2.0f * a.z_coef * a.grad_scale / n;
-    int turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += (int64_t)gridDim.x * GROUPS)
-        balance_row<DT, SIGMOID, LANES, VECS, VEC>(a, s, sh, turn, z_unit, r0 + group, r0 + group < a.rows, lane);
+    int turn = 0, stage = 0;
+    bool next_takes = takes_part(a, first);
+    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += step) {
+        const int64_t r = r0 + group;
+        const bool takes = next_takes;
+        next_takes = takes_part(a, r + step);
+        Raw<DT> raw[VECS];
+        if constexpr (VEC) {
+            fetch(r + (Rows::STAGES - 1) * step, (stage + Rows::STAGES - 1) % Rows::STAGES);
+            fetch_wait<Rows::STAGES - 1>();
+            Rows::take(raw, ring, stage, 0);
+            stage = (stage + 1) % Rows::STAGES;
+        } else {
+            load_row<DT, VEC, LANES>(raw, a.x, takes ? r * a.ldx : 0, lane, takes ? a.experts : 0);
+        }
+        balance_row<DT, SIGMOID, LANES, VECS, VEC>(a, raw, s, sh, turn, z_unit, r, r < a.rows, takes, lane);
+    }
     meet_sums<LANES, VECS>(s, meet, meet_z, lane);
     float *const part = a.part + (int64_t)blockIdx.x * (a.experts + 1);
     for (int e = threadIdx.x; e < a.experts; e += NT)
@@ -321,6 +362,10 @@ __global__ void __launch_bounds__(FEW_THREADS) balance_few_kernel(const BalanceA
         counts[threadIdx.x] = 0;
     if (threadIdx.x == 0)
         tokens = 0;
+    // the first token's logits are on their way while the ids are counted, the next one's while one is at work
+    Raw<DT> next[1];
+    bool next_takes = takes_part(a, group);
+    load_row<DT, VEC, LANES>(next, a.x, next_takes ? group * a.ldx : 0, lane, next_takes ? a.experts : 0);
     __syncthreads();
     count_ids(a, counts, &tokens, threadIdx.x, FEW_THREADS);
     __syncthreads();
@@ -329,8 +374,14 @@ __global__ void __launch_bounds__(FEW_THREADS) balance_few_kernel(const BalanceA
     begin_sums<LANES, 1>(a, s, counts, n, lane);
     const float z_unit = 2.0f * a.z_coef * a.grad_scale / n;
     int turn = 0;
-    for (int64_t r0 = 0; r0 < a.rows; r0 += GROUPS)
-        balance_row<DT, SIGMOID, LANES, 1, VEC>(a, s, sh, turn, z_unit, r0 + group, r0 + group < a.rows, lane);
+    for (int64_t r0 = 0; r0 < a.rows; r0 += GROUPS) {
+        const int64_t r = r0 + group;
+        const Raw<DT> raw[1] = {next[0]};
+        const bool takes = next_takes;
+        next_takes = takes_part(a, r + GROUPS);
+        load_row<DT, VEC, LANES>(next, a.x, next_takes ? (r + GROUPS) * a.ldx : 0, lane, next_takes ? a.experts : 0);
+        balance_row<DT, SIGMOID, LANES, 1, VEC>(a, raw, s, sh, turn, z_unit, r, r < a.rows, takes, lane);
+    }
     meet_sums<LANES, 1>(s, meet, meet_z, lane);
     float dot = 0.0f;
     if (threadIdx.x < a.experts) {
@@ -365,41 +416,37 @@ int launch_rows(BalanceArgs &a, cudaStream_t s)
                              "balance_few");
         }
     }
-    static std::atomic<int> cache{0};
+    static Resident cache;
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
     DeviceInfo di;
     int st = device_info(&di);
     Workspace ws;
     if (st == RED_OK)
         st = get_workspace(&ws);
+    constexpr size_t SMEM = VEC ? Ring<DT, LANES, VECS, 1>::BYTES : 0;
     unsigned grid = 1;
     if (st == RED_OK)
-        st = resident_grid(balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>, cache, NT, (a.rows + GROUPS - 1) / GROUPS,
-                           2 * (int64_t)di.sms, &grid);
+        st = resident_grid(balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>, cache, NT, SMEM,
+                           (a.rows + GROUPS - 1) / GROUPS, (int64_t)(WS_PART_ELEMS / (size_t)(a.experts + 1)) - 1, &grid);
     if (st != RED_OK)
         return st;
     a.tick = ws.tick;
     a.part = static_cast<float *>(ws.part);
     const int64_t per = 8 * COUNT_NT, want = (a.rows * a.k + per - 1) / per;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(want < di.sms ? want : di.sms));
-    cfg.blockDim = dim3(COUNT_NT);
-    cfg.dynamicSmemBytes = (size_t)(a.experts + 1) * sizeof(unsigned);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    st = cuda_fail(cudaLaunchKernelEx(&cfg, balance_count_kernel, (const BalanceArgs)a), "balance_count");
+    st = cuda_fail(launch_pdl_dynamic(balance_count_kernel, dim3((unsigned)(want < di.sms ? want : di.sms)), dim3(COUNT_NT),
+                                      (size_t)(a.experts + 1) * sizeof(unsigned), s, a),
+                   "balance_count");
     if (st == RED_OK)
-        st = cuda_fail(launch_pdl(balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>, dim3(grid), dim3(NT), s, a),
+        st = cuda_fail(launch_pdl_dynamic(balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>, dim3(grid), dim3(NT), SMEM, s,
+                                          a),
                        "balance_rows");
     if (st == RED_OK)
         st = cuda_fail(launch_pdl(balance_join_kernel, dim3((unsigned)(a.experts / 32 + 1)), dim3(256), s, a, (int)grid),
                        "balance_join");
     if (st == RED_OK)
         count_launches(3);
+    else  // the next call finds the counters as they were
+        cudaMemsetAsync(a.tick, 0, (RED_BALANCE_MAX_EXPERTS + 2) * sizeof(unsigned), s);
     return st;
 }
 

@@ -12,48 +12,105 @@
 
 namespace red {
 
+// Threads of a CTA: one group, or several in 256.
+template <int LANES>
+constexpr int GROUP_CTA = LANES > 32 ? LANES : 256;
+
 // ------------------------------------------------------------- row access
 
-// Eight consecutive elements from i on; those at or behind len are 0.
-template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const void *p, int64_t row, int i, int len, float (&v)[8])
+// Eight elements as they lie in memory.
+template <int DT>
+struct Raw {
+    uint32_t u[DT == RED_F32 ? 8 : 4];
+};
+
+template <int DT>
+__device__ __forceinline__ void widen(const Raw<DT> &r, float (&v)[8])
 {
-    if (VEC && i + 8 <= len) {
-        if constexpr (DT == RED_F32) {
-            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + row + i);
-            const float4 a = q[0], b = q[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + row + i);
-            const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+    if constexpr (DT == RED_F32) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[2 * k] = Elem<DT>::widen(u[k] & 0xffffu);
-                v[2 * k + 1] = Elem<DT>::widen(u[k] >> 16);
+        for (int k = 0; k < 8; ++k)
+            v[k] = __uint_as_float(r.u[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[2 * k] = Elem<DT>::widen(r.u[k] & 0xffffu);
+            v[2 * k + 1] = Elem<DT>::widen(r.u[k] >> 16);
+        }
+    }
+}
+template <int DT>
+__device__ __forceinline__ Raw<DT> narrow(const float (&v)[8])
+{
+    Raw<DT> r;
+    if constexpr (DT == RED_F32) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            r.u[k] = __float_as_uint(v[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            r.u[k] = (uint32_t)Elem<DT>::narrow(v[2 * k]) | (uint32_t)Elem<DT>::narrow(v[2 * k + 1]) << 16;
+    }
+    return r;
+}
+
+template <int DT>
+__device__ __forceinline__ Raw<DT> load_some(const void *p, int64_t at, int n)
+{
+    Raw<DT> r;
+#pragma unroll
+    for (int k = 0; k < (DT == RED_F32 ? 8 : 4); ++k) {
+        if constexpr (DT == RED_F32) {
+            r.u[k] = k < n ? static_cast<const uint32_t *>(p)[at + k] : 0u;
+        } else {
+            const uint16_t *q = static_cast<const uint16_t *>(p) + at;
+            r.u[k] = (2 * k < n ? (uint32_t)q[2 * k] : 0u) | (2 * k + 1 < n ? (uint32_t)q[2 * k + 1] << 16 : 0u);
+        }
+    }
+    return r;
+}
+
+// A lane's vectors of a row (`row`: the row's first element); 0 behind its end.
+// The loads are issued together: nothing here looks at what they bring.
+template <int DT, bool VEC, int LANES, int VECS>
+__device__ __forceinline__ void load_row(Raw<DT> (&r)[VECS], const void *p, int64_t row, int lane, int len)
+{
+    if constexpr (VEC) {
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+            const int i = (v * LANES + lane) * 8;
+            const bool full = i + 8 <= len;
+            constexpr int WORDS = DT == RED_F32 ? 8 : 4;
+            const uint4 *q =
+                reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + (row + i) * (DT == RED_F32 ? 4 : 2));
+#pragma unroll
+            for (int k = 0; k < WORDS; k += 4) {
+                const uint4 x = full ? q[k / 4] : make_uint4(0, 0, 0, 0);
+                r[v].u[k] = x.x, r[v].u[k + 1] = x.y, r[v].u[k + 2] = x.z, r[v].u[k + 3] = x.w;
             }
         }
-        return;
+        if (len % 8 == 0)
+            return;
     }
+    // elements one by one: of one lane's last vector, or of all
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        v[k] = i + k < len ? load_elem<DT>(p, row + i + k) : 0.0f;
+    for (int v = 0; v < VECS; ++v) {
+        const int i = (v * LANES + lane) * 8;
+        if (!VEC || (i < len && i + 8 > len))
+            r[v] = load_some<DT>(p, row + i, len - i);
+    }
 }
 
 template <int DT, bool VEC>
 __device__ __forceinline__ void store8(void *p, int64_t row, int i, int len, const float (&v)[8])
 {
     if (VEC && i + 8 <= len) {
-        if constexpr (DT == RED_F32) {
-            float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + row + i);
-            q[0] = make_float4(v[0], v[1], v[2], v[3]);
-            q[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            uint32_t u[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                u[k] = (uint32_t)Elem<DT>::narrow(v[2 * k]) | (uint32_t)Elem<DT>::narrow(v[2 * k + 1]) << 16;
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + row + i) = make_uint4(u[0], u[1], u[2], u[3]);
-        }
+        const Raw<DT> r = narrow<DT>(v);
+        uint4 *q = reinterpret_cast<uint4 *>(static_cast<char *>(p) + (row + i) * (DT == RED_F32 ? 4 : 2));
+        q[0] = make_uint4(r.u[0], r.u[1], r.u[2], r.u[3]);
+        if constexpr (DT == RED_F32)
+            q[1] = make_uint4(r.u[4], r.u[5], r.u[6], r.u[7]);
         return;
     }
 #pragma unroll
@@ -61,6 +118,65 @@ __device__ __forceinline__ void store8(void *p, int64_t row, int i, int len, con
         if (i + k < len)
             store_elem<DT>(p, row + i + k, v[k]);
 }
+
+// ------------------------------------------------------- rows fetched ahead
+
+__device__ __forceinline__ void fetch16(void *dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void fetch_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A ring of rows in shared memory, fetched while earlier rows are at work: each
+// thread fetches its own vectors of ARRAYS matrices and reads them back itself, so
+// that no barrier is needed.  Only rows on 16-byte boundaries go this way (VEC);
+// others are loaded when they are wanted.
+template <int DT, int LANES, int VECS, int ARRAYS>
+struct Ring {
+    static constexpr int NT = GROUP_CTA<LANES>, UNITS = DT == RED_F32 ? 2 : 1;
+    static constexpr int STAGE = ARRAYS * VECS * UNITS * NT * 16;
+    // up to four rows ahead in 100 KB, which lets two CTAs share an SM; two where a row takes as much
+    static constexpr int FIT = STAGE > 51200 ? 204800 / STAGE : 102400 / STAGE;
+    static constexpr int STAGES = FIT < 1 ? 1 : FIT > 4 ? 4 : FIT;
+    static constexpr size_t BYTES = (size_t)STAGE * STAGES;
+
+    static __device__ __forceinline__ uint4 *slot(unsigned char *ring, int stage, int array, int v)
+    {
+        return reinterpret_cast<uint4 *>(ring) + ((stage * ARRAYS + array) * VECS + v) * UNITS * NT + threadIdx.x;
+    }
+    static __device__ __forceinline__ void fetch(unsigned char *ring, int stage, int array, const void *p, int64_t row,
+                                                 int lane, int len)
+    {
+        constexpr int SIZE = DT == RED_F32 ? 4 : 2;
+#pragma unroll
+        for (int v = 0; v < VECS; ++v)
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+                const int i = (v * LANES + lane) * 8 + u * 4;  // (u > 0: fp32 alone)
+                const int left = (len - i) * SIZE;
+                const uint32_t bytes = left <= 0 ? 0 : left < 16 ? left : 16;
+                fetch16(slot(ring, stage, array, v) + u * NT,
+                        static_cast<const char *>(p) + (bytes ? (row + i) * SIZE : 0), bytes);
+            }
+    }
+    static __device__ __forceinline__ void take(Raw<DT> (&r)[VECS], unsigned char *ring, int stage, int array)
+    {
+#pragma unroll
+        for (int v = 0; v < VECS; ++v)
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+                const uint4 x = slot(ring, stage, array, v)[u * NT];
+                r[v].u[4 * u] = x.x, r[v].u[4 * u + 1] = x.y, r[v].u[4 * u + 2] = x.z, r[v].u[4 * u + 3] = x.w;
+            }
+    }
+};
 
 // ------------------------------------------------------------ group reduction
 
@@ -112,10 +228,6 @@ struct Max {  // NaN wins
     }
 };
 
-// Threads of a CTA: one group, or several in 256.
-template <int LANES>
-constexpr int GROUP_CTA = LANES > 32 ? LANES : 256;
-
 // The group of a row of `vecs` vectors (up to 2048).  Calls f with (lanes,
 // vectors per lane).
 template <class F>
@@ -135,10 +247,16 @@ int with_group(int vecs, F f)
         return RED_GROUP(32, 4);
     if (vecs <= 256)
         return RED_GROUP(128, 2);
+    if (vecs <= 384)
+        return RED_GROUP(128, 3);
     if (vecs <= 512)
         return RED_GROUP(256, 2);
+    if (vecs <= 768)
+        return RED_GROUP(256, 3);
     if (vecs <= 1024)
         return RED_GROUP(256, 4);
+    if (vecs <= 1536)
+        return RED_GROUP(512, 3);
     return RED_GROUP(512, 4);
 #undef RED_GROUP
 }
@@ -149,16 +267,32 @@ inline bool aligned_rows(const void *p, int64_t ld, int64_t rows, int elem)
     return !p || ((uintptr_t)p % 16 == 0 && (rows < 2 || ld * elem % 16 == 0));
 }
 
+// CTAs per SM of a kernel with `smem` bytes of dynamic shared memory, per device.
+struct Resident {
+    std::atomic<int> per_sm[64] = {};
+};
+
 // CTAs of a persistent grid: what is resident at once, or what there is to do.
 template <class K>
-int resident_grid(K kernel, std::atomic<int> &cache, int threads, int64_t ctas, int64_t most, unsigned *grid)
+int resident_grid(K kernel, Resident &cache, int threads, size_t smem, int64_t ctas, int64_t most, unsigned *grid)
 {
     DeviceInfo di;
     const int st = device_info(&di);
     if (st != RED_OK)
         return st;
-    const int per_sm = cached_occupancy(cache, (const void *)kernel, threads);
-    int64_t cap = (int64_t)(per_sm > 0 ? per_sm : 1) * di.sms;
+    int per_sm = cache.per_sm[di.dev].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        cudaError_t e = cudaSuccess;
+        if (smem > 0)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, (const void *)kernel, threads, smem);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "occupancy");
+        per_sm = per_sm > 0 ? per_sm : 1;
+        cache.per_sm[di.dev].store(per_sm, std::memory_order_relaxed);
+    }
+    int64_t cap = (int64_t)per_sm * di.sms;
     cap = cap < most ? cap : most;
     *grid = (unsigned)(ctas < cap ? ctas : cap);
     return RED_OK;

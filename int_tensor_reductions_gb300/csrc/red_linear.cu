@@ -70,9 +70,15 @@ __device__ __forceinline__ V block_fold(V v, V *sh, F f)
     return v;
 }
 
-// One CTA: which rows take part and, for the gradients, their coefficients,
-// divided by a power of two so that the largest is between 1 and 2 (f16 holds
-// nothing below 6e-8, and a mean over a batch has weights of 1e-4).
+// The largest coefficient of a call becomes this: the last bf16 below 2, where its
+// rounding is finest relative to the value.  The gradient by the target's logit,
+// -(1 - p) of the coefficient, is most of a row's gradient: with equal weights of 1 /
+// 6144, which are 1.33 times a power of two, the errors of dh were 1.53 times those of
+// rounding dh alone with a power of two as the unit, and are 1.15 times those with
+// this.  f16 holds nothing below 6e-8: coefficients of a mean need a unit anyway.
+constexpr float MOST = 1.9921875f;
+
+// One CTA: which rows take part and, for the gradients, their coefficients.
 template <bool GRAD>
 __global__ void __launch_bounds__(SCAN_NT) linear_scan_kernel(const ScanArgs a)
 {
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(SCAN_NT) linear_scan_kernel(const ScanArgs a)
         }
         top = block_fold(top, tops, [](float x, float y) { return fmaxf(x, y); });
         if (top > 0.0f && top < __builtin_huge_valf())
-            unit = exp2f(fminf(fmaxf((float)ilogbf(top), -120.0f), 120.0f));
+            unit = fminf(fmaxf(top, 1e-36f), 1e36f) / MOST;
     }
     const float inv = 1.0f / unit;
     int before = 0;

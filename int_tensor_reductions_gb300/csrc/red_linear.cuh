@@ -14,7 +14,7 @@ namespace red {
 // Device-side facts of a call, first in its workspace.
 struct LinearHead {
     int live;      // rows that take part
-    float unit;    // what the coefficients were divided by (a power of two; gradients)
+    float unit;    // what the coefficients were divided by (gradients)
 };
 
 // Workspace of a call: rows that take part, packed, and what the passes hand on.

@@ -9,7 +9,8 @@
 // memory once and that is what bounds them.  A group is 8 to 32 lanes of a warp
 // (rows of up to 1024) or a CTA (up to 16384); a lane holds up to four vectors
 // of eight consecutive elements.  Rows off the 16-byte boundaries go through the
-// same code with loads of one element.
+// same code with loads of one element.  Rows are fetched into shared memory while
+// earlier ones are at work (Ring in red_groups.cuh).
 //
 // The backward keeps each lane's share of dw in registers over all the rows of
 // its group; the groups' shares go to the workspace and a second kernel adds them
@@ -51,39 +52,58 @@ int rmsnorm_forward(const NormArgs &a, int kind, cudaStream_t s);
 template <int DT>
 int rmsnorm_backward(const NormGradArgs &a, int wtype, void *dw, cudaStream_t s);
 
-#ifdef RED_RMSNORM_DT  // the kernels, for one type of x
+#ifdef RED_RMSNORM_DT  // the kernels of one direction (RED_RMSNORM_BACKWARD), for one type of x
 
 namespace {
 
-// Eight weights, of x's type or fp32; 1 where there are none.
-template <int DT, bool VEC>
-__device__ __forceinline__ void load_weight(const void *w, bool wide, int i, int len, float (&v)[8])
-{
-    if (!w) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = 1.0f;
-    } else if (DT == RED_F32 || wide) {
-        load8<RED_F32, VEC>(w, 0, i, len, v);
-    } else {
-        load8<DT, VEC>(w, 0, i, len, v);
-    }
-}
+// A lane's weights, of x's type or fp32; 1 where there are none.  They are the same
+// for every row of a group and stay in registers.
+template <int DT, bool WIDE, bool VEC, int LANES, int VECS>
+struct Weights {
+    static constexpr int WT = WIDE ? RED_F32 : DT;
+    Raw<WT> raw[VECS];
 
+    __device__ __forceinline__ Weights(const void *w, int lane, int len)
+    {
+        load_row<WT, VEC, LANES>(raw, w, 0, lane, w ? len : 0);
+        if (!w) {
+            float ones[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+#pragma unroll
+            for (int v = 0; v < VECS; ++v)
+                raw[v] = narrow<WT>(ones);
+        }
+    }
+    __device__ __forceinline__ void at(int v, float (&w)[8]) const { widen<WT>(raw[v], w); }
+};
+
+#ifndef RED_RMSNORM_BACKWARD
 // ----------------------------------------------------------------- forward
 
 // The largest value of an 8-bit type.
 template <int KIND>
 constexpr float TOP = KIND == RED_QUANT_E4M3 ? 448.0f : 127.0f;
 
-// Eight 8-bit values, to nearest, beyond the largest: the largest.
+// The scale of values of at most `most`, and its inverse (finite where the scale
+// has none in fp32).
 template <int KIND>
-__device__ __forceinline__ uint64_t narrow8(const float (&v)[8], float scale)
+__device__ __forceinline__ float scale_of(float most, float *inv)
+{
+    const float scale = most == 0.0f ? 1.0f : most * (1.0f / TOP<KIND>);
+    *inv = fminf(__frcp_rn(scale), 3.402823466e38f);
+    return scale;
+}
+
+// Eight 8-bit values, to nearest, beyond the largest: the largest.  A product with
+// the scale's inverse: it is off by 1.5 units of fp32's last place, which moves one
+// value in a million across a border between two of 8 bits, and eight divisions
+// took more time than all else (16384 x 8192 bf16 295 us with them, DIVNOW without).
+template <int KIND>
+__device__ __forceinline__ uint64_t narrow8(const float (&v)[8], float inv)
 {
     uint64_t r = 0;
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
-        const float a = __fdiv_rn(v[k], scale), b = __fdiv_rn(v[k + 1], scale);
+        const float a = v[k] * inv, b = v[k + 1] * inv;
         uint32_t two;
         if constexpr (KIND == RED_QUANT_E4M3) {
             uint16_t h;
@@ -114,7 +134,7 @@ __device__ __forceinline__ void store_q(uint8_t *q, int64_t row, int i, int len,
 }
 
 // KIND: 0 for y in x's type, else the 8-bit type.
-template <int DT, int KIND, int LANES, int VECS, bool VEC>
+template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC>
 __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArgs a)
 {
     pdl_enter();
@@ -122,33 +142,36 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArg
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     int turn = 0;
+    const Weights<DT, WIDE, VEC, LANES, VECS> weights(a.weight, lane, a.len);
     // every group of a CTA takes part in the shuffles to the end
     for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += (int64_t)gridDim.x * GROUPS) {
         const bool here = r0 + group < a.rows;
         const int64_t r = here ? r0 + group : a.rows - 1;
+        Raw<DT> raw[VECS], res[VECS];
+        load_row<DT, VEC, LANES>(raw, a.x, r * a.ldx, lane, a.len);
+        if (a.residual)
+            load_row<DT, VEC, LANES>(res, a.residual, r * a.ldr, lane, a.len);
         float t[VECS][8];
         float sum = 0.0f;
 #pragma unroll
-        for (int v = 0; v < VECS; ++v)
-            load8<DT, VEC>(a.x, r * a.ldx, (v * LANES + lane) * 8, a.len, t[v]);
-        if (a.residual) {
-#pragma unroll
-            for (int v = 0; v < VECS; ++v) {
+        for (int v = 0; v < VECS; ++v) {
+            widen<DT>(raw[v], t[v]);
+            if (a.residual) {
                 float s[8];
-                const int i = (v * LANES + lane) * 8;
-                load8<DT, VEC>(a.residual, r * a.ldr, i, a.len, s);
+                widen<DT>(res[v], s);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     t[v][k] += s[k];
-                if (here)
-                    store8<DT, VEC>(a.total, r * a.ldt, i, a.len, t[v]);
             }
-        }
-#pragma unroll
-        for (int v = 0; v < VECS; ++v)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 sum = fmaf(t[v][k], t[v][k], sum);
+        }
+        if (a.residual && here) {
+#pragma unroll
+            for (int v = 0; v < VECS; ++v)
+                store8<DT, VEC>(a.total, r * a.ldt, (v * LANES + lane) * 8, a.len, t[v]);
+        }
         sum = group_fold<LANES>(sum, sh, turn, Add());
         const float rstd = __frsqrt_rn(fmaf(sum, a.inv_len, a.eps));
         if (a.rstd && lane == 0 && here)
@@ -158,7 +181,7 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArg
         for (int v = 0; v < VECS; ++v) {
             const int i = (v * LANES + lane) * 8;
             float w[8];
-            load_weight<DT, VEC>(a.weight, a.wide, i, a.len, w);
+            weights.at(v, w);
             float most = 0.0f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -174,11 +197,12 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArg
                 const int lanes = min(a.block / 8, LANES < 32 ? LANES : 32);
                 for (int o = lanes / 2; o; o >>= 1)
                     most = Max()(most, __shfl_xor_sync(0xffffffffu, most, o));
-                const float scale = most == 0.0f ? 1.0f : __fdiv_rn(most, TOP<KIND>);
+                float inv;
+                const float scale = scale_of<KIND>(most, &inv);
                 if (here && i < a.len) {
                     if (lane % lanes == 0)
                         a.scales[r * a.blocks + i / a.block] = scale;
-                    store_q<KIND>(static_cast<uint8_t *>(a.y), r * a.ldy, i, a.len, VEC, narrow8<KIND>(t[v], scale));
+                    store_q<KIND>(static_cast<uint8_t *>(a.y), r * a.ldy, i, a.len, VEC, narrow8<KIND>(t[v], inv));
                 }
             } else {
                 top = Max()(top, most);
@@ -186,22 +210,24 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArg
         }
         if (KIND != 0 && !a.block) {
             top = group_fold<LANES>(top, sh, turn, Max());
-            const float scale = top == 0.0f ? 1.0f : __fdiv_rn(top, TOP<KIND>);
+            float inv;
+            const float scale = scale_of<KIND>(top, &inv);
             if (here) {
                 if (lane == 0)
                     a.scales[r] = scale;
 #pragma unroll
                 for (int v = 0; v < VECS; ++v)
                     store_q<KIND>(static_cast<uint8_t *>(a.y), r * a.ldy, (v * LANES + lane) * 8, a.len, VEC,
-                                  narrow8<KIND>(t[v], scale));
+                                  narrow8<KIND>(t[v], inv));
             }
         }
     }
 }
 
+#else
 // ---------------------------------------------------------------- backward
 
-template <int DT, int LANES, int VECS, bool VEC>
+template <int DT, bool WIDE, int LANES, int VECS, bool VEC>
 __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_grad_kernel(const NormGradArgs a)
 {
     pdl_enter();
@@ -209,57 +235,89 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_grad_kernel(const No
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
     // groups of one warp or less meet in shared memory before the workspace
     __shared__ float meet[GROUPS > 1 ? VECS * LANES * 8 : 1];
+    using Rows = Ring<DT, LANES, VECS, 3>;
+    extern __shared__ __align__(16) unsigned char ring[];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-    int turn = 0;
+    const int64_t step = (int64_t)gridDim.x * GROUPS, first = (int64_t)blockIdx.x * GROUPS + group;
+    int turn = 0, stage = 0;
+    auto fetch = [&](int64_t r, int to) {
+        if (r < a.rows) {
+            Rows::fetch(ring, to, 0, a.x, r * a.ldx, lane, a.len);
+            Rows::fetch(ring, to, 1, a.dy, r * a.ldy, lane, a.len);
+            if (a.dtotal)
+                Rows::fetch(ring, to, 2, a.dtotal, r * a.ldt, lane, a.len);
+        }
+        fetch_commit();
+    };
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < Rows::STAGES - 1; ++k)
+            fetch(first + k * step, k);
+    }
+    const Weights<DT, WIDE, VEC, LANES, VECS> weights(a.weight, lane, a.len);
     float dw[VECS][8];
 #pragma unroll
     for (int v = 0; v < VECS; ++v)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             dw[v][k] = 0.0f;
-    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += (int64_t)gridDim.x * GROUPS) {
+    float rstd_next = first < a.rows ? a.rstd[first] : 0.0f;
+    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += step) {
         const bool here = r0 + group < a.rows;
         const int64_t r = here ? r0 + group : a.rows - 1;
-        const float rstd = a.rstd[r];
-        float h[VECS][8], g[VECS][8];
+        Raw<DT> x[VECS], dy[VECS], dt[VECS];
+        const float rstd = rstd_next;
+        if (r0 + group + step < a.rows)
+            rstd_next = a.rstd[r0 + group + step];
+        if constexpr (VEC) {
+            fetch(r0 + group + (Rows::STAGES - 1) * step, (stage + Rows::STAGES - 1) % Rows::STAGES);
+            fetch_wait<Rows::STAGES - 1>();
+            Rows::take(x, ring, stage, 0);
+            Rows::take(dy, ring, stage, 1);
+        } else {
+            load_row<DT, VEC, LANES>(x, a.x, r * a.ldx, lane, a.len);
+            load_row<DT, VEC, LANES>(dy, a.dy, r * a.ldy, lane, a.len);
+            if (a.dtotal)
+                load_row<DT, VEC, LANES>(dt, a.dtotal, r * a.ldt, lane, a.len);
+        }
         float c = 0.0f;
 #pragma unroll
         for (int v = 0; v < VECS; ++v) {
-            load8<DT, VEC>(a.x, r * a.ldx, (v * LANES + lane) * 8, a.len, h[v]);
-            load8<DT, VEC>(a.dy, r * a.ldy, (v * LANES + lane) * 8, a.len, g[v]);
-        }
-#pragma unroll
-        for (int v = 0; v < VECS; ++v) {
-            const int i = (v * LANES + lane) * 8;
-            float w[8];
-            load_weight<DT, VEC>(a.weight, a.wide, i, a.len, w);
+            float h[8], g[8], w[8];
+            widen<DT>(x[v], h);
+            widen<DT>(dy[v], g);
+            weights.at(v, w);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                h[v][k] *= rstd;
+                h[k] *= rstd;
                 if (here)
-                    dw[v][k] = fmaf(g[v][k], h[v][k], dw[v][k]);
-                g[v][k] *= w[k];
-                c = fmaf(g[v][k], h[v][k], c);
+                    dw[v][k] = fmaf(g[k], h[k], dw[v][k]);
+                c = fmaf(g[k] * w[k], h[k], c);
             }
         }
         c = group_fold<LANES>(c, sh, turn, Add()) * a.inv_len;
+        if constexpr (VEC) {
+            if (a.dtotal)
+                Rows::take(dt, ring, stage, 2);
+            stage = (stage + 1) % Rows::STAGES;
+        }
         if (!here)
             continue;
+        // h and g again, from what the loads brought: registers for them would be other rows' loads in flight
 #pragma unroll
         for (int v = 0; v < VECS; ++v) {
-            const int i = (v * LANES + lane) * 8;
-            float d[8];
-            if (a.dtotal) {
-                load8<DT, VEC>(a.dtotal, r * a.ldt, i, a.len, d);
+            float h[8], g[8], w[8], d[8];
+            widen<DT>(x[v], h);
+            widen<DT>(dy[v], g);
+            weights.at(v, w);
+            if (a.dtotal)
+                widen<DT>(dt[v], d);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    d[k] = fmaf(fmaf(-h[v][k], c, g[v][k]), rstd, d[k]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    d[k] = fmaf(-h[v][k], c, g[v][k]) * rstd;
+            for (int k = 0; k < 8; ++k) {
+                const float n = fmaf(-h[k] * rstd, c, g[k] * w[k]);
+                d[k] = a.dtotal ? fmaf(n, rstd, d[k]) : n * rstd;
             }
-            store8<DT, VEC>(a.dx, r * a.ldd, i, a.len, d);
+            store8<DT, VEC>(a.dx, r * a.ldd, (v * LANES + lane) * 8, a.len, d);
         }
     }
     if (!a.part)
@@ -322,29 +380,62 @@ __global__ void __launch_bounds__(256) rmsnorm_join_kernel(const float *part, in
     }
 }
 
+#endif
+
 // ---------------------------------------------------------------- launches
 
-template <int DT, int KIND, int LANES, int VECS, bool VEC>
+#ifndef RED_RMSNORM_BACKWARD
+template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC>
 int forward(const NormArgs &a, cudaStream_t s)
 {
-    static std::atomic<int> cache{0};
+    static Resident cache;
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
     unsigned grid;
-    const int st = resident_grid(rmsnorm_kernel<DT, KIND, LANES, VECS, VEC>, cache, NT, (a.rows + GROUPS - 1) / GROUPS,
+    const int st = resident_grid(rmsnorm_kernel<DT, WIDE, KIND, LANES, VECS, VEC>, cache, NT, 0, (a.rows + GROUPS - 1) / GROUPS,
                            INT32_MAX, &grid);
     if (st != RED_OK)
         return st;
     count_launches(1);
-    return cuda_fail(launch_pdl(rmsnorm_kernel<DT, KIND, LANES, VECS, VEC>, dim3(grid), dim3(NT), s, a), "rmsnorm");
+    return cuda_fail(launch_pdl(rmsnorm_kernel<DT, WIDE, KIND, LANES, VECS, VEC>, dim3(grid), dim3(NT), s, a), "rmsnorm");
 }
 
-template <int DT, int LANES, int VECS, bool VEC>
+}  // namespace
+
+template <int DT, bool WIDE, bool VEC>
+int forward_of(const NormArgs &a, int kind, cudaStream_t s)
+{
+    return with_group((a.len + 7) / 8, [&](auto lanes, auto vecs) {
+        constexpr int L = decltype(lanes)::value, V = decltype(vecs)::value;
+        return kind == 0               ? forward<DT, WIDE, 0, L, V, VEC>(a, s)
+               : kind == RED_QUANT_E4M3 ? forward<DT, WIDE, RED_QUANT_E4M3, L, V, VEC>(a, s)
+                                        : forward<DT, WIDE, RED_QUANT_I8, L, V, VEC>(a, s);
+    });
+}
+
+template <int DT>
+int rmsnorm_forward(const NormArgs &a, int kind, cudaStream_t s)
+{
+    const int elem = DT == RED_F32 ? 4 : 2;
+    const bool vec = aligned_rows(a.x, a.ldx, a.rows, elem) && aligned_rows(a.residual, a.ldr, a.rows, elem) &&
+                     aligned_rows(a.total, a.ldt, a.rows, elem) && aligned_rows(a.weight, 0, 1, 1) &&
+                     (kind ? (uintptr_t)a.y % 8 == 0 && (a.rows < 2 || a.ldy % 8 == 0)
+                           : aligned_rows(a.y, a.ldy, a.rows, elem));
+    if (DT != RED_F32 && a.wide)
+        return vec ? forward_of<DT, true, true>(a, kind, s) : forward_of<DT, true, false>(a, kind, s);
+    return vec ? forward_of<DT, DT == RED_F32, true>(a, kind, s) : forward_of<DT, DT == RED_F32, false>(a, kind, s);
+}
+
+template int rmsnorm_forward<RED_RMSNORM_DT>(const NormArgs &, int, cudaStream_t);
+
+#else
+template <int DT, bool WIDE, int LANES, int VECS, bool VEC>
 int backward(NormGradArgs a, int wtype, void *dw, cudaStream_t s)
 {
-    static std::atomic<int> cache{0};
+    static Resident cache;
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
+    constexpr size_t SMEM = VEC ? Ring<DT, LANES, VECS, 3>::BYTES : 0;
     unsigned grid;
-    int st = resident_grid(rmsnorm_grad_kernel<DT, LANES, VECS, VEC>, cache, NT, (a.rows + GROUPS - 1) / GROUPS,
+    int st = resident_grid(rmsnorm_grad_kernel<DT, WIDE, LANES, VECS, VEC>, cache, NT, SMEM, (a.rows + GROUPS - 1) / GROUPS,
                      (int64_t)(WS_PART_ELEMS / (size_t)a.len), &grid);
     if (st != RED_OK)
         return st;
@@ -355,7 +446,7 @@ int backward(NormGradArgs a, int wtype, void *dw, cudaStream_t s)
             return st;
         a.part = static_cast<float *>(ws.part);
     }
-    st = cuda_fail(launch_pdl(rmsnorm_grad_kernel<DT, LANES, VECS, VEC>, dim3(grid), dim3(NT), s, a), "rmsnorm_grad");
+    st = cuda_fail(launch_pdl_dynamic(rmsnorm_grad_kernel<DT, WIDE, LANES, VECS, VEC>, dim3(grid), dim3(NT), SMEM, s, a), "rmsnorm_grad");
     if (st != RED_OK || !dw) {
         count_launches(1);
         return st;
@@ -368,22 +459,11 @@ int backward(NormGradArgs a, int wtype, void *dw, cudaStream_t s)
 
 }  // namespace
 
-template <int DT>
-int rmsnorm_forward(const NormArgs &a, int kind, cudaStream_t s)
+template <int DT, bool WIDE, bool VEC>
+int backward_of(const NormGradArgs &a, int wtype, void *dw, cudaStream_t s)
 {
-    const int elem = DT == RED_F32 ? 4 : 2;
-    const bool vec = aligned_rows(a.x, a.ldx, a.rows, elem) && aligned_rows(a.residual, a.ldr, a.rows, elem) &&
-                     aligned_rows(a.total, a.ldt, a.rows, elem) && aligned_rows(a.weight, 0, 1, 1) &&
-                     (kind ? (uintptr_t)a.y % 8 == 0 && (a.rows < 2 || a.ldy % 8 == 0) : aligned_rows(a.y, a.ldy, a.rows, elem));
     return with_group((a.len + 7) / 8, [&](auto lanes, auto vecs) {
-        constexpr int L = decltype(lanes)::value, V = decltype(vecs)::value;
-        switch (kind) {
-        case 0: return vec ? forward<DT, 0, L, V, true>(a, s) : forward<DT, 0, L, V, false>(a, s);
-        case RED_QUANT_E4M3:
-            return vec ? forward<DT, RED_QUANT_E4M3, L, V, true>(a, s) : forward<DT, RED_QUANT_E4M3, L, V, false>(a, s);
-        default:
-            return vec ? forward<DT, RED_QUANT_I8, L, V, true>(a, s) : forward<DT, RED_QUANT_I8, L, V, false>(a, s);
-        }
+        return backward<DT, WIDE, decltype(lanes)::value, decltype(vecs)::value, VEC>(a, wtype, dw, s);
     });
 }
 
@@ -394,15 +474,15 @@ int rmsnorm_backward(const NormGradArgs &a, int wtype, void *dw, cudaStream_t s)
     const bool vec = aligned_rows(a.x, a.ldx, a.rows, elem) && aligned_rows(a.dy, a.ldy, a.rows, elem) &&
                      aligned_rows(a.dtotal, a.ldt, a.rows, elem) && aligned_rows(a.dx, a.ldd, a.rows, elem) &&
                      aligned_rows(a.weight, 0, 1, 1);
-    return with_group((a.len + 7) / 8, [&](auto lanes, auto vecs) {
-        constexpr int L = decltype(lanes)::value, V = decltype(vecs)::value;
-        return vec ? backward<DT, L, V, true>(a, wtype, dw, s) : backward<DT, L, V, false>(a, wtype, dw, s);
-    });
+    if (DT != RED_F32 && a.wide)
+        return vec ? backward_of<DT, true, true>(a, wtype, dw, s) : backward_of<DT, true, false>(a, wtype, dw, s);
+    return vec ? backward_of<DT, DT == RED_F32, true>(a, wtype, dw, s)
+               : backward_of<DT, DT == RED_F32, false>(a, wtype, dw, s);
 }
 
-template int rmsnorm_forward<RED_RMSNORM_DT>(const NormArgs &, int, cudaStream_t);
 template int rmsnorm_backward<RED_RMSNORM_DT>(const NormGradArgs &, int, void *, cudaStream_t);
 
+#endif
 #endif
 
 }  // namespace red
