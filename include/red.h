@@ -551,8 +551,8 @@ enum red_quant {
 
 /*
  * red_rmsnorm_quant -- the same with y in 8 bits and a scale for each `block`
- * neighbouring values of a row (32, 64, 128 or 256; the last block of a row may
- * be shorter), or for each row (block = 0):
+ * neighbouring values of a row (32, 64 or 128; the last block of a row may be
+ * shorter), or for each row (block = 0):
  *     scale = max |y| / (448 or 127), 1 where that is 0;  q = y / scale, to nearest (ties to even).
  *   q        rows x len bytes, row stride ldq;
  *   scales   rows x ceil(len / block) floats (rows floats for block = 0).

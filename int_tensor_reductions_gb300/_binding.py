@@ -531,8 +531,8 @@ def red_rmsnorm_quant(x: torch.Tensor, weight: torch.Tensor | None = None, resid
                       eps: float = 1e-6, kind="e4m3", block: int = 0, out: torch.Tensor | None = None,
                       total: torch.Tensor | None = None, stream=None):
     """red_rmsnorm with y in 8 bits: ``kind`` "e4m3" (float8_e4m3fn) or "int8",
-    with a scale for each row (``block`` 0) or for each ``block`` (32, 64, 128
-    or 256) neighbouring values of it: y is about q * scale.  Returns (q,
+    with a scale for each row (``block`` 0) or for each ``block`` (32, 64
+    or 128) neighbouring values of it: y is about q * scale.  Returns (q,
     scales, total, rstd), scales (rows, blocks) fp32."""
     at, user = (None, None) if stream is None else _on(stream, x.device)
     return _done((_entry or _losses()).rmsnorm_quant(x, weight, residual, eps, _kind(kind, _QUANT_KINDS), block, out,

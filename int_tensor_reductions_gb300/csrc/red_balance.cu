@@ -24,7 +24,7 @@ namespace {
 // ticket; sums per CTA.
 __device__ __forceinline__ unsigned *ticket_of(unsigned *tick) { return tick + RED_BALANCE_MAX_EXPERTS + 1; }
 
-constexpr int COUNT_NT = 256;
+constexpr int COUNT_NT = 1024;
 
 // Adds the ids' entries to the counters in shared memory: eight loads at a time, and
 // what depends on them afterwards (one after the other they took 8 us of 500,000).
@@ -74,9 +74,9 @@ __global__ void __launch_bounds__(COUNT_NT) balance_count_kernel(const BalanceAr
 }
 
 // A lane's share of what the rows need: c_e (in units of grad_scale), and its sums.
-template <int VECS>
+template <int N, int E>
 struct RowSums {
-    float c[VECS][8], p[VECS][8];
+    float c[N][E], p[N][E];
     float z;
 };
 
@@ -86,15 +86,15 @@ __device__ __forceinline__ bool takes_part(const BalanceArgs &a, int64_t r)
 }
 __device__ __forceinline__ float tokens_of(unsigned n) { return (float)(n ? n : 1u); }
 
-template <int LANES, int VECS>
-__device__ __forceinline__ void begin_sums(const BalanceArgs &a, RowSums<VECS> &s, const unsigned *counts, float n, int lane)
+template <int LANES, int N, int E>
+__device__ __forceinline__ void begin_sums(const BalanceArgs &a, RowSums<N, E> &s, const unsigned *counts, float n, int lane)
 {
     const float unit = a.coef * a.grad_scale * (float)a.experts / ((float)a.k * n * n);
 #pragma unroll
-    for (int v = 0; v < VECS; ++v)
+    for (int v = 0; v < N; ++v)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int e = (v * LANES + lane) * 8 + k;
+        for (int k = 0; k < E; ++k) {
+            const int e = (v * LANES + lane) * E + k;
             s.c[v][k] = e < a.experts ? (float)counts[e] * unit : 0.0f;
             s.p[v][k] = 0.0f;
         }
@@ -103,35 +103,39 @@ __device__ __forceinline__ void begin_sums(const BalanceArgs &a, RowSums<VECS> &
 
 // One token's logits: its probabilities into the sums, its gradient to memory.
 // `here`: there is such a token; a group without one goes along.
-template <int DT, bool SIGMOID, int LANES, int VECS, bool VEC>
-__device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw<DT> (&raw)[VECS], RowSums<VECS> &s,
+template <int DT, bool SIGMOID, int LANES, bool VEC, int N, int E>
+__device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&raw)[N], RowSums<N, E> &s,
                                             GroupShared<LANES> &sh, int &turn, float z_unit, int64_t r, bool here,
                                             bool takes, int lane)
 {
-    float x[VECS][8];
+    float x[N][E];
     float top = NEG_INF;
 #pragma unroll
-    for (int v = 0; v < VECS; ++v) {
-        const int i = (v * LANES + lane) * 8;
+    for (int v = 0; v < N; ++v) {
+        const int i = (v * LANES + lane) * E;
         widen<DT>(raw[v], x[v]);
+        if (i + E > a.experts) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (!takes || i + k >= a.experts)
-                x[v][k] = NEG_INF;
-            if (!SIGMOID)
+            for (int k = 0; k < E; ++k)
+                if (i + k >= a.experts)
+                    x[v][k] = NEG_INF;
+        }
+        if (!SIGMOID) {
+#pragma unroll
+            for (int k = 0; k < E; ++k)
                 top = Max()(top, x[v][k]);
         }
     }
     float sum = 0.0f, off = 0.0f;  // (differences first: a row of the type's lowest value has no room for a product)
-    float e[VECS][8];  // exponentials, or sigmoids
+    float e[N][E];  // exponentials, or sigmoids
     if constexpr (!SIGMOID) {
         top = group_fold<LANES>(top, sh, turn, Max());
         off = top == NEG_INF ? 0.0f : top;
     }
 #pragma unroll
-    for (int v = 0; v < VECS; ++v)
+    for (int v = 0; v < N; ++v)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < E; ++k) {
             e[v][k] = SIGMOID ? __fdividef(1.0f, 1.0f + ex2(-x[v][k] * LOG2E)) : ex2((x[v][k] - off) * LOG2E);
             if (SIGMOID && x[v][k] == NEG_INF)
                 e[v][k] = 0.0f;
@@ -139,15 +143,27 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw<DT> 
         }
     sum = group_fold<LANES>(sum, sh, turn, Add());
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // nothing but -inf: no probabilities
+    if (!takes) {  // (its results so far are not looked at: they may be NaN)
+#pragma unroll
+        for (int v = 0; v < N; ++v)
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+                x[v][k] = e[v][k] = 0.0f;
+        sum = 0.0f;
+    } else {
+#pragma unroll
+        for (int v = 0; v < N; ++v)
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+                x[v][k] = e[v][k] * inv;
+    }
     float d = 0.0f;
 #pragma unroll
-    for (int v = 0; v < VECS; ++v)
+    for (int v = 0; v < N; ++v)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float p = e[v][k] * inv;
-            s.p[v][k] += p;
-            d = fmaf(p, s.c[v][k], d);
-            x[v][k] = p;
+        for (int k = 0; k < E; ++k) {
+            s.p[v][k] += x[v][k];
+            d = fmaf(x[v][k], s.c[v][k], d);
         }
     float by_lse = 0.0f;
     if constexpr (!SIGMOID) {
@@ -160,44 +176,43 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw<DT> 
     d = group_fold<LANES>(d, sh, turn, Add());
     if (!here)
         return;
+    const float shift = by_lse - d;
 #pragma unroll
-    for (int v = 0; v < VECS; ++v) {
-        float g[8];
+    for (int v = 0; v < N; ++v) {
+        float g[E];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < E; ++k) {
             const float p = x[v][k];
-            g[k] = SIGMOID ? p * (1.0f - e[v][k]) * (s.c[v][k] - d) : p * (s.c[v][k] - d + by_lse);
-            if (!takes)
-                g[k] = 0.0f;
+            g[k] = SIGMOID ? p * (1.0f - e[v][k]) * (s.c[v][k] - d) : p * (s.c[v][k] + shift);
         }
-        store8<DT, VEC>(a.dx, r * a.ldd, (v * LANES + lane) * 8, a.experts, g);
+        store_unit<DT, VEC>(a.dx, r * a.ldd, (v * LANES + lane) * E, a.experts, g);
     }
 }
 
 // The groups' sums of a CTA in `meet` (a row of LANES * VECS * 8 per warp, or per
 // CTA), ready for sum_of().
-template <int LANES, int VECS>
-__device__ __forceinline__ void meet_sums(RowSums<VECS> &s, float *meet, float *meet_z, int lane)
+template <int LANES, int N, int E>
+__device__ __forceinline__ void meet_sums(RowSums<N, E> &s, float *meet, float *meet_z, int lane)
 {
-    constexpr int WIDTH = LANES * VECS * 8;
+    constexpr int WIDTH = LANES * N * E;
     float *const row = LANES > 32 ? meet : meet + threadIdx.x / 32 * WIDTH;
     if constexpr (LANES < 32) {
 #pragma unroll
         for (int o = LANES; o < 32; o <<= 1) {
 #pragma unroll
-            for (int v = 0; v < VECS; ++v)
+            for (int v = 0; v < N; ++v)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < E; ++k)
                     s.p[v][k] += __shfl_xor_sync(0xffffffffu, s.p[v][k], o);
             s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
         }
     }
     if (LANES > 32 || threadIdx.x % 32 < LANES) {
 #pragma unroll
-        for (int v = 0; v < VECS; ++v)
+        for (int v = 0; v < N; ++v)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                row[(v * LANES + lane) * 8 + k] = s.p[v][k];
+            for (int k = 0; k < E; ++k)
+                row[(v * LANES + lane) * E + k] = s.p[v][k];
     }
     if (LANES > 32 ? threadIdx.x == 0 : threadIdx.x % 32 == 0)
         meet_z[LANES > 32 ? 0 : threadIdx.x / 32] = s.z;
@@ -230,10 +245,10 @@ template <int DT, bool SIGMOID, int LANES, int VECS, bool VEC>
 __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const BalanceArgs a)
 {
     pdl_enter();
-    constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
+    constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES, N = UNITS<DT, VECS>, E = UNIT<DT>;
     __shared__ GroupShared<LANES> sh;
     __shared__ float meet[(LANES > 32 ? 1 : NT / 32) * LANES * VECS * 8], meet_z[NT / 32];
-    using Rows = Ring<DT, LANES, VECS, 1>;
+    using Rows = Ring<DT, LANES, UNITS<DT, VECS>, 1>;
     extern __shared__ __align__(16) unsigned char ring[];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const int64_t step = (int64_t)gridDim.x * GROUPS, first = (int64_t)blockIdx.x * GROUPS + group;
@@ -248,8 +263,8 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const Ba
             fetch(first + k * step, k);
     }
     const float n = tokens_of(a.tick[RED_BALANCE_MAX_EXPERTS]);
-    RowSums<VECS> s;
-    begin_sums<LANES, VECS>(a, s, a.tick, n, lane);
+    RowSums<N, E> s;
+    begin_sums<LANES>(a, s, a.tick, n, lane);
     const float z_unit = 2.0f * a.z_coef * a.grad_scale / n;
     int turn = 0, stage = 0;
     bool next_takes = takes_part(a, first);
@@ -257,18 +272,20 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const Ba
         const int64_t r = r0 + group;
         const bool takes = next_takes;
         next_takes = takes_part(a, r + step);
-        Raw<DT> raw[VECS];
+        Raw raw[N];
         if constexpr (VEC) {
             fetch(r + (Rows::STAGES - 1) * step, (stage + Rows::STAGES - 1) % Rows::STAGES);
             fetch_wait<Rows::STAGES - 1>();
-            Rows::take(raw, ring, stage, 0);
+#pragma unroll
+            for (int v = 0; v < N; ++v)
+                raw[v] = Rows::take(ring, stage, 0, v);
             stage = (stage + 1) % Rows::STAGES;
         } else {
             load_row<DT, VEC, LANES>(raw, a.x, takes ? r * a.ldx : 0, lane, takes ? a.experts : 0);
         }
-        balance_row<DT, SIGMOID, LANES, VECS, VEC>(a, raw, s, sh, turn, z_unit, r, r < a.rows, takes, lane);
+        balance_row<DT, SIGMOID, LANES, VEC>(a, raw, s, sh, turn, z_unit, r, r < a.rows, takes, lane);
     }
-    meet_sums<LANES, VECS>(s, meet, meet_z, lane);
+    meet_sums<LANES>(s, meet, meet_z, lane);
     float *const part = a.part + (int64_t)blockIdx.x * (a.experts + 1);
     for (int e = threadIdx.x; e < a.experts; e += NT)
         part[e] = sum_of<LANES, VECS, NT>(meet, e);
@@ -288,27 +305,29 @@ __device__ __forceinline__ void write_stats(const BalanceArgs &a, unsigned token
     a.stats[3] = (float)tokens;
 }
 
-// 32 experts per CTA by 8 lanes of parts; the last CTA does the totals and clears the counters.
-__global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a, int parts)
+// 32 experts per CTA by 32 lanes of parts; the last CTA does the totals and clears the counters.
+constexpr int JOIN_NT = 1024;
+__global__ void __launch_bounds__(JOIN_NT) balance_join_kernel(const BalanceArgs a, int parts)
 {
     pdl_enter();
-    __shared__ float sums[8][33];
+    __shared__ float sums[32][33];
     __shared__ bool last;
-    const int e = blockIdx.x * 32 + threadIdx.x % 32, turn = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32, turn = threadIdx.x / 32;
     const unsigned tokens = a.tick[RED_BALANCE_MAX_EXPERTS];
     float p = 0.0f;
-    if (e <= a.experts) {
-#pragma unroll 4
-        for (int i = turn; i < parts; i += 8)
-            p += a.part[(int64_t)i * (a.experts + 1) + e];
+    if (blockIdx.x * 32 + lane <= a.experts) {
+#pragma unroll 8
+        for (int i = turn; i < parts; i += 32)
+            p += a.part[(int64_t)i * (a.experts + 1) + blockIdx.x * 32 + lane];
     }
-    sums[turn][threadIdx.x % 32] = p;
+    sums[turn][lane] = p;
     __syncthreads();
+    p = sums[lane][turn];  // expert `turn` of the 32, a share per lane
+    for (int o = 16; o; o >>= 1)
+        p += __shfl_xor_sync(0xffffffffu, p, o);
     float *const terms = a.part + (int64_t)parts * (a.experts + 1);  // one per expert, and the sum of lse^2
-    if (turn == 0 && e <= a.experts) {
-#pragma unroll
-        for (int k = 1; k < 8; ++k)
-            p += sums[k][threadIdx.x % 32];
+    const int e = blockIdx.x * 32 + turn;
+    if (lane == 0 && e <= a.experts) {
         if (e < a.experts) {
             const unsigned count = a.tick[e];
             a.counts[e] = count;
@@ -327,7 +346,7 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a, 
         return;
     __threadfence();
     float dot = 0.0f;
-    for (int i = threadIdx.x; i < a.experts; i += 256)
+    for (int i = threadIdx.x; i < a.experts; i += JOIN_NT)
         dot += __ldcg(terms + i);
     for (int o = 16; o; o >>= 1)
         dot += __shfl_xor_sync(0xffffffffu, dot, o);
@@ -336,83 +355,118 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a, 
     __syncthreads();
     if (threadIdx.x == 0) {
         dot = 0.0f;
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < JOIN_NT / 32; ++k)
             dot += sums[0][k];
         write_stats(a, tokens, dot, __ldcg(terms + a.experts));
         *ticket_of(a.tick) = 0;
     }
-    for (int i = threadIdx.x; i <= a.experts; i += 256)
+    for (int i = threadIdx.x; i <= a.experts; i += JOIN_NT)
         a.tick[i < a.experts ? i : RED_BALANCE_MAX_EXPERTS] = 0;
 }
 
-// Few tokens: one CTA counts, passes over the rows and joins, in shared memory.
-constexpr int FEW_THREADS = 1024;
+// Few tokens: the CTAs of one cluster count, pass over the rows and join, through
+// shared memory.  us, softmax f32 k 6: 257 x 64 8.4 with one
+// CTA of 1024 threads, 6.9 with a cluster; 1000 x 64 14.8, 7.6; 4000 x 64 14.4 with a cluster, 11.7 with the three
+// kernels below.
+constexpr int FEW_THREADS = 512;
 constexpr int FEW_EXPERTS = 256;
+constexpr int FEW_CLUSTER = 8;
 
 template <int DT, bool SIGMOID, int LANES, bool VEC>
 __global__ void __launch_bounds__(FEW_THREADS) balance_few_kernel(const BalanceArgs a)
 {
     pdl_enter();
-    constexpr int GROUPS = FEW_THREADS / LANES;
+    constexpr int GROUPS = FEW_THREADS / LANES, N = UNITS<DT, 1>, E = UNIT<DT>;
     __shared__ GroupShared<LANES> sh;
-    __shared__ float meet[FEW_THREADS / 32 * LANES * 8], meet_z[FEW_THREADS / 32], dots[FEW_THREADS / 32];
-    __shared__ unsigned counts[FEW_EXPERTS], tokens;
+    __shared__ float meet[FEW_THREADS / 32 * LANES * 8], meet_z[FEW_THREADS / 32], dots[FEW_EXPERTS / 32];
+    __shared__ float share[FEW_EXPERTS + 1], sums[FEW_EXPERTS + 1];
+    __shared__ unsigned mine[FEW_EXPERTS + 1], counts[FEW_EXPERTS + 1];  // experts, tokens
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-    if (threadIdx.x < FEW_EXPERTS)
-        counts[threadIdx.x] = 0;
-    if (threadIdx.x == 0)
-        tokens = 0;
+    const int ctas = cluster_size(), rank = cluster_rank();
+    const int64_t step = ctas * GROUPS, first = rank * GROUPS + group;
+    for (int e = threadIdx.x; e <= FEW_EXPERTS; e += FEW_THREADS)
+        mine[e] = 0;
     // the first token's logits are on their way while the ids are counted, the next one's while one is at work
-    Raw<DT> next[1];
-    bool next_takes = takes_part(a, group);
-    load_row<DT, VEC, LANES>(next, a.x, next_takes ? group * a.ldx : 0, lane, next_takes ? a.experts : 0);
+    Raw next[N];
+    bool next_takes = takes_part(a, first);
+    load_row<DT, VEC, LANES>(next, a.x, next_takes ? first * a.ldx : 0, lane, next_takes ? a.experts : 0);
     __syncthreads();
-    count_ids(a, counts, &tokens, threadIdx.x, FEW_THREADS);
+    count_ids(a, mine, mine + FEW_EXPERTS, rank * FEW_THREADS + threadIdx.x, ctas * FEW_THREADS);
     __syncthreads();
+    if (ctas > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+    if (threadIdx.x <= FEW_EXPERTS) {
+        unsigned n = 0;
+        for (int c = 0; c < ctas; ++c)
+            n += *in_cta(mine + threadIdx.x, c);
+        counts[threadIdx.x] = n;
+    }
+    __syncthreads();
+    const unsigned tokens = counts[FEW_EXPERTS];
     const float n = tokens_of(tokens);
-    RowSums<1> s;
-    begin_sums<LANES, 1>(a, s, counts, n, lane);
+    RowSums<N, E> s;
+    begin_sums<LANES>(a, s, counts, n, lane);
     const float z_unit = 2.0f * a.z_coef * a.grad_scale / n;
     int turn = 0;
-    for (int64_t r0 = 0; r0 < a.rows; r0 += GROUPS) {
+    for (int64_t r0 = rank * GROUPS; r0 < a.rows; r0 += step) {
         const int64_t r = r0 + group;
-        const Raw<DT> raw[1] = {next[0]};
+        Raw raw[N];
+#pragma unroll
+        for (int v = 0; v < N; ++v)
+            raw[v] = next[v];
         const bool takes = next_takes;
-        next_takes = takes_part(a, r + GROUPS);
-        load_row<DT, VEC, LANES>(next, a.x, next_takes ? (r + GROUPS) * a.ldx : 0, lane, next_takes ? a.experts : 0);
-        balance_row<DT, SIGMOID, LANES, 1, VEC>(a, raw, s, sh, turn, z_unit, r, r < a.rows, takes, lane);
+        next_takes = takes_part(a, r + step);
+        load_row<DT, VEC, LANES>(next, a.x, next_takes ? (r + step) * a.ldx : 0, lane, next_takes ? a.experts : 0);
+        balance_row<DT, SIGMOID, LANES, VEC>(a, raw, s, sh, turn, z_unit, r, r < a.rows, takes, lane);
     }
-    meet_sums<LANES, 1>(s, meet, meet_z, lane);
+    meet_sums<LANES>(s, meet, meet_z, lane);
+    if (threadIdx.x < a.experts)
+        share[threadIdx.x] = sum_of<LANES, 1, FEW_THREADS>(meet, threadIdx.x);
+    if (threadIdx.x == 0)
+        share[a.experts] = sum_of_z<LANES, FEW_THREADS>(meet_z);
+    // every sum to the first CTA
+    float *const all = in_cta(sums, 0);
+    cluster_sums(share, a.experts + 1, [&](int e, float sum) { all[e] = sum; });
+    if (rank != 0)
+        return;
+    __syncthreads();
     float dot = 0.0f;
     if (threadIdx.x < a.experts) {
-        const float p = sum_of<LANES, 1, FEW_THREADS>(meet, threadIdx.x);
+        const float p = sums[threadIdx.x];
         a.counts[threadIdx.x] = counts[threadIdx.x];
         a.prob[threadIdx.x] = p / n;
         dot = (float)counts[threadIdx.x] * p;
     }
     for (int o = 16; o; o >>= 1)
         dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (threadIdx.x % 32 == 0)
+    if (threadIdx.x % 32 == 0 && threadIdx.x < FEW_EXPERTS)
         dots[threadIdx.x / 32] = dot;
     __syncthreads();
     if (threadIdx.x == 0) {
         dot = 0.0f;
         for (int k = 0; k < FEW_EXPERTS / 32; ++k)
             dot += dots[k];
-        write_stats(a, tokens, dot, sum_of_z<LANES, FEW_THREADS>(meet_z));
+        write_stats(a, tokens, dot, sums[a.experts]);
     }
 }
 
-// One CTA does all of it up to this many logits.
-constexpr int64_t FEW_LOGITS = 1 << 16;
+// One cluster does all of it up to this many logits; a CTA of it has at least this many.
+constexpr int64_t FEW_LOGITS = 1 << 17, FEW_PER_CTA = 1 << 12;
 
 template <int DT, bool SIGMOID, int LANES, int VECS, bool VEC>
 int launch_rows(BalanceArgs &a, cudaStream_t s)
 {
     if constexpr (VECS == 1) {
-        if (a.rows * a.experts <= FEW_LOGITS) {
+        const int64_t logits = a.rows * a.experts;
+        if (logits <= FEW_LOGITS) {
+            unsigned cluster = 1;
+            while (cluster < FEW_CLUSTER && cluster * FEW_PER_CTA < logits)
+                cluster *= 2;
             count_launches(1);
-            return cuda_fail(launch_pdl(balance_few_kernel<DT, SIGMOID, LANES, VEC>, dim3(1), dim3(FEW_THREADS), s, a),
+            return cuda_fail(launch_pdl_smem(balance_few_kernel<DT, SIGMOID, LANES, VEC>, cluster, FEW_THREADS, 0, cluster,
+                                             s, a),
                              "balance_few");
         }
     }
@@ -423,25 +477,26 @@ int launch_rows(BalanceArgs &a, cudaStream_t s)
     Workspace ws;
     if (st == RED_OK)
         st = get_workspace(&ws);
-    constexpr size_t SMEM = VEC ? Ring<DT, LANES, VECS, 1>::BYTES : 0;
+    constexpr size_t SMEM = VEC ? Ring<DT, LANES, UNITS<DT, VECS>, 1>::BYTES : 0;
     unsigned grid = 1;
+    auto *const kernel = balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>;
     if (st == RED_OK)
-        st = resident_grid(balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>, cache, NT, SMEM,
-                           (a.rows + GROUPS - 1) / GROUPS, (int64_t)(WS_PART_ELEMS / (size_t)(a.experts + 1)) - 1, &grid);
+        st = resident_grid(kernel, cache, NT, SMEM, (a.rows + GROUPS - 1) / GROUPS,
+                           (int64_t)(WS_PART_ELEMS / (size_t)(a.experts + 1)) - 1, &grid);
     if (st != RED_OK)
         return st;
     a.tick = ws.tick;
     a.part = static_cast<float *>(ws.part);
-    const int64_t per = 8 * COUNT_NT, want = (a.rows * a.k + per - 1) / per;
+    const int64_t per = 4 * COUNT_NT, want = (a.rows * a.k + per - 1) / per;
     st = cuda_fail(launch_pdl_dynamic(balance_count_kernel, dim3((unsigned)(want < di.sms ? want : di.sms)), dim3(COUNT_NT),
                                       (size_t)(a.experts + 1) * sizeof(unsigned), s, a),
                    "balance_count");
     if (st == RED_OK)
-        st = cuda_fail(launch_pdl_dynamic(balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>, dim3(grid), dim3(NT), SMEM, s,
-                                          a),
+        st = cuda_fail(launch_pdl_dynamic(kernel, dim3(grid), dim3(NT), SMEM, s, a),
                        "balance_rows");
     if (st == RED_OK)
-        st = cuda_fail(launch_pdl(balance_join_kernel, dim3((unsigned)(a.experts / 32 + 1)), dim3(256), s, a, (int)grid),
+        st = cuda_fail(launch_pdl(balance_join_kernel, dim3((unsigned)(a.experts / 32 + 1)), dim3(JOIN_NT), s, a,
+                                  (int)grid),
                        "balance_join");
     if (st == RED_OK)
         count_launches(3);

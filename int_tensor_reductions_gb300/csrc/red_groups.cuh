@@ -1,7 +1,9 @@
 // red_groups.cuh -- rows held in the registers of a group of lanes: loads and
-// stores of eight consecutive elements per lane, reductions over the group, and
-// the group that a row's length asks for.  8 to 32 lanes of a warp, or a whole
-// CTA, hold a row; vector v of lane l starts at element (v * LANES + l) * 8.
+// stores of 16 bytes per lane, reductions over the group, and the group that a
+// row's length asks for.  8 to 32 lanes of a warp, or a whole CTA, hold a row;
+// unit u of lane l is the E elements (16 bytes) from (u * LANES + l) * E on.  (Eight
+// consecutive fp32 values per lane would be two loads of every other 16 bytes:
+// norm 16384 x 4096 f32 231 us, as it is 173.)
 #pragma once
 
 #include <cstdint>
@@ -9,6 +11,7 @@
 
 #include "red_internal.h"
 #include "red_loss.cuh"
+#include "red_pipeline.cuh"
 
 namespace red {
 
@@ -18,49 +21,51 @@ constexpr int GROUP_CTA = LANES > 32 ? LANES : 256;
 
 // ------------------------------------------------------------- row access
 
-// Eight elements as they lie in memory.
+// Elements of a unit, and units of a lane that holds `VECS` times eight elements.
 template <int DT>
+constexpr int UNIT = DT == RED_F32 ? 4 : 8;
+template <int DT, int VECS>
+constexpr int UNITS = VECS * 8 / UNIT<DT>;
+
+// A unit as it lies in memory.
 struct Raw {
-    uint32_t u[DT == RED_F32 ? 8 : 4];
+    uint32_t u[4];
 };
 
 template <int DT>
-__device__ __forceinline__ void widen(const Raw<DT> &r, float (&v)[8])
+__device__ __forceinline__ void widen(const Raw &r, float (&v)[UNIT<DT>])
 {
-    if constexpr (DT == RED_F32) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (DT == RED_F32) {
             v[k] = __uint_as_float(r.u[k]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        } else {
             v[2 * k] = Elem<DT>::widen(r.u[k] & 0xffffu);
             v[2 * k + 1] = Elem<DT>::widen(r.u[k] >> 16);
         }
     }
 }
 template <int DT>
-__device__ __forceinline__ Raw<DT> narrow(const float (&v)[8])
+__device__ __forceinline__ Raw narrow(const float (&v)[UNIT<DT>])
 {
-    Raw<DT> r;
-    if constexpr (DT == RED_F32) {
+    Raw r;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (DT == RED_F32)
             r.u[k] = __float_as_uint(v[k]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
+        else
             r.u[k] = (uint32_t)Elem<DT>::narrow(v[2 * k]) | (uint32_t)Elem<DT>::narrow(v[2 * k + 1]) << 16;
     }
     return r;
 }
 
+// The first n elements of a unit, one by one; 0 behind them.
 template <int DT>
-__device__ __forceinline__ Raw<DT> load_some(const void *p, int64_t at, int n)
+__device__ __forceinline__ Raw load_some(const void *p, int64_t at, int n)
 {
-    Raw<DT> r;
+    Raw r;
 #pragma unroll
-    for (int k = 0; k < (DT == RED_F32 ? 8 : 4); ++k) {
+    for (int k = 0; k < 4; ++k) {
         if constexpr (DT == RED_F32) {
             r.u[k] = k < n ? static_cast<const uint32_t *>(p)[at + k] : 0u;
         } else {
@@ -71,50 +76,44 @@ __device__ __forceinline__ Raw<DT> load_some(const void *p, int64_t at, int n)
     return r;
 }
 
-// A lane's vectors of a row (`row`: the row's first element); 0 behind its end.
+// A lane's units of a row (`row`: the row's first element); 0 behind its end.
 // The loads are issued together: nothing here looks at what they bring.
-template <int DT, bool VEC, int LANES, int VECS>
-__device__ __forceinline__ void load_row(Raw<DT> (&r)[VECS], const void *p, int64_t row, int lane, int len)
+template <int DT, bool VEC, int LANES, int N>
+__device__ __forceinline__ void load_row(Raw (&r)[N], const void *p, int64_t row, int lane, int len)
 {
+    constexpr int E = UNIT<DT>;
     if constexpr (VEC) {
 #pragma unroll
-        for (int v = 0; v < VECS; ++v) {
-            const int i = (v * LANES + lane) * 8;
-            const bool full = i + 8 <= len;
-            constexpr int WORDS = DT == RED_F32 ? 8 : 4;
-            const uint4 *q =
-                reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + (row + i) * (DT == RED_F32 ? 4 : 2));
-#pragma unroll
-            for (int k = 0; k < WORDS; k += 4) {
-                const uint4 x = full ? q[k / 4] : make_uint4(0, 0, 0, 0);
-                r[v].u[k] = x.x, r[v].u[k + 1] = x.y, r[v].u[k + 2] = x.z, r[v].u[k + 3] = x.w;
-            }
+        for (int u = 0; u < N; ++u) {
+            const int i = (u * LANES + lane) * E;
+            const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + (row + i) * (16 / E));
+            const uint4 x = i + E <= len ? *q : make_uint4(0, 0, 0, 0);
+            r[u].u[0] = x.x, r[u].u[1] = x.y, r[u].u[2] = x.z, r[u].u[3] = x.w;
         }
-        if (len % 8 == 0)
+        if (len % E == 0)
             return;
     }
-    // elements one by one: of one lane's last vector, or of all
+    // elements one by one: of one lane's last unit, or of all
 #pragma unroll
-    for (int v = 0; v < VECS; ++v) {
-        const int i = (v * LANES + lane) * 8;
-        if (!VEC || (i < len && i + 8 > len))
-            r[v] = load_some<DT>(p, row + i, len - i);
+    for (int u = 0; u < N; ++u) {
+        const int i = (u * LANES + lane) * E;
+        if (!VEC || (i < len && i + E > len))
+            r[u] = load_some<DT>(p, row + i, len - i);
     }
 }
 
 template <int DT, bool VEC>
-__device__ __forceinline__ void store8(void *p, int64_t row, int i, int len, const float (&v)[8])
+__device__ __forceinline__ void store_unit(void *p, int64_t row, int i, int len, const float (&v)[UNIT<DT>])
 {
-    if (VEC && i + 8 <= len) {
-        const Raw<DT> r = narrow<DT>(v);
-        uint4 *q = reinterpret_cast<uint4 *>(static_cast<char *>(p) + (row + i) * (DT == RED_F32 ? 4 : 2));
-        q[0] = make_uint4(r.u[0], r.u[1], r.u[2], r.u[3]);
-        if constexpr (DT == RED_F32)
-            q[1] = make_uint4(r.u[4], r.u[5], r.u[6], r.u[7]);
+    constexpr int E = UNIT<DT>;
+    if (VEC && i + E <= len) {
+        const Raw r = narrow<DT>(v);
+        *reinterpret_cast<uint4 *>(static_cast<char *>(p) + (row + i) * (16 / E)) =
+            make_uint4(r.u[0], r.u[1], r.u[2], r.u[3]);
         return;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < E; ++k)
         if (i + k < len)
             store_elem<DT>(p, row + i + k, v[k]);
 }
@@ -135,46 +134,37 @@ __device__ __forceinline__ void fetch_wait()
 }
 
 // A ring of rows in shared memory, fetched while earlier rows are at work: each
-// thread fetches its own vectors of ARRAYS matrices and reads them back itself, so
+// thread fetches its own units of ARRAYS matrices and reads them back itself, so
 // that no barrier is needed.  Only rows on 16-byte boundaries go this way (VEC);
 // others are loaded when they are wanted.
-template <int DT, int LANES, int VECS, int ARRAYS>
+template <int DT, int LANES, int N, int ARRAYS>
 struct Ring {
-    static constexpr int NT = GROUP_CTA<LANES>, UNITS = DT == RED_F32 ? 2 : 1;
-    static constexpr int STAGE = ARRAYS * VECS * UNITS * NT * 16;
-    // up to four rows ahead in 100 KB, which lets two CTAs share an SM; two where a row takes as much
-    static constexpr int FIT = STAGE > 51200 ? 204800 / STAGE : 102400 / STAGE;
-    static constexpr int STAGES = FIT < 1 ? 1 : FIT > 4 ? 4 : FIT;
+    static constexpr int NT = GROUP_CTA<LANES>;
+    static constexpr int STAGE = ARRAYS * N * NT * 16;
+    // one row at work, one on its way; more are no use (norm 30000 x 512 bf16 with four 18.4 us, with two 17.3)
+    static constexpr int STAGES = 2 * STAGE <= 204800 ? 2 : 1;
     static constexpr size_t BYTES = (size_t)STAGE * STAGES;
 
-    static __device__ __forceinline__ uint4 *slot(unsigned char *ring, int stage, int array, int v)
+    static __device__ __forceinline__ uint4 *slot(unsigned char *ring, int stage, int array, int u)
     {
-        return reinterpret_cast<uint4 *>(ring) + ((stage * ARRAYS + array) * VECS + v) * UNITS * NT + threadIdx.x;
+        return reinterpret_cast<uint4 *>(ring) + ((stage * ARRAYS + array) * N + u) * NT + threadIdx.x;
     }
     static __device__ __forceinline__ void fetch(unsigned char *ring, int stage, int array, const void *p, int64_t row,
                                                  int lane, int len)
     {
-        constexpr int SIZE = DT == RED_F32 ? 4 : 2;
+        constexpr int E = UNIT<DT>;
 #pragma unroll
-        for (int v = 0; v < VECS; ++v)
-#pragma unroll
-            for (int u = 0; u < UNITS; ++u) {
-                const int i = (v * LANES + lane) * 8 + u * 4;  // (u > 0: fp32 alone)
-                const int left = (len - i) * SIZE;
-                const uint32_t bytes = left <= 0 ? 0 : left < 16 ? left : 16;
-                fetch16(slot(ring, stage, array, v) + u * NT,
-                        static_cast<const char *>(p) + (bytes ? (row + i) * SIZE : 0), bytes);
-            }
+        for (int u = 0; u < N; ++u) {
+            const int i = (u * LANES + lane) * E;
+            const int left = (len - i) * (16 / E);
+            const uint32_t bytes = left <= 0 ? 0 : left < 16 ? left : 16;
+            fetch16(slot(ring, stage, array, u), static_cast<const char *>(p) + (bytes ? (row + i) * (16 / E) : 0), bytes);
+        }
     }
-    static __device__ __forceinline__ void take(Raw<DT> (&r)[VECS], unsigned char *ring, int stage, int array)
+    static __device__ __forceinline__ Raw take(unsigned char *ring, int stage, int array, int u)
     {
-#pragma unroll
-        for (int v = 0; v < VECS; ++v)
-#pragma unroll
-            for (int u = 0; u < UNITS; ++u) {
-                const uint4 x = slot(ring, stage, array, v)[u * NT];
-                r[v].u[4 * u] = x.x, r[v].u[4 * u + 1] = x.y, r[v].u[4 * u + 2] = x.z, r[v].u[4 * u + 3] = x.w;
-            }
+        const uint4 x = *slot(ring, stage, array, u);
+        return {{x.x, x.y, x.z, x.w}};
     }
 };
 
@@ -228,6 +218,30 @@ struct Max {  // NaN wins
     }
 };
 
+// Sums over the CTAs of a cluster of what each has in `share` (n floats in shared
+// memory at the same place; all threads): f(i, sum) for this CTA's part of 0..n, in a
+// fixed order.  One CTA alone goes through all of it.
+template <class F>
+__device__ __forceinline__ void cluster_sums(float *share, int n, F f)
+{
+    const int ctas = cluster_size(), rank = cluster_rank();
+    __syncthreads();
+    if (ctas > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+    for (int i = rank * blockDim.x + threadIdx.x; i < n; i += ctas * blockDim.x) {
+        float sum = 0.0f;
+        for (int c = 0; c < ctas; ++c)
+            sum += *in_cta(share + i, c);
+        f(i, sum);
+    }
+    if (ctas > 1) {  // (shared memory lives until the others have read it)
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
 // The group of a row of `vecs` vectors (up to 2048).  Calls f with (lanes,
 // vectors per lane).
 template <class F>
@@ -267,12 +281,12 @@ inline bool aligned_rows(const void *p, int64_t ld, int64_t rows, int elem)
     return !p || ((uintptr_t)p % 16 == 0 && (rows < 2 || ld * elem % 16 == 0));
 }
 
-// CTAs per SM of a kernel with `smem` bytes of dynamic shared memory, per device.
+// CTAs per SM of a kernel, per device.
 struct Resident {
     std::atomic<int> per_sm[64] = {};
 };
 
-// CTAs of a persistent grid: what is resident at once, or what there is to do.
+// CTAs of a persistent grid: what is resident at once, or what there is to do; at most `most`.
 template <class K>
 int resident_grid(K kernel, Resident &cache, int threads, size_t smem, int64_t ctas, int64_t most, unsigned *grid)
 {

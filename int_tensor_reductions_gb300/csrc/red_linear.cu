@@ -18,7 +18,9 @@
 #include <cuda.h>
 
 #include "red_linear.cuh"
+#include "red_loss.cuh"
 #include "red_mma.cuh"
+#include "red_prims.cuh"
 
 namespace red {
 namespace {

@@ -22,7 +22,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include "red_loss_rows.cuh"
+#include "red_pipeline.cuh"
 
 namespace red {
 

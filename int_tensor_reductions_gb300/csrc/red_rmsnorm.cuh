@@ -34,7 +34,7 @@ struct NormArgs {
     void *y, *total;
     int64_t ldy, ldt;
     float *rstd, *scales;
-    int block, blocks;  // values and number of blocks per row; 0: one scale per row
+    int block, blocks;  // values of a block (fewer than len) and blocks per row; 0 and 1: one scale per row
 };
 struct NormGradArgs {
     const void *dy, *x, *weight, *dtotal;
@@ -43,37 +43,61 @@ struct NormGradArgs {
     int len;
     bool wide;
     float inv_len;
-    void *dx;
-    float *part;  // shares of dw, one of len per CTA; NULL: not wanted
+    void *dx, *dw;  // dw NULL: not wanted
+    int wtype;      // of the weight and dw
+    float *part;    // shares of dw, one of len per CTA
 };
 
 template <int DT>
 int rmsnorm_forward(const NormArgs &a, int kind, cudaStream_t s);
 template <int DT>
-int rmsnorm_backward(const NormGradArgs &a, int wtype, void *dw, cudaStream_t s);
+int rmsnorm_backward(const NormGradArgs &a, cudaStream_t s);
 
 #ifdef RED_RMSNORM_DT  // the kernels of one direction (RED_RMSNORM_BACKWARD), for one type of x
 
 namespace {
 
 // A lane's weights, of x's type or fp32; 1 where there are none.  They are the same
-// for every row of a group and stay in registers.
-template <int DT, bool WIDE, bool VEC, int LANES, int VECS>
+// for every row of a group and stay in registers.  WIDE: fp32 beside rows of 16
+// bits, whose units are two of the weight's.
+template <int DT, bool WIDE, bool VEC, int LANES, int N>
 struct Weights {
-    static constexpr int WT = WIDE ? RED_F32 : DT;
-    Raw<WT> raw[VECS];
+    static constexpr int E = UNIT<DT>, WT = WIDE ? RED_F32 : DT, WORDS = WIDE && DT != RED_F32 ? 8 : 4;
+    uint32_t raw[N][WORDS];
 
     __device__ __forceinline__ Weights(const void *w, int lane, int len)
     {
-        load_row<WT, VEC, LANES>(raw, w, 0, lane, w ? len : 0);
-        if (!w) {
-            float ones[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
 #pragma unroll
-            for (int v = 0; v < VECS; ++v)
-                raw[v] = narrow<WT>(ones);
-        }
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int h = 0; h < WORDS; h += 4) {
+                constexpr int EW = UNIT<WT>;
+                const int i = (u * LANES + lane) * E + h;
+                Raw r;
+                if (!w) {
+                    float ones[EW];
+#pragma unroll
+                    for (int k = 0; k < EW; ++k)
+                        ones[k] = 1.0f;
+                    r = narrow<WT>(ones);
+                } else if (VEC && i + EW <= len) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const char *>(w) + (int64_t)i * (16 / EW));
+                    r = {{x.x, x.y, x.z, x.w}};
+                } else {
+                    r = load_some<WT>(w, i, len - i);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    raw[u][h + k] = r.u[k];
+            }
     }
-    __device__ __forceinline__ void at(int v, float (&w)[8]) const { widen<WT>(raw[v], w); }
+    __device__ __forceinline__ void at(int u, float (&w)[E]) const
+    {
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            w[k] = WT == RED_F32 ? __uint_as_float(raw[u][k % WORDS])
+                                 : Elem<WT == RED_F32 ? RED_F16 : WT>::widen(raw[u][k / 2 % WORDS] >> (k % 2 * 16) & 0xffffu);
+    }
 };
 
 #ifndef RED_RMSNORM_BACKWARD
@@ -93,16 +117,16 @@ __device__ __forceinline__ float scale_of(float most, float *inv)
     return scale;
 }
 
-// Eight 8-bit values, to nearest, beyond the largest: the largest.  A product with
+// A unit's values in 8 bits, to nearest, beyond the largest: the largest.  A product with
 // the scale's inverse: it is off by 1.5 units of fp32's last place, which moves one
 // value in a million across a border between two of 8 bits, and eight divisions
-// took more time than all else (16384 x 8192 bf16 295 us with them, DIVNOW without).
-template <int KIND>
-__device__ __forceinline__ uint64_t narrow8(const float (&v)[8], float inv)
+// took more time than all else (16384 x 8192 bf16 295 us with them, 221 without).
+template <int KIND, int E>
+__device__ __forceinline__ uint64_t narrow8(const float (&v)[E], float inv)
 {
     uint64_t r = 0;
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
+    for (int k = 0; k < E; k += 2) {
         const float a = v[k] * inv, b = v[k + 1] * inv;
         uint32_t two;
         if constexpr (KIND == RED_QUANT_E4M3) {
@@ -120,105 +144,136 @@ __device__ __forceinline__ uint64_t narrow8(const float (&v)[8], float inv)
     return r;
 }
 
-template <int KIND>
+template <int E>
 __device__ __forceinline__ void store_q(uint8_t *q, int64_t row, int i, int len, bool vec, uint64_t v)
 {
-    if (vec && i + 8 <= len) {
-        *reinterpret_cast<uint64_t *>(q + row + i) = v;
+    if (vec && i + E <= len) {
+        if (E == 8)
+            *reinterpret_cast<uint64_t *>(q + row + i) = v;
+        else
+            *reinterpret_cast<uint32_t *>(q + row + i) = (uint32_t)v;
         return;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < E; ++k)
         if (i + k < len)
             q[row + i + k] = (uint8_t)(v >> (8 * k));
 }
 
 // KIND: 0 for y in x's type, else the 8-bit type.
-template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC>
+template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC, bool RING>
 __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArgs a)
 {
     pdl_enter();
     __shared__ GroupShared<LANES> sh;
-    constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
+    constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES, N = UNITS<DT, VECS>, E = UNIT<DT>;
+    using Rows = Ring<DT, LANES, UNITS<DT, VECS>, 2>;
+    extern __shared__ __align__(16) unsigned char ring[];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
-    int turn = 0;
-    const Weights<DT, WIDE, VEC, LANES, VECS> weights(a.weight, lane, a.len);
+    const int64_t step = (int64_t)gridDim.x * GROUPS, first = (int64_t)blockIdx.x * GROUPS + group;
+    int turn = 0, stage = 0;
+    auto fetch = [&](int64_t r, int to) {
+        if (r < a.rows) {
+            Rows::fetch(ring, to, 0, a.x, r * a.ldx, lane, a.len);
+            if (a.residual)
+                Rows::fetch(ring, to, 1, a.residual, r * a.ldr, lane, a.len);
+        }
+        fetch_commit();
+    };
+    if constexpr (RING) {
+#pragma unroll
+        for (int k = 0; k < Rows::STAGES - 1; ++k)
+            fetch(first + k * step, k);
+    }
+    const Weights<DT, WIDE, VEC, LANES, N> weights(a.weight, lane, a.len);
     // every group of a CTA takes part in the shuffles to the end
-    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += (int64_t)gridDim.x * GROUPS) {
+    for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += step) {
         const bool here = r0 + group < a.rows;
         const int64_t r = here ? r0 + group : a.rows - 1;
-        Raw<DT> raw[VECS], res[VECS];
-        load_row<DT, VEC, LANES>(raw, a.x, r * a.ldx, lane, a.len);
-        if (a.residual)
-            load_row<DT, VEC, LANES>(res, a.residual, r * a.ldr, lane, a.len);
-        float t[VECS][8];
+        Raw raw[N], res[N];
+        if constexpr (RING) {
+            fetch(r0 + group + (Rows::STAGES - 1) * step, (stage + Rows::STAGES - 1) % Rows::STAGES);
+            fetch_wait<Rows::STAGES - 1>();
+#pragma unroll
+            for (int v = 0; v < N; ++v) {
+                raw[v] = Rows::take(ring, stage, 0, v);
+                if (a.residual)
+                    res[v] = Rows::take(ring, stage, 1, v);
+            }
+            stage = (stage + 1) % Rows::STAGES;
+        } else {
+            load_row<DT, VEC, LANES>(raw, a.x, r * a.ldx, lane, a.len);
+            if (a.residual)
+                load_row<DT, VEC, LANES>(res, a.residual, r * a.ldr, lane, a.len);
+        }
+        float t[N][E];
         float sum = 0.0f;
 #pragma unroll
-        for (int v = 0; v < VECS; ++v) {
+        for (int v = 0; v < N; ++v) {
             widen<DT>(raw[v], t[v]);
             if (a.residual) {
-                float s[8];
+                float s[E];
                 widen<DT>(res[v], s);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < E; ++k)
                     t[v][k] += s[k];
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < E; ++k)
                 sum = fmaf(t[v][k], t[v][k], sum);
         }
         if (a.residual && here) {
 #pragma unroll
-            for (int v = 0; v < VECS; ++v)
-                store8<DT, VEC>(a.total, r * a.ldt, (v * LANES + lane) * 8, a.len, t[v]);
+            for (int v = 0; v < N; ++v)
+                store_unit<DT, VEC>(a.total, r * a.ldt, (v * LANES + lane) * E, a.len, t[v]);
         }
         sum = group_fold<LANES>(sum, sh, turn, Add());
         const float rstd = __frsqrt_rn(fmaf(sum, a.inv_len, a.eps));
         if (a.rstd && lane == 0 && here)
             a.rstd[r] = rstd;
-        float top = 0.0f;
+        float most[N];
 #pragma unroll
-        for (int v = 0; v < VECS; ++v) {
-            const int i = (v * LANES + lane) * 8;
-            float w[8];
+        for (int v = 0; v < N; ++v) {
+            float w[E];
             weights.at(v, w);
-            float most = 0.0f;
+            most[v] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < E; ++k) {
                 t[v][k] = t[v][k] * rstd * w[k];
                 if (KIND != 0)
-                    most = Max()(most, fabsf(t[v][k]));
+                    most[v] = Max()(most[v], fabsf(t[v][k]));
             }
-            if constexpr (KIND == 0) {
-                if (here)
-                    store8<DT, VEC>(a.y, r * a.ldy, i, a.len, t[v]);
-            } else if (a.block) {
-                // a block is 4, 8, 16 or 32 neighbouring lanes' vectors
-                const int lanes = min(a.block / 8, LANES < 32 ? LANES : 32);
-                for (int o = lanes / 2; o; o >>= 1)
-                    most = Max()(most, __shfl_xor_sync(0xffffffffu, most, o));
-                float inv;
-                const float scale = scale_of<KIND>(most, &inv);
-                if (here && i < a.len) {
-                    if (lane % lanes == 0)
-                        a.scales[r * a.blocks + i / a.block] = scale;
-                    store_q<KIND>(static_cast<uint8_t *>(a.y), r * a.ldy, i, a.len, VEC, narrow8<KIND>(t[v], inv));
-                }
-            } else {
-                top = Max()(top, most);
-            }
+            if (KIND == 0 && here)
+                store_unit<DT, VEC>(a.y, r * a.ldy, (v * LANES + lane) * E, a.len, t[v]);
         }
-        if (KIND != 0 && !a.block) {
-            top = group_fold<LANES>(top, sh, turn, Max());
-            float inv;
-            const float scale = scale_of<KIND>(top, &inv);
-            if (here) {
-                if (lane == 0)
-                    a.scales[r] = scale;
+        if constexpr (KIND != 0) {
+            if (a.block) {
+                // a block is 4 to 32 neighbouring lanes' units
+                const int lanes = a.block / E;
 #pragma unroll
-                for (int v = 0; v < VECS; ++v)
-                    store_q<KIND>(static_cast<uint8_t *>(a.y), r * a.ldy, (v * LANES + lane) * 8, a.len, VEC,
-                                  narrow8<KIND>(t[v], inv));
+                for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                    for (int v = 0; v < N; ++v) {
+                        const float other = __shfl_xor_sync(0xffffffffu, most[v], o);
+                        if (o < lanes)
+                            most[v] = Max()(most[v], other);
+                    }
+            } else {
+#pragma unroll
+                for (int v = 1; v < N; ++v)
+                    most[0] = Max()(most[0], most[v]);
+                most[0] = group_fold<LANES>(most[0], sh, turn, Max());
+            }
+#pragma unroll
+            for (int v = 0; v < N; ++v) {
+                const int i = (v * LANES + lane) * E;
+                float inv;
+                const float scale = scale_of<KIND>(a.block ? most[v] : most[0], &inv);
+                if (here && i < a.len) {
+                    if (a.block ? lane % (a.block / E) == 0 : v == 0 && lane == 0)
+                        a.scales[r * a.blocks + (a.block ? i / a.block : 0)] = scale;
+                    store_q<E>(static_cast<uint8_t *>(a.y), r * a.ldy, i, a.len, VEC, narrow8<KIND>(t[v], inv));
+                }
             }
         }
     }
@@ -227,15 +282,34 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArg
 #else
 // ---------------------------------------------------------------- backward
 
+__device__ __forceinline__ void store_typed(int type, void *p, int64_t i, float v)
+{
+    if (type == RED_F32)
+        store_elem<RED_F32>(p, i, v);
+    else if (type == RED_F16)
+        store_elem<RED_F16>(p, i, v);
+    else
+        store_elem<RED_BF16>(p, i, v);
+}
+
+// Column i of this CTA's share of dw; the only CTA's is dw itself.
+__device__ __forceinline__ void write_share(const NormGradArgs &a, int i, float v)
+{
+    if (gridDim.x == 1)
+        store_typed(a.wtype, a.dw, i, v);
+    else
+        a.part[(int64_t)blockIdx.x * a.len + i] = v;
+}
+
 template <int DT, bool WIDE, int LANES, int VECS, bool VEC>
 __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_grad_kernel(const NormGradArgs a)
 {
     pdl_enter();
     __shared__ GroupShared<LANES> sh;
-    constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
+    constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES, N = UNITS<DT, VECS>, E = UNIT<DT>;
     // groups of one warp or less meet in shared memory before the workspace
-    __shared__ float meet[GROUPS > 1 ? VECS * LANES * 8 : 1];
-    using Rows = Ring<DT, LANES, VECS, 3>;
+    __shared__ float meet[GROUPS > 1 ? NT / 32 * N * LANES * E : 1];
+    using Rows = Ring<DT, LANES, UNITS<DT, VECS>, 3>;
     extern __shared__ __align__(16) unsigned char ring[];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const int64_t step = (int64_t)gridDim.x * GROUPS, first = (int64_t)blockIdx.x * GROUPS + group;
@@ -254,26 +328,24 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_grad_kernel(const No
         for (int k = 0; k < Rows::STAGES - 1; ++k)
             fetch(first + k * step, k);
     }
-    const Weights<DT, WIDE, VEC, LANES, VECS> weights(a.weight, lane, a.len);
-    float dw[VECS][8];
+    const Weights<DT, WIDE, VEC, LANES, N> weights(a.weight, lane, a.len);
+    float dw[N][E];
 #pragma unroll
-    for (int v = 0; v < VECS; ++v)
+    for (int v = 0; v < N; ++v)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < E; ++k)
             dw[v][k] = 0.0f;
     float rstd_next = first < a.rows ? a.rstd[first] : 0.0f;
     for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += step) {
         const bool here = r0 + group < a.rows;
         const int64_t r = here ? r0 + group : a.rows - 1;
-        Raw<DT> x[VECS], dy[VECS], dt[VECS];
+        Raw x[N], dy[N], dt[N];  // (in shared memory where rows are fetched ahead)
         const float rstd = rstd_next;
         if (r0 + group + step < a.rows)
             rstd_next = a.rstd[r0 + group + step];
         if constexpr (VEC) {
             fetch(r0 + group + (Rows::STAGES - 1) * step, (stage + Rows::STAGES - 1) % Rows::STAGES);
             fetch_wait<Rows::STAGES - 1>();
-            Rows::take(x, ring, stage, 0);
-            Rows::take(dy, ring, stage, 1);
         } else {
             load_row<DT, VEC, LANES>(x, a.x, r * a.ldx, lane, a.len);
             load_row<DT, VEC, LANES>(dy, a.dy, r * a.ldy, lane, a.len);
@@ -282,13 +354,13 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_grad_kernel(const No
         }
         float c = 0.0f;
 #pragma unroll
-        for (int v = 0; v < VECS; ++v) {
-            float h[8], g[8], w[8];
-            widen<DT>(x[v], h);
-            widen<DT>(dy[v], g);
+        for (int v = 0; v < N; ++v) {
+            float h[E], g[E], w[E];
+            widen<DT>(VEC ? Rows::take(ring, stage, 0, v) : x[v], h);
+            widen<DT>(VEC ? Rows::take(ring, stage, 1, v) : dy[v], g);
             weights.at(v, w);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < E; ++k) {
                 h[k] *= rstd;
                 if (here)
                     dw[v][k] = fmaf(g[k], h[k], dw[v][k]);
@@ -296,88 +368,88 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_grad_kernel(const No
             }
         }
         c = group_fold<LANES>(c, sh, turn, Add()) * a.inv_len;
-        if constexpr (VEC) {
-            if (a.dtotal)
-                Rows::take(dt, ring, stage, 2);
-            stage = (stage + 1) % Rows::STAGES;
-        }
+        const int at = stage;
+        stage = (stage + 1) % Rows::STAGES;
         if (!here)
             continue;
-        // h and g again, from what the loads brought: registers for them would be other rows' loads in flight
+        // h and g again, from what the loads brought: registers hold the weights and dw
 #pragma unroll
-        for (int v = 0; v < VECS; ++v) {
-            float h[8], g[8], w[8], d[8];
-            widen<DT>(x[v], h);
-            widen<DT>(dy[v], g);
+        for (int v = 0; v < N; ++v) {
+            float h[E], g[E], w[E], d[E];
+            widen<DT>(VEC ? Rows::take(ring, at, 0, v) : x[v], h);
+            widen<DT>(VEC ? Rows::take(ring, at, 1, v) : dy[v], g);
             weights.at(v, w);
             if (a.dtotal)
-                widen<DT>(dt[v], d);
+                widen<DT>(VEC ? Rows::take(ring, at, 2, v) : dt[v], d);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < E; ++k) {
                 const float n = fmaf(-h[k] * rstd, c, g[k] * w[k]);
                 d[k] = a.dtotal ? fmaf(n, rstd, d[k]) : n * rstd;
             }
-            store8<DT, VEC>(a.dx, r * a.ldd, (v * LANES + lane) * 8, a.len, d);
+            store_unit<DT, VEC>(a.dx, r * a.ldd, (v * LANES + lane) * E, a.len, d);
         }
     }
-    if (!a.part)
+    if (!a.dw)
         return;
     if constexpr (GROUPS > 1) {
-        for (int turn_of = 0; turn_of < GROUPS; ++turn_of) {
-            if (group == turn_of) {
+        // the groups of a warp by shuffles, the warps through shared memory
 #pragma unroll
-                for (int v = 0; v < VECS; ++v)
+        for (int v = 0; v < N; ++v)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float *m = &meet[(v * 8 + k) * LANES + lane];
-                        *m = turn_of == 0 ? dw[v][k] : *m + dw[v][k];
-                    }
+            for (int k = 0; k < E; ++k) {
+#pragma unroll
+                for (int o = LANES; o < 32; o <<= 1)
+                    dw[v][k] += __shfl_xor_sync(0xffffffffu, dw[v][k], o);
+                if (threadIdx.x % 32 < LANES)
+                    meet[(threadIdx.x / 32 * N + v) * LANES * E + lane * E + k] = dw[v][k];
             }
-            __syncthreads();
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.len; i += NT) {
+            float sum = meet[i];
+#pragma unroll
+            for (int w = 1; w < NT / 32; ++w)
+                sum += meet[w * N * LANES * E + i];
+            write_share(a, i, sum);
         }
+    } else {
 #pragma unroll
-        for (int v = 0; v < VECS; ++v)
+        for (int v = 0; v < N; ++v) {
+            const int i = (v * LANES + lane) * E;
+            if (gridDim.x > 1 && a.len % 4 == 0 && i + E <= a.len) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                dw[v][k] = meet[(v * 8 + k) * LANES + lane];
-        if (group != 0)
-            return;
+                for (int k = 0; k < E; k += 4)
+                    *reinterpret_cast<float4 *>(a.part + (int64_t)blockIdx.x * a.len + i + k) =
+                        make_float4(dw[v][k], dw[v][k + 1], dw[v][k + 2], dw[v][k + 3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (i + k < a.len)
+                        write_share(a, i + k, dw[v][k]);
+            }
+        }
     }
-#pragma unroll
-    for (int v = 0; v < VECS; ++v)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int i = (v * LANES + lane) * 8 + k;
-            if (i < a.len)
-                a.part[(int64_t)blockIdx.x * a.len + i] = dw[v][k];
-        }
 }
 
-// dw from the CTAs' shares: 32 columns by 8 lanes of shares, in a fixed order.
-__global__ void __launch_bounds__(256) rmsnorm_join_kernel(const float *part, int parts, int len, int wtype, void *dw)
+// dw from the CTAs' shares: 32 columns by 32 lanes of shares, in a fixed order.
+constexpr int JOIN_TURNS = 32;
+__global__ void __launch_bounds__(32 * JOIN_TURNS) rmsnorm_join_kernel(const NormGradArgs a, int parts)
 {
     pdl_enter();
-    __shared__ float sums[8][33];
-    const int col = blockIdx.x * 32 + threadIdx.x % 32, turn = threadIdx.x / 32;
+    __shared__ float sums[JOIN_TURNS][33];
+    const int lane = threadIdx.x % 32, turn = threadIdx.x / 32, col = blockIdx.x * 32 + lane;
     float s = 0.0f;
-    if (col < len) {
-#pragma unroll 4
-        for (int p = turn; p < parts; p += 8)
-            s += part[(int64_t)p * len + col];
+    if (col < a.len) {
+#pragma unroll 8
+        for (int p = turn; p < parts; p += JOIN_TURNS)
+            s += a.part[(int64_t)p * a.len + col];
     }
-    sums[turn][threadIdx.x % 32] = s;
+    sums[turn][lane] = s;
     __syncthreads();
-    if (turn == 0 && col < len) {
-#pragma unroll
-        for (int k = 1; k < 8; ++k)
-            s += sums[k][threadIdx.x % 32];
-        if (wtype == RED_F32)
-            store_elem<RED_F32>(dw, col, s);
-        else if (wtype == RED_F16)
-            store_elem<RED_F16>(dw, col, s);
-        else
-            store_elem<RED_BF16>(dw, col, s);
-    }
+    s = sums[lane][turn];  // column `turn` of the 32, a share per lane
+    for (int o = 16; o; o >>= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0 && blockIdx.x * 32 + turn < a.len)
+        store_typed(a.wtype, a.dw, blockIdx.x * 32 + turn, s);
 }
 
 #endif
@@ -385,18 +457,19 @@ __global__ void __launch_bounds__(256) rmsnorm_join_kernel(const float *part, in
 // ---------------------------------------------------------------- launches
 
 #ifndef RED_RMSNORM_BACKWARD
-template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC>
+template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC, bool RING>
 int forward(const NormArgs &a, cudaStream_t s)
 {
     static Resident cache;
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
+    constexpr size_t SMEM = RING ? Ring<DT, LANES, UNITS<DT, VECS>, 2>::BYTES : 0;
+    auto *const kernel = rmsnorm_kernel<DT, WIDE, KIND, LANES, VECS, VEC, RING>;
     unsigned grid;
-    const int st = resident_grid(rmsnorm_kernel<DT, WIDE, KIND, LANES, VECS, VEC>, cache, NT, 0, (a.rows + GROUPS - 1) / GROUPS,
-                           INT32_MAX, &grid);
+    const int st = resident_grid(kernel, cache, NT, SMEM, (a.rows + GROUPS - 1) / GROUPS, INT32_MAX, &grid);
     if (st != RED_OK)
         return st;
     count_launches(1);
-    return cuda_fail(launch_pdl(rmsnorm_kernel<DT, WIDE, KIND, LANES, VECS, VEC>, dim3(grid), dim3(NT), s, a), "rmsnorm");
+    return cuda_fail(launch_pdl_dynamic(kernel, dim3(grid), dim3(NT), SMEM, s, a), "rmsnorm");
 }
 
 }  // namespace
@@ -406,9 +479,19 @@ int forward_of(const NormArgs &a, int kind, cudaStream_t s)
 {
     return with_group((a.len + 7) / 8, [&](auto lanes, auto vecs) {
         constexpr int L = decltype(lanes)::value, V = decltype(vecs)::value;
-        return kind == 0               ? forward<DT, WIDE, 0, L, V, VEC>(a, s)
-               : kind == RED_QUANT_E4M3 ? forward<DT, WIDE, RED_QUANT_E4M3, L, V, VEC>(a, s)
-                                        : forward<DT, WIDE, RED_QUANT_I8, L, V, VEC>(a, s);
+        // Rows fetched ahead or loaded where they are wanted, us at bf16: without a residual 16384 x
+        // 4096 43 / 54, in 8 bits 16384 x 8192 176 / 208, with a residual 8192 x 2048 20 / 22, 4097 x
+        // 5120 28 / 36 -- but with two matrices read and two of 16 bits written, and most of the
+        // lanes' units in use, 16384 x 4096 94 / 83, 16384 x 8192 186 / 172, 65536 x 1024 91 / 83, 60000 x
+        // 640 (five eighths of the units) 52 / 65.  fp32 is the same either way.
+        constexpr bool DIRECT = VEC && V != 3 && L * V >= 128 && DT != RED_F32;
+        if constexpr (DIRECT) {
+            if (kind == 0 && a.residual && a.len > 6 * L * V)
+                return forward<DT, WIDE, 0, L, V, VEC, false>(a, s);
+        }
+        return kind == 0                ? forward<DT, WIDE, 0, L, V, VEC, VEC>(a, s)
+               : kind == RED_QUANT_E4M3 ? forward<DT, WIDE, RED_QUANT_E4M3, L, V, VEC, VEC>(a, s)
+                                        : forward<DT, WIDE, RED_QUANT_I8, L, V, VEC, VEC>(a, s);
     });
 }
 
@@ -429,58 +512,62 @@ template int rmsnorm_forward<RED_RMSNORM_DT>(const NormArgs &, int, cudaStream_t
 
 #else
 template <int DT, bool WIDE, int LANES, int VECS, bool VEC>
-int backward(NormGradArgs a, int wtype, void *dw, cudaStream_t s)
+int backward(NormGradArgs a, cudaStream_t s)
 {
     static Resident cache;
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
-    constexpr size_t SMEM = VEC ? Ring<DT, LANES, VECS, 3>::BYTES : 0;
+    constexpr size_t SMEM = VEC ? Ring<DT, LANES, UNITS<DT, VECS>, 3>::BYTES : 0;
     unsigned grid;
-    int st = resident_grid(rmsnorm_grad_kernel<DT, WIDE, LANES, VECS, VEC>, cache, NT, SMEM, (a.rows + GROUPS - 1) / GROUPS,
-                     (int64_t)(WS_PART_ELEMS / (size_t)a.len), &grid);
+    auto *const kernel = rmsnorm_grad_kernel<DT, WIDE, LANES, VECS, VEC>;
+    int st = resident_grid(kernel, cache, NT, SMEM, (a.rows + GROUPS - 1) / GROUPS,
+                           (int64_t)(WS_PART_ELEMS / (size_t)a.len), &grid);
     if (st != RED_OK)
         return st;
-    if (dw) {
+    const bool join = a.dw && grid > 1;
+    if (join) {
         Workspace ws;
         st = get_workspace(&ws);
         if (st != RED_OK)
             return st;
         a.part = static_cast<float *>(ws.part);
     }
-    st = cuda_fail(launch_pdl_dynamic(rmsnorm_grad_kernel<DT, WIDE, LANES, VECS, VEC>, dim3(grid), dim3(NT), SMEM, s, a), "rmsnorm_grad");
-    if (st != RED_OK || !dw) {
-        count_launches(1);
+    st = cuda_fail(launch_pdl_dynamic(kernel, dim3(grid), dim3(NT), SMEM, s, a),
+                   "rmsnorm_grad");
+    if (st != RED_OK)
         return st;
-    }
-    count_launches(2);
-    return cuda_fail(launch_pdl(rmsnorm_join_kernel, dim3((unsigned)((a.len + 31) / 32)), dim3(256), s, a.part, (int)grid,
-                                a.len, wtype, dw),
+    count_launches(1);
+    if (!join)
+        return RED_OK;
+    count_launches(1);
+    return cuda_fail(launch_pdl(rmsnorm_join_kernel, dim3((unsigned)((a.len + 31) / 32)), dim3(32 * JOIN_TURNS), s, a,
+                                (int)grid),
                      "rmsnorm_join");
 }
 
 }  // namespace
 
 template <int DT, bool WIDE, bool VEC>
-int backward_of(const NormGradArgs &a, int wtype, void *dw, cudaStream_t s)
+int backward_of(const NormGradArgs &a, cudaStream_t s)
 {
     return with_group((a.len + 7) / 8, [&](auto lanes, auto vecs) {
-        return backward<DT, WIDE, decltype(lanes)::value, decltype(vecs)::value, VEC>(a, wtype, dw, s);
+        return backward<DT, WIDE, decltype(lanes)::value, decltype(vecs)::value, VEC>(a, s);
     });
 }
 
 template <int DT>
-int rmsnorm_backward(const NormGradArgs &a, int wtype, void *dw, cudaStream_t s)
+int rmsnorm_backward(const NormGradArgs &a, cudaStream_t s)
 {
     const int elem = DT == RED_F32 ? 4 : 2;
     const bool vec = aligned_rows(a.x, a.ldx, a.rows, elem) && aligned_rows(a.dy, a.ldy, a.rows, elem) &&
                      aligned_rows(a.dtotal, a.ldt, a.rows, elem) && aligned_rows(a.dx, a.ldd, a.rows, elem) &&
                      aligned_rows(a.weight, 0, 1, 1);
     if (DT != RED_F32 && a.wide)
-        return vec ? backward_of<DT, true, true>(a, wtype, dw, s) : backward_of<DT, true, false>(a, wtype, dw, s);
-    return vec ? backward_of<DT, DT == RED_F32, true>(a, wtype, dw, s)
-               : backward_of<DT, DT == RED_F32, false>(a, wtype, dw, s);
+        return vec ? backward_of<DT, true, true>(a, s) : backward_of<DT, true, false>(a, s);
+    return vec ? backward_of<DT, DT == RED_F32, true>(a, s)
+               : backward_of<DT, DT == RED_F32, false>(a, s);
 }
 
-template int rmsnorm_backward<RED_RMSNORM_DT>(const NormGradArgs &, int, void *, cudaStream_t);
+template int rmsnorm_backward<RED_RMSNORM_DT>(const NormGradArgs &, cudaStream_t);
 
 #endif
 #endif

@@ -108,15 +108,19 @@ int red_rmsnorm_quant(int dtype, const void *x, int64_t rows, int64_t len, int64
     const char *who = "red_rmsnorm_quant";
     if (kind != RED_QUANT_E4M3 && kind != RED_QUANT_I8)
         return fail(RED_EINVAL, "%s: unknown kind %d", who, kind);
-    if (block != 0 && block != 32 && block != 64 && block != 128 && block != 256)
-        return fail(RED_EINVAL, "%s: block = %lld is not 0, 32, 64, 128 or 256", who, (long long)block);
+    if (block != 0 && block != 32 && block != 64 && block != 128)
+        return fail(RED_EINVAL, "%s: block = %lld is not 0, 32, 64 or 128", who, (long long)block);
     if (rows > 0 && (!scales || (uintptr_t)scales % 4 != 0))
         return fail(RED_EINVAL, "%s: scales is NULL or not 4-byte aligned", who);
     NormArgs a = {};
     a.x = x, a.residual = residual, a.weight = weight, a.rows = rows, a.ldx = ldx, a.ldr = ldr, a.eps = eps;
     a.y = q, a.ldy = ldq, a.total = total, a.ldt = ldt, a.rstd = rstd, a.scales = scales;
-    a.block = (int)block;
-    a.blocks = block ? (int)((len + block - 1) / block) : 1;
+    if (block > 0 && block < len) {  // (else one scale per row, whichever it is called)
+        a.block = (int)block;
+        a.blocks = (int)((len + block - 1) / block);
+    } else {
+        a.blocks = 1;
+    }
     return forward(who, dtype, a, len, wtype, kind, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -149,13 +153,13 @@ int red_rmsnorm_grad(int dtype, const void *dy, int64_t lddy, const void *x, int
         return fail(RED_EINVAL, "%s: rstd is NULL or not 4-byte aligned", who);
     NormGradArgs a = {};
     a.dy = dy, a.x = x, a.weight = weight, a.dtotal = dtotal, a.rstd = rstd, a.rows = rows, a.ldy = lddy, a.ldx = ldx;
-    a.ldt = ldt, a.ldd = ldd, a.dx = dx;
+    a.ldt = ldt, a.ldd = ldd, a.dx = dx, a.dw = dweight, a.wtype = wtype;
     a.len = (int)len;
     a.wide = wtype == RED_F32;
     a.inv_len = (float)(1.0 / (double)len);
-    return dtype == RED_F32   ? rmsnorm_backward<RED_F32>(a, wtype, dweight, s)
-           : dtype == RED_F16 ? rmsnorm_backward<RED_F16>(a, wtype, dweight, s)
-                              : rmsnorm_backward<RED_BF16>(a, wtype, dweight, s);
+    return dtype == RED_F32   ? rmsnorm_backward<RED_F32>(a, s)
+           : dtype == RED_F16 ? rmsnorm_backward<RED_F16>(a, s)
+                              : rmsnorm_backward<RED_BF16>(a, s);
 }
 
 }  // extern "C"

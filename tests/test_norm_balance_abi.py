@@ -52,7 +52,7 @@ def test_shared_refusals(itr, call, bad):
      dict(res=R + 1), dict(total=T + 1), dict(ldr=15), dict(ldt=15), dict(total=X, ldt=24), dict(total=Y))] + [
     (norm, dict(y=X, ldy=24)), (norm, dict(y=R, ldy=24)), (norm, dict(y=Y + 1)),
     (quant, dict(kind=0)), (quant, dict(kind=3)), (quant, dict(block=16)), (quant, dict(block=-32)),
-    (quant, dict(block=512)), (quant, dict(scales=None)), (quant, dict(scales=Q + 2)), (quant, dict(y=X)),
+    (quant, dict(block=256)), (quant, dict(scales=None)), (quant, dict(scales=Q + 2)), (quant, dict(y=X)),
     (grad, dict(dy=None)), (grad, dict(dx=None)), (grad, dict(lddy=15)), (grad, dict(ldd=15)), (grad, dict(ldt=15)),
     (grad, dict(dx=Y, ldd=24)), (grad, dict(dx=X, ldd=24)), (grad, dict(dx=T, ldd=24)), (grad, dict(rstd=None)),
     (grad, dict(dw=Q + 1)),
