@@ -393,12 +393,34 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
 
 // ----------------------------------------------------------- join of the parts
 
-// A warp per row: (maximum, sum) pairs of the tiles to lse and logp.
+// (maximum, sum) pairs of a row's tiles to its lse and logp: a warp per row, or a CTA
+// where rows are few.
+struct Pair {
+    float m, l;
+    __device__ __forceinline__ void join(float om, float ol)
+    {
+        const float top = fmaxf(m, om);
+        const float ref = top == NEG_INF ? 0.0f : top;
+        l = l * ex2(m - ref) + ol * ex2(om - ref);
+        m = top;
+    }
+    __device__ __forceinline__ void join_lanes()
+    {
+        for (int o = 16; o; o >>= 1) {
+            const float om = __shfl_xor_sync(0xffffffffu, m, o), ol = __shfl_xor_sync(0xffffffffu, l, o);
+            join(om, ol);
+        }
+    }
+};
+
+template <int LANES>
 __global__ void __launch_bounds__(256) linear_join_kernel(const LinearWork w, int64_t rows, float s2, float *logp, float *lse)
 {
     pdl_enter();
-    const int lane = threadIdx.x % 32;
-    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < rows; r += (int64_t)gridDim.x * 8) {
+    __shared__ float2 warps[8];
+    constexpr int GROUPS = 256 / LANES;
+    const int lane = threadIdx.x % LANES;
+    for (int64_t r = (int64_t)blockIdx.x * GROUPS + threadIdx.x / LANES; r < rows; r += (int64_t)gridDim.x * GROUPS) {
         const int at = w.pos[r];
         if (at < 0) {
             if (lane == 0)
@@ -406,26 +428,28 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearWork w, in
             continue;
         }
         const float2 *part = w.part + (int64_t)at * w.slots;
-        float m = NEG_INF, l = 0.0f;
-        for (int64_t i = lane; i < w.slots; i += 32) {
-            const float2 p = part[i];
-            const float top = fmaxf(m, p.x);
-            const float ref = top == NEG_INF ? 0.0f : top;
-            l = l * ex2(m - ref) + p.y * ex2(p.x - ref);
-            m = top;
+        Pair p = {NEG_INF, 0.0f};
+#pragma unroll 4
+        for (int64_t i = lane; i < w.slots; i += LANES) {
+            const float2 o = part[i];
+            p.join(o.x, o.y);
         }
-        for (int o = 16; o; o >>= 1) {
-            const float om = __shfl_xor_sync(0xffffffffu, m, o), ol = __shfl_xor_sync(0xffffffffu, l, o);
-            const float top = fmaxf(m, om);
-            const float ref = top == NEG_INF ? 0.0f : top;
-            l = l * ex2(m - ref) + ol * ex2(om - ref);
-            m = top;
+        p.join_lanes();
+        if constexpr (LANES > 32) {  // (a CTA's row is the same for all its threads)
+            __syncthreads();
+            if (lane % 32 == 0)
+                warps[lane / 32] = make_float2(p.m, p.l);
+            __syncthreads();
+            p = {NEG_INF, 0.0f};
+            if (lane % 32 < LANES / 32)
+                p = {warps[lane % 32].x, warps[lane % 32].y};
+            p.join_lanes();
         }
         if (lane == 0) {
             constexpr float LN2 = 0.6931471805599453f;
-            const float log_l = log2f(l);
-            lse[r] = (m + log_l) * LN2;
-            logp[r] = (fmaf(w.taken[at], s2, -m) - log_l) * LN2;
+            const float log_l = log2f(p.l);
+            lse[r] = (p.m + log_l) * LN2;
+            logp[r] = (fmaf(w.taken[at], s2, -p.m) - log_l) * LN2;
         }
     }
 }
@@ -441,6 +465,7 @@ struct ProductArgs {
     LinearWork work;
     int v0, v_count;    // the piece: first column of the vocabulary, columns
     int n_tiles;        // along dim
+    int splits;         // of dh, along the vocabulary
     int first;          // dh: store (1) or add (0)
     uint16_t *dweight;  // dw's memory, for the end of rows that do not end on 16 bytes
     int64_t lddw;
@@ -534,14 +559,17 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
     const int live = a.work.head->live;
     const int h_rows = a.with_dh ? (live + TILE - 1) / TILE : 0;
     const int w_rows = a.with_dw ? (a.v_count + TILE - 1) / TILE : 0;
-    const int h_tiles = h_rows * a.n_tiles, tiles = h_tiles + w_rows * a.n_tiles;
+    const int h_each = h_rows * a.n_tiles, h_tiles = h_each * a.splits, tiles = h_tiles + w_rows * a.n_tiles;
     const int v_blocks = (a.v_count + BLOCK_K - 1) / BLOCK_K, r_blocks = (live + BLOCK_K - 1) / BLOCK_K;
+    const int v_each = (v_blocks + a.splits - 1) / a.splits;
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
     auto job = [&](int t) {
         if (t < h_tiles) {
-            const TileAt at = tile_at(t, h_rows, a.n_tiles);
-            return TileJob{&a.g_k, &a.w_n, at.m * TILE, at.n * TILE, 0, a.v0, v_blocks, true, false};
+            const int split = t / h_each, k = split * v_each;
+            const TileAt at = tile_at(t - split * h_each, h_rows, a.n_tiles);
+            return TileJob{&a.g_k, &a.w_n, at.m * TILE, at.n * TILE, k * BLOCK_K, a.v0 + k * BLOCK_K,
+                           max(0, min(v_each, v_blocks - k)), true, false};
         }
         const TileAt at = tile_at(t - h_tiles, w_rows, a.n_tiles);
         return TileJob{&a.g_m, &a.h_n, at.m * TILE, at.n * TILE, 0, 0, r_blocks, false, false};
@@ -578,7 +606,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
             const int row = j.a_row + rank * HALF + group * 32, col = j.b_row + half * HALF;
             const uint32_t free = j.blocks == 0 ? 0 : empty[acc.slot];
             if (t < h_tiles)
-                store_product<DT, true>(a, ok, from, free, row, col, unit, staging, lane);
+                store_product<DT, true>(a, ok, from, free, row + t / h_each * (int)a.work.padded, col, unit, staging, lane);
             else
                 store_product<DT, false>(a, ok, from, free, row, col, unit, staging, lane);
             if (j.blocks != 0)
@@ -591,32 +619,38 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
     mma_end(b, warp);
 }
 
-// The sums of the pieces to the rows' gradients, rounded once; a warp per row.
-// Zeros where a row takes no part.
+// The sums of the pieces, and of their splits, to the rows' gradients, rounded once:
+// a thread per eight elements.  Zeros where a row takes no part.
 template <int DT>
 __global__ void __launch_bounds__(256)
     linear_scatter_kernel(const LinearWork w, int64_t rows, int64_t dim, uint16_t *dhidden, int64_t ldd)
 {
     pdl_enter();
-    const int lane = threadIdx.x % 32;
     const float unit = w.head->unit;
-    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < rows; r += (int64_t)gridDim.x * 8) {
+    const int64_t vecs = (dim + 7) / 8, split = w.padded * w.dim4;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * vecs; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / vecs, d = (i - r * vecs) * 8;
         const int at = w.pos[r];
-        uint16_t *to = dhidden + r * ldd;
-        const float *from = w.dhidden + (int64_t)at * w.dim4;
-        const int64_t vecs = dim / 8;
-        for (int64_t i = lane; i < vecs; i += 32) {
-            uint4 o = make_uint4(0, 0, 0, 0);
-            if (at >= 0) {
-                const float4 x = reinterpret_cast<const float4 *>(from)[2 * i];
-                const float4 y = reinterpret_cast<const float4 *>(from)[2 * i + 1];
-                o = make_uint4(pack2<DT>(x.x * unit, x.y * unit), pack2<DT>(x.z * unit, x.w * unit),
-                               pack2<DT>(y.x * unit, y.y * unit), pack2<DT>(y.z * unit, y.w * unit));
+        uint16_t *to = dhidden + r * ldd + d;
+        float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (at >= 0) {
+            const float *from = w.dhidden + (int64_t)at * w.dim4 + d;
+            const bool both = d + 4 < dim;
+#pragma unroll 4
+            for (int s = 0; s < w.splits; ++s) {
+                const float4 lo = *reinterpret_cast<const float4 *>(from + s * split);
+                const float4 hi = both ? *reinterpret_cast<const float4 *>(from + s * split + 4) : make_float4(0, 0, 0, 0);
+                x[0] += lo.x, x[1] += lo.y, x[2] += lo.z, x[3] += lo.w;
+                x[4] += hi.x, x[5] += hi.y, x[6] += hi.z, x[7] += hi.w;
             }
-            reinterpret_cast<uint4 *>(to)[i] = o;
         }
-        for (int64_t i = vecs * 8 + lane; i < dim; i += 32)
-            to[i] = at >= 0 ? (uint16_t)pack2<DT>(from[i] * unit, 0.0f) : (uint16_t)0;
+        if (d + 8 <= dim) {
+            *reinterpret_cast<uint4 *>(to) = make_uint4(pack2<DT>(x[0] * unit, x[1] * unit), pack2<DT>(x[2] * unit, x[3] * unit),
+                                                        pack2<DT>(x[4] * unit, x[5] * unit), pack2<DT>(x[6] * unit, x[7] * unit));
+        } else {
+            for (int k = 0; k < 8 && d + k < dim; ++k)
+                to[k] = (uint16_t)pack2<DT>(x[k] * unit, 0.0f);
+        }
     }
 }
 
@@ -783,7 +817,13 @@ LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, boo
         take(w.lse2, rows * 4);
         take(g, w.padded * w.piece_cols * 2);
         w.piece = g;
-        take(w.dhidden, w.padded * w.dim4 * 4);
+        // dh of few rows is few tiles that are long: shares of the vocabulary fill the pairs of CTAs
+        // (64 x 1024 x 32001: four tiles of 501 blocks of K, products 191 us; 18 shares SPLITNOW)
+        const int64_t tiles = w.padded / TILE * (up(dim, TILE) / TILE), blocks = w.piece_cols / BLOCK_K;
+        int64_t splits = w.piece_cols < up(vocab, TILE) ? 1 : 72 / tiles;
+        splits = splits < blocks / 8 ? splits : blocks / 8;
+        w.splits = splits < 1 ? 1 : (int)splits;
+        take(w.dhidden, w.splits * w.padded * w.dim4 * 4);
     }
     w.bytes = at;
     return w;
@@ -805,7 +845,9 @@ int launch_linear_logprob(const LinearArgs &a, float *logp, float *lse, void *wo
     l.s2 = (float)(a.scale * 1.4426950408889634);
     const int64_t tiles = w.padded / TILE * l.n_tiles;
     RETURN_IF((a.dtype == RED_BF16 ? launch_logits<RED_BF16, false>(tiles, s, l) : launch_logits<RED_F16, false>(tiles, s, l)));
-    RETURN_IF(cuda_fail(launch_pdl(linear_join_kernel, dim3(warp_rows_grid(a.rows)), dim3(256), s, w, a.rows, l.s2, logp,
+    const bool few = a.rows <= 2048;
+    RETURN_IF(cuda_fail(launch_pdl(few ? linear_join_kernel<256> : linear_join_kernel<32>,
+                                   dim3(few ? (unsigned)a.rows : warp_rows_grid(a.rows)), dim3(256), s, w, a.rows, l.s2, logp,
                                    lse),
                         "linear_join"));
     count_launches(1);
@@ -826,7 +868,7 @@ int launch_linear_logprob_grad(const LinearArgs &a, const float *lse, const floa
     RETURN_IF(matrix_map(&p.g_m, a.dtype, w.piece, w.piece_cols, w.padded, w.piece_cols, 64, BLOCK_K));
     RETURN_IF(matrix_map(&p.w_n, a.dtype, a.weight, a.dim, a.vocab, a.ldw, 64, BLOCK_K));
     RETURN_IF(matrix_map(&p.h_n, a.dtype, w.hidden, a.dim, w.padded, w.ld, 64, BLOCK_K));
-    RETURN_IF(matrix_map(&p.dh, RED_F32, w.dhidden, a.dim, w.padded, w.dim4, 32, 32));
+    RETURN_IF(matrix_map(&p.dh, RED_F32, w.dhidden, a.dim, w.padded * w.splits, w.dim4, 32, 32));
     if (dweight)
         RETURN_IF(matrix_map(&p.dw, a.dtype, dweight, a.dim, a.vocab, lddw, 64, 32));
     else
@@ -836,6 +878,7 @@ int launch_linear_logprob_grad(const LinearArgs &a, const float *lse, const floa
     l.k_blocks = (int)(up(a.dim, BLOCK_K) / BLOCK_K);
     l.s2 = (float)(a.scale * 1.4426950408889634);
     p.n_tiles = (int)(up(a.dim, TILE) / TILE);
+    p.splits = w.splits;
     p.with_dh = dhidden != nullptr;
     p.with_dw = dweight != nullptr;
     p.dweight = static_cast<uint16_t *>(dweight);
@@ -849,7 +892,7 @@ int launch_linear_logprob_grad(const LinearArgs &a, const float *lse, const floa
         p.v_count = (int)count;
         p.first = v0 == 0;
         const int64_t m_tiles = w.padded / TILE;
-        const int64_t tiles = (p.with_dh ? m_tiles : 0) * p.n_tiles + (int64_t)(p.with_dw ? l.n_tiles : 0) * p.n_tiles;
+        const int64_t tiles = (p.with_dh ? m_tiles * w.splits : 0) * p.n_tiles + (int64_t)(p.with_dw ? l.n_tiles : 0) * p.n_tiles;
         if (a.dtype == RED_BF16) {
             RETURN_IF((launch_logits<RED_BF16, true>(m_tiles * l.n_tiles, s, l)));
             RETURN_IF(launch_products<RED_BF16>(tiles, s, p));
@@ -860,7 +903,7 @@ int launch_linear_logprob_grad(const LinearArgs &a, const float *lse, const floa
     }
     if (dhidden) {
         auto *const kernel = a.dtype == RED_BF16 ? linear_scatter_kernel<RED_BF16> : linear_scatter_kernel<RED_F16>;
-        RETURN_IF(cuda_fail(launch_pdl(kernel, dim3(warp_rows_grid(a.rows)), dim3(256), s, w, a.rows, a.dim,
+        RETURN_IF(cuda_fail(launch_pdl(kernel, dim3(warp_rows_grid(a.rows * up(a.dim, 8) / 8 / 32 + 1)), dim3(256), s, w, a.rows, a.dim,
                                        static_cast<uint16_t *>(dhidden), ldd),
                             "linear_scatter"));
         count_launches(1);

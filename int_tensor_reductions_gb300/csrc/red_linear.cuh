@@ -28,10 +28,11 @@ struct LinearWork {
     float2 *part;       // packed x slots: (maximum, sum)         (forward)
     float *by_target, *by_p, *lse2;  // packed coefficients       (gradients)
     void *piece;        // padded x piece: gradient by the logits (gradients)
-    float *dhidden;     // padded x dim4 sums                     (gradients)
+    float *dhidden;     // splits x padded x dim4 sums            (gradients)
     int64_t padded, ld, dim4;
     int64_t slots;      // of part, per row
     int64_t piece_cols;
+    int splits;         // shares of dh along the vocabulary
     int64_t bytes;
 };
 
