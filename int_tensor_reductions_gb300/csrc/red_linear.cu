@@ -28,7 +28,7 @@ namespace {
 // Blocks of 64 of K whose products are summed by the tensor cores before the
 // sum moves to fp32 registers.  The tensor cores' additions round toward
 // zero, so a long sum drifts with its number of steps.
-constexpr int CHUNK = 8;
+constexpr int CHUNK = 16;
 // Rows of tiles that are taken in turn along the vocabulary.
 constexpr int BAND = 16;
 
@@ -214,31 +214,31 @@ struct LogitArgs {
 };
 
 // One warp's 32 rows x 128 columns of z / scale in fp32 registers: the sums of
-// the chunks.
-__device__ __forceinline__ void take_sums(float (&z)[HALF], MmaBarriers &b, AccPos &acc, int blocks, uint32_t lanes,
+// the chunks.  Whether they are right: after a wait that ran out they are whatever
+// tensor memory held (and what is made of them has to become NaN; filling them
+// here costs the registers of a second set).
+__device__ __forceinline__ bool take_sums(float (&z)[HALF], MmaBarriers &b, AccPos &acc, int blocks, uint32_t lanes,
                                           int half, uint32_t (&empty)[2])
 {
+    bool ok = true;
     for (int k = 0; k < blocks; k += CHUNK) {
-        const bool ok = mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
+        ok &= mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
         tmem_after();
         const uint32_t from = b.tmem + lanes + acc.slot * TILE + half * HALF;
-        if (!ok) {
-#pragma unroll
-            for (int i = 0; i < HALF; ++i)
-                z[i] = __int_as_float(0x7fffffff);
-        } else if (k == 0) {
+        if (k == 0) {
 #pragma unroll
             for (int i = 0; i < HALF; i += 16)
                 tmem_load16(from + i, reinterpret_cast<uint32_t *>(z + i));
             tmem_wait();
         } else {
 #pragma unroll
-            for (int i = 0; i < HALF; i += 16) {
-                uint32_t v[16];
+            for (int i = 0; i < HALF; i += 32) {
+                uint32_t v[32];
                 tmem_load16(from + i, v);
+                tmem_load16(from + i + 16, v + 16);
                 tmem_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int j = 0; j < 32; ++j)
                     z[i + j] += __uint_as_float(v[j]);
             }
         }
@@ -248,6 +248,7 @@ __device__ __forceinline__ void take_sums(float (&z)[HALF], MmaBarriers &b, AccP
             arrive_at(empty[acc.slot]);
         acc.next();
     }
+    return ok;
 }
 
 // Two floats as 16-bit values, the first in the low half.
@@ -313,7 +314,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
             const int target = takes ? a.work.target[row] - col : -1;
             const bool tail = col + HALF > a.vocab;
             float z[HALF];
-            take_sums(z, b, acc, a.k_blocks, (uint32_t)(group * 32) << 16, half, empty);
+            const bool ok = take_sums(z, b, acc, a.k_blocks, (uint32_t)(group * 32) << 16, half, empty);
+            constexpr float NOTHING = __builtin_nanf("");
             if constexpr (!GRAD) {
                 if (tail) {
 #pragma unroll
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
                     for (int i = 0; i < HALF; ++i)
                         zt = i == target ? z[i] : zt;
                     if ((unsigned)target < (unsigned)HALF)
-                        a.work.taken[row] = zt;
+                        a.work.taken[row] = ok ? zt : NOTHING;
                 }
                 float m = NEG_INF;
 #pragma unroll
@@ -341,10 +343,10 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
                     l[i % 4] += ex2(fmaf(z[i], a.s2, -off));
                 if (takes)
                     a.work.part[(int64_t)row * a.work.slots + (at.n * 2 + half)] =
-                        make_float2(m2, (l[0] + l[1]) + (l[2] + l[3]));
+                        make_float2(m2, ok ? (l[0] + l[1]) + (l[2] + l[3]) : NOTHING);
             } else {
                 const float ct = takes ? a.work.by_target[row] : 0.0f;
-                const float cp = takes ? a.work.by_p[row] : 0.0f;
+                const float cp = !ok ? NOTHING : takes ? a.work.by_p[row] : 0.0f;
                 const float lse2 = takes ? a.work.lse2[row] : 0.0f;
                 const bool here = __any_sync(0xffffffffu, (unsigned)target < (unsigned)HALF);
 #pragma unroll
@@ -364,13 +366,14 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     // 32 rows of 64 columns through shared memory, 16-byte units swizzled as the map says
+                    unsigned char *const box = staging + c * BOX_BYTES;
                     if (lane == 0)
-                        store_read();
+                        store_read<1>();
                     __syncwarp();
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
                         const float *v = z + c * 64 + u * 8;
-                        *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) * 16)) =
+                        *reinterpret_cast<uint4 *>(box + lane * 128 + ((u ^ (lane & 7)) * 16)) =
                             make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
                                        pack2<DT>(v[6], v[7]));
                     }
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
                     __syncwarp();
                     if (lane == 0) {
                         tma_store(&a.g, at.n * TILE + half * HALF + c * 64, at.m * TILE + rank * HALF + group * 32,
-                                  staging);
+                                  box);
                         store_commit();
                     }
                 }
@@ -494,10 +497,10 @@ __device__ __forceinline__ void store_product(const ProductArgs &a, bool ok, uin
             for (int i = 0; i < WIDTH; ++i)
                 v[i] = 0.0f;
         }
-        if (!ok) {
+        if (!ok) {  // (a wait ran out)
 #pragma unroll
             for (int i = 0; i < WIDTH; ++i)
-                v[i] = __int_as_float(0x7fffffff);
+                v[i] = __builtin_nanf("");
         }
         if (c + WIDTH == HALF && free) {
             tmem_before();
@@ -516,8 +519,9 @@ __device__ __forceinline__ void store_product(const ProductArgs &a, bool ok, uin
             }
             continue;
         }
+        unsigned char *const box = staging + c / WIDTH % 2 * BOX_BYTES;
         if (lane == 0)
-            store_read();
+            store_read<1>();
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -530,17 +534,17 @@ __device__ __forceinline__ void store_product(const ProductArgs &a, bool ok, uin
                 o = make_uint4(pack2<DT>(x[0] * unit, x[1] * unit), pack2<DT>(x[2] * unit, x[3] * unit),
                                pack2<DT>(x[4] * unit, x[5] * unit), pack2<DT>(x[6] * unit, x[7] * unit));
             }
-            *reinterpret_cast<uint4 *>(staging + lane * 128 + ((u ^ (lane & 7)) * 16)) = o;
+            *reinterpret_cast<uint4 *>(box + lane * 128 + ((u ^ (lane & 7)) * 16)) = o;
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
             if (DH && a.first)
-                tma_store(&a.dh, col + c, row, staging);
+                tma_store(&a.dh, col + c, row, box);
             else if (DH)
-                tma_add(&a.dh, col + c, row, staging);
+                tma_add(&a.dh, col + c, row, box);
             else
-                tma_store(&a.dw, col + c, a.v0 + row, staging);
+                tma_store(&a.dw, col + c, a.v0 + row, box);
             store_commit();
         }
     }
@@ -564,6 +568,18 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
     const int v_each = (v_blocks + a.splits - 1) / a.splits;
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
+    // The i-th tile of this pair: dh's in turn, then dw's.  A pair whose turn at dh does not come as
+    // often as the others' gets as many more of dw's first (dh's tiles take v_each blocks of K, dw's r_blocks).
+    const int rest = h_tiles % pairs, w_tiles = tiles - h_tiles;
+    const int more = rest == 0 || r_blocks == 0 ? 0 : min((v_each + r_blocks / 2) / r_blocks, w_tiles / (pairs - rest));
+    const int h_mine = h_tiles / pairs + (pair < rest), w_more = pair < rest ? 0 : more;
+    auto tile_of = [&](int i) {
+        if (i < h_mine)
+            return i * pairs + pair;
+        i -= h_mine;
+        const int w = i < w_more ? i * (pairs - rest) + pair - rest : more * (pairs - rest) + (i - w_more) * pairs + pair;
+        return w < w_tiles ? h_tiles + w : -1;
+    };
     auto job = [&](int t) {
         if (t < h_tiles) {
             const int split = t / h_each, k = split * v_each;
@@ -576,7 +592,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
     };
     if (warp == 0 && lane == 0) {
         RingPos pos;
-        for (int t = pair; t < tiles; t += pairs)
+        for (int i = 0, t; (t = tile_of(i)) >= 0; ++i)
             if (!copy_tile(job(t), b, ring, pos, rank)) {
                 drain_copies(b, pos, rank);
                 break;
@@ -584,7 +600,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
     } else if (warp == 1 && lane == 0 && rank == 0) {
         RingPos pos;
         AccPos acc;
-        for (int t = pair; t < tiles; t += pairs) {
+        for (int i = 0, t; (t = tile_of(i)) >= 0; ++i) {
             const TileJob j = job(t);
             if (!multiply_tile(j, b, ring, pos, acc, instruction_desc(DT == RED_BF16, j.a_along_k, j.b_along_k),
                                1 << 30)) {
@@ -598,7 +614,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
         uint32_t empty[2] = {leader_addr(&b.acc_empty[0]), leader_addr(&b.acc_empty[1])};
         unsigned char *const staging = ring + STAGES * STAGE_BYTES + (warp - 4) * STAGING_BYTES;
         const float unit = a.work.head->unit;
-        for (int t = pair; t < tiles; t += pairs) {
+        for (int i = 0, t; (t = tile_of(i)) >= 0; ++i) {
             const TileJob j = job(t);
             const bool ok = j.blocks == 0 || mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
             tmem_after();
