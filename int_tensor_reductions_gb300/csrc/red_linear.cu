@@ -57,7 +57,7 @@ struct ScanArgs {
     LinearWork w;
 };
 
-template <class V, class F>
+template <int NT, class V, class F>
 __device__ __forceinline__ V block_fold(V v, V *sh, F f)
 {
     for (int o = 16; o; o >>= 1)
@@ -66,8 +66,8 @@ __device__ __forceinline__ V block_fold(V v, V *sh, F f)
     if (threadIdx.x % 32 == 0)
         sh[threadIdx.x / 32] = v;
     __syncthreads();
-    v = sh[threadIdx.x % 32];
-    for (int o = 16; o; o >>= 1)
+    v = sh[threadIdx.x % (NT / 32)];
+    for (int o = NT / 64; o; o >>= 1)
         v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
@@ -81,12 +81,11 @@ __device__ __forceinline__ V block_fold(V v, V *sh, F f)
 constexpr float MOST = 1.9921875f;
 
 // One CTA: which rows take part and, for the gradients, their coefficients.
-template <bool GRAD>
-__global__ void __launch_bounds__(SCAN_NT) linear_scan_kernel(const ScanArgs a)
+// By the whole CTA of NT threads; the number of rows that take part.  f(place, row)
+// for each; `writes`: to the workspace.
+template <bool GRAD, int NT, int EACH, class F>
+__device__ __forceinline__ int scan_rows(const ScanArgs &a, int *sums, float *tops, bool writes, F f)
 {
-    pdl_enter();
-    __shared__ int sums[32];
-    __shared__ float tops[32];
     const int tid = threadIdx.x;
     auto coefs = [&](int64_t r, float &by_target, float &by_p) {
         const float d = a.dlogp[r], n = a.dlse ? a.dlse[r] : 0.0f;
@@ -105,23 +104,23 @@ __global__ void __launch_bounds__(SCAN_NT) linear_scan_kernel(const ScanArgs a)
     float unit = 1.0f;
     if constexpr (GRAD) {
         float top = 0.0f;
-        for (int64_t r = tid; r < a.rows; r += SCAN_NT) {
+        for (int64_t r = tid; r < a.rows; r += NT) {
             float x = 0.0f, y = 0.0f;
             if (live(r, x, y))
                 top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
         }
-        top = block_fold(top, tops, [](float x, float y) { return fmaxf(x, y); });
+        top = block_fold<NT>(top, tops, [](float x, float y) { return fmaxf(x, y); });
         if (top > 0.0f && top < __builtin_huge_valf())
             unit = fminf(fmaxf(top, 1e-36f), 1e36f) / MOST;
     }
     const float inv = 1.0f / unit;
     int before = 0;
-    for (int64_t r0 = 0; r0 < a.rows; r0 += SCAN_NT * SCAN_ROWS) {
-        const int64_t first = r0 + (int64_t)tid * SCAN_ROWS;
-        float ct[SCAN_ROWS], cp[SCAN_ROWS];
+    for (int64_t r0 = 0; r0 < a.rows; r0 += NT * EACH) {
+        const int64_t first = r0 + (int64_t)tid * EACH;
+        float ct[EACH], cp[EACH];
         unsigned mask = 0;
 #pragma unroll
-        for (int i = 0; i < SCAN_ROWS; ++i) {
+        for (int i = 0; i < EACH; ++i) {
             ct[i] = cp[i] = 0.0f;
             if (live(first + i, ct[i], cp[i]))
                 mask |= 1u << i;
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(SCAN_NT) linear_scan_kernel(const ScanArgs a)
         if (tid % 32 == 31)
             sums[tid / 32] = upto;
         __syncthreads();
-        const int sum = sums[tid % 32];
+        const int sum = tid % 32 < NT / 32 ? sums[tid % 32] : 0;
         int scan = sum;
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, scan, o);
@@ -148,30 +147,66 @@ __global__ void __launch_bounds__(SCAN_NT) linear_scan_kernel(const ScanArgs a)
         const int all = __shfl_sync(0xffffffffu, scan, 31);
         int at = before + warps_before + upto - mine;
 #pragma unroll
-        for (int i = 0; i < SCAN_ROWS; ++i) {
+        for (int i = 0; i < EACH; ++i) {
             const int64_t r = first + i;
             if (r >= a.rows)
                 break;
-            if (!(mask >> i & 1)) {
-                a.w.pos[r] = -1;
+            const bool takes = mask >> i & 1;
+            if (writes)
+                a.w.pos[r] = takes ? at : -1;
+            if (!takes)
                 continue;
-            }
-            a.w.pos[r] = at;
-            a.w.idx[at] = (int)r;
-            a.w.target[at] = (int)a.target[r];
-            if constexpr (GRAD) {
-                a.w.by_target[at] = ct[i] * inv;
-                a.w.by_p[at] = cp[i] * inv;
-                a.w.lse2[at] = a.lse[r] * LOG2E;
+            f(at, (int)r);
+            if (writes) {
+                a.w.idx[at] = (int)r;
+                a.w.target[at] = (int)a.target[r];
+                if constexpr (GRAD) {
+                    a.w.by_target[at] = ct[i] * inv;
+                    a.w.by_p[at] = cp[i] * inv;
+                    a.w.lse2[at] = a.lse[r] * LOG2E;
+                }
             }
             ++at;
         }
         before += all;
     }
-    if (tid == 0) {
+    if (writes && tid == 0) {
         a.w.head->live = before;
         a.w.head->unit = unit;
     }
+    return before;
+}
+
+template <bool GRAD>
+__global__ void __launch_bounds__(SCAN_NT) linear_scan_kernel(const ScanArgs a)
+{
+    pdl_enter();
+    __shared__ int sums[32];
+    __shared__ float tops[32];
+    scan_rows<GRAD, SCAN_NT, SCAN_ROWS>(a, sums, tops, true, [](int, int) {});
+}
+
+// Row `row` of the hidden states (-1: zeros) to packed row r, by a warp.
+__device__ __forceinline__ void pack_row(const void *hidden, int64_t dim, int64_t ldh, const LinearWork &w, int64_t r,
+                                         int row, int lane)
+{
+    const int64_t vecs = dim / 8;
+    const int tail = (int)(dim % 8);
+    uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(w.hidden) + r * w.ld);
+    const uint16_t *from = row >= 0 ? static_cast<const uint16_t *>(hidden) + row * ldh : nullptr;
+    const uint4 *v = reinterpret_cast<const uint4 *>(from);
+    int64_t i = lane;
+    for (; i + 96 < vecs && from; i += 128) {
+        const uint4 v0 = v[i], v1 = v[i + 32], v2 = v[i + 64], v3 = v[i + 96];
+        to[i] = v0;
+        to[i + 32] = v1;
+        to[i + 64] = v2;
+        to[i + 96] = v3;
+    }
+    for (; i < vecs; i += 32)
+        to[i] = from ? v[i] : make_uint4(0, 0, 0, 0);
+    if (lane < tail)
+        reinterpret_cast<uint16_t *>(to)[vecs * 8 + lane] = from ? from[vecs * 8 + lane] : (uint16_t)0;
 }
 
 // The hidden states of the rows that take part, packed; a warp per row.  Zeros
@@ -181,26 +216,32 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const void *hidden, in
     pdl_enter();
     const int live = w.head->live;
     const int64_t end = ((int64_t)live + TILE - 1) / TILE * TILE;
-    const int lane = threadIdx.x % 32;
-    const int64_t vecs = dim / 8;
-    const int tail = (int)(dim % 8);
-    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < end; r += (int64_t)gridDim.x * 8) {
-        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(w.hidden) + r * w.ld);
-        const uint16_t *from = r < live ? static_cast<const uint16_t *>(hidden) + (int64_t)w.idx[r] * ldh : nullptr;
-        const uint4 *v = reinterpret_cast<const uint4 *>(from);
-        int64_t i = lane;
-        for (; i + 96 < vecs && from; i += 128) {
-            const uint4 v0 = v[i], v1 = v[i + 32], v2 = v[i + 64], v3 = v[i + 96];
-            to[i] = v0;
-            to[i + 32] = v1;
-            to[i + 64] = v2;
-            to[i + 96] = v3;
-        }
-        for (; i < vecs; i += 32)
-            to[i] = from ? v[i] : make_uint4(0, 0, 0, 0);
-        if (lane < tail)
-            reinterpret_cast<uint16_t *>(to)[vecs * 8 + lane] = from ? from[vecs * 8 + lane] : (uint16_t)0;
-    }
+    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < end; r += (int64_t)gridDim.x * 8)
+        pack_row(hidden, dim, ldh, w, r, r < live ? w.idx[r] : -1, threadIdx.x % 32);
+}
+
+// Both for few rows, in one launch: every CTA does the scan for itself, and packs
+// eight rows.
+constexpr int GATHER_ROWS = 1024;
+template <bool GRAD>
+__global__ void __launch_bounds__(256) linear_gather_kernel(const ScanArgs a, const void *hidden, int64_t dim, int64_t ldh)
+{
+    pdl_enter();
+    __shared__ int sums[32];
+    __shared__ float tops[32];
+    __shared__ int row_of[8];
+    const bool writes = blockIdx.x == 0;
+    const int first_packed = blockIdx.x * 8;
+    if (threadIdx.x < 8)
+        row_of[threadIdx.x] = -1;
+    const int live = scan_rows<GRAD, 256, GATHER_ROWS / 256>(a, sums, tops, writes, [&](int at, int r) {
+        if (at >= first_packed && at < first_packed + 8)
+            row_of[at - first_packed] = r;
+    });
+    __syncthreads();
+    const int64_t r = first_packed + threadIdx.x / 32;
+    if (r < (live + TILE - 1) / TILE * TILE)
+        pack_row(hidden, dim, ldh, a.w, r, row_of[threadIdx.x / 32], threadIdx.x % 32);
 }
 
 // --------------------------------------------------------------- logit tiles
@@ -285,14 +326,14 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
     if (warp < 4)
         fewer_registers();
     if (warp == 0 && lane == 0) {
-        RingPos pos;
+        RingPos<> pos;
         for (int t = pair; t < tiles; t += pairs)
             if (!copy_tile(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, rank)) {
                 drain_copies(b, pos, rank);
                 break;
             }
     } else if (warp == 1 && lane == 0 && rank == 0) {
-        RingPos pos;
+        RingPos<> pos;
         AccPos acc;
         const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true);
         for (int t = pair; t < tiles; t += pairs)
@@ -417,7 +458,8 @@ struct Pair {
 };
 
 template <int LANES>
-__global__ void __launch_bounds__(256) linear_join_kernel(const LinearWork w, int64_t rows, float s2, float *logp, float *lse)
+__global__ void __launch_bounds__(256) 
+    linear_join_kernel(const LinearWork w, int64_t rows, int64_t slots, float s2, float *logp, float *lse)
 {
     pdl_enter();
     __shared__ float2 warps[8];
@@ -433,7 +475,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearWork w, in
         const float2 *part = w.part + (int64_t)at * w.slots;
         Pair p = {NEG_INF, 0.0f};
 #pragma unroll 4
-        for (int64_t i = lane; i < w.slots; i += LANES) {
+        for (int64_t i = lane; i < slots; i += LANES) {
             const float2 o = part[i];
             p.join(o.x, o.y);
         }
@@ -457,18 +499,301 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearWork w, in
     }
 }
 
+// ------------------------------------------------------------ few rows
+
+// Up to 128 rows: the weights' way through memory is what bounds a call, and tiles
+// of 256 rows x 256 columns would load as much of (packed, mostly empty) rows as of
+// weights, 76 at a time.  Here the weights are the operand with 128 rows, the hidden
+// states the one with ROWS = 16, 32, 64 or 128, and each CTA takes its share of the
+// vocabulary, equal to within 16 columns, so that all SMs stream weights to the end.
+// us, 256 x 256 tiles against this: FEWNOW
+constexpr int FEW_ROWS = 128, FEW_THREADS = 256, FEW_STEP = 16, FEW_MAX_CTAS = 512;
+
+template <int ROWS>
+struct Few {
+    static constexpr int STAGE = OPERAND_BYTES + ROWS * BLOCK_K * 2;
+    static constexpr int N = 212992 / STAGE < 12 ? 212992 / STAGE : 12;  // stages
+    static constexpr size_t SMEM = (size_t)N * STAGE + 1024;
+    static constexpr int COLUMNS = 2 * ROWS;  // of tensor memory
+    struct Shared {
+        uint64_t full[N], empty[N], acc_full[2], acc_empty[2], drain;
+        uint32_t tmem;
+        int failed;
+        float2 stats[4][ROWS];
+        int target[ROWS];
+        float4 coefs[ROWS];  // by p, by the target, lse, target (as bits)
+    };
+};
+
+struct FewArgs {
+    CUtensorMap h, w, w_end;  // boxes of 64 x ROWS, 64 x 128, 64 x 16
+    LinearWork work;
+    int vocab, k_blocks;
+    float s2;
+};
+
+__device__ __forceinline__ float max_of_warp(float v)
+{
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Sums over the warp of 32 (or the first 16) values per lane: lane i gets the i-th.
+template <int N>
+__device__ __forceinline__ float sums_of_warp(float *v, int lane)
+{
+    static_assert(N == 16 || N == 32, "");
+    if constexpr (N == 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+    }
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return v[0];
+}
+
+template <int DT, bool GRAD, int ROWS>
+__global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid_constant__ FewArgs a)
+{
+    using F = Few<ROWS>;
+    extern __shared__ unsigned char raw[];
+    __shared__ typename F::Shared b;
+    unsigned char *const ring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < F::N; ++i) {
+            mbar_init(&b.full[i], 1);
+            mbar_init(&b.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.acc_full[i], 1);
+            mbar_init(&b.acc_empty[i], 4);
+        }
+        mbar_init(&b.drain, 1);
+        b.failed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2)
+        tmem_alloc_alone<F::COLUMNS>(&b.tmem);
+    pdl_enter();
+    const int live = a.work.head->live;
+    for (int r = threadIdx.x; r < ROWS; r += FEW_THREADS) {
+        const bool takes = r < live;
+        b.target[r] = takes ? a.work.target[r] : -1;
+        if (GRAD)
+            b.coefs[r] = takes ? make_float4(a.work.by_p[r], a.work.by_target[r], a.work.lse2[r], 0.0f)
+                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    tmem_before();
+    __syncthreads();
+    tmem_after();
+    // this CTA's columns of the vocabulary
+    const int units = (a.vocab + FEW_STEP - 1) / FEW_STEP;
+    const int begin = (int)((int64_t)units * blockIdx.x / gridDim.x) * FEW_STEP;
+    const int end = min((int)((int64_t)units * (blockIdx.x + 1) / gridDim.x) * FEW_STEP, a.vocab);
+
+    if (live == 0) {
+        // nothing takes part: no products (gradients of few rows still want their zeros)
+        if (GRAD && warp >= 4)
+            for (int v = begin + threadIdx.x - 128; v < end; v += 128)
+                for (int i = 0; i < ROWS / 8; ++i)
+                    reinterpret_cast<uint4 *>(a.work.piece)[(int64_t)v * (ROWS / 8) + i] = make_uint4(0, 0, 0, 0);
+    } else if (warp == 0 && lane == 0) {
+        RingPos<F::N> pos;
+        bool ok = true;
+        for (int v = begin; v < end && ok; v += HALF)
+            for (int k = 0; k < a.k_blocks; ++k) {
+                if (!mbar_wait(&b.empty[pos.stage], pos.phase ^ 1, &b.failed, 0)) {
+                    ok = false;
+                    break;
+                }
+                const int boxes = (min(end - v, HALF) + FEW_STEP - 1) / FEW_STEP;
+                uint64_t *const bar = &b.full[pos.stage];
+                mbar_expect(bar, (uint32_t)((boxes * FEW_STEP + ROWS) * BLOCK_K * 2));
+                unsigned char *const at = ring + pos.stage * F::STAGE;
+                if (boxes * FEW_STEP == HALF) {
+                    tma_load_alone(at, &a.w, k * BLOCK_K, v, bar);
+                } else {
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_alone(at + i * FEW_STEP * BLOCK_K * 2, &a.w_end, k * BLOCK_K, v + i * FEW_STEP, bar);
+                }
+                tma_load_alone(at + OPERAND_BYTES, &a.h, k * BLOCK_K, 0, bar);
+                pos.next();
+            }
+        if (!ok)
+            for (int k = 0; k < F::N; ++k)
+                for (int n = 0; n < 65536 && !mbar_try(&b.full[k], k < pos.stage ? pos.phase : pos.phase ^ 1); ++n) {
+                }
+    } else if (warp == 1 && lane == 0) {
+        RingPos<F::N> pos;
+        AccPos acc;
+        bool ok = true;
+        const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true, HALF, ROWS);
+        for (int v = begin; v < end && ok; v += HALF)
+            for (int k0 = 0; k0 < a.k_blocks && ok; k0 += CHUNK) {
+                if (!mbar_wait(&b.acc_empty[acc.slot], acc.phase ^ 1, &b.failed, 0)) {
+                    ok = false;
+                    break;
+                }
+                tmem_after();
+                const uint32_t d = b.tmem + acc.slot * ROWS;
+                for (int k = k0; k < min(k0 + CHUNK, a.k_blocks); ++k) {
+                    if (!mbar_wait(&b.full[pos.stage], pos.phase, &b.failed, 0)) {
+                        ok = false;
+                        break;
+                    }
+                    tmem_after();
+                    const unsigned char *at = ring + pos.stage * F::STAGE;
+                    const uint64_t da = operand_desc(at, true), db = operand_desc(at + OPERAND_BYTES, true);
+#pragma unroll
+                    for (int s = 0; s < BLOCK_K / 16; ++s)
+                        mma_alone(d, da + s * step_k(true), db + s * step_k(true), idesc, k > k0 || s > 0);
+                    mma_commit_alone(&b.empty[pos.stage]);
+                    pos.next();
+                }
+                if (ok)
+                    mma_commit_alone(&b.acc_full[acc.slot]);
+                acc.next();
+            }
+        if (!ok) {
+            mma_commit_alone(&b.drain);
+            for (int n = 0; n < 65536 && !mbar_try(&b.drain, 0); ++n) {
+            }
+        }
+    } else if (warp >= 4) {
+        constexpr int GROUP = ROWS < 32 ? ROWS : 32, GROUPS = ROWS / GROUP;
+        const int part = warp - 4;
+        AccPos acc;
+        float m[GROUPS], l[GROUPS];  // lane i: of rows g * 32 + i
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g)
+            m[g] = NEG_INF, l[g] = 0.0f;
+        for (int v0 = begin; v0 < end; v0 += HALF) {
+            const int first = v0 + part * 32, v = first + lane;
+            const bool valid = v < end;
+            float z[ROWS];
+            bool ok = true;
+            for (int k = 0; k < a.k_blocks; k += CHUNK) {
+                ok &= mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
+                tmem_after();
+                const uint32_t from = b.tmem + ((uint32_t)(part * 32) << 16) + acc.slot * ROWS;
+                if (k == 0) {
+#pragma unroll
+                    for (int i = 0; i < ROWS; i += 16)
+                        tmem_load16(from + i, reinterpret_cast<uint32_t *>(z + i));
+                    tmem_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < ROWS; i += 16) {
+                        uint32_t x[16];
+                        tmem_load16(from + i, x);
+                        tmem_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            z[i + j] += __uint_as_float(x[j]);
+                    }
+                }
+                tmem_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&b.acc_empty[acc.slot]);
+                acc.next();
+            }
+            const float fine = ok ? 0.0f : __builtin_nanf("");
+            if constexpr (!GRAD) {
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) {
+                    // a target among this warp's columns
+                    const int t = lane < GROUP ? b.target[g * 32 + lane] - first : -1;
+                    unsigned here = __ballot_sync(0xffffffffu, t >= 0 && t < 32 && first + t < end);
+                    while (here) {
+                        const int i = __ffs(here) - 1;
+                        here &= here - 1;
+                        float x = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < GROUP; ++j)
+                            x = j == i ? z[g * 32 + j] : x;
+                        x = __shfl_sync(0xffffffffu, x, __shfl_sync(0xffffffffu, t, i));
+                        if (lane == 0)
+                            a.work.taken[g * 32 + i] = x + fine;
+                    }
+                    float e[GROUP];
+                    float top = NEG_INF;  // of row `lane`
+#pragma unroll
+                    for (int j = 0; j < GROUP; ++j) {
+                        const float x = valid ? z[g * 32 + j] : NEG_INF;
+                        const float most = max_of_warp(x);
+                        e[j] = ex2(fmaf(x, a.s2, most == NEG_INF ? 0.0f : -(most * a.s2)));
+                        top = j == lane ? most : top;
+                    }
+                    const float sum = sums_of_warp<GROUP>(e, lane) + fine;
+                    Pair p = {m[g], l[g]};
+                    p.join(top * a.s2, sum);
+                    m[g] = p.m, l[g] = p.l;
+                }
+            } else {
+                uint4 *to = reinterpret_cast<uint4 *>(a.work.piece) + (int64_t)v * (ROWS / 8);
+#pragma unroll
+                for (int i = 0; i < ROWS; i += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 c = b.coefs[i + j];
+                        x[j] = fmaf(c.x, ex2(fmaf(z[i + j], a.s2, -c.z)), fine);
+                        if (v == b.target[i + j])
+                            x[j] += c.y;
+                    }
+                    if (valid)
+                        to[i / 8] = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
+                                               pack2<DT>(x[6], x[7]));
+                }
+            }
+        }
+        if constexpr (!GRAD) {
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g)
+                if (lane < GROUP)
+                    b.stats[part][g * 32 + lane] = make_float2(m[g], l[g]);
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const int r = threadIdx.x - 128;
+            if (r < live) {
+                Pair p = {NEG_INF, 0.0f};
+                for (int w = 0; w < 4; ++w)
+                    p.join(b.stats[w][r].x, b.stats[w][r].y);
+                a.work.part[(int64_t)r * a.work.slots + blockIdx.x] = make_float2(p.m, p.l);
+            }
+        }
+    }
+    __syncwarp();
+    tmem_before();
+    __syncthreads();
+    tmem_after();
+    if (warp == 2)
+        tmem_free_alone<F::COLUMNS>(b.tmem);
+}
+
 // ------------------------------------------------------- products with weights
 
 struct ProductArgs {
-    CUtensorMap g_k;    // piece, along the vocabulary: boxes of 64 x 128        (dh: A)
+    CUtensorMap g_h;    // piece (dh: A): boxes of 64 of the vocabulary x 128 rows, of few rows 64 rows x 64
     CUtensorMap w_n;    // weights, along dim: boxes of 64 x 64                  (dh: B)
-    CUtensorMap g_m;    // piece: boxes of 64 (vocabulary) x 64 (rows)           (dw: A)
+    CUtensorMap g_w;    // piece (dw: A): boxes of 64 of the vocabulary x 64 rows, of few rows 64 rows x 128
     CUtensorMap h_n;    // packed hidden states, along dim: boxes of 64 x 64     (dw: B)
     CUtensorMap dh, dw; // results: boxes of 32 x 32 fp32, 64 x 32 16-bit
     LinearWork work;
     int v0, v_count;    // the piece: first column of the vocabulary, columns
     int n_tiles;        // along dim
     int splits;         // of dh, along the vocabulary
+    bool few;           // the piece lies along the rows
     int first;          // dh: store (1) or add (0)
     uint16_t *dweight;  // dw's memory, for the end of rows that do not end on 16 bytes
     int64_t lddw;
@@ -569,9 +894,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
     // The i-th tile of this pair: dh's in turn, then dw's.  A pair whose turn at dh does not come as
-    // often as the others' gets as many more of dw's first (dh's tiles take v_each blocks of K, dw's r_blocks).
+    // often as the others' gets as many more of dw's first.  What a tile takes, in eighths of the time of
+    // one block of K in the tensor cores: dh's its blocks, or 22 each where few rows of tiles share what a
+    // block loads of the weights, dw's its blocks, or the 11 that its way to memory takes.
     const int rest = h_tiles % pairs, w_tiles = tiles - h_tiles;
-    const int more = rest == 0 || r_blocks == 0 ? 0 : min((v_each + r_blocks / 2) / r_blocks, w_tiles / (pairs - rest));
+    const int h_cost = v_each * max(8, 22 / max(h_rows, 1)), w_cost = 8 * max(r_blocks, 11);
+    const int more = rest == 0 ? 0 : min((h_cost + w_cost / 2) / w_cost, w_tiles / (pairs - rest));
     const int h_mine = h_tiles / pairs + (pair < rest), w_more = pair < rest ? 0 : more;
     auto tile_of = [&](int i) {
         if (i < h_mine)
@@ -584,21 +912,21 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
         if (t < h_tiles) {
             const int split = t / h_each, k = split * v_each;
             const TileAt at = tile_at(t - split * h_each, h_rows, a.n_tiles);
-            return TileJob{&a.g_k, &a.w_n, at.m * TILE, at.n * TILE, k * BLOCK_K, a.v0 + k * BLOCK_K,
-                           max(0, min(v_each, v_blocks - k)), true, false};
+            return TileJob{&a.g_h, &a.w_n, at.m * TILE, at.n * TILE, k * BLOCK_K, a.v0 + k * BLOCK_K,
+                           max(0, min(v_each, v_blocks - k)), !a.few, false};
         }
         const TileAt at = tile_at(t - h_tiles, w_rows, a.n_tiles);
-        return TileJob{&a.g_m, &a.h_n, at.m * TILE, at.n * TILE, 0, 0, r_blocks, false, false};
+        return TileJob{&a.g_w, &a.h_n, at.m * TILE, at.n * TILE, 0, 0, r_blocks, a.few, false};
     };
     if (warp == 0 && lane == 0) {
-        RingPos pos;
+        RingPos<> pos;
         for (int i = 0, t; (t = tile_of(i)) >= 0; ++i)
             if (!copy_tile(job(t), b, ring, pos, rank)) {
                 drain_copies(b, pos, rank);
                 break;
             }
     } else if (warp == 1 && lane == 0 && rank == 0) {
-        RingPos pos;
+        RingPos<> pos;
         AccPos acc;
         for (int i = 0, t; (t = tile_of(i)) >= 0; ++i) {
             const TileJob j = job(t);
@@ -671,6 +999,8 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ launches
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -780,6 +1110,43 @@ int launch_products(int64_t tiles, cudaStream_t s, const ProductArgs &a)
     return launch_pairs(linear_products_kernel<DT>, cache, tiles, s, a, "linear_products");
 }
 
+template <int DT, bool GRAD, int ROWS>
+int launch_few_rows(FewArgs &a, unsigned *grid, cudaStream_t s)
+{
+    static std::atomic<bool> ready[MAX_DEVICES];
+    DeviceInfo di;
+    RETURN_IF(device_info(&di));
+    auto *const kernel = linear_few_kernel<DT, GRAD, ROWS>;
+    if (!ready[di.dev].load(std::memory_order_relaxed)) {
+        RETURN_IF(cuda_fail(
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Few<ROWS>::SMEM),
+            "cudaFuncSetAttribute"));
+        ready[di.dev].store(true, std::memory_order_relaxed);
+    }
+    const int units = (a.vocab + FEW_STEP - 1) / FEW_STEP, most = di.sms < FEW_MAX_CTAS ? di.sms : FEW_MAX_CTAS;
+    *grid = (unsigned)(units < most ? units : most);
+    RETURN_IF(cuda_fail(launch_pdl_smem(kernel, *grid, FEW_THREADS, Few<ROWS>::SMEM, 1, s, a), "linear_few"));
+    count_launches(1);
+    return RED_OK;
+}
+// `grid`: the CTAs that it took, one slot of the statistics each.
+template <bool GRAD>
+int launch_few(const LinearArgs &a, const LinearWork &w, unsigned *grid, cudaStream_t s)
+{
+    FewArgs f;
+    RETURN_IF(matrix_map(&f.h, a.dtype, w.hidden, a.dim, w.padded, w.ld, BLOCK_K, w.few));
+    RETURN_IF(matrix_map(&f.w, a.dtype, a.weight, a.dim, a.vocab, a.ldw, BLOCK_K, HALF));
+    RETURN_IF(matrix_map(&f.w_end, a.dtype, a.weight, a.dim, a.vocab, a.ldw, BLOCK_K, FEW_STEP));
+    f.work = w;
+    f.vocab = (int)a.vocab;
+    f.k_blocks = (int)(up(a.dim, BLOCK_K) / BLOCK_K);
+    f.s2 = (float)(a.scale * 1.4426950408889634);
+#define FEW_OF(rows) \
+    (a.dtype == RED_BF16 ? launch_few_rows<RED_BF16, GRAD, rows>(f, grid, s) : launch_few_rows<RED_F16, GRAD, rows>(f, grid, s))
+    return w.few == 16 ? FEW_OF(16) : w.few == 32 ? FEW_OF(32) : w.few == 64 ? FEW_OF(64) : FEW_OF(128);
+#undef FEW_OF
+}
+
 unsigned warp_rows_grid(int64_t rows) { return (unsigned)((rows + 7) / 8 < 65536 ? (rows + 7) / 8 : 65536); }
 
 template <bool GRAD>
@@ -787,6 +1154,12 @@ int pack_rows(const LinearArgs &a, const LinearWork &w, const float *lse, const 
               cudaStream_t s)
 {
     const ScanArgs scan = {a.target, a.rows, a.vocab, lse, dlogp, dlse, a.scale, w};
+    if (a.rows <= GATHER_ROWS) {
+        count_launches(1);
+        return cuda_fail(launch_pdl(linear_gather_kernel<GRAD>, dim3((unsigned)(w.padded / 8)), dim3(256), s, scan, a.hidden,
+                                    a.dim, a.ldh),
+                         "linear_gather");
+    }
     RETURN_IF(cuda_fail(launch_pdl(linear_scan_kernel<GRAD>, dim3(1), dim3(SCAN_NT), s, scan), "linear_scan"));
     RETURN_IF(cuda_fail(launch_pdl(linear_pack_kernel, dim3(warp_rows_grid(w.padded)), dim3(256), s, a.hidden, a.dim,
                                    a.ldh, w),
@@ -794,8 +1167,6 @@ int pack_rows(const LinearArgs &a, const LinearWork &w, const float *lse, const 
     count_launches(2);
     return RED_OK;
 }
-
-int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 }  // namespace
 
@@ -811,7 +1182,8 @@ LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, boo
     w.padded = up(rows, TILE);
     w.ld = up(dim, 8);
     w.dim4 = up(dim, 4);
-    w.slots = up(vocab, TILE) / HALF;
+    w.few = rows > FEW_ROWS ? 0 : rows > 64 ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
+    w.slots = w.few ? FEW_MAX_CTAS : up(vocab, TILE) / HALF;
     take(w.head, sizeof(LinearHead));
     take(w.pos, rows * 4);
     take(w.idx, rows * 4);
@@ -827,11 +1199,11 @@ LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, boo
         // pass over the sums of dh too often
         int64_t cols = ((int64_t)1 << 27) / w.padded / TILE * TILE;
         cols = cols < 4096 ? 4096 : cols;
-        w.piece_cols = cols < up(vocab, TILE) ? cols : up(vocab, TILE);
+        w.piece_cols = cols < up(vocab, TILE) && !w.few ? cols : up(vocab, TILE);
         take(w.by_target, rows * 4);
         take(w.by_p, rows * 4);
         take(w.lse2, rows * 4);
-        take(g, w.padded * w.piece_cols * 2);
+        take(g, (w.few ? w.few : w.padded) * w.piece_cols * 2);
         w.piece = g;
         // dh of few rows is few tiles that are long: shares of the vocabulary fill the pairs of CTAs
         // (64 x 1024 x 32001: four tiles of 501 blocks of K, products 191 us; 18 shares SPLITNOW)
@@ -849,22 +1221,31 @@ int launch_linear_logprob(const LinearArgs &a, float *logp, float *lse, void *wo
 {
     const LinearWork w = linear_work(work, a.rows, a.dim, a.vocab, false);
     RETURN_IF(pack_rows<false>(a, w, nullptr, nullptr, nullptr, s));
-    LogitArgs l;
-    RETURN_IF(matrix_map(&l.h, a.dtype, w.hidden, a.dim, w.padded, w.ld, BLOCK_K, HALF));
-    RETURN_IF(matrix_map(&l.w, a.dtype, a.weight, a.dim, a.vocab, a.ldw, BLOCK_K, HALF));
-    l.g = l.w;
-    l.work = w;
-    l.v0 = 0;
-    l.n_tiles = (int)(up(a.vocab, TILE) / TILE);
-    l.vocab = (int)a.vocab;
-    l.k_blocks = (int)(up(a.dim, BLOCK_K) / BLOCK_K);
-    l.s2 = (float)(a.scale * 1.4426950408889634);
-    const int64_t tiles = w.padded / TILE * l.n_tiles;
-    RETURN_IF((a.dtype == RED_BF16 ? launch_logits<RED_BF16, false>(tiles, s, l) : launch_logits<RED_F16, false>(tiles, s, l)));
-    const bool few = a.rows <= 2048;
-    RETURN_IF(cuda_fail(launch_pdl(few ? linear_join_kernel<256> : linear_join_kernel<32>,
-                                   dim3(few ? (unsigned)a.rows : warp_rows_grid(a.rows)), dim3(256), s, w, a.rows, l.s2, logp,
-                                   lse),
+    const float s2 = (float)(a.scale * 1.4426950408889634);
+    int64_t slots = w.slots;
+    if (w.few) {
+        unsigned grid;
+        RETURN_IF(launch_few<false>(a, w, &grid, s));
+        slots = grid;
+    } else {
+        LogitArgs l;
+        RETURN_IF(matrix_map(&l.h, a.dtype, w.hidden, a.dim, w.padded, w.ld, BLOCK_K, HALF));
+        RETURN_IF(matrix_map(&l.w, a.dtype, a.weight, a.dim, a.vocab, a.ldw, BLOCK_K, HALF));
+        l.g = l.w;
+        l.work = w;
+        l.v0 = 0;
+        l.n_tiles = (int)(up(a.vocab, TILE) / TILE);
+        l.vocab = (int)a.vocab;
+        l.k_blocks = (int)(up(a.dim, BLOCK_K) / BLOCK_K);
+        l.s2 = s2;
+        const int64_t tiles = w.padded / TILE * l.n_tiles;
+        RETURN_IF((a.dtype == RED_BF16 ? launch_logits<RED_BF16, false>(tiles, s, l)
+                                       : launch_logits<RED_F16, false>(tiles, s, l)));
+    }
+    const bool wide = a.rows <= 2048;
+    RETURN_IF(cuda_fail(launch_pdl(wide ? linear_join_kernel<256> : linear_join_kernel<32>,
+                                   dim3(wide ? (unsigned)a.rows : warp_rows_grid(a.rows)), dim3(256), s, w, a.rows, slots, s2,
+                                   logp, lse),
                         "linear_join"));
     count_launches(1);
     return RED_OK;
@@ -879,9 +1260,15 @@ int launch_linear_logprob_grad(const LinearArgs &a, const float *lse, const floa
     ProductArgs p;
     RETURN_IF(matrix_map(&l.h, a.dtype, w.hidden, a.dim, w.padded, w.ld, BLOCK_K, HALF));
     RETURN_IF(matrix_map(&l.w, a.dtype, a.weight, a.dim, a.vocab, a.ldw, BLOCK_K, HALF));
-    RETURN_IF(matrix_map(&l.g, a.dtype, w.piece, w.piece_cols, w.padded, w.piece_cols, 64, 32));
-    RETURN_IF(matrix_map(&p.g_k, a.dtype, w.piece, w.piece_cols, w.padded, w.piece_cols, BLOCK_K, HALF));
-    RETURN_IF(matrix_map(&p.g_m, a.dtype, w.piece, w.piece_cols, w.padded, w.piece_cols, 64, BLOCK_K));
+    if (w.few) {
+        RETURN_IF(matrix_map(&p.g_h, a.dtype, w.piece, w.few, a.vocab, w.few, 64, BLOCK_K));
+        RETURN_IF(matrix_map(&p.g_w, a.dtype, w.piece, w.few, a.vocab, w.few, BLOCK_K, HALF));
+    } else {
+        RETURN_IF(matrix_map(&l.g, a.dtype, w.piece, w.piece_cols, w.padded, w.piece_cols, 64, 32));
+        RETURN_IF(matrix_map(&p.g_h, a.dtype, w.piece, w.piece_cols, w.padded, w.piece_cols, BLOCK_K, HALF));
+        RETURN_IF(matrix_map(&p.g_w, a.dtype, w.piece, w.piece_cols, w.padded, w.piece_cols, 64, BLOCK_K));
+    }
+    p.few = w.few != 0;
     RETURN_IF(matrix_map(&p.w_n, a.dtype, a.weight, a.dim, a.vocab, a.ldw, 64, BLOCK_K));
     RETURN_IF(matrix_map(&p.h_n, a.dtype, w.hidden, a.dim, w.padded, w.ld, 64, BLOCK_K));
     RETURN_IF(matrix_map(&p.dh, RED_F32, w.dhidden, a.dim, w.padded * w.splits, w.dim4, 32, 32));
@@ -909,13 +1296,13 @@ int launch_linear_logprob_grad(const LinearArgs &a, const float *lse, const floa
         p.first = v0 == 0;
         const int64_t m_tiles = w.padded / TILE;
         const int64_t tiles = (p.with_dh ? m_tiles * w.splits : 0) * p.n_tiles + (int64_t)(p.with_dw ? l.n_tiles : 0) * p.n_tiles;
-        if (a.dtype == RED_BF16) {
-            RETURN_IF((launch_logits<RED_BF16, true>(m_tiles * l.n_tiles, s, l)));
-            RETURN_IF(launch_products<RED_BF16>(tiles, s, p));
-        } else {
-            RETURN_IF((launch_logits<RED_F16, true>(m_tiles * l.n_tiles, s, l)));
-            RETURN_IF(launch_products<RED_F16>(tiles, s, p));
-        }
+        unsigned grid;
+        if (w.few)
+            RETURN_IF(launch_few<true>(a, w, &grid, s));
+        else
+            RETURN_IF((a.dtype == RED_BF16 ? launch_logits<RED_BF16, true>(m_tiles * l.n_tiles, s, l)
+                                           : launch_logits<RED_F16, true>(m_tiles * l.n_tiles, s, l)));
+        RETURN_IF((a.dtype == RED_BF16 ? launch_products<RED_BF16>(tiles, s, p) : launch_products<RED_F16>(tiles, s, p)));
     }
     if (dhidden) {
         auto *const kernel = a.dtype == RED_BF16 ? linear_scatter_kernel<RED_BF16> : linear_scatter_kernel<RED_F16>;

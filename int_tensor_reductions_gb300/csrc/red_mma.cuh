@@ -117,6 +117,40 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar)
         : "memory");
 }
 
+// The same of one CTA alone: a tile of 128 rows.
+__device__ __forceinline__ void tma_load_alone(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+template <int COLUMNS>
+__device__ __forceinline__ void tmem_alloc_alone(uint32_t *where)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(where)), "n"(COLUMNS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+template <int COLUMNS>
+__device__ __forceinline__ void tmem_free_alone(uint32_t base)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(COLUMNS));
+}
+__device__ __forceinline__ void mma_alone(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_alone(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
 // 16 columns of this warp's 32 lanes of tensor memory: lane i gets row i.
 __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t *v)
 {
@@ -140,11 +174,12 @@ __device__ __forceinline__ uint64_t operand_desc(const void *p, bool along_k)
 // One step of 16 of K further, in the descriptor's units of 16 bytes.
 __host__ __device__ constexpr uint64_t step_k(bool along_k) { return along_k ? 2 : 128; }
 
-// f16 or bf16 operands, fp32 accumulators, a tile of 256 x 256.
-__device__ __forceinline__ uint32_t instruction_desc(bool bf16, bool a_along_k, bool b_along_k)
+// f16 or bf16 operands, fp32 accumulators, a tile of rows x cols.
+__device__ __forceinline__ uint32_t instruction_desc(bool bf16, bool a_along_k, bool b_along_k, int rows = TILE,
+                                                     int cols = TILE)
 {
     return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (a_along_k ? 0u : 1u << 15) | (b_along_k ? 0u : 1u << 16) |
-           (uint32_t)(TILE / 8) << 17 | (uint32_t)(TILE / 16) << 24;
+           (uint32_t)(cols / 8) << 17 | (uint32_t)(rows / 16) << 24;
 }
 
 // ------------------------------------------------------------- the pipeline
@@ -185,12 +220,13 @@ __device__ __forceinline__ void load_operand(unsigned char *dst, const CUtensorM
 }
 
 // Ring positions that copies and products go through in the same order.
+template <int N = STAGES>
 struct RingPos {
     int stage = 0;
     uint32_t phase = 0;
     __device__ __forceinline__ void next()
     {
-        if (++stage == STAGES) {
+        if (++stage == N) {
             stage = 0;
             phase ^= 1;
         }
@@ -198,7 +234,7 @@ struct RingPos {
 };
 
 // The copies of one tile (one thread of each CTA).  Whether to go on.
-__device__ __forceinline__ bool copy_tile(const TileJob &j, MmaBarriers &b, unsigned char *ring, RingPos &pos, int rank)
+__device__ __forceinline__ bool copy_tile(const TileJob &j, MmaBarriers &b, unsigned char *ring, RingPos<> &pos, int rank)
 {
     for (int k = 0; k < j.blocks; ++k) {
         if (!mbar_wait(&b.empty[pos.stage], pos.phase ^ 1, &b.failed, 0))
@@ -227,7 +263,7 @@ struct AccPos {
 
 // The products of one tile (one thread of the leader), handed over after every
 // `chunk` blocks of K, each time in the other accumulator.  Whether to go on.
-__device__ __forceinline__ bool multiply_tile(const TileJob &j, MmaBarriers &b, const unsigned char *ring, RingPos &pos,
+__device__ __forceinline__ bool multiply_tile(const TileJob &j, MmaBarriers &b, const unsigned char *ring, RingPos<> &pos,
                                               AccPos &acc, uint32_t idesc, int chunk)
 {
     const uint64_t ka = step_k(j.a_along_k), kb = step_k(j.b_along_k);
@@ -297,7 +333,7 @@ __device__ __forceinline__ void mma_end(MmaBarriers &b, int warp)
 
 // What is left after a wait ran out: the copies and products in flight are
 // waited for, within limits, before the CTA ends.
-__device__ __forceinline__ void drain_copies(MmaBarriers &b, const RingPos &pos, int rank)
+__device__ __forceinline__ void drain_copies(MmaBarriers &b, const RingPos<> &pos, int rank)
 {
     if (rank == 0)
         for (int k = 0; k < STAGES; ++k)

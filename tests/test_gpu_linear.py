@@ -43,7 +43,7 @@ def inputs(rows, dim, vocab, dtype, ignore=0.25, pad=0, seed=0):
     return hidden, weight, target, dlogp, dlse
 
 
-SHAPES = [(1, 8, 1), (1, 1, 5), (2, 64, 256), (3, 70, 257), (5, 100, 1000), (64, 512, 2049), (128, 72, 255),
+SHAPES = [(1, 8, 1), (1, 1, 5), (2, 64, 256), (3, 70, 257), (5, 100, 1000), (16, 1040, 777), (17, 200, 5000), (33, 136, 130), (64, 512, 2049), (100, 2056, 20000), (128, 72, 255),
           (129, 576, 513), (255, 64, 4097), (256, 1000, 300), (257, 1032, 1111), (300, 24, 9000), (1000, 520, 3001),
           (4100, 40, 700)]
 

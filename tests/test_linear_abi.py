@@ -62,7 +62,8 @@ def test_scratch_sizes(itr):
     size = itr.lib().red_linear_work_bytes
     assert size(-1, 8, 8, 0) == size(1, 0, 8, 1) == size(1, 8, 0, 0) == itr.RED_EINVAL
     assert size(0, 8, 8, 0) >= 0
-    assert size(4, 64, 1000, 1) >= 256 * 64 * 2 + 256 * 1024 * 2
+    assert size(4, 64, 1000, 1) >= 256 * 64 * 2 + 16 * 1000 * 2
+    assert size(400, 64, 1000, 1) >= 512 * 64 * 2 + 512 * 1000 * 2
     wide = size(8192, 4096, 131072, 1)
     assert wide == size(8192, 4096, 262144, 1) < 8192 * 131072 * 2
 
