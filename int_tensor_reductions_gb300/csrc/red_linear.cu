@@ -504,10 +504,11 @@ __global__ void __launch_bounds__(256)
 // Up to 128 rows: the weights' way through memory is what bounds a call, and tiles
 // of 256 rows x 256 columns would load as much of (packed, mostly empty) rows as of
 // weights, 76 at a time.  Here the weights are the operand with 128 rows, the hidden
-// states the one with ROWS = 16, 32, 64 or 128, and each CTA takes its share of the
-// vocabulary, equal to within 16 columns, so that all SMs stream weights to the end.
-// us, 256 x 256 tiles against this: FEWNOW
-constexpr int FEW_ROWS = 128, FEW_THREADS = 256, FEW_STEP = 16, FEW_MAX_CTAS = 512;
+// states the one with ROWS = 16, 32, 64 or 128, and each CTA takes an equal share of the
+// vocabulary in tiles of equal height (up to 128), so that all SMs stream weights to the
+// end; a tile is one copy per block of K, whatever its height.  us, 256 x 256 tiles, this
+// with tiles of 128 and an end in boxes of 16, as it is: FEWNOW
+constexpr int FEW_ROWS = 128, FEW_THREADS = 256, FEW_MAX_CTAS = 512;
 
 template <int ROWS>
 struct Few {
@@ -526,9 +527,10 @@ struct Few {
 };
 
 struct FewArgs {
-    CUtensorMap h, w, w_end;  // boxes of 64 x ROWS, 64 x 128, 64 x 16
+    CUtensorMap h, w;  // boxes of 64 x ROWS, 64 x height
     LinearWork work;
     int vocab, k_blocks;
+    int height, tiles;  // of each CTA
     float s2;
 };
 
@@ -597,9 +599,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
     __syncthreads();
     tmem_after();
     // this CTA's columns of the vocabulary
-    const int units = (a.vocab + FEW_STEP - 1) / FEW_STEP;
-    const int begin = (int)((int64_t)units * blockIdx.x / gridDim.x) * FEW_STEP;
-    const int end = min((int)((int64_t)units * (blockIdx.x + 1) / gridDim.x) * FEW_STEP, a.vocab);
+    const int begin = blockIdx.x * a.tiles * a.height, end = min(begin + a.tiles * a.height, a.vocab);
 
     if (live == 0) {
         // nothing takes part: no products (gradients of few rows still want their zeros)
@@ -610,22 +610,16 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
     } else if (warp == 0 && lane == 0) {
         RingPos<F::N> pos;
         bool ok = true;
-        for (int v = begin; v < end && ok; v += HALF)
+        for (int v = begin; v < end && ok; v += a.height)
             for (int k = 0; k < a.k_blocks; ++k) {
                 if (!mbar_wait(&b.empty[pos.stage], pos.phase ^ 1, &b.failed, 0)) {
                     ok = false;
                     break;
                 }
-                const int boxes = (min(end - v, HALF) + FEW_STEP - 1) / FEW_STEP;
                 uint64_t *const bar = &b.full[pos.stage];
-                mbar_expect(bar, (uint32_t)((boxes * FEW_STEP + ROWS) * BLOCK_K * 2));
+                mbar_expect(bar, (uint32_t)((a.height + ROWS) * BLOCK_K * 2));
                 unsigned char *const at = ring + pos.stage * F::STAGE;
-                if (boxes * FEW_STEP == HALF) {
-                    tma_load_alone(at, &a.w, k * BLOCK_K, v, bar);
-                } else {
-                    for (int i = 0; i < boxes; ++i)
-                        tma_load_alone(at + i * FEW_STEP * BLOCK_K * 2, &a.w_end, k * BLOCK_K, v + i * FEW_STEP, bar);
-                }
+                tma_load_alone(at, &a.w, k * BLOCK_K, v, bar);
                 tma_load_alone(at + OPERAND_BYTES, &a.h, k * BLOCK_K, 0, bar);
                 pos.next();
             }
@@ -638,7 +632,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
         AccPos acc;
         bool ok = true;
         const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true, HALF, ROWS);
-        for (int v = begin; v < end && ok; v += HALF)
+        for (int v = begin; v < end && ok; v += a.height)
             for (int k0 = 0; k0 < a.k_blocks && ok; k0 += CHUNK) {
                 if (!mbar_wait(&b.acc_empty[acc.slot], acc.phase ^ 1, &b.failed, 0)) {
                     ok = false;
@@ -677,9 +671,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g)
             m[g] = NEG_INF, l[g] = 0.0f;
-        for (int v0 = begin; v0 < end; v0 += HALF) {
+        for (int v0 = begin; v0 < end; v0 += a.height) {
             const int first = v0 + part * 32, v = first + lane;
-            const bool valid = v < end;
+            const int stop = min(v0 + a.height, end);  // (rows of the tile behind it hold what was there before)
+            const bool valid = v < stop;
             float z[ROWS];
             bool ok = true;
             for (int k = 0; k < a.k_blocks; k += CHUNK) {
@@ -714,7 +709,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
                 for (int g = 0; g < GROUPS; ++g) {
                     // a target among this warp's columns
                     const int t = lane < GROUP ? b.target[g * 32 + lane] - first : -1;
-                    unsigned here = __ballot_sync(0xffffffffu, t >= 0 && t < 32 && first + t < end);
+                    unsigned here = __ballot_sync(0xffffffffu, t >= 0 && t < 32 && first + t < stop);
                     while (here) {
                         const int i = __ffs(here) - 1;
                         here &= here - 1;
@@ -1111,7 +1106,7 @@ int launch_products(int64_t tiles, cudaStream_t s, const ProductArgs &a)
 }
 
 template <int DT, bool GRAD, int ROWS>
-int launch_few_rows(FewArgs &a, unsigned *grid, cudaStream_t s)
+int launch_few_rows(const LinearArgs &l, FewArgs &a, unsigned *grid, cudaStream_t s)
 {
     static std::atomic<bool> ready[MAX_DEVICES];
     DeviceInfo di;
@@ -1123,8 +1118,13 @@ int launch_few_rows(FewArgs &a, unsigned *grid, cudaStream_t s)
             "cudaFuncSetAttribute"));
         ready[di.dev].store(true, std::memory_order_relaxed);
     }
-    const int units = (a.vocab + FEW_STEP - 1) / FEW_STEP, most = di.sms < FEW_MAX_CTAS ? di.sms : FEW_MAX_CTAS;
-    *grid = (unsigned)(units < most ? units : most);
+    // equal shares of whole tiles; a share of less than 16 columns is not worth a CTA
+    const int most = di.sms < FEW_MAX_CTAS ? di.sms : FEW_MAX_CTAS;
+    const int share = a.vocab / most < 16 ? 16 : (a.vocab + most - 1) / most;
+    a.tiles = (share + HALF - 1) / HALF;
+    a.height = (share + a.tiles - 1) / a.tiles;
+    *grid = (unsigned)((a.vocab + a.tiles * a.height - 1) / (a.tiles * a.height));
+    RETURN_IF(matrix_map(&a.w, l.dtype, l.weight, l.dim, l.vocab, l.ldw, BLOCK_K, a.height));
     RETURN_IF(cuda_fail(launch_pdl_smem(kernel, *grid, FEW_THREADS, Few<ROWS>::SMEM, 1, s, a), "linear_few"));
     count_launches(1);
     return RED_OK;
@@ -1135,14 +1135,13 @@ int launch_few(const LinearArgs &a, const LinearWork &w, unsigned *grid, cudaStr
 {
     FewArgs f;
     RETURN_IF(matrix_map(&f.h, a.dtype, w.hidden, a.dim, w.padded, w.ld, BLOCK_K, w.few));
-    RETURN_IF(matrix_map(&f.w, a.dtype, a.weight, a.dim, a.vocab, a.ldw, BLOCK_K, HALF));
-    RETURN_IF(matrix_map(&f.w_end, a.dtype, a.weight, a.dim, a.vocab, a.ldw, BLOCK_K, FEW_STEP));
     f.work = w;
     f.vocab = (int)a.vocab;
     f.k_blocks = (int)(up(a.dim, BLOCK_K) / BLOCK_K);
     f.s2 = (float)(a.scale * 1.4426950408889634);
 #define FEW_OF(rows) \
-    (a.dtype == RED_BF16 ? launch_few_rows<RED_BF16, GRAD, rows>(f, grid, s) : launch_few_rows<RED_F16, GRAD, rows>(f, grid, s))
+    (a.dtype == RED_BF16 ? launch_few_rows<RED_BF16, GRAD, rows>(a, f, grid, s)          \
+                           : launch_few_rows<RED_F16, GRAD, rows>(a, f, grid, s))
     return w.few == 16 ? FEW_OF(16) : w.few == 32 ? FEW_OF(32) : w.few == 64 ? FEW_OF(64) : FEW_OF(128);
 #undef FEW_OF
 }
