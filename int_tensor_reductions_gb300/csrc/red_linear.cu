@@ -889,19 +889,28 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
     // The i-th tile of this pair: dh's in turn, then dw's.  A pair whose turn at dh does not come as
-    // often as the others' gets as many more of dw's first.  What a tile takes, in eighths of the time of
-    // one block of K in the tensor cores: dh's its blocks, or 22 each where few rows of tiles share what a
+    // often as the others' gets as many more of dw's.  What a tile takes, in eighths of the time of one
+    // block of K in the tensor cores: dh's its blocks, or 22 each where few rows of tiles share what a
     // block loads of the weights, dw's its blocks, or the 11 that its way to memory takes.
+    // Of few rows dh is no more than reading and dw no more than writing, of 32 KB a block and 128 KB a
+    // tile; memory reads and writes at once at 6.8 TB/s and only writes at 4, so beyond what L2 holds every
+    // other pair begins with dw (gradient 128 x 4096 x 32768 209 -> 203 us; 64 x 1024 x 32001 63 -> 67).
     const int rest = h_tiles % pairs, w_tiles = tiles - h_tiles;
-    const int h_cost = v_each * max(8, 22 / max(h_rows, 1)), w_cost = 8 * max(r_blocks, 11);
+    const int h_cost = a.few ? v_each : v_each * max(8, 22 / max(h_rows, 1)), w_cost = a.few ? 4 : 8 * max(r_blocks, 11);
     const int more = rest == 0 ? 0 : min((h_cost + w_cost / 2) / w_cost, w_tiles / (pairs - rest));
     const int h_mine = h_tiles / pairs + (pair < rest), w_more = pair < rest ? 0 : more;
+    const int w_shared = w_tiles - more * (pairs - rest);
+    const int w_mine = w_more + w_shared / pairs + (pair < w_shared % pairs);
+    const bool w_first = a.few && pair % 2 != 0 && w_tiles > 800;
     auto tile_of = [&](int i) {
+        if (i >= h_mine + w_mine)
+            return -1;
+        i -= w_first ? w_mine : 0;
+        i += i < 0 ? h_mine + w_mine : 0;  // as if dh's came first
         if (i < h_mine)
             return i * pairs + pair;
         i -= h_mine;
-        const int w = i < w_more ? i * (pairs - rest) + pair - rest : more * (pairs - rest) + (i - w_more) * pairs + pair;
-        return w < w_tiles ? h_tiles + w : -1;
+        return h_tiles + (i < w_more ? i * (pairs - rest) + pair - rest : more * (pairs - rest) + (i - w_more) * pairs + pair);
     };
     auto job = [&](int t) {
         if (t < h_tiles) {
@@ -910,7 +919,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
             return TileJob{&a.g_h, &a.w_n, at.m * TILE, at.n * TILE, k * BLOCK_K, a.v0 + k * BLOCK_K,
                            max(0, min(v_each, v_blocks - k)), !a.few, false};
         }
-        const TileAt at = tile_at(t - h_tiles, w_rows, a.n_tiles);
+        t -= h_tiles;
+        const TileAt at = a.few ? TileAt{t / a.n_tiles, t % a.n_tiles} : tile_at(t, w_rows, a.n_tiles);
         return TileJob{&a.g_w, &a.h_n, at.m * TILE, at.n * TILE, 0, 0, r_blocks, a.few, false};
     };
     if (warp == 0 && lane == 0) {
