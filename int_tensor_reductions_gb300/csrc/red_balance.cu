@@ -174,8 +174,6 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
     if (!a.dx)
         return;
     d = group_fold<LANES>(d, sh, turn, Add());
-    if (!here)
-        return;
     const float shift = by_lse - d;
 #pragma unroll
     for (int v = 0; v < N; ++v) {
@@ -185,7 +183,7 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
             const float p = x[v][k];
             g[k] = SIGMOID ? p * (1.0f - e[v][k]) * (s.c[v][k] - d) : p * (s.c[v][k] + shift);
         }
-        store_unit<DT, VEC>(a.dx, r * a.ldd, (v * LANES + lane) * E, a.experts, g);
+        store_unit<DT, VEC, LANES>(a.dx, r * a.ldd, (v * LANES + lane) * E, a.experts, here, g);
     }
 }
 
@@ -248,7 +246,7 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const Ba
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES, N = UNITS<DT, VECS>, E = UNIT<DT>;
     __shared__ GroupShared<LANES> sh;
     __shared__ float meet[(LANES > 32 ? 1 : NT / 32) * LANES * VECS * 8], meet_z[NT / 32];
-    using Rows = Ring<DT, LANES, UNITS<DT, VECS>, 1>;
+    using Rows = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 1>;
     extern __shared__ __align__(16) unsigned char ring[];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const int64_t step = (int64_t)gridDim.x * GROUPS, first = (int64_t)blockIdx.x * GROUPS + group;
@@ -257,11 +255,9 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const Ba
             Rows::fetch(ring, to, 0, a.x, r * a.ldx, lane, a.experts);
         fetch_commit();
     };
-    if constexpr (VEC) {
 #pragma unroll
-        for (int k = 0; k < Rows::STAGES - 1; ++k)
-            fetch(first + k * step, k);
-    }
+    for (int k = 0; k < Rows::STAGES - 1; ++k)
+        fetch(first + k * step, k);
     const float n = tokens_of(a.tick[RED_BALANCE_MAX_EXPERTS]);
     RowSums<N, E> s;
     begin_sums<LANES>(a, s, a.tick, n, lane);
@@ -273,16 +269,12 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const Ba
         const bool takes = next_takes;
         next_takes = takes_part(a, r + step);
         Raw raw[N];
-        if constexpr (VEC) {
-            fetch(r + (Rows::STAGES - 1) * step, (stage + Rows::STAGES - 1) % Rows::STAGES);
-            fetch_wait<Rows::STAGES - 1>();
+        fetch(r + (Rows::STAGES - 1) * step, (stage + Rows::STAGES - 1) % Rows::STAGES);
+        fetch_wait<Rows::STAGES - 1>();
 #pragma unroll
-            for (int v = 0; v < N; ++v)
-                raw[v] = Rows::take(ring, stage, 0, v);
-            stage = (stage + 1) % Rows::STAGES;
-        } else {
-            load_row<DT, VEC, LANES>(raw, a.x, takes ? r * a.ldx : 0, lane, takes ? a.experts : 0);
-        }
+        for (int v = 0; v < N; ++v)
+            raw[v] = Rows::take(ring, stage, 0, v, a.x, r * a.ldx, lane, a.experts);
+        stage = (stage + 1) % Rows::STAGES;
         balance_row<DT, SIGMOID, LANES, VEC>(a, raw, s, sh, turn, z_unit, r, r < a.rows, takes, lane);
     }
     meet_sums<LANES>(s, meet, meet_z, lane);
@@ -477,7 +469,7 @@ int launch_rows(BalanceArgs &a, cudaStream_t s)
     Workspace ws;
     if (st == RED_OK)
         st = get_workspace(&ws);
-    constexpr size_t SMEM = VEC ? Ring<DT, LANES, UNITS<DT, VECS>, 1>::BYTES : 0;
+    constexpr size_t SMEM = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 1>::BYTES;
     unsigned grid = 1;
     auto *const kernel = balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>;
     if (st == RED_OK)

@@ -76,55 +76,151 @@ __device__ __forceinline__ Raw load_some(const void *p, int64_t at, int n)
     return r;
 }
 
+// Rows that start anywhere (on an element): 16-byte blocks of memory are read and
+// written whole and their bytes moved in registers.  `off` is a row's distance from
+// the block it starts in, the same for all its units.  A block that a row shares
+// with what lies before or behind it is read whole, too (it is one transaction, and
+// never crosses into memory that no allocation holds), and written by elements.
+// (Element by element, norm 8000 x 4095 bf16: 192 us, as it is SHIFTNOW.)
+__device__ __forceinline__ int block_offset(const void *p) { return (int)((uintptr_t)p & 15); }
+
+// 16 bytes from byte `off` of the 32 in lo, hi on.
+template <int DT>
+__device__ __forceinline__ Raw window(const uint4 &lo, const uint4 &hi, int off)
+{
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const bool by2 = off & 8, by1 = off & 4;
+#pragma unroll
+    for (int k = 0; k < 6; ++k)
+        w[k] = by2 ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+        w[k] = by1 ? w[k + 1] : w[k];
+    Raw r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        r.u[k] = DT != RED_F32 ? __funnelshift_r(w[k], w[k + 1], off << 3 & 16) : w[k];
+    return r;
+}
+// Zeros from element n on.
+template <int DT>
+__device__ __forceinline__ Raw keep(Raw r, int n)
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (DT == RED_F32)
+            r.u[k] = k < n ? r.u[k] : 0u;
+        else
+            r.u[k] = 2 * k + 1 < n ? r.u[k] : 2 * k < n ? r.u[k] & 0xffffu : 0u;
+    }
+    return r;
+}
+
 // A lane's units of a row (`row`: the row's first element); 0 behind its end.
 // The loads are issued together: nothing here looks at what they bring.
 template <int DT, bool VEC, int LANES, int N>
 __device__ __forceinline__ void load_row(Raw (&r)[N], const void *p, int64_t row, int lane, int len)
 {
-    constexpr int E = UNIT<DT>;
+    constexpr int E = UNIT<DT>, SIZE = 16 / E;
+    const char *const at = static_cast<const char *>(p) + row * SIZE;
     if constexpr (VEC) {
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const int i = (u * LANES + lane) * E;
-            const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + (row + i) * (16 / E));
-            const uint4 x = i + E <= len ? *q : make_uint4(0, 0, 0, 0);
+            const uint4 x = i + E <= len ? *reinterpret_cast<const uint4 *>(at + (int64_t)i * SIZE) : make_uint4(0, 0, 0, 0);
             r[u].u[0] = x.x, r[u].u[1] = x.y, r[u].u[2] = x.z, r[u].u[3] = x.w;
         }
         if (len % E == 0)
             return;
-    }
-    // elements one by one: of one lane's last unit, or of all
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-        const int i = (u * LANES + lane) * E;
-        if (!VEC || (i < len && i + E > len))
-            r[u] = load_some<DT>(p, row + i, len - i);
+        for (int u = 0; u < N; ++u) {  // one lane's last unit
+            const int i = (u * LANES + lane) * E;
+            if (i < len && i + E > len)
+                r[u] = load_some<DT>(p, row + i, len - i);
+        }
+    } else {
+        const int off = block_offset(at);
+        uint4 lo[N], hi[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int i = (u * LANES + lane) * E;
+            const uint4 *const q = reinterpret_cast<const uint4 *>(at - off + (int64_t)i * SIZE);
+            lo[u] = i < len ? q[0] : make_uint4(0, 0, 0, 0);
+            hi[u] = i < len && (len - i) * SIZE + off > 16 ? q[1] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            r[u] = keep<DT>(window<DT>(lo[u], hi[u], off), len - (u * LANES + lane) * E);
     }
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void store_unit(void *p, int64_t row, int i, int len, const float (&v)[UNIT<DT>])
+// Bytes lo .. hi of a block (whole elements), from `r`, which holds it in place.
+template <int DT>
+__device__ __forceinline__ void store_some(char *block, const Raw &r, int lo, int hi)
 {
-    constexpr int E = UNIT<DT>;
-    if (VEC && i + E <= len) {
-        const Raw r = narrow<DT>(v);
-        *reinterpret_cast<uint4 *>(static_cast<char *>(p) + (row + i) * (16 / E)) =
-            make_uint4(r.u[0], r.u[1], r.u[2], r.u[3]);
-        return;
-    }
 #pragma unroll
-    for (int k = 0; k < E; ++k)
-        if (i + k < len)
-            store_elem<DT>(p, row + i + k, v[k]);
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (DT == RED_F32) {
+            if (4 * k >= lo && 4 * k < hi)
+                *reinterpret_cast<uint32_t *>(block + 4 * k) = r.u[k];
+        } else {
+            if (4 * k >= lo && 4 * k < hi)
+                *reinterpret_cast<uint16_t *>(block + 4 * k) = (uint16_t)r.u[k];
+            if (4 * k + 2 >= lo && 4 * k + 2 < hi)
+                *reinterpret_cast<uint16_t *>(block + 4 * k + 2) = (uint16_t)(r.u[k] >> 16);
+        }
+    }
+}
+
+// Unit i / E of a row, of which the first len - i elements are written, where `here`.
+// All lanes of the warp call it, with neighbouring units of a row in the lanes of a group.
+template <int DT, bool VEC, int LANES>
+__device__ __forceinline__ void store_unit(void *p, int64_t row, int i, int len, bool here, const float (&v)[UNIT<DT>])
+{
+    constexpr int E = UNIT<DT>, SIZE = 16 / E, W = LANES < 32 ? LANES : 32;
+    const Raw r = narrow<DT>(v);
+    char *const at = static_cast<char *>(p) + (row + i) * SIZE;
+    if constexpr (VEC) {
+        if (!here)
+            return;
+        if (i + E <= len)
+            *reinterpret_cast<uint4 *>(at) = make_uint4(r.u[0], r.u[1], r.u[2], r.u[3]);
+        else if (i < len)
+            store_some<DT>(at, r, 0, (len - i) * SIZE);
+    } else {
+        const int off = block_offset(at);
+        uint4 before;
+        before.x = __shfl_up_sync(0xffffffffu, r.u[0], 1, W);
+        before.y = __shfl_up_sync(0xffffffffu, r.u[1], 1, W);
+        before.z = __shfl_up_sync(0xffffffffu, r.u[2], 1, W);
+        before.w = __shfl_up_sync(0xffffffffu, r.u[3], 1, W);
+        if (!here || i >= len)
+            return;
+        const int bytes = min(len - i, E) * SIZE, lane = threadIdx.x % W;
+        const uint4 own = make_uint4(r.u[0], r.u[1], r.u[2], r.u[3]);
+        // the block that this unit begins in: the end of the lane's before, and what fits of its own
+        const Raw block = off == 0 ? r : window<DT>(before, own, 16 - off);
+        const int lo = lane == 0 ? off : 0, hi = min(off + bytes, 16);
+        if (lo == 0 && hi == 16)
+            *reinterpret_cast<uint4 *>(at - off) = make_uint4(block.u[0], block.u[1], block.u[2], block.u[3]);
+        else
+            store_some<DT>(at - off, block, lo, hi);
+        // the rest, where no lane behind takes it
+        if (off + bytes > 16 && (lane == W - 1 || i + E >= len))
+            store_some<DT>(at - off + 16, window<DT>(own, own, 16 - off), 0, off + bytes - 16);
+    }
 }
 
 // ------------------------------------------------------- rows fetched ahead
 
+template <bool KEEP>  // in L1, where another lane wants the same block
 __device__ __forceinline__ void fetch16(void *dst, const void *src, uint32_t bytes)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-                 "r"(bytes)
-                 : "memory");
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (KEEP)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -135,36 +231,62 @@ __device__ __forceinline__ void fetch_wait()
 
 // A ring of rows in shared memory, fetched while earlier rows are at work: each
 // thread fetches its own units of ARRAYS matrices and reads them back itself, so
-// that no barrier is needed.  Only rows on 16-byte boundaries go this way (VEC);
-// others are loaded when they are wanted.
-template <int DT, int LANES, int N, int ARRAYS>
+// that no barrier is needed.  Of rows off the 16-byte blocks (VEC false) it fetches the
+// two blocks that a unit lies in.
+template <int DT, bool VEC, int LANES, int N, int ARRAYS>
 struct Ring {
-    static constexpr int NT = GROUP_CTA<LANES>;
-    static constexpr int STAGE = ARRAYS * N * NT * 16;
+    static constexpr int NT = GROUP_CTA<LANES>, E = UNIT<DT>, SIZE = 16 / E, BLOCKS = VEC ? 1 : 2;
+    static constexpr int STAGE = ARRAYS * N * BLOCKS * NT * 16;
     // one row at work, one on its way; more are no use (norm 30000 x 512 bf16 with four 18.4 us, with two 17.3)
     static constexpr int STAGES = 2 * STAGE <= 204800 ? 2 : 1;
-    static constexpr size_t BYTES = (size_t)STAGE * STAGES;
+    // the longest fp32 rows off the blocks do not fit: they are loaded where they are wanted
+    static constexpr bool LATE = STAGE > 212992;
+    static constexpr size_t BYTES = LATE ? 0 : (size_t)STAGE * STAGES;
 
     static __device__ __forceinline__ uint4 *slot(unsigned char *ring, int stage, int array, int u)
     {
-        return reinterpret_cast<uint4 *>(ring) + ((stage * ARRAYS + array) * N + u) * NT + threadIdx.x;
+        return reinterpret_cast<uint4 *>(ring) + ((stage * ARRAYS + array) * N + u) * BLOCKS * NT + threadIdx.x;
     }
     static __device__ __forceinline__ void fetch(unsigned char *ring, int stage, int array, const void *p, int64_t row,
                                                  int lane, int len)
     {
-        constexpr int E = UNIT<DT>;
+        if (LATE)
+            return;
+        const char *const at = static_cast<const char *>(p) + row * SIZE;
+        const int off = VEC ? 0 : block_offset(at);
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const int i = (u * LANES + lane) * E;
-            const int left = (len - i) * (16 / E);
-            const uint32_t bytes = left <= 0 ? 0 : left < 16 ? left : 16;
-            fetch16(slot(ring, stage, array, u), static_cast<const char *>(p) + (bytes ? (row + i) * (16 / E) : 0), bytes);
+            uint4 *const to = slot(ring, stage, array, u);
+            if constexpr (VEC) {
+                const int left = (len - i) * SIZE;
+                const uint32_t bytes = left <= 0 ? 0 : left < 16 ? left : 16;
+                fetch16<false>(to, bytes ? at + (int64_t)i * SIZE : at, bytes);
+            } else {
+                const char *const block = at - off + (int64_t)i * SIZE;
+                const bool one = i < len, two = one && (len - i) * SIZE + off > 16;
+                fetch16<true>(to, one ? block : at - off, one ? 16 : 0);
+                fetch16<true>(to + NT, two ? block + 16 : at - off, two ? 16 : 0);
+            }
         }
     }
-    static __device__ __forceinline__ Raw take(unsigned char *ring, int stage, int array, int u)
+    // `row` and `len` as they were fetched; `lane`'s unit u.
+    static __device__ __forceinline__ Raw take(unsigned char *ring, int stage, int array, int u, const void *p, int64_t row,
+                                               int lane, int len)
     {
-        const uint4 x = *slot(ring, stage, array, u);
-        return {{x.x, x.y, x.z, x.w}};
+        const uint4 *const from = slot(ring, stage, array, u);
+        if constexpr (LATE) {
+            Raw r[1];
+            load_row<DT, VEC, 1>(r, p, row + (u * LANES + lane) * E, 0, len - (u * LANES + lane) * E);
+            return r[0];
+        } else if constexpr (VEC) {
+            const uint4 x = from[0];
+            return {{x.x, x.y, x.z, x.w}};
+        } else {
+            const uint4 x = from[0];
+            const int off = block_offset(static_cast<const char *>(p) + row * SIZE);
+            return keep<DT>(window<DT>(x, from[NT], off), len - (u * LANES + lane) * E);
+        }
     }
 };
 

@@ -7,10 +7,9 @@
 // Both directions are one pass: a group of lanes holds a row in registers, in
 // fp32, between its reduction and its results, so that each matrix crosses
 // memory once and that is what bounds them.  A group is 8 to 32 lanes of a warp
-// (rows of up to 1024) or a CTA (up to 16384); a lane holds up to four vectors
-// of eight consecutive elements.  Rows off the 16-byte boundaries go through the
-// same code with loads of one element.  Rows are fetched into shared memory while
-// earlier ones are at work (Ring in red_groups.cuh).
+// (rows of up to 1024) or a CTA (up to 16384); a lane holds up to 32 elements.
+// Rows are fetched into shared memory while earlier ones are at work (Ring in
+// red_groups.cuh, and how rows off the 16-byte blocks of memory are read and written).
 //
 // The backward keeps each lane's share of dw in registers over all the rows of
 // its group; the groups' shares go to the workspace and a second kernel adds them
@@ -144,20 +143,41 @@ __device__ __forceinline__ uint64_t narrow8(const float (&v)[E], float inv)
     return r;
 }
 
-template <int E>
-__device__ __forceinline__ void store_q(uint8_t *q, int64_t row, int i, int len, bool vec, uint64_t v)
+// A unit's 8-bit values, as store_unit; off the blocks of E bytes (ALIGNED false) they
+// are moved the same way.
+template <int E, bool ALIGNED, int LANES>
+__device__ __forceinline__ void store_q(uint8_t *q, int64_t row, int i, int len, bool here, uint64_t v)
 {
-    if (vec && i + E <= len) {
-        if (E == 8)
-            *reinterpret_cast<uint64_t *>(q + row + i) = v;
-        else
-            *reinterpret_cast<uint32_t *>(q + row + i) = (uint32_t)v;
-        return;
-    }
+    using Block = std::conditional_t<E == 8, uint64_t, uint32_t>;
+    constexpr int W = LANES < 32 ? LANES : 32;
+    uint8_t *const at = q + row + i;
+    auto some = [](uint8_t *block, Block bits, int lo, int hi) {
 #pragma unroll
-    for (int k = 0; k < E; ++k)
-        if (i + k < len)
-            q[row + i + k] = (uint8_t)(v >> (8 * k));
+        for (int k = 0; k < E; ++k)
+            if (k >= lo && k < hi)
+                block[k] = (uint8_t)(bits >> (8 * k));
+    };
+    const Block own = (Block)v;
+    if constexpr (ALIGNED) {
+        if (here && i + E <= len)
+            *reinterpret_cast<Block *>(at) = own;
+        else if (here && i < len)
+            some(at, own, 0, len - i);
+    } else {
+        const int off = (int)((uintptr_t)at % E), lane = threadIdx.x % W;
+        const Block before = __shfl_up_sync(0xffffffffu, own, 1, W);
+        if (!here || i >= len)
+            return;
+        const int bytes = min(len - i, E);
+        const Block block = off == 0 ? own : (Block)(own << (8 * off)) | (Block)(before >> (8 * (E - off)));
+        const int lo = lane == 0 ? off : 0, hi = min(off + bytes, E);
+        if (lo == 0 && hi == E)
+            *reinterpret_cast<Block *>(at - off) = block;
+        else
+            some(at - off, block, lo, hi);
+        if (off + bytes > E && (lane == W - 1 || i + E >= len))
+            some(at - off + E, (Block)(own >> (8 * (E - off))), 0, off + bytes - E);
+    }
 }
 
 // KIND: 0 for y in x's type, else the 8-bit type.
@@ -167,7 +187,7 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArg
     pdl_enter();
     __shared__ GroupShared<LANES> sh;
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES, N = UNITS<DT, VECS>, E = UNIT<DT>;
-    using Rows = Ring<DT, LANES, UNITS<DT, VECS>, 2>;
+    using Rows = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 2>;
     extern __shared__ __align__(16) unsigned char ring[];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const int64_t step = (int64_t)gridDim.x * GROUPS, first = (int64_t)blockIdx.x * GROUPS + group;
@@ -196,9 +216,9 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArg
             fetch_wait<Rows::STAGES - 1>();
 #pragma unroll
             for (int v = 0; v < N; ++v) {
-                raw[v] = Rows::take(ring, stage, 0, v);
+                raw[v] = Rows::take(ring, stage, 0, v, a.x, r * a.ldx, lane, a.len);
                 if (a.residual)
-                    res[v] = Rows::take(ring, stage, 1, v);
+                    res[v] = Rows::take(ring, stage, 1, v, a.residual, r * a.ldr, lane, a.len);
             }
             stage = (stage + 1) % Rows::STAGES;
         } else {
@@ -222,10 +242,10 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArg
             for (int k = 0; k < E; ++k)
                 sum = fmaf(t[v][k], t[v][k], sum);
         }
-        if (a.residual && here) {
+        if (a.residual) {
 #pragma unroll
             for (int v = 0; v < N; ++v)
-                store_unit<DT, VEC>(a.total, r * a.ldt, (v * LANES + lane) * E, a.len, t[v]);
+                store_unit<DT, VEC, LANES>(a.total, r * a.ldt, (v * LANES + lane) * E, a.len, here, t[v]);
         }
         sum = group_fold<LANES>(sum, sh, turn, Add());
         const float rstd = __frsqrt_rn(fmaf(sum, a.inv_len, a.eps));
@@ -243,8 +263,8 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArg
                 if (KIND != 0)
                     most[v] = Max()(most[v], fabsf(t[v][k]));
             }
-            if (KIND == 0 && here)
-                store_unit<DT, VEC>(a.y, r * a.ldy, (v * LANES + lane) * E, a.len, t[v]);
+            if (KIND == 0)
+                store_unit<DT, VEC, LANES>(a.y, r * a.ldy, (v * LANES + lane) * E, a.len, here, t[v]);
         }
         if constexpr (KIND != 0) {
             if (a.block) {
@@ -269,11 +289,9 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArg
                 const int i = (v * LANES + lane) * E;
                 float inv;
                 const float scale = scale_of<KIND>(a.block ? most[v] : most[0], &inv);
-                if (here && i < a.len) {
-                    if (a.block ? lane % (a.block / E) == 0 : v == 0 && lane == 0)
-                        a.scales[r * a.blocks + (a.block ? i / a.block : 0)] = scale;
-                    store_q<E>(static_cast<uint8_t *>(a.y), r * a.ldy, i, a.len, VEC, narrow8<KIND>(t[v], inv));
-                }
+                if (here && i < a.len && (a.block ? lane % (a.block / E) == 0 : v == 0 && lane == 0))
+                    a.scales[r * a.blocks + (a.block ? i / a.block : 0)] = scale;
+                store_q<E, VEC, LANES>(static_cast<uint8_t *>(a.y), r * a.ldy, i, a.len, here, narrow8<KIND>(t[v], inv));
             }
         }
     }
@@ -309,7 +327,7 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_grad_kernel(const No
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES, N = UNITS<DT, VECS>, E = UNIT<DT>;
     // groups of one warp or less meet in shared memory before the workspace
     __shared__ float meet[GROUPS > 1 ? NT / 32 * N * LANES * E : 1];
-    using Rows = Ring<DT, LANES, UNITS<DT, VECS>, 3>;
+    using Rows = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 3>;
     extern __shared__ __align__(16) unsigned char ring[];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const int64_t step = (int64_t)gridDim.x * GROUPS, first = (int64_t)blockIdx.x * GROUPS + group;
@@ -323,11 +341,9 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_grad_kernel(const No
         }
         fetch_commit();
     };
-    if constexpr (VEC) {
 #pragma unroll
-        for (int k = 0; k < Rows::STAGES - 1; ++k)
-            fetch(first + k * step, k);
-    }
+    for (int k = 0; k < Rows::STAGES - 1; ++k)
+        fetch(first + k * step, k);
     const Weights<DT, WIDE, VEC, LANES, N> weights(a.weight, lane, a.len);
     float dw[N][E];
 #pragma unroll
@@ -339,25 +355,20 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_grad_kernel(const No
     for (int64_t r0 = (int64_t)blockIdx.x * GROUPS; r0 < a.rows; r0 += step) {
         const bool here = r0 + group < a.rows;
         const int64_t r = here ? r0 + group : a.rows - 1;
-        Raw x[N], dy[N], dt[N];  // (in shared memory where rows are fetched ahead)
         const float rstd = rstd_next;
         if (r0 + group + step < a.rows)
             rstd_next = a.rstd[r0 + group + step];
-        if constexpr (VEC) {
-            fetch(r0 + group + (Rows::STAGES - 1) * step, (stage + Rows::STAGES - 1) % Rows::STAGES);
-            fetch_wait<Rows::STAGES - 1>();
-        } else {
-            load_row<DT, VEC, LANES>(x, a.x, r * a.ldx, lane, a.len);
-            load_row<DT, VEC, LANES>(dy, a.dy, r * a.ldy, lane, a.len);
-            if (a.dtotal)
-                load_row<DT, VEC, LANES>(dt, a.dtotal, r * a.ldt, lane, a.len);
-        }
+        fetch(r0 + group + (Rows::STAGES - 1) * step, (stage + Rows::STAGES - 1) % Rows::STAGES);
+        fetch_wait<Rows::STAGES - 1>();
+        auto take = [&](int array, int v, const void *p, int64_t ld, float (&to)[E]) {
+            widen<DT>(Rows::take(ring, stage, array, v, p, r * ld, lane, a.len), to);
+        };
         float c = 0.0f;
 #pragma unroll
         for (int v = 0; v < N; ++v) {
             float h[E], g[E], w[E];
-            widen<DT>(VEC ? Rows::take(ring, stage, 0, v) : x[v], h);
-            widen<DT>(VEC ? Rows::take(ring, stage, 1, v) : dy[v], g);
+            take(0, v, a.x, a.ldx, h);
+            take(1, v, a.dy, a.ldy, g);
             weights.at(v, w);
 #pragma unroll
             for (int k = 0; k < E; ++k) {
@@ -368,26 +379,23 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_grad_kernel(const No
             }
         }
         c = group_fold<LANES>(c, sh, turn, Add()) * a.inv_len;
-        const int at = stage;
-        stage = (stage + 1) % Rows::STAGES;
-        if (!here)
-            continue;
-        // h and g again, from what the loads brought: registers hold the weights and dw
+        // h and g again from shared memory: registers hold the weights and dw
 #pragma unroll
         for (int v = 0; v < N; ++v) {
             float h[E], g[E], w[E], d[E];
-            widen<DT>(VEC ? Rows::take(ring, at, 0, v) : x[v], h);
-            widen<DT>(VEC ? Rows::take(ring, at, 1, v) : dy[v], g);
+            take(0, v, a.x, a.ldx, h);
+            take(1, v, a.dy, a.ldy, g);
             weights.at(v, w);
             if (a.dtotal)
-                widen<DT>(VEC ? Rows::take(ring, at, 2, v) : dt[v], d);
+                take(2, v, a.dtotal, a.ldt, d);
 #pragma unroll
             for (int k = 0; k < E; ++k) {
                 const float n = fmaf(-h[k] * rstd, c, g[k] * w[k]);
                 d[k] = a.dtotal ? fmaf(n, rstd, d[k]) : n * rstd;
             }
-            store_unit<DT, VEC>(a.dx, r * a.ldd, (v * LANES + lane) * E, a.len, d);
+            store_unit<DT, VEC, LANES>(a.dx, r * a.ldd, (v * LANES + lane) * E, a.len, here, d);
         }
+        stage = (stage + 1) % Rows::STAGES;
     }
     if (!a.dw)
         return;
@@ -462,7 +470,7 @@ int forward(const NormArgs &a, cudaStream_t s)
 {
     static Resident cache;
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
-    constexpr size_t SMEM = RING ? Ring<DT, LANES, UNITS<DT, VECS>, 2>::BYTES : 0;
+    constexpr size_t SMEM = RING ? Ring<DT, VEC, LANES, UNITS<DT, VECS>, 2>::BYTES : 0;
     auto *const kernel = rmsnorm_kernel<DT, WIDE, KIND, LANES, VECS, VEC, RING>;
     unsigned grid;
     const int st = resident_grid(kernel, cache, NT, SMEM, (a.rows + GROUPS - 1) / GROUPS, INT32_MAX, &grid);
@@ -489,9 +497,9 @@ int forward_of(const NormArgs &a, int kind, cudaStream_t s)
             if (kind == 0 && a.residual && a.len > 6 * L * V)
                 return forward<DT, WIDE, 0, L, V, VEC, false>(a, s);
         }
-        return kind == 0                ? forward<DT, WIDE, 0, L, V, VEC, VEC>(a, s)
-               : kind == RED_QUANT_E4M3 ? forward<DT, WIDE, RED_QUANT_E4M3, L, V, VEC, VEC>(a, s)
-                                        : forward<DT, WIDE, RED_QUANT_I8, L, V, VEC, VEC>(a, s);
+        return kind == 0                ? forward<DT, WIDE, 0, L, V, VEC, true>(a, s)
+               : kind == RED_QUANT_E4M3 ? forward<DT, WIDE, RED_QUANT_E4M3, L, V, VEC, true>(a, s)
+                                        : forward<DT, WIDE, RED_QUANT_I8, L, V, VEC, true>(a, s);
     });
 }
 
@@ -516,7 +524,7 @@ int backward(NormGradArgs a, cudaStream_t s)
 {
     static Resident cache;
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
-    constexpr size_t SMEM = VEC ? Ring<DT, LANES, UNITS<DT, VECS>, 3>::BYTES : 0;
+    constexpr size_t SMEM = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 3>::BYTES;
     unsigned grid;
     auto *const kernel = rmsnorm_grad_kernel<DT, WIDE, LANES, VECS, VEC>;
     int st = resident_grid(kernel, cache, NT, SMEM, (a.rows + GROUPS - 1) / GROUPS,
