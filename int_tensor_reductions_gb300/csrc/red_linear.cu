@@ -459,20 +459,21 @@ struct Pair {
 
 template <int LANES>
 __global__ void __launch_bounds__(256) 
-    linear_join_kernel(const LinearWork w, int64_t rows, int64_t slots, float s2, float *logp, float *lse)
+    linear_join_kernel(const LinearWork w, const int64_t *targets, int64_t vocab, int64_t rows, int64_t slots, float s2,
+                       float *logp, float *lse)
 {
     pdl_enter();
     __shared__ float2 warps[8];
     constexpr int GROUPS = 256 / LANES;
     const int lane = threadIdx.x % LANES;
     for (int64_t r = (int64_t)blockIdx.x * GROUPS + threadIdx.x / LANES; r < rows; r += (int64_t)gridDim.x * GROUPS) {
-        const int at = w.pos[r];
+        const int64_t at = !w.few ? w.pos[r] : targets[r] >= 0 && targets[r] < vocab ? r : -1;
         if (at < 0) {
             if (lane == 0)
                 logp[r] = lse[r] = 0.0f;
             continue;
         }
-        const float2 *part = w.part + (int64_t)at * w.slots;
+        const float2 *part = w.part + at * w.slots;
         Pair p = {NEG_INF, 0.0f};
 #pragma unroll 4
         for (int64_t i = lane; i < slots; i += LANES) {
@@ -532,6 +533,10 @@ struct FewArgs {
     int vocab, k_blocks;
     int height, tiles;  // of each CTA
     float s2;
+    // Forward: the rows as they are, `rows` of them with these targets.  One that takes no part is no
+    // more than a column that nobody reads; the gradients take packed rows (its NaN would reach dw).
+    const int64_t *targets;
+    int rows;
 };
 
 __device__ __forceinline__ float max_of_warp(float v)
@@ -587,10 +592,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
     if (warp == 2)
         tmem_alloc_alone<F::COLUMNS>(&b.tmem);
     pdl_enter();
-    const int live = a.work.head->live;
+    const int live = GRAD ? a.work.head->live : a.rows;
     for (int r = threadIdx.x; r < ROWS; r += FEW_THREADS) {
         const bool takes = r < live;
-        b.target[r] = takes ? a.work.target[r] : -1;
+        if (GRAD) {
+            b.target[r] = takes ? a.work.target[r] : -1;
+        } else {
+            const int64_t t = takes ? a.targets[r] : -1;
+            b.target[r] = t >= 0 && t < a.vocab ? (int)t : -1;
+        }
         if (GRAD)
             b.coefs[r] = takes ? make_float4(a.work.by_p[r], a.work.by_target[r], a.work.lse2[r], 0.0f)
                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1144,7 +1154,12 @@ template <bool GRAD>
 int launch_few(const LinearArgs &a, const LinearWork &w, unsigned *grid, cudaStream_t s)
 {
     FewArgs f;
-    RETURN_IF(matrix_map(&f.h, a.dtype, w.hidden, a.dim, w.padded, w.ld, BLOCK_K, w.few));
+    if (GRAD)
+        RETURN_IF(matrix_map(&f.h, a.dtype, w.hidden, a.dim, w.padded, w.ld, BLOCK_K, w.few));
+    else
+        RETURN_IF(matrix_map(&f.h, a.dtype, a.hidden, a.dim, a.rows, a.ldh, BLOCK_K, w.few));
+    f.targets = a.target;
+    f.rows = (int)a.rows;
     f.work = w;
     f.vocab = (int)a.vocab;
     f.k_blocks = (int)(up(a.dim, BLOCK_K) / BLOCK_K);
@@ -1229,7 +1244,8 @@ LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, boo
 int launch_linear_logprob(const LinearArgs &a, float *logp, float *lse, void *work, cudaStream_t s)
 {
     const LinearWork w = linear_work(work, a.rows, a.dim, a.vocab, false);
-    RETURN_IF(pack_rows<false>(a, w, nullptr, nullptr, nullptr, s));
+    if (!w.few)
+        RETURN_IF(pack_rows<false>(a, w, nullptr, nullptr, nullptr, s));
     const float s2 = (float)(a.scale * 1.4426950408889634);
     int64_t slots = w.slots;
     if (w.few) {
@@ -1253,8 +1269,8 @@ int launch_linear_logprob(const LinearArgs &a, float *logp, float *lse, void *wo
     }
     const bool wide = a.rows <= 2048;
     RETURN_IF(cuda_fail(launch_pdl(wide ? linear_join_kernel<256> : linear_join_kernel<32>,
-                                   dim3(wide ? (unsigned)a.rows : warp_rows_grid(a.rows)), dim3(256), s, w, a.rows, slots, s2,
-                                   logp, lse),
+                                   dim3(wide ? (unsigned)a.rows : warp_rows_grid(a.rows)), dim3(256), s, w, a.target, a.vocab,
+                                   a.rows, slots, s2, logp, lse),
                         "linear_join"));
     count_launches(1);
     return RED_OK;

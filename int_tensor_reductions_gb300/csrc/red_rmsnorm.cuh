@@ -181,8 +181,10 @@ __device__ __forceinline__ void store_q(uint8_t *q, int64_t row, int i, int len,
 }
 
 // KIND: 0 for y in x's type, else the 8-bit type.
+// (Registers are left to the compiler, but for one case that it makes 70 of, and three CTAs per SM: with 64, and four,
+// 16384 x 4096 bf16 91 -> 83 us.  A bound of one CTA per SM has it take more than 128: 16384 x 8192 173 -> 264.)
 template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC, bool RING>
-__global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_kernel(const NormArgs a)
+__global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VECS == 2 && VEC && !RING ? 4 : 0) rmsnorm_kernel(const NormArgs a)
 {
     pdl_enter();
     __shared__ GroupShared<LANES> sh;
