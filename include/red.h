@@ -478,7 +478,8 @@ int red_preference(int dtype, const void *x, int64_t rows, int64_t len, int64_t 
  *   hidden   rows x dim, row stride ldh;  weight: vocab x dim, row stride ldw.
  *            Every matrix starts on a 16-byte boundary and its row stride is a
  *            multiple of 8 elements (where it has more than one row), dim
- *            itself is any number up to 2^20; rows and vocab up to 2^24.
+ *            itself is any number up to 2^20; rows and vocab up to 2^24, their
+ *            product up to 2^46.
  *   target   one int64 column of the vocabulary per row; a row whose target is
  *            outside [0, vocab) is ignored: its results are 0, and what it holds
  *            (NaN, say) reaches no other row and no gradient.

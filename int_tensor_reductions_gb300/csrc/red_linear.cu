@@ -507,8 +507,12 @@ __global__ void __launch_bounds__(256)
 // weights, 76 at a time.  Here the weights are the operand with 128 rows, the hidden
 // states the one with ROWS = 16, 32, 64 or 128, and each CTA takes an equal share of the
 // vocabulary in tiles of equal height (up to 128), so that all SMs stream weights to the
-// end; a tile is one copy per block of K, whatever its height.  us, 256 x 256 tiles, this
-// with tiles of 128 and an end in boxes of 16, as it is: FEWNOW
+// end; a tile is one copy per block of K, whatever its height.  Forward, us, with tiles of
+// 256 x 256 / of 128 with an end in boxes of 16 / of equal height / the rows unpacked
+// (as it is): 1 x 2048 x 65536 61, 58, 52, 47; 16 x 4096 x 50257 -, 88, 75, 69.  The
+// stages in flight are not what bounds it (4 of 18 KB instead of 11 cost 8%, 7 cost 2%),
+// nor is the rows' distance in memory; 128 bytes of each of many rows at a time come at 5.4
+// to 5.7 TB/s where one stream of all rows comes at 6.5.
 constexpr int FEW_ROWS = 128, FEW_THREADS = 256, FEW_MAX_CTAS = 512;
 
 template <int ROWS>
@@ -1197,6 +1201,8 @@ int pack_rows(const LinearArgs &a, const LinearWork &w, const float *lse, const 
 LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, bool grad)
 {
     LinearWork w = {};
+    if (rows == 0)
+        return w;
     unsigned char *const p = static_cast<unsigned char *>(base);
     int64_t at = 0;
     auto take = [&](auto *&field, int64_t bytes) {
@@ -1230,7 +1236,7 @@ LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, boo
         take(g, (w.few ? w.few : w.padded) * w.piece_cols * 2);
         w.piece = g;
         // dh of few rows is few tiles that are long: shares of the vocabulary fill the pairs of CTAs
-        // (64 x 1024 x 32001: four tiles of 501 blocks of K, products 191 us; 18 shares SPLITNOW)
+        // (64 x 1024 x 32001: four tiles of 501 blocks of K, products 191 us, in 18 shares 46)
         const int64_t tiles = w.padded / TILE * (up(dim, TILE) / TILE), blocks = w.piece_cols / BLOCK_K;
         int64_t splits = w.piece_cols < up(vocab, TILE) ? 1 : 72 / tiles;
         splits = splits < blocks / 8 ? splits : blocks / 8;

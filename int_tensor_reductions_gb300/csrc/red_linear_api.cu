@@ -9,6 +9,7 @@ namespace {
 
 constexpr int64_t MAX_ROWS = int64_t(1) << 24;  // rows and columns of tiles are 32-bit coordinates
 constexpr int64_t MAX_DIM = int64_t(1) << 20;
+constexpr int64_t MAX_LOGITS = int64_t(1) << 46;  // tiles are counted in 32 bits
 constexpr int64_t MAX_STRIDE = int64_t(1) << 36;
 
 bool bad_ptr(const void *p, uintptr_t align) { return !p || ((uintptr_t)p) % align != 0; }
@@ -19,6 +20,8 @@ int check_sizes(const char *who, int64_t rows, int64_t dim, int64_t vocab)
     if (rows < 0 || rows > MAX_ROWS || dim < 1 || dim > MAX_DIM || vocab < 1 || vocab > MAX_ROWS)
         return fail(RED_EINVAL, "%s: rows = %lld, dim = %lld, vocab = %lld out of range", who, (long long)rows,
                     (long long)dim, (long long)vocab);
+    if (rows > MAX_LOGITS / vocab)
+        return fail(RED_EINVAL, "%s: rows * vocab = %lld * %lld is over 2^46", who, (long long)rows, (long long)vocab);
     return RED_OK;
 }
 

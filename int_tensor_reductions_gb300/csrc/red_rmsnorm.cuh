@@ -112,7 +112,8 @@ template <int KIND>
 __device__ __forceinline__ float scale_of(float most, float *inv)
 {
     const float scale = most == 0.0f ? 1.0f : most * (1.0f / TOP<KIND>);
-    *inv = fminf(__frcp_rn(scale), 3.402823466e38f);
+    const float r = __frcp_rn(scale);
+    *inv = r > 3.402823466e38f ? 3.402823466e38f : r;  // (a NaN stays one)
     return scale;
 }
 

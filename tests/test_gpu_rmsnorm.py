@@ -223,6 +223,11 @@ def test_nan_and_infinity_stay_in_their_row(length, dtype):
     assert bool(y[2].isnan().all() and y[4, length - 1].isnan() and (y[4, :length - 1] == 0).all() and (y[6] == 0).all())
     q, scales, _, _ = itr.red_rmsnorm_quant(x, w, block=32)
     assert bool(scales[2].isnan().all() and q[2].float().isnan().all() and not scales[keep].isnan().any())
+    spoilt = w.clone()
+    spoilt[3] = math.nan  # one column: its block of each row
+    q, scales, _, _ = itr.red_rmsnorm_quant(x[:2], spoilt, block=32)
+    assert bool(scales[:, 0].isnan().all() and not scales[:, 1:].isnan().any() and q[:, :32].float().isnan().all())
+    assert bool(q[:, 32:].float().isfinite().all())
     dy = randn(9, length, dtype, 2)
     good = torch.where(rstd.isfinite() & (rstd > 0), rstd, 1.0)
     want = itr.red_rmsnorm_grad(dy, torch.where(x.isfinite(), x, 0.0), good, w)[0]
