@@ -445,6 +445,48 @@ PyObject *linear_logprob_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
 
 // ------------------------------------------------- root-mean-square norm
 
+// New results of a call.  Small ones share an allocation: each is a microsecond of the
+// host's time, and that of a norm of one row is 2 us on the GPU.  Large ones do not, so
+// that one that is kept keeps no other's memory.
+class Results {
+    static constexpr int64_t SMALL = 1 << 20, ALIGN = 128;
+    const Logits &l;
+    const bool merged;
+    at::Tensor whole;
+    int64_t used = 0;
+
+public:
+    // `bytes`: of all of them, `count` in number.
+    Results(const Logits &like, int64_t bytes, int count) : l(like), merged(bytes <= SMALL)
+    {
+        if (merged)
+            whole = at::empty({bytes + count * ALIGN}, l.x.options().dtype(at::kByte));
+    }
+    at::Tensor rows(int64_t n, int64_t cols, int64_t ld, at::ScalarType type)
+    {
+        if (!merged)
+            return ld == cols ? at::empty({n, cols}, l.x.options().dtype(type))
+                              : at::empty_strided({n, cols}, {ld, 1}, l.x.options().dtype(type));
+        return part({n, cols}, {ld, 1}, n * ld, type);
+    }
+    at::Tensor vector(int64_t n, at::ScalarType type)
+    {
+        return merged ? part({n}, {1}, n, type) : at::empty({n}, l.x.options().dtype(type));
+    }
+
+private:
+    at::Tensor part(c10::IntArrayRef sizes, c10::IntArrayRef strides, int64_t elements, at::ScalarType type)
+    {
+        auto impl = c10::make_intrusive<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(whole.storage()),
+                                                         whole.key_set(), c10::scalarTypeToTypeMeta(type));
+        const int64_t size = (int64_t)c10::elementSize(type);
+        impl->set_storage_offset(used / size);
+        impl->set_sizes_and_strides(sizes, strides);
+        used += (elements * size + ALIGN - 1) / ALIGN * ALIGN;
+        return at::Tensor(std::move(impl));
+    }
+};
+
 // A matrix like x: dtype, device and shape; its row stride through *ld.
 const at::Tensor &beside(const Logits &l, PyObject *o, const char *name, int64_t *ld)
 {
@@ -453,12 +495,6 @@ const at::Tensor &beside(const Logits &l, PyObject *o, const char *name, int64_t
         refuse("%s must have x's dtype, device and shape", name);
     *ld = Logits::stride(t, name);
     return t;
-}
-// A new matrix in x's layout.
-at::Tensor new_rows(const Logits &l)
-{
-    return l.ld == l.len ? at::empty({l.rows, l.len}, l.x.options())
-                         : at::empty_strided({l.rows, l.len}, {l.ld, 1}, l.x.options());
 }
 // The weight (len values of x's type or fp32; None: 1) and its type.
 const void *norm_weight(const Logits &l, PyObject *o, int *wtype)
@@ -489,16 +525,19 @@ struct NormInputs {
             residual = beside(l, res, "residual", &ldr).data_ptr();
     }
     // After the stream is set: what the call allocates is that stream's.
-    void results(PyObject *given_total)
+    void results(Results &made, PyObject *given_total)
     {
         if (with_residual) {
-            total = given_total == Py_None ? new_rows(l) : beside(l, given_total, "total", &ldt);
+            total = given_total == Py_None ? made.rows(l.rows, l.len, l.ld, l.x.scalar_type())
+                                           : beside(l, given_total, "total", &ldt);
             ldt = Logits::stride(total, "total");
         } else if (given_total != Py_None) {
             refuse("total comes with a residual");
         }
-        rstd = l.floats(l.rows);
+        rstd = made.vector(l.rows, at::kFloat);
     }
+    // Bytes of y (or 8-bit values and scales), total and rstd, at most.
+    int64_t bytes() const { return l.rows * (2 * l.ld * (int64_t)l.x.element_size() + 4 * (l.len / 32 + 2)); }
     void *total_ptr() const { return total.defined() ? total.data_ptr() : nullptr; }
 };
 
@@ -509,8 +548,10 @@ PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n)
         NormInputs in(a[0], a[1], a[2]);
         const OnStream on(a[6], in.l);
         int64_t ldy = in.l.ld;
-        const at::Tensor y = a[4] == Py_None ? new_rows(in.l) : beside(in.l, a[4], "out", &ldy);
-        in.results(a[5]);
+        Results made(in.l, in.bytes(), 3);
+        const at::Tensor y = a[4] == Py_None ? made.rows(in.l.rows, in.l.len, in.l.ld, in.l.x.scalar_type())
+                                             : beside(in.l, a[4], "out", &ldy);
+        in.results(made, a[5]);
         RETURN_IF_REFUSED(red_rmsnorm(in.l.dtype, in.l.x.data_ptr(), in.l.rows, in.l.len, in.l.ld, in.residual, in.ldr,
                                       in.wtype, in.weight, (float)number(a[3]), y.data_ptr(), ldy, in.total_ptr(),
                                       in.ldt, data(in.rstd), on.stream));
@@ -526,17 +567,19 @@ PyObject *rmsnorm_quant(PyObject *, PyObject *const *a, Py_ssize_t n)
         const OnStream on(a[8], in.l);
         const int kind = integer(a[4], "kind"), block = integer(a[5], "block");
         const at::ScalarType type = kind == RED_QUANT_I8 ? at::kChar : at::kFloat8_e4m3fn;
+        Results made(in.l, in.bytes(), 4);
         at::Tensor q;
         if (a[6] == Py_None) {
-            q = at::empty({in.l.rows, in.l.len}, in.l.x.options().dtype(type));
+            q = made.rows(in.l.rows, in.l.len, in.l.len, type);
         } else {
             q = tensor(a[6], "out");
             if (q.scalar_type() != type || !q.is_cuda() || q.get_device() != in.l.device || q.sizes() != in.l.x.sizes())
                 refuse("out must be of the 8-bit type, on x's device and of x's shape");
         }
+        // (a block that the call refuses has no scales)
         const int64_t blocks = block > 0 ? (in.l.len + block - 1) / block : 1;
-        const at::Tensor scales = at::empty({in.l.rows, blocks}, in.l.x.options().dtype(at::kFloat));
-        in.results(a[7]);
+        const at::Tensor scales = made.rows(block < 32 ? in.l.rows * (block == 0) : in.l.rows, blocks, blocks, at::kFloat);
+        in.results(made, a[7]);
         RETURN_IF_REFUSED(red_rmsnorm_quant(in.l.dtype, in.l.x.data_ptr(), in.l.rows, in.l.len, in.l.ld, in.residual,
                                             in.ldr, in.wtype, in.weight, (float)number(a[3]), kind, block, q.data_ptr(),
                                             Logits::stride(q, "out"), data(scales), in.total_ptr(), in.ldt,
@@ -557,11 +600,13 @@ PyObject *rmsnorm_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
         int wtype;
         const void *weight = norm_weight(l, a[3], &wtype);
         const void *dtotal = a[4] == Py_None ? nullptr : beside(l, a[4], "dtotal", &ldt).data_ptr();
-        const at::Tensor dx = a[5] == Py_None ? new_rows(l) : beside(l, a[5], "grad", &ldd);
+        Results made(l, l.rows * l.ld * (int64_t)l.x.element_size() + 4 * l.len, 2);
+        const at::Tensor dx = a[5] == Py_None ? made.rows(l.rows, l.len, l.ld, l.x.scalar_type())
+                                              : beside(l, a[5], "grad", &ldd);
         at::Tensor dw;
         if (a[6] == Py_None) {
             if (weight)
-                dw = at::empty({l.len}, tensor(a[3], "weight").options());
+                dw = made.vector(l.len, tensor(a[3], "weight").scalar_type());
         } else if (a[6] != Py_False) {
             dw = tensor(a[6], "grad_weight");
             if (dw.scalar_type() != (weight ? tensor(a[3], "weight") : l.x).scalar_type() || !dw.is_cuda() ||
@@ -596,14 +641,20 @@ PyObject *balance(PyObject *, PyObject *const *a, Py_ssize_t n)
                 refuse("live must be a contiguous vector of one bool or uint8 per row on x's device");
             live = static_cast<const uint8_t *>(t.data_ptr());
         }
-        const Gradient g(a[7], l, "grad");
-        const at::Tensor counts = at::empty({l.len}, l.x.options().dtype(at::kLong));
-        const auto [prob, stats] = float_vectors(l, {l.len, 4});
+        Results made(l, l.rows * l.ld * (int64_t)l.x.element_size() + 12 * l.len + 16, 4);
+        at::Tensor dx;
+        int64_t ldd = l.ld;
+        if (a[7] == Py_None)
+            dx = made.rows(l.rows, l.len, l.ld, l.x.scalar_type());
+        else if (a[7] != Py_False)
+            dx = beside(l, a[7], "grad", &ldd);
+        const at::Tensor counts = made.vector(l.len, at::kLong), prob = made.vector(l.len, at::kFloat),
+                         stats = made.vector(4, at::kFloat);
         RETURN_IF_REFUSED(red_balance(l.dtype, l.x.data_ptr(), l.rows, l.len, l.ld, id, k, live,
                                       integer(a[5], "kind"), (float)number(a[3]), (float)number(a[4]),
                                       (float)number(a[6]), static_cast<int64_t *>(counts.data_ptr()), data(prob),
-                                      data(stats), g.ptr, g.ld, on.stream));
-        return results(counts, prob, stats, g.t);
+                                      data(stats), dx.defined() ? dx.data_ptr() : nullptr, ldd, on.stream));
+        return results(counts, prob, stats, dx);
     });
 }
 

@@ -65,7 +65,7 @@ def test_gradients(example, rows):
     losses, grads, ids = example.step(model, tokens, target)
     want, exact = definition(example, model, tokens, target, ids)
     for got, w in zip(losses.tolist(), want):
-        assert abs(got - float(w)) <= 8 * 2.0 ** -8 * abs(float(w))
+        assert abs(got - w.item()) <= 8 * 2.0 ** -8 * abs(w.item())
     for name, w in exact.items():
         off = float((grads[name].double() - w).norm() / w.norm())
         assert off <= 8 * 2.0 ** -8, f"{name}: {off}"
