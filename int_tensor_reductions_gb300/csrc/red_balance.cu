@@ -20,9 +20,13 @@
 namespace red {
 namespace {
 
-// Workspace: counters of the experts and of the tokens (zero between calls) and a
-// ticket; sums per CTA.
-__device__ __forceinline__ unsigned *ticket_of(unsigned *tick) { return tick + RED_BALANCE_MAX_EXPERTS + 1; }
+// Workspace: counters of the experts and of the tokens (zero between calls), the number of
+// tokens for the join, and the CTAs' sums: of p for each expert, of lse^2, of count_e p_te.
+__device__ __forceinline__ unsigned *tokens_seen(const BalanceArgs &a) { return reinterpret_cast<unsigned *>(a.part); }
+__device__ __forceinline__ float *sums_at(const BalanceArgs &a, int64_t cta)
+{
+    return a.part + 4 + cta * (a.experts + 2);
+}
 
 constexpr int COUNT_NT = 1024;
 
@@ -61,7 +65,10 @@ __device__ __forceinline__ void count_ids(const BalanceArgs &a, unsigned *counts
 
 __global__ void __launch_bounds__(COUNT_NT) balance_count_kernel(const BalanceArgs a)
 {
-    pdl_enter();
+    // The rows kernel may come once what precedes this call is done: its first rows are
+    // on their way while the ids are counted.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     extern __shared__ unsigned counts[];  // experts, tokens
     for (int e = threadIdx.x; e <= a.experts; e += COUNT_NT)
         counts[e] = 0;
@@ -73,11 +80,12 @@ __global__ void __launch_bounds__(COUNT_NT) balance_count_kernel(const BalanceAr
             atomicAdd(a.tick + (e < a.experts ? e : RED_BALANCE_MAX_EXPERTS), counts[e]);
 }
 
-// A lane's share of what the rows need: c_e (in units of grad_scale), and its sums.
+// A lane's share of the counts, and its sums over rows.
 template <int N, int E>
 struct RowSums {
     float c[N][E], p[N][E];
-    float z;
+    float z, d;    // of lse^2, and of the tokens' sums of count_e p_te
+    float unit;    // of count_e in the gradient
 };
 
 __device__ __forceinline__ bool takes_part(const BalanceArgs &a, int64_t r)
@@ -89,16 +97,16 @@ __device__ __forceinline__ float tokens_of(unsigned n) { return (float)(n ? n : 
 template <int LANES, int N, int E>
 __device__ __forceinline__ void begin_sums(const BalanceArgs &a, RowSums<N, E> &s, const unsigned *counts, float n, int lane)
 {
-    const float unit = a.coef * a.grad_scale * (float)a.experts / ((float)a.k * n * n);
+    s.unit = a.coef * a.grad_scale * (float)a.experts / ((float)a.k * n * n);
 #pragma unroll
     for (int v = 0; v < N; ++v)
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             const int e = (v * LANES + lane) * E + k;
-            s.c[v][k] = e < a.experts ? (float)counts[e] * unit : 0.0f;
+            s.c[v][k] = e < a.experts ? (float)counts[e] : 0.0f;
             s.p[v][k] = 0.0f;
         }
-    s.z = 0.0f;
+    s.z = s.d = 0.0f;
 }
 
 // One token's logits: its probabilities into the sums, its gradient to memory.
@@ -126,12 +134,14 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
                 top = Max()(top, x[v][k]);
         }
     }
-    float sum = 0.0f, off = 0.0f;  // (differences first: a row of the type's lowest value has no room for a product)
+    float off = 0.0f;  // (differences first: a row of the type's lowest value has no room for a product)
     float e[N][E];  // exponentials, or sigmoids
     if constexpr (!SIGMOID) {
         top = group_fold<LANES>(top, sh, turn, Max());
         off = top == NEG_INF ? 0.0f : top;
     }
+    // sum of e and of e * c, for sum of p * c
+    float2 sums = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int v = 0; v < N; ++v)
 #pragma unroll
@@ -139,17 +149,20 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
             e[v][k] = SIGMOID ? __fdividef(1.0f, 1.0f + ex2(-x[v][k] * LOG2E)) : ex2((x[v][k] - off) * LOG2E);
             if (SIGMOID && x[v][k] == NEG_INF)
                 e[v][k] = 0.0f;
-            sum += e[v][k];
+            sums.x += e[v][k];
+            sums.y = fmaf(e[v][k], s.c[v][k], sums.y);
         }
-    sum = group_fold<LANES>(sum, sh, turn, Add());
+    sums = group_sums<LANES>(sums, sh, turn);
+    float sum = sums.x;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // nothing but -inf: no probabilities
+    float d = sums.y * inv;
     if (!takes) {  // (its results so far are not looked at: they may be NaN)
 #pragma unroll
         for (int v = 0; v < N; ++v)
 #pragma unroll
             for (int k = 0; k < E; ++k)
                 x[v][k] = e[v][k] = 0.0f;
-        sum = 0.0f;
+        sum = d = 0.0f;
     } else {
 #pragma unroll
         for (int v = 0; v < N; ++v)
@@ -157,14 +170,12 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
             for (int k = 0; k < E; ++k)
                 x[v][k] = e[v][k] * inv;
     }
-    float d = 0.0f;
 #pragma unroll
     for (int v = 0; v < N; ++v)
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
+        for (int k = 0; k < E; ++k)
             s.p[v][k] += x[v][k];
-            d = fmaf(x[v][k], s.c[v][k], d);
-        }
+    s.d += d;
     float by_lse = 0.0f;
     if constexpr (!SIGMOID) {
         const float lse = sum == 0.0f ? 0.0f : fmaf(log2f(sum), 0.6931471805599453f, off);
@@ -173,15 +184,14 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
     }
     if (!a.dx)
         return;
-    d = group_fold<LANES>(d, sh, turn, Add());
-    const float shift = by_lse - d;
+    const float shift = by_lse - d * s.unit;
 #pragma unroll
     for (int v = 0; v < N; ++v) {
         float g[E];
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             const float p = x[v][k];
-            g[k] = SIGMOID ? p * (1.0f - e[v][k]) * (s.c[v][k] - d) : p * (s.c[v][k] + shift);
+            g[k] = (SIGMOID ? p * (1.0f - e[v][k]) : p) * fmaf(s.c[v][k], s.unit, shift);
         }
         store_unit<DT, VEC, LANES>(a.dx, r * a.ldd, (v * LANES + lane) * E, a.experts, here, g);
     }
@@ -190,7 +200,7 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
 // The groups' sums of a CTA in `meet` (a row of LANES * VECS * 8 per warp, or per
 // CTA), ready for sum_of().
 template <int LANES, int N, int E>
-__device__ __forceinline__ void meet_sums(RowSums<N, E> &s, float *meet, float *meet_z, int lane)
+__device__ __forceinline__ void meet_sums(RowSums<N, E> &s, float *meet, float2 *meet_zd, int lane)
 {
     constexpr int WIDTH = LANES * N * E;
     float *const row = LANES > 32 ? meet : meet + threadIdx.x / 32 * WIDTH;
@@ -203,6 +213,7 @@ __device__ __forceinline__ void meet_sums(RowSums<N, E> &s, float *meet, float *
                 for (int k = 0; k < E; ++k)
                     s.p[v][k] += __shfl_xor_sync(0xffffffffu, s.p[v][k], o);
             s.z += __shfl_xor_sync(0xffffffffu, s.z, o);
+            s.d += __shfl_xor_sync(0xffffffffu, s.d, o);
         }
     }
     if (LANES > 32 || threadIdx.x % 32 < LANES) {
@@ -213,7 +224,7 @@ __device__ __forceinline__ void meet_sums(RowSums<N, E> &s, float *meet, float *
                 row[(v * LANES + lane) * E + k] = s.p[v][k];
     }
     if (LANES > 32 ? threadIdx.x == 0 : threadIdx.x % 32 == 0)
-        meet_z[LANES > 32 ? 0 : threadIdx.x / 32] = s.z;
+        meet_zd[LANES > 32 ? 0 : threadIdx.x / 32] = make_float2(s.z, s.d);
     __syncthreads();
 }
 template <int LANES, int VECS, int NT>
@@ -228,24 +239,26 @@ __device__ __forceinline__ float sum_of(const float *meet, int e)
     return p;
 }
 template <int LANES, int NT>
-__device__ __forceinline__ float sum_of_z(const float *meet_z)
+__device__ __forceinline__ float2 sum_of_zd(const float2 *meet_zd)
 {
-    float z = meet_z[0];
+    float2 s = meet_zd[0];
     if constexpr (LANES <= 32) {
 #pragma unroll
-        for (int w = 1; w < NT / 32; ++w)
-            z += meet_z[w];
+        for (int w = 1; w < NT / 32; ++w) {
+            s.x += meet_zd[w].x;
+            s.y += meet_zd[w].y;
+        }
     }
-    return z;
+    return s;
 }
 
 template <int DT, bool SIGMOID, int LANES, int VECS, bool VEC>
 __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const BalanceArgs a)
 {
-    pdl_enter();
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES, N = UNITS<DT, VECS>, E = UNIT<DT>;
     __shared__ GroupShared<LANES> sh;
-    __shared__ float meet[(LANES > 32 ? 1 : NT / 32) * LANES * VECS * 8], meet_z[NT / 32];
+    __shared__ float meet[(LANES > 32 ? 1 : NT / 32) * LANES * VECS * 8];
+    __shared__ float2 meet_zd[NT / 32];
     using Rows = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 1>;
     extern __shared__ __align__(16) unsigned char ring[];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
@@ -258,6 +271,7 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const Ba
 #pragma unroll
     for (int k = 0; k < Rows::STAGES - 1; ++k)
         fetch(first + k * step, k);
+    pdl_enter();  // (x is the caller's, complete before the counts began)
     const float n = tokens_of(a.tick[RED_BALANCE_MAX_EXPERTS]);
     RowSums<N, E> s;
     begin_sums<LANES>(a, s, a.tick, n, lane);
@@ -277,12 +291,17 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const Ba
         stage = (stage + 1) % Rows::STAGES;
         balance_row<DT, SIGMOID, LANES, VEC>(a, raw, s, sh, turn, z_unit, r, r < a.rows, takes, lane);
     }
-    meet_sums<LANES>(s, meet, meet_z, lane);
-    float *const part = a.part + (int64_t)blockIdx.x * (a.experts + 1);
+    meet_sums<LANES>(s, meet, meet_zd, lane);
+    float *const part = sums_at(a, blockIdx.x);
     for (int e = threadIdx.x; e < a.experts; e += NT)
         part[e] = sum_of<LANES, VECS, NT>(meet, e);
-    if (threadIdx.x == 0)
-        part[a.experts] = sum_of_z<LANES, NT>(meet_z);
+    if (threadIdx.x == 0) {
+        const float2 zd = sum_of_zd<LANES, NT>(meet_zd);
+        part[a.experts] = zd.x;
+        part[a.experts + 1] = zd.y;
+        if (blockIdx.x == 0)
+            *tokens_seen(a) = a.tick[RED_BALANCE_MAX_EXPERTS];
+    }
 }
 
 // loss, its two parts and the tokens, from sum_e count_e * (sum of p_e) and the sum of lse^2.
@@ -297,67 +316,48 @@ __device__ __forceinline__ void write_stats(const BalanceArgs &a, unsigned token
     a.stats[3] = (float)tokens;
 }
 
-// Eight experts per CTA by 128 lanes of parts (65536 x 64 bf16, 760 parts: with 32 by 32 the join took 7.5 us, as
-// it is 6.6); the last CTA does the totals and clears the counters.
+// Eight columns of the CTAs' sums per CTA by 128 lanes of CTAs.  Each clears the counters
+// that it has read; that of the tokens has been read by then, and is `seen` besides.
 constexpr int JOIN_NT = 1024, JOIN_WIDTH = 8;
 __global__ void __launch_bounds__(JOIN_NT) balance_join_kernel(const BalanceArgs a, int parts)
 {
     pdl_enter();
     __shared__ float sums[JOIN_NT / 32][JOIN_WIDTH];
-    __shared__ bool last;
-    const int col = threadIdx.x % JOIN_WIDTH, e = blockIdx.x * JOIN_WIDTH + col;
-    const unsigned tokens = a.tick[RED_BALANCE_MAX_EXPERTS];
+    __shared__ float zd[2];
+    // the last two columns are of one CTA
+    const int col = threadIdx.x % JOIN_WIDTH, e = a.experts + 2 - (blockIdx.x + 1) * JOIN_WIDTH + col;
+    const unsigned tokens = *tokens_seen(a);
     float p = 0.0f;
-    if (e <= a.experts) {
+    if (e >= 0) {
 #pragma unroll 8
         for (int i = threadIdx.x / JOIN_WIDTH; i < parts; i += JOIN_NT / JOIN_WIDTH)
-            p += a.part[(int64_t)i * (a.experts + 1) + e];
+            p += sums_at(a, i)[e];
     }
     for (int o = 16; o >= JOIN_WIDTH; o >>= 1)
         p += __shfl_xor_sync(0xffffffffu, p, o);
     if (threadIdx.x % 32 < JOIN_WIDTH)
         sums[threadIdx.x / 32][col] = p;
     __syncthreads();
-    float *const terms = a.part + (int64_t)parts * (a.experts + 1);  // one per expert, and the sum of lse^2
-    if (threadIdx.x < JOIN_WIDTH && e <= a.experts) {
+    if (threadIdx.x < JOIN_WIDTH && e >= 0) {
         p = 0.0f;
 #pragma unroll
         for (int w = 0; w < JOIN_NT / 32; ++w)
             p += sums[w][col];
         if (e < a.experts) {
-            const unsigned count = a.tick[e];
-            a.counts[e] = count;
+            a.counts[e] = a.tick[e];
+            a.tick[e] = 0;
             a.prob[e] = p / tokens_of(tokens);
-            terms[e] = (float)count * p;
         } else {
-            terms[e] = p;
+            zd[e - a.experts] = p;
         }
-        __threadfence();
     }
-    __syncthreads();
-    if (threadIdx.x == 0)
-        last = atomicAdd(ticket_of(a.tick), 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!last)
-        return;
-    __threadfence();
-    float dot = 0.0f;
-    for (int i = threadIdx.x; i < a.experts; i += JOIN_NT)
-        dot += __ldcg(terms + i);
-    for (int o = 16; o; o >>= 1)
-        dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (threadIdx.x % 32 == 0)
-        sums[threadIdx.x / 32][0] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        dot = 0.0f;
-        for (int k = 0; k < JOIN_NT / 32; ++k)
-            dot += sums[k][0];
-        write_stats(a, tokens, dot, __ldcg(terms + a.experts));
-        *ticket_of(a.tick) = 0;
+    if (blockIdx.x == 0) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            a.tick[RED_BALANCE_MAX_EXPERTS] = 0;
+            write_stats(a, tokens, zd[1], zd[0]);
+        }
     }
-    for (int i = threadIdx.x; i <= a.experts; i += JOIN_NT)
-        a.tick[i < a.experts ? i : RED_BALANCE_MAX_EXPERTS] = 0;
 }
 
 // Few tokens: the CTAs of one cluster count, pass over the rows and join, through
@@ -374,8 +374,9 @@ __global__ void __launch_bounds__(FEW_THREADS) balance_few_kernel(const BalanceA
     pdl_enter();
     constexpr int GROUPS = FEW_THREADS / LANES, N = UNITS<DT, 1>, E = UNIT<DT>;
     __shared__ GroupShared<LANES> sh;
-    __shared__ float meet[FEW_THREADS / 32 * LANES * 8], meet_z[FEW_THREADS / 32], dots[FEW_EXPERTS / 32];
-    __shared__ float share[FEW_EXPERTS + 1], sums[FEW_EXPERTS + 1];
+    __shared__ float meet[FEW_THREADS / 32 * LANES * 8];
+    __shared__ float2 meet_zd[FEW_THREADS / 32];
+    __shared__ float share[FEW_EXPERTS + 2], sums[FEW_EXPERTS + 2];
     __shared__ unsigned mine[FEW_EXPERTS + 1], counts[FEW_EXPERTS + 1];  // experts, tokens
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const int ctas = cluster_size(), rank = cluster_rank();
@@ -417,35 +418,26 @@ __global__ void __launch_bounds__(FEW_THREADS) balance_few_kernel(const BalanceA
         load_row<DT, VEC, LANES>(next, a.x, next_takes ? (r + step) * a.ldx : 0, lane, next_takes ? a.experts : 0);
         balance_row<DT, SIGMOID, LANES, VEC>(a, raw, s, sh, turn, z_unit, r, r < a.rows, takes, lane);
     }
-    meet_sums<LANES>(s, meet, meet_z, lane);
+    meet_sums<LANES>(s, meet, meet_zd, lane);
     if (threadIdx.x < a.experts)
         share[threadIdx.x] = sum_of<LANES, 1, FEW_THREADS>(meet, threadIdx.x);
-    if (threadIdx.x == 0)
-        share[a.experts] = sum_of_z<LANES, FEW_THREADS>(meet_z);
+    if (threadIdx.x == 0) {
+        const float2 zd = sum_of_zd<LANES, FEW_THREADS>(meet_zd);
+        share[a.experts] = zd.x;
+        share[a.experts + 1] = zd.y;
+    }
     // every sum to the first CTA
     float *const all = in_cta(sums, 0);
-    cluster_sums(share, a.experts + 1, [&](int e, float sum) { all[e] = sum; });
+    cluster_sums(share, a.experts + 2, [&](int e, float sum) { all[e] = sum; });
     if (rank != 0)
         return;
     __syncthreads();
-    float dot = 0.0f;
     if (threadIdx.x < a.experts) {
-        const float p = sums[threadIdx.x];
         a.counts[threadIdx.x] = counts[threadIdx.x];
-        a.prob[threadIdx.x] = p / n;
-        dot = (float)counts[threadIdx.x] * p;
+        a.prob[threadIdx.x] = sums[threadIdx.x] / n;
     }
-    for (int o = 16; o; o >>= 1)
-        dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (threadIdx.x % 32 == 0 && threadIdx.x < FEW_EXPERTS)
-        dots[threadIdx.x / 32] = dot;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        dot = 0.0f;
-        for (int k = 0; k < FEW_EXPERTS / 32; ++k)
-            dot += dots[k];
-        write_stats(a, tokens, dot, sums[a.experts]);
-    }
+    if (threadIdx.x == 0)
+        write_stats(a, tokens, sums[a.experts + 1], sums[a.experts]);
 }
 
 // One cluster does all of it up to this many logits; a CTA of it has at least this many.
@@ -478,7 +470,7 @@ int launch_rows(BalanceArgs &a, cudaStream_t s)
     auto *const kernel = balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>;
     if (st == RED_OK)
         st = resident_grid(kernel, cache, NT, SMEM, (a.rows + GROUPS - 1) / GROUPS,
-                           (int64_t)(WS_PART_ELEMS / (size_t)(a.experts + 1)) - 1, &grid);
+                           (int64_t)(WS_PART_ELEMS / (size_t)(a.experts + 2)) - 1, &grid);
     if (st != RED_OK)
         return st;
     a.tick = ws.tick;
@@ -491,13 +483,13 @@ int launch_rows(BalanceArgs &a, cudaStream_t s)
         st = cuda_fail(launch_pdl_dynamic(kernel, dim3(grid), dim3(NT), SMEM, s, a),
                        "balance_rows");
     if (st == RED_OK)
-        st = cuda_fail(launch_pdl(balance_join_kernel, dim3((unsigned)(a.experts / JOIN_WIDTH + 1)), dim3(JOIN_NT), s, a,
+        st = cuda_fail(launch_pdl(balance_join_kernel, dim3((unsigned)((a.experts + 1) / JOIN_WIDTH + 1)), dim3(JOIN_NT), s, a,
                                   (int)grid),
                        "balance_join");
     if (st == RED_OK)
         count_launches(3);
     else  // the next call finds the counters as they were
-        cudaMemsetAsync(a.tick, 0, (RED_BALANCE_MAX_EXPERTS + 2) * sizeof(unsigned), s);
+        cudaMemsetAsync(a.tick, 0, (RED_BALANCE_MAX_EXPERTS + 1) * sizeof(unsigned), s);
     return st;
 }
 

@@ -294,7 +294,7 @@ struct Ring {
 
 template <int LANES>
 struct GroupShared {
-    float part[2][LANES / 32];
+    float2 part[2][LANES / 32];
 };
 template <>
 struct GroupShared<8> {
@@ -317,12 +317,38 @@ __device__ __forceinline__ float group_fold(float v, GroupShared<LANES> &sh, int
     if constexpr (LANES > 32) {
         constexpr int WARPS = LANES / 32;
         if (threadIdx.x % 32 == 0)
+            sh.part[turn][threadIdx.x / 32].x = v;
+        __syncthreads();
+        v = sh.part[turn][threadIdx.x % WARPS].x;
+#pragma unroll
+        for (int o = WARPS / 2; o; o >>= 1)
+            v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+        turn ^= 1;
+    }
+    return v;
+}
+
+// Two sums at once: the second costs no latency of its own.
+template <int LANES>
+__device__ __forceinline__ float2 group_sums(float2 v, GroupShared<LANES> &sh, int &turn)
+{
+    auto add = [&](int o) {
+        const float x = __shfl_xor_sync(0xffffffffu, v.x, o), y = __shfl_xor_sync(0xffffffffu, v.y, o);
+        v.x += x;
+        v.y += y;
+    };
+#pragma unroll
+    for (int o = (LANES < 32 ? LANES : 32) / 2; o; o >>= 1)
+        add(o);
+    if constexpr (LANES > 32) {
+        constexpr int WARPS = LANES / 32;
+        if (threadIdx.x % 32 == 0)
             sh.part[turn][threadIdx.x / 32] = v;
         __syncthreads();
         v = sh.part[turn][threadIdx.x % WARPS];
 #pragma unroll
         for (int o = WARPS / 2; o; o >>= 1)
-            v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+            add(o);
         turn ^= 1;
     }
     return v;
