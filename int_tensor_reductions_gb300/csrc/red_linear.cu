@@ -360,6 +360,10 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
             const int target = takes ? a.work.target[row] - col : -1;
             const bool tail = col + HALF > a.vocab;
             float z[HALF];
+            // (the row's coefficients are on their way while the products are)
+            float ct = 0.0f, cp = 0.0f, lse2 = 0.0f;
+            if (GRAD && takes)
+                ct = a.work.by_target[row], cp = a.work.by_p[row], lse2 = a.work.lse2[row];
             const bool ok = take_sums<CHUNK<GRAD>>(z, b, acc, a.k_blocks, (uint32_t)(group * 32) << 16, half, empty);
             constexpr float NOTHING = __builtin_nanf("");
             if constexpr (!GRAD) {
@@ -391,9 +395,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
                     a.work.part[(int64_t)row * a.work.slots + (at.n * 2 + half)] =
                         make_float2(m2, ok ? (l[0] + l[1]) + (l[2] + l[3]) : NOTHING);
             } else {
-                const float ct = takes ? a.work.by_target[row] : 0.0f;
-                const float cp = !ok ? NOTHING : takes ? a.work.by_p[row] : 0.0f;
-                const float lse2 = takes ? a.work.lse2[row] : 0.0f;
+                cp = ok ? cp : NOTHING;
                 const bool here = __any_sync(0xffffffffu, (unsigned)target < (unsigned)HALF);
 #pragma unroll
                 for (int i = 0; i < HALF; ++i)
@@ -817,10 +819,11 @@ struct ProductArgs {
 
 // A warp's 32 rows x 128 columns of a product from tensor memory (`free`: the
 // barrier that gives the accumulators back; 0: there were no products, the sums
-// are 0) to memory, 128 bytes of each row at a time.
+// are 0) to memory, 128 bytes of each row at a time, where they are `wanted` (rows of
+// a tile behind the last one are not).
 template <int DT, bool DH>
 __device__ __forceinline__ void store_product(const ProductArgs &a, bool ok, uint32_t from, uint32_t free, int row,
-                                              int col, float unit, unsigned char *staging, int lane)
+                                              int col, bool wanted, float unit, unsigned char *staging, int lane)
 {
     constexpr int WIDTH = DH ? 32 : 64;
 #pragma unroll
@@ -847,6 +850,8 @@ __device__ __forceinline__ void store_product(const ProductArgs &a, bool ok, uin
             if (lane == 0)
                 arrive_at(free);
         }
+        if (!wanted)
+            continue;
         if (!DH && a.dim % 8 != 0 && col + c < a.dim && col + c + WIDTH > a.dim) {
             // (a map's box ends on 16 bytes, here beyond the row)
             const int64_t r = (int64_t)a.v0 + row + lane;
@@ -974,9 +979,10 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
             const int row = j.a_row + rank * HALF + group * 32, col = j.b_row + half * HALF;
             const uint32_t free = j.blocks == 0 ? 0 : empty[acc.slot];
             if (t < h_tiles)
-                store_product<DT, true>(a, ok, from, free, row + t / h_each * (int)a.work.padded, col, unit, staging, lane);
+                store_product<DT, true>(a, ok, from, free, row + t / h_each * (int)a.work.padded, col, row < live, unit,
+                                        staging, lane);
             else
-                store_product<DT, false>(a, ok, from, free, row, col, unit, staging, lane);
+                store_product<DT, false>(a, ok, from, free, row, col, true, unit, staging, lane);
             if (j.blocks != 0)
                 acc.next();
         }
@@ -988,35 +994,32 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
 }
 
 // The sums of the pieces, and of their splits, to the rows' gradients, rounded once:
-// a thread per eight elements.  Zeros where a row takes no part.
+// a thread per four elements.  Zeros where a row takes no part.
 template <int DT>
 __global__ void __launch_bounds__(256)
     linear_scatter_kernel(const LinearWork w, int64_t rows, int64_t dim, uint16_t *dhidden, int64_t ldd)
 {
     pdl_enter();
     const float unit = w.head->unit;
-    const int64_t vecs = (dim + 7) / 8, split = w.padded * w.dim4;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * vecs; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / vecs, d = (i - r * vecs) * 8;
+    const int64_t quads = w.dim4 / 4, split = w.padded * w.dim4;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * quads; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / quads, d = (i - r * quads) * 4;
         const int at = w.pos[r];
         uint16_t *to = dhidden + r * ldd + d;
-        float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (at >= 0) {
             const float *from = w.dhidden + (int64_t)at * w.dim4 + d;
-            const bool both = d + 4 < dim;
-#pragma unroll 4
+#pragma unroll 8
             for (int s = 0; s < w.splits; ++s) {
-                const float4 lo = *reinterpret_cast<const float4 *>(from + s * split);
-                const float4 hi = both ? *reinterpret_cast<const float4 *>(from + s * split + 4) : make_float4(0, 0, 0, 0);
-                x[0] += lo.x, x[1] += lo.y, x[2] += lo.z, x[3] += lo.w;
-                x[4] += hi.x, x[5] += hi.y, x[6] += hi.z, x[7] += hi.w;
+                const float4 v = *reinterpret_cast<const float4 *>(from + s * split);
+                x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
             }
         }
-        if (d + 8 <= dim) {
-            *reinterpret_cast<uint4 *>(to) = make_uint4(pack2<DT>(x[0] * unit, x[1] * unit), pack2<DT>(x[2] * unit, x[3] * unit),
-                                                        pack2<DT>(x[4] * unit, x[5] * unit), pack2<DT>(x[6] * unit, x[7] * unit));
+        if (d + 4 <= dim) {
+            *reinterpret_cast<uint2 *>(to) =
+                make_uint2(pack2<DT>(x[0] * unit, x[1] * unit), pack2<DT>(x[2] * unit, x[3] * unit));
         } else {
-            for (int k = 0; k < 8 && d + k < dim; ++k)
+            for (int k = 0; k < 4 && d + k < dim; ++k)
                 to[k] = (uint16_t)pack2<DT>(x[k] * unit, 0.0f);
         }
     }
@@ -1234,7 +1237,9 @@ LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, boo
         // pass over the sums of dh too often
         int64_t cols = ((int64_t)1 << 27) / w.padded / TILE * TILE;
         cols = cols < 4096 ? 4096 : cols;
-        w.piece_cols = cols < up(vocab, TILE) && !w.few ? cols : up(vocab, TILE);
+        // (pieces of equal width, half as much again at most: a narrow last one leaves CTAs without work)
+        const int64_t pieces = w.few ? 1 : (2 * vocab + cols) / (2 * cols);
+        w.piece_cols = up((vocab + (pieces > 1 ? pieces : 1) - 1) / (pieces > 1 ? pieces : 1), TILE);
         take(w.by_target, rows * 4);
         take(w.by_p, rows * 4);
         take(w.lse2, rows * 4);
@@ -1342,7 +1347,7 @@ int launch_linear_logprob_grad(const LinearArgs &a, const float *lse, const floa
     }
     if (dhidden) {
         auto *const kernel = a.dtype == RED_BF16 ? linear_scatter_kernel<RED_BF16> : linear_scatter_kernel<RED_F16>;
-        RETURN_IF(cuda_fail(launch_pdl(kernel, dim3(warp_rows_grid(a.rows * up(a.dim, 8) / 8 / 32 + 1)), dim3(256), s, w, a.rows, a.dim,
+        RETURN_IF(cuda_fail(launch_pdl(kernel, dim3(warp_rows_grid(a.rows * w.dim4 / 4 / 32 + 1)), dim3(256), s, w, a.rows, a.dim,
                                        static_cast<uint16_t *>(dhidden), ldd),
                             "linear_scatter"));
         count_launches(1);
