@@ -322,8 +322,9 @@ __device__ __forceinline__ void write_share(const NormGradArgs &a, int i, float 
         a.part[(int64_t)blockIdx.x * a.len + i] = v;
 }
 
+// (128 registers where shared memory has room for two CTAs: with 132, and one CTA, 16384 x 8192 bf16 177 us, 161 so.)
 template <int DT, bool WIDE, int LANES, int VECS, bool VEC>
-__global__ void __launch_bounds__(GROUP_CTA<LANES>) rmsnorm_grad_kernel(const NormGradArgs a)
+__global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VECS == 4 && VEC ? 2 : 0) rmsnorm_grad_kernel(const NormGradArgs a)
 {
     pdl_enter();
     __shared__ GroupShared<LANES> sh;
