@@ -106,7 +106,8 @@ enum red_dtype {
  * CTA (the last-block stages count arrivals and the last arrival does the
  * fold).  The losses over logits wait for the CTAs of their own cluster, at
  * the hardware's barrier, and inside a CTA for its own bulk copies, with a
- * limit: what its CTA has not written when such a wait runs out becomes NaN. */
+ * limit: what its CTA has not written when such a wait runs out becomes NaN.
+ * The products of red_linear_logprob wait inside a pair of CTAs the same way. */
 enum red_status { RED_OK = 0, RED_EINVAL = -1, RED_ECUDA = -2, RED_ENOMEM = -3 };
 
 /* Grid stage of red_full (how the per-CTA partials become one scalar). */
@@ -504,10 +505,11 @@ int red_linear_logprob(int dtype, const void *hidden, int64_t rows, int64_t dim,
  *     dhidden = g * weight,  dweight = g^T * hidden,
  * with p_j = e^(z[r, j] - lse[r]), lse as red_linear_logprob left it.  A row
  * whose dlogp and dlse are both 0 is ignored, too.  The vocabulary is taken in
- * pieces; g is rounded to dtype once, in units that the largest
- * coefficient sets, and each result once more; their sums are fp32.
+ * pieces; g is rounded to dtype once, in units that the largest coefficient
+ * sets, and each result once more; their sums are fp32.
  *   dhidden  rows x dim, row stride ldd, or NULL for none.  May be `hidden`.
- *   dweight  vocab x dim, row stride lddw, or NULL for none (not both).
+ *   dweight  vocab x dim, row stride lddw, or NULL for none (not both).  Results
+ *            must not overlap an input otherwise, nor each other.
  *   work     red_linear_work_bytes(..., 1) bytes.
  */
 int red_linear_logprob_grad(int dtype, const void *hidden, int64_t rows, int64_t dim, int64_t ldh,

@@ -261,11 +261,12 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const Ba
     __shared__ float2 meet_zd[NT / 32];
     using Rows = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 1>;
     extern __shared__ __align__(16) unsigned char ring[];
+    const Rows rows = {ring, 1};
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const int64_t step = (int64_t)gridDim.x * GROUPS, first = (int64_t)blockIdx.x * GROUPS + group;
     auto fetch = [&](int64_t r, int to) {
         if (r < a.rows)  // (one that is out is fetched, too: what says so is not known yet)
-            Rows::fetch(ring, to, 0, a.x, r * a.ldx, lane, a.experts);
+            rows.fetch(to, 0, a.x, r * a.ldx, lane, a.experts);
         fetch_commit();
     };
 #pragma unroll
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>) balance_rows_kernel(const Ba
         fetch_wait<Rows::STAGES - 1>();
 #pragma unroll
         for (int v = 0; v < N; ++v)
-            raw[v] = Rows::take(ring, stage, 0, v, a.x, r * a.ldx, lane, a.experts);
+            raw[v] = rows.take(stage, 0, v, a.x, r * a.ldx, lane, a.experts);
         stage = (stage + 1) % Rows::STAGES;
         balance_row<DT, SIGMOID, LANES, VEC>(a, raw, s, sh, turn, z_unit, r, r < a.rows, takes, lane);
     }
@@ -465,11 +466,11 @@ int launch_rows(BalanceArgs &a, cudaStream_t s)
     Workspace ws;
     if (st == RED_OK)
         st = get_workspace(&ws);
-    constexpr size_t SMEM = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 1>::BYTES;
+    constexpr size_t SMEM = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 1>::bytes(1);
     unsigned grid = 1;
     auto *const kernel = balance_rows_kernel<DT, SIGMOID, LANES, VECS, VEC>;
     if (st == RED_OK)
-        st = resident_grid(kernel, cache, NT, SMEM, (a.rows + GROUPS - 1) / GROUPS,
+        st = resident_grid(kernel, cache, NT, SMEM, SMEM, (a.rows + GROUPS - 1) / GROUPS,
                            (int64_t)(WS_PART_ELEMS / (size_t)(a.experts + 2)) - 1, &grid);
     if (st != RED_OK)
         return st;

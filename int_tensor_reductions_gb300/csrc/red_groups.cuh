@@ -230,25 +230,28 @@ __device__ __forceinline__ void fetch_wait()
 }
 
 // A ring of rows in shared memory, fetched while earlier rows are at work: each
-// thread fetches its own units of ARRAYS matrices and reads them back itself, so
-// that no barrier is needed.  Of rows off the 16-byte blocks (VEC false) it fetches the
+// thread fetches its own units of up to MOST matrices (`arrays` of them in a call: what one
+// does without leaves room for another CTA) and reads them back itself, so that no
+// barrier is needed.  Of rows off the 16-byte blocks (VEC false) it fetches the
 // two blocks that a unit lies in.
-template <int DT, bool VEC, int LANES, int N, int ARRAYS>
+template <int DT, bool VEC, int LANES, int N, int MOST>
 struct Ring {
     static constexpr int NT = GROUP_CTA<LANES>, E = UNIT<DT>, SIZE = 16 / E, BLOCKS = VEC ? 1 : 2;
-    static constexpr int STAGE = ARRAYS * N * BLOCKS * NT * 16;
+    static constexpr int ARRAY = N * BLOCKS * NT * 16, STAGE = MOST * ARRAY;
     // one row at work, one on its way; more are no use (norm 30000 x 512 bf16 with four 18.4 us, with two 17.3)
     static constexpr int STAGES = 2 * STAGE <= 204800 ? 2 : 1;
     // the longest fp32 rows off the blocks do not fit: they are loaded where they are wanted
     static constexpr bool LATE = STAGE > 212992;
-    static constexpr size_t BYTES = LATE ? 0 : (size_t)STAGE * STAGES;
+    static constexpr size_t bytes(int arrays) { return LATE ? 0 : (size_t)ARRAY * arrays * STAGES; }
 
-    static __device__ __forceinline__ uint4 *slot(unsigned char *ring, int stage, int array, int u)
+    unsigned char *ring;
+    int arrays;
+
+    __device__ __forceinline__ uint4 *slot(int stage, int array, int u) const
     {
-        return reinterpret_cast<uint4 *>(ring) + ((stage * ARRAYS + array) * N + u) * BLOCKS * NT + threadIdx.x;
+        return reinterpret_cast<uint4 *>(ring) + ((stage * arrays + array) * N + u) * BLOCKS * NT + threadIdx.x;
     }
-    static __device__ __forceinline__ void fetch(unsigned char *ring, int stage, int array, const void *p, int64_t row,
-                                                 int lane, int len)
+    __device__ __forceinline__ void fetch(int stage, int array, const void *p, int64_t row, int lane, int len) const
     {
         if (LATE)
             return;
@@ -257,7 +260,7 @@ struct Ring {
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const int i = (u * LANES + lane) * E;
-            uint4 *const to = slot(ring, stage, array, u);
+            uint4 *const to = slot(stage, array, u);
             if constexpr (VEC) {
                 const int left = (len - i) * SIZE;
                 const uint32_t bytes = left <= 0 ? 0 : left < 16 ? left : 16;
@@ -271,10 +274,9 @@ struct Ring {
         }
     }
     // `row` and `len` as they were fetched; `lane`'s unit u.
-    static __device__ __forceinline__ Raw take(unsigned char *ring, int stage, int array, int u, const void *p, int64_t row,
-                                               int lane, int len)
+    __device__ __forceinline__ Raw take(int stage, int array, int u, const void *p, int64_t row, int lane, int len) const
     {
-        const uint4 *const from = slot(ring, stage, array, u);
+        const uint4 *const from = slot(stage, array, u);
         if constexpr (LATE) {
             Raw r[1];
             load_row<DT, VEC, 1>(r, p, row + (u * LANES + lane) * E, 0, len - (u * LANES + lane) * E);
@@ -429,14 +431,17 @@ inline bool aligned_rows(const void *p, int64_t ld, int64_t rows, int elem)
     return !p || ((uintptr_t)p % 16 == 0 && (rows < 2 || ld * elem % 16 == 0));
 }
 
-// CTAs per SM of a kernel, per device.
+// CTAs per SM of a kernel with one size of dynamic shared memory, per device.
 struct Resident {
     std::atomic<int> per_sm[64] = {};
 };
 
 // CTAs of a persistent grid: what is resident at once, or what there is to do; at most `most`.
+// `smem_most`: the most dynamic shared memory of any call of the kernel (its leave is the
+// kernel's, not the call's).
 template <class K>
-int resident_grid(K kernel, Resident &cache, int threads, size_t smem, int64_t ctas, int64_t most, unsigned *grid)
+int resident_grid(K kernel, Resident &cache, int threads, size_t smem, size_t smem_most, int64_t ctas, int64_t most,
+                  unsigned *grid)
 {
     DeviceInfo di;
     const int st = device_info(&di);
@@ -445,8 +450,8 @@ int resident_grid(K kernel, Resident &cache, int threads, size_t smem, int64_t c
     int per_sm = cache.per_sm[di.dev].load(std::memory_order_relaxed);
     if (per_sm == 0) {
         cudaError_t e = cudaSuccess;
-        if (smem > 0)
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (smem_most > 0)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_most);
         if (e == cudaSuccess)
             e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, (const void *)kernel, threads, smem);
         if (e != cudaSuccess)

@@ -224,9 +224,9 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const void *hidden, in
         pack_row(hidden, dim, ldh, w, r, r < live ? w.idx[r] : -1, threadIdx.x % 32);
 }
 
-// Both for few rows, in one launch: every CTA does the scan for itself, and packs
-// eight rows.
-constexpr int GATHER_ROWS = 1024;
+// Both for up to a few thousand rows, in one launch: every CTA does the scan for itself,
+// and packs eight rows.
+constexpr int GATHER_ROWS = 4096;
 template <bool GRAD>
 __global__ void __launch_bounds__(256) linear_gather_kernel(const ScanArgs a, const void *hidden, int64_t dim, int64_t ldh)
 {
@@ -522,6 +522,12 @@ __global__ void __launch_bounds__(256)
 // to 5.7 TB/s where one stream of all rows comes at 6.5.
 constexpr int FEW_ROWS = 128, FEW_THREADS = 256, FEW_MAX_CTAS = 512;
 
+// As CHUNK; the forward waits for memory anyway, and the likelihood of a token that is
+// all but certain hangs on the errors of the others' logits (1 x 2048 x 65536: logp off by
+// 2.3e-6 of itself with 8 blocks).
+template <bool GRAD>
+constexpr int FEW_CHUNK = GRAD ? 16 : 2;
+
 template <int ROWS>
 struct Few {
     static constexpr int STAGE = OPERAND_BYTES + ROWS * BLOCK_K * 2;
@@ -654,14 +660,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
         bool ok = true;
         const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true, HALF, ROWS);
         for (int v = begin; v < end && ok; v += a.height)
-            for (int k0 = 0; k0 < a.k_blocks && ok; k0 += CHUNK<GRAD>) {
+            for (int k0 = 0; k0 < a.k_blocks && ok; k0 += FEW_CHUNK<GRAD>) {
                 if (!mbar_wait(&b.acc_empty[acc.slot], acc.phase ^ 1, &b.failed, 0)) {
                     ok = false;
                     break;
                 }
                 tmem_after();
                 const uint32_t d = b.tmem + acc.slot * ROWS;
-                for (int k = k0; k < min(k0 + CHUNK<GRAD>, a.k_blocks); ++k) {
+                for (int k = k0; k < min(k0 + FEW_CHUNK<GRAD>, a.k_blocks); ++k) {
                     if (!mbar_wait(&b.full[pos.stage], pos.phase, &b.failed, 0)) {
                         ok = false;
                         break;
@@ -698,7 +704,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
             const bool valid = v < stop;
             float z[ROWS];
             bool ok = true;
-            for (int k = 0; k < a.k_blocks; k += CHUNK<GRAD>) {
+            for (int k = 0; k < a.k_blocks; k += FEW_CHUNK<GRAD>) {
                 ok &= mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
                 tmem_after();
                 const uint32_t from = b.tmem + ((uint32_t)(part * 32) << 16) + acc.slot * ROWS;

@@ -192,14 +192,15 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VECS == 2 &&
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES, N = UNITS<DT, VECS>, E = UNIT<DT>;
     using Rows = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 2>;
     extern __shared__ __align__(16) unsigned char ring[];
+    const Rows rows = {ring, a.residual ? 2 : 1};
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const int64_t step = (int64_t)gridDim.x * GROUPS, first = (int64_t)blockIdx.x * GROUPS + group;
     int turn = 0, stage = 0;
     auto fetch = [&](int64_t r, int to) {
         if (r < a.rows) {
-            Rows::fetch(ring, to, 0, a.x, r * a.ldx, lane, a.len);
+            rows.fetch(to, 0, a.x, r * a.ldx, lane, a.len);
             if (a.residual)
-                Rows::fetch(ring, to, 1, a.residual, r * a.ldr, lane, a.len);
+                rows.fetch(to, 1, a.residual, r * a.ldr, lane, a.len);
         }
         fetch_commit();
     };
@@ -219,9 +220,9 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VECS == 2 &&
             fetch_wait<Rows::STAGES - 1>();
 #pragma unroll
             for (int v = 0; v < N; ++v) {
-                raw[v] = Rows::take(ring, stage, 0, v, a.x, r * a.ldx, lane, a.len);
+                raw[v] = rows.take(stage, 0, v, a.x, r * a.ldx, lane, a.len);
                 if (a.residual)
-                    res[v] = Rows::take(ring, stage, 1, v, a.residual, r * a.ldr, lane, a.len);
+                    res[v] = rows.take(stage, 1, v, a.residual, r * a.ldr, lane, a.len);
             }
             stage = (stage + 1) % Rows::STAGES;
         } else {
@@ -333,15 +334,16 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VECS == 4 &&
     __shared__ float meet[GROUPS > 1 ? NT / 32 * N * LANES * E : 1];
     using Rows = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 3>;
     extern __shared__ __align__(16) unsigned char ring[];
+    const Rows rows = {ring, a.dtotal ? 3 : 2};
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
     const int64_t step = (int64_t)gridDim.x * GROUPS, first = (int64_t)blockIdx.x * GROUPS + group;
     int turn = 0, stage = 0;
     auto fetch = [&](int64_t r, int to) {
         if (r < a.rows) {
-            Rows::fetch(ring, to, 0, a.x, r * a.ldx, lane, a.len);
-            Rows::fetch(ring, to, 1, a.dy, r * a.ldy, lane, a.len);
+            rows.fetch(to, 0, a.x, r * a.ldx, lane, a.len);
+            rows.fetch(to, 1, a.dy, r * a.ldy, lane, a.len);
             if (a.dtotal)
-                Rows::fetch(ring, to, 2, a.dtotal, r * a.ldt, lane, a.len);
+                rows.fetch(to, 2, a.dtotal, r * a.ldt, lane, a.len);
         }
         fetch_commit();
     };
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VECS == 4 &&
         fetch(r0 + group + (Rows::STAGES - 1) * step, (stage + Rows::STAGES - 1) % Rows::STAGES);
         fetch_wait<Rows::STAGES - 1>();
         auto take = [&](int array, int v, const void *p, int64_t ld, float (&to)[E]) {
-            widen<DT>(Rows::take(ring, stage, array, v, p, r * ld, lane, a.len), to);
+            widen<DT>(rows.take(stage, array, v, p, r * ld, lane, a.len), to);
         };
         float c = 0.0f;
 #pragma unroll
@@ -472,16 +474,19 @@ __global__ void __launch_bounds__(32 * JOIN_TURNS) rmsnorm_join_kernel(const Nor
 template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC, bool RING>
 int forward(const NormArgs &a, cudaStream_t s)
 {
-    static Resident cache;
+    static Resident caches[2];
+    Resident &cache = caches[a.residual != nullptr];
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
-    constexpr size_t SMEM = RING ? Ring<DT, VEC, LANES, UNITS<DT, VECS>, 2>::BYTES : 0;
+    using Rows = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 2>;
+    const size_t smem = RING ? Rows::bytes(a.residual ? 2 : 1) : 0;
     auto *const kernel = rmsnorm_kernel<DT, WIDE, KIND, LANES, VECS, VEC, RING>;
     unsigned grid;
-    const int st = resident_grid(kernel, cache, NT, SMEM, (a.rows + GROUPS - 1) / GROUPS, INT32_MAX, &grid);
+    const int st = resident_grid(kernel, cache, NT, smem, RING ? Rows::bytes(2) : 0, (a.rows + GROUPS - 1) / GROUPS,
+                                 INT32_MAX, &grid);
     if (st != RED_OK)
         return st;
     count_launches(1);
-    return cuda_fail(launch_pdl_dynamic(kernel, dim3(grid), dim3(NT), SMEM, s, a), "rmsnorm");
+    return cuda_fail(launch_pdl_dynamic(kernel, dim3(grid), dim3(NT), smem, s, a), "rmsnorm");
 }
 
 }  // namespace
@@ -526,12 +531,14 @@ template int rmsnorm_forward<RED_RMSNORM_DT>(const NormArgs &, int, cudaStream_t
 template <int DT, bool WIDE, int LANES, int VECS, bool VEC>
 int backward(NormGradArgs a, cudaStream_t s)
 {
-    static Resident cache;
+    static Resident caches[2];
+    Resident &cache = caches[a.dtotal != nullptr];
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
-    constexpr size_t SMEM = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 3>::BYTES;
+    using Rows = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 3>;
+    const size_t smem = Rows::bytes(a.dtotal ? 3 : 2);
     unsigned grid;
     auto *const kernel = rmsnorm_grad_kernel<DT, WIDE, LANES, VECS, VEC>;
-    int st = resident_grid(kernel, cache, NT, SMEM, (a.rows + GROUPS - 1) / GROUPS,
+    int st = resident_grid(kernel, cache, NT, smem, Rows::bytes(3), (a.rows + GROUPS - 1) / GROUPS,
                            (int64_t)(WS_PART_ELEMS / (size_t)a.len), &grid);
     if (st != RED_OK)
         return st;
@@ -543,7 +550,7 @@ int backward(NormGradArgs a, cudaStream_t s)
             return st;
         a.part = static_cast<float *>(ws.part);
     }
-    st = cuda_fail(launch_pdl_dynamic(kernel, dim3(grid), dim3(NT), SMEM, s, a),
+    st = cuda_fail(launch_pdl_dynamic(kernel, dim3(grid), dim3(NT), smem, s, a),
                    "rmsnorm_grad");
     if (st != RED_OK)
         return st;
