@@ -3,8 +3,9 @@
 // gradients, without the logits z = scale * h w^T ever being in memory.
 //
 //   forward    z tile by tile on the tensor cores; each tile leaves, per row,
-//              its maximum and its sum of exponentials (and the target's z);
-//              a join makes lse and logp of them.
+//              its maximum and its sum of exponentials, without the target's; a
+//              join adds that, from a product of its own in fp32, and makes lse
+//              and logp.
 //   backward   piece by piece of the vocabulary: z again, from it the gradient
 //              by the logits,
 //                  g_j = dlogp ([j = target] - p_j) + dlse p_j,  p_j = e^(z_j - lse),
@@ -27,12 +28,13 @@ namespace {
 
 // Blocks of 64 of K whose products are summed by the tensor cores before the sum
 // moves to fp32 registers.  The tensor cores' additions round toward zero, so a long
-// sum drifts with its number of steps: relative errors of logp (its norm) and times of
-// 6144 x 4096 x 65536 bf16 are, with 8 blocks, 2.9e-7 and 1790 us, with 16, 6.0e-7 and
-// 1725, with 32, 1.2e-6 and 1744 (fp32 products by the plain form: 6e-7).  What
-// becomes of the gradients' logits is rounded to 16 bits.
-template <bool GRAD>
-constexpr int CHUNK = GRAD ? 16 : 8;
+// sum drifts with its number of steps: 6144 x 4096 x 65536 bf16 takes, with 8 blocks,
+// 1790 us, with 16, 1725, with 32, 1744, and the errors of logits double each time.
+// What they would do most harm to is the target's logit: the likelihood of a token that
+// is all but certain is the distance of its logit from the others', and logits at the
+// end of the range drift furthest.  That one is summed apart (target_logit): a
+// reading of N rows of both matrices.
+constexpr int CHUNK = 16;
 // Rows of tiles that are taken in turn along the vocabulary.
 constexpr int BAND = 16;
 
@@ -49,15 +51,48 @@ __device__ __forceinline__ TileAt tile_at(int t, int m_tiles, int n_tiles)
     return {band * BAND + in % high, in / high};
 }
 
+// Sum of the products of two rows (16-byte aligned) over `lanes` lanes: this one's share.
+template <int DT>
+__device__ __forceinline__ float dot_share(const uint16_t *h, const uint16_t *w, int64_t dim, int lane, int lanes)
+{
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t vecs = dim / 8;
+#pragma unroll 4
+    for (int64_t i = lane; i < vecs; i += lanes) {
+        const uint4 x = reinterpret_cast<const uint4 *>(h)[i], y = reinterpret_cast<const uint4 *>(w)[i];
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            s[k] = fmaf(Elem<DT>::widen(u[k] & 0xffffu), Elem<DT>::widen(v[k] & 0xffffu), s[k]);
+            s[k] = fmaf(Elem<DT>::widen(u[k] >> 16), Elem<DT>::widen(v[k] >> 16), s[k]);
+        }
+    }
+    if (lane < dim % 8)
+        s[0] = fmaf(Elem<DT>::widen(h[vecs * 8 + lane]), Elem<DT>::widen(w[vecs * 8 + lane]), s[0]);
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+__device__ __forceinline__ float sum_of_lanes(float v)
+{
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// Row r's hidden state times the weights of `target`, by a warp.
+__device__ __forceinline__ float dot_by_warp(const LinearArgs &a, int64_t r, int64_t target, int lane)
+{
+    const uint16_t *h = static_cast<const uint16_t *>(a.hidden) + r * a.ldh;
+    const uint16_t *w = static_cast<const uint16_t *>(a.weight) + target * a.ldw;
+    return sum_of_lanes(a.dtype == RED_BF16 ? dot_share<RED_BF16>(h, w, a.dim, lane, 32)
+                                            : dot_share<RED_F16>(h, w, a.dim, lane, 32));
+}
+
 // ------------------------------------------------------ rows that take part
 
 constexpr int SCAN_NT = 1024, SCAN_ROWS = 8;
 
 struct ScanArgs {
-    const int64_t *target;
-    int64_t rows, vocab;
+    LinearArgs in;
     const float *lse, *dlogp, *dlse;  // gradients only
-    float scale;
     LinearWork w;
 };
 
@@ -88,30 +123,38 @@ constexpr float MOST = 1.9921875f;
 // By the whole CTA of NT threads; the number of rows that take part.  f(place, row)
 // for each; `writes`: to the workspace.
 template <bool GRAD, int NT, int EACH, class F>
-__device__ __forceinline__ int scan_rows(const ScanArgs &a, int *sums, float *tops, bool writes, F f)
+__device__ __forceinline__ int scan_rows(const ScanArgs &a, int *sums, float *tops, bool writes, float &unit, F f)
 {
     const int tid = threadIdx.x;
-    auto coefs = [&](int64_t r, float &by_target, float &by_p) {
-        const float d = a.dlogp[r], n = a.dlse ? a.dlse[r] : 0.0f;
-        by_target = d * a.scale;
-        by_p = (n - d) * a.scale;
-        return !(d == 0.0f && n == 0.0f);
+    // (what a row needs is loaded at once, whether it takes part or not: one load after the other takes the
+    // latency of each, for every CTA of the gather)
+    struct Row {
+        int64_t target;
+        float d, n;
     };
-    auto live = [&](int64_t r, float &by_target, float &by_p) {
-        if (r >= a.rows)
-            return false;
-        const int64_t t = a.target[r];
-        if (t < 0 || t >= a.vocab)
-            return false;
-        return GRAD ? coefs(r, by_target, by_p) : true;
+    auto load = [&](int64_t r) {
+        Row row = {-1, 0.0f, 0.0f};
+        if (r < a.in.rows) {
+            row.target = a.in.target[r];
+            if constexpr (GRAD) {
+                row.d = a.dlogp[r];
+                row.n = a.dlse ? a.dlse[r] : 0.0f;
+            }
+        }
+        return row;
     };
-    float unit = 1.0f;
+    auto takes_part = [&](const Row &row) {
+        return row.target >= 0 && row.target < a.in.vocab && (!GRAD || !(row.d == 0.0f && row.n == 0.0f));
+    };
+    auto by_p = [&](const Row &row) { return (row.n - row.d) * a.in.scale; };
+    unit = 1.0f;
     if constexpr (GRAD) {
         float top = 0.0f;
-        for (int64_t r = tid; r < a.rows; r += NT) {
-            float x = 0.0f, y = 0.0f;
-            if (live(r, x, y))
-                top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+#pragma unroll 4
+        for (int64_t r = tid; r < a.in.rows; r += NT) {
+            const Row row = load(r);
+            if (takes_part(row))
+                top = fmaxf(top, fmaxf(fabsf(row.d * a.in.scale), fabsf(by_p(row))));
         }
         top = block_fold<NT>(top, tops, [](float x, float y) { return fmaxf(x, y); });
         if (top > 0.0f && top < __builtin_huge_valf())
@@ -119,16 +162,16 @@ __device__ __forceinline__ int scan_rows(const ScanArgs &a, int *sums, float *to
     }
     const float inv = 1.0f / unit;
     int before = 0;
-    for (int64_t r0 = 0; r0 < a.rows; r0 += NT * EACH) {
+    for (int64_t r0 = 0; r0 < a.in.rows; r0 += NT * EACH) {
         const int64_t first = r0 + (int64_t)tid * EACH;
-        float ct[EACH], cp[EACH];
+        Row row[EACH];
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            row[i] = load(first + i);
         unsigned mask = 0;
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            ct[i] = cp[i] = 0.0f;
-            if (live(first + i, ct[i], cp[i]))
-                mask |= 1u << i;
-        }
+        for (int i = 0; i < EACH; ++i)
+            mask |= takes_part(row[i]) ? 1u << i : 0u;
         const int mine = __popc(mask);
         int upto = mine;  // inclusive sum over the block
         for (int o = 1; o < 32; o <<= 1) {
@@ -153,7 +196,7 @@ __device__ __forceinline__ int scan_rows(const ScanArgs &a, int *sums, float *to
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
             const int64_t r = first + i;
-            if (r >= a.rows)
+            if (r >= a.in.rows)
                 break;
             const bool takes = mask >> i & 1;
             if (writes)
@@ -163,10 +206,9 @@ __device__ __forceinline__ int scan_rows(const ScanArgs &a, int *sums, float *to
             f(at, (int)r);
             if (writes) {
                 a.w.idx[at] = (int)r;
-                a.w.target[at] = (int)a.target[r];
+                a.w.target[at] = (int)row[i].target;
                 if constexpr (GRAD) {
-                    a.w.by_target[at] = ct[i] * inv;
-                    a.w.by_p[at] = cp[i] * inv;
+                    a.w.by_p[at] = by_p(row[i]) * inv;
                     a.w.lse2[at] = a.lse[r] * LOG2E;
                 }
             }
@@ -187,7 +229,20 @@ __global__ void __launch_bounds__(SCAN_NT) linear_scan_kernel(const ScanArgs a)
     pdl_enter();
     __shared__ int sums[32];
     __shared__ float tops[32];
-    scan_rows<GRAD, SCAN_NT, SCAN_ROWS>(a, sums, tops, true, [](int, int) {});
+    float unit;
+    scan_rows<GRAD, SCAN_NT, SCAN_ROWS>(a, sums, tops, true, unit, [](int, int) {});
+}
+
+// g at the target of packed row r (`row` of the input), by a warp: from a logit of its own.
+// 1 - p of a token that is all but certain is as exact as lse.
+__device__ __forceinline__ void write_at_target(const ScanArgs &a, int64_t r, int64_t row, float unit, int lane)
+{
+    const float z = dot_by_warp(a.in, row, a.in.target[row], lane);
+    if (lane == 0) {
+        const float d = a.dlogp[row], n = a.dlse ? a.dlse[row] : 0.0f;
+        const float p = expf(fmaf(z, a.in.scale, -a.lse[row]));
+        a.w.at_target[r] = (d + (n - d) * p) * a.in.scale * (1.0f / unit);
+    }
 }
 
 // Row `row` of the hidden states (-1: zeros) to packed row r, by a warp.
@@ -215,20 +270,26 @@ __device__ __forceinline__ void pack_row(const void *hidden, int64_t dim, int64_
 
 // The hidden states of the rows that take part, packed; a warp per row.  Zeros
 // up to a whole tile behind them.
-__global__ void __launch_bounds__(256) linear_pack_kernel(const void *hidden, int64_t dim, int64_t ldh, const LinearWork w)
+template <bool GRAD>
+__global__ void __launch_bounds__(256) linear_pack_kernel(const ScanArgs a)
 {
     pdl_enter();
-    const int live = w.head->live;
+    const int live = a.w.head->live;
     const int64_t end = ((int64_t)live + TILE - 1) / TILE * TILE;
-    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < end; r += (int64_t)gridDim.x * 8)
-        pack_row(hidden, dim, ldh, w, r, r < live ? w.idx[r] : -1, threadIdx.x % 32);
+    const int lane = threadIdx.x % 32;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < end; r += (int64_t)gridDim.x * 8) {
+        const int row = r < live ? a.w.idx[r] : -1;
+        pack_row(a.in.hidden, a.in.dim, a.in.ldh, a.w, r, row, lane);
+        if (GRAD && row >= 0)
+            write_at_target(a, r, row, a.w.head->unit, lane);
+    }
 }
 
 // Both for up to a few thousand rows, in one launch: every CTA does the scan for itself,
 // and packs eight rows.
 constexpr int GATHER_ROWS = 4096;
-template <bool GRAD>
-__global__ void __launch_bounds__(256) linear_gather_kernel(const ScanArgs a, const void *hidden, int64_t dim, int64_t ldh)
+template <bool GRAD, int EACH>
+__global__ void __launch_bounds__(256) linear_gather_kernel(const ScanArgs a)
 {
     pdl_enter();
     __shared__ int sums[32];
@@ -238,14 +299,19 @@ __global__ void __launch_bounds__(256) linear_gather_kernel(const ScanArgs a, co
     const int first_packed = blockIdx.x * 8;
     if (threadIdx.x < 8)
         row_of[threadIdx.x] = -1;
-    const int live = scan_rows<GRAD, 256, GATHER_ROWS / 256>(a, sums, tops, writes, [&](int at, int r) {
+    float unit;
+    const int live = scan_rows<GRAD, 256, EACH>(a, sums, tops, writes, unit, [&](int at, int r) {
         if (at >= first_packed && at < first_packed + 8)
             row_of[at - first_packed] = r;
     });
     __syncthreads();
     const int64_t r = first_packed + threadIdx.x / 32;
-    if (r < (live + TILE - 1) / TILE * TILE)
-        pack_row(hidden, dim, ldh, a.w, r, row_of[threadIdx.x / 32], threadIdx.x % 32);
+    if (r >= (live + TILE - 1) / TILE * TILE)
+        return;
+    const int row = row_of[threadIdx.x / 32];
+    pack_row(a.in.hidden, a.in.dim, a.in.ldh, a.w, r, row, threadIdx.x % 32);
+    if (GRAD && row >= 0)
+        write_at_target(a, r, row, unit, threadIdx.x % 32);
 }
 
 // --------------------------------------------------------------- logit tiles
@@ -262,7 +328,6 @@ struct LogitArgs {
 // the chunks.  Whether they are right: after a wait that ran out they are whatever
 // tensor memory held (and what is made of them has to become NaN; filling them
 // here costs the registers of a second set).
-template <int CHUNK>
 __device__ __forceinline__ bool take_sums(float (&z)[HALF], MmaBarriers &b, AccPos &acc, int blocks, uint32_t lanes,
                                           int half, uint32_t (&empty)[2])
 {
@@ -342,7 +407,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
         AccPos acc;
         const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true);
         for (int t = pair; t < tiles; t += pairs)
-            if (!multiply_tile(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, acc, idesc, CHUNK<GRAD>)) {
+            if (!multiply_tile(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, acc, idesc, CHUNK)) {
                 drain_products(b);
                 break;
             }
@@ -361,10 +426,10 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
             const bool tail = col + HALF > a.vocab;
             float z[HALF];
             // (the row's coefficients are on their way while the products are)
-            float ct = 0.0f, cp = 0.0f, lse2 = 0.0f;
+            float gt = 0.0f, cp = 0.0f, lse2 = 0.0f;
             if (GRAD && takes)
-                ct = a.work.by_target[row], cp = a.work.by_p[row], lse2 = a.work.lse2[row];
-            const bool ok = take_sums<CHUNK<GRAD>>(z, b, acc, a.k_blocks, (uint32_t)(group * 32) << 16, half, empty);
+                gt = a.work.at_target[row], cp = a.work.by_p[row], lse2 = a.work.lse2[row];
+            const bool ok = take_sums(z, b, acc, a.k_blocks, (uint32_t)(group * 32) << 16, half, empty);
             constexpr float NOTHING = __builtin_nanf("");
             if constexpr (!GRAD) {
                 if (tail) {
@@ -374,12 +439,9 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
                             z[i] = NEG_INF;
                 }
                 if (__any_sync(0xffffffffu, (unsigned)target < (unsigned)HALF)) {
-                    float zt = 0.0f;
 #pragma unroll
                     for (int i = 0; i < HALF; ++i)
-                        zt = i == target ? z[i] : zt;
-                    if ((unsigned)target < (unsigned)HALF)
-                        a.work.taken[row] = ok ? zt : NOTHING;
+                        z[i] = i == target ? NEG_INF : z[i];  // (the join adds it)
                 }
                 float m = NEG_INF;
 #pragma unroll
@@ -396,6 +458,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
                         make_float2(m2, ok ? (l[0] + l[1]) + (l[2] + l[3]) : NOTHING);
             } else {
                 cp = ok ? cp : NOTHING;
+                gt = ok ? gt : NOTHING;
                 const bool here = __any_sync(0xffffffffu, (unsigned)target < (unsigned)HALF);
 #pragma unroll
                 for (int i = 0; i < HALF; ++i)
@@ -403,7 +466,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
                 if (here) {
 #pragma unroll
                     for (int i = 0; i < HALF; ++i)
-                        z[i] = i == target ? z[i] + ct : z[i];
+                        z[i] = i == target ? gt : z[i];
                 }
                 if (tail) {
 #pragma unroll
@@ -465,22 +528,23 @@ struct Pair {
 };
 
 template <int LANES>
-__global__ void __launch_bounds__(256) 
-    linear_join_kernel(const LinearWork w, const int64_t *targets, int64_t vocab, int64_t rows, int64_t slots, float s2,
-                       float *logp, float *lse)
+__global__ void __launch_bounds__(256)
+    linear_join_kernel(const LinearArgs a, const LinearWork w, int64_t slots, float s2, float *logp, float *lse)
 {
     pdl_enter();
     __shared__ float2 warps[8];
+    __shared__ float dots[8];
     constexpr int GROUPS = 256 / LANES;
     const int lane = threadIdx.x % LANES;
-    for (int64_t r = (int64_t)blockIdx.x * GROUPS + threadIdx.x / LANES; r < rows; r += (int64_t)gridDim.x * GROUPS) {
-        const int64_t at = !w.few ? w.pos[r] : targets[r] >= 0 && targets[r] < vocab ? r : -1;
-        if (at < 0) {
+    for (int64_t r = (int64_t)blockIdx.x * GROUPS + threadIdx.x / LANES; r < a.rows; r += (int64_t)gridDim.x * GROUPS) {
+        const int64_t target = a.target[r];
+        const bool takes = target >= 0 && target < a.vocab;
+        if (!takes) {  // (a CTA's row is the same for all its threads)
             if (lane == 0)
                 logp[r] = lse[r] = 0.0f;
             continue;
         }
-        const float2 *part = w.part + at * w.slots;
+        const float2 *part = w.part + (w.few ? r : (int64_t)w.pos[r]) * w.slots;
         Pair p = {NEG_INF, 0.0f};
 #pragma unroll 4
         for (int64_t i = lane; i < slots; i += LANES) {
@@ -488,21 +552,44 @@ __global__ void __launch_bounds__(256)
             p.join(o.x, o.y);
         }
         p.join_lanes();
-        if constexpr (LANES > 32) {  // (a CTA's row is the same for all its threads)
+        float z;  // the target's product
+        if constexpr (LANES > 32) {
+            const uint16_t *hr = static_cast<const uint16_t *>(a.hidden) + r * a.ldh;
+            const uint16_t *wr = static_cast<const uint16_t *>(a.weight) + target * a.ldw;
+            z = sum_of_lanes(a.dtype == RED_BF16 ? dot_share<RED_BF16>(hr, wr, a.dim, lane, LANES)
+                                                 : dot_share<RED_F16>(hr, wr, a.dim, lane, LANES));
             __syncthreads();
-            if (lane % 32 == 0)
+            if (lane % 32 == 0) {
                 warps[lane / 32] = make_float2(p.m, p.l);
+                dots[lane / 32] = z;
+            }
             __syncthreads();
             p = {NEG_INF, 0.0f};
             if (lane % 32 < LANES / 32)
                 p = {warps[lane % 32].x, warps[lane % 32].y};
             p.join_lanes();
+            z = 0.0f;
+#pragma unroll
+            for (int k = 0; k < LANES / 32; ++k)
+                z += dots[k];
+        } else {
+            z = dot_by_warp(a, r, target, lane);
         }
         if (lane == 0) {
             constexpr float LN2 = 0.6931471805599453f;
-            const float log_l = log2f(p.l);
-            lse[r] = (p.m + log_l) * LN2;
-            logp[r] = (fmaf(w.taken[at], s2, -p.m) - log_l) * LN2;
+            const float z2 = z * s2, off = z2 - p.m;  // (a NaN goes on; +inf, and only +inf, is one below)
+            float lp, norm;
+            if (off >= 0.0f) {
+                lp = log1pf(p.l * ex2(-off));
+                norm = fmaf(z, a.scale, lp);
+                lp = (z2 - z2) - lp;
+            } else {
+                const float all = logf(p.l + ex2(off));
+                norm = fmaf(p.m, LN2, all);
+                lp = fmaf(off, LN2, -all);
+            }
+            logp[r] = lp;
+            lse[r] = norm + (z2 - z2);
         }
     }
 }
@@ -522,12 +609,6 @@ __global__ void __launch_bounds__(256)
 // to 5.7 TB/s where one stream of all rows comes at 6.5.
 constexpr int FEW_ROWS = 128, FEW_THREADS = 256, FEW_MAX_CTAS = 512;
 
-// As CHUNK; the forward waits for memory anyway, and the likelihood of a token that is
-// all but certain hangs on the errors of the others' logits (1 x 2048 x 65536: logp off by
-// 2.3e-6 of itself with 8 blocks).
-template <bool GRAD>
-constexpr int FEW_CHUNK = GRAD ? 16 : 2;
-
 template <int ROWS>
 struct Few {
     static constexpr int STAGE = OPERAND_BYTES + ROWS * BLOCK_K * 2;
@@ -540,7 +621,7 @@ struct Few {
         int failed;
         float2 stats[4][ROWS];
         int target[ROWS];
-        float4 coefs[ROWS];  // by p, by the target, lse, target (as bits)
+        float4 coefs[ROWS];  // of p, g at the target, lse
     };
 };
 
@@ -619,7 +700,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
             b.target[r] = t >= 0 && t < a.vocab ? (int)t : -1;
         }
         if (GRAD)
-            b.coefs[r] = takes ? make_float4(a.work.by_p[r], a.work.by_target[r], a.work.lse2[r], 0.0f)
+            b.coefs[r] = takes ? make_float4(a.work.by_p[r], a.work.at_target[r], a.work.lse2[r], 0.0f)
                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     tmem_before();
@@ -660,14 +741,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
         bool ok = true;
         const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true, HALF, ROWS);
         for (int v = begin; v < end && ok; v += a.height)
-            for (int k0 = 0; k0 < a.k_blocks && ok; k0 += FEW_CHUNK<GRAD>) {
+            for (int k0 = 0; k0 < a.k_blocks && ok; k0 += CHUNK) {
                 if (!mbar_wait(&b.acc_empty[acc.slot], acc.phase ^ 1, &b.failed, 0)) {
                     ok = false;
                     break;
                 }
                 tmem_after();
                 const uint32_t d = b.tmem + acc.slot * ROWS;
-                for (int k = k0; k < min(k0 + FEW_CHUNK<GRAD>, a.k_blocks); ++k) {
+                for (int k = k0; k < min(k0 + CHUNK, a.k_blocks); ++k) {
                     if (!mbar_wait(&b.full[pos.stage], pos.phase, &b.failed, 0)) {
                         ok = false;
                         break;
@@ -704,7 +785,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
             const bool valid = v < stop;
             float z[ROWS];
             bool ok = true;
-            for (int k = 0; k < a.k_blocks; k += FEW_CHUNK<GRAD>) {
+            for (int k = 0; k < a.k_blocks; k += CHUNK) {
                 ok &= mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
                 tmem_after();
                 const uint32_t from = b.tmem + ((uint32_t)(part * 32) << 16) + acc.slot * ROWS;
@@ -737,16 +818,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
                     // a target among this warp's columns
                     const int t = lane < GROUP ? b.target[g * 32 + lane] - first : -1;
                     unsigned here = __ballot_sync(0xffffffffu, t >= 0 && t < 32 && first + t < stop);
-                    while (here) {
+                    while (here) {  // (the join adds it)
                         const int i = __ffs(here) - 1;
                         here &= here - 1;
-                        float x = 0.0f;
+                        const bool mine = lane == __shfl_sync(0xffffffffu, t, i);
 #pragma unroll
                         for (int j = 0; j < GROUP; ++j)
-                            x = j == i ? z[g * 32 + j] : x;
-                        x = __shfl_sync(0xffffffffu, x, __shfl_sync(0xffffffffu, t, i));
-                        if (lane == 0)
-                            a.work.taken[g * 32 + i] = x + fine;
+                            z[g * 32 + j] = mine && j == i ? NEG_INF : z[g * 32 + j];
                     }
                     float e[GROUP];
                     float top = NEG_INF;  // of row `lane`
@@ -770,9 +848,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float4 c = b.coefs[i + j];
-                        x[j] = fmaf(c.x, ex2(fmaf(z[i + j], a.s2, -c.z)), fine);
-                        if (v == b.target[i + j])
-                            x[j] += c.y;
+                        x[j] = (v == b.target[i + j] ? c.y : c.x * ex2(fmaf(z[i + j], a.s2, -c.z))) + fine;
                     }
                     if (valid)
                         to[i / 8] = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
@@ -1195,16 +1271,15 @@ template <bool GRAD>
 int pack_rows(const LinearArgs &a, const LinearWork &w, const float *lse, const float *dlogp, const float *dlse,
               cudaStream_t s)
 {
-    const ScanArgs scan = {a.target, a.rows, a.vocab, lse, dlogp, dlse, a.scale, w};
+    const ScanArgs scan = {a, lse, dlogp, dlse, w};
     if (a.rows <= GATHER_ROWS) {
         count_launches(1);
-        return cuda_fail(launch_pdl(linear_gather_kernel<GRAD>, dim3((unsigned)(w.padded / 8)), dim3(256), s, scan, a.hidden,
-                                    a.dim, a.ldh),
+        return cuda_fail(launch_pdl(a.rows <= 1024 ? linear_gather_kernel<GRAD, 4> : linear_gather_kernel<GRAD, 16>,
+                                    dim3((unsigned)(w.padded / 8)), dim3(256), s, scan),
                          "linear_gather");
     }
     RETURN_IF(cuda_fail(launch_pdl(linear_scan_kernel<GRAD>, dim3(1), dim3(SCAN_NT), s, scan), "linear_scan"));
-    RETURN_IF(cuda_fail(launch_pdl(linear_pack_kernel, dim3(warp_rows_grid(w.padded)), dim3(256), s, a.hidden, a.dim,
-                                   a.ldh, w),
+    RETURN_IF(cuda_fail(launch_pdl(linear_pack_kernel<GRAD>, dim3(warp_rows_grid(w.padded)), dim3(256), s, scan),
                         "linear_pack"));
     count_launches(2);
     return RED_OK;
@@ -1236,7 +1311,6 @@ LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, boo
     take(h, w.padded * w.ld * 2);
     w.hidden = h;
     if (!grad) {
-        take(w.taken, rows * 4);
         take(w.part, rows * w.slots * 8);
     } else {
         // a piece's gradient by the logits takes 256 MB; pieces narrower than 4096 columns would
@@ -1246,7 +1320,7 @@ LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, boo
         // (pieces of equal width, half as much again at most: a narrow last one leaves CTAs without work)
         const int64_t pieces = w.few ? 1 : (2 * vocab + cols) / (2 * cols);
         w.piece_cols = up((vocab + (pieces > 1 ? pieces : 1) - 1) / (pieces > 1 ? pieces : 1), TILE);
-        take(w.by_target, rows * 4);
+        take(w.at_target, rows * 4);
         take(w.by_p, rows * 4);
         take(w.lse2, rows * 4);
         take(g, (w.few ? w.few : w.padded) * w.piece_cols * 2);
@@ -1291,8 +1365,8 @@ int launch_linear_logprob(const LinearArgs &a, float *logp, float *lse, void *wo
     }
     const bool wide = a.rows <= 2048;
     RETURN_IF(cuda_fail(launch_pdl(wide ? linear_join_kernel<256> : linear_join_kernel<32>,
-                                   dim3(wide ? (unsigned)a.rows : warp_rows_grid(a.rows)), dim3(256), s, w, a.target, a.vocab,
-                                   a.rows, slots, s2, logp, lse),
+                                   dim3(wide ? (unsigned)a.rows : warp_rows_grid(a.rows)), dim3(256), s, a, w, slots, s2,
+                                   logp, lse),
                         "linear_join"));
     count_launches(1);
     return RED_OK;

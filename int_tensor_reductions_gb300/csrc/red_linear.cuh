@@ -24,9 +24,8 @@ struct LinearWork {
     int *idx;           // packed: row
     int *target;        // packed: target
     void *hidden;       // packed hidden states, `padded` rows of `ld` elements, zeros behind the last
-    float *taken;       // packed: the target's product          (forward)
     float2 *part;       // packed x slots: (maximum, sum)         (forward)
-    float *by_target, *by_p, *lse2;  // packed coefficients       (gradients)
+    float *at_target, *by_p, *lse2;  // packed: g at the target, coefficient of p, lse (gradients)
     void *piece;        // padded x piece: gradient by the logits (gradients)
     float *dhidden;     // splits x padded x dim4 sums            (gradients)
     int64_t padded, ld, dim4;
