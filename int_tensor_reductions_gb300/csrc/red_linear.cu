@@ -32,7 +32,7 @@ namespace {
 // 1790 us, with 16, 1725, with 32, 1744, and the errors of logits double each time.
 // What they would do most harm to is the target's logit: the likelihood of a token that
 // is all but certain is the distance of its logit from the others', and logits at the
-// end of the range drift furthest.  That one is summed apart (target_logit): a
+// end of the range drift furthest.  That one is summed apart (dot_by_warp): a
 // reading of N rows of both matrices.
 constexpr int CHUNK = 16;
 // Rows of tiles that are taken in turn along the vocabulary.
@@ -116,8 +116,11 @@ __device__ __forceinline__ V block_fold(V v, V *sh, F f)
 // -(1 - p) of the coefficient, is most of a row's gradient: with equal weights of 1 /
 // 6144, which are 1.33 times a power of two, the errors of dh were 1.53 times those of
 // rounding dh alone with a power of two as the unit, and are 1.15 times those with
-// this.  f16 holds nothing below 6e-8: coefficients of a mean need a unit anyway.
+// this.  In f16 it is 2^13 times that: a probability keeps all its digits down to 4e-9
+// (6e-5 of 1.99 is where f16's steps stop shrinking: an even choice among 262144 was off by
+// 0.4% each), and g, at most twice the largest coefficient, stays off the type's end.
 constexpr float MOST = 1.9921875f;
+__device__ __forceinline__ float most_of(int dtype) { return dtype == RED_F16 ? MOST * 8192.0f : MOST; }
 
 // One CTA: which rows take part and, for the gradients, their coefficients.
 // By the whole CTA of NT threads; the number of rows that take part.  f(place, row)
@@ -158,7 +161,7 @@ __device__ __forceinline__ int scan_rows(const ScanArgs &a, int *sums, float *to
         }
         top = block_fold<NT>(top, tops, [](float x, float y) { return fmaxf(x, y); });
         if (top > 0.0f && top < __builtin_huge_valf())
-            unit = fminf(fmaxf(top, 1e-36f), 1e36f) / MOST;
+            unit = fminf(fmaxf(top, 1e-32f), 1e36f) / most_of(a.in.dtype);
     }
     const float inv = 1.0f / unit;
     int before = 0;
@@ -581,7 +584,7 @@ __global__ void __launch_bounds__(256)
             float lp, norm;
             if (off >= 0.0f) {
                 lp = log1pf(p.l * ex2(-off));
-                norm = fmaf(z, a.scale, lp);
+                norm = fmaf(z, a.scale, lp) + (z2 - z2);
                 lp = (z2 - z2) - lp;
             } else {
                 const float all = logf(p.l + ex2(off));
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(256)
                 lp = fmaf(off, LN2, -all);
             }
             logp[r] = lp;
-            lse[r] = norm + (z2 - z2);
+            lse[r] = norm;
         }
     }
 }
@@ -710,11 +713,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
     const int begin = blockIdx.x * a.tiles * a.height, end = min(begin + a.tiles * a.height, a.vocab);
 
     if (live == 0) {
-        // nothing takes part: no products (gradients of few rows still want their zeros)
-        if (GRAD && warp >= 4)
-            for (int v = begin + threadIdx.x - 128; v < end; v += 128)
-                for (int i = 0; i < ROWS / 8; ++i)
-                    reinterpret_cast<uint4 *>(a.work.piece)[(int64_t)v * (ROWS / 8) + i] = make_uint4(0, 0, 0, 0);
+        // nothing takes part, and nothing reads the piece
     } else if (warp == 0 && lane == 0) {
         RingPos<F::N> pos;
         bool ok = true;

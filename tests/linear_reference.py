@@ -3,7 +3,7 @@ arithmetic may be off by.
 
 Tolerances (u = 2**-24, v = half an eps of the 16-bit type):
   * a logit is a sum of dim products.  The tensor cores add 16 at a time, each
-    step off by at most 2 ulp (they round toward zero), up to 32 steps in a
+    step off by less than an ulp (they round toward zero), up to 64 steps in a
     row, and the sums of those are added in fp32: off by less than
     (64 + 32 + dim / 512) * 2u of the sum A of the products' magnitudes.
   * logp and lse: their logits, and the fp32 arithmetic of a softmax

@@ -171,6 +171,60 @@ def test_half_precision_coefficients():
         ref.check_gradients(*got, dlogp * size, dlse * size)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [2, 200])
+def test_even_choice_of_many(rows, dtype):
+    """Probabilities of 4e-6 keep their digits in the 16-bit gradient by the logits: hidden states of one value,
+    and weights of 0 but for a constant, make every p = 1 / vocab."""
+    vocab, dim = 2 ** 18, 32
+    hidden = torch.full((rows, dim), 0.5, dtype=dtype, device=DEV)
+    weight = torch.full((vocab, dim), 0.25, dtype=dtype, device=DEV)
+    target = torch.arange(rows, device=DEV) * 1000
+    dlogp = torch.linspace(-300.0, -100.0, rows, device=DEV)
+    logp, lse = itr.red_linear_logprob(hidden, weight, target)
+    gh, gw = itr.red_linear_logprob_grad(hidden, weight, target, lse, dlogp)
+    want = -0.5 * float(dlogp.double().sum()) / vocab  # of every token that is no target
+    rest = torch.ones(vocab, dtype=torch.bool, device=DEV)
+    rest[target] = False
+    # g and the result are rounded once each, p is off by the rounding of lse = 16.5 (2e-6) and its own 3e-5
+    half = torch.finfo(dtype).eps / 2
+    assert float((gw[rest].double() / want - 1).abs().max()) <= 2 * half + half * half + 4e-5
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [3, 290])
+def test_almost_certain(rows, dtype):
+    """log p of about -1e-4, relative to itself: what the others' logits and the target's are off by, the sum of their
+    exponentials (3e-5), and the rounding of the arguments."""
+    hidden, weight, target, _, _ = inputs(rows, 64, 900, dtype, 0.0)
+    hidden.copy_(9.0 * weight[target].float())
+    ref = Reference(hidden, weight, target)
+    logp, _ = itr.red_linear_logprob(hidden, weight, target)
+    assert float(ref.logp.median()) > -1e-2
+    z = ref.lse.abs() + ref.logp.abs()
+    off = (logp.double() - ref.logp).abs() / ref.logp.abs()
+    assert bool((off <= 2 * ref.dz + 3e-5 + z * 4 * 2.0 ** -24).all())
+
+
+@pytest.mark.parametrize("rows", [3, 290])
+def test_token_ruled_out(rows):
+    """Weights of -inf where all hidden states are above 0: a token without a probability, target or not."""
+    hidden, weight, target, _, _ = inputs(rows, 64, 900, torch.bfloat16, 0.0)
+    hidden[:, 7] = 1.0
+    weight[5, 7] = -math.inf
+    target[:] = target.where(target != 5, 6)
+    target[1] = 5
+    z = hidden.double() @ weight.double().t()
+    logp, lse = itr.red_linear_logprob(hidden, weight, target)
+    want = torch.logsumexp(z, 1)
+    tol = 1e-3  # (logits of some tens: the finite ones are held to more elsewhere)
+    assert float((lse.double() - want).abs().max()) < tol
+    assert float(logp[1]) == -math.inf
+    rest = torch.arange(rows, device=DEV) != 1
+    want = z.gather(1, target[:, None])[:, 0] - want
+    assert float((logp.double() - want)[rest].abs().max()) < tol
+
+
 def test_gradient_by_differences():
     """The forward pass at both sides, along directions of 16-bit steps."""
     rows, dim, vocab = 20, 64, 500
