@@ -487,6 +487,14 @@ private:
     }
 };
 
+// Row stride of a new matrix like x: x's where that is a padding, else (rows out of a
+// larger tensor: every row would take as much memory as in that) to the next 16 bytes.
+int64_t new_ld(const Logits &l)
+{
+    const int64_t unit = 16 / (int64_t)l.x.element_size();
+    return l.ld - l.len <= 128 ? l.ld : (l.len + unit - 1) / unit * unit;
+}
+
 // A matrix like x: dtype, device and shape; its row stride through *ld.
 const at::Tensor &beside(const Logits &l, PyObject *o, const char *name, int64_t *ld)
 {
@@ -528,7 +536,7 @@ struct NormInputs {
     void results(Results &made, PyObject *given_total)
     {
         if (with_residual) {
-            total = given_total == Py_None ? made.rows(l.rows, l.len, l.ld, l.x.scalar_type())
+            total = given_total == Py_None ? made.rows(l.rows, l.len, new_ld(l), l.x.scalar_type())
                                            : beside(l, given_total, "total", &ldt);
             ldt = Logits::stride(total, "total");
         } else if (given_total != Py_None) {
@@ -537,7 +545,7 @@ struct NormInputs {
         rstd = made.vector(l.rows, at::kFloat);
     }
     // Bytes of y (or 8-bit values and scales), total and rstd, at most.
-    int64_t bytes() const { return l.rows * (2 * l.ld * (int64_t)l.x.element_size() + 4 * (l.len / 32 + 2)); }
+    int64_t bytes() const { return l.rows * (2 * new_ld(l) * (int64_t)l.x.element_size() + 4 * (l.len / 32 + 2)); }
     void *total_ptr() const { return total.defined() ? total.data_ptr() : nullptr; }
 };
 
@@ -547,9 +555,9 @@ PyObject *rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n)
     return guarded("rmsnorm", n, 7, [&] {
         NormInputs in(a[0], a[1], a[2]);
         const OnStream on(a[6], in.l);
-        int64_t ldy = in.l.ld;
+        int64_t ldy = new_ld(in.l);
         Results made(in.l, in.bytes(), 3);
-        const at::Tensor y = a[4] == Py_None ? made.rows(in.l.rows, in.l.len, in.l.ld, in.l.x.scalar_type())
+        const at::Tensor y = a[4] == Py_None ? made.rows(in.l.rows, in.l.len, ldy, in.l.x.scalar_type())
                                              : beside(in.l, a[4], "out", &ldy);
         in.results(made, a[5]);
         RETURN_IF_REFUSED(red_rmsnorm(in.l.dtype, in.l.x.data_ptr(), in.l.rows, in.l.len, in.l.ld, in.residual, in.ldr,
@@ -594,14 +602,14 @@ PyObject *rmsnorm_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
     return guarded("rmsnorm_grad", n, 8, [&] {
         const Logits l(a[1]);
         const OnStream on(a[7], l);
-        int64_t lddy, ldt = 0, ldd = l.ld;
+        int64_t lddy, ldt = 0, ldd = new_ld(l);
         const at::Tensor &dy = beside(l, a[0], "dy", &lddy);
         const float *rstd = l.vector<float>(a[2], "rstd", l.rows);
         int wtype;
         const void *weight = norm_weight(l, a[3], &wtype);
         const void *dtotal = a[4] == Py_None ? nullptr : beside(l, a[4], "dtotal", &ldt).data_ptr();
-        Results made(l, l.rows * l.ld * (int64_t)l.x.element_size() + 4 * l.len, 2);
-        const at::Tensor dx = a[5] == Py_None ? made.rows(l.rows, l.len, l.ld, l.x.scalar_type())
+        Results made(l, l.rows * ldd * (int64_t)l.x.element_size() + 4 * l.len, 2);
+        const at::Tensor dx = a[5] == Py_None ? made.rows(l.rows, l.len, ldd, l.x.scalar_type())
                                               : beside(l, a[5], "grad", &ldd);
         at::Tensor dw;
         if (a[6] == Py_None) {
@@ -641,11 +649,11 @@ PyObject *balance(PyObject *, PyObject *const *a, Py_ssize_t n)
                 refuse("live must be a contiguous vector of one bool or uint8 per row on x's device");
             live = static_cast<const uint8_t *>(t.data_ptr());
         }
-        Results made(l, l.rows * l.ld * (int64_t)l.x.element_size() + 12 * l.len + 16, 4);
+        int64_t ldd = new_ld(l);
+        Results made(l, l.rows * ldd * (int64_t)l.x.element_size() + 12 * l.len + 16, 4);
         at::Tensor dx;
-        int64_t ldd = l.ld;
         if (a[7] == Py_None)
-            dx = made.rows(l.rows, l.len, l.ld, l.x.scalar_type());
+            dx = made.rows(l.rows, l.len, ldd, l.x.scalar_type());
         else if (a[7] != Py_False)
             dx = beside(l, a[7], "grad", &ldd);
         const at::Tensor counts = made.vector(l.len, at::kLong), prob = made.vector(l.len, at::kFloat),
