@@ -603,8 +603,8 @@ enum red_balance_kind {
  *   dx       grad_scale * d loss / dx (counts are constants), rows of stride ldd;
  *            0 for a token that is out, whatever its logits hold.  May be x
  *            (ldd == ld then), or NULL for none.
- * -inf takes an expert out of a token's choice; a token with nothing else has
- * no probabilities and a gradient of 0.  NaN (and +inf, of a softmax) in a token
+ * -inf takes an expert out of a token's choice; a token with nothing else (and, of
+ * sigmoids, one with nothing above -700) has no probabilities and a gradient of 0.  NaN (and +inf, of a softmax) in a token
  * that takes part makes its gradient, prob and the loss NaN.  Results are the same from call to
  * call, bit for bit.  Uses the workspace.
  */

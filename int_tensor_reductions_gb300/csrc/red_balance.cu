@@ -142,6 +142,7 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
     }
     // sum of e and of e * c, for sum of p * c
     float2 sums = make_float2(0.0f, 0.0f);
+    [[maybe_unused]] float keep = 1.0f;  // sigmoids: e is p's numerator and the sigmoid; 0: the numerator alone
 #pragma unroll
     for (int v = 0; v < N; ++v)
 #pragma unroll
@@ -153,6 +154,32 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
             sums.y = fmaf(e[v][k], s.c[v][k], sums.y);
         }
     sums = group_sums<LANES>(sums, sh, turn);
+    if constexpr (SIGMOID) {
+        // Logits below -69 throughout: 1 + e^x is 1, and p the softmax, whose terms do not underflow.
+        // Below -700 (a mask's lowest value, in 64 bits a sigmoid of 0) there are no probabilities.
+        // (For all groups of a warp at once: the others' sums become what they were.)
+        const bool low = sums.x < 1e-30f;
+        if (__any_sync(0xffffffffu, low)) {
+#pragma unroll
+            for (int v = 0; v < N; ++v)
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    top = Max()(top, x[v][k]);
+            top = group_fold<LANES>(top, sh, turn, Max());
+            keep = low ? 0.0f : 1.0f;
+            sums = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int v = 0; v < N; ++v)
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    if (low)
+                        e[v][k] = top < -700.0f ? 0.0f : ex2((x[v][k] - top) * LOG2E);
+                    sums.x += e[v][k];
+                    sums.y = fmaf(e[v][k], s.c[v][k], sums.y);
+                }
+            sums = group_sums<LANES>(sums, sh, turn);
+        }
+    }
     float sum = sums.x;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // nothing but -inf: no probabilities
     float d = sums.y * inv;
@@ -191,7 +218,7 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             const float p = x[v][k];
-            g[k] = (SIGMOID ? p * (1.0f - e[v][k]) : p) * fmaf(s.c[v][k], s.unit, shift);
+            g[k] = (SIGMOID ? p * fmaf(-keep, e[v][k], 1.0f) : p) * fmaf(s.c[v][k], s.unit, shift);
         }
         store_unit<DT, VEC, LANES>(a.dx, r * a.ldd, (v * LANES + lane) * E, a.experts, here, g);
     }

@@ -130,6 +130,32 @@ def test_masks_and_odd_ids(rows, experts, kind):
         assert bool((got[3][1] == 0).all())
 
 
+@pytest.mark.parametrize("rows,experts", [(60, 16), (900, 8), (6000, 64), (90, 1000)])
+def test_sigmoids_near_zero(rows, experts):
+    """Tokens whose sigmoids are below fp32's smallest have probabilities all the same."""
+    for dtype in DTYPES:
+        x, ids, live = inputs(rows, experts, 4, dtype)
+        x[::3] -= 100.0
+        x[1::7] -= 60.0
+        x[5, 1:] = torch.finfo(dtype).min
+        x[8] -= 600.0
+        got = itr.red_balance(x, ids, live=live, coef=0.1, kind="sigmoid")
+        check(x, ids, live, got, "sigmoid", 0.1, 0.0, 1.0)
+
+
+def test_results_of_rows_out_of_a_larger_tensor():
+    """Results do not take the row stride of what x was cut from."""
+    whole = torch.randn((20, 50, 64), device=DEV)
+    x = whole[:, -1]
+    ids = torch.topk(x, 2, 1).indices
+    grad = itr.red_balance(x, ids)[3]
+    assert grad.stride(0) == 64 and torch.equal(grad, itr.red_balance(x.contiguous(), ids)[3])
+    y, _, rstd = itr.red_rmsnorm(x)
+    assert y.stride(0) == 64 and torch.equal(y, itr.red_rmsnorm(x.contiguous())[0])
+    dx, _ = itr.red_rmsnorm_grad(y, x, rstd)
+    assert dx.stride(0) == 64 and torch.equal(dx, itr.red_rmsnorm_grad(y, x.contiguous(), rstd)[0])
+
+
 @pytest.mark.parametrize("rows,experts", [(60, 16), (6000, 64)])
 def test_nobody_takes_part(rows, experts):
     x, ids, live = inputs(rows, experts, 2, torch.float32)
