@@ -122,23 +122,30 @@ __device__ __forceinline__ V block_fold(V v, V *sh, F f)
 constexpr float MOST = 1.9921875f;
 __device__ __forceinline__ float most_of(int dtype) { return dtype == RED_F16 ? MOST * 8192.0f : MOST; }
 
-// One CTA: which rows take part and, for the gradients, their coefficients.
-// By the whole CTA of NT threads; the number of rows that take part.  f(place, row)
-// for each; `writes`: to the workspace.
+// Which rows take part and, for the gradients, their coefficients, by a CTA of NT
+// threads; the number of rows that take part.  f(place, row) for each; `writes`: to the
+// workspace.  Thread t has rows t, t + NT, ... of a round, so that loads are of
+// neighbours, and what a row needs is loaded at once, whether it takes part or not: one
+// load after the other takes the latency of each, for every CTA of the gather.
+template <int NT, int EACH>
+struct ScanShared {
+    int counts[EACH * (NT / 32)], all;
+    float tops[32];
+};
 template <bool GRAD, int NT, int EACH, class F>
-__device__ __forceinline__ int scan_rows(const ScanArgs &a, int *sums, float *tops, bool writes, float &unit, F f)
+__device__ __forceinline__ int scan_rows(const ScanArgs &a, ScanShared<NT, EACH> &sh, bool writes, float &unit, F f)
 {
-    const int tid = threadIdx.x;
-    // (what a row needs is loaded at once, whether it takes part or not: one load after the other takes the
-    // latency of each, for every CTA of the gather)
+    constexpr int WARPS = NT / 32, ROUND = NT * EACH;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     struct Row {
-        int64_t target;
+        int target;  // -1: outside the vocabulary
         float d, n;
     };
     auto load = [&](int64_t r) {
         Row row = {-1, 0.0f, 0.0f};
         if (r < a.in.rows) {
-            row.target = a.in.target[r];
+            const int64_t t = a.in.target[r];
+            row.target = t >= 0 && t < a.in.vocab ? (int)t : -1;
             if constexpr (GRAD) {
                 row.d = a.dlogp[r];
                 row.n = a.dlse ? a.dlse[r] : 0.0f;
@@ -147,77 +154,89 @@ __device__ __forceinline__ int scan_rows(const ScanArgs &a, int *sums, float *to
         return row;
     };
     auto takes_part = [&](const Row &row) {
-        return row.target >= 0 && row.target < a.in.vocab && (!GRAD || !(row.d == 0.0f && row.n == 0.0f));
+        return row.target >= 0 && (!GRAD || !(row.d == 0.0f && row.n == 0.0f));
     };
     auto by_p = [&](const Row &row) { return (row.n - row.d) * a.in.scale; };
+    auto larger = [&](float top, const Row &row) {
+        return takes_part(row) ? fmaxf(top, fmaxf(fabsf(row.d * a.in.scale), fabsf(by_p(row)))) : top;
+    };
+    Row row[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        row[i] = load(i * NT + tid);
     unit = 1.0f;
     if constexpr (GRAD) {
         float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            top = larger(top, row[i]);
 #pragma unroll 4
-        for (int64_t r = tid; r < a.in.rows; r += NT) {
-            const Row row = load(r);
-            if (takes_part(row))
-                top = fmaxf(top, fmaxf(fabsf(row.d * a.in.scale), fabsf(by_p(row))));
-        }
-        top = block_fold<NT>(top, tops, [](float x, float y) { return fmaxf(x, y); });
+        for (int64_t r = ROUND + tid; r < a.in.rows; r += NT)
+            top = larger(top, load(r));
+        top = block_fold<NT>(top, sh.tops, [](float x, float y) { return fmaxf(x, y); });
         if (top > 0.0f && top < __builtin_huge_valf())
             unit = fminf(fmaxf(top, 1e-32f), 1e36f) / most_of(a.in.dtype);
     }
     const float inv = 1.0f / unit;
     int before = 0;
-    for (int64_t r0 = 0; r0 < a.in.rows; r0 += NT * EACH) {
-        const int64_t first = r0 + (int64_t)tid * EACH;
-        Row row[EACH];
+    for (int64_t r0 = 0; r0 < a.in.rows; r0 += ROUND) {
+        if (r0 > 0) {
+            __syncthreads();  // (the last round's counts have been read)
 #pragma unroll
-        for (int i = 0; i < EACH; ++i)
-            row[i] = load(first + i);
-        unsigned mask = 0;
-#pragma unroll
-        for (int i = 0; i < EACH; ++i)
-            mask |= takes_part(row[i]) ? 1u << i : 0u;
-        const int mine = __popc(mask);
-        int upto = mine;  // inclusive sum over the block
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (tid % 32 >= o)
-                upto += v;
+            for (int i = 0; i < EACH; ++i)
+                row[i] = load(r0 + i * NT + tid);
         }
-        __syncthreads();
-        if (tid % 32 == 31)
-            sums[tid / 32] = upto;
-        __syncthreads();
-        const int sum = tid % 32 < NT / 32 ? sums[tid % 32] : 0;
-        int scan = sum;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, scan, o);
-            if (tid % 32 >= o)
-                scan += v;
-        }
-        const int warps_before = __shfl_sync(0xffffffffu, scan - sum, tid / 32);
-        const int all = __shfl_sync(0xffffffffu, scan, 31);
-        int at = before + warps_before + upto - mine;
+        unsigned takes[EACH];  // by the warp's lanes
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
-            const int64_t r = first + i;
+            takes[i] = __ballot_sync(0xffffffffu, takes_part(row[i]));
+            if (lane == 0)
+                sh.counts[i * WARPS + warp] = __popc(takes[i]);
+        }
+        __syncthreads();
+        if (warp == 0) {  // exclusive sums, in the order of the rows
+            constexpr int MINE = EACH * WARPS / 32;
+            int c[MINE], sum = 0;
+#pragma unroll
+            for (int k = 0; k < MINE; ++k) {
+                c[k] = sum;
+                sum += sh.counts[lane * MINE + k];
+            }
+            int upto = sum;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o)
+                    upto += v;
+            }
+#pragma unroll
+            for (int k = 0; k < MINE; ++k)
+                sh.counts[lane * MINE + k] = upto - sum + c[k];
+            if (lane == 31)
+                sh.all = upto;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int64_t r = r0 + i * NT + tid;
             if (r >= a.in.rows)
                 break;
-            const bool takes = mask >> i & 1;
+            const int at = before + sh.counts[i * WARPS + warp] + __popc(takes[i] & ((1u << lane) - 1u));
+            const bool here = takes[i] >> lane & 1;
             if (writes)
-                a.w.pos[r] = takes ? at : -1;
-            if (!takes)
+                a.w.pos[r] = here ? at : -1;
+            if (!here)
                 continue;
             f(at, (int)r);
             if (writes) {
                 a.w.idx[at] = (int)r;
-                a.w.target[at] = (int)row[i].target;
+                a.w.target[at] = row[i].target;
                 if constexpr (GRAD) {
                     a.w.by_p[at] = by_p(row[i]) * inv;
                     a.w.lse2[at] = a.lse[r] * LOG2E;
                 }
             }
-            ++at;
         }
-        before += all;
+        before += sh.all;
     }
     if (writes && tid == 0) {
         a.w.head->live = before;
@@ -230,10 +249,9 @@ template <bool GRAD>
 __global__ void __launch_bounds__(SCAN_NT) linear_scan_kernel(const ScanArgs a)
 {
     pdl_enter();
-    __shared__ int sums[32];
-    __shared__ float tops[32];
+    __shared__ ScanShared<SCAN_NT, SCAN_ROWS> sh;
     float unit;
-    scan_rows<GRAD, SCAN_NT, SCAN_ROWS>(a, sums, tops, true, unit, [](int, int) {});
+    scan_rows<GRAD, SCAN_NT, SCAN_ROWS>(a, sh, true, unit, [](int, int) {});
 }
 
 // g at the target of packed row r (`row` of the input), by a warp: from a logit of its own.
@@ -295,15 +313,14 @@ template <bool GRAD, int EACH>
 __global__ void __launch_bounds__(256) linear_gather_kernel(const ScanArgs a)
 {
     pdl_enter();
-    __shared__ int sums[32];
-    __shared__ float tops[32];
+    __shared__ ScanShared<256, EACH> sh;
     __shared__ int row_of[8];
     const bool writes = blockIdx.x == 0;
     const int first_packed = blockIdx.x * 8;
     if (threadIdx.x < 8)
         row_of[threadIdx.x] = -1;
     float unit;
-    const int live = scan_rows<GRAD, 256, EACH>(a, sums, tops, writes, unit, [&](int at, int r) {
+    const int live = scan_rows<GRAD, 256, EACH>(a, sh, writes, unit, [&](int at, int r) {
         if (at >= first_packed && at < first_packed + 8)
             row_of[at - first_packed] = r;
     });
