@@ -525,6 +525,13 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
     mma_end(b, warp);
 }
 
+__device__ __forceinline__ float max_of_warp(float v)
+{
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // ----------------------------------------------------------- join of the parts
 
 // (maximum, sum) pairs of a row's tiles to its lse and logp: a warp per row, or a CTA
@@ -540,10 +547,9 @@ struct Pair {
     }
     __device__ __forceinline__ void join_lanes()
     {
-        for (int o = 16; o; o >>= 1) {
-            const float om = __shfl_xor_sync(0xffffffffu, m, o), ol = __shfl_xor_sync(0xffffffffu, l, o);
-            join(om, ol);
-        }
+        const float top = max_of_warp(m);
+        l = sum_of_lanes(l * ex2(m - (top == NEG_INF ? 0.0f : top)));
+        m = top;
     }
 };
 
@@ -656,13 +662,6 @@ struct FewArgs {
     const int64_t *targets;
     int rows;
 };
-
-__device__ __forceinline__ float max_of_warp(float v)
-{
-    float r;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
 
 // Sums over the warp of 32 (or the first 16) values per lane: lane i gets the i-th.
 template <int N>
