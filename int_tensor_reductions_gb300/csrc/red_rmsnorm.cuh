@@ -33,7 +33,8 @@ struct NormArgs {
     void *y, *total;
     int64_t ldy, ldt;
     float *rstd, *scales;
-    int block, blocks;  // values of a block (fewer than len) and blocks per row; 0 and 1: one scale per row
+    int block, blocks;  // values of a block (a power of two below len) and blocks per row; 0 and 1: one scale per row
+    int block_log2;
 };
 struct NormGradArgs {
     const void *dy, *x, *weight, *dtotal;
@@ -182,10 +183,14 @@ __device__ __forceinline__ void store_q(uint8_t *q, int64_t row, int i, int len,
 }
 
 // KIND: 0 for y in x's type, else the 8-bit type.
-// (Registers are left to the compiler, but for one case that it makes 70 of, and three CTAs per SM: with 64, and four,
-// 16384 x 4096 bf16 91 -> 83 us.  A bound of one CTA per SM has it take more than 128: 16384 x 8192 173 -> 264.)
+// (Registers are left to the compiler, but for two cases.  One that it makes 70 of, and three CTAs per SM: with 64, and
+// four, 16384 x 4096 bf16 91 -> 83 us.  One that it makes 92 to 128 of, and two: with 80, and three, 16384 x 5120 without a
+// residual 63 -> 58 us, in e4m3 with one 120 -> 116, but with one in bf16 135.1 -> 135.7 (and in f32, left alone, 206 ->
+// 221).  A bound of one CTA per SM has it take more than 128: 16384 x 8192 173 -> 264; 80 for rows that long are too
+// few: 85 -> 104.)
 template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC, bool RING>
-__global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VECS == 2 && VEC && !RING ? 4 : 0) rmsnorm_kernel(const NormArgs a)
+__global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VEC ? (VECS == 2 && !RING ? 4 : VECS == 3 && RING && DT != RED_F32 ? 3 : 0) : 0)
+    rmsnorm_kernel(const NormArgs a)
 {
     pdl_enter();
     __shared__ GroupShared<LANES> sh;
@@ -277,11 +282,9 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VECS == 2 &&
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-                    for (int v = 0; v < N; ++v) {
-                        const float other = __shfl_xor_sync(0xffffffffu, most[v], o);
-                        if (o < lanes)
-                            most[v] = Max()(most[v], other);
-                    }
+                    for (int v = 0; v < N; ++v)
+                        if (o < lanes)  // (the same for all)
+                            most[v] = Max()(most[v], __shfl_xor_sync(0xffffffffu, most[v], o));
             } else {
 #pragma unroll
                 for (int v = 1; v < N; ++v)
@@ -293,8 +296,8 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VECS == 2 &&
                 const int i = (v * LANES + lane) * E;
                 float inv;
                 const float scale = scale_of<KIND>(a.block ? most[v] : most[0], &inv);
-                if (here && i < a.len && (a.block ? lane % (a.block / E) == 0 : v == 0 && lane == 0))
-                    a.scales[r * a.blocks + (a.block ? i / a.block : 0)] = scale;
+                if (here && i < a.len && (a.block ? (i & (a.block - 1)) == 0 : i == 0))
+                    a.scales[r * a.blocks + (i >> a.block_log2)] = scale;
                 store_q<E, VEC, LANES>(static_cast<uint8_t *>(a.y), r * a.ldy, i, a.len, here, narrow8<KIND>(t[v], inv));
             }
         }

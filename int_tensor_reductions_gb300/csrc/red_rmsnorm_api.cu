@@ -117,6 +117,7 @@ int red_rmsnorm_quant(int dtype, const void *x, int64_t rows, int64_t len, int64
     a.y = q, a.ldy = ldq, a.total = total, a.ldt = ldt, a.rstd = rstd, a.scales = scales;
     if (block > 0 && block < len) {  // (else one scale per row, whichever it is called)
         a.block = (int)block;
+        a.block_log2 = block == 32 ? 5 : block == 64 ? 6 : 7;
         a.blocks = (int)((len + block - 1) / block);
     } else {
         a.blocks = 1;
