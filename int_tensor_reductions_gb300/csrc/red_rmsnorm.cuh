@@ -121,7 +121,7 @@ __device__ __forceinline__ float scale_of(float most, float *inv)
 // A unit's values in 8 bits, to nearest, beyond the largest: the largest.  A product with
 // the scale's inverse: it is off by 1.5 units of fp32's last place, which moves one
 // value in a million across a border between two of 8 bits, and eight divisions
-// took more time than all else (16384 x 8192 bf16 295 us with them, 221 without).
+// cost more (16384 x 8192 bf16 178 us with them, 161 as it is; 4097 x 5120 42, 27).
 template <int KIND, int E>
 __device__ __forceinline__ uint64_t narrow8(const float (&v)[E], float inv)
 {
@@ -500,7 +500,7 @@ int forward_of(const NormArgs &a, int kind, cudaStream_t s)
     return with_group((a.len + 7) / 8, [&](auto lanes, auto vecs) {
         constexpr int L = decltype(lanes)::value, V = decltype(vecs)::value;
         // Rows fetched ahead or loaded where they are wanted, us at bf16: without a residual 16384 x
-        // 4096 43 / 54, in 8 bits 16384 x 8192 176 / 208, with a residual 8192 x 2048 20 / 22, 4097 x
+        // 4096 43 / 54, in 8 bits 16384 x 8192 161 / 167 and 4097 x 5120 27 / 39, with a residual 8192 x 2048 20 / 22, 4097 x
         // 5120 28 / 36 -- but with two matrices read and two of 16 bits written, and most of the
         // lanes' units in use, 16384 x 4096 94 / 83, 16384 x 8192 186 / 172, 65536 x 1024 91 / 83, 60000 x
         // 640 (five eighths of the units) 52 / 65.  fp32 is the same either way.
