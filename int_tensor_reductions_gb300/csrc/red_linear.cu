@@ -1091,27 +1091,47 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
 }
 
 // The sums of the pieces, and of their splits, to the rows' gradients, rounded once:
-// a thread per four elements.  Zeros where a row takes no part.
-template <int DT>
+// a thread per four elements, or (SHARES 8) one of each of eight warps, an eighth of the
+// splits each.  Zeros where a row takes no part.
+template <int DT, int SHARES>
 __global__ void __launch_bounds__(256)
     linear_scatter_kernel(const LinearWork w, int64_t rows, int64_t dim, uint16_t *dhidden, int64_t ldd)
 {
     pdl_enter();
+    constexpr int WIDTH = 256 / SHARES;
+    __shared__ float4 shares[SHARES][WIDTH];
     const float unit = w.head->unit;
     const int64_t quads = w.dim4 / 4, split = w.padded * w.dim4;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * quads; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / quads, d = (i - r * quads) * 4;
-        const int at = w.pos[r];
+    const int share = threadIdx.x / WIDTH, place = threadIdx.x % WIDTH;
+    for (int64_t i0 = (int64_t)blockIdx.x * WIDTH; i0 < rows * quads; i0 += (int64_t)gridDim.x * WIDTH) {
+        const int64_t i = i0 + place;
+        const bool here = i < rows * quads;
+        const int64_t r = here ? i / quads : 0, d = here ? (i - r * quads) * 4 : 0;
+        const int at = here ? w.pos[r] : -1;
         uint16_t *to = dhidden + r * ldd + d;
         float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (at >= 0) {
             const float *from = w.dhidden + (int64_t)at * w.dim4 + d;
-#pragma unroll 8
-            for (int s = 0; s < w.splits; ++s) {
+#pragma unroll 4
+            for (int s = share; s < w.splits; s += SHARES) {
                 const float4 v = *reinterpret_cast<const float4 *>(from + s * split);
                 x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
             }
         }
+        if constexpr (SHARES > 1) {
+            __syncthreads();  // (the last round's shares have been read)
+            shares[share][place] = make_float4(x[0], x[1], x[2], x[3]);
+            __syncthreads();
+            if (share != 0)
+                continue;
+#pragma unroll
+            for (int k = 1; k < SHARES; ++k) {
+                const float4 v = shares[k][place];
+                x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+            }
+        }
+        if (!here)
+            continue;
         if (d + 4 <= dim) {
             *reinterpret_cast<uint2 *>(to) =
                 make_uint2(pack2<DT>(x[0] * unit, x[1] * unit), pack2<DT>(x[2] * unit, x[3] * unit));
@@ -1441,9 +1461,14 @@ int launch_linear_logprob_grad(const LinearArgs &a, const float *lse, const floa
         RETURN_IF((a.dtype == RED_BF16 ? launch_products<RED_BF16>(tiles, s, p) : launch_products<RED_F16>(tiles, s, p)));
     }
     if (dhidden) {
-        auto *const kernel = a.dtype == RED_BF16 ? linear_scatter_kernel<RED_BF16> : linear_scatter_kernel<RED_F16>;
-        RETURN_IF(cuda_fail(launch_pdl(kernel, dim3(warp_rows_grid(a.rows * w.dim4 / 4 / 32 + 1)), dim3(256), s, w, a.rows, a.dim,
-                                       static_cast<uint16_t *>(dhidden), ldd),
+        // A CTA's places: 256, or 32 in eight shares.  The whole gradient, us, without / with shares: 18 splits (64 x 1024 x
+        // 32001) 61 / 58, 9 (300 x 1024 x 8192) 38 / 39, 4 (128 x 4096 x 32768) 206 / 211.
+        const bool shares = w.splits >= 16;
+        auto *const kernel = a.dtype == RED_BF16
+                                 ? (shares ? linear_scatter_kernel<RED_BF16, 8> : linear_scatter_kernel<RED_BF16, 1>)
+                                 : (shares ? linear_scatter_kernel<RED_F16, 8> : linear_scatter_kernel<RED_F16, 1>);
+        const unsigned grid = warp_rows_grid(a.rows * w.dim4 / 4 / (shares ? 4 : 32) + 1);
+        RETURN_IF(cuda_fail(launch_pdl(kernel, dim3(grid), dim3(256), s, w, a.rows, a.dim, static_cast<uint16_t *>(dhidden), ldd),
                             "linear_scatter"));
         count_launches(1);
     }
