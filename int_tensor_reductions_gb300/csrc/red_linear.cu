@@ -958,6 +958,10 @@ __device__ __forceinline__ void store_product(const ProductArgs &a, bool ok, uin
                     if (col + c + i < a.dim)
                         a.dweight[r * a.lddw + col + c + i] = (uint16_t)pack2<DT>(v[i] * unit, 0.0f);
             }
+            // An empty group in the place of the box's store: the boxes take turns, and what store_read<1>
+            // leaves pending has to be the other one's.
+            if (lane == 0)
+                store_commit();
             continue;
         }
         unsigned char *const box = staging + c / WIDTH % 2 * BOX_BYTES;
