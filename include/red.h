@@ -474,8 +474,10 @@ int red_preference(int dtype, const void *x, int64_t rows, int64_t len, int64_t 
  *     z[r, j] = scale * sum_d hidden[r, d] * weight[j, d],
  *     lse[r] = log sum_j e^z[r, j],  logp[r] = z[r, target[r]] - lse[r].
  * Conventions:
- *   dtype    RED_F16 or RED_BF16, of all matrices.  Products are summed in fp32;
- *            logits, maxima and sums of exponentials are fp32 throughout.
+ *   dtype    RED_F16 or RED_BF16, of all matrices.  Products are summed in fp32,
+ *            those of a run of 128 to 1024 of dim by the tensor cores (each of their
+ *            steps of 16 rounds toward zero); logits (up to 1e9 in magnitude), maxima
+ *            and sums of exponentials are fp32 throughout.
  *   hidden   rows x dim, row stride ldh;  weight: vocab x dim, row stride ldw.
  *            Every matrix starts on a 16-byte boundary and its row stride is a
  *            multiple of 8 elements (where it has more than one row), dim
@@ -503,7 +505,8 @@ int red_linear_logprob(int dtype, const void *hidden, int64_t rows, int64_t dim,
  * dlogp[r] and dlse[r] (NULL: 0) of some loss by logp[r] and lse[r],
  *     g[r, j] = scale * (dlogp[r] * ([j == target[r]] - p_j) + dlse[r] * p_j),
  *     dhidden = g * weight,  dweight = g^T * hidden,
- * with p_j = e^(z[r, j] - lse[r]), lse as red_linear_logprob left it.  A row
+ * with p_j = e^(z[r, j] - lse[r]), lse as red_linear_logprob left it (p is as
+ * exact as lse: off by the rounding of a number of its size).  A row
  * whose dlogp and dlse are both 0 is ignored, too.  The vocabulary is taken in
  * pieces; g is rounded to dtype once, in units that the largest coefficient
  * sets, and each result once more; their sums are fp32.

@@ -27,10 +27,13 @@ namespace red {
 namespace {
 
 // Blocks of 64 of K whose products are summed by the tensor cores before the sum
-// moves to fp32 registers.  The tensor cores' additions round toward zero, so a long
-// sum drifts with its number of steps: 6144 x 4096 x 65536 bf16 takes, with 8 blocks,
-// 1790 us, with 16, 1725, with 32, 1744, and the errors of logits double each time.
-// What they would do most harm to is the target's logit: the likelihood of a token that
+// moves to fp32 registers (tiles of 256 x 256; of few rows, see Few).  The tensor cores'
+// additions round toward zero, so a long sum drifts with its number of steps, four to a
+// block, and lse with the logits: by -1.9e-6 on average at logits of a bell of width 1.5 (lse 11,
+// dim 1024 to 8192), -1.2e-6 with 12 blocks and -0.8e-6 with 8, while 6144 x 4096 x 65536 bf16
+// takes 1660, 1713 and 1808 us.  Against 64 bits logp is then off by 2.8e-7 to 3.9e-7 of its norm
+// (300 rows; fp32 products of torch: 2.4e-7 at dim 1024, 5.8e-7 at 4096, 8.7e-7 at 8192).
+// What the drift would do most harm to is the target's logit: the likelihood of a token that
 // is all but certain is the distance of its logit from the others', and logits at the
 // end of the range drift furthest.  That one is summed apart (dot_by_warp): a
 // reading of N rows of both matrices.
@@ -382,6 +385,19 @@ __device__ __forceinline__ bool take_sums(float (&z)[HALF], MmaBarriers &b, AccP
     return ok;
 }
 
+// What the exponents of terms under the maximum m are relative to: m * s2, rounded, and the factor that makes their
+// sum relative to m itself, 2^(the rounding).  Maxima of tiles differ by the size of the logits, and their products'
+// roundings would be in every term of one of them: of logits near 20, 1e-6.
+struct Base {
+    float off;
+
+    __device__ __forceinline__ Base(float m, float s2) { off = m == NEG_INF ? 0.0f : __fmul_rn(m, s2); }
+    __device__ __forceinline__ float factor(float m, float s2) const
+    {
+        return m == NEG_INF ? 1.0f : ex2(-fmaf(m, s2, -off));
+    }
+};
+
 // Two floats as 16-bit values, the first in the low half.
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
@@ -467,15 +483,14 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
 #pragma unroll
                 for (int i = 0; i < HALF; i += 2)
                     m = fmaxf(m, fmaxf(z[i], z[i + 1]));
-                const float m2 = m * a.s2;
-                const float off = m == NEG_INF ? 0.0f : m2;
+                const Base base(m, a.s2);
                 float l[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < HALF; ++i)
-                    l[i % 4] += ex2(fmaf(z[i], a.s2, -off));
+                    l[i % 4] += ex2(fmaf(z[i], a.s2, -base.off));
                 if (takes)
                     a.work.part[(int64_t)row * a.work.slots + (at.n * 2 + half)] =
-                        make_float2(m2, ok ? (l[0] + l[1]) + (l[2] + l[3]) : NOTHING);
+                        make_float2(m, ok ? ((l[0] + l[1]) + (l[2] + l[3])) * base.factor(m, a.s2) : NOTHING);
             } else {
                 cp = ok ? cp : NOTHING;
                 gt = ok ? gt : NOTHING;
@@ -538,17 +553,17 @@ __device__ __forceinline__ float max_of_warp(float v)
 // where rows are few.
 struct Pair {
     float m, l;
-    __device__ __forceinline__ void join(float om, float ol)
+    __device__ __forceinline__ void join(float om, float ol, float s2)
     {
         const float top = fmaxf(m, om);
         const float ref = top == NEG_INF ? 0.0f : top;
-        l = l * ex2(m - ref) + ol * ex2(om - ref);
+        l = l * ex2((m - ref) * s2) + ol * ex2((om - ref) * s2);
         m = top;
     }
-    __device__ __forceinline__ void join_lanes()
+    __device__ __forceinline__ void join_lanes(float s2)
     {
         const float top = max_of_warp(m);
-        l = sum_of_lanes(l * ex2(m - (top == NEG_INF ? 0.0f : top)));
+        l = sum_of_lanes(l * ex2((m - (top == NEG_INF ? 0.0f : top)) * s2));
         m = top;
     }
 };
@@ -575,9 +590,9 @@ __global__ void __launch_bounds__(256)
 #pragma unroll 4
         for (int64_t i = lane; i < slots; i += LANES) {
             const float2 o = part[i];
-            p.join(o.x, o.y);
+            p.join(o.x, o.y, s2);
         }
-        p.join_lanes();
+        p.join_lanes(s2);
         float z;  // the target's product
         if constexpr (LANES > 32) {
             const uint16_t *hr = static_cast<const uint16_t *>(a.hidden) + r * a.ldh;
@@ -593,7 +608,7 @@ __global__ void __launch_bounds__(256)
             p = {NEG_INF, 0.0f};
             if (lane % 32 < LANES / 32)
                 p = {warps[lane % 32].x, warps[lane % 32].y};
-            p.join_lanes();
+            p.join_lanes(s2);
             z = 0.0f;
 #pragma unroll
             for (int k = 0; k < LANES / 32; ++k)
@@ -602,17 +617,16 @@ __global__ void __launch_bounds__(256)
             z = dot_by_warp(a, r, target, lane);
         }
         if (lane == 0) {
-            constexpr float LN2 = 0.6931471805599453f;
-            const float z2 = z * s2, off = z2 - p.m;  // (a NaN goes on; +inf, and only +inf, is one below)
+            const float off = z - p.m;  // (a NaN goes on; +inf, and only +inf, is one below)
             float lp, norm;
             if (off >= 0.0f) {
-                lp = log1pf(p.l * ex2(-off));
-                norm = fmaf(z, a.scale, lp) + (z2 - z2);
-                lp = (z2 - z2) - lp;
+                lp = log1pf(p.l * ex2(-off * s2));
+                norm = fmaf(z, a.scale, lp) + (z - z);
+                lp = (z - z) - lp;
             } else {
-                const float all = logf(p.l + ex2(off));
-                norm = fmaf(p.m, LN2, all);
-                lp = fmaf(off, LN2, -all);
+                const float all = logf(p.l + ex2(off * s2));
+                norm = fmaf(p.m, a.scale, all);
+                lp = fmaf(off, a.scale, -all);
             }
             logp[r] = lp;
             lse[r] = norm;
@@ -640,7 +654,12 @@ struct Few {
     static constexpr int STAGE = OPERAND_BYTES + ROWS * BLOCK_K * 2;
     static constexpr int N = 212992 / STAGE < 12 ? 212992 / STAGE : 12;  // stages
     static constexpr size_t SMEM = (size_t)N * STAGE + 1024;
-    static constexpr int COLUMNS = 2 * ROWS;  // of tensor memory
+    // The blocks of a chunk go to ACCS sums in turn, which meet in fp32 registers: 8 to 16 steps that round toward
+    // zero in a row instead of the 64 of one sum of 16 blocks.  One row's log-probability stands alone, and was
+    // off by up to 2.2e-6 of itself (1 x 1024 x 32001; 6.2e-7 so).
+    static constexpr int ACCS = ROWS <= 32 ? 8 : 256 / ROWS;
+    static constexpr int CHUNK = ROWS <= 64 ? 16 : 8;
+    static constexpr int COLUMNS = 2 * ACCS * ROWS;  // of tensor memory
     struct Shared {
         uint64_t full[N], empty[N], acc_full[2], acc_empty[2], drain;
         uint32_t tmem;
@@ -692,7 +711,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
     extern __shared__ unsigned char raw[];
     __shared__ typename F::Shared b;
     unsigned char *const ring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;  // (the same for a warp)
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::N; ++i) {
             mbar_init(&b.full[i], 1);
@@ -750,39 +769,48 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
             for (int k = 0; k < F::N; ++k)
                 for (int n = 0; n < 65536 && !mbar_try(&b.full[k], k < pos.stage ? pos.phase : pos.phase ^ 1); ++n) {
                 }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
+        // All lanes wait and one issues: what the products take is then known to be the same for the warp, and a block
+        // of K is not bound by one thread's moving it there (1 x 2048 x 65536 with eight sums 50.3 -> 45.0 us).
+        const bool leader = elect_one();
         RingPos<F::N> pos;
         AccPos acc;
         bool ok = true;
         const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true, HALF, ROWS);
         for (int v = begin; v < end && ok; v += a.height)
-            for (int k0 = 0; k0 < a.k_blocks && ok; k0 += CHUNK) {
+            for (int k0 = 0; k0 < a.k_blocks && ok; k0 += F::CHUNK) {
                 if (!mbar_wait(&b.acc_empty[acc.slot], acc.phase ^ 1, &b.failed, 0)) {
                     ok = false;
                     break;
                 }
                 tmem_after();
-                const uint32_t d = b.tmem + acc.slot * ROWS;
-                for (int k = k0; k < min(k0 + CHUNK, a.k_blocks); ++k) {
+                for (int k = k0; k < min(k0 + F::CHUNK, a.k_blocks); ++k) {
                     if (!mbar_wait(&b.full[pos.stage], pos.phase, &b.failed, 0)) {
                         ok = false;
                         break;
                     }
                     tmem_after();
                     const unsigned char *at = ring + pos.stage * F::STAGE;
+                    const uint32_t d = b.tmem + (acc.slot * F::ACCS + (k - k0) % F::ACCS) * ROWS;
                     const uint64_t da = operand_desc(at, true), db = operand_desc(at + OPERAND_BYTES, true);
+                    if (leader) {
 #pragma unroll
-                    for (int s = 0; s < BLOCK_K / 16; ++s)
-                        mma_alone(d, da + s * step_k(true), db + s * step_k(true), idesc, k > k0 || s > 0);
-                    mma_commit_alone(&b.empty[pos.stage]);
+                        for (int s = 0; s < BLOCK_K / 16; ++s)
+                            mma_alone(d, da + s * step_k(true), db + s * step_k(true), idesc, k - k0 >= F::ACCS || s > 0);
+                        mma_commit_alone(&b.empty[pos.stage]);
+                    }
+                    __syncwarp();
                     pos.next();
                 }
-                if (ok)
+                if (ok && leader)
                     mma_commit_alone(&b.acc_full[acc.slot]);
+                __syncwarp();
                 acc.next();
             }
         if (!ok) {
-            mma_commit_alone(&b.drain);
+            if (leader)
+                mma_commit_alone(&b.drain);
+            __syncwarp();
             for (int n = 0; n < 65536 && !mbar_try(&b.drain, 0); ++n) {
             }
         }
@@ -800,24 +828,26 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
             const bool valid = v < stop;
             float z[ROWS];
             bool ok = true;
-            for (int k = 0; k < a.k_blocks; k += CHUNK) {
+            for (int k = 0; k < a.k_blocks; k += F::CHUNK) {
                 ok &= mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
                 tmem_after();
-                const uint32_t from = b.tmem + ((uint32_t)(part * 32) << 16) + acc.slot * ROWS;
-                if (k == 0) {
+                uint32_t from = b.tmem + ((uint32_t)(part * 32) << 16) + acc.slot * F::ACCS * ROWS;
+                for (int n = 0; n < min(F::ACCS, a.k_blocks - k); ++n, from += ROWS) {
+                    if (k == 0 && n == 0) {
 #pragma unroll
-                    for (int i = 0; i < ROWS; i += 16)
-                        tmem_load16(from + i, reinterpret_cast<uint32_t *>(z + i));
-                    tmem_wait();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < ROWS; i += 16) {
-                        uint32_t x[16];
-                        tmem_load16(from + i, x);
+                        for (int i = 0; i < ROWS; i += 16)
+                            tmem_load16(from + i, reinterpret_cast<uint32_t *>(z + i));
                         tmem_wait();
+                    } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            z[i + j] += __uint_as_float(x[j]);
+                        for (int i = 0; i < ROWS; i += 16) {
+                            uint32_t x[16];
+                            tmem_load16(from + i, x);
+                            tmem_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                z[i + j] += __uint_as_float(x[j]);
+                        }
                     }
                 }
                 tmem_before();
@@ -847,12 +877,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
                     for (int j = 0; j < GROUP; ++j) {
                         const float x = valid ? z[g * 32 + j] : NEG_INF;
                         const float most = max_of_warp(x);
-                        e[j] = ex2(fmaf(x, a.s2, most == NEG_INF ? 0.0f : -(most * a.s2)));
+                        e[j] = ex2(fmaf(x, a.s2, -Base(most, a.s2).off));
                         top = j == lane ? most : top;
                     }
-                    const float sum = sums_of_warp<GROUP>(e, lane) + fine;
+                    const float sum = sums_of_warp<GROUP>(e, lane) * Base(top, a.s2).factor(top, a.s2) + fine;
                     Pair p = {m[g], l[g]};
-                    p.join(top * a.s2, sum);
+                    p.join(top, sum, a.s2);
                     m[g] = p.m, l[g] = p.l;
                 }
             } else {
@@ -881,7 +911,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
             if (r < live) {
                 Pair p = {NEG_INF, 0.0f};
                 for (int w = 0; w < 4; ++w)
-                    p.join(b.stats[w][r].x, b.stats[w][r].y);
+                    p.join(b.stats[w][r].x, b.stats[w][r].y, a.s2);
                 a.work.part[(int64_t)r * a.work.slots + blockIdx.x] = make_float2(p.m, p.l);
             }
         }

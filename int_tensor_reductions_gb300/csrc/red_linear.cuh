@@ -24,7 +24,7 @@ struct LinearWork {
     int *idx;           // packed: row
     int *target;        // packed: target
     void *hidden;       // packed hidden states, `padded` rows of `ld` elements, zeros behind the last
-    float2 *part;       // packed x slots: (maximum, sum)         (forward)
+    float2 *part;       // packed x slots: (maximum of z / scale, sum)   (forward)
     float *at_target, *by_p, *lse2;  // packed: g at the target, coefficient of p, lse (gradients)
     void *piece;        // padded x piece: gradient by the logits (gradients)
     float *dhidden;     // splits x padded x dim4 sums            (gradients)

@@ -151,6 +151,14 @@ __device__ __forceinline__ void mma_commit_alone(uint64_t *bar)
                  : "memory");
 }
 
+// One lane of a warp (all of it calls), always the same.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
+}
+
 // 16 columns of this warp's 32 lanes of tensor memory: lane i gets row i.
 __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t *v)
 {
