@@ -509,7 +509,8 @@ int red_linear_logprob(int dtype, const void *hidden, int64_t rows, int64_t dim,
  * exact as lse: off by the rounding of a number of its size).  A row
  * whose dlogp and dlse are both 0 is ignored, too.  The vocabulary is taken in
  * pieces; g is rounded to dtype once, in units that the largest coefficient
- * sets, and each result once more; their sums are fp32.
+ * sets, and each result once more; their sums are fp32, those of a run of up to
+ * 4096 rows or columns (16384 columns where rows are up to 128) by the tensor cores.
  *   dhidden  rows x dim, row stride ldd, or NULL for none.  May be `hidden`.
  *   dweight  vocab x dim, row stride lddw, or NULL for none (not both).  Results
  *            must not overlap an input otherwise, nor each other.

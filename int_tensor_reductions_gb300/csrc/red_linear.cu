@@ -38,6 +38,10 @@ namespace {
 // end of the range drift furthest.  That one is summed apart (dot_by_warp): a
 // reading of N rows of both matrices.
 constexpr int CHUNK = 16;
+// The same of the gradients' sums, which are rounded to 16 bits at the end.  256 steps of terms of one sign are off by
+// 3e-5 (measured: 1e-7 a step, of dw of 262144 rows -1.65e-3 in one run, three times f16's rounding, and -2e-5
+// in runs of these); a sum of up to SHORT_PRODUCTS blocks, 1e-4, may be one run where rows are few.
+constexpr int CHUNK_PRODUCTS = 64, SHORT_PRODUCTS = 256;
 // Rows of tiles that are taken in turn along the vocabulary.
 constexpr int BAND = 16;
 
@@ -347,15 +351,16 @@ struct LogitArgs {
     float s2;          // scale * log2(e)
 };
 
-// One warp's 32 rows x 128 columns of z / scale in fp32 registers: the sums of
-// the chunks.  Whether they are right: after a wait that ran out they are whatever
+// One warp's 32 rows x 128 columns of a product in fp32 registers: the sums of
+// the chunks of EACH blocks.  Whether they are right: after a wait that ran out they are whatever
 // tensor memory held (and what is made of them has to become NaN; filling them
 // here costs the registers of a second set).
+template <int EACH>
 __device__ __forceinline__ bool take_sums(float (&z)[HALF], MmaBarriers &b, AccPos &acc, int blocks, uint32_t lanes,
                                           int half, uint32_t (&empty)[2])
 {
     bool ok = true;
-    for (int k = 0; k < blocks; k += CHUNK) {
+    for (int k = 0; k < blocks; k += EACH) {
         ok &= mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
         tmem_after();
         const uint32_t from = b.tmem + lanes + acc.slot * TILE + half * HALF;
@@ -438,13 +443,14 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
                 drain_copies(b, pos, rank);
                 break;
             }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
+        const bool issues = elect_one();
         RingPos<> pos;
         AccPos acc;
         const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true);
         for (int t = pair; t < tiles; t += pairs)
-            if (!multiply_tile(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, acc, idesc, CHUNK)) {
-                drain_products(b);
+            if (!multiply_tile<true>(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, acc, idesc, CHUNK, issues)) {
+                drain_products<true>(b, issues);
                 break;
             }
     } else if (warp >= 4) {
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
             float gt = 0.0f, cp = 0.0f, lse2 = 0.0f;
             if (GRAD && takes)
                 gt = a.work.at_target[row], cp = a.work.by_p[row], lse2 = a.work.lse2[row];
-            const bool ok = take_sums(z, b, acc, a.k_blocks, (uint32_t)(group * 32) << 16, half, empty);
+            const bool ok = take_sums<CHUNK>(z, b, acc, a.k_blocks, (uint32_t)(group * 32) << 16, half, empty);
             constexpr float NOTHING = __builtin_nanf("");
             if constexpr (!GRAD) {
                 if (tail) {
@@ -772,7 +778,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
     } else if (warp == 1) {
         // All lanes wait and one issues: what the products take is then known to be the same for the warp, and a block
         // of K is not bound by one thread's moving it there (1 x 2048 x 65536 with eight sums 50.3 -> 45.0 us).
-        const bool leader = elect_one();
+        const bool issues = elect_one();
         RingPos<F::N> pos;
         AccPos acc;
         bool ok = true;
@@ -793,7 +799,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
                     const unsigned char *at = ring + pos.stage * F::STAGE;
                     const uint32_t d = b.tmem + (acc.slot * F::ACCS + (k - k0) % F::ACCS) * ROWS;
                     const uint64_t da = operand_desc(at, true), db = operand_desc(at + OPERAND_BYTES, true);
-                    if (leader) {
+                    if (issues) {
 #pragma unroll
                         for (int s = 0; s < BLOCK_K / 16; ++s)
                             mma_alone(d, da + s * step_k(true), db + s * step_k(true), idesc, k - k0 >= F::ACCS || s > 0);
@@ -802,13 +808,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
                     __syncwarp();
                     pos.next();
                 }
-                if (ok && leader)
+                if (ok && issues)
                     mma_commit_alone(&b.acc_full[acc.slot]);
                 __syncwarp();
                 acc.next();
             }
         if (!ok) {
-            if (leader)
+            if (issues)
                 mma_commit_alone(&b.drain);
             __syncwarp();
             for (int n = 0; n < 65536 && !mbar_try(&b.drain, 0); ++n) {
@@ -944,15 +950,67 @@ struct ProductArgs {
     int with_dh, with_dw;
 };
 
-// A warp's 32 rows x 128 columns of a product from tensor memory (`free`: the
-// barrier that gives the accumulators back; 0: there were no products, the sums
-// are 0) to memory, 128 bytes of each row at a time, where they are `wanted` (rows of
-// a tile behind the last one are not).
+// WIDTH columns of a warp's 32 rows of a product, 128 bytes of each row, to memory.
+template <bool DH>
+constexpr int PRODUCT_WIDTH = DH ? 32 : 64;
 template <int DT, bool DH>
-__device__ __forceinline__ void store_product(const ProductArgs &a, bool ok, uint32_t from, uint32_t free, int row,
-                                              int col, bool wanted, float unit, unsigned char *staging, int lane)
+__device__ __forceinline__ void store_columns(const ProductArgs &a, const float *v, int row, int col, int c, float unit,
+                                              unsigned char *staging, int lane)
 {
-    constexpr int WIDTH = DH ? 32 : 64;
+    constexpr int WIDTH = PRODUCT_WIDTH<DH>;
+    if (!DH && a.dim % 8 != 0 && col + c < a.dim && col + c + WIDTH > a.dim) {
+        // (a map's box ends on 16 bytes, here beyond the row)
+        const int64_t r = (int64_t)a.v0 + row + lane;
+        if (r < a.vocab) {
+#pragma unroll
+            for (int i = 0; i < WIDTH; ++i)
+                if (col + c + i < a.dim)
+                    a.dweight[r * a.lddw + col + c + i] = (uint16_t)pack2<DT>(v[i] * unit, 0.0f);
+        }
+        // An empty group in the place of the box's store: the boxes take turns, and what store_read<1>
+        // leaves pending has to be the other one's.
+        if (lane == 0)
+            store_commit();
+        return;
+    }
+    unsigned char *const box = staging + c / WIDTH % 2 * BOX_BYTES;
+    if (lane == 0)
+        store_read<1>();
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        uint4 o;
+        if constexpr (DH) {
+            const float *x = v + u * 4;
+            o = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        } else {
+            const float *x = v + u * 8;
+            o = make_uint4(pack2<DT>(x[0] * unit, x[1] * unit), pack2<DT>(x[2] * unit, x[3] * unit),
+                           pack2<DT>(x[4] * unit, x[5] * unit), pack2<DT>(x[6] * unit, x[7] * unit));
+        }
+        *reinterpret_cast<uint4 *>(box + lane * 128 + ((u ^ (lane & 7)) * 16)) = o;
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (DH && a.first)
+            tma_store(&a.dh, col + c, row, box);
+        else if (DH)
+            tma_add(&a.dh, col + c, row, box);
+        else
+            tma_store(&a.dw, col + c, a.v0 + row, box);
+        store_commit();
+    }
+}
+
+// A warp's 32 rows x 128 columns of a product to memory from the only sums of it in tensor memory (`free`: the
+// barrier that gives the accumulators back; 0: there were no products, the sums are 0), where they are `wanted` (rows
+// of a tile behind the last one are not): piece by piece, so that the first one is on its way early.
+template <int DT, bool DH>
+__device__ __forceinline__ void store_short(const ProductArgs &a, bool ok, uint32_t from, uint32_t free, int row, int col,
+                                            bool wanted, float unit, unsigned char *staging, int lane)
+{
+    constexpr int WIDTH = PRODUCT_WIDTH<DH>;
 #pragma unroll
     for (int c = 0; c < HALF; c += WIDTH) {
         float v[WIDTH];
@@ -977,55 +1035,26 @@ __device__ __forceinline__ void store_product(const ProductArgs &a, bool ok, uin
             if (lane == 0)
                 arrive_at(free);
         }
-        if (!wanted)
-            continue;
-        if (!DH && a.dim % 8 != 0 && col + c < a.dim && col + c + WIDTH > a.dim) {
-            // (a map's box ends on 16 bytes, here beyond the row)
-            const int64_t r = (int64_t)a.v0 + row + lane;
-            if (r < a.vocab) {
-#pragma unroll
-                for (int i = 0; i < WIDTH; ++i)
-                    if (col + c + i < a.dim)
-                        a.dweight[r * a.lddw + col + c + i] = (uint16_t)pack2<DT>(v[i] * unit, 0.0f);
-            }
-            // An empty group in the place of the box's store: the boxes take turns, and what store_read<1>
-            // leaves pending has to be the other one's.
-            if (lane == 0)
-                store_commit();
-            continue;
-        }
-        unsigned char *const box = staging + c / WIDTH % 2 * BOX_BYTES;
-        if (lane == 0)
-            store_read<1>();
-        __syncwarp();
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            uint4 o;
-            if constexpr (DH) {
-                const float *x = v + u * 4;
-                o = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-            } else {
-                const float *x = v + u * 8;
-                o = make_uint4(pack2<DT>(x[0] * unit, x[1] * unit), pack2<DT>(x[2] * unit, x[3] * unit),
-                               pack2<DT>(x[4] * unit, x[5] * unit), pack2<DT>(x[6] * unit, x[7] * unit));
-            }
-            *reinterpret_cast<uint4 *>(box + lane * 128 + ((u ^ (lane & 7)) * 16)) = o;
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if (DH && a.first)
-                tma_store(&a.dh, col + c, row, box);
-            else if (DH)
-                tma_add(&a.dh, col + c, row, box);
-            else
-                tma_store(&a.dw, col + c, a.v0 + row, box);
-            store_commit();
-        }
+        if (wanted)
+            store_columns<DT, DH>(a, v, row, col, c, unit, staging, lane);
     }
 }
+// The same from registers.
+template <int DT, bool DH>
+__device__ __forceinline__ void store_long(const ProductArgs &a, const float (&z)[HALF], int row, int col, float unit,
+                                           unsigned char *staging, int lane)
+{
+#pragma unroll
+    for (int c = 0; c < HALF; c += PRODUCT_WIDTH<DH>)
+        store_columns<DT, DH>(a, z + c, row, col, c, unit, staging, lane);
+}
 
-template <int DT>
+// LONG: products of more than SHORT_PRODUCTS blocks of K, summed in chunks of CHUNK_PRODUCTS.  (Tiles of many rows
+// take the same time either way, as long as the registers stay below 168: with a split of them between the warps, as for
+// the tiles of logits, the warp that issues products is too slow, and 4096 x 2048 x 50257 bf16 takes 1010 us instead of
+// 934.  dw of few rows, which is no more than a way to memory, takes 161 us instead of 147 at 128 x 4096 x 32768.  There one
+// thread issues the products: when they are issued faster, dh's reads and dw's writes mix less, 16 x 4096 x 50257 268 -> 281.)
+template <int DT, bool LONG>
 __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const __grid_constant__ ProductArgs a)
 {
     extern __shared__ unsigned char raw[];
@@ -1085,14 +1114,15 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
                 drain_copies(b, pos, rank);
                 break;
             }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0 && (LONG || lane == 0)) {
+        const bool issues = LONG ? elect_one() : true;
         RingPos<> pos;
         AccPos acc;
         for (int i = 0, t; (t = tile_of(i)) >= 0; ++i) {
             const TileJob j = job(t);
-            if (!multiply_tile(j, b, ring, pos, acc, instruction_desc(DT == RED_BF16, j.a_along_k, j.b_along_k),
-                               1 << 30)) {
-                drain_products(b);
+            if (!multiply_tile<LONG>(j, b, ring, pos, acc, instruction_desc(DT == RED_BF16, j.a_along_k, j.b_along_k),
+                               LONG ? CHUNK_PRODUCTS : SHORT_PRODUCTS, issues)) {
+                drain_products<LONG>(b, issues);
                 break;
             }
         }
@@ -1104,18 +1134,33 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
         const float unit = a.work.head->unit;
         for (int i = 0, t; (t = tile_of(i)) >= 0; ++i) {
             const TileJob j = job(t);
-            const bool ok = j.blocks == 0 || mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
-            tmem_after();
-            const uint32_t from = b.tmem + ((uint32_t)(group * 32) << 16) + acc.slot * TILE + half * HALF;
             const int row = j.a_row + rank * HALF + group * 32, col = j.b_row + half * HALF;
-            const uint32_t free = j.blocks == 0 ? 0 : empty[acc.slot];
-            if (t < h_tiles)
-                store_product<DT, true>(a, ok, from, free, row + t / h_each * (int)a.work.padded, col, row < live, unit,
-                                        staging, lane);
-            else
-                store_product<DT, false>(a, ok, from, free, row, col, true, unit, staging, lane);
-            if (j.blocks != 0)
-                acc.next();
+            if constexpr (LONG) {
+                float z[HALF];
+                if (!take_sums<CHUNK_PRODUCTS>(z, b, acc, j.blocks, (uint32_t)(group * 32) << 16, half, empty) ||
+                    j.blocks == 0) {
+                    // a wait ran out, or there are no products
+#pragma unroll
+                    for (int k = 0; k < HALF; ++k)
+                        z[k] = j.blocks == 0 ? 0.0f : __builtin_nanf("");
+                }
+                if (t >= h_tiles)
+                    store_long<DT, false>(a, z, row, col, unit, staging, lane);
+                else if (row < live)
+                    store_long<DT, true>(a, z, row + t / h_each * (int)a.work.padded, col, unit, staging, lane);
+            } else {
+                const bool ok = j.blocks == 0 || mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
+                tmem_after();
+                const uint32_t from = b.tmem + ((uint32_t)(group * 32) << 16) + acc.slot * TILE + half * HALF;
+                const uint32_t free = j.blocks == 0 ? 0 : empty[acc.slot];
+                if (t < h_tiles)
+                    store_short<DT, true>(a, ok, from, free, row + t / h_each * (int)a.work.padded, col, row < live, unit,
+                                          staging, lane);
+                else
+                    store_short<DT, false>(a, ok, from, free, row, col, true, unit, staging, lane);
+                if (j.blocks != 0)
+                    acc.next();
+            }
         }
         if (lane == 0)
             store_done();
@@ -1281,11 +1326,18 @@ int launch_logits(int64_t tiles, cudaStream_t s, const LogitArgs &a)
     static std::atomic<int> cache[MAX_DEVICES];
     return launch_pairs(linear_logits_kernel<DT, GRAD>, cache, tiles, s, a, "linear_logits");
 }
-template <int DT>
+template <int DT, bool LONG>
 int launch_products(int64_t tiles, cudaStream_t s, const ProductArgs &a)
 {
     static std::atomic<int> cache[MAX_DEVICES];
-    return launch_pairs(linear_products_kernel<DT>, cache, tiles, s, a, "linear_products");
+    return launch_pairs(linear_products_kernel<DT, LONG>, cache, tiles, s, a, "linear_products");
+}
+template <int DT>
+int launch_products(int64_t tiles, cudaStream_t s, const ProductArgs &a)
+{
+    const int64_t blocks = up(a.v_count, BLOCK_K) / BLOCK_K;  // of dh; dw of few rows has two at most
+    return a.few && (blocks + a.splits - 1) / a.splits <= SHORT_PRODUCTS ? launch_products<DT, false>(tiles, s, a)
+                                                                         : launch_products<DT, true>(tiles, s, a);
 }
 
 template <int DT, bool GRAD, int ROWS>

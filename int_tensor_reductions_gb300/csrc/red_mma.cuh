@@ -269,10 +269,15 @@ struct AccPos {
     }
 };
 
-// The products of one tile (one thread of the leader), handed over after every
-// `chunk` blocks of K, each time in the other accumulator.  Whether to go on.
+// The products of one tile (by the leading CTA), handed over after every `chunk` blocks of
+// K, each time in the other accumulator.  Whether to go on.
+// WARP: all lanes of a warp wait and one, the one that `issues` (elect_one()), issues: what the
+// products take is then known to be the same for the warp, and one thread's moving it there
+// takes as long as the products of a block (forward 6144 x 4096 x 65536 1775 -> 1662 us, 2777 x 1024 x 50257 168 -> 156).
+// Else one thread calls.
+template <bool WARP>
 __device__ __forceinline__ bool multiply_tile(const TileJob &j, MmaBarriers &b, const unsigned char *ring, RingPos<> &pos,
-                                              AccPos &acc, uint32_t idesc, int chunk)
+                                              AccPos &acc, uint32_t idesc, int chunk, bool issues)
 {
     const uint64_t ka = step_k(j.a_along_k), kb = step_k(j.b_along_k);
     for (int k0 = 0; k0 < j.blocks; k0 += chunk) {
@@ -287,13 +292,20 @@ __device__ __forceinline__ bool multiply_tile(const TileJob &j, MmaBarriers &b, 
             tmem_after();
             const unsigned char *at = ring + pos.stage * STAGE_BYTES;
             const uint64_t da = operand_desc(at, j.a_along_k), db = operand_desc(at + OPERAND_BYTES, j.b_along_k);
+            if (issues) {
 #pragma unroll
-            for (int s = 0; s < BLOCK_K / 16; ++s)
-                mma(d, da + s * ka, db + s * kb, idesc, k > k0 || s > 0);
-            mma_commit(&b.empty[pos.stage]);
+                for (int s = 0; s < BLOCK_K / 16; ++s)
+                    mma(d, da + s * ka, db + s * kb, idesc, k > k0 || s > 0);
+                mma_commit(&b.empty[pos.stage]);
+            }
+            if (WARP)
+                __syncwarp();
             pos.next();
         }
-        mma_commit(&b.acc_full[acc.slot]);
+        if (issues)
+            mma_commit(&b.acc_full[acc.slot]);
+        if (WARP)
+            __syncwarp();
         acc.next();
     }
     return true;
@@ -348,9 +360,13 @@ __device__ __forceinline__ void drain_copies(MmaBarriers &b, const RingPos<> &po
             for (int n = 0; n < 65536 && !mbar_try(&b.full[k], k < pos.stage ? pos.phase : pos.phase ^ 1); ++n) {
             }
 }
-__device__ __forceinline__ void drain_products(MmaBarriers &b)
+template <bool WARP>
+__device__ __forceinline__ void drain_products(MmaBarriers &b, bool issues)
 {
-    mma_commit(&b.drain);
+    if (issues)
+        mma_commit(&b.drain);
+    if (WARP)
+        __syncwarp();
     for (int n = 0; n < 65536 && !mbar_try(&b.drain, 0); ++n) {
     }
 }
