@@ -109,6 +109,10 @@ __device__ __forceinline__ void begin_sums(const BalanceArgs &a, RowSums<N, E> &
     s.z = s.d = 0.0f;
 }
 
+// The sigmoid of what balance_row keeps of it.
+__device__ __forceinline__ bool negative(float e) { return __float_as_int(e) < 0; }
+__device__ __forceinline__ float numerator(float e) { return negative(e) ? 1.0f + e : e; }
+
 // One token's logits: its probabilities into the sums, its gradient to memory.
 // `here`: there is such a token; a group without one goes along.
 template <int DT, bool SIGMOID, int LANES, bool VEC, int N, int E>
@@ -135,23 +139,30 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
         }
     }
     float off = 0.0f;  // (differences first: a row of the type's lowest value has no room for a product)
-    float e[N][E];  // exponentials, or sigmoids
+    // exponentials, or of a sigmoid and its complement the smaller one, negative where it is the complement: 1 - s of an s
+    // near 1 has no digits (at a logit of 10 it was off by 5e-4, from 17 on it was 0, and so was the gradient)
+    float e[N][E];
     if constexpr (!SIGMOID) {
         top = group_fold<LANES>(top, sh, turn, Max());
         off = top == NEG_INF ? 0.0f : top;
     }
     // sum of e and of e * c, for sum of p * c
     float2 sums = make_float2(0.0f, 0.0f);
-    [[maybe_unused]] float keep = 1.0f;  // sigmoids: e is p's numerator and the sigmoid; 0: the numerator alone
+    [[maybe_unused]] float keep = 1.0f;  // sigmoids: 0 where e is p's numerator alone, and the complement 1
 #pragma unroll
     for (int v = 0; v < N; ++v)
 #pragma unroll
         for (int k = 0; k < E; ++k) {
-            e[v][k] = SIGMOID ? __fdividef(1.0f, 1.0f + ex2(-x[v][k] * LOG2E)) : ex2((x[v][k] - off) * LOG2E);
-            if (SIGMOID && x[v][k] == NEG_INF)
-                e[v][k] = 0.0f;
-            sums.x += e[v][k];
-            sums.y = fmaf(e[v][k], s.c[v][k], sums.y);
+            float n;  // of p: its numerator
+            if constexpr (SIGMOID) {
+                const float u = ex2(-fabsf(x[v][k]) * LOG2E), r = __fdividef(1.0f, 1.0f + u);
+                n = x[v][k] >= 0.0f ? r : u * r;
+                e[v][k] = x[v][k] >= 0.0f ? -(u * r) : n;
+            } else {
+                n = e[v][k] = ex2((x[v][k] - off) * LOG2E);
+            }
+            sums.x += n;
+            sums.y = fmaf(n, s.c[v][k], sums.y);
         }
     sums = group_sums<LANES>(sums, sh, turn);
     if constexpr (SIGMOID) {
@@ -174,8 +185,9 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
                 for (int k = 0; k < E; ++k) {
                     if (low)
                         e[v][k] = top < -700.0f ? 0.0f : ex2((x[v][k] - top) * LOG2E);
-                    sums.x += e[v][k];
-                    sums.y = fmaf(e[v][k], s.c[v][k], sums.y);
+                    const float n = numerator(e[v][k]);
+                    sums.x += n;
+                    sums.y = fmaf(n, s.c[v][k], sums.y);
                 }
             sums = group_sums<LANES>(sums, sh, turn);
         }
@@ -195,7 +207,7 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
         for (int v = 0; v < N; ++v)
 #pragma unroll
             for (int k = 0; k < E; ++k)
-                x[v][k] = e[v][k] * inv;
+                x[v][k] = (SIGMOID ? numerator(e[v][k]) : e[v][k]) * inv;
     }
 #pragma unroll
     for (int v = 0; v < N; ++v)
@@ -218,7 +230,8 @@ __device__ __forceinline__ void balance_row(const BalanceArgs &a, const Raw (&ra
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             const float p = x[v][k];
-            g[k] = (SIGMOID ? p * fmaf(-keep, e[v][k], 1.0f) : p) * fmaf(s.c[v][k], s.unit, shift);
+            g[k] = (SIGMOID ? p * (negative(e[v][k]) ? -e[v][k] : fmaf(-keep, e[v][k], 1.0f)) : p) *
+                   fmaf(s.c[v][k], s.unit, shift);
         }
         store_unit<DT, VEC, LANES>(a.dx, r * a.ldd, (v * LANES + lane) * E, a.experts, here, g);
     }
