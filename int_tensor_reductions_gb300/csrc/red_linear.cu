@@ -29,15 +29,16 @@ namespace {
 // Blocks of 64 of K whose products are summed by the tensor cores before the sum
 // moves to fp32 registers (tiles of 256 x 256; of few rows, see Few).  The tensor cores'
 // additions round toward zero, so a long sum drifts with its number of steps, four to a
-// block, and lse with the logits: by -1.9e-6 on average at logits of a bell of width 1.5 (lse 11,
-// dim 1024 to 8192), -1.2e-6 with 12 blocks and -0.8e-6 with 8, while 6144 x 4096 x 65536 bf16
-// takes 1660, 1713 and 1808 us.  Against 64 bits logp is then off by 2.8e-7 to 3.9e-7 of its norm
-// (300 rows; fp32 products of torch: 2.4e-7 at dim 1024, 5.8e-7 at 4096, 8.7e-7 at 8192).
+// block, and lse with the logits: by -0.8e-6 on average at logits of a bell of width 1.5 (lse 11,
+// dim 1024 to 8192; -1.9e-6 with 16 blocks), while 6144 x 4096 x 65536 bf16 takes 1675 us (1643
+// with 16) and 2777 x 1024 x 50257 168 (162).  Against 64 bits logp is then off by 1.4e-7 to 2.0e-7 of its
+// norm (300 rows; fp32 products of torch: 2.4e-7 at dim 1024, 5.8e-7 at 4096, 8.7e-7 at 8192).
+// The gradients' logits, whose p are rounded to 16 bits, take 16.
 // What the drift would do most harm to is the target's logit: the likelihood of a token that
 // is all but certain is the distance of its logit from the others', and logits at the
 // end of the range drift furthest.  That one is summed apart (dot_by_warp): a
 // reading of N rows of both matrices.
-constexpr int CHUNK = 16;
+constexpr int CHUNK = 8, CHUNK_GRAD = 16;
 // The same of the gradients' sums, which are rounded to 16 bits at the end.  256 steps of terms of one sign are off by
 // 3e-5 (measured: 1e-7 a step, of dw of 262144 rows -1.65e-3 in one run, three times f16's rounding, and -2e-5
 // in runs of these); a sum of up to SHORT_PRODUCTS blocks, 1e-4, may be one run where rows are few.
@@ -449,7 +450,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
         AccPos acc;
         const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true);
         for (int t = pair; t < tiles; t += pairs)
-            if (!multiply_tile<true>(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, acc, idesc, CHUNK, issues)) {
+            if (!multiply_tile<true>(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, acc, idesc,
+                                     GRAD ? CHUNK_GRAD : CHUNK, issues)) {
                 drain_products<true>(b, issues);
                 break;
             }
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
             float gt = 0.0f, cp = 0.0f, lse2 = 0.0f;
             if (GRAD && takes)
                 gt = a.work.at_target[row], cp = a.work.by_p[row], lse2 = a.work.lse2[row];
-            const bool ok = take_sums<CHUNK>(z, b, acc, a.k_blocks, (uint32_t)(group * 32) << 16, half, empty);
+            const bool ok = take_sums<GRAD ? CHUNK_GRAD : CHUNK>(z, b, acc, a.k_blocks, (uint32_t)(group * 32) << 16, half, empty);
             constexpr float NOTHING = __builtin_nanf("");
             if constexpr (!GRAD) {
                 if (tail) {

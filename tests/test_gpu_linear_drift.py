@@ -3,8 +3,8 @@
 Products are positive and of about one size, so that a partial sum grows by an even share with each step: n steps in
 a row are off by less than an ulp each, 2u of the partial sum (u = 2**-24), in all by (n + 1)u of the whole, and the
 additions of m such sums to nearest by (m + 1) / 2 u.  dim is 1024, 16 blocks of 64: of up to 32 rows eight sums of 8
-steps (9u + 4.5u), up to 64 rows four of 16 (17u + 2.5u), up to 128 two times two of 16 (the same), beyond one of 64
-(65u + u).  lse is a mean of logits that are off by that, beside 1.2e-5 and its own rounding (2u).
+steps (9u + 4.5u), up to 64 rows four of 16 (17u + 2.5u), up to 128 two times two of 16 (the same), beyond two of 32
+(33u + 1.5u).  lse is a mean of logits that are off by that, beside 1.2e-5 and its own rounding (2u).
 """
 import pytest
 import torch
@@ -23,7 +23,7 @@ def _lib():
 
 
 @pytest.mark.parametrize("size", [1.0, 1e4, 1e6])
-@pytest.mark.parametrize("rows,steps", [(1, 13.5), (16, 13.5), (20, 13.5), (50, 19.5), (100, 19.5), (300, 66.0)])
+@pytest.mark.parametrize("rows,steps", [(1, 13.5), (16, 13.5), (20, 13.5), (50, 19.5), (100, 19.5), (300, 34.5)])
 @pytest.mark.parametrize("dim", [1000, 1024])
 def test_logits_of_one_sign(dim, rows, steps, size):
     g = torch.Generator(device=DEV)
