@@ -493,7 +493,8 @@ int red_preference(int dtype, const void *x, int64_t rows, int64_t len, int64_t 
  *            workspace: two of them may run at the same time, with scratch
  *            and results of their own.
  * +inf or NaN in a row that takes part, or in the weights, makes NaN of what
- * depends on it.  Results are the same from call to call, bit for bit.
+ * depends on it.  A logit of -inf is a probability of 0 (and a dweight of 0 where every
+ * row has it; dhidden is NaN, as 0 * -inf is).  Results are the same from call to call, bit for bit.
  */
 int64_t red_linear_work_bytes(int64_t rows, int64_t dim, int64_t vocab, int grad);
 int red_linear_logprob(int dtype, const void *hidden, int64_t rows, int64_t dim, int64_t ldh, const void *weight,

@@ -511,6 +511,12 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
                     for (int i = 0; i < HALF; ++i)
                         z[i] = i == target ? gt : z[i];
                 }
+                if (__any_sync(0xffffffffu, !takes)) {
+                    // rows behind the last one: their logits are 0, or NaN where a weight is -inf
+#pragma unroll
+                    for (int i = 0; i < HALF; ++i)
+                        z[i] = takes ? z[i] : 0.0f;
+                }
                 if (tail) {
 #pragma unroll
                     for (int i = 0; i < HALF; ++i)
@@ -901,7 +907,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float4 c = b.coefs[i + j];
-                        x[j] = (v == b.target[i + j] ? c.y : c.x * ex2(fmaf(z[i + j], a.s2, -c.z))) + fine;
+                        const float g = v == b.target[i + j] ? c.y : c.x * ex2(fmaf(z[i + j], a.s2, -c.z));
+                        // (rows behind the last one: their logits are 0, or NaN where a weight is -inf)
+                        x[j] = (i + j < live ? g : 0.0f) + fine;
                     }
                     if (valid)
                         to[i / 8] = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),

@@ -1,4 +1,6 @@
 """Gradients of red_linear_logprob where a CTA writes several tiles of them, against the 64-bit definition."""
+import math
+
 import pytest
 import torch
 
@@ -28,3 +30,22 @@ def test_ends_of_rows_in_many_tiles(rows, dim, vocab):
     for _ in range(5):
         again = itr.red_linear_logprob_grad(hidden, weight, target, lse, dlogp)
         assert torch.equal(again[0], gh) and torch.equal(again[1], gw)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 16, 20, 64, 100, 128, 192, 250, 256, 300])
+def test_weights_gradient_with_a_token_ruled_out(rows):
+    """A token of weights -inf has probability 0 in every row, and a gradient of 0, whatever number of rows a tile holds."""
+    hidden, weight, target, dlogp, dlse = inputs(rows, 64, 900, torch.bfloat16, 0.0)
+    hidden[:, 7] = 1.0
+    weight[5, 7] = -math.inf
+    target[:] = target.where(target != 5, 6)
+    _, lse = itr.red_linear_logprob(hidden, weight, target)
+    _, gw = itr.red_linear_logprob_grad(hidden, weight, target, lse, dlogp, dlse=dlse, grad_hidden=False)
+    assert bool((gw[5] == 0).all())
+    # without the token
+    rest = torch.arange(900, device=DEV) != 5
+    moved = target - (target > 5).long()
+    ref = Reference(hidden, weight[rest], moved)
+    _, clean = itr.red_linear_logprob(hidden, weight[rest], moved)
+    ref.check_gradients(None, gw[rest], dlogp, dlse)
+    assert float((lse - clean).abs().max()) <= 2.4e-5  # (the same logits, a softmax in fp32 each)
