@@ -515,7 +515,10 @@ int red_linear_logprob(int dtype, const void *hidden, int64_t rows, int64_t dim,
  *   dhidden  rows x dim, row stride ldd, or NULL for none.  May be `hidden`.
  *   dweight  vocab x dim, row stride lddw, or NULL for none (not both).  Results
  *            must not overlap an input otherwise, nor each other.
- *   work     red_linear_work_bytes(..., 1) bytes.
+ *   work     red_linear_work_bytes(..., 1) bytes: g of a piece of the vocabulary (at most
+ *            384 MiB up to 32768 rows, 12 KiB a row beyond, 12 GiB in all, or 1 KiB a row
+ *            where that is more), the packed hidden states (2 bytes of each element)
+ *            and dhidden in fp32.
  */
 int red_linear_logprob_grad(int dtype, const void *hidden, int64_t rows, int64_t dim, int64_t ldh,
                             const void *weight, int64_t vocab, int64_t ldw, float scale, const int64_t *target,

@@ -1444,11 +1444,15 @@ LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, boo
     if (!grad) {
         take(w.part, rows * w.slots * 8);
     } else {
-        // a piece's gradient by the logits takes 256 MB; pieces narrower than 4096 columns would
-        // pass over the sums of dh too often
-        int64_t cols = ((int64_t)1 << 27) / w.padded / TILE * TILE;
-        cols = cols < 4096 ? 4096 : cols;
-        // (pieces of equal width, half as much again at most: a narrow last one leaves CTAs without work)
+        // A piece's gradient by the logits takes 256 MiB, and 4096 columns where rows are more than 32768: narrower
+        // pieces pass over the sums of dh too often (262144 x 512 x 32768 bf16: 20.6 ms, 29.8 in pieces of 2048 columns;
+        // 524288 x 256 x 32768 34.9, 91.7 in pieces of 1024).  That goes up to 8 GiB; beyond 2^20 rows
+        // pieces are narrower all the same, down to a tile's 256 columns.  Pieces are of equal width,
+        // which may be half as much again, or one tile more: a narrow last one leaves CTAs without work.
+        const int64_t most = ((int64_t)1 << 32) / w.padded;
+        int64_t cols = ((int64_t)1 << 27) / w.padded;
+        cols = cols < 4096 ? (most < 4096 ? most : 4096) : cols;
+        cols = cols < TILE ? TILE : cols / TILE * TILE;
         const int64_t pieces = w.few ? 1 : (2 * vocab + cols) / (2 * cols);
         w.piece_cols = up((vocab + (pieces > 1 ? pieces : 1) - 1) / (pieces > 1 ? pieces : 1), TILE);
         take(w.at_target, rows * 4);

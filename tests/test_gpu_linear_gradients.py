@@ -49,3 +49,12 @@ def test_weights_gradient_with_a_token_ruled_out(rows):
     _, clean = itr.red_linear_logprob(hidden, weight[rest], moved)
     ref.check_gradients(None, gw[rest], dlogp, dlse)
     assert float((lse - clean).abs().max()) <= 2.4e-5  # (the same logits, a softmax in fp32 each)
+
+
+def test_pieces_of_many_rows():
+    """Pieces of 4096 columns at most where g of them takes more than 256 MiB."""
+    hidden, weight, target, dlogp, _ = inputs(70000, 16, 9000, torch.bfloat16)
+    ref = Reference(hidden, weight, target)
+    logp, lse = itr.red_linear_logprob(hidden, weight, target)
+    ref.check_forward(logp, lse)
+    ref.check_gradients(*itr.red_linear_logprob_grad(hidden, weight, target, lse, dlogp), dlogp)
