@@ -165,8 +165,10 @@ __device__ __forceinline__ int scan_rows(const ScanArgs &a, ScanShared<NT, EACH>
         return row.target >= 0 && (!GRAD || !(row.d == 0.0f && row.n == 0.0f));
     };
     auto by_p = [&](const Row &row) { return (row.n - row.d) * a.in.scale; };
+    // (a coefficient that is no number, or infinite, is its row's matter)
+    auto size = [](float v) { return fabsf(v) < __builtin_huge_valf() ? fabsf(v) : 0.0f; };
     auto larger = [&](float top, const Row &row) {
-        return takes_part(row) ? fmaxf(top, fmaxf(fabsf(row.d * a.in.scale), fabsf(by_p(row)))) : top;
+        return takes_part(row) ? fmaxf(top, fmaxf(size(row.d * a.in.scale), size(by_p(row)))) : top;
     };
     Row row[EACH];
 #pragma unroll
@@ -182,7 +184,7 @@ __device__ __forceinline__ int scan_rows(const ScanArgs &a, ScanShared<NT, EACH>
         for (int64_t r = ROUND + tid; r < a.in.rows; r += NT)
             top = larger(top, load(r));
         top = block_fold<NT>(top, sh.tops, [](float x, float y) { return fmaxf(x, y); });
-        if (top > 0.0f && top < __builtin_huge_valf())
+        if (top > 0.0f)
             unit = fminf(fmaxf(top, 1e-32f), 1e36f) / most_of(a.in.dtype);
     }
     const float inv = 1.0f / unit;

@@ -58,3 +58,20 @@ def test_pieces_of_many_rows():
     logp, lse = itr.red_linear_logprob(hidden, weight, target)
     ref.check_forward(logp, lse)
     ref.check_gradients(*itr.red_linear_logprob_grad(hidden, weight, target, lse, dlogp), dlogp)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows", [40, 300])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_coefficient_that_is_no_number(bad, rows, dtype):
+    """An infinite dlogp is its row's matter: the others' hidden gradients are what they are without that row."""
+    hidden, weight, target, dlogp, dlse = inputs(rows, 72, 3000, dtype, 0.0)
+    dlogp, dlse = dlogp * 1e-5, dlse * 1e-5
+    _, lse = itr.red_linear_logprob(hidden, weight, target)
+    dlogp[1] = dlse[1] = 0.0
+    want, _ = itr.red_linear_logprob_grad(hidden, weight, target, lse, dlogp, dlse=dlse)
+    dlogp[1] = bad
+    got, gw = itr.red_linear_logprob_grad(hidden, weight, target, lse, dlogp, dlse=dlse)
+    rest = torch.arange(rows, device=DEV) != 1
+    assert torch.equal(got[rest], want[rest])
+    assert not bool(got[1].isfinite().any()) and not bool(gw.isfinite().any())
