@@ -564,7 +564,8 @@ enum red_quant {
  * red_rmsnorm_quant -- the same with y in 8 bits and a scale for each `block`
  * neighbouring values of a row (32, 64 or 128; the last block of a row may be
  * shorter), or for each row (block = 0):
- *     scale = max |y| / (448 or 127), 1 where that is 0;  q = y / scale, to nearest (ties to even).
+ *     scale = max |y| / (448 or 127), at least 2^-126, and 1 where every y is 0;
+ *     q = y / scale, to nearest (ties to even).
  * (The quotient is a product with the scale's inverse, within 2e-7 of it before it is rounded.)
  *   q        rows x len bytes, row stride ldq;
  *   scales   rows x ceil(len / block) floats (rows floats for block = 0).

@@ -107,15 +107,13 @@ struct Weights {
 template <int KIND>
 constexpr float TOP = KIND == RED_QUANT_E4M3 ? 448.0f : 127.0f;
 
-// The scale of values of at most `most`, and its inverse (finite where the scale
-// has none in fp32).
+// The scale of values of at most `most` (a NaN stays one): not below 2^-126, where a scale has few digits
+// and no inverse in fp32.  (Taking values and scale 2^64 times as large there costs 8 to 12% of every call: 16384 x
+// 8192 f32 in e4m3 142 -> 160 us.)
 template <int KIND>
-__device__ __forceinline__ float scale_of(float most, float *inv)
+__device__ __forceinline__ float scale_of(float most)
 {
-    const float scale = most == 0.0f ? 1.0f : most * (1.0f / TOP<KIND>);
-    const float r = __frcp_rn(scale);
-    *inv = r > 3.402823466e38f ? 3.402823466e38f : r;  // (a NaN stays one)
-    return scale;
+    return most == 0.0f ? 1.0f : Max()(most * (1.0f / TOP<KIND>), 1.175494351e-38f);
 }
 
 // A unit's values in 8 bits, to nearest, beyond the largest: the largest.  A product with
@@ -294,8 +292,8 @@ __global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VEC ? (VECS 
 #pragma unroll
             for (int v = 0; v < N; ++v) {
                 const int i = (v * LANES + lane) * E;
-                float inv;
-                const float scale = scale_of<KIND>(a.block ? most[v] : most[0], &inv);
+                const float scale = scale_of<KIND>(a.block ? most[v] : most[0]);
+                const float inv = __frcp_rn(scale);
                 if (here && i < a.len && (a.block ? (i & (a.block - 1)) == 0 : i == 0))
                     a.scales[r * a.blocks + (i >> a.block_log2)] = scale;
                 store_q<E, VEC, LANES>(static_cast<uint8_t *>(a.y), r * a.ldy, i, a.len, here, narrow8<KIND>(t[v], inv));
