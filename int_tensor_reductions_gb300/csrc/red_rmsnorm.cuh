@@ -180,14 +180,16 @@ __device__ __forceinline__ void store_q(uint8_t *q, int64_t row, int i, int len,
     }
 }
 
-// KIND: 0 for y in x's type, else the 8-bit type.
+// KIND: 0 for y in x's type, else the 8-bit type.  LONE: no residual.
 // (Registers are left to the compiler, but for two cases.  One that it makes 70 of, and three CTAs per SM: with 64, and
-// four, 16384 x 4096 bf16 91 -> 83 us.  One that it makes 92 to 128 of, and two: with 80, and three, 16384 x 5120 without a
-// residual 63 -> 58 us, in e4m3 with one 120 -> 116, but with one in bf16 135.1 -> 135.7 (and in f32, left alone, 206 ->
-// 221).  A bound of one CTA per SM has it take more than 128: 16384 x 8192 173 -> 264; 80 for rows that long are too
-// few: 85 -> 104.)
-template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC, bool RING>
-__global__ void __launch_bounds__(GROUP_CTA<LANES>, LANES == 256 && VEC ? (VECS == 2 && !RING ? 4 : VECS == 3 && RING && DT != RED_F32 ? 3 : 0) : 0)
+// four, 16384 x 4096 bf16 91 -> 83 us.  One that it makes 92 to 128 of, and two, where only x is read and y written: with
+// 80, and three, 16384 x 5120 bf16 without a residual 62.8 -> 57.2, x 6144 69.5 -> 63.2; but with one 106.0 -> 117.2 (2000 rows 12.6 -> 11.8), in e4m3 with
+// one 93.9 -> 98.5 and without 68.4 -> 72.5.  A bound of one CTA per SM has it take more than 128: 16384 x 8192 173 -> 264; 80
+// for rows that long are too few: 85 -> 104.)
+template <int LANES, int VECS, bool VEC, bool RING, bool LONE>
+constexpr int NORM_CTAS = LANES == 256 && VEC ? (VECS == 2 && !RING ? 4 : VECS == 3 && LONE ? 3 : 0) : 0;
+template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC, bool RING, bool LONE>
+__global__ void __launch_bounds__(GROUP_CTA<LANES>, NORM_CTAS<LANES, VECS, VEC, RING, LONE>)
     rmsnorm_kernel(const NormArgs a)
 {
     pdl_enter();
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(32 * JOIN_TURNS) rmsnorm_join_kernel(const Nor
 // ---------------------------------------------------------------- launches
 
 #ifndef RED_RMSNORM_BACKWARD
-template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC, bool RING>
+template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC, bool RING, bool LONE = false>
 int forward(const NormArgs &a, cudaStream_t s)
 {
     static Resident caches[2];
@@ -480,7 +482,7 @@ int forward(const NormArgs &a, cudaStream_t s)
     constexpr int NT = GROUP_CTA<LANES>, GROUPS = NT / LANES;
     using Rows = Ring<DT, VEC, LANES, UNITS<DT, VECS>, 2>;
     const size_t smem = RING ? Rows::bytes(a.residual ? 2 : 1) : 0;
-    auto *const kernel = rmsnorm_kernel<DT, WIDE, KIND, LANES, VECS, VEC, RING>;
+    auto *const kernel = rmsnorm_kernel<DT, WIDE, KIND, LANES, VECS, VEC, RING, LONE>;
     unsigned grid;
     const int st = resident_grid(kernel, cache, NT, smem, RING ? Rows::bytes(2) : 0, (a.rows + GROUPS - 1) / GROUPS,
                                  INT32_MAX, &grid);
@@ -506,6 +508,10 @@ int forward_of(const NormArgs &a, int kind, cudaStream_t s)
         if constexpr (DIRECT) {
             if (kind == 0 && a.residual && a.len > 6 * L * V)
                 return forward<DT, WIDE, 0, L, V, VEC, false>(a, s);
+        }
+        if constexpr (VEC && V == 3 && L == 256 && DT != RED_F32) {
+            if (kind == 0 && !a.residual)
+                return forward<DT, WIDE, 0, L, V, VEC, true, true>(a, s);
         }
         return kind == 0                ? forward<DT, WIDE, 0, L, V, VEC, true>(a, s)
                : kind == RED_QUANT_E4M3 ? forward<DT, WIDE, RED_QUANT_E4M3, L, V, VEC, true>(a, s)
