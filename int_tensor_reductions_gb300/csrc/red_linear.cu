@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
         for (int t = pair; t < tiles; t += pairs)
             if (!multiply_tile<true>(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, acc, idesc,
                                      GRAD ? CHUNK_GRAD : CHUNK, issues)) {
-                drain_products<true>(b, issues);
+                drain_products(b, issues);
                 break;
             }
     } else if (warp >= 4) {
@@ -795,13 +795,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
         const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true, HALF, ROWS);
         for (int v = begin; v < end && ok; v += a.height)
             for (int k0 = 0; k0 < a.k_blocks && ok; k0 += F::CHUNK) {
-                if (!mbar_wait(&b.acc_empty[acc.slot], acc.phase ^ 1, &b.failed, 0)) {
+                if (!agreed(mbar_wait(&b.acc_empty[acc.slot], acc.phase ^ 1, &b.failed, 0))) {
                     ok = false;
                     break;
                 }
                 tmem_after();
                 for (int k = k0; k < min(k0 + F::CHUNK, a.k_blocks); ++k) {
-                    if (!mbar_wait(&b.full[pos.stage], pos.phase, &b.failed, 0)) {
+                    if (!agreed(mbar_wait(&b.full[pos.stage], pos.phase, &b.failed, 0))) {
                         ok = false;
                         break;
                     }
@@ -815,18 +815,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
                             mma_alone(d, da + s * step_k(true), db + s * step_k(true), idesc, k - k0 >= F::ACCS || s > 0);
                         mma_commit_alone(&b.empty[pos.stage]);
                     }
-                    __syncwarp();
                     pos.next();
                 }
                 if (ok && issues)
                     mma_commit_alone(&b.acc_full[acc.slot]);
-                __syncwarp();
                 acc.next();
             }
         if (!ok) {
             if (issues)
                 mma_commit_alone(&b.drain);
-            __syncwarp();
             for (int n = 0; n < 65536 && !mbar_try(&b.drain, 0); ++n) {
             }
         }
@@ -1134,7 +1131,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
             const TileJob j = job(t);
             if (!multiply_tile<LONG>(j, b, ring, pos, acc, instruction_desc(DT == RED_BF16, j.a_along_k, j.b_along_k),
                                LONG ? CHUNK_PRODUCTS : SHORT_PRODUCTS, issues)) {
-                drain_products<LONG>(b, issues);
+                drain_products(b, issues);
                 break;
             }
         }

@@ -159,6 +159,13 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// Whether all lanes of a warp say so (WARP false: the one thread).
+template <bool WARP = true>
+__device__ __forceinline__ bool agreed(bool ok)
+{
+    return WARP ? __all_sync(0xffffffffu, ok) != 0 : ok;
+}
+
 // 16 columns of this warp's 32 lanes of tensor memory: lane i gets row i.
 __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t *v)
 {
@@ -274,20 +281,20 @@ struct AccPos {
 // WARP: all lanes of a warp wait and one, the one that `issues` (elect_one()), issues: what the
 // products take is then known to be the same for the warp, and one thread's moving it there
 // takes as long as the products of a block (forward 6144 x 4096 x 65536 1775 -> 1662 us, 2777 x 1024 x 50257 168 -> 156).
-// Else one thread calls.
+// The lanes agree on each wait, one of which may have run out.  Else one thread calls.
 template <bool WARP>
 __device__ __forceinline__ bool multiply_tile(const TileJob &j, MmaBarriers &b, const unsigned char *ring, RingPos<> &pos,
                                               AccPos &acc, uint32_t idesc, int chunk, bool issues)
 {
     const uint64_t ka = step_k(j.a_along_k), kb = step_k(j.b_along_k);
     for (int k0 = 0; k0 < j.blocks; k0 += chunk) {
-        if (!mbar_wait(&b.acc_empty[acc.slot], acc.phase ^ 1, &b.failed, 0))
+        if (!agreed<WARP>(mbar_wait(&b.acc_empty[acc.slot], acc.phase ^ 1, &b.failed, 0)))
             return false;
         tmem_after();
         const uint32_t d = b.tmem + acc.slot * TILE;
         const int k1 = min(k0 + chunk, j.blocks);
         for (int k = k0; k < k1; ++k) {
-            if (!mbar_wait(&b.full[pos.stage], pos.phase, &b.failed, 0))
+            if (!agreed<WARP>(mbar_wait(&b.full[pos.stage], pos.phase, &b.failed, 0)))
                 return false;
             tmem_after();
             const unsigned char *at = ring + pos.stage * STAGE_BYTES;
@@ -298,14 +305,10 @@ __device__ __forceinline__ bool multiply_tile(const TileJob &j, MmaBarriers &b, 
                     mma(d, da + s * ka, db + s * kb, idesc, k > k0 || s > 0);
                 mma_commit(&b.empty[pos.stage]);
             }
-            if (WARP)
-                __syncwarp();
             pos.next();
         }
         if (issues)
             mma_commit(&b.acc_full[acc.slot]);
-        if (WARP)
-            __syncwarp();
         acc.next();
     }
     return true;
@@ -360,13 +363,10 @@ __device__ __forceinline__ void drain_copies(MmaBarriers &b, const RingPos<> &po
             for (int n = 0; n < 65536 && !mbar_try(&b.full[k], k < pos.stage ? pos.phase : pos.phase ^ 1); ++n) {
             }
 }
-template <bool WARP>
 __device__ __forceinline__ void drain_products(MmaBarriers &b, bool issues)
 {
     if (issues)
         mma_commit(&b.drain);
-    if (WARP)
-        __syncwarp();
     for (int n = 0; n < 65536 && !mbar_try(&b.drain, 0); ++n) {
     }
 }
