@@ -80,11 +80,6 @@ __device__ __forceinline__ void store_read()
 }
 __device__ __forceinline__ void store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
-{
-    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
-
 // Tensor memory of the pair: all 512 columns in each of its CTAs.  One warp of
 // each CTA.
 __device__ __forceinline__ void tmem_alloc(uint32_t *where)
