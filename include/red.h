@@ -510,7 +510,9 @@ int red_linear_logprob(int dtype, const void *hidden, int64_t rows, int64_t dim,
  * exact as lse: off by the rounding of a number of its size).  A row
  * whose dlogp and dlse are both 0 is ignored, too.  The vocabulary is taken in
  * pieces; g is rounded to dtype once, in units that the largest coefficient
- * sets, and each result once more; their sums are fp32, those of a run of up to
+ * sets, and each result once more (in f16 the unit is the same for all rows: of a
+ * row whose coefficient is 1e-6 of the largest, probabilities below 4e-3 are
+ * rounded to steps of 4e-6, and its dhidden with them); their sums are fp32, those of a run of up to
  * 4096 rows or columns (16384 columns where rows are up to 128) by the tensor cores.
  *   dhidden  rows x dim, row stride ldd, or NULL for none.  May be `hidden`.
  *   dweight  vocab x dim, row stride lddw, or NULL for none (not both).  Results
@@ -535,7 +537,7 @@ int red_linear_logprob_grad(int dtype, const void *hidden, int64_t rows, int64_t
  *            gradients; wtype: dtype or RED_F32, of weight and dweight.
  *            Arithmetic is in fp32; each result is rounded once, to nearest (y
  *            from the sum t before it is rounded to total).
- *   rows, len   1 <= len <= RED_RMSNORM_MAX_LEN; each matrix has a row stride of
+ *   rows, len   rows up to 2^30, 1 <= len <= RED_RMSNORM_MAX_LEN; each matrix has a row stride of
  *            its own (>= len), needs the alignment of its elements only, and is
  *            not touched between columns len and its stride.  Rows on 16-byte
  *            boundaries are read fastest.
@@ -545,7 +547,8 @@ int red_linear_logprob_grad(int dtype, const void *hidden, int64_t rows, int64_t
  *            must not overlap them otherwise, nor each other.
  *   rstd     rows floats (the backward wants them), or NULL.
  *   eps      0 .. 1e30.
- * Squares are summed in fp32: rows of values beyond 1e19 overflow.  NaN and
+ * Squares are summed in fp32: rows of values beyond 1e19 overflow, and with eps = 0
+ * rows of values below 1e-19 lose digits.  NaN and
  * infinities spread over their row and no further (in dweight, over their
  * column).  Results are the same from call to call, bit for bit.
  */
@@ -614,9 +617,9 @@ enum red_balance_kind {
  *            0 for a token that is out, whatever its logits hold.  May be x
  *            (ldd == ld then), or NULL for none.
  * -inf takes an expert out of a token's choice; a token with nothing else (and, of
- * sigmoids, one with nothing above -700) has no probabilities and a gradient of 0.  NaN (and +inf, of a softmax) in a token
- * that takes part makes its gradient, prob and the loss NaN.  Results are the same from call to
- * call, bit for bit.  Uses the workspace.
+ * sigmoids, one with nothing above -700) has no probabilities and a gradient of 0.  NaN
+ * (and +inf, of a softmax) in a token that takes part makes its gradient, prob and the
+ * loss NaN.  Results are the same from call to call, bit for bit.  Uses the workspace.
  */
 #define RED_BALANCE_MAX_EXPERTS 4096
 int red_balance(int dtype, const void *x, int64_t rows, int64_t experts, int64_t ld, const int64_t *ids, int64_t k,

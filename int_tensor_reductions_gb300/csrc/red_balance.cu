@@ -11,8 +11,9 @@
 // so that after the counts one pass reads the logits, writes the gradient and
 // sums p.  Three kernels: counts (integer atomics: any order gives the same),
 // rows, and a join of the CTAs' sums; one CTA does all three where tokens are
-// few.  Bound by the logits' and the gradient's way through memory, or for
-// few tokens by latency.
+// few.  Bound by instructions: 65536 x 256 sigmoids take 33.0 us in f32 and 29.7 in
+// bf16, half the bytes (softmax 31.7, 26.2; memory's share 19.9 and 10), and the rows' kernel 74%
+// of the issue slots.  Few tokens are bound by latency.
 #include "red_balance.cuh"
 #include "red_groups.cuh"
 #include "red_prims.cuh"

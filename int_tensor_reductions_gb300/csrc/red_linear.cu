@@ -658,8 +658,9 @@ __global__ void __launch_bounds__(256)
 // states the one with ROWS = 16, 32, 64 or 128, and each CTA takes an equal share of the
 // vocabulary in tiles of equal height (up to 128), so that all SMs stream weights to the
 // end; a tile is one copy per block of K, whatever its height.  Forward, us, with tiles of
-// 256 x 256 / of 128 with an end in boxes of 16 / of equal height / the rows unpacked
-// (as it is): 1 x 2048 x 65536 61, 58, 52, 47; 16 x 4096 x 50257 -, 88, 75, 69.  The
+// 256 x 256 / of 128 with an end in boxes of 16 / of equal height / the rows unpacked / the
+// products issued by an elected lane, from several sums (as it is): 1 x 2048 x 65536 61, 58, 52, 47, 46;
+// 16 x 4096 x 50257 -, 88, 75, 69, 67.  The
 // stages in flight are not what bounds it (4 of 18 KB instead of 11 cost 8%, 7 cost 2%),
 // nor is the rows' distance in memory; 128 bytes of each of many rows at a time come at 5.4
 // to 5.7 TB/s where one stream of all rows comes at 6.5.

@@ -80,6 +80,7 @@ __device__ __forceinline__ void store_read()
 }
 __device__ __forceinline__ void store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // Tensor memory of the pair: all 512 columns in each of its CTAs.  One warp of
 // each CTA.
 __device__ __forceinline__ void tmem_alloc(uint32_t *where)
