@@ -475,7 +475,7 @@ int red_preference(int dtype, const void *x, int64_t rows, int64_t len, int64_t 
  *     lse[r] = log sum_j e^z[r, j],  logp[r] = z[r, target[r]] - lse[r].
  * Conventions:
  *   dtype    RED_F16 or RED_BF16, of all matrices.  Products are summed in fp32,
- *            those of a run of 128 to 512 of dim by the tensor cores (each of their
+ *            those of a run of 128 to 704 of dim by the tensor cores (each of their
  *            steps of 16 rounds toward zero); logits (up to 1e9 in magnitude), maxima
  *            and sums of exponentials are fp32 throughout.
  *   hidden   rows x dim, row stride ldh;  weight: vocab x dim, row stride ldw.

@@ -39,6 +39,12 @@ namespace {
 // end of the range drift furthest.  That one is summed apart (dot_by_warp): a
 // reading of N rows of both matrices.
 constexpr int CHUNK = 8, CHUNK_GRAD = 16;
+// Chunks of about CHUNK blocks, of equal length: 9 blocks are one chunk, not 8 and 1 (198 x 528 x 81709 30.6 us; 35.3 so).
+int even_chunk(int blocks)
+{
+    const int n = (blocks + CHUNK / 2) / CHUNK;
+    return n < 2 ? blocks : (blocks + n - 1) / n;
+}
 // The same of the gradients' sums, which are rounded to 16 bits at the end.  256 steps of terms of one sign are off by
 // 3e-5 (measured: 1e-7 a step, of dw of 262144 rows -1.65e-3 in one run, three times f16's rounding, and -2e-5
 // in runs of these); a sum of up to SHORT_PRODUCTS blocks, 1e-4, may be one run where rows are few.
@@ -351,19 +357,19 @@ struct LogitArgs {
     LinearWork work;
     int v0, n_tiles;   // columns of the vocabulary: the first, and tiles from it on
     int vocab, k_blocks;
+    int chunk;         // blocks of K to a run of sums
     float s2;          // scale * log2(e)
 };
 
 // One warp's 32 rows x 128 columns of a product in fp32 registers: the sums of
-// the chunks of EACH blocks.  Whether they are right: after a wait that ran out they are whatever
+// the chunks of `each` blocks.  Whether they are right: after a wait that ran out they are whatever
 // tensor memory held (and what is made of them has to become NaN; filling them
 // here costs the registers of a second set).
-template <int EACH>
-__device__ __forceinline__ bool take_sums(float (&z)[HALF], MmaBarriers &b, AccPos &acc, int blocks, uint32_t lanes,
-                                          int half, uint32_t (&empty)[2])
+__device__ __forceinline__ bool take_sums(float (&z)[HALF], MmaBarriers &b, AccPos &acc, int blocks, int each,
+                                          uint32_t lanes, int half, uint32_t (&empty)[2])
 {
     bool ok = true;
-    for (int k = 0; k < blocks; k += EACH) {
+    for (int k = 0; k < blocks; k += each) {
         ok &= mbar_wait(&b.acc_full[acc.slot], acc.phase, &b.failed, 0);
         tmem_after();
         const uint32_t from = b.tmem + lanes + acc.slot * TILE + half * HALF;
@@ -452,8 +458,8 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
         AccPos acc;
         const uint32_t idesc = instruction_desc(DT == RED_BF16, true, true);
         for (int t = pair; t < tiles; t += pairs)
-            if (!multiply_tile<true>(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, acc, idesc,
-                                     GRAD ? CHUNK_GRAD : CHUNK, issues)) {
+            if (!multiply_tile<true>(job(tile_at(t, m_tiles, a.n_tiles)), b, ring, pos, acc, idesc, a.chunk,
+                                     issues)) {
                 drain_products(b, issues);
                 break;
             }
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_logits_kernel(const __g
             float gt = 0.0f, cp = 0.0f, lse2 = 0.0f;
             if (GRAD && takes)
                 gt = a.work.at_target[row], cp = a.work.by_p[row], lse2 = a.work.lse2[row];
-            const bool ok = take_sums<GRAD ? CHUNK_GRAD : CHUNK>(z, b, acc, a.k_blocks, (uint32_t)(group * 32) << 16, half, empty);
+            const bool ok = take_sums(z, b, acc, a.k_blocks, a.chunk, (uint32_t)(group * 32) << 16, half, empty);
             constexpr float NOTHING = __builtin_nanf("");
             if constexpr (!GRAD) {
                 if (tail) {
@@ -666,16 +672,18 @@ __global__ void __launch_bounds__(256)
 // to 5.7 TB/s where one stream of all rows comes at 6.5.
 constexpr int FEW_ROWS = 128, FEW_THREADS = 256, FEW_MAX_CTAS = 512;
 
-template <int ROWS>
+template <int ROWS, bool GRAD>
 struct Few {
     static constexpr int STAGE = OPERAND_BYTES + ROWS * BLOCK_K * 2;
     static constexpr int N = 212992 / STAGE < 12 ? 212992 / STAGE : 12;  // stages
     static constexpr size_t SMEM = (size_t)N * STAGE + 1024;
     // The blocks of a chunk go to ACCS sums in turn, which meet in fp32 registers: 8 to 16 steps that round toward
     // zero in a row instead of the 64 of one sum of 16 blocks.  One row's log-probability stands alone, and was
-    // off by up to 2.2e-6 of itself (1 x 1024 x 32001; 6.2e-7 so).
-    static constexpr int ACCS = ROWS <= 32 ? 8 : 256 / ROWS;
-    static constexpr int CHUNK = ROWS <= 64 ? 16 : 8;
+    // off by up to 2.2e-6 of itself (1 x 1024 x 32001; 6.2e-7 so).  The gradients' logits, whose p are rounded to 16 bits,
+    // have one sum: their weights may come from L2, and the epilogue is then what a tile waits for (a step of 100 x
+    // 1024 x 32001 91 us with two sums, 88 so).
+    static constexpr int ACCS = GRAD ? 1 : ROWS <= 32 ? 8 : 256 / ROWS;
+    static constexpr int CHUNK = GRAD || ROWS <= 64 ? 16 : 8;
     static constexpr int COLUMNS = 2 * ACCS * ROWS;  // of tensor memory
     struct Shared {
         uint64_t full[N], empty[N], acc_full[2], acc_empty[2], drain;
@@ -724,7 +732,7 @@ __device__ __forceinline__ float sums_of_warp(float *v, int lane)
 template <int DT, bool GRAD, int ROWS>
 __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid_constant__ FewArgs a)
 {
-    using F = Few<ROWS>;
+    using F = Few<ROWS, GRAD>;
     extern __shared__ unsigned char raw[];
     __shared__ typename F::Shared b;
     unsigned char *const ring = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
@@ -1147,7 +1155,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
             const int row = j.a_row + rank * HALF + group * 32, col = j.b_row + half * HALF;
             if constexpr (LONG) {
                 float z[HALF];
-                if (!take_sums<CHUNK_PRODUCTS>(z, b, acc, j.blocks, (uint32_t)(group * 32) << 16, half, empty) ||
+                if (!take_sums(z, b, acc, j.blocks, CHUNK_PRODUCTS, (uint32_t)(group * 32) << 16, half, empty) ||
                     j.blocks == 0) {
                     // a wait ran out, or there are no products
 #pragma unroll
@@ -1345,9 +1353,11 @@ int launch_products(int64_t tiles, cudaStream_t s, const ProductArgs &a)
 template <int DT>
 int launch_products(int64_t tiles, cudaStream_t s, const ProductArgs &a)
 {
-    const int64_t blocks = up(a.v_count, BLOCK_K) / BLOCK_K;  // of dh; dw of few rows has two at most
-    return a.few && (blocks + a.splits - 1) / a.splits <= SHORT_PRODUCTS ? launch_products<DT, false>(tiles, s, a)
-                                                                         : launch_products<DT, true>(tiles, s, a);
+    // dw alone of up to 1024 rows, too, is bound by its way to memory (719 x 6976 x 3827 94 us, 115 by the other kernel; 1000 x
+    // 1024 x 50257 152, 153; with dh 126 and 211, 125 and 209 by the other)
+    const int64_t blocks = up(a.v_count, BLOCK_K) / BLOCK_K;  // of dh
+    const bool is_short = a.few ? (blocks + a.splits - 1) / a.splits <= SHORT_PRODUCTS : !a.with_dh && a.work.padded <= 1024;
+    return is_short ? launch_products<DT, false>(tiles, s, a) : launch_products<DT, true>(tiles, s, a);
 }
 
 template <int DT, bool GRAD, int ROWS>
@@ -1359,7 +1369,7 @@ int launch_few_rows(const LinearArgs &l, FewArgs &a, unsigned *grid, cudaStream_
     auto *const kernel = linear_few_kernel<DT, GRAD, ROWS>;
     if (!ready[di.dev].load(std::memory_order_relaxed)) {
         RETURN_IF(cuda_fail(
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Few<ROWS>::SMEM),
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Few<ROWS, GRAD>::SMEM),
             "cudaFuncSetAttribute"));
         ready[di.dev].store(true, std::memory_order_relaxed);
     }
@@ -1370,7 +1380,7 @@ int launch_few_rows(const LinearArgs &l, FewArgs &a, unsigned *grid, cudaStream_
     a.height = (share + a.tiles - 1) / a.tiles;
     *grid = (unsigned)((a.vocab + a.tiles * a.height - 1) / (a.tiles * a.height));
     RETURN_IF(matrix_map(&a.w, l.dtype, l.weight, l.dim, l.vocab, l.ldw, BLOCK_K, a.height));
-    RETURN_IF(cuda_fail(launch_pdl_smem(kernel, *grid, FEW_THREADS, Few<ROWS>::SMEM, 1, s, a), "linear_few"));
+    RETURN_IF(cuda_fail(launch_pdl_smem(kernel, *grid, FEW_THREADS, Few<ROWS, GRAD>::SMEM, 1, s, a), "linear_few"));
     count_launches(1);
     return RED_OK;
 }
@@ -1493,6 +1503,7 @@ int launch_linear_logprob(const LinearArgs &a, float *logp, float *lse, void *wo
         l.n_tiles = (int)(up(a.vocab, TILE) / TILE);
         l.vocab = (int)a.vocab;
         l.k_blocks = (int)(up(a.dim, BLOCK_K) / BLOCK_K);
+        l.chunk = even_chunk(l.k_blocks);
         l.s2 = s2;
         const int64_t tiles = w.padded / TILE * l.n_tiles;
         RETURN_IF((a.dtype == RED_BF16 ? launch_logits<RED_BF16, false>(tiles, s, l)
@@ -1535,6 +1546,7 @@ int launch_linear_logprob_grad(const LinearArgs &a, const float *lse, const floa
     l.work = p.work = w;
     l.vocab = (int)a.vocab;
     l.k_blocks = (int)(up(a.dim, BLOCK_K) / BLOCK_K);
+    l.chunk = CHUNK_GRAD;
     l.s2 = (float)(a.scale * 1.4426950408889634);
     p.n_tiles = (int)(up(a.dim, TILE) / TILE);
     p.splits = w.splits;
