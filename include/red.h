@@ -512,7 +512,9 @@ int red_linear_logprob(int dtype, const void *hidden, int64_t rows, int64_t dim,
  * pieces; g is rounded to dtype once, in units that the largest coefficient
  * sets, and each result once more (in f16 the unit is the same for all rows: of a
  * row whose coefficient is 1e-6 of the largest, probabilities below 4e-3 are
- * rounded to steps of 4e-6, and its dhidden with them); their sums are fp32, those of a run of up to
+ * rounded to steps of 4e-6, and its dhidden with them; of up to 16 rows, and of 17
+ * to 32, 33 to 64 or 65 to 128 where at most 16, 32 or 64 take part, g is kept in
+ * two such parts, 16 bits or more of it); their sums are fp32, those of a run of up to
  * 4096 rows or columns (16384 columns where rows are up to 128) by the tensor cores.
  *   dhidden  rows x dim, row stride ldd, or NULL for none.  May be `hidden`.
  *   dweight  vocab x dim, row stride lddw, or NULL for none (not both).  Results

@@ -322,6 +322,12 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const ScanArgs a)
     }
 }
 
+// Of few rows, at most half as many as there are columns of the piece: g in two parts of 16 bits, packed row r's in
+// columns r and r + few / 2, whose packed row is r's again.  A gradient by few logits is most of the results'
+// error when it is rounded to 16 bits once: of one row, every value of dw is a single product (1 to 3 rows of f16:
+// 1.1 to 1.6 times the error that rounding the results leaves; not to be seen beside it so).
+__device__ __forceinline__ bool two_parts(int live, int few) { return live <= few / 2; }
+
 // Both for up to a few thousand rows, in one launch: every CTA does the scan for itself,
 // and packs eight rows.
 constexpr int GATHER_ROWS = 4096;
@@ -330,23 +336,26 @@ __global__ void __launch_bounds__(256) linear_gather_kernel(const ScanArgs a)
 {
     pdl_enter();
     __shared__ ScanShared<256, EACH> sh;
-    __shared__ int row_of[8];
+    __shared__ int row_of[8], twin_of[8];
     const bool writes = blockIdx.x == 0;
     const int first_packed = blockIdx.x * 8;
     if (threadIdx.x < 8)
-        row_of[threadIdx.x] = -1;
+        row_of[threadIdx.x] = twin_of[threadIdx.x] = -1;
     float unit;
     const int live = scan_rows<GRAD, 256, EACH>(a, sh, writes, unit, [&](int at, int r) {
         if (at >= first_packed && at < first_packed + 8)
             row_of[at - first_packed] = r;
+        const int twin = at + a.w.few / 2 - first_packed;
+        if (GRAD && twin >= 0 && twin < 8)
+            twin_of[twin] = r;
     });
     __syncthreads();
     const int64_t r = first_packed + threadIdx.x / 32;
     if (r >= (live + TILE - 1) / TILE * TILE)
         return;
-    const int row = row_of[threadIdx.x / 32];
+    const int row = GRAD && r >= live && two_parts(live, a.w.few) ? twin_of[threadIdx.x / 32] : row_of[threadIdx.x / 32];
     pack_row(a.in.hidden, a.in.dim, a.in.ldh, a.w, r, row, threadIdx.x % 32);
-    if (GRAD && row >= 0)
+    if (GRAD && row >= 0 && r < live)
         write_at_target(a, r, row, unit, threadIdx.x % 32);
 }
 
@@ -909,9 +918,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
                 }
             } else {
                 uint4 *to = reinterpret_cast<uint4 *>(a.work.piece) + (int64_t)v * (ROWS / 8);
-#pragma unroll
-                for (int i = 0; i < ROWS; i += 8) {
-                    float x[8];
+                auto logit_gradients = [&](int i, float (&x)[8]) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float4 c = b.coefs[i + j];
@@ -919,9 +926,36 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) linear_few_kernel(const __grid
                         // (rows behind the last one: their logits are 0, or NaN where a weight is -inf)
                         x[j] = (i + j < live ? g : 0.0f) + fine;
                     }
-                    if (valid)
-                        to[i / 8] = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
-                                               pack2<DT>(x[6], x[7]));
+                };
+                auto pack8 = [](const float (&x)[8]) {
+                    return make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]),
+                                      pack2<DT>(x[6], x[7]));
+                };
+                if (two_parts(live, ROWS)) {
+#pragma unroll
+                    for (int i = 0; i < ROWS / 2; i += 8) {
+                        float x[8];
+                        logit_gradients(i, x);
+                        const uint4 whole = pack8(x);
+                        const uint32_t u[4] = {whole.x, whole.y, whole.z, whole.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {  // what that leaves
+                            x[2 * k] -= Elem<DT>::widen(u[k] & 0xffffu);
+                            x[2 * k + 1] -= Elem<DT>::widen(u[k] >> 16);
+                        }
+                        if (valid) {
+                            to[i / 8] = whole;
+                            to[i / 8 + ROWS / 16] = pack8(x);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < ROWS; i += 8) {
+                        float x[8];
+                        logit_gradients(i, x);
+                        if (valid)
+                            to[i / 8] = pack8(x);
+                    }
                 }
             }
         }
@@ -1082,7 +1116,9 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
     const int rank = cluster_rank();
     mma_begin(b, warp, lane);
     pdl_enter();
-    const int live = a.work.head->live;
+    const int taken = a.work.head->live;
+    // packed rows, with those of g's second parts
+    const int live = a.few && taken > 0 && two_parts(taken, a.work.few) ? a.work.few / 2 + taken : taken;
     const int h_rows = a.with_dh ? (live + TILE - 1) / TILE : 0;
     const int w_rows = a.with_dw ? (a.v_count + TILE - 1) / TILE : 0;
     const int h_each = h_rows * a.n_tiles, h_tiles = h_each * a.splits, tiles = h_tiles + w_rows * a.n_tiles;
@@ -1213,6 +1249,13 @@ __global__ void __launch_bounds__(256)
             for (int s = share; s < w.splits; s += SHARES) {
                 const float4 v = *reinterpret_cast<const float4 *>(from + s * split);
                 x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+            }
+            if (two_parts(w.head->live, w.few)) {
+                from += w.few / 2 * w.dim4;
+                for (int s = share; s < w.splits; s += SHARES) {
+                    const float4 v = *reinterpret_cast<const float4 *>(from + s * split);
+                    x[0] += v.x, x[1] += v.y, x[2] += v.z, x[3] += v.w;
+                }
             }
         }
         if constexpr (SHARES > 1) {
@@ -1443,6 +1486,11 @@ LinearWork linear_work(void *base, int64_t rows, int64_t dim, int64_t vocab, boo
     w.ld = up(dim, 8);
     w.dim4 = up(dim, 4);
     w.few = rows > FEW_ROWS ? 0 : rows > 64 ? 128 : rows > 32 ? 64 : rows > 16 ? 32 : 16;
+    // Of up to 16 rows there is room for g in two parts (two_parts()): 1 x 2048 x 65536 184.4 -> 186.8 us, 16 x 4096 x 50257
+    // 268.4 -> 269.9.  Always so up to 32 rows 32 x 2048 x 65536 takes 190.5 instead of 187.5, up to 64 rows 64 x 1024 x 32001
+    // 62.5 instead of 57.6: of that many rows the error is 1.2 to 1.4 times the results' rounding without.
+    if (grad && rows <= 16)
+        w.few = rows <= 8 ? 16 : 32;
     w.slots = w.few ? FEW_MAX_CTAS : up(vocab, TILE) / HALF;
     take(w.head, sizeof(LinearHead));
     take(w.pos, rows * 4);

@@ -31,7 +31,7 @@ struct LinearWork {
     int64_t padded, ld, dim4;
     int64_t slots;      // of part, per row
     int64_t piece_cols;
-    int few;            // few rows: 16, 32, 64 or 128, and piece is vocab x few
+    int few;            // few rows: 16, 32, 64 or 128 columns, and piece is vocab x few
     int splits;         // shares of dh along the vocabulary
     int64_t bytes;
 };

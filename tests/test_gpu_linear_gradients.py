@@ -75,3 +75,33 @@ def test_a_coefficient_that_is_no_number(bad, rows, dtype):
     rest = torch.arange(rows, device=DEV) != 1
     assert torch.equal(got[rest], want[rest])
     assert not bool(got[1].isfinite().any()) and not bool(gw.isfinite().any())
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows,taken", [(1, 1), (2, 2), (5, 5), (8, 8), (9, 9), (13, 12), (16, 16), (16, 3), (20, 16), (40, 32),
+                                        (64, 1), (64, 31), (128, 64), (100, 50), (128, 2)])
+def test_gradients_of_few_rows(rows, taken, dtype):
+    """Up to 16 rows, and up to half of the next power of two from 32 on: g is kept in two parts of 16 bits, and its
+    rounding is not to be seen beside the results'.
+
+    g is off by half = eps / 2 of what a first part leaves, half**2 of it, beside p's error (as in linear_reference, of
+    p's share alone); sums and results as there.
+    """
+    half, u = torch.finfo(dtype).eps / 2, 2.0 ** -24
+    for dim, vocab, scale in ((136, 3000, 1.0), (1040, 5001, 0.7), (2600, 729, 1.25)):
+        hidden, weight, target, dlogp, dlse = inputs(rows, dim, vocab, dtype, 0.0, pad=8)
+        target[torch.arange(rows, device=DEV) * taken % rows >= taken] = -100  # all but `taken` rows, spread out
+        assert int((target >= 0).sum()) == taken
+        dlogp[:] = dlogp.sign() * (1.0 + torch.arange(rows, device=DEV) * 0.37)
+        ref = Reference(hidden, weight, target, scale)
+        _, lse = itr.red_linear_logprob(hidden, weight, target, scale=scale)
+        gh, gw = itr.red_linear_logprob_grad(hidden, weight, target, lse, dlogp, dlse=dlse, scale=scale)
+        ref.gradients(dlogp, dlse)
+        by_p = ((dlse.double() - dlogp.double()).abs() * scale)[:, None] * ref.p
+        dg = by_p * (2 * ref.dz + 3e-5 + 4 * u * ref.lse.abs())[:, None] + half * half * ref.g.abs() + 1e-9
+        dg = torch.where(ref.live[:, None], dg, 0.0)
+        for got, want, tol in ((gh, ref.g @ ref.w, dg @ ref.w.abs() + (ref.g.abs() @ ref.w.abs()) * (vocab / 16 + 16) * 2 * u),
+                               (gw, ref.g.t() @ ref.h, dg.t() @ ref.h.abs() + (ref.g.abs().t() @ ref.h.abs()) * 50 * u)):
+            off = (got.double() - want).abs()
+            tol = tol + half * (want.abs() + tol) + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+            assert bool((off <= tol).all()), float((off - tol).max())
