@@ -509,20 +509,22 @@ int red_linear_logprob(int dtype, const void *hidden, int64_t rows, int64_t dim,
  * with p_j = e^(z[r, j] - lse[r]), lse as red_linear_logprob left it (p is as
  * exact as lse: off by the rounding of a number of its size).  A row
  * whose dlogp and dlse are both 0 is ignored, too.  The vocabulary is taken in
- * pieces; g is rounded to dtype once, in units that the largest coefficient
- * sets, and each result once more (in f16 the unit is the same for all rows: of a
- * row whose coefficient is 1e-6 of the largest, probabilities below 4e-3 are
- * rounded to steps of 4e-6, and its dhidden with them; of up to 16 rows, and of 17
- * to 32, 33 to 64 or 65 to 128 where at most 16, 32 or 64 take part, g is kept in
- * two such parts, 16 bits or more of it); their sums are fp32, those of a run of up to
+ * pieces.  g is rounded to dtype once, in units that the largest coefficient
+ * sets, and each result once more; their sums are fp32, those of a run of up to
  * 4096 rows or columns (16384 columns where rows are up to 128) by the tensor cores.
+ * In f16 the unit is the same for all rows: of a row whose coefficient is 1e-6 of
+ * the largest, probabilities below 4e-3 are rounded to steps of 4e-6, and its
+ * dhidden with them.  Where few rows take part (up to 16; of 17 to 32, 33 to 64 or
+ * 65 to 128 rows at most 16, 32 or 64) g is kept in two parts of dtype, and its
+ * rounding is not to be seen beside the results'.
  *   dhidden  rows x dim, row stride ldd, or NULL for none.  May be `hidden`.
  *   dweight  vocab x dim, row stride lddw, or NULL for none (not both).  Results
  *            must not overlap an input otherwise, nor each other.
- *   work     red_linear_work_bytes(..., 1) bytes: g of a piece of the vocabulary (at most
- *            384 MiB up to 32768 rows, 12 KiB a row beyond, 12 GiB in all, or 1 KiB a row
- *            where that is more), the packed hidden states (2 bytes of each element)
- *            and dhidden in fp32.
+ *   work     red_linear_work_bytes(..., 1) bytes: g of a piece of the vocabulary (up to
+ *            128 rows of all of it, 256 bytes a token at most; up to 32768 rows at most
+ *            384 MiB, beyond 12 KiB a row and 12 GiB in all, or 1 KiB a row where that is
+ *            more), the packed hidden states (2 bytes of each element) and dhidden in
+ *            fp32, of few rows in shares.
  */
 int red_linear_logprob_grad(int dtype, const void *hidden, int64_t rows, int64_t dim, int64_t ldh,
                             const void *weight, int64_t vocab, int64_t ldw, float scale, const int64_t *target,

@@ -105,3 +105,15 @@ def test_gradients_of_few_rows(rows, taken, dtype):
             off = (got.double() - want).abs()
             tol = tol + half * (want.abs() + tol) + (2.0 ** -25 if dtype == torch.float16 else 0.0)
             assert bool((off <= tol).all()), float((off - tol).max())
+
+
+@pytest.mark.parametrize("rows", [5, 100])
+def test_few_rows_of_a_long_vocabulary(rows):
+    """dh of few rows in shares of more than 16384 columns: its sums move to fp32 registers on the way."""
+    hidden, weight, target, dlogp, _ = inputs(rows, 4104, 70000, torch.float16, 0.0)
+    ref = Reference(hidden, weight, target)
+    _, lse = itr.red_linear_logprob(hidden, weight, target)
+    gh, gw = itr.red_linear_logprob_grad(hidden, weight, target, lse, dlogp)
+    ref.check_gradients(gh, gw, dlogp)
+    again = itr.red_linear_logprob_grad(hidden, weight, target, lse, dlogp)
+    assert torch.equal(again[0], gh) and torch.equal(again[1], gw)
