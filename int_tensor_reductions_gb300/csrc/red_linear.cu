@@ -1101,7 +1101,8 @@ __device__ __forceinline__ void store_long(const ProductArgs &a, const float (&z
         store_columns<DT, DH>(a, z + c, row, col, c, unit, staging, lane);
 }
 
-// LONG: products of more than SHORT_PRODUCTS blocks of K, summed in chunks of CHUNK_PRODUCTS.  (Tiles of many rows
+// LONG: sums in chunks of CHUNK_PRODUCTS blocks of K, where there are many rows or more than SHORT_PRODUCTS blocks of
+// them; else one run.  (Tiles of many rows
 // take the same time either way, as long as the registers stay below 168: with a split of them between the warps, as for
 // the tiles of logits, the warp that issues products is too slow, and 4096 x 2048 x 50257 bf16 takes 1010 us instead of
 // 934.  dw of few rows, which is no more than a way to memory, takes 161 us instead of 147 at 128 x 4096 x 32768.  There one
@@ -1175,7 +1176,7 @@ __global__ void __launch_bounds__(MMA_THREADS, 1) linear_products_kernel(const _
         for (int i = 0, t; (t = tile_of(i)) >= 0; ++i) {
             const TileJob j = job(t);
             if (!multiply_tile<LONG>(j, b, ring, pos, acc, instruction_desc(DT == RED_BF16, j.a_along_k, j.b_along_k),
-                               LONG ? CHUNK_PRODUCTS : SHORT_PRODUCTS, issues)) {
+                                     LONG ? CHUNK_PRODUCTS : SHORT_PRODUCTS, issues)) {
                 drain_products(b, issues);
                 break;
             }

@@ -183,9 +183,9 @@ __device__ __forceinline__ void store_q(uint8_t *q, int64_t row, int i, int len,
 // KIND: 0 for y in x's type, else the 8-bit type.  LONE: no residual.
 // (Registers are left to the compiler, but for two cases.  One that it makes 70 of, and three CTAs per SM: with 64, and
 // four, 16384 x 4096 bf16 91 -> 83 us.  One that it makes 92 to 128 of, and two, where only x is read and y written: with
-// 80, and three, 16384 x 5120 bf16 without a residual 62.8 -> 57.2, x 6144 69.5 -> 63.2; but with one 106.0 -> 117.2 (2000 rows 12.6 -> 11.8), in e4m3 with
-// one 93.9 -> 98.5 and without 68.4 -> 72.5.  A bound of one CTA per SM has it take more than 128: 16384 x 8192 173 -> 264; 80
-// for rows that long are too few: 85 -> 104.)
+// 80, and three, 16384 x 5120 bf16 without a residual 62.8 -> 57.2, x 6144 69.5 -> 63.2; but with one 106.0 -> 117.2
+// (2000 rows 12.6 -> 11.8), in e4m3 with one 93.9 -> 98.5 and without 68.4 -> 72.5.  A bound of one CTA per SM has it
+// take more than 128: 16384 x 8192 173 -> 264; 80 for rows that long are too few: 85 -> 104.)
 template <int LANES, int VECS, bool VEC, bool RING, bool LONE>
 constexpr int NORM_CTAS = LANES == 256 && VEC ? (VECS == 2 && !RING ? 4 : VECS == 3 && LONE ? 3 : 0) : 0;
 template <int DT, bool WIDE, int KIND, int LANES, int VECS, bool VEC, bool RING, bool LONE>
